@@ -422,7 +422,7 @@ def _run_own(st):
             out["dscores"] = b["dscores"]
         return out
     if c["op"] == "rows":
-        ctr.ctr_expert_dispatch(st["x"], st["token"], b["xs"], b["ws"])
+        ctr.ctr_expert_dispatch(st["x"], st["slot"], st["token"], b["xs"], b["ws"])
         ctr.ctr_expert_combine(st["ys"], st["slot"], st["weight"], b["y"], b["ws"])
         out = {"xs": b["xs"], "y": b["y"]}
         if c["train"]:
