@@ -50,7 +50,8 @@ typedef enum {
   CTR_ERR_CUDA = -5,               /* a CUDA runtime call or launch failed */
   CTR_ERR_TIMEOUT = -6,            /* device: a bounded wait ran out */
   CTR_ERR_NOT_IMPLEMENTED = -7,
-  CTR_ERR_BAD_OFFSETS = -8         /* device: offsets not monotone or not ending at n_ids */
+  CTR_ERR_BAD_OFFSETS = -8,        /* device: offsets not monotone or not ending at n_ids */
+  CTR_ERR_BAD_VALUE = -9           /* device: a NaN or +inf where a number is needed */
 } ctr_status;
 
 typedef enum { CTR_F32 = 0, CTR_BF16 = 1 } ctr_dtype;
@@ -409,6 +410,164 @@ int ctr_embedding_bag_bwd_update_opt(const float* grad_pooled, int64_t g_stride_
                                      const int32_t* sorted_bag, int64_t n_ids, float lr, void* table, ctr_dtype dtype,
                                      int32_t d, int64_t total_rows, float* grad_unique_out, int phases,
                                      const ctr_optimizer* opt, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* b. Expert layer on the interaction output                                  */
+/* ------------------------------------------------------------------------ */
+/* Source: "DHEN" notes, the mixture-of-experts section (a gate sends each
+ * sample to a few experts and adds their results up).  The pages give no
+ * shapes or kernels; the formulas below are this library's.
+ *
+ * A sample is called a token here; a token's k chosen experts are its choices.
+ * Row order: the (token, choice) pairs sorted by expert, then by token.  Row r
+ * of that order belongs to token[r], expert e owns rows offsets[e] ..
+ * offsets[e+1]-1, and choice j of token t is row slot[t*k + j] (-1: no row).
+ * offsets[experts] = routed rows <= tokens*k; token[r] = -1 beyond them.
+ * All maps are int32; tokens*k < 2^31; 1 <= experts <= CTR_MAX_EXPERTS,
+ * 1 <= k <= min(experts, CTR_MAX_CHOICES).  Matrices are row-major with a row
+ * stride ld >= the row's elements (in elements); any alignment of the element
+ * type is accepted (16-byte aligned rows take wider loads).
+ * A NULL pointer is refused unless the text says optional; a call with zero
+ * tokens or rows writes what has no token (offsets, norms) and succeeds. */
+#define CTR_MAX_EXPERTS 512
+#define CTR_MAX_CHOICES 16
+
+/* Routing.  With l = scores[t, :] (fp32 or bf16; fp32 arithmetic) and A = the
+ * experts with l_e > -inf:
+ *   choice j = the j-th largest l_e over A, ties to the lower index
+ *   weight_j = exp(l_e - m) / sum over B of exp(l_i - m),   m = max l,
+ *              B = A, or the choices alone if renormalize != 0
+ * A token with fewer than k experts in A gets expert -1, weight 0, slot -1 for
+ * the rest (all of them where A is empty).  A token with a NaN or +inf score is
+ * treated as if A were empty, and flagged CTR_ERR_BAD_VALUE.
+ * Outputs: expert int32, weight fp32, slot int32 [tokens, k] (dense), token
+ * int32 [tokens*k], offsets int32 [experts + 1].
+ * Workspace: ctr_expert_route_workspace_size(tokens, experts, k) bytes. */
+size_t ctr_expert_route_workspace_size(int64_t tokens, int32_t experts, int32_t k);
+int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, int64_t ld_scores,
+                     int32_t k, int renormalize, int32_t* expert, float* weight, int32_t* slot, int32_t* token,
+                     int32_t* offsets, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* Its gradient, the choices held fixed: with p = the softmax over B (0 outside),
+ * g_e = dweight_j for the expert of choice j (0 for the others),
+ *   dscores[t, e] = p_e (g_e - sum_i p_i g_i)
+ * in the scores' type.  Masked scores and tokens with nothing routed get 0.
+ * expert is the output of ctr_expert_route on the same scores; ws: as there or
+ * ctr_expert_workspace_size() bytes. */
+int ctr_expert_route_bwd(const float* dweight, const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts,
+                         int64_t ld_scores, int32_t k, int renormalize, const int32_t* expert, void* dscores,
+                         int64_t ld_dscores, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* Tokens into row order: out[slot[t*k+j], :] = x[t, :], and zeros in the rows
+ * r with token[r] = -1.  out is [tokens*k, d].  ws (these calls and
+ * ctr_expert_combine*): ctr_expert_workspace_size() bytes, the error word.
+ * Device errors: CTR_ERR_INDEX_OUT_OF_RANGE (a slot >= tokens*k: skipped). */
+size_t ctr_expert_workspace_size(void);
+int ctr_expert_dispatch(const void* x, ctr_dtype dtype, int64_t tokens, int32_t d, int64_t ldx, int32_t k,
+                        const int32_t* slot, const int32_t* token, void* out, int64_t ldo, void* ws, size_t ws_bytes,
+                        ctr_stream_t stream);
+
+/* Rows back to tokens: y[t, :] = sum over j with slot >= 0 of weight[t*k+j] *
+ * rows[slot[t*k+j], :], summed in fp32 in the order of j and rounded once; a
+ * token without rows gets zeros.  weight NULL: all 1 (then this is also the
+ * gradient of ctr_expert_dispatch: dx from the rows' gradient). */
+int ctr_expert_combine(const void* rows, ctr_dtype dtype, int64_t tokens, int32_t d, int64_t ld_rows, int32_t k,
+                       const int32_t* slot, const float* weight, void* y, int64_t ldy, void* ws, size_t ws_bytes,
+                       ctr_stream_t stream);
+
+/* Gradient of ctr_expert_combine:
+ *   drows[slot[t*k+j], :] = weight[t*k+j] dy[t, :]   (zeros in rows with token[r] = -1)
+ *   dweight[t*k+j] = <dy[t, :], rows[slot[t*k+j], :]>  (fp32; 0 where slot = -1) */
+int ctr_expert_combine_bwd(const void* dy, ctr_dtype dtype, int64_t tokens, int32_t d, int64_t ld_dy, int32_t k,
+                           const void* rows, int64_t ld_rows, const int32_t* slot, const float* weight,
+                           const int32_t* token, void* drows, int64_t ld_drows, float* dweight, void* ws,
+                           size_t ws_bytes, ctr_stream_t stream);
+
+/* ---- 8-bit products with a scale per block of 128 ----------------------- */
+/* Codes are e4m3 (4 exponent bits, 3 mantissa bits, largest value 448), one
+ * byte each.  A block's scale and codes are, in fp32 with m = the block's
+ * largest |x| but at least 2^-100,
+ *   scale = m / 448,   code = e4m3(x * (448 / m))   (nearest even)
+ * so the value that a code stands for is code * scale.  A block with a NaN or
+ * an infinity gives NaN results for the rows it enters.
+ * Layouts (P(n) = n rounded up to a multiple of 128, B(n) = P(n) / 128):
+ *   row codes      [rows, P(cols)], zeros past cols; row scales fp32 [B(cols),
+ *                  ld_scale], one per row and 128 columns: scale[c/128][r]
+ *   block codes    [groups, n, P(k)] with scales [groups, B(n), B(k)], one per
+ *                  128 x 128 block; their transpose [groups, k, P(n)] with
+ *                  scales [groups, B(k), B(n)]
+ *   column codes   [cols, P_rows], the transpose of grouped rows: each group's
+ *                  rows start at a multiple of 128 along the row axis and are
+ *                  filled up with zeros; P_rows = ctr_fp8_padded_rows(rows,
+ *                  groups).  Scales by column, [P_rows / 128, cols], or by
+ *                  128 x 128 block, [B(cols), P_rows / 128].
+ * Codes must be 16-byte aligned. */
+int64_t ctr_fp8_padded_rows(int64_t rows, int32_t groups);
+
+/* Row codes of x [x_rows, cols], or of its rows row_index[r] for r < rows
+ * (optional, int32; -1 gives a zero row).  Device errors:
+ * CTR_ERR_INDEX_OUT_OF_RANGE (an index >= x_rows: a zero row).  ws: the error
+ * word (256 bytes), in every ctr_fp8_quantize_* call. */
+int ctr_fp8_quantize_rows(const void* x, ctr_dtype dtype, int64_t x_rows, int64_t rows, int64_t cols, int64_t ldx,
+                          const int32_t* row_index, uint8_t* q, float* scale, int64_t ld_scale, void* ws,
+                          size_t ws_bytes, ctr_stream_t stream);
+
+/* Row codes and column codes of the same rows in one read, for a training
+ * step.  offsets: int32 [groups + 1], offsets[0] = 0, rows of group g are
+ * offsets[g] .. offsets[g+1]-1, offsets[groups] <= rows (rows beyond have no
+ * group: their row codes are not written).  cols_by_block: 0 = a scale per
+ * column and 128 rows (the left operand of ctr_fp8_matmul_wgrad), 1 = a scale
+ * per 128 x 128 block (the right one).  Device errors: as above, and
+ * CTR_ERR_BAD_OFFSETS (nothing is written). */
+int ctr_fp8_quantize_rows_cols(const void* x, ctr_dtype dtype, int64_t x_rows, int64_t rows, int64_t cols, int64_t ldx,
+                               const int32_t* row_index, const int32_t* offsets, int32_t groups, int cols_by_block,
+                               uint8_t* q, float* scale, int64_t ld_scale, uint8_t* qc, float* scale_c, void* ws,
+                               size_t ws_bytes, ctr_stream_t stream);
+
+/* Block codes of w [groups, n, k] (dense), and of its transpose where qt and
+ * scale_t (both or neither) are given. */
+int ctr_fp8_quantize_blocks(const void* w, ctr_dtype dtype, int32_t groups, int64_t n, int64_t k, uint8_t* q,
+                            float* scale, uint8_t* qt, float* scale_t, void* ws, size_t ws_bytes,
+                            ctr_stream_t stream);
+
+/* out[r, :] = W_g a_r for the rows r of group g: with a, b the values that the
+ * row codes (a, [rows, P(k)]) and block codes (b, [groups, n, P(k)]) stand for,
+ *   out[r, i] = sum over c < k of a[r, c] b[g, i, c],
+ * blocks of 128 summed by the tensor cores in fp32, the blocks' sums scaled and
+ * added in fp32, one rounding to out_dtype.  offsets as above; NULL means that
+ * all rows are group 0 (groups = 1).  Rows past offsets[groups] get zeros.
+ * out [rows, n], row stride ldo.  Device errors: CTR_ERR_BAD_OFFSETS (zeros are
+ * written), CTR_ERR_TIMEOUT.  The input gradient of out = W x is the same call
+ * with dout's row codes and the transposed block codes.
+ * Workspace (both products): ctr_fp8_matmul_workspace_size(rows, groups, n, k). */
+size_t ctr_fp8_matmul_workspace_size(int64_t rows, int32_t groups, int64_t n, int64_t k);
+int ctr_fp8_matmul(const uint8_t* a, const float* a_scale, int64_t ld_scale, const uint8_t* b, const float* b_scale,
+                   const int32_t* offsets, int64_t rows, int32_t groups, int64_t n, int64_t k, void* out,
+                   ctr_dtype out_dtype, int64_t ldo, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* Weight gradient: out[g, i, j] = sum over the rows r of group g of d[r, i]
+ * x[r, j], from column codes of d (by column, [n, P_rows]) and of x (by block,
+ * [k, P_rows]) made with the same offsets.  out [groups, n, k], dense; zeros
+ * for a group without rows. */
+int ctr_fp8_matmul_wgrad(const uint8_t* d, const float* d_scale, const uint8_t* x, const float* x_scale,
+                         const int32_t* offsets, int64_t rows, int32_t groups, int64_t n, int64_t k, void* out,
+                         ctr_dtype out_dtype, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* ---- Global gradient norm and clipping ---------------------------------- */
+/* norm = sqrt(sum over every element of every tensor of g^2), and
+ *   outs[i] = grads[i] * c,   c = norm > max_norm ? max_norm / norm : 1
+ * (the product in fp32, rounded once to the tensor's type).  grads, outs,
+ * dtypes and counts are host arrays of n_tensors entries (outs optional: norm
+ * only; outs[i] may be grads[i] but must not overlap anything else).  Blocks of
+ * elements are squared and added in fp32, what is joined is joined in fp64, and
+ * magnitudes whose squares leave fp32's range are squared in fp64, so norm is
+ * right wherever it is an fp32 number.  A norm that is not finite leaves the
+ * gradients as they are (c = 1) for the caller to see: norm (fp32 [1], device)
+ * reports it.  max_norm >= 0 and not NaN.  Tensors need element alignment only.
+ * Workspace: ctr_clip_grads_workspace_size() bytes. */
+size_t ctr_clip_grads_workspace_size(void);
+int ctr_clip_grads(const void* const* grads, void* const* outs, const int32_t* dtypes, const int64_t* counts,
+                   int32_t n_tensors, float max_norm, float* norm, void* ws, size_t ws_bytes, ctr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* Allocation-free dedup (no counterpart in the paper)                       */

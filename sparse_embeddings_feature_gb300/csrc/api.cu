@@ -91,6 +91,7 @@ extern "C" const char* ctr_status_string(int status) {
     case CTR_ERR_TIMEOUT: return "CTR_ERR_TIMEOUT";
     case CTR_ERR_NOT_IMPLEMENTED: return "CTR_ERR_NOT_IMPLEMENTED";
     case CTR_ERR_BAD_OFFSETS: return "CTR_ERR_BAD_OFFSETS";
+    case CTR_ERR_BAD_VALUE: return "CTR_ERR_BAD_VALUE";
     default: return "CTR_ERR_UNKNOWN";
   }
 }

@@ -1,0 +1,794 @@
+// b1/b2. Expert routing, and rows into expert order and back.
+//
+// Source: "DHEN" notes, the mixture-of-experts section (a gate sends each
+// sample to a few experts); the formulas and the row order are stated in
+// include/ctr.h.
+//
+// Routing.  A token's scores are spread over a group of lanes, EPL consecutive
+// scores to a lane; the k choices are k rounds of "best score not yet taken"
+// (in-lane scan, then an xor-shuffle tournament whose ties go to the lower
+// index).  The stable order by expert is a counting sort without atomics on
+// counts: a block's tile of up to 256 tokens is a bit matrix [expert][token]
+// in shared memory, so a choice's rank within the tile is a population count
+// of the bits before it, and the tile's count of an expert the count of all.
+// Three launches: choices + tile counts; exclusive sums of the counts over the
+// tiles (one warp column per expert); ranks and the two maps.  Few tokens run
+// as one block and one launch.
+//
+// Rows.  A token's group of lanes reads its row once and writes its k rows (or
+// reads k rows and writes one): every byte crosses HBM once, and rows of 1 KB
+// and more keep scattered writes whole.  Bound by HBM.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "common.cuh"
+#include "rows.cuh"
+
+namespace ctr {
+namespace {
+
+constexpr int kRouteThreads = 256;
+constexpr int kTileTokens = 256;      // tokens of a tile, at most
+// One block does it all up to this many scores (tokens x experts) and kTileTokens tokens.
+constexpr int64_t kOneBlockScores = 16384;
+
+struct RouteArgs {
+  const void* scores;
+  int64_t tokens, ld;
+  int32_t experts, k, lanes, tile, tiles;  // lanes: per token; tile: tokens of a tile
+  int32_t renormalize, vec;                // vec: rows start 16-byte aligned
+  int32_t* expert;
+  float* weight;
+  int32_t* slot;
+  int32_t* token;
+  int32_t* offsets;
+  int32_t* counts;  // [tiles][experts], then [experts] totals
+  int* err;
+};
+
+// Scores base .. base + EPL - 1 of a row; -inf past the last expert.
+template <typename T, int EPL>
+__device__ __forceinline__ void load_scores(const T* row, int base, int experts, bool vec, float (&v)[EPL]) {
+  constexpr int per = 16 / (int)sizeof(T);
+  if (vec && base + EPL <= experts) {
+#pragma unroll
+    for (int i = 0; i < EPL; i += per) {
+      float f[per];
+      Chunk<T, 16>::unpack(*(const uint4*)(row + base + i), f);
+#pragma unroll
+      for (int q = 0; q < per; ++q) v[i + q] = f[q];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = base + i < experts ? to_f32<T>(row[base + i]) : -INFINITY;
+  }
+}
+
+// Exclusive sum of totals[0 .. experts) into start (shared); returns the sum.  All threads.
+__device__ __forceinline__ int expert_starts(const int* totals, int experts, int* start, int* warp_sum) {
+  const int e0 = 2 * threadIdx.x;
+  const int a = e0 < experts ? totals[e0] : 0, b = e0 + 1 < experts ? totals[e0 + 1] : 0;
+  int x = a + b;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if ((threadIdx.x & 31) >= o) x += y;
+  }
+  if ((threadIdx.x & 31) == 31) warp_sum[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kRouteThreads / 32; ++w) {
+    if (w < (int)(threadIdx.x >> 5)) before += warp_sum[w];
+    all += warp_sum[w];
+  }
+  const int first = before + x - a - b;
+  if (e0 < experts) start[e0] = first;
+  if (e0 + 1 < experts) start[e0 + 1] = first + a;
+  __syncthreads();
+  return all;
+}
+
+// Ranks of the tile's choices from its bit matrix: slot and token of each, given the first row of
+// every expert's choices in this tile.  `before` gets each word's count of earlier tokens.
+__device__ __forceinline__ void write_slots(const RouteArgs& a, int64_t t0, int n, const uint32_t* bits,
+                                            uint16_t* before, const int* first) {
+  const int words = a.tile / 32;
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+    int c = 0;
+    for (int w = 0; w < words; ++w) {
+      before[e * words + w] = (uint16_t)c;
+      c += __popc(bits[e * words + w]);
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * a.k; i += kRouteThreads) {
+    const int64_t at = t0 * a.k + i;
+    const int e = a.expert[at];
+    int s = -1;
+    if (e >= 0) {
+      const int t = i / a.k, w = e * words + (t >> 5);
+      s = first[e] + before[w] + __popc(bits[w] & ((1u << (t & 31)) - 1));
+      a.token[s] = (int32_t)(t0 + t);
+    }
+    a.slot[at] = s;
+  }
+}
+
+template <typename T, int EPL, int KMAX>
+__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
+  extern __shared__ uint32_t bits[];  // [experts][tile / 32], then uint16 before[...] and int first[experts]
+  const int words = a.tile / 32;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
+  const int n = (int)imin64(a.tile, a.tokens - t0);
+  for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
+  __syncthreads();
+  const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
+  const int per_pass = kRouteThreads / a.lanes;
+  for (int p0 = 0; p0 < n; p0 += per_pass) {  // the same trips in every lane: the shuffles need all of them
+    const int tl = p0 + (int)threadIdx.x / a.lanes;
+    const bool mine = tl < n;
+    const int base = sub * EPL;
+    float v[EPL];
+    if (mine) {
+      load_scores<T, EPL>((const T*)a.scores + (t0 + tl) * a.ld, base, a.experts, a.vec != 0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+    }
+    bool odd = false;  // NaN or +inf: the token is routed nowhere
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) odd |= !(v[i] < INFINITY);
+    const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
+    const bool bad = (__ballot_sync(kFull, odd) & group) != 0;
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+      if (sub == 0) set_error(a.err, CTR_ERR_BAD_VALUE);
+    }
+    uint32_t taken = 0;
+    float z[KMAX], m = 0.f, chosen = 0.f;
+    int idx[KMAX];
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      if (j < a.k) {
+        float best = -INFINITY;
+        int at = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (!((taken >> i) & 1) && v[i] > best) {
+            best = v[i];
+            at = base + i;
+          }
+        for (int o = 1; o < a.lanes; o <<= 1) {
+          const float ob = __shfl_xor_sync(kFull, best, o);
+          const int oi = __shfl_xor_sync(kFull, at, o);
+          if (ob > best || (ob == best && oi < at)) {
+            best = ob;
+            at = oi;
+          }
+        }
+        const bool live = best > -INFINITY;
+        if (j == 0) m = live ? best : 0.f;
+        if (live && at >= base && at < base + EPL) taken |= 1u << (at - base);
+        idx[j] = live ? at : -1;
+        z[j] = live ? expf(best - m) : 0.f;
+        chosen += z[j];
+      }
+    }
+    float total = chosen;
+    if (!a.renormalize) {
+      total = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) total += expf(v[i] - m);  // exp(-inf) = 0: masked scores add nothing
+      for (int o = 1; o < a.lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
+    }
+    if (mine && sub == 0) {
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        if (j < a.k) {
+          const int64_t at = (t0 + tl) * a.k + j;
+          a.expert[at] = idx[j];
+          a.weight[at] = idx[j] >= 0 ? z[j] / total : 0.f;
+          if (idx[j] >= 0) atomicOr(&bits[idx[j] * words + (tl >> 5)], 1u << (tl & 31));
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (a.tiles > 1) {
+    for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+      int c = 0;
+      for (int w = 0; w < words; ++w) c += __popc(bits[e * words + w]);
+      a.counts[(int64_t)blockIdx.x * a.experts + e] = c;
+    }
+    return;
+  }
+  // a single tile: its counts are the totals
+  __shared__ int warp_sum[kRouteThreads / 32];
+  uint16_t* before = (uint16_t*)(bits + a.experts * words);
+  int* first = (int*)(before + ((a.experts * words + 1) & ~1));
+  int* totals = first + a.experts;
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
+    int c = 0;
+    for (int w = 0; w < words; ++w) c += __popc(bits[e * words + w]);
+    totals[e] = c;
+  }
+  __syncthreads();
+  const int all = expert_starts(totals, a.experts, first, warp_sum);
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) a.offsets[e] = first[e];
+  if (threadIdx.x == 0) a.offsets[a.experts] = all;
+  write_slots(a, t0, n, bits, before, first);
+  for (int64_t r = all + threadIdx.x; r < a.tokens * a.k; r += kRouteThreads) a.token[r] = -1;
+}
+
+// counts[tile][e] -> exclusive sum over the tiles, and the totals: 32 experts to a block, one to a
+// lane, the tiles cut into one segment a warp.
+__global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a) {
+  __shared__ int seg[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  const int per = (a.tiles + 31) / 32;
+  const int b0 = min(a.tiles, warp * per), b1 = min(a.tiles, b0 + per);
+  int sum = 0;
+  if (e < a.experts)
+    for (int b = b0; b < b1; ++b) sum += a.counts[(int64_t)b * a.experts + e];
+  seg[warp][lane] = sum;
+  __syncthreads();
+  int run = 0, all = 0;
+  for (int w = 0; w < 32; ++w) {
+    if (w < warp) run += seg[w][lane];
+    all += seg[w][lane];
+  }
+  if (e >= a.experts) return;
+  for (int b = b0; b < b1; ++b) {
+    int* c = &a.counts[(int64_t)b * a.experts + e];
+    const int x = *c;
+    *c = run;
+    run += x;
+  }
+  if (warp == 0) a.counts[(int64_t)a.tiles * a.experts + e] = all;
+}
+
+__global__ void __launch_bounds__(kRouteThreads) route_rank_kernel(const RouteArgs a) {
+  extern __shared__ uint32_t bits[];
+  __shared__ int warp_sum[kRouteThreads / 32];
+  const int words = a.tile / 32;
+  uint16_t* before = (uint16_t*)(bits + a.experts * words);
+  int* first = (int*)(before + ((a.experts * words + 1) & ~1));
+  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
+  const int n = (int)imin64(a.tile, a.tokens - t0);
+  for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * a.k; i += kRouteThreads) {
+    const int e = a.expert[t0 * a.k + i], t = i / a.k;
+    if (e >= 0) atomicOr(&bits[e * words + (t >> 5)], 1u << (t & 31));
+  }
+  const int all = expert_starts(a.counts + (int64_t)a.tiles * a.experts, a.experts, first, warp_sum);
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) a.offsets[e] = first[e];
+    if (threadIdx.x == 0) a.offsets[a.experts] = all;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.experts; e += kRouteThreads)
+    first[e] += a.counts[(int64_t)blockIdx.x * a.experts + e];
+  __syncthreads();
+  write_slots(a, t0, n, bits, before, first);
+  for (int64_t r = all + (int64_t)blockIdx.x * kRouteThreads + threadIdx.x; r < a.tokens * a.k;
+       r += (int64_t)gridDim.x * kRouteThreads)
+    a.token[r] = -1;
+}
+
+__global__ void route_empty_kernel(int32_t* offsets, int experts) {
+  for (int e = threadIdx.x; e <= experts; e += blockDim.x) offsets[e] = 0;
+}
+
+template <typename T, int EPL>
+__global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArgs a, const float* dweight, T* dscores,
+                                                                  int64_t ldd, int vec_out) {
+  const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
+  const int base = sub * EPL;
+  const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / a.lanes);
+  const int64_t g0 = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) / a.lanes;
+  const int64_t trips = ceil_div(a.tokens, groups);  // the same in every lane
+  for (int64_t trip = 0; trip < trips; ++trip) {
+    const int64_t t = g0 + trip * groups;
+    const bool mine = t < a.tokens;
+    float v[EPL], g[EPL];
+    if (mine) {
+      load_scores<T, EPL>((const T*)a.scores + t * a.ld, base, a.experts, a.vec != 0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+    }
+    uint32_t sel = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) g[i] = 0.f;
+    if (mine) {
+      for (int j = 0; j < a.k; ++j) {
+        const int at = a.expert[t * a.k + j] - base;
+        if (at >= 0 && at < EPL) {
+          const float d = dweight[t * a.k + j];
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (i == at) g[i] = d;
+          sel |= 1u << at;
+        }
+      }
+    }
+    // a token with no choice (all masked, or flagged by the routing) has no gradient
+    const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
+    const bool routed = (__ballot_sync(kFull, sel != 0) & group) != 0;
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m = fmaxf(m, v[i]);
+    for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (!routed) m = 0.f;
+    float total = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const bool in = a.renormalize ? ((sel >> i) & 1) : true;
+      v[i] = in && routed ? expf(v[i] - m) : 0.f;
+      total += v[i];
+      dot += v[i] * g[i];
+    }
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      total += __shfl_xor_sync(kFull, total, o);
+      dot += __shfl_xor_sync(kFull, dot, o);
+    }
+    if (!mine) continue;
+    const float inv = routed ? 1.f / total : 0.f;
+    dot *= inv;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) v[i] = v[i] * inv * (g[i] - dot);
+    T* out = dscores + t * ldd + base;
+    constexpr int per = 16 / (int)sizeof(T);
+    if (vec_out && base + EPL <= a.experts) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += per) {
+        float f[per];
+#pragma unroll
+        for (int q = 0; q < per; ++q) f[q] = v[i + q];
+        *(uint4*)(out + i) = Chunk<T, 16>::pack(f);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (base + i < a.experts) out[i] = from_f32<T>(v[i]);
+    }
+  }
+}
+
+// Lanes per token: 8 scores a lane (16 above 256 experts), a power of two.
+int route_lanes(int experts) {
+  int lanes = 1;
+  while (lanes < 32 && lanes * 8 < experts) lanes *= 2;
+  return lanes;
+}
+
+// Tokens of a tile: small batches are cut finer so that they spread over the SMs.
+int route_tile(int64_t tokens, int experts) {
+  if (tokens <= kTileTokens && tokens * experts <= kOneBlockScores) return kTileTokens;
+  int tile = kTileTokens;
+  while (tile > 32 && ceil_div(tokens, tile) < num_sms()) tile /= 2;
+  return tile;
+}
+
+size_t route_smem(int experts, int tile) {
+  const size_t cells = (size_t)experts * (tile / 32);
+  return cells * 4 + align_up(cells, 2) * 2 + (size_t)experts * 8;
+}
+
+int check_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, int64_t ld, int32_t k) {
+  if (!dtype_ok(dtype) || tokens < 0 || experts < 1 || k < 1 || k > experts || ld < experts) return CTR_ERR_INVALID_ARG;
+  if (tokens > 0 && !scores) return CTR_ERR_INVALID_ARG;
+  if (((uintptr_t)scores % dtype_bytes(dtype)) != 0) return CTR_ERR_INVALID_ARG;
+  if (experts > CTR_MAX_EXPERTS || k > CTR_MAX_CHOICES || tokens > INT32_MAX / k) return CTR_ERR_UNSUPPORTED;
+  return CTR_OK;
+}
+
+template <typename T, int EPL>
+void launch_choose(const RouteArgs& a, size_t smem, cudaStream_t s) {
+  if (a.k <= 4)
+    route_choose_kernel<T, EPL, 4><<<a.tiles, kRouteThreads, smem, s>>>(a);
+  else
+    route_choose_kernel<T, EPL, CTR_MAX_CHOICES><<<a.tiles, kRouteThreads, smem, s>>>(a);
+  count_launch();
+}
+
+// ---------------------------------------------------------------------------
+// rows
+// ---------------------------------------------------------------------------
+constexpr int kRowThreads = 256;
+constexpr int kUnroll = 4;  // chunks of a row a lane holds at once
+
+struct RowArgs {
+  const char* x;     // token rows (dispatch: read; backward: dy)
+  const char* rows;  // expert-ordered rows that are read
+  char* out;         // dispatch, backward: expert-ordered rows; combine: token rows
+  int64_t tokens, total;  // total = tokens * k rows
+  int64_t ldx, ldr, ldo;  // bytes
+  int32_t k, chunks, lanes;
+  const int32_t* slot;
+  const int32_t* token;
+  const float* weight;
+  float* dweight;
+  int* err;
+};
+
+__device__ __forceinline__ int checked_slot(const RowArgs& a, int64_t i) {
+  const int s = __ldg(a.slot + i);
+  if (s >= a.total) {
+    set_error(a.err, CTR_ERR_INDEX_OUT_OF_RANGE);
+    return -1;
+  }
+  return s;
+}
+
+// Zeros in the rows that no token has: 32 rows to a warp.
+template <typename Raw>
+__device__ __forceinline__ void zero_unused(const RowArgs& a, const Raw& zero) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
+  for (int64_t r0 = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * 32; r0 < a.total;
+       r0 += warps * 32) {
+    const bool unused = r0 + lane < a.total && __ldg(a.token + r0 + lane) < 0;
+    unsigned todo = __ballot_sync(kFull, unused);
+    while (todo) {
+      const int b = __ffs(todo) - 1;
+      todo &= todo - 1;
+      Raw* out = (Raw*)(a.out + (r0 + b) * a.ldo);
+      for (int c = lane; c < a.chunks; c += 32) out[c] = zero;
+    }
+  }
+}
+
+template <int VB>
+__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a) {
+  using Raw = typename RawOf<VB>::type;
+  const int sub = threadIdx.x & (a.lanes - 1);
+  const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
+  for (int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes; t < a.tokens; t += groups) {
+    const Raw* x = (const Raw*)(a.x + t * a.ldx);
+    for (int c0 = sub; c0 < a.chunks; c0 += kUnroll * a.lanes) {
+      Raw v[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (c0 + u * a.lanes < a.chunks) v[u] = __ldcs(x + c0 + u * a.lanes);
+      for (int j = 0; j < a.k; ++j) {
+        const int s = checked_slot(a, t * a.k + j);
+        if (s < 0) continue;
+        Raw* out = (Raw*)(a.out + s * a.ldo);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (c0 + u * a.lanes < a.chunks) out[c0 + u * a.lanes] = v[u];
+      }
+    }
+  }
+  zero_unused<Raw>(a, Raw{});
+}
+
+template <typename T, int VB>
+__global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
+  using Ch = Chunk<T, VB>;
+  using Raw = typename Ch::Raw;
+  const int sub = threadIdx.x & (a.lanes - 1);
+  const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
+  for (int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes; t < a.tokens; t += groups) {
+    Raw* y = (Raw*)(a.out + t * a.ldo);
+    for (int c0 = sub; c0 < a.chunks; c0 += kUnroll * a.lanes) {
+      float acc[kUnroll][Ch::n];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+        for (int i = 0; i < Ch::n; ++i) acc[u][i] = 0.f;
+#pragma unroll 2
+      for (int j = 0; j < a.k; ++j) {
+        const int s = checked_slot(a, t * a.k + j);
+        if (s < 0) continue;
+        const float w = a.weight ? __ldg(a.weight + t * a.k + j) : 1.f;
+        const Raw* r = (const Raw*)(a.rows + s * a.ldr);
+        Raw v[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (c0 + u * a.lanes < a.chunks) v[u] = __ldcs(r + c0 + u * a.lanes);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (c0 + u * a.lanes < a.chunks) {
+            float f[Ch::n];
+            Ch::unpack(v[u], f);
+#pragma unroll
+            for (int i = 0; i < Ch::n; ++i) acc[u][i] = fmaf(w, f[i], acc[u][i]);
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u)
+        if (c0 + u * a.lanes < a.chunks) y[c0 + u * a.lanes] = Ch::pack(acc[u]);
+    }
+  }
+}
+
+template <typename T, int VB>
+__global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(const RowArgs a) {
+  using Ch = Chunk<T, VB>;
+  using Raw = typename Ch::Raw;
+  const int sub = threadIdx.x & (a.lanes - 1);
+  const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
+  const int64_t trips = ceil_div(a.tokens, groups);  // the same in every lane: the shuffles need all of them
+  int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes;
+  for (int64_t trip = 0; trip < trips; ++trip, t += groups) {
+    const bool mine = t < a.tokens;
+    const Raw* dy = (const Raw*)(a.x + t * a.ldx);
+    for (int j = 0; j < a.k; ++j) {
+      const int s = mine ? checked_slot(a, t * a.k + j) : -1;
+      float dot = 0.f;
+      if (s >= 0) {
+        const float w = __ldg(a.weight + t * a.k + j);
+        const Raw* r = (const Raw*)(a.rows + s * a.ldr);
+        Raw* out = (Raw*)(a.out + s * a.ldo);
+        for (int c0 = sub; c0 < a.chunks; c0 += kUnroll * a.lanes) {
+          Raw v[kUnroll], g[kUnroll];
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u)
+            if (c0 + u * a.lanes < a.chunks) {
+              v[u] = __ldcs(r + c0 + u * a.lanes);
+              g[u] = dy[c0 + u * a.lanes];  // read once per choice: from L1 after the first
+            }
+#pragma unroll
+          for (int u = 0; u < kUnroll; ++u)
+            if (c0 + u * a.lanes < a.chunks) {
+              float f[Ch::n], d[Ch::n];
+              Ch::unpack(v[u], f);
+              Ch::unpack(g[u], d);
+#pragma unroll
+              for (int i = 0; i < Ch::n; ++i) {
+                dot = fmaf(d[i], f[i], dot);
+                d[i] *= w;
+              }
+              out[c0 + u * a.lanes] = Ch::pack(d);
+            }
+        }
+      }
+      for (int o = 1; o < a.lanes; o <<= 1) dot += __shfl_xor_sync(kFull, dot, o);
+      if (mine && sub == 0) a.dweight[t * a.k + j] = dot;
+    }
+  }
+  zero_unused<Raw>(a, Raw{});
+}
+
+int check_rows(ctr_dtype dtype, int64_t tokens, int32_t d, int32_t k, void* ws, size_t ws_bytes) {
+  if (!dtype_ok(dtype) || tokens < 0 || d < 1 || k < 1) return CTR_ERR_INVALID_ARG;
+  if (k > CTR_MAX_CHOICES || tokens > INT32_MAX / k) return CTR_ERR_UNSUPPORTED;
+  if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
+  return CTR_OK;
+}
+
+// Chunk count, lanes per row and grid of a row kernel.
+int plan_rows(RowArgs* a, int64_t row_bytes, int vb) {
+  a->chunks = (int32_t)(row_bytes / vb);
+  a->lanes = 1;
+  while (a->lanes < 32 && a->lanes < a->chunks) a->lanes *= 2;
+  const int64_t blocks = ceil_div(a->tokens * a->lanes, kRowThreads);
+  return (int)imax64(1, imin64(blocks, (int64_t)num_sms() * 16));
+}
+
+#define CTR_LAUNCH_TYPED(kernel, dtype, vb, grid, stream, args)                              \
+  do {                                                                                       \
+    if ((dtype) == CTR_F32) {                                                                \
+      if ((vb) == 16) kernel<float, 16><<<grid, kRowThreads, 0, stream>>>(args);             \
+      else if ((vb) == 8) kernel<float, 8><<<grid, kRowThreads, 0, stream>>>(args);          \
+      else kernel<float, 4><<<grid, kRowThreads, 0, stream>>>(args);                         \
+    } else {                                                                                 \
+      if ((vb) == 16) kernel<__nv_bfloat16, 16><<<grid, kRowThreads, 0, stream>>>(args);     \
+      else if ((vb) == 8) kernel<__nv_bfloat16, 8><<<grid, kRowThreads, 0, stream>>>(args);  \
+      else if ((vb) == 4) kernel<__nv_bfloat16, 4><<<grid, kRowThreads, 0, stream>>>(args);  \
+      else kernel<__nv_bfloat16, 2><<<grid, kRowThreads, 0, stream>>>(args);                 \
+    }                                                                                        \
+    count_launch();                                                                          \
+  } while (0)
+
+}  // namespace
+}  // namespace ctr
+
+using namespace ctr;
+
+extern "C" size_t ctr_expert_workspace_size(void) { return kWsHeader; }
+
+extern "C" size_t ctr_expert_route_workspace_size(int64_t tokens, int32_t experts, int32_t k) {
+  if (tokens < 0 || experts < 1 || k < 1) return 0;
+  WsSizer z;
+  z.take<int32_t>((size_t)(ceil_div(tokens, 32) + 1) * experts);  // tiles hold at least 32 tokens
+  return z.used;
+}
+
+extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts,
+                                int64_t ld_scores, int32_t k, int renormalize, int32_t* expert, float* weight,
+                                int32_t* slot, int32_t* token, int32_t* offsets, void* ws, size_t ws_bytes,
+                                ctr_stream_t stream) {
+  const int st = check_route(scores, dtype, tokens, experts, ld_scores, k);
+  if (st != CTR_OK) return st;
+  if (!offsets || (tokens > 0 && (!expert || !weight || !slot || !token))) return CTR_ERR_INVALID_ARG;
+  if (!ws_valid(ws, ws_bytes, ctr_expert_route_workspace_size(tokens, experts, k))) return CTR_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (tokens == 0) {
+    route_empty_kernel<<<1, 128, 0, s>>>(offsets, experts);
+    count_launch();
+    return launch_status();
+  }
+  RouteArgs a = {};
+  a.scores = scores;
+  a.tokens = tokens;
+  a.ld = ld_scores;
+  a.experts = experts;
+  a.k = k;
+  a.lanes = route_lanes(experts);
+  a.tile = route_tile(tokens, experts);
+  a.tiles = (int32_t)ceil_div(tokens, a.tile);
+  a.renormalize = renormalize != 0;
+  const int eb = dtype_bytes(dtype);
+  a.vec = ((uintptr_t)scores % 16) == 0 && (ld_scores * eb) % 16 == 0;
+  a.expert = expert;
+  a.weight = weight;
+  a.slot = slot;
+  a.token = token;
+  a.offsets = offsets;
+  WsCarver c(ws, ws_bytes);
+  a.counts = c.take<int32_t>((size_t)(a.tiles + 1) * experts);
+  a.err = (int*)ws;
+  const size_t smem = route_smem(experts, a.tile);
+  if (dtype == CTR_F32) {
+    if (experts <= 256) launch_choose<float, 8>(a, smem, s);
+    else launch_choose<float, 16>(a, smem, s);
+  } else {
+    if (experts <= 256) launch_choose<__nv_bfloat16, 8>(a, smem, s);
+    else launch_choose<__nv_bfloat16, 16>(a, smem, s);
+  }
+  if (a.tiles > 1) {
+    route_scan_kernel<<<(unsigned)ceil_div(experts, 32), 1024, 0, s>>>(a);
+    count_launch();
+    route_rank_kernel<<<a.tiles, kRouteThreads, smem, s>>>(a);
+    count_launch();
+  }
+  return launch_status();
+}
+
+extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ctr_dtype dtype, int64_t tokens,
+                                    int32_t experts, int64_t ld_scores, int32_t k, int renormalize,
+                                    const int32_t* expert, void* dscores, int64_t ld_dscores, void* ws,
+                                    size_t ws_bytes, ctr_stream_t stream) {
+  const int st = check_route(scores, dtype, tokens, experts, ld_scores, k);
+  if (st != CTR_OK) return st;
+  if (ld_dscores < experts || (tokens > 0 && (!dweight || !expert || !dscores))) return CTR_ERR_INVALID_ARG;
+  if (((uintptr_t)dscores % dtype_bytes(dtype)) != 0) return CTR_ERR_INVALID_ARG;
+  if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
+  if (tokens == 0) return CTR_OK;
+  RouteArgs a = {};
+  a.scores = scores;
+  a.tokens = tokens;
+  a.ld = ld_scores;
+  a.experts = experts;
+  a.k = k;
+  a.lanes = route_lanes(experts);
+  a.renormalize = renormalize != 0;
+  const int eb = dtype_bytes(dtype);
+  a.vec = ((uintptr_t)scores % 16) == 0 && (ld_scores * eb) % 16 == 0;
+  const int vec_out = ((uintptr_t)dscores % 16) == 0 && (ld_dscores * eb) % 16 == 0;
+  a.expert = const_cast<int32_t*>(expert);
+  a.err = (int*)ws;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int grid = (int)imin64(ceil_div(tokens * a.lanes, kRouteThreads), (int64_t)num_sms() * 16);
+  if (dtype == CTR_F32) {
+    if (experts <= 256)
+      route_bwd_kernel<float, 8><<<grid, kRouteThreads, 0, s>>>(a, dweight, (float*)dscores, ld_dscores, vec_out);
+    else
+      route_bwd_kernel<float, 16><<<grid, kRouteThreads, 0, s>>>(a, dweight, (float*)dscores, ld_dscores, vec_out);
+  } else {
+    if (experts <= 256)
+      route_bwd_kernel<__nv_bfloat16, 8>
+          <<<grid, kRouteThreads, 0, s>>>(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out);
+    else
+      route_bwd_kernel<__nv_bfloat16, 16>
+          <<<grid, kRouteThreads, 0, s>>>(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out);
+  }
+  count_launch();
+  return launch_status();
+}
+
+extern "C" int ctr_expert_dispatch(const void* x, ctr_dtype dtype, int64_t tokens, int32_t d, int64_t ldx, int32_t k,
+                                   const int32_t* slot, const int32_t* token, void* out, int64_t ldo, void* ws,
+                                   size_t ws_bytes, ctr_stream_t stream) {
+  const int st = check_rows(dtype, tokens, d, k, ws, ws_bytes);
+  if (st != CTR_OK) return st;
+  if (ldx < d || ldo < d) return CTR_ERR_INVALID_ARG;
+  if (tokens == 0) return CTR_OK;
+  const int eb = dtype_bytes(dtype);
+  if (!x || !slot || !token || !out || ((uintptr_t)x % eb) || ((uintptr_t)out % eb)) return CTR_ERR_INVALID_ARG;
+  RowArgs a = {};
+  a.x = (const char*)x;
+  a.out = (char*)out;
+  a.tokens = tokens;
+  a.total = tokens * k;
+  a.ldx = ldx * eb;
+  a.ldo = ldo * eb;
+  a.k = k;
+  a.slot = slot;
+  a.token = token;
+  a.err = (int*)ws;
+  const int64_t row = (int64_t)d * eb;
+  const int vb = vector_bytes({(uint64_t)(uintptr_t)x, (uint64_t)(uintptr_t)out, (uint64_t)a.ldx, (uint64_t)a.ldo,
+                               (uint64_t)row}, eb);
+  const int grid = plan_rows(&a, row, vb);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (vb == 16) dispatch_kernel<16><<<grid, kRowThreads, 0, s>>>(a);
+  else if (vb == 8) dispatch_kernel<8><<<grid, kRowThreads, 0, s>>>(a);
+  else if (vb == 4) dispatch_kernel<4><<<grid, kRowThreads, 0, s>>>(a);
+  else dispatch_kernel<2><<<grid, kRowThreads, 0, s>>>(a);
+  count_launch();
+  return launch_status();
+}
+
+extern "C" int ctr_expert_combine(const void* rows, ctr_dtype dtype, int64_t tokens, int32_t d, int64_t ld_rows,
+                                  int32_t k, const int32_t* slot, const float* weight, void* y, int64_t ldy, void* ws,
+                                  size_t ws_bytes, ctr_stream_t stream) {
+  const int st = check_rows(dtype, tokens, d, k, ws, ws_bytes);
+  if (st != CTR_OK) return st;
+  if (ld_rows < d || ldy < d) return CTR_ERR_INVALID_ARG;
+  if (tokens == 0) return CTR_OK;
+  const int eb = dtype_bytes(dtype);
+  if (!rows || !slot || !y || ((uintptr_t)rows % eb) || ((uintptr_t)y % eb)) return CTR_ERR_INVALID_ARG;
+  RowArgs a = {};
+  a.rows = (const char*)rows;
+  a.out = (char*)y;
+  a.tokens = tokens;
+  a.total = tokens * k;
+  a.ldr = ld_rows * eb;
+  a.ldo = ldy * eb;
+  a.k = k;
+  a.slot = slot;
+  a.weight = weight;
+  a.err = (int*)ws;
+  const int64_t row = (int64_t)d * eb;
+  const int vb = vector_bytes({(uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)y, (uint64_t)a.ldr, (uint64_t)a.ldo,
+                               (uint64_t)row}, eb);
+  const int grid = plan_rows(&a, row, vb);
+  cudaStream_t s = (cudaStream_t)stream;
+  CTR_LAUNCH_TYPED(combine_kernel, dtype, vb, grid, s, a);
+  return launch_status();
+}
+
+extern "C" int ctr_expert_combine_bwd(const void* dy, ctr_dtype dtype, int64_t tokens, int32_t d, int64_t ld_dy,
+                                      int32_t k, const void* rows, int64_t ld_rows, const int32_t* slot,
+                                      const float* weight, const int32_t* token, void* drows, int64_t ld_drows,
+                                      float* dweight, void* ws, size_t ws_bytes, ctr_stream_t stream) {
+  const int st = check_rows(dtype, tokens, d, k, ws, ws_bytes);
+  if (st != CTR_OK) return st;
+  if (ld_dy < d || ld_rows < d || ld_drows < d) return CTR_ERR_INVALID_ARG;
+  if (tokens == 0) return CTR_OK;
+  const int eb = dtype_bytes(dtype);
+  if (!dy || !rows || !slot || !weight || !token || !drows || !dweight) return CTR_ERR_INVALID_ARG;
+  if (((uintptr_t)dy % eb) || ((uintptr_t)rows % eb) || ((uintptr_t)drows % eb)) return CTR_ERR_INVALID_ARG;
+  RowArgs a = {};
+  a.x = (const char*)dy;
+  a.rows = (const char*)rows;
+  a.out = (char*)drows;
+  a.tokens = tokens;
+  a.total = tokens * k;
+  a.ldx = ld_dy * eb;
+  a.ldr = ld_rows * eb;
+  a.ldo = ld_drows * eb;
+  a.k = k;
+  a.slot = slot;
+  a.token = token;
+  a.weight = weight;
+  a.dweight = dweight;
+  a.err = (int*)ws;
+  const int64_t row = (int64_t)d * eb;
+  const int vb = vector_bytes({(uint64_t)(uintptr_t)dy, (uint64_t)(uintptr_t)rows, (uint64_t)(uintptr_t)drows,
+                               (uint64_t)a.ldx, (uint64_t)a.ldr, (uint64_t)a.ldo, (uint64_t)row}, eb);
+  const int grid = plan_rows(&a, row, vb);
+  cudaStream_t s = (cudaStream_t)stream;
+  CTR_LAUNCH_TYPED(combine_bwd_kernel, dtype, vb, grid, s, a);
+  return launch_status();
+}

@@ -1,0 +1,423 @@
+// b3. e4m3 codes with a scale per block of 128: rows, rows + columns, blocks.
+//
+// With m = max(largest |x| of the block, 2^-100):  scale = m / 448,  code =
+// e4m3(x * (448 / m)), all in fp32 (two correctly rounded divisions a block, one
+// multiplication and one conversion a value).  The floor of 2^-100 keeps 448 / m
+// finite: values below it are zero for the product's purposes.
+//
+// Rows: 16 lanes hold a block of 128 values, 8 each (one or two 16-byte loads),
+// the maximum is four xor-shuffles, and the 128 codes leave as one 128-byte
+// store of 8 bytes a lane.  Bound by HBM.
+//
+// Tiles (rows + columns, blocks): a CTA reads a 128 x 128 tile once, keeps it in
+// shared memory in its own type, and writes both orders of codes from it, each
+// as 128 consecutive bytes: a second pass over x would cost as much as the
+// first.  The column order is read back one column to a pair of threads, 64
+// values each, so their codes leave in 16-byte stores.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "common.cuh"
+#include "rows.cuh"
+
+namespace ctr {
+namespace {
+
+constexpr float kTop = 448.f;         // largest e4m3 value
+constexpr float kFloor = 0x1p-100f;
+constexpr int kQThreads = 256;
+
+// NaN stays NaN (the comparison is false for it).
+__device__ __forceinline__ float at_least_floor(float m) { return m < kFloor ? kFloor : m; }
+
+// The larger magnitude, NaN winning: magnitudes compare as their bits.
+__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+template <int N>
+__device__ __forceinline__ uint32_t max_bits(const float (&v)[N]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) m = max(m, mag_bits(v[i]));
+  return m;
+}
+
+__device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+// Columns c0 .. c0 + 7 of a row of `cols` elements as fp32; zeros past the end.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t c0, int64_t cols, bool vec, float (&v)[8]) {
+  constexpr int per = 16 / (int)sizeof(T);
+  if (vec && c0 + 8 <= cols) {
+#pragma unroll
+    for (int i = 0; i < 8; i += per) {
+      float f[per];
+      Chunk<T, 16>::unpack(*(const uint4*)(row + c0 + i), f);
+#pragma unroll
+      for (int q = 0; q < per; ++q) v[i + q] = f[q];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? to_f32<T>(row[c0 + i]) : 0.f;
+  }
+}
+
+// Row of x for row r of the codes: row_index[r], or r; -1 for a zero row.
+__device__ __forceinline__ int64_t source_row(const int32_t* row_index, int64_t r, int64_t x_rows, int* err) {
+  if (!row_index) return r;
+  const int64_t i = __ldg(row_index + r);
+  if (i >= x_rows) {
+    set_error(err, CTR_ERR_INDEX_OUT_OF_RANGE);
+    return -1;
+  }
+  return i;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* x, int64_t x_rows, int64_t rows,
+                                                                  int64_t cols, int64_t ldx, int vec,
+                                                                  const int32_t* row_index, uint8_t* q, float* scale,
+                                                                  int64_t ld_scale, int blocks_per_row, int* err) {
+  const int64_t pad = (int64_t)blocks_per_row * 128;
+  const int lane16 = threadIdx.x & 15;
+  const int64_t units = rows * blocks_per_row;  // blocks of 128, one to 16 lanes
+  const int64_t step = (int64_t)gridDim.x * (kQThreads / 16);
+  const int64_t trips = ceil_div(units, step);  // the same in every lane: the shuffles need all of them
+  int64_t u = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);
+  for (int64_t trip = 0; trip < trips; ++trip, u += step) {
+    const bool mine = u < units;
+    const int64_t r = mine ? u / blocks_per_row : 0;
+    const int kb = mine ? (int)(u - r * blocks_per_row) : 0;
+    float v[8];
+    const int64_t src = mine ? source_row(row_index, r, x_rows, err) : -1;
+    if (src >= 0) {
+      load8(x + src * ldx, (int64_t)kb * 128 + lane16 * 8, cols, vec != 0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+    uint32_t m = max_bits(v);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+    const float amax = at_least_floor(__uint_as_float(m));
+    const float inv = __fdiv_rn(kTop, amax);
+    if (mine) {
+      *(uint2*)(q + r * pad + (int64_t)kb * 128 + lane16 * 8) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
+      if (lane16 == 0) scale[kb * ld_scale + r] = __fdiv_rn(amax, kTop);
+    }
+  }
+}
+
+struct TileArgs {
+  const void* x;
+  int64_t x_rows, rows, cols, ldx;
+  const int32_t* row_index;
+  const int32_t* offsets;  // NULL: `groups` groups of `rows` rows each
+  int32_t groups, vec, col_blocks;
+  uint8_t* q;
+  float* scale;
+  int64_t ldq, ld_scale;  // scale: [col block][row], or with blocks [group][row block][col block]
+  uint8_t* qt;
+  float* scale_t;
+  int64_t ldt, ld_scale_t;  // qt: [col][ldt]; scale_t: [tile][cols] by column, [col block][tile] by block
+  int* err;
+};
+
+// One 128 x 128 tile.  ROW_BLOCK: the row codes have one scale for the tile (else one a row);
+// COL_BLOCK: the column codes have (else one a column).
+template <typename T, bool ROW_BLOCK, bool COL_BLOCK>
+__global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs a) {
+  // a row of the tile is 128 elements and 8 bytes more, so that a column's reads spread over the banks
+  constexpr int kLd = 128 + 8 / (int)sizeof(T);
+  extern __shared__ __align__(16) uint8_t smem[];
+  T* tile = (T*)smem;
+  __shared__ uint32_t col_max[2][128];
+  __shared__ uint32_t warp_max[kQThreads / 32];
+  __shared__ int where[4];  // group, first row, rows, tile number (of all groups)
+  const int col0 = blockIdx.y * 128;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (a.offsets) {
+    // the groups' tiles come one after another: find this block's (one warp, 32 groups at a time)
+    if (warp == 0) {
+      if (lane == 0) where[2] = 0;
+      __syncwarp();
+      int seen = 0;
+      bool ok = __ldg(a.offsets) == 0;
+      for (int g0 = 0; g0 < a.groups; g0 += 32) {
+        const int g = g0 + lane;
+        int lo = 0, hi = 0;
+        if (g < a.groups) {
+          lo = __ldg(a.offsets + g);
+          hi = __ldg(a.offsets + g + 1);
+          ok = ok && lo >= 0 && hi >= lo && hi <= a.rows;
+        }
+        const int mine = ok ? (hi - lo + 127) / 128 : 0;
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFull, incl, o);
+          if (lane >= o) incl += y;
+        }
+        const int t = (int)blockIdx.x - (seen + incl - mine);
+        if (t >= 0 && t < mine) {
+          where[0] = g;
+          where[1] = lo + t * 128;
+          where[2] = min(128, hi - lo - t * 128);
+          where[3] = blockIdx.x;
+        }
+        seen += __shfl_sync(kFull, incl, 31);
+      }
+      const bool good = __all_sync(kFull, ok);
+      __syncwarp();
+      if (!good) {
+        if (lane == 0) {
+          set_error(a.err, CTR_ERR_BAD_OFFSETS);
+          where[2] = 0;
+        }
+      }
+    }
+  } else if (threadIdx.x == 0) {
+    const int per = (int)((a.rows + 127) / 128);
+    const int g = blockIdx.x / per, t = blockIdx.x - g * per;
+    where[0] = g;
+    where[1] = t * 128;
+    where[2] = (int)imin64(128, a.rows - t * 128);
+    where[3] = t;
+  }
+  __syncthreads();
+  const int g = where[0], row0 = where[1], n = where[2], tnum = where[3];
+  if (n <= 0) return;
+  const int64_t xbase = a.offsets ? 0 : (int64_t)g * a.rows;  // rows of earlier groups
+
+  // Row order: 16 lanes a row, 8 values each; rows past n are zeros (the column codes' filling).
+  const int lane16 = threadIdx.x & 15;
+  const int64_t qcol = col0 + lane16 * 8;
+  uint32_t tile_max = 0;
+#pragma unroll 4
+  for (int p = 0; p < 8; ++p) {
+    const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
+    float v[8];
+    int64_t src = -1;
+    if (i < n) src = xbase + source_row(a.row_index, row0 + i, a.x_rows, a.err);
+    if (src >= 0) {
+      load8((const T*)a.x + src * a.ldx, qcol, a.cols, a.vec != 0, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+    T* dst = tile + i * kLd + lane16 * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dst[e] = from_f32<T>(v[e]);
+    uint32_t m = max_bits(v);
+    if constexpr (ROW_BLOCK) {
+      tile_max = max(tile_max, m);
+    } else {
+      if constexpr (COL_BLOCK) tile_max = max(tile_max, m);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+      const float amax = at_least_floor(__uint_as_float(m));
+      const float inv = __fdiv_rn(kTop, amax);
+      if (i < n) {
+        *(uint2*)(a.q + (int64_t)(row0 + i) * a.ldq + qcol) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
+        if (lane16 == 0) a.scale[(int64_t)blockIdx.y * a.ld_scale + row0 + i] = __fdiv_rn(amax, kTop);
+      }
+    }
+  }
+  float block_amax = 0.f, block_inv = 0.f;
+  if constexpr (ROW_BLOCK || COL_BLOCK) {
+    tile_max = __reduce_max_sync(kFull, tile_max);
+    if (lane == 0) warp_max[warp] = tile_max;
+    __syncthreads();
+    tile_max = 0;
+#pragma unroll
+    for (int w = 0; w < kQThreads / 32; ++w) tile_max = max(tile_max, warp_max[w]);
+    block_amax = at_least_floor(__uint_as_float(tile_max));
+    block_inv = __fdiv_rn(kTop, block_amax);
+  } else {
+    __syncthreads();
+  }
+  if constexpr (ROW_BLOCK) {
+    const int64_t row_blocks = (a.rows + 127) / 128;
+#pragma unroll 4
+    for (int p = 0; p < 8; ++p) {
+      const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
+      if (i >= n) continue;
+      const T* src = tile + i * kLd + lane16 * 8;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = to_f32<T>(src[e]);
+      *(uint2*)(a.q + (xbase + row0 + i) * a.ldq + qcol) =
+          make_uint2(codes4(v, block_inv), codes4(v + 4, block_inv));
+    }
+    if (threadIdx.x == 0) {
+      const float s = __fdiv_rn(block_amax, kTop);
+      a.scale[((int64_t)g * row_blocks + tnum) * a.col_blocks + blockIdx.y] = s;
+      if (a.qt) a.scale_t[((int64_t)g * a.col_blocks + blockIdx.y) * row_blocks + tnum] = s;
+    }
+    if (!a.qt) return;
+  }
+  // Column order: a column to two threads, 64 of its rows each.
+  const int c = threadIdx.x & 127, half = threadIdx.x >> 7;
+  float amax = block_amax, inv = block_inv;
+  if constexpr (!COL_BLOCK) {
+    uint32_t m = 0;
+#pragma unroll 8
+    for (int i = 0; i < 64; ++i) m = max(m, mag_bits(to_f32<T>(tile[(half * 64 + i) * kLd + c])));
+    col_max[half][c] = m;
+    __syncthreads();
+    amax = at_least_floor(__uint_as_float(max(col_max[0][c], col_max[1][c])));
+    inv = __fdiv_rn(kTop, amax);
+  }
+  if (col0 + c >= a.cols) return;
+  const int64_t qrow = (ROW_BLOCK ? (int64_t)g * a.cols : 0) + col0 + c;
+  uint4* out = (uint4*)(a.qt + qrow * a.ldt + (int64_t)tnum * 128 + half * 64);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    uint32_t w[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = to_f32<T>(tile[(half * 64 + p * 16 + b * 4 + e) * kLd + c]);
+      w[b] = codes4(v, inv);
+    }
+    out[p] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if constexpr (!ROW_BLOCK) {
+    if constexpr (COL_BLOCK) {
+      if (threadIdx.x == 0) a.scale_t[(int64_t)blockIdx.y * a.ld_scale_t + tnum] = __fdiv_rn(amax, kTop);
+    } else {
+      if (half == 0) a.scale_t[(int64_t)tnum * a.ld_scale_t + col0 + c] = __fdiv_rn(amax, kTop);
+    }
+  }
+}
+
+template <typename T, bool ROW_BLOCK, bool COL_BLOCK>
+int launch_tiles(const TileArgs& a, int64_t tiles, cudaStream_t s) {
+  auto k = quantize_tile_kernel<T, ROW_BLOCK, COL_BLOCK>;
+  const int smem = 128 * (128 * (int)sizeof(T) + 8);
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return CTR_ERR_CUDA;
+  k<<<dim3((unsigned)tiles, (unsigned)a.col_blocks), kQThreads, smem, s>>>(a);
+  count_launch();
+  return launch_status();
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p % 16) == 0; }
+
+}  // namespace
+}  // namespace ctr
+
+using namespace ctr;
+
+extern "C" int64_t ctr_fp8_padded_rows(int64_t rows, int32_t groups) {
+  if (rows < 0 || groups < 1) return -1;
+  // a group of c rows takes ceil(c / 128) <= c tiles
+  return 128 * imax64(1, imin64((rows + 127 * (int64_t)groups) / 128, rows));
+}
+
+extern "C" int ctr_fp8_quantize_rows(const void* x, ctr_dtype dtype, int64_t x_rows, int64_t rows, int64_t cols,
+                                     int64_t ldx, const int32_t* row_index, uint8_t* q, float* scale,
+                                     int64_t ld_scale, void* ws, size_t ws_bytes, ctr_stream_t stream) {
+  if (!dtype_ok(dtype) || x_rows < 0 || rows < 0 || cols < 1 || ldx < cols || ld_scale < rows)
+    return CTR_ERR_INVALID_ARG;
+  if (!row_index && rows > x_rows) return CTR_ERR_INVALID_ARG;
+  if (rows > INT32_MAX || cols > INT32_MAX) return CTR_ERR_UNSUPPORTED;
+  if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
+  if (rows == 0) return CTR_OK;
+  const int eb = dtype_bytes(dtype);
+  if (!x || !q || !scale || ((uintptr_t)x % eb) || !aligned16(q)) return CTR_ERR_INVALID_ARG;
+  const int vec = aligned16(x) && (ldx * eb) % 16 == 0;
+  const int kb = (int)ceil_div(cols, 128);
+  const int grid = (int)imin64(ceil_div(rows * kb, kQThreads / 16), (int64_t)num_sms() * 16);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == CTR_F32)
+    quantize_rows_kernel<<<grid, kQThreads, 0, s>>>((const float*)x, x_rows, rows, cols, ldx, vec, row_index, q,
+                                                    scale, ld_scale, kb, (int*)ws);
+  else
+    quantize_rows_kernel<<<grid, kQThreads, 0, s>>>((const __nv_bfloat16*)x, x_rows, rows, cols, ldx, vec, row_index,
+                                                    q, scale, ld_scale, kb, (int*)ws);
+  count_launch();
+  return launch_status();
+}
+
+extern "C" int ctr_fp8_quantize_rows_cols(const void* x, ctr_dtype dtype, int64_t x_rows, int64_t rows, int64_t cols,
+                                          int64_t ldx, const int32_t* row_index, const int32_t* offsets,
+                                          int32_t groups, int cols_by_block, uint8_t* q, float* scale,
+                                          int64_t ld_scale, uint8_t* qc, float* scale_c, void* ws, size_t ws_bytes,
+                                          ctr_stream_t stream) {
+  if (!dtype_ok(dtype) || x_rows < 0 || rows < 0 || cols < 1 || ldx < cols || ld_scale < rows || groups < 1)
+    return CTR_ERR_INVALID_ARG;
+  if (!offsets || (!row_index && rows > x_rows) || (cols_by_block != 0 && cols_by_block != 1))
+    return CTR_ERR_INVALID_ARG;
+  if (rows > INT32_MAX || cols > INT32_MAX || groups > CTR_MAX_EXPERTS) return CTR_ERR_UNSUPPORTED;
+  if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
+  if (rows == 0) return CTR_OK;
+  const int eb = dtype_bytes(dtype);
+  if (!x || !q || !scale || !qc || !scale_c || ((uintptr_t)x % eb) || !aligned16(q) || !aligned16(qc))
+    return CTR_ERR_INVALID_ARG;
+  const int64_t padded = ctr_fp8_padded_rows(rows, groups), tiles = padded / 128;
+  if (tiles > INT32_MAX || ceil_div(cols, 128) > 65535) return CTR_ERR_UNSUPPORTED;
+  TileArgs a = {};
+  a.x = x;
+  a.x_rows = x_rows;
+  a.rows = rows;
+  a.cols = cols;
+  a.ldx = ldx;
+  a.row_index = row_index;
+  a.offsets = offsets;
+  a.groups = groups;
+  a.vec = aligned16(x) && (ldx * eb) % 16 == 0;
+  a.col_blocks = (int32_t)ceil_div(cols, 128);
+  a.q = q;
+  a.scale = scale;
+  a.ldq = (int64_t)a.col_blocks * 128;
+  a.ld_scale = ld_scale;
+  a.qt = qc;
+  a.scale_t = scale_c;
+  a.ldt = padded;
+  a.ld_scale_t = cols_by_block ? tiles : cols;
+  a.err = (int*)ws;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (dtype == CTR_F32)
+    return cols_by_block ? launch_tiles<float, false, true>(a, tiles, s) : launch_tiles<float, false, false>(a, tiles, s);
+  return cols_by_block ? launch_tiles<__nv_bfloat16, false, true>(a, tiles, s)
+                       : launch_tiles<__nv_bfloat16, false, false>(a, tiles, s);
+}
+
+extern "C" int ctr_fp8_quantize_blocks(const void* w, ctr_dtype dtype, int32_t groups, int64_t n, int64_t k,
+                                       uint8_t* q, float* scale, uint8_t* qt, float* scale_t, void* ws,
+                                       size_t ws_bytes, ctr_stream_t stream) {
+  if (!dtype_ok(dtype) || groups < 1 || n < 1 || k < 1 || (qt == nullptr) != (scale_t == nullptr))
+    return CTR_ERR_INVALID_ARG;
+  if (n > INT32_MAX || k > INT32_MAX || groups > CTR_MAX_EXPERTS) return CTR_ERR_UNSUPPORTED;
+  if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
+  const int eb = dtype_bytes(dtype);
+  if (!w || !q || !scale || ((uintptr_t)w % eb) || !aligned16(q) || !aligned16(qt)) return CTR_ERR_INVALID_ARG;
+  const int64_t tiles = groups * ceil_div(n, 128);
+  if (tiles > INT32_MAX || ceil_div(k, 128) > 65535) return CTR_ERR_UNSUPPORTED;
+  TileArgs a = {};
+  a.x = w;
+  a.x_rows = n;
+  a.rows = n;
+  a.cols = k;
+  a.ldx = k;
+  a.groups = groups;
+  a.vec = aligned16(w) && (k * eb) % 16 == 0;
+  a.col_blocks = (int32_t)ceil_div(k, 128);
+  a.q = q;
+  a.scale = scale;
+  a.ldq = (int64_t)a.col_blocks * 128;
+  a.qt = qt;
+  a.scale_t = scale_t;
+  a.ldt = ceil_div(n, 128) * 128;
+  a.err = (int*)ws;
+  cudaStream_t s = (cudaStream_t)stream;
+  return dtype == CTR_F32 ? launch_tiles<float, true, true>(a, tiles, s)
+                          : launch_tiles<__nv_bfloat16, true, true>(a, tiles, s);
+}

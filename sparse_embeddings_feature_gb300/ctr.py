@@ -24,6 +24,8 @@ DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 # status codes (ctr_status in include/ctr.h)
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE = 0, -1, -2, -3
 ERR_INDEX_OUT_OF_RANGE, ERR_CUDA, ERR_TIMEOUT, ERR_NOT_IMPLEMENTED, ERR_BAD_OFFSETS = -4, -5, -6, -7, -8
+ERR_BAD_VALUE = -9
+MAX_EXPERTS, MAX_CHOICES = 512, 16
 
 _lock = threading.Lock()
 _lib = None
@@ -65,6 +67,24 @@ _SIGS = {
     "ctr_dot_interaction_bwd_mode": (C.c_int, [_p, _p, _i32, _i32, _i32, C.c_int, _p, _p, _sz, _p]),
     "ctr_embedding_bag_bwd_update_phases": (C.c_int, [_p, _i64, _i64, _p, _i32, _i32, C.c_int, _p, _p, _p, _p, _i64,
                                                       _f32, _p, C.c_int, _i32, _i64, _p, C.c_int, _p, _sz, _p]),
+    "ctr_expert_route_workspace_size": (_sz, [_i64, _i32, _i32]),
+    "ctr_expert_route": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _i32, C.c_int, _p, _p, _p, _p, _p, _p, _sz, _p]),
+    "ctr_expert_route_bwd": (C.c_int, [_p, _p, C.c_int, _i64, _i32, _i64, _i32, C.c_int, _p, _p, _i64, _p, _sz, _p]),
+    "ctr_expert_workspace_size": (_sz, []),
+    "ctr_expert_dispatch": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _i32, _p, _p, _p, _i64, _p, _sz, _p]),
+    "ctr_expert_combine": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _i32, _p, _p, _p, _i64, _p, _sz, _p]),
+    "ctr_expert_combine_bwd": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _i32, _p, _i64, _p, _p, _p, _p, _i64, _p, _p,
+                                         _sz, _p]),
+    "ctr_fp8_padded_rows": (C.c_int64, [_i64, _i32]),
+    "ctr_fp8_quantize_rows": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _i64, _p, _p, _p, _i64, _p, _sz, _p]),
+    "ctr_fp8_quantize_rows_cols": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _i64, _p, _p, _i32, C.c_int, _p, _p, _i64,
+                                             _p, _p, _p, _sz, _p]),
+    "ctr_fp8_quantize_blocks": (C.c_int, [_p, C.c_int, _i32, _i64, _i64, _p, _p, _p, _p, _p, _sz, _p]),
+    "ctr_fp8_matmul_workspace_size": (_sz, [_i64, _i32, _i64, _i64]),
+    "ctr_fp8_matmul": (C.c_int, [_p, _p, _i64, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _i64, _p, _sz, _p]),
+    "ctr_fp8_matmul_wgrad": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _p, _sz, _p]),
+    "ctr_clip_grads_workspace_size": (_sz, []),
+    "ctr_clip_grads": (C.c_int, [_p, _p, _p, _p, _i32, _f32, _p, _p, _sz, _p]),
 }
 
 
@@ -372,3 +392,314 @@ def ctr_embedding_bag_bwd_update_phases(grad_pooled: torch.Tensor, g_stride_b: i
                                                    DTYPES[table.dtype], d, total_rows, _ptr(grad_unique_out),
                                                    int(phases), _ptr(ws), ws.numel(), _stream(stream))
     _ok("ctr_embedding_bag_bwd_update_phases", st)
+
+
+# ---------------------------------------------------------------------------
+# expert layer
+# ---------------------------------------------------------------------------
+# These calls take their sizes from the tensors' shapes, so the shapes, types and
+# layouts are checked here: the library sees only pointers.  Matrices may have a
+# row stride; maps, weights, codes and scales are dense.
+def _mat(t: torch.Tensor, what: str, dtypes=(torch.float32, torch.bfloat16)) -> torch.Tensor:
+    """A 2-d CUDA matrix whose rows are contiguous; returns it."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dim() != 2 or t.dtype not in dtypes:
+        raise ValueError(f"{what} must be a matrix of {' or '.join(str(d) for d in dtypes)}, not "
+                         f"{t.dim()}-d {t.dtype}")
+    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{what} must have contiguous rows that do not overlap")
+    return t
+
+
+def _ld(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+
+
+def _dense(t: torch.Tensor, what: str, dtype, shape) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not "
+                         f"{t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _same(t: torch.Tensor, other: torch.Tensor, what: str) -> None:
+    if t.dtype != other.dtype:
+        raise ValueError(f"{what} must be {other.dtype}, not {t.dtype}")
+
+
+def _want(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def ctr_expert_workspace_size() -> int:
+    return int(lib().ctr_expert_workspace_size())
+
+
+def ctr_expert_route_workspace_size(tokens: int, experts: int, k: int) -> int:
+    return int(lib().ctr_expert_route_workspace_size(tokens, experts, k))
+
+
+def ctr_expert_route(scores: torch.Tensor, k: int, renormalize: bool, expert: torch.Tensor, weight: torch.Tensor,
+                     slot: torch.Tensor, token: torch.Tensor, offsets: torch.Tensor, ws: torch.Tensor,
+                     stream=None) -> None:
+    """The k best experts of every token (row of scores), their softmax weights, and the order by expert."""
+    T, E = _mat(scores, "scores").shape
+    i32 = torch.int32
+    _dense(expert, "expert", i32, (T, k))
+    _dense(weight, "weight", torch.float32, (T, k))
+    _dense(slot, "slot", i32, (T, k))
+    _dense(token, "token", i32, (T * k,))
+    _dense(offsets, "offsets", i32, (E + 1,))
+    st = lib().ctr_expert_route(_ptr(scores), DTYPES[scores.dtype], T, E, _ld(scores), int(k), 1 if renormalize else 0,
+                                _ptr(expert), _ptr(weight), _ptr(slot), _ptr(token), _ptr(offsets), _ptr(ws),
+                                ws.numel(), _stream(stream))
+    _ok("ctr_expert_route", st)
+
+
+def ctr_expert_route_bwd(dweight: torch.Tensor, scores: torch.Tensor, renormalize: bool, expert: torch.Tensor,
+                         dscores: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    T, E = _mat(scores, "scores").shape
+    _want(expert.dim() == 2, "expert must be a matrix")
+    k = expert.shape[1]
+    _dense(expert, "expert", torch.int32, (T, k))
+    _dense(dweight, "dweight", torch.float32, (T, k))
+    _same(_mat(dscores, "dscores"), scores, "dscores")
+    _want(dscores.shape == scores.shape, "dscores must have the shape of scores")
+    st = lib().ctr_expert_route_bwd(_ptr(dweight), _ptr(scores), DTYPES[scores.dtype], T, E, _ld(scores), k,
+                                    1 if renormalize else 0, _ptr(expert), _ptr(dscores), _ld(dscores), _ptr(ws),
+                                    ws.numel(), _stream(stream))
+    _ok("ctr_expert_route_bwd", st)
+
+
+def _slots(slot: torch.Tensor, T: int) -> int:
+    _want(isinstance(slot, torch.Tensor) and slot.dim() == 2, "slot must be a matrix")
+    _dense(slot, "slot", torch.int32, (T, slot.shape[1]))
+    return slot.shape[1]
+
+
+def ctr_expert_dispatch(x: torch.Tensor, slot: torch.Tensor, token: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
+                        stream=None) -> None:
+    """Token rows of x into the order by expert: out [T*k, d]."""
+    T, d = _mat(x, "x").shape
+    k = _slots(slot, T)
+    _dense(token, "token", torch.int32, (T * k,))
+    _same(_mat(out, "out"), x, "out")
+    _want(tuple(out.shape) == (T * k, d), f"out must be {(T * k, d)}")
+    st = lib().ctr_expert_dispatch(_ptr(x), DTYPES[x.dtype], T, d, _ld(x), k, _ptr(slot), _ptr(token), _ptr(out),
+                                   _ld(out), _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_expert_dispatch", st)
+
+
+def ctr_expert_combine(rows: torch.Tensor, slot: torch.Tensor, weight: Optional[torch.Tensor], y: torch.Tensor,
+                       ws: torch.Tensor, stream=None) -> None:
+    """Rows [T*k, d] added back to tokens under the weights (None: all 1, the gradient of the dispatch)."""
+    T, d = _mat(y, "y").shape
+    k = _slots(slot, T)
+    _same(_mat(rows, "rows"), y, "rows")
+    _want(tuple(rows.shape) == (T * k, d), f"rows must be {(T * k, d)}")
+    if weight is not None:
+        _dense(weight, "weight", torch.float32, (T, k))
+    st = lib().ctr_expert_combine(_ptr(rows), DTYPES[y.dtype], T, d, _ld(rows), k, _ptr(slot), _ptr(weight), _ptr(y),
+                                  _ld(y), _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_expert_combine", st)
+
+
+def ctr_expert_combine_bwd(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor,
+                           token: torch.Tensor, drows: torch.Tensor, dweight: torch.Tensor, ws: torch.Tensor,
+                           stream=None) -> None:
+    T, d = _mat(dy, "dy").shape
+    k = _slots(slot, T)
+    for t, what in ((rows, "rows"), (drows, "drows")):
+        _same(_mat(t, what), dy, what)
+        _want(tuple(t.shape) == (T * k, d), f"{what} must be {(T * k, d)}")
+    _dense(weight, "weight", torch.float32, (T, k))
+    _dense(dweight, "dweight", torch.float32, (T, k))
+    _dense(token, "token", torch.int32, (T * k,))
+    st = lib().ctr_expert_combine_bwd(_ptr(dy), DTYPES[dy.dtype], T, d, _ld(dy), k, _ptr(rows), _ld(rows), _ptr(slot),
+                                      _ptr(weight), _ptr(token), _ptr(drows), _ld(drows), _ptr(dweight), _ptr(ws),
+                                      ws.numel(), _stream(stream))
+    _ok("ctr_expert_combine_bwd", st)
+
+
+# -- 8-bit products -----------------------------------------------------------
+FP8_COLS_BY_COLUMN, FP8_COLS_BY_BLOCK = 0, 1
+
+
+def fp8_blocks(n: int) -> int:
+    """Blocks of 128 that n elements take."""
+    return -(-int(n) // 128)
+
+
+def fp8_padded(n: int) -> int:
+    """n rounded up to whole blocks: the row length of codes."""
+    return 128 * fp8_blocks(n)
+
+
+def fp8_padded_rows(rows: int, groups: int) -> int:
+    """Row length of the column codes of `rows` rows in `groups` groups."""
+    return int(lib().ctr_fp8_padded_rows(rows, groups))
+
+
+def ctr_fp8_matmul_workspace_size(rows: int, groups: int, n: int, k: int) -> int:
+    return int(lib().ctr_fp8_matmul_workspace_size(rows, groups, n, k))
+
+
+def _scales(scale: torch.Tensor, what: str, blocks: int, rows: int) -> int:
+    """Checks row scales [blocks, rows] (a row stride is allowed); returns the stride."""
+    _mat(scale, what, (torch.float32,))
+    _want(tuple(scale.shape) == (blocks, rows), f"{what} must be {(blocks, rows)}, not {tuple(scale.shape)}")
+    return _ld(scale)
+
+
+def _index(row_index: Optional[torch.Tensor], q: torch.Tensor, x: torch.Tensor) -> int:
+    _want(isinstance(q, torch.Tensor) and q.dim() == 2, "q must be a matrix")
+    rows = q.shape[0]
+    if row_index is not None:
+        _dense(row_index, "row_index", torch.int32, (rows,))
+    else:
+        _want(rows <= x.shape[0], "without row_index, q may not have more rows than x")
+    return rows
+
+
+def ctr_fp8_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, ws: torch.Tensor,
+                          row_index: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Row codes q [rows, padded cols] and scales [blocks, rows] of x, or of its rows row_index."""
+    n, cols = _mat(x, "x").shape
+    rows = _index(row_index, q, x)
+    _dense(q, "q", torch.uint8, (rows, fp8_padded(cols)))
+    lds = _scales(scale, "scale", fp8_blocks(cols), rows)
+    st = lib().ctr_fp8_quantize_rows(_ptr(x), DTYPES[x.dtype], n, rows, cols, _ld(x), _ptr(row_index), _ptr(q),
+                                     _ptr(scale), lds, _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_fp8_quantize_rows", st)
+
+
+def ctr_fp8_quantize_rows_cols(x: torch.Tensor, offsets: torch.Tensor, q: torch.Tensor, scale: torch.Tensor,
+                               qc: torch.Tensor, scale_c: torch.Tensor, cols_by: int, ws: torch.Tensor,
+                               row_index: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Row codes as above, and the column codes qc [cols, padded rows] of the grouped rows, in one read of x."""
+    n, cols = _mat(x, "x").shape
+    rows = _index(row_index, q, x)
+    groups = offsets.numel() - 1
+    _dense(offsets, "offsets", torch.int32, (groups + 1,))
+    _want(groups >= 1, "offsets must have at least two entries")
+    padded = fp8_padded_rows(rows, groups)
+    _dense(q, "q", torch.uint8, (rows, fp8_padded(cols)))
+    lds = _scales(scale, "scale", fp8_blocks(cols), rows)
+    _dense(qc, "qc", torch.uint8, (cols, padded))
+    _dense(scale_c, "scale_c", torch.float32, (padded // 128, cols) if cols_by == FP8_COLS_BY_COLUMN
+           else (fp8_blocks(cols), padded // 128))
+    st = lib().ctr_fp8_quantize_rows_cols(_ptr(x), DTYPES[x.dtype], n, rows, cols, _ld(x), _ptr(row_index),
+                                          _ptr(offsets), groups, int(cols_by), _ptr(q), _ptr(scale), lds, _ptr(qc),
+                                          _ptr(scale_c), _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_fp8_quantize_rows_cols", st)
+
+
+def ctr_fp8_quantize_blocks(w: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, ws: torch.Tensor,
+                            qt: Optional[torch.Tensor] = None, scale_t: Optional[torch.Tensor] = None,
+                            stream=None) -> None:
+    """Block codes of w [groups, n, k], and of its transpose where qt and scale_t are given."""
+    _want(isinstance(w, torch.Tensor) and w.dim() == 3 and w.dtype in DTYPES, "w must be [groups, n, k] fp32 or bf16")
+    G, n, k = w.shape
+    _dense(w, "w", w.dtype, (G, n, k))
+    _dense(q, "q", torch.uint8, (G, n, fp8_padded(k)))
+    _dense(scale, "scale", torch.float32, (G, fp8_blocks(n), fp8_blocks(k)))
+    if qt is not None or scale_t is not None:
+        _want(qt is not None and scale_t is not None, "qt and scale_t go together")
+        _dense(qt, "qt", torch.uint8, (G, k, fp8_padded(n)))
+        _dense(scale_t, "scale_t", torch.float32, (G, fp8_blocks(k), fp8_blocks(n)))
+    st = lib().ctr_fp8_quantize_blocks(_ptr(w), DTYPES[w.dtype], G, n, k, _ptr(q), _ptr(scale), _ptr(qt),
+                                       _ptr(scale_t), _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_fp8_quantize_blocks", st)
+
+
+def ctr_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
+                   offsets: Optional[torch.Tensor], out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """out[r] = W_g a_r for the rows of each group, from row codes a [rows, P(k)] and block codes b [groups, n, P(k)]."""
+    _want(isinstance(b, torch.Tensor) and b.dim() == 3, "b must be [groups, n, padded k]")
+    G, n, kp = b.shape
+    rows = _mat(out, "out").shape[0]
+    _want(kp % 128 == 0 and kp > 0, "codes must have whole blocks of 128")
+    _want(out.shape[1] == n, f"out must have {n} columns")
+    _dense(a, "a", torch.uint8, (rows, kp))
+    _dense(b, "b", torch.uint8, (G, n, kp))
+    lds = _scales(a_scale, "a_scale", kp // 128, rows)
+    _dense(b_scale, "b_scale", torch.float32, (G, fp8_blocks(n), kp // 128))
+    if offsets is not None:
+        _dense(offsets, "offsets", torch.int32, (G + 1,))
+    st = lib().ctr_fp8_matmul(_ptr(a), _ptr(a_scale), lds, _ptr(b), _ptr(b_scale), _ptr(offsets), rows, G, n, kp,
+                              _ptr(out), DTYPES[out.dtype], _ld(out), _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_fp8_matmul", st)
+
+
+def ctr_fp8_matmul_wgrad(d: torch.Tensor, d_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
+                         offsets: torch.Tensor, out: torch.Tensor, ws: torch.Tensor, rows: Optional[int] = None,
+                         stream=None) -> None:
+    """out[g] = d_g^T x_g [n, k] from column codes of d (by column) and of x (by block).
+
+    `rows` is the row count the codes were made for (it fixes their padding); by
+    default the largest that has the codes' padded length."""
+    _want(isinstance(out, torch.Tensor) and out.dim() == 3 and out.dtype in DTYPES, "out must be [groups, n, k]")
+    G, n, k = out.shape
+    _dense(out, "out", out.dtype, (G, n, k))
+    _want(isinstance(d, torch.Tensor) and d.dim() == 2, "d must be a matrix")
+    padded = d.shape[1]
+    if rows is None:
+        rows = _rows_of_padding(padded, G)
+    _want(fp8_padded_rows(rows, G) == padded, f"codes of {rows} rows in {G} groups are {fp8_padded_rows(rows, G)} long")
+    _dense(d, "d", torch.uint8, (n, padded))
+    _dense(x, "x", torch.uint8, (k, padded))
+    _dense(d_scale, "d_scale", torch.float32, (padded // 128, n))
+    _dense(x_scale, "x_scale", torch.float32, (fp8_blocks(k), padded // 128))
+    _dense(offsets, "offsets", torch.int32, (G + 1,))
+    st = lib().ctr_fp8_matmul_wgrad(_ptr(d), _ptr(d_scale), _ptr(x), _ptr(x_scale), _ptr(offsets), rows, G, n, k,
+                                    _ptr(out), DTYPES[out.dtype], _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_fp8_matmul_wgrad", st)
+
+
+def _rows_of_padding(padded: int, groups: int) -> int:
+    """The most rows whose column codes are `padded` long: ctr_fp8_padded_rows is 128 max(1, min((rows + 127
+    groups) / 128, rows))."""
+    tiles = padded // 128
+    return max(tiles, (tiles + 1) * 128 - 1 - 127 * groups)
+
+
+# -- gradient clipping ----------------------------------------------------------
+class GradList:
+    """Host arrays of ctr_clip_grads for a list of tensors (built once, kept alive with them)."""
+
+    def __init__(self, grads, outs):
+        n = len(grads)
+        self.n, self.grads, self.outs = n, list(grads), None if outs is None else list(outs)
+        self.ptrs = (C.c_void_p * max(1, n))(*[t.data_ptr() for t in grads])
+        self.out_ptrs = None if outs is None else (C.c_void_p * max(1, n))(*[t.data_ptr() for t in outs])
+        self.dtypes = (C.c_int32 * max(1, n))(*[DTYPES[t.dtype] for t in grads])
+        self.counts = (C.c_int64 * max(1, n))(*[t.numel() for t in grads])
+
+
+def grad_list(grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None) -> GradList:
+    """A list for ctr_clip_grads: dense fp32 or bf16 CUDA tensors, and where the clipped ones go
+    (`grads` itself for in place; None for the norm alone)."""
+    for t in list(grads) + list(outs or []):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in DTYPES or not t.is_contiguous():
+            raise ValueError("gradients must be contiguous fp32 or bf16 CUDA tensors")
+    if outs is not None:
+        _want(len(outs) == len(grads), "outs must be as many as grads")
+        for g, o in zip(grads, outs):
+            _want(g.dtype == o.dtype and g.numel() == o.numel(), "outs must have the types and sizes of grads")
+    return GradList(grads, outs)
+
+
+def ctr_clip_grads_workspace_size() -> int:
+    return int(lib().ctr_clip_grads_workspace_size())
+
+
+def ctr_clip_grads(grads: GradList, max_norm: float, norm: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    """The global norm of a grad_list into norm (fp32 [1]), and its outs = grads * min(1, max_norm / norm)."""
+    _dense(norm, "norm", torch.float32, (1,))
+    st = lib().ctr_clip_grads(grads.ptrs, grads.out_ptrs, grads.dtypes, grads.counts, grads.n, float(max_norm),
+                              _ptr(norm), _ptr(ws), ws.numel(), _stream(stream))
+    _ok("ctr_clip_grads", st)
