@@ -3,14 +3,15 @@
 //   norm = sqrt(sum g^2),  out = g * (norm > max_norm ? max_norm / norm : 1)
 //
 // The tensors are cut into chunks of kChunk elements, handed to the blocks in a
-// fixed order.  A thread squares and adds 16-byte pieces in fp32 (four
-// accumulators), moves them into fp64 every few chunks, and joins are fp64 in a
-// fixed order, so the result does not change from run to run.  A piece whose
-// largest magnitude would leave fp32's range when squared (or lose its square
-// below it) is squared in fp64 instead; for gradients of ordinary size that
-// branch is never taken.  The last block to finish adds the blocks' sums up.
-// Two passes over the data, bound by HBM: the second walks the chunks in
-// reverse, so what the first read last is still in L2.
+// fixed order.  A thread squares and adds its part of a chunk in fp32 (four
+// accumulators), adds up to kFlush chunks in fp32 and then moves the sum into
+// fp64; joins are fp64 in a fixed order, so the result does not change from run
+// to run.  A part whose sum of squares comes near either end of fp32's range is
+// read again and squared in fp64 by its warp (fp64 in the common path, even
+// predicated off, tripled the pass: 724 us against 230 for 5e8 elements).  The
+// last block to finish adds the blocks' sums up.  Two passes over the data, bound
+// by HBM: the second walks the chunks in reverse, so what the first read last is
+// still in L2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -27,8 +28,11 @@ constexpr int kListMax = 256;       // tensors of one launch
 constexpr int kClipBlocksPerSm = 6;
 constexpr int kMaxBlocks = 2048;    // bound of the grid, for the workspace
 constexpr int kFlush = 8;           // chunks between moves of the fp32 sums into fp64
-constexpr float kBig = 0x1p50f;     // squares of larger values (2^100) could overflow in a sum
-constexpr float kSmall = 0x1p-55f;  // squares of smaller ones (2^-110) lose accuracy near fp32's floor
+// A thread's sum over its part of a chunk is used within these bounds: above, a sum of them could
+// overflow; below, squares that fall under fp32's smallest numbers would weigh in (at or above it
+// they are under 2^-149 x 32 of 2^-100).
+constexpr float kBig = 0x1p100f;
+constexpr float kSmall = 0x1p-100f;
 
 struct ClipList {
   const void* g[kListMax];
@@ -56,50 +60,57 @@ __device__ __forceinline__ int tensor_of(const ClipList& l, int64_t chunk) {
   return lo;
 }
 
-template <int N>
-__device__ __forceinline__ void add_squares(const float (&f)[N], float (&acc)[4], double& wide) {
-  float m = 0.f;
+// Sum of squares of this thread's part of a chunk: 16-byte pieces where the chunk is aligned.
+template <typename T>
+__device__ __forceinline__ float chunk_squares(const T* g, int n) {
+  constexpr int per = 16 / (int)sizeof(T);
+  constexpr int pieces = kChunk / per / kClipThreads;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  int i0 = 0;
+  if (((uintptr_t)g & 15) == 0) {
+    const int full = n / per;
+    i0 = full * per;
+    uint4 raw[pieces];
 #pragma unroll
-  for (int i = 0; i < N; ++i) m = fmaxf(m, fabsf(f[i]));
-  if (m > kBig || (m < kSmall && m > 0.f)) {
+    for (int p = 0; p < pieces; ++p) {
+      const int i = threadIdx.x + p * kClipThreads;
+      raw[p] = i < full ? ((const uint4*)g)[i] : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-    for (int i = 0; i < N; ++i) wide += (double)f[i] * (double)f[i];
-  } else {
+    for (int p = 0; p < pieces; ++p) {
+      float f[per];
+      Chunk<T, 16>::unpack(raw[p], f);
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i & 3] = fmaf(f[i], f[i], acc[i & 3]);
+      for (int i = 0; i < per; ++i) acc[i & 3] = fmaf(f[i], f[i], acc[i & 3]);
+    }
   }
+#pragma unroll 4
+  for (int i = i0 + threadIdx.x; i < n; i += kClipThreads) {
+    const float f = to_f32<T>(g[i]);
+    acc[0] = fmaf(f, f, acc[0]);
+  }
+  return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
+// The same elements of the same thread in fp64.
 template <typename T>
-__device__ __forceinline__ void chunk_squares(const T* g, int n, float (&acc)[4], double& wide) {
+__device__ __noinline__ double chunk_squares_wide(const T* g, int n) {
   constexpr int per = 16 / (int)sizeof(T);
+  double s = 0.0;
   int i0 = 0;
   if (((uintptr_t)g & 15) == 0) {
     i0 = n / per * per;
-    constexpr int pieces = kChunk / per / kClipThreads;
-    const int full = n / per;
-    if (n == kChunk) {
-      uint4 raw[pieces];
-#pragma unroll
-      for (int p = 0; p < pieces; ++p) raw[p] = ((const uint4*)g)[threadIdx.x + p * kClipThreads];
-#pragma unroll
-      for (int p = 0; p < pieces; ++p) {
-        float f[per];
-        Chunk<T, 16>::unpack(raw[p], f);
-        add_squares(f, acc, wide);
+    for (int p = threadIdx.x * per; p < i0; p += kClipThreads * per)
+      for (int e = 0; e < per; ++e) {
+        const float f = to_f32<T>(g[p + e]);
+        if (f != 0.f) s += (double)f * (double)f;  // true for NaN
       }
-    } else {
-      for (int p = threadIdx.x; p < full; p += kClipThreads) {
-        float f[per];
-        Chunk<T, 16>::unpack(((const uint4*)g)[p], f);
-        add_squares(f, acc, wide);
-      }
-    }
   }
   for (int i = i0 + threadIdx.x; i < n; i += kClipThreads) {
-    const float f[1] = {to_f32<T>(g[i])};
-    add_squares(f, acc, wide);
+    const float f = to_f32<T>(g[i]);
+    if (f != 0.f) s += (double)f * (double)f;
   }
+  return s;
 }
 
 __global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constant__ ClipList l, ClipState* st,
@@ -107,22 +118,30 @@ __global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constan
                                                             int last) {
   __shared__ double warp_sum[kClipThreads / 32];
   __shared__ bool am_last;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float acc = 0.f;
   double wide = 0.0;
   int since = 0;
   for (int64_t c = blockIdx.x; c < l.first[l.count]; c += gridDim.x) {
     const int t = tensor_of(l, c);
     const int64_t e0 = (c - l.first[t]) * kChunk;
     const int n = (int)imin64(kChunk, l.n[t] - e0);
-    if (l.dtype[t] == CTR_F32) chunk_squares((const float*)l.g[t] + e0, n, acc, wide);
-    else chunk_squares((const __nv_bfloat16*)l.g[t] + e0, n, acc, wide);
+    const bool f32 = l.dtype[t] == CTR_F32;
+    const float* g32 = (const float*)l.g[t] + e0;
+    const __nv_bfloat16* g16 = (const __nv_bfloat16*)l.g[t] + e0;
+    const float sum = f32 ? chunk_squares(g32, n) : chunk_squares(g16, n);
+    const bool odd = !(sum <= kBig) || (sum < kSmall && (int)threadIdx.x < n);
+    if (__any_sync(kFull, odd)) {
+      wide += f32 ? chunk_squares_wide(g32, n) : chunk_squares_wide(g16, n);
+    } else {
+      acc += sum;
+    }
     if (++since == kFlush) {
-      wide += (double)((acc[0] + acc[1]) + (acc[2] + acc[3]));
-      acc[0] = acc[1] = acc[2] = acc[3] = 0.f;
+      wide += (double)acc;
+      acc = 0.f;
       since = 0;
     }
   }
-  wide += (double)((acc[0] + acc[1]) + (acc[2] + acc[3]));
+  wide += (double)acc;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) wide += __shfl_down_sync(kFull, wide, o);
   if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = wide;

@@ -7,13 +7,15 @@
 //
 // Rows: 16 lanes hold a block of 128 values, 8 each (one or two 16-byte loads),
 // the maximum is four xor-shuffles, and the 128 codes leave as one 128-byte
-// store of 8 bytes a lane.  Bound by HBM.
+// store of 8 bytes a lane.  A lane group takes up to four blocks of one row at
+// once, so four loads are in flight and no index is divided.  Bound by HBM.
 //
 // Tiles (rows + columns, blocks): a CTA reads a 128 x 128 tile once, keeps it in
 // shared memory in its own type, and writes both orders of codes from it, each
 // as 128 consecutive bytes: a second pass over x would cost as much as the
-// first.  The column order is read back one column to a pair of threads, 64
-// values each, so their codes leave in 16-byte stores.
+// first.  For the column order a thread holds 32 rows of two neighbouring columns
+// in registers (one shared-memory read of both columns' values per row) for the
+// maximum and for the codes, which leave in 16-byte stores.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -33,14 +35,18 @@ constexpr int kQThreads = 256;
 // NaN stays NaN (the comparison is false for it).
 __device__ __forceinline__ float at_least_floor(float m) { return m < kFloor ? kFloor : m; }
 
-// The larger magnitude, NaN winning: magnitudes compare as their bits.
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger magnitude, NaN winning.
+__device__ __forceinline__ float max_mag(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
 
 template <int N>
-__device__ __forceinline__ uint32_t max_bits(const float (&v)[N]) {
-  uint32_t m = 0;
+__device__ __forceinline__ float max_mag(const float (&v)[N]) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) m = max(m, mag_bits(v[i]));
+  for (int i = 0; i < N; ++i) m = max_mag(m, v[i]);
   return m;
 }
 
@@ -79,37 +85,39 @@ __device__ __forceinline__ int64_t source_row(const int32_t* row_index, int64_t 
   return i;
 }
 
+constexpr int kRowBlocks = 4;  // blocks of one row that a lane group takes at once
+
 template <typename T>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* x, int64_t x_rows, int64_t rows,
                                                                   int64_t cols, int64_t ldx, int vec,
                                                                   const int32_t* row_index, uint8_t* q, float* scale,
-                                                                  int64_t ld_scale, int blocks_per_row, int* err) {
-  const int64_t pad = (int64_t)blocks_per_row * 128;
+                                                                  int64_t ld_scale, int blocks, int* err) {
   const int lane16 = threadIdx.x & 15;
-  const int64_t units = rows * blocks_per_row;  // blocks of 128, one to 16 lanes
-  const int64_t step = (int64_t)gridDim.x * (kQThreads / 16);
-  const int64_t trips = ceil_div(units, step);  // the same in every lane: the shuffles need all of them
-  int64_t u = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);
-  for (int64_t trip = 0; trip < trips; ++trip, u += step) {
-    const bool mine = u < units;
-    const int64_t r = mine ? u / blocks_per_row : 0;
-    const int kb = mine ? (int)(u - r * blocks_per_row) : 0;
-    float v[8];
-    const int64_t src = mine ? source_row(row_index, r, x_rows, err) : -1;
-    if (src >= 0) {
-      load8(x + src * ldx, (int64_t)kb * 128 + lane16 * 8, cols, vec != 0, v);
+  const int64_t r = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);
+  const int kb0 = blockIdx.y * kRowBlocks;
+  const int64_t src = r < rows ? source_row(row_index, r, x_rows, err) : -1;
+  const T* row = x + (src >= 0 ? src * ldx : 0);
+  float v[kRowBlocks][8];
+#pragma unroll
+  for (int b = 0; b < kRowBlocks; ++b) {
+    if (src >= 0 && kb0 + b < blocks) {
+      load8(row, (int64_t)(kb0 + b) * 128 + lane16 * 8, cols, vec != 0, v[b]);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      for (int i = 0; i < 8; ++i) v[b][i] = 0.f;
     }
-    uint32_t m = max_bits(v);
+  }
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-    const float amax = at_least_floor(__uint_as_float(m));
+  for (int b = 0; b < kRowBlocks; ++b) {
+    float m = max_mag(v[b]);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, o));
+    const float amax = at_least_floor(m);
     const float inv = __fdiv_rn(kTop, amax);
-    if (mine) {
-      *(uint2*)(q + r * pad + (int64_t)kb * 128 + lane16 * 8) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
-      if (lane16 == 0) scale[kb * ld_scale + r] = __fdiv_rn(amax, kTop);
+    if (r < rows && kb0 + b < blocks) {
+      *(uint2*)(q + (r * blocks + kb0 + b) * 128 + lane16 * 8) =
+          make_uint2(codes4(v[b], inv), codes4(v[b] + 4, inv));
+      if (lane16 == 0) scale[(kb0 + b) * ld_scale + r] = __fdiv_rn(amax, kTop);
     }
   }
 }
@@ -129,16 +137,26 @@ struct TileArgs {
   int* err;
 };
 
+// Values of two neighbouring columns of a tile row.
+__device__ __forceinline__ float2 two(const float* p) { return *(const float2*)p; }
+__device__ __forceinline__ float2 two(const __nv_bfloat16* p) { return __bfloat1622float2(*(const __nv_bfloat162*)p); }
+
+// A tile row is 128 elements and 16 bytes more: 16-byte stores stay aligned and a row's do not
+// meet the next one's banks.
+template <typename T>
+constexpr int tile_ld() {
+  return 128 + 16 / (int)sizeof(T);
+}
+
 // One 128 x 128 tile.  ROW_BLOCK: the row codes have one scale for the tile (else one a row);
 // COL_BLOCK: the column codes have (else one a column).
 template <typename T, bool ROW_BLOCK, bool COL_BLOCK>
 __global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs a) {
-  // a row of the tile is 128 elements and 8 bytes more, so that a column's reads spread over the banks
-  constexpr int kLd = 128 + 8 / (int)sizeof(T);
+  constexpr int kLd = tile_ld<T>();
   extern __shared__ __align__(16) uint8_t smem[];
   T* tile = (T*)smem;
-  __shared__ uint32_t col_max[2][128];
-  __shared__ uint32_t warp_max[kQThreads / 32];
+  __shared__ float col_max[4][128];
+  __shared__ float warp_max[kQThreads / 32];
   __shared__ int where[4];  // group, first row, rows, tile number (of all groups)
   const int col0 = blockIdx.y * 128;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -198,7 +216,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs
   // Row order: 16 lanes a row, 8 values each; rows past n are zeros (the column codes' filling).
   const int lane16 = threadIdx.x & 15;
   const int64_t qcol = col0 + lane16 * 8;
-  uint32_t tile_max = 0;
+  float tile_max = 0.f;
 #pragma unroll 4
   for (int p = 0; p < 8; ++p) {
     const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
@@ -211,17 +229,20 @@ __global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.f;
     }
-    T* dst = tile + i * kLd + lane16 * 8;
+    constexpr int per = 16 / (int)sizeof(T);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dst[e] = from_f32<T>(v[e]);
-    uint32_t m = max_bits(v);
-    if constexpr (ROW_BLOCK) {
-      tile_max = max(tile_max, m);
-    } else {
-      if constexpr (COL_BLOCK) tile_max = max(tile_max, m);
+    for (int e = 0; e < 8; e += per) {
+      float f[per];
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-      const float amax = at_least_floor(__uint_as_float(m));
+      for (int b = 0; b < per; ++b) f[b] = v[e + b];
+      *(uint4*)(tile + i * kLd + lane16 * 8 + e) = Chunk<T, 16>::pack(f);
+    }
+    float m = max_mag(v);
+    if constexpr (ROW_BLOCK || COL_BLOCK) tile_max = max_mag(tile_max, m);
+    if constexpr (!ROW_BLOCK) {
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, o));
+      const float amax = at_least_floor(m);
       const float inv = __fdiv_rn(kTop, amax);
       if (i < n) {
         *(uint2*)(a.q + (int64_t)(row0 + i) * a.ldq + qcol) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
@@ -231,13 +252,14 @@ __global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs
   }
   float block_amax = 0.f, block_inv = 0.f;
   if constexpr (ROW_BLOCK || COL_BLOCK) {
-    tile_max = __reduce_max_sync(kFull, tile_max);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) tile_max = max_mag(tile_max, __shfl_xor_sync(kFull, tile_max, o));
     if (lane == 0) warp_max[warp] = tile_max;
     __syncthreads();
-    tile_max = 0;
+    tile_max = 0.f;
 #pragma unroll
-    for (int w = 0; w < kQThreads / 32; ++w) tile_max = max(tile_max, warp_max[w]);
-    block_amax = at_least_floor(__uint_as_float(tile_max));
+    for (int w = 0; w < kQThreads / 32; ++w) tile_max = max_mag(tile_max, warp_max[w]);
+    block_amax = at_least_floor(tile_max);
     block_inv = __fdiv_rn(kTop, block_amax);
   } else {
     __syncthreads();
@@ -248,10 +270,8 @@ __global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs
     for (int p = 0; p < 8; ++p) {
       const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
       if (i >= n) continue;
-      const T* src = tile + i * kLd + lane16 * 8;
       float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = to_f32<T>(src[e]);
+      load8(tile + i * kLd, lane16 * 8, 128, true, v);
       *(uint2*)(a.q + (xbase + row0 + i) * a.ldq + qcol) =
           make_uint2(codes4(v, block_inv), codes4(v + 4, block_inv));
     }
@@ -262,46 +282,73 @@ __global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs
     }
     if (!a.qt) return;
   }
-  // Column order: a column to two threads, 64 of its rows each.
-  const int c = threadIdx.x & 127, half = threadIdx.x >> 7;
-  float amax = block_amax, inv = block_inv;
+  // Column order: two columns and 32 of their rows to a thread.
+  const int c = (threadIdx.x & 63) * 2, part = threadIdx.x >> 6;
+  float2 v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = two(tile + (part * 32 + i) * kLd + c);
+  float inv0 = block_inv, inv1 = block_inv;
   if constexpr (!COL_BLOCK) {
-    uint32_t m = 0;
-#pragma unroll 8
-    for (int i = 0; i < 64; ++i) m = max(m, mag_bits(to_f32<T>(tile[(half * 64 + i) * kLd + c])));
-    col_max[half][c] = m;
+    float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      m0 = max_mag(m0, v[i].x);
+      m1 = max_mag(m1, v[i].y);
+    }
+    *(float2*)&col_max[part][c] = make_float2(m0, m1);
     __syncthreads();
-    amax = at_least_floor(__uint_as_float(max(col_max[0][c], col_max[1][c])));
-    inv = __fdiv_rn(kTop, amax);
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      m0 = max_mag(m0, col_max[p][c]);
+      m1 = max_mag(m1, col_max[p][c + 1]);
+    }
+    m0 = at_least_floor(m0);
+    m1 = at_least_floor(m1);
+    inv0 = __fdiv_rn(kTop, m0);
+    inv1 = __fdiv_rn(kTop, m1);
+    if (part == 0) {
+      float* s = a.scale_t + (int64_t)tnum * a.ld_scale_t + col0 + c;
+      if (col0 + c < a.cols) s[0] = __fdiv_rn(m0, kTop);
+      if (col0 + c + 1 < a.cols) s[1] = __fdiv_rn(m1, kTop);
+    }
+  } else if constexpr (!ROW_BLOCK) {
+    if (threadIdx.x == 0) a.scale_t[(int64_t)blockIdx.y * a.ld_scale_t + tnum] = __fdiv_rn(block_amax, kTop);
   }
-  if (col0 + c >= a.cols) return;
-  const int64_t qrow = (ROW_BLOCK ? (int64_t)g * a.cols : 0) + col0 + c;
-  uint4* out = (uint4*)(a.qt + qrow * a.ldt + (int64_t)tnum * 128 + half * 64);
+  // The codes go through shared memory (over the tile, which is in registers now), so that eight
+  // lanes write a column's 128 bytes together: 32-byte pieces straight from the registers made the
+  // pass a third slower.
+  constexpr int kCodeLd = 144;
+  uint8_t* codes = smem;
+  __syncthreads();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = h ? v[4 * b + e].y : v[4 * b + e].x;
+      w[b] = codes4(f, h ? inv1 : inv0);
+    }
+    uint4* dst = (uint4*)(codes + (c + h) * kCodeLd + part * 32);
+    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+  __syncthreads();
+  const int64_t qrow = (ROW_BLOCK ? (int64_t)g * a.cols : 0) + col0;
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    uint32_t w[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = to_f32<T>(tile[(half * 64 + p * 16 + b * 4 + e) * kLd + c]);
-      w[b] = codes4(v, inv);
-    }
-    out[p] = make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  if constexpr (!ROW_BLOCK) {
-    if constexpr (COL_BLOCK) {
-      if (threadIdx.x == 0) a.scale_t[(int64_t)blockIdx.y * a.ld_scale_t + tnum] = __fdiv_rn(amax, kTop);
-    } else {
-      if (half == 0) a.scale_t[(int64_t)tnum * a.ld_scale_t + col0 + c] = __fdiv_rn(amax, kTop);
-    }
+    const int cc = p * 32 + (threadIdx.x >> 3), piece = threadIdx.x & 7;
+    if (col0 + cc < a.cols)
+      *(uint4*)(a.qt + (qrow + cc) * a.ldt + (int64_t)tnum * 128 + piece * 16) =
+          *(const uint4*)(codes + cc * kCodeLd + piece * 16);
   }
 }
 
 template <typename T, bool ROW_BLOCK, bool COL_BLOCK>
 int launch_tiles(const TileArgs& a, int64_t tiles, cudaStream_t s) {
   auto k = quantize_tile_kernel<T, ROW_BLOCK, COL_BLOCK>;
-  const int smem = 128 * (128 * (int)sizeof(T) + 8);
+  const int smem = 128 * tile_ld<T>() * (int)sizeof(T);
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return CTR_ERR_CUDA;
   k<<<dim3((unsigned)tiles, (unsigned)a.col_blocks), kQThreads, smem, s>>>(a);
   count_launch();
@@ -327,14 +374,14 @@ extern "C" int ctr_fp8_quantize_rows(const void* x, ctr_dtype dtype, int64_t x_r
   if (!dtype_ok(dtype) || x_rows < 0 || rows < 0 || cols < 1 || ldx < cols || ld_scale < rows)
     return CTR_ERR_INVALID_ARG;
   if (!row_index && rows > x_rows) return CTR_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || cols > INT32_MAX) return CTR_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || cols > 65535 * 128) return CTR_ERR_UNSUPPORTED;
   if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
   if (rows == 0) return CTR_OK;
   const int eb = dtype_bytes(dtype);
   if (!x || !q || !scale || ((uintptr_t)x % eb) || !aligned16(q)) return CTR_ERR_INVALID_ARG;
   const int vec = aligned16(x) && (ldx * eb) % 16 == 0;
   const int kb = (int)ceil_div(cols, 128);
-  const int grid = (int)imin64(ceil_div(rows * kb, kQThreads / 16), (int64_t)num_sms() * 16);
+  const dim3 grid((unsigned)ceil_div(rows, kQThreads / 16), (unsigned)ceil_div(kb, kRowBlocks));
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == CTR_F32)
     quantize_rows_kernel<<<grid, kQThreads, 0, s>>>((const float*)x, x_rows, rows, cols, ldx, vec, row_index, q,

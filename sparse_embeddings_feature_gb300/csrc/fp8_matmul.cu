@@ -6,16 +6,21 @@
 // S is four tcgen05.mma (kind::f8f6f4, K = 32 each) into a fresh fp32 TMEM
 // accumulator; the scaled sum over kb lives in registers.  Scales are arbitrary
 // fp32 numbers, so they cannot ride in the instruction (which takes powers of
-// two); what it costs is reading every block's accumulator back once: 128 x 256
-// values at 128 lanes a clock, half the time that the block's products take, and
-// hidden behind them.
+// two); what it costs is reading every block's accumulator back once, beside the
+// next block's products.
 //
-// Roles (persistent CTAs, one per SM): warp 0 loads the 128-byte-wide operand
-// tiles by TMA (128-byte swizzle, a ring of stages), warp 1 owns TMEM and issues
-// the MMAs into two accumulators in turn, warps 2..9 scale and add: a thread
-// owns one row (TMEM lane) and half of the tile's columns, so a row scale is one
-// register and a block scale is uniform, and one packed multiply-add covers two
-// values.  A tile's rows never leave their group: rows past it belong to the
+// PAIR: two CTAs of a cluster (two SMs) share one 256 x 256 tile: each holds 128
+// rows of either operand (32 KB a block of 128), the even one issues the
+// cta_group::2 MMAs for both, and each keeps the 128 rows of the accumulator that
+// are its own.  A single CTA takes 128 x 128.  The operand tiles come through L2,
+// whose share of an SM (about 70 bytes a cycle) is what 128 x 256 tiles of one CTA
+// ran into: 48 KB a block take 700 cycles, the products 512.
+//
+// Roles: warp 0 loads the operand tiles by TMA (128-byte swizzle, a ring of
+// stages); warp 1 of the issuing CTA owns the MMAs, into two accumulators in turn;
+// warp 2 copies the scales to shared memory, eight blocks at a time; 8 warps scale
+// and add: a thread owns one row (TMEM lane) and half of the columns, and one
+// packed multiply-add covers two values.  A tile's rows never leave their group: rows past it belong to the
 // next group or lie outside the tensor (TMA fills zeros) and are not stored.
 // Every mbarrier wait is bounded by a wall-clock limit; on expiry the kernel
 // records CTR_ERR_TIMEOUT, waits (bounded) for its own copies and MMAs, frees
@@ -32,13 +37,27 @@
 namespace ctr {
 namespace {
 
-constexpr int kMmThreads = 320;      // producer, issuer, 8 scaling warps
 constexpr int kScaleWarps = 8;
-constexpr int kBM = 128;             // rows of a tile
-constexpr uint32_t kABytes = kBM * 128;
-constexpr int kSuper = 8;            // row tiles that take the column tiles together
-constexpr uint32_t kStageRow = 17;   // words of a staged row (16 data words), odd: no bank conflicts
-constexpr uint32_t kStagingBytes = 32 * kStageRow * 4;
+constexpr int kMmThreads = 128 + 32 * kScaleWarps;  // warps 0..3: loads, MMAs, scales, none; then scaling
+// Registers: 384 threads are launched with 168 each (the most that three warps to a scheduler
+// leave); the first four warps give some up so that a scaling thread can hold 128 sums and 64 values
+// on their way.  56 x 128 + 224 x 256 = 168 x 384.
+constexpr int kLaunchRegs = 168, kControlRegs = 56, kScaleRegs = 224;
+static_assert(kControlRegs * 128 + kScaleRegs * 32 * kScaleWarps <= kLaunchRegs * kMmThreads,
+              "more registers than launched");
+constexpr int kBM = 128;                        // rows of either operand that a CTA holds
+constexpr uint32_t kOperandBytes = kBM * 128;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr int kStages = 4;
+constexpr int kSuper = 8;                       // row tiles that take the column tiles together
+constexpr int kChunk = 8;                       // blocks whose scales come together
+// A scaling warp's pieces of the result on their way out: 32 rows of 128 bytes each, two of them, in
+// the 128-byte swizzle (16-byte part i of row r at i ^ (r mod 8)).
+constexpr uint32_t kPieceBytes = 32 * 128;
+constexpr uint32_t kStagingBytes = 2 * kPieceBytes;
+// Scales: two chunks of [block][row], then two of [128-column half][block].
+constexpr uint32_t kScaleBytes = 2 * kChunk * (kBM + 2) * 4;
+constexpr int kMmSmem = (int)(1024 + kStages * kStageBytes + kScaleWarps * kStagingBytes + kScaleBytes);
 
 struct MmArgs {
   const float* sa;
@@ -50,7 +69,7 @@ struct MmArgs {
   int64_t rows;
   int32_t groups, m, n, kb;  // m: rows of a group's result (weight gradient); kb: blocks (product)
   int32_t nt, mt;            // column tiles; row tiles of a group (weight gradient)
-  int32_t out_f32, wide_rows;  // wide_rows: output rows start 32-byte aligned
+  int32_t out_f32, wide_rows;  // wide_rows: output rows start 16-byte aligned, and TMA may store them
 };
 
 // kind::f8f6f4 instruction descriptor: e4m3 x e4m3 -> fp32, both K-major.
@@ -58,27 +77,102 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// The issued MMAs' completion arrives at the barrier `bar`, in both CTAs of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+// Loads into this CTA's shared memory, counted at `bar` (of the pair's even CTA).
+template <bool PAIR>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+  else
+    tma_load_2d(dst, map, c0, c1, bar);
+}
+
+// Address of the same variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+// Bounded wait of a whole warp.  The hint lets the hardware park the warp for up to 20 us a try:
+// warps that poll take issue slots from the ones that scale.
+__device__ __forceinline__ bool park(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(kFull, ok)) return true;
+    if (t0 == 0) t0 = globaltimer();
+    if (__any_sync(kFull, globaltimer() - t0 > kWaitLimitNs)) return false;
+  }
+}
+
+// One lane of the warp, the same every time.  The roles' loops are run by whole warps, so that
+// their values stay in uniform registers; only the copies, MMAs and arrivals are one lane's.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
-__device__ __forceinline__ void tmem_ld16_async(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// Arrival at a barrier of either CTA.  Release at CTA scope (the default): what it orders are this
+// thread's accumulator reads, which are complete; at cluster scope an arrival took 1500 cycles.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// acc += f * v for 16 values, two at a time.  volatile: stays after the wait for the load of v.
-__device__ __forceinline__ void scale_add16(uint64_t* acc, const uint32_t (&v)[16], uint64_t f2) {
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// acc += f * v for 32 values, two at a time.  volatile: stays after the wait for the load of v.
+__device__ __forceinline__ void scale_add32(uint64_t* acc, const uint32_t (&v)[32], uint64_t f2) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 16; ++i)
     asm volatile(
         "{\n\t.reg .b64 t;\n\t"
         "mov.b64 t, {%1, %2};\n\t"
@@ -87,9 +181,10 @@ __device__ __forceinline__ void scale_add16(uint64_t* acc, const uint32_t (&v)[1
         : "r"(v[2 * i]), "r"(v[2 * i + 1]), "l"(f2));
 }
 
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+// One fp32 number into shared memory, without waiting; zero where `take` is false (then `any` is a
+// valid address that is not read).
+__device__ __forceinline__ void copy_scale(uint32_t dst, const float* src, bool take, const float* any) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(take ? src : any), "r"(take ? 4 : 0)
                : "memory");
 }
 
@@ -100,34 +195,36 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 
 struct Tile {
   int32_t nkb;        // blocks to sum
-  int32_t rows;       // rows of the tile inside the group
-  int64_t a_row;      // first row of the left operand
-  int64_t b_row;      // first row of the right operand
-  int64_t k0;         // first block along the summed axis
-  int64_t sb0;        // row of the block scales for the tile's first 128 columns
-  int64_t out_row;    // first output row
+  int32_t rows;       // rows of this CTA's half of the tile inside the group (may be <= 0)
+  int32_t a_row;      // first row of this CTA's left operand
+  int32_t b_row;      // first row of this CTA's right operand
+  int32_t k0;         // first block along the summed axis
+  int32_t sb0;        // row of the block scales for the tile's first 128 columns
   int32_t col;        // first column of the result
+  int64_t out_row;    // first output row of this CTA
 };
 
-template <bool WGRAD>
-__device__ __forceinline__ Tile locate(const MmArgs& p, const int32_t* start, int64_t t, int bn) {
+// Tile t, as seen from CTA `rank` of a pair (0 alone).
+template <bool PAIR, bool WGRAD>
+__device__ __forceinline__ Tile locate(const MmArgs& p, const int32_t* start, const int32_t* offs, int t, int rank) {
+  constexpr int kTileM = PAIR ? 2 * kBM : kBM, kBN = PAIR ? 256 : 128;
   Tile x;
   int g, mi, ni;
   if constexpr (WGRAD) {
-    const int64_t per = (int64_t)p.mt * p.nt;
-    g = (int)(t / per);
-    const int l = (int)(t - g * per);
+    const int per = p.mt * p.nt;
+    g = t / per;
+    const int l = t - g * per;
     ni = l / p.mt;
     mi = l - ni * p.mt;
     x.nkb = start[g + 1] - start[g];
     x.k0 = start[g];
-    x.rows = min(kBM, p.m - mi * kBM);
-    x.a_row = (int64_t)mi * kBM;
-    x.b_row = (int64_t)ni * bn;
-    x.sb0 = (int64_t)ni * (bn / 128);
-    x.out_row = (int64_t)g * p.m + mi * kBM;
+    x.a_row = mi * kTileM + rank * kBM;
+    x.rows = min(kBM, p.m - x.a_row);
+    x.b_row = ni * kBN;
+    x.sb0 = ni * (kBN / 128);
+    x.out_row = (int64_t)g * p.m + x.a_row;
   } else {
-    const int64_t u = t / p.nt;
+    const int u = t / p.nt;
     int lo = 0, hi = p.groups - 1;  // the group whose row tiles [start[g], start[g+1]) hold u
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -135,35 +232,37 @@ __device__ __forceinline__ Tile locate(const MmArgs& p, const int32_t* start, in
       else hi = mid - 1;
     }
     g = lo;
-    const int64_t l = t - (int64_t)start[g] * p.nt;
+    const int l = t - start[g] * p.nt;
     const int mts = start[g + 1] - start[g];
-    const int64_t per = (int64_t)kSuper * p.nt;
-    const int sg = (int)(l / per);
-    const int rem = (int)(l - sg * per);
+    const int per = kSuper * p.nt;
+    const int sg = l / per;
+    const int rem = l - sg * per;
     const int mm = min(kSuper, mts - sg * kSuper);
     ni = rem / mm;
     mi = sg * kSuper + rem - ni * mm;
-    const int64_t r0 = p.offsets ? __ldg(p.offsets + g) : 0;
-    const int64_t r1 = p.offsets ? __ldg(p.offsets + g + 1) : p.rows;
+    const int r0 = offs[g], r1 = offs[g + 1];
     x.nkb = p.kb;
     x.k0 = 0;
-    x.rows = (int)imin64(kBM, r1 - r0 - (int64_t)mi * kBM);
-    x.a_row = r0 + (int64_t)mi * kBM;
-    x.b_row = (int64_t)g * p.n + (int64_t)ni * bn;
-    x.sb0 = (int64_t)g * ((p.n + 127) / 128) + (int64_t)ni * (bn / 128);
+    x.a_row = r0 + mi * kTileM + rank * kBM;
+    x.rows = min(kBM, r1 - x.a_row);
+    x.b_row = g * p.n + ni * kBN;
+    x.sb0 = g * ((p.n + 127) / 128) + ni * (kBN / 128);
     x.out_row = x.a_row;
   }
-  x.col = ni * bn;
+  if constexpr (PAIR) x.b_row += rank * kBM;
+  x.col = ni * kBN;
   return x;
 }
 
-// 128-row tiles before each group (start[groups] = all), by one warp.  Bad offsets: all zero and flagged.
-__device__ __forceinline__ void group_starts(const MmArgs& p, int32_t* start) {
+// Tiles of `size` rows before each group (start[groups] = all) and the groups' first rows, by one
+// warp.  Bad offsets: all zero and flagged.
+__device__ __forceinline__ void group_starts(const MmArgs& p, int32_t* start, int32_t* offs, int size) {
   const int lane = threadIdx.x & 31;
   if (!p.offsets) {
     if (lane == 0) {
-      start[0] = 0;
-      start[1] = (int32_t)((p.rows + 127) / 128);
+      start[0] = offs[0] = 0;
+      offs[1] = (int32_t)p.rows;
+      start[1] = (int32_t)((p.rows + size - 1) / size);
     }
     return;
   }
@@ -177,45 +276,58 @@ __device__ __forceinline__ void group_starts(const MmArgs& p, int32_t* start) {
       hi = __ldg(p.offsets + g + 1);
       ok = ok && lo >= 0 && hi >= lo && hi <= p.rows;
     }
-    int incl = ok ? (hi - lo + 127) / 128 : 0;
+    int incl = ok ? (hi - lo + size - 1) / size : 0;
     const int mine = incl;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += y;
     }
-    if (g < p.groups) start[g] = seen + incl - mine;
+    if (g < p.groups) {
+      start[g] = seen + incl - mine;
+      offs[g + 1] = hi;
+    }
     seen += __shfl_sync(kFull, incl, 31);
   }
-  if (lane == 0) start[p.groups] = seen;
+  if (lane == 0) {
+    start[p.groups] = seen;
+    offs[0] = 0;
+  }
   const bool good = __all_sync(kFull, ok);
   __syncwarp();
   if (!good) {
     if (lane == 0) set_error(p.err, CTR_ERR_BAD_OFFSETS);
-    for (int g = lane; g <= p.groups; g += 32) start[g] = 0;
+    for (int g = lane; g <= p.groups; g += 32) start[g] = offs[g] = 0;
   }
 }
 
-template <int BN, bool WGRAD>
+template <bool PAIR, bool WGRAD>
 __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs p,
                                                                    const __grid_constant__ CUtensorMap amap,
-                                                                   const __grid_constant__ CUtensorMap bmap) {
-  constexpr uint32_t kStageBytes = kABytes + BN * 128u;
-  constexpr int kStages = (192 * 1024) / kStageBytes;
-  constexpr int kHalf = BN / 2;  // columns of a scaling thread
+                                                                   const __grid_constant__ CUtensorMap bmap,
+                                                                   const __grid_constant__ CUtensorMap omap) {
+  constexpr int kBN = PAIR ? 256 : 128;
+  constexpr int kCols = kBN / 2;  // columns of a scaling thread
+  constexpr int kCtas = PAIR ? 2 : 1;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bars[2 * kStages + 4];
+  __shared__ uint64_t bars[2 * kStages + 8];
   __shared__ uint32_t tmem_base_slot;
-  __shared__ int abort_flag;
-  __shared__ int32_t start[CTR_MAX_EXPERTS + 1];
+  __shared__ int32_t start[CTR_MAX_EXPERTS + 1], offs[CTR_MAX_EXPERTS + 1];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;  // swizzled tiles need 1024-byte alignment
-  const uint32_t full0 = smem_u32(&bars[0]);
-  const uint32_t empty0 = smem_u32(&bars[kStages]);
-  const uint32_t tfull0 = smem_u32(&bars[2 * kStages]);
-  const uint32_t tempty0 = smem_u32(&bars[2 * kStages + 2]);
+  uint8_t* after_stages = smem_raw + (base - raw) + kStages * kStageBytes;
+  float* row_scales = (float*)(after_stages + kScaleWarps * kStagingBytes);  // [2][kChunk][kBM]
+  float* col_scales = row_scales + 2 * kChunk * kBM;                         // [2][2][kChunk]
+  const uint32_t full0 = smem_u32(&bars[0]);                 // a stage's operands are there (pair: the even CTA's)
+  const uint32_t empty0 = smem_u32(&bars[kStages]);          // a stage's MMAs are done
+  const uint32_t tfull0 = smem_u32(&bars[2 * kStages]);      // an accumulator's MMAs and scales are there
+  const uint32_t tempty0 = smem_u32(&bars[2 * kStages + 2]); // an accumulator has been read (pair: the even CTA's)
+  const uint32_t cfull0 = smem_u32(&bars[2 * kStages + 4]);  // a chunk of scales is there
+  const uint32_t cempty0 = smem_u32(&bars[2 * kStages + 6]); // and has been used
+  uint32_t rank = 0;
+  if constexpr (PAIR) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -224,231 +336,290 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, kScaleWarps);
+      mbar_init(tempty0 + 8 * b, kCtas * kScaleWarps);
+      mbar_init(cfull0 + 8 * b, 32);
+      mbar_init(cempty0 + 8 * b, kScaleWarps);
     }
-    abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
-                 "r"(2 * BN)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
+                   "r"(2 * kBN)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
+                   "r"(2 * kBN)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
   }
-  if (warp == 2) group_starts(p, start);
+  if (warp == 4) group_starts(p, start, offs, WGRAD ? 128 : kCtas * kBM);
   fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are ready too
   fence_after();
   const uint32_t tmem = tmem_base_slot;
-  const int64_t ntiles = WGRAD ? (int64_t)p.groups * p.mt * p.nt : (int64_t)start[p.groups] * p.nt;
+  const int ntiles = (WGRAD ? p.groups * p.mt : start[p.groups]) * p.nt;
+  const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    if (lane == 0) {
-      int64_t it = 0;
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
+    if (warp == 0) {
+      // ---------------- TMA producer ----------------
+      const uint32_t count_at = PAIR ? in_cta(full0, 0) : full0;
+      int s = 0;
+      uint32_t ph = 0, issued = 0;  // issued: blocks so far, at most kStages counted
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
-        const Tile x = locate<WGRAD>(p, start, t, BN);
-        for (int j = 0; j < x.nkb; ++j, ++it) {
-          const int s = (int)(it % kStages);
-          const uint32_t ph = (uint32_t)((it / kStages) & 1);
-          if (!mbar_wait(empty0 + 8 * s, ph ^ 1)) {
-            set_error(p.err, CTR_ERR_TIMEOUT);
-            atomicExch(&abort_flag, 1);
-          }
-          if (*(volatile int*)&abort_flag) {
+      for (int t = first; ok && t < ntiles; t += step) {
+        const Tile x = locate<PAIR, WGRAD>(p, start, offs, t, (int)rank);
+        for (int j = 0; j < x.nkb; ++j) {
+          if (!park(empty0 + 8 * s, ph ^ 1)) {
+            if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
             ok = false;
             break;
           }
-          mbar_expect_tx(full0 + 8 * s, kStageBytes);
           const uint32_t dst = base + (uint32_t)s * kStageBytes;
-          const int32_t k = (int32_t)((x.k0 + j) * 128);
-          tma_load_2d(dst, &amap, k, (int32_t)x.a_row, full0 + 8 * s);
-          tma_load_2d(dst + kABytes, &bmap, k, (int32_t)x.b_row, full0 + 8 * s);
+          const int32_t k = (x.k0 + j) * 128;
+          if (elected()) {
+            if (rank == 0) mbar_expect_tx(full0 + 8 * s, kCtas * kStageBytes);
+            load_tile<PAIR>(dst, &amap, k, x.a_row, count_at + 8 * s);
+            load_tile<PAIR>(dst + kOperandBytes, &bmap, k, x.b_row, count_at + 8 * s);
+          }
+          __syncwarp();
+          if (issued < kStages) ++issued;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
-      // drain: every issued load must have landed before the CTA can exit
-      for (int s = 0; s < kStages && s < it; ++s) {
-        const int64_t last = it - 1 - ((it - 1 - s) % kStages);  // last iteration using stage s
-        if (!mbar_wait(full0 + 8 * s, (uint32_t)((last / kStages) & 1))) set_error(p.err, CTR_ERR_TIMEOUT);
+      // drain: every issued load must have landed before the CTA can exit.  The last round's MMAs free
+      // the stages; after a failure no MMA may come, and a stage's own barrier says that it is filled
+      // (a pair's odd CTA has none and waits the limit out).
+      for (uint32_t i = 0; i < issued; ++i) {
+        s = s == 0 ? kStages - 1 : s - 1;
+        if (s == kStages - 1) ph ^= 1;
+        if (!park((ok || rank != 0 ? empty0 : full0) + 8 * s, ph) && lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
       }
     }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3(kBM, BN);
-      int64_t it = 0;
+    if (warp == 1 && rank == 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idesc = idesc_e4m3(kCtas * kBM, kBN);
+      const uint64_t desc0 = smem_desc_sw128(base);
+      int s = 0;
+      uint32_t ph = 0, b = 0, bph = 0, issued = 0;  // issued: blocks so far, at most 2 counted
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
-        const int nkb = WGRAD ? locate<WGRAD>(p, start, t, BN).nkb : p.kb;
-        for (int j = 0; j < nkb; ++j, ++it) {
-          const int s = (int)(it % kStages);
-          const uint32_t ph = (uint32_t)((it / kStages) & 1);
-          const int b = (int)(it & 1);
-          if (!mbar_wait(tempty0 + 8 * b, (uint32_t)((it >> 1) & 1) ^ 1) || !mbar_wait(full0 + 8 * s, ph)) {
-            set_error(p.err, CTR_ERR_TIMEOUT);
-            atomicExch(&abort_flag, 1);
-          }
-          if (*(volatile int*)&abort_flag) {
+      for (int t = first; ok && t < ntiles; t += step) {
+        const int nkb = WGRAD ? locate<PAIR, WGRAD>(p, start, offs, t, 0).nkb : p.kb;
+        for (int j = 0; j < nkb; ++j) {
+          if (!park(full0 + 8 * s, ph) || !park(tempty0 + 8 * b, bph ^ 1)) {
+            if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
             ok = false;
             break;
           }
           fence_after();
-          const uint32_t a0 = base + (uint32_t)s * kStageBytes;
+          const uint64_t da = desc0 + (uint64_t)((uint32_t)s * (kStageBytes >> 4));  // addresses in units of 16 bytes
+          if (elected()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_e4m3(tmem + (uint32_t)(b * BN), smem_desc_sw128(a0 + k * 32u), smem_desc_sw128(a0 + kABytes + k * 32u),
-                     idesc, k != 0);
-          mma_commit(empty0 + 8 * s);
-          mma_commit(tfull0 + 8 * b);
+            for (int k = 0; k < 4; ++k)
+              mma_e4m3<PAIR>(tmem + b * kBN, da + 2 * k, da + (kOperandBytes >> 4) + 2 * k, idesc, k != 0);
+            commit<PAIR>(empty0 + 8 * s);
+            commit<PAIR>(tfull0 + 8 * b);
+          }
+          __syncwarp();
+          if (issued < 2) ++issued;
+          bph ^= b;
+          b ^= 1;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
       // drain: the last commits must have arrived before TMEM is freed
-      for (int b = 0; b < 2 && b < it; ++b) {
-        const int64_t last = it - 1 - ((it - 1 - b) % 2);
-        if (!mbar_wait(tfull0 + 8 * b, (uint32_t)((last >> 1) & 1))) set_error(p.err, CTR_ERR_TIMEOUT);
+      for (uint32_t i = 0; i < issued; ++i) {
+        b ^= 1;
+        bph ^= b;
+        if (!park(tfull0 + 8 * b, bph) && lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
       }
     }
+    if (warp == 2) {
+      // ---------------- scales ----------------
+      // kChunk blocks at a time by asynchronous copies of one scale each, which need no register and
+      // stall no one (through registers, with a barrier a block, the reads' latency bounded the kernel).
+      // Rows past the group and columns past the result get zeros.
+      uint32_t b = 0, ph = 0;
+      bool ok = true;
+      for (int t = first; ok && t < ntiles; t += step) {
+        const Tile x = locate<PAIR, WGRAD>(p, start, offs, t, (int)rank);
+        const float* sa = p.sa + (int64_t)x.k0 * p.ld_sa + x.a_row + lane;
+        const int h = lane / kChunk, u = lane % kChunk;  // 16 lanes: a block scale each
+        const bool has_b = h < kCtas && x.col + 128 * h < p.n;
+        const float* sb = p.sb + (int64_t)(x.sb0 + h) * p.ld_sb + x.k0 + u;
+        for (int j0 = 0; j0 < x.nkb; j0 += kChunk) {
+          if (!park(cempty0 + 8 * b, ph ^ 1)) {
+            if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
+            ok = false;
+            break;
+          }
+          const uint32_t dst = smem_u32(row_scales + b * (kChunk * kBM) + lane);
+          for (int j = j0; j < j0 + kChunk && j < x.nkb; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              copy_scale(dst + ((j - j0) * kBM + 32 * r) * 4, sa + (int64_t)j * p.ld_sa + 32 * r, lane + 32 * r < x.rows,
+                         p.sa);
+          if (h < 2)
+            copy_scale(smem_u32(col_scales + (b * 2 + h) * kChunk + u), sb + j0, has_b && j0 + u < x.nkb, p.sb);
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(cfull0 + 8 * b) : "memory");
+          ph ^= b;
+          b ^= 1;
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kScaleRegs));
     // ---------------- scaling warps ----------------
     const int q = warp & 3;             // TMEM lane quarter this warp may read
-    const int half = (warp - 2) >> 2;   // which half of the columns
-    const int row = q * 32 + lane;
-    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * kHalf);
-    uint32_t* staging = (uint32_t*)(smem_raw + (base - raw) + (size_t)kStages * kStageBytes) +
-                        (size_t)(warp - 2) * (kStagingBytes / 4);
-    int64_t it = 0;
+    const int part = (warp - 4) >> 2;   // which half of the columns
+    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(part * kCols);
+    const float* row_scale = row_scales + q * 32 + lane;
+    const float* col_scale = col_scales + (part * kCols / 128) * kChunk;
+    uint8_t* staging = after_stages + (size_t)(warp - 4) * kStagingBytes;
+    const uint32_t tempty_at = PAIR ? in_cta(tempty0, 0) : tempty0;
+    uint32_t b = 0, ph = 0, cb = 0, cph = 0;  // accumulator, chunk of scales
+    uint32_t turn = 0;                         // piece of the staging
     bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < ntiles; t += gridDim.x) {
-      const Tile x = locate<WGRAD>(p, start, t, BN);
-      uint64_t acc[kHalf / 2];
+    for (int t = first; ok && t < ntiles; t += step) {
+      const Tile x = locate<PAIR, WGRAD>(p, start, offs, t, (int)rank);
+      uint64_t acc[kCols / 2];
 #pragma unroll
-      for (int i = 0; i < kHalf / 2; ++i) acc[i] = 0;
-      const bool live = row < x.rows;
-      const int c0 = x.col + half * kHalf;  // this warp's first column
-      const float* sa = p.sa + x.k0 * p.ld_sa + x.a_row + row;
-      const float* sb = p.sb + (x.sb0 + (half * kHalf) / 128) * p.ld_sb + x.k0;
-      const bool cols = c0 < p.n;  // else the whole half lies past the result
-      float s_next = live && cols && x.nkb > 0 ? __ldg(sa) * __ldg(sb) : 0.f;
-      for (int j = 0; j < x.nkb; ++j, ++it) {
-        const int b = (int)(it & 1);
-        const float f = s_next;
-        if (live && cols && j + 1 < x.nkb) s_next = __ldg(sa + (int64_t)(j + 1) * p.ld_sa) * __ldg(sb + j + 1);
-        bool fail = !mbar_wait(tfull0 + 8 * b, (uint32_t)((it >> 1) & 1));
-        fail = fail || *(volatile int*)&abort_flag != 0;
-        if (__any_sync(kFull, fail)) {
-          if (lane == 0 && !*(volatile int*)&abort_flag) {
-            set_error(p.err, CTR_ERR_TIMEOUT);
-            atomicExch(&abort_flag, 1);
-          }
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
+      for (int j = 0; j < x.nkb; ++j) {
+        const int u = j % kChunk;
+        if ((u == 0 && !park(cfull0 + 8 * cb, cph)) || !park(tfull0 + 8 * b, ph)) {
+          if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
           ok = false;
           break;
         }
         fence_after();
+        const float f = row_scale[(cb * kChunk + u) * kBM] * col_scale[cb * (2 * kChunk) + u];
         uint64_t f2;
         asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "r"(__float_as_uint(f)));
-        const uint32_t tb = lane_base + (uint32_t)(b * BN);
-        uint32_t v0[16], v1[16];
-        tmem_ld16_async(tb, v0);
 #pragma unroll
-        for (int c = 0; c < kHalf / 32; ++c) {
+        for (int c = 0; c < kCols; c += 64) {
+          uint32_t v0[32], v1[32];
+          tmem_ld32_async(lane_base + b * kBN + c, v0);
+          tmem_ld32_async(lane_base + b * kBN + c + 32, v1);
           tmem_wait_ld();
-          tmem_ld16_async(tb + c * 32 + 16, v1);
-          scale_add16(acc + c * 16, v0, f2);
-          tmem_wait_ld();
-          if (c + 1 < kHalf / 32) tmem_ld16_async(tb + c * 32 + 32, v0);
-          scale_add16(acc + c * 16 + 8, v1, f2);
+          if (c + 64 == kCols) {  // the accumulator is in registers: the next MMAs may have it
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if (rank == 0) mbar_arrive(tempty0 + 8 * b);
+              else arrive_at(tempty_at + 8 * b);
+            }
+          }
+          scale_add32(acc + c / 2, v0, f2);
+          scale_add32(acc + c / 2 + 16, v1, f2);
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty0 + 8 * b);
+        if (u == kChunk - 1 || j + 1 == x.nkb) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(cempty0 + 8 * cb);
+          cph ^= cb;
+          cb ^= 1;
+        }
+        ph ^= b;
+        b ^= 1;
       }
       if (!ok) break;
-      // ---- the tile's rows leave: straight from registers where every row starts 32-byte aligned,
-      // else through shared memory, so that a store covers consecutive columns of a row
-      const int64_t orow = x.out_row + row;
+      // ---- the rows leave through shared memory, 32 rows of 128 bytes at a time (64 columns of bf16, 32
+      // of fp32), two pieces in turn.  Where the output's rows are 16-byte aligned a piece of 32 rows
+      // leaves as one TMA store, which drains while the next tile is summed (stores from the threads, or a
+      // bulk copy a row, held the warps up for 3800 cycles a tile); else, and at a group's last rows and the
+      // result's last columns, the warp stores elements, consecutive columns together.
+      const int nrows = min(32, x.rows - q * 32);
+      const int eb = p.out_f32 ? 4 : 2, width = 128 / eb;
+      const int64_t ld = p.ldo * eb;
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 32) {
-        if (c0 + c >= p.n) break;
-        float f[32];
+      for (int c = 0; c < kCols; c += 32) {
+        if (!p.out_f32 && c % 64 != 0) continue;
+        const int col = x.col + part * kCols + c;
+        if (col >= p.n || nrows <= 0) break;
+        uint8_t* piece = staging + turn * kPieceBytes;
+        turn ^= 1;
+        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last piece in this place has left
+        __syncwarp();
+        uint8_t* row = piece + lane * 128;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          uint32_t lo, hi;
-          asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(acc[c / 2 + i]));
-          f[2 * i] = __uint_as_float(lo);
-          f[2 * i + 1] = __uint_as_float(hi);
-        }
-        const bool whole = c0 + c + 32 <= p.n;
-        if (p.out_f32) {
-          if (p.wide_rows && whole) {
-            if (live) {
-              float* dst = (float*)p.out + orow * p.ldo + c0 + c;
+        for (int i = 0; i < 8; ++i) {
+          uint32_t w[4];
+          if (p.out_f32) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t w[8];
+            for (int k = 0; k < 2; ++k)
+              asm("mov.b64 {%0, %1}, %2;" : "=r"(w[2 * k]), "=r"(w[2 * k + 1]) : "l"(acc[c / 2 + 2 * i + k]));
+          } else if (c % 64 == 0) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(f[8 * i + e]);
-                st_global_v8(dst + 8 * i, w);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              __syncwarp();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) staging[lane * kStageRow + i] = __float_as_uint(f[16 * h + i]);
-              __syncwarp();
-              const int cc = lane & 15, col = c0 + c + 16 * h + cc;
-#pragma unroll 4
-              for (int r = lane >> 4; r < 32; r += 2)
-                if (q * 32 + r < x.rows && col < p.n)
-                  ((float*)p.out)[(x.out_row + q * 32 + r) * p.ldo + col] =
-                      __uint_as_float(staging[r * kStageRow + cc]);
+            for (int k = 0; k < 4; ++k) {
+              uint32_t lo, hi;
+              asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(acc[c / 2 + 4 * i + k]));
+              w[k] = bf16_pair(__uint_as_float(lo), __uint_as_float(hi));
             }
           }
+          *(uint4*)(row + ((i ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (p.wide_rows && nrows == 32 && col + width <= p.n) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0)
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                             (uint64_t)&omap),
+                         "r"(col), "r"((int32_t)(x.out_row + q * 32)), "r"(smem_u32(piece))
+                         : "memory");
         } else {
-          if (p.wide_rows && whole) {
-            if (live) {
-              __nv_bfloat16* dst = (__nv_bfloat16*)p.out + orow * p.ldo + c0 + c;
+          __syncwarp();
+          char* out = p.out + ((x.out_row + q * 32) * p.ldo + col) * eb;
+          for (int r = 0; r < nrows; ++r) {
+            const uint8_t* src = piece + r * 128;
+            if (p.out_f32) {
+              if (col + lane < p.n)
+                ((float*)(out + r * ld))[lane] = *(const float*)(src + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
+            } else {
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                uint32_t w[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = bf16_pair(f[16 * i + 2 * e], f[16 * i + 2 * e + 1]);
-                st_global_v8(dst + 16 * i, w);
-              }
+              for (int h = 0; h < 64; h += 32)
+                if (col + h + lane < p.n)
+                  ((uint16_t*)(out + r * ld))[h + lane] =
+                      *(const uint16_t*)(src + ((((h + lane) >> 3) ^ (r & 7)) * 16) + ((h + lane) & 7) * 2);
             }
-          } else {
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) staging[lane * kStageRow + i] = bf16_pair(f[2 * i], f[2 * i + 1]);
-            __syncwarp();
-            const int col = c0 + c + lane;
-#pragma unroll 4
-            for (int r = 0; r < 32; ++r)
-              if (q * 32 + r < x.rows && col < p.n)
-                ((uint16_t*)p.out)[(x.out_row + q * 32 + r) * p.ldo + col] =
-                    ((const uint16_t*)(staging + r * kStageRow))[lane];
           }
         }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     }
+    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     if (!WGRAD && p.offsets) {
       // rows past the last group: zeros
-      const int64_t used = start[p.groups] > 0 ? __ldg(p.offsets + p.groups) : 0;
+      const int64_t used = offs[p.groups];
       const int64_t stride = (int64_t)gridDim.x * kScaleWarps;
-      for (int64_t r = used + (int64_t)blockIdx.x * kScaleWarps + (warp - 2); r < p.rows; r += stride)
+      for (int64_t r = used + (int64_t)blockIdx.x * kScaleWarps + (warp - 4); r < p.rows; r += stride)
         for (int c = lane; c < p.n; c += 32) {
           if (p.out_f32) ((float*)p.out)[r * p.ldo + c] = 0.f;
           else ((uint16_t*)p.out)[r * p.ldo + c] = 0;
         }
     }
   }
+  __syncwarp();
   fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // nothing of this CTA is the other's target any more
   if (warp == 1) {
     fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kBN) : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kBN) : "memory");
   }
 }
 
@@ -465,26 +636,56 @@ bool code_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t row_byt
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool WGRAD>
+// The output in pieces of 128 bytes x 32 rows.
+bool out_map(CUtensorMap* map, const MmArgs& p, int64_t rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const int eb = p.out_f32 ? 4 : 2;
+  cuuint64_t gdim[2] = {(cuuint64_t)p.n, (cuuint64_t)rows};
+  cuuint64_t gstride[1] = {(cuuint64_t)(p.ldo * eb)};
+  cuuint32_t bx[2] = {(cuuint32_t)(128 / eb), 32};
+  cuuint32_t es[2] = {1, 1};
+  return enc(map, p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out, gdim,
+             gstride, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool PAIR, bool WGRAD>
 int launch_mm(MmArgs& p, const uint8_t* a, int64_t a_rows, const uint8_t* b, int64_t b_rows, int64_t row_bytes,
               int64_t tiles_m, cudaStream_t s) {
   CUtensorMap amap, bmap;
-  if (!code_map(&amap, a, a_rows, row_bytes, kBM) || !code_map(&bmap, b, b_rows, row_bytes, BN)) return CTR_ERR_CUDA;
-  p.nt = (int32_t)ceil_div(p.n, BN);
-  constexpr uint32_t stage = kABytes + BN * 128u;
-  const int smem = (int)(1024 + (192 * 1024) / stage * stage + kScaleWarps * kStagingBytes);
-  auto k = fp8_matmul_kernel<BN, WGRAD>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return CTR_ERR_CUDA;
-  const int64_t tiles = tiles_m * p.nt;
-  const int grid = (int)imax64(1, imin64(tiles, num_sms()));
-  k<<<grid, kMmThreads, smem, s>>>(p, amap, bmap);
+  if (!code_map(&amap, a, a_rows, row_bytes, kBM) || !code_map(&bmap, b, b_rows, row_bytes, kBM)) return CTR_ERR_CUDA;
+  CUtensorMap omap = amap;  // not used unless the output's rows are aligned
+  if (p.wide_rows && !out_map(&omap, p, WGRAD ? (int64_t)p.groups * p.m : p.rows)) return CTR_ERR_CUDA;
+  constexpr int kCtas = PAIR ? 2 : 1;
+  p.nt = (int32_t)ceil_div(p.n, PAIR ? 256 : 128);
+  if (WGRAD) p.mt = (int32_t)ceil_div(p.m, kCtas * kBM);
+  auto k = fp8_matmul_kernel<PAIR, WGRAD>;
+  // the split of registers between the warps waits for ever if the kernel was launched with fewer
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, k) != cudaSuccess || fa.numRegs != kLaunchRegs) return CTR_ERR_CUDA;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem) != cudaSuccess)
+    return CTR_ERR_CUDA;
+  const int64_t tiles = (WGRAD ? (int64_t)p.groups * p.mt : tiles_m) * p.nt;
+  if (tiles > INT32_MAX - 65536) return CTR_ERR_UNSUPPORTED;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(kCtas * imax64(1, imin64(tiles, num_sms() / kCtas))));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = kMmSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kCtas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = PAIR ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, p, amap, bmap, omap);
   count_launch();
-  return launch_status();
+  return e == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
 }
 
-// 256 columns a tile halve the reads of the left operand and use the tensor cores best; 128 where
-// that would leave SMs without a tile, or half a tile empty.
-bool tile_256(int64_t tiles_m, int64_t n) { return n > 128 && tiles_m * ceil_div(n, 256) >= num_sms(); }
+// A pair of CTAs on 256 x 256 tiles where there are tiles for most of the pairs.
+bool use_pair(int64_t tiles_m256, int64_t n) { return n > 128 && tiles_m256 * ceil_div(n, 256) >= num_sms() / 3; }
 
 int check_mm(const void* a, const float* sa, const void* b, const float* sb, const int32_t* offsets, int64_t rows,
              int32_t groups, int64_t n, int64_t k, const void* out, int out_dtype, void* ws, size_t ws_bytes) {
@@ -533,12 +734,14 @@ extern "C" int ctr_fp8_matmul(const uint8_t* a, const float* a_scale, int64_t ld
   p.n = (int32_t)n;
   p.out_f32 = out_dtype == CTR_F32;
   const int eb = dtype_bytes(out_dtype);
-  p.wide_rows = ((uintptr_t)out % 32) == 0 && (ldo * eb) % 32 == 0;
-  const int64_t tiles_m = offsets ? ctr_fp8_padded_rows(rows, groups) / 128 : ceil_div(rows, 128);
+  p.wide_rows = ((uintptr_t)out % 16) == 0 && (ldo * eb) % 16 == 0 && ldo * eb < (1ll << 40);
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t row_bytes = (int64_t)p.kb * 128;
-  if (tile_256(tiles_m, n)) return launch_mm<256, false>(p, a, rows, b, groups * n, row_bytes, tiles_m, s);
-  return launch_mm<128, false>(p, a, rows, b, groups * n, row_bytes, tiles_m, s);
+  const int64_t m256 = ceil_div(rows + 255 * (int64_t)(groups - 1), 256);  // row tiles, at most
+  const int64_t m128 = ceil_div(rows + 127 * (int64_t)(groups - 1), 128);
+  if (rows >= 128 * (int64_t)groups && use_pair(ceil_div(rows, 256), n))
+    return launch_mm<true, false>(p, a, rows, b, groups * n, row_bytes, m256, s);
+  return launch_mm<false, false>(p, a, rows, b, groups * n, row_bytes, m128, s);
 }
 
 extern "C" int ctr_fp8_matmul_wgrad(const uint8_t* d, const float* d_scale, const uint8_t* x, const float* x_scale,
@@ -562,12 +765,10 @@ extern "C" int ctr_fp8_matmul_wgrad(const uint8_t* d, const float* d_scale, cons
   p.groups = groups;
   p.m = (int32_t)n;
   p.n = (int32_t)k;
-  p.mt = (int32_t)ceil_div(n, kBM);
   p.out_f32 = out_dtype == CTR_F32;
   const int eb = dtype_bytes(out_dtype);
-  p.wide_rows = ((uintptr_t)out % 32) == 0 && (k * eb) % 32 == 0;
-  const int64_t tiles_m = (int64_t)groups * p.mt;
+  p.wide_rows = ((uintptr_t)out % 16) == 0 && (k * eb) % 16 == 0 && groups * n < INT32_MAX;
   cudaStream_t s = (cudaStream_t)stream;
-  if (tile_256(tiles_m, k)) return launch_mm<256, true>(p, d, n, x, k, padded, tiles_m, s);
-  return launch_mm<128, true>(p, d, n, x, k, padded, tiles_m, s);
+  if (n > 128 && use_pair(groups * ceil_div(n, 256), k)) return launch_mm<true, true>(p, d, n, x, k, padded, 0, s);
+  return launch_mm<false, true>(p, d, n, x, k, padded, 0, s);
 }

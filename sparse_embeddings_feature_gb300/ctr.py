@@ -97,6 +97,8 @@ class CtrError(RuntimeError):
 def lib() -> C.CDLL:
     """Load libctr.so, building it first if the sources changed.  Raises if that fails."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -125,12 +127,14 @@ def _ok(name: str, st: int) -> None:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return C.c_void_p(s.cuda_stream)
+    # the current stream's handle, without building a torch.cuda.Stream object on every call
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _host_i32(a) -> C.Array:
@@ -400,29 +404,31 @@ def ctr_embedding_bag_bwd_update_phases(grad_pooled: torch.Tensor, g_stride_b: i
 # These calls take their sizes from the tensors' shapes, so the shapes, types and
 # layouts are checked here: the library sees only pointers.  Matrices may have a
 # row stride; maps, weights, codes and scales are dense.
-def _mat(t: torch.Tensor, what: str, dtypes=(torch.float32, torch.bfloat16)) -> torch.Tensor:
-    """A 2-d CUDA matrix whose rows are contiguous; returns it."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dim() != 2 or t.dtype not in dtypes:
-        raise ValueError(f"{what} must be a matrix of {' or '.join(str(d) for d in dtypes)}, not "
-                         f"{t.dim()}-d {t.dtype}")
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{what} must have contiguous rows that do not overlap")
-    return t
+_F = (torch.float32, torch.bfloat16)
+_F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+
+
+def _mat(t: torch.Tensor, what: str, dtypes=_F) -> torch.Tensor:
+    """A 2-d CUDA matrix whose rows are contiguous and do not overlap; returns it."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2:
+        if t.is_contiguous():
+            return t
+        (rows, cols), (ld, step) = t.shape, t.stride()
+        if (cols <= 1 or step == 1) and (rows <= 1 or ld >= cols):
+            return t
+    raise ValueError(f"{what} must be a CUDA matrix of {' or '.join(str(d) for d in dtypes)} with contiguous rows "
+                     f"that do not overlap")
 
 
 def _ld(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else max(1, cols)
 
 
 def _dense(t: torch.Tensor, what: str, dtype, shape) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not "
-                         f"{t.dtype} {tuple(t.shape)}")
-    return t
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return t
+    raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
 
 
 def _same(t: torch.Tensor, other: torch.Tensor, what: str) -> None:
