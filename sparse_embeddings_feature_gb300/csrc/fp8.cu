@@ -141,21 +141,53 @@ struct TileArgs {
 __device__ __forceinline__ float2 two(const float* p) { return *(const float2*)p; }
 __device__ __forceinline__ float2 two(const __nv_bfloat16* p) { return __bfloat1622float2(*(const __nv_bfloat162*)p); }
 
-// A tile row is 128 elements and 16 bytes more: 16-byte stores stay aligned and a row's do not
+// A tile row is 128 elements and 16 bytes more: 16-byte accesses stay aligned and a row's do not
 // meet the next one's banks.
 template <typename T>
 constexpr int tile_ld() {
   return 128 + 16 / (int)sizeof(T);
 }
 
+// Largest magnitudes, NaN winning, two values at a time: bf16 pairs stay packed.
+template <typename T>
+struct MaxPair;
+template <>
+struct MaxPair<float> {
+  float x = 0.f, y = 0.f;
+  __device__ __forceinline__ void add(const float* p) {
+    const float2 v = *(const float2*)p;
+    x = max_mag(x, v.x);
+    y = max_mag(y, v.y);
+  }
+  __device__ __forceinline__ float2 get() const { return make_float2(x, y); }
+};
+template <>
+struct MaxPair<__nv_bfloat16> {
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+  __device__ __forceinline__ void add(const __nv_bfloat16* p) { m = __hmax2_nan(m, __habs2(*(const __nv_bfloat162*)p)); }
+  __device__ __forceinline__ float2 get() const { return __bfloat1622float2(m); }
+};
+
+// B bytes into shared memory without waiting, of which the first `take` come from src and the rest
+// are zeros.
+template <int B>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int take) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  if constexpr (B == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(take) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(take) : "memory");
+}
+
 // One 128 x 128 tile.  ROW_BLOCK: the row codes have one scale for the tile (else one a row);
 // COL_BLOCK: the column codes have (else one a column).
 template <typename T, bool ROW_BLOCK, bool COL_BLOCK>
-__global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs a) {
+__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_tile_kernel(const TileArgs a) {
   constexpr int kLd = tile_ld<T>();
   extern __shared__ __align__(16) uint8_t smem[];
   T* tile = (T*)smem;
-  __shared__ float col_max[4][128];
+  __shared__ float col_max[4][128];  // then [0]: the columns' multipliers
+  __shared__ float row_max[128];     // then the rows' multipliers
   __shared__ float warp_max[kQThreads / 32];
   __shared__ int where[4];  // group, first row, rows, tile number (of all groups)
   const int col0 = blockIdx.y * 128;
@@ -213,126 +245,137 @@ __global__ void __launch_bounds__(kQThreads) quantize_tile_kernel(const TileArgs
   if (n <= 0) return;
   const int64_t xbase = a.offsets ? 0 : (int64_t)g * a.rows;  // rows of earlier groups
 
-  // Row order: 16 lanes a row, 8 values each; rows past n are zeros (the column codes' filling).
+  // The tile into shared memory by asynchronous copies: nothing waits in registers, so that five CTAs
+  // an SM keep their reads in flight.  Rows past n and columns past the end are zeros.
   const int lane16 = threadIdx.x & 15;
+  const int ncols = (int)imin64(128, a.cols - col0);
+  if (a.vec) {
+    constexpr int per = 16 / (int)sizeof(T), parts = 128 / per;  // 16-byte parts of a row
+    const int c = ((int)threadIdx.x % parts) * per;
+    const int take = max(0, min(16, (ncols - c) * (int)sizeof(T)));
+    const T* from = (const T*)a.x + xbase * a.ldx + (take ? col0 + c : 0);
+#pragma unroll 4
+    for (int i = (int)threadIdx.x / parts; i < 128; i += kQThreads / parts) {
+      const int64_t src = i < n ? source_row(a.row_index, row0 + i, a.x_rows, a.err) : -1;
+      copy_async<16>(tile + i * kLd + c, src >= 0 ? from + src * a.ldx : (const T*)a.x, src >= 0 ? take : 0);
+    }
+  } else {
+    for (int i = warp; i < 128; i += kQThreads / 32) {
+      const int64_t src = i < n ? xbase + source_row(a.row_index, row0 + i, a.x_rows, a.err) : -1;
+      const T* row = (const T*)a.x + (src >= 0 ? src * a.ldx + col0 : 0);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int c = h * 32 + lane;
+        const bool take = src >= 0 && c < ncols;
+        if constexpr (sizeof(T) == 4) copy_async<4>(tile + i * kLd + c, take ? row + c : (const T*)a.x, take ? 4 : 0);
+        else tile[i * kLd + c] = take ? row[c] : from_f32<T>(0.f);
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+
+  // Maxima.  Rows: 16 lanes a row, 8 values each; columns: two and 32 of their rows to a thread.
   const int64_t qcol = col0 + lane16 * 8;
+  const int c = (threadIdx.x & 63) * 2, part = threadIdx.x >> 6;
+  const T* mine = tile + part * 32 * kLd + c;
   float tile_max = 0.f;
 #pragma unroll 4
   for (int p = 0; p < 8; ++p) {
     const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
-    float v[8];
-    int64_t src = -1;
-    if (i < n) src = xbase + source_row(a.row_index, row0 + i, a.x_rows, a.err);
-    if (src >= 0) {
-      load8((const T*)a.x + src * a.ldx, qcol, a.cols, a.vec != 0, v);
-    } else {
+    MaxPair<T> mp;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-    }
-    constexpr int per = 16 / (int)sizeof(T);
-#pragma unroll
-    for (int e = 0; e < 8; e += per) {
-      float f[per];
-#pragma unroll
-      for (int b = 0; b < per; ++b) f[b] = v[e + b];
-      *(uint4*)(tile + i * kLd + lane16 * 8 + e) = Chunk<T, 16>::pack(f);
-    }
-    float m = max_mag(v);
+    for (int e = 0; e < 8; e += 2) mp.add(tile + i * kLd + lane16 * 8 + e);
+    const float2 m2 = mp.get();
+    float m = max_mag(m2.x, m2.y);
     if constexpr (ROW_BLOCK || COL_BLOCK) tile_max = max_mag(tile_max, m);
     if constexpr (!ROW_BLOCK) {
 #pragma unroll
       for (int o = 1; o < 16; o <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, o));
-      const float amax = at_least_floor(m);
-      const float inv = __fdiv_rn(kTop, amax);
-      if (i < n) {
-        *(uint2*)(a.q + (int64_t)(row0 + i) * a.ldq + qcol) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
-        if (lane16 == 0) a.scale[(int64_t)blockIdx.y * a.ld_scale + row0 + i] = __fdiv_rn(amax, kTop);
-      }
+      if (lane16 == 0) row_max[i] = m;
     }
+  }
+  if constexpr (!COL_BLOCK) {
+    MaxPair<T> mp;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) mp.add(mine + i * kLd);
+    *(float2*)&col_max[part][c] = mp.get();
   }
   float block_amax = 0.f, block_inv = 0.f;
   if constexpr (ROW_BLOCK || COL_BLOCK) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) tile_max = max_mag(tile_max, __shfl_xor_sync(kFull, tile_max, o));
     if (lane == 0) warp_max[warp] = tile_max;
-    __syncthreads();
+  }
+  __syncthreads();
+  // Scales and multipliers: a row or a column to a thread.
+  if constexpr (ROW_BLOCK || COL_BLOCK) {
     tile_max = 0.f;
 #pragma unroll
     for (int w = 0; w < kQThreads / 32; ++w) tile_max = max_mag(tile_max, warp_max[w]);
     block_amax = at_least_floor(tile_max);
     block_inv = __fdiv_rn(kTop, block_amax);
-  } else {
-    __syncthreads();
   }
   if constexpr (ROW_BLOCK) {
-    const int64_t row_blocks = (a.rows + 127) / 128;
-#pragma unroll 4
-    for (int p = 0; p < 8; ++p) {
-      const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
-      if (i >= n) continue;
-      float v[8];
-      load8(tile + i * kLd, lane16 * 8, 128, true, v);
-      *(uint2*)(a.q + (xbase + row0 + i) * a.ldq + qcol) =
-          make_uint2(codes4(v, block_inv), codes4(v + 4, block_inv));
-    }
     if (threadIdx.x == 0) {
+      const int64_t row_blocks = (a.rows + 127) / 128;
       const float s = __fdiv_rn(block_amax, kTop);
       a.scale[((int64_t)g * row_blocks + tnum) * a.col_blocks + blockIdx.y] = s;
       if (a.qt) a.scale_t[((int64_t)g * a.col_blocks + blockIdx.y) * row_blocks + tnum] = s;
     }
-    if (!a.qt) return;
-  }
-  // Column order: two columns and 32 of their rows to a thread.
-  const int c = (threadIdx.x & 63) * 2, part = threadIdx.x >> 6;
-  float2 v[32];
+  } else {
+    const int i = threadIdx.x & 127;
+    if (threadIdx.x < 128) {
+      const float m = at_least_floor(row_max[i]);
+      row_max[i] = __fdiv_rn(kTop, m);
+      if (i < n) a.scale[(int64_t)blockIdx.y * a.ld_scale + row0 + i] = __fdiv_rn(m, kTop);
+    } else if constexpr (!COL_BLOCK) {
+      float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = two(tile + (part * 32 + i) * kLd + c);
-  float inv0 = block_inv, inv1 = block_inv;
-  if constexpr (!COL_BLOCK) {
-    float m0 = 0.f, m1 = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      m0 = max_mag(m0, v[i].x);
-      m1 = max_mag(m1, v[i].y);
+      for (int p = 0; p < 4; ++p) m = max_mag(m, col_max[p][i]);
+      m = at_least_floor(m);
+      col_max[0][i] = __fdiv_rn(kTop, m);
+      if (i < ncols) a.scale_t[(int64_t)tnum * a.ld_scale_t + col0 + i] = __fdiv_rn(m, kTop);
+    } else if (i == 0) {
+      a.scale_t[(int64_t)blockIdx.y * a.ld_scale_t + tnum] = __fdiv_rn(block_amax, kTop);
     }
-    *(float2*)&col_max[part][c] = make_float2(m0, m1);
     __syncthreads();
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      m0 = max_mag(m0, col_max[p][c]);
-      m1 = max_mag(m1, col_max[p][c + 1]);
-    }
-    m0 = at_least_floor(m0);
-    m1 = at_least_floor(m1);
-    inv0 = __fdiv_rn(kTop, m0);
-    inv1 = __fdiv_rn(kTop, m1);
-    if (part == 0) {
-      float* s = a.scale_t + (int64_t)tnum * a.ld_scale_t + col0 + c;
-      if (col0 + c < a.cols) s[0] = __fdiv_rn(m0, kTop);
-      if (col0 + c + 1 < a.cols) s[1] = __fdiv_rn(m1, kTop);
-    }
-  } else if constexpr (!ROW_BLOCK) {
-    if (threadIdx.x == 0) a.scale_t[(int64_t)blockIdx.y * a.ld_scale_t + tnum] = __fdiv_rn(block_amax, kTop);
   }
-  // The codes go through shared memory (over the tile, which is in registers now), so that eight
-  // lanes write a column's 128 bytes together: 32-byte pieces straight from the registers made the
-  // pass a third slower.
+  // Row codes.
+  uint8_t* q = a.q + ((ROW_BLOCK ? xbase : 0) + row0) * a.ldq + qcol;
+#pragma unroll 4
+  for (int p = 0; p < 8; ++p) {
+    const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
+    float v[8];
+    load8(tile + i * kLd, lane16 * 8, 128, true, v);
+    const float inv = ROW_BLOCK ? block_inv : row_max[i];
+    if (i < n) *(uint2*)(q + i * a.ldq) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
+  }
+  if (!a.qt) return;
+  const float inv0 = COL_BLOCK ? block_inv : col_max[0][c], inv1 = COL_BLOCK ? block_inv : col_max[0][c + 1];
+  // The codes go through shared memory (over the tile, which is in registers by then), so that eight
+  // lanes write a column's 128 bytes together.
+  uint32_t w[2][8];
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    float f0[4], f1[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = two(mine + (4 * b + e) * kLd);
+      f0[e] = v.x;
+      f1[e] = v.y;
+    }
+    w[0][b] = codes4(f0, inv0);
+    w[1][b] = codes4(f1, inv1);
+  }
   constexpr int kCodeLd = 144;
   uint8_t* codes = smem;
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t w[8];
-#pragma unroll
-    for (int b = 0; b < 8; ++b) {
-      float f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = h ? v[4 * b + e].y : v[4 * b + e].x;
-      w[b] = codes4(f, h ? inv1 : inv0);
-    }
     uint4* dst = (uint4*)(codes + (c + h) * kCodeLd + part * 32);
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    dst[0] = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
+    dst[1] = make_uint4(w[h][4], w[h][5], w[h][6], w[h][7]);
   }
   __syncthreads();
   const int64_t qrow = (ROW_BLOCK ? (int64_t)g * a.cols : 0) + col0;
