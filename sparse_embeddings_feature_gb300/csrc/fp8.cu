@@ -7,8 +7,9 @@
 //
 // Rows: 16 lanes hold a block of 128 values, 8 each (one or two 16-byte loads),
 // the maximum is four xor-shuffles, and the 128 codes leave as one 128-byte
-// store of 8 bytes a lane.  A lane group takes up to four blocks of one row at
-// once, so four loads are in flight and no index is divided.  Bound by HBM.
+// store of 8 bytes a lane.  A lane group takes two to four blocks of one row at
+// once, has the next row's loads in flight while it converts, and divides once
+// for all of them.  Bound by HBM.
 //
 // Tiles (rows + columns, blocks): a CTA reads a 128 x 128 tile once, keeps it in
 // shared memory in its own type, and writes both orders of codes from it, each
@@ -85,40 +86,113 @@ __device__ __forceinline__ int64_t source_row(const int32_t* row_index, int64_t 
   return i;
 }
 
-constexpr int kRowBlocks = 4;  // blocks of one row that a lane group takes at once
+// Largest magnitudes, NaN winning, two values at a time: bf16 pairs stay packed.
+template <typename T>
+struct MaxPair;
+template <>
+struct MaxPair<float> {
+  float x = 0.f, y = 0.f;
+  __device__ __forceinline__ void add(const float* p) {
+    const float2 v = *(const float2*)p;
+    x = max_mag(x, v.x);
+    y = max_mag(y, v.y);
+  }
+  __device__ __forceinline__ float2 get() const { return make_float2(x, y); }
+};
+template <>
+struct MaxPair<__nv_bfloat16> {
+  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
+  __device__ __forceinline__ void add(const __nv_bfloat16* p) { m = __hmax2_nan(m, __habs2(*(const __nv_bfloat162*)p)); }
+  __device__ __forceinline__ float2 get() const { return __bfloat1622float2(m); }
+};
+
+// Blocks of one row that a lane group takes at once: 64 bytes of loads a lane.
+template <typename T>
+constexpr int row_blocks() {
+  return 8 / (int)sizeof(T);
+}
+
+template <typename T>
+struct RowPart {
+  static constexpr int kBlocks = row_blocks<T>();
+  uint4 raw[kBlocks][sizeof(T) / 2];  // 8 values of each block
+};
+
+// The lane's 8 values of blocks kb0, kb0 + 1, .. of row src (-1: zeros); zeros past the row's end.
+template <typename T>
+__device__ __forceinline__ void load_part(RowPart<T>& p, const T* x, int64_t ldx, int64_t src, int kb0, int lane16,
+                                          int64_t cols, bool vec) {
+  constexpr int per = 16 / (int)sizeof(T);
+#pragma unroll
+  for (int b = 0; b < RowPart<T>::kBlocks; ++b) {
+    const int64_t c = (int64_t)(kb0 + b) * 128 + lane16 * 8;
+    const T* row = x + src * ldx + c;
+#pragma unroll
+    for (int h = 0; h < 8 / per; ++h) {
+      if (vec && src >= 0 && c + (h + 1) * per <= cols) {
+        p.raw[b][h] = __ldg((const uint4*)(row + h * per));
+      } else {
+        float f[per];
+#pragma unroll
+        for (int i = 0; i < per; ++i) f[i] = src >= 0 && c + h * per + i < cols ? to_f32<T>(row[h * per + i]) : 0.f;
+        p.raw[b][h] = Chunk<T, 16>::pack(f);
+      }
+    }
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* x, int64_t x_rows, int64_t rows,
                                                                   int64_t cols, int64_t ldx, int vec,
                                                                   const int32_t* row_index, uint8_t* q, float* scale,
                                                                   int64_t ld_scale, int blocks, int* err) {
+  constexpr int kBlocks = row_blocks<T>(), per = 16 / (int)sizeof(T);
   const int lane16 = threadIdx.x & 15;
-  const int64_t r = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);
-  const int kb0 = blockIdx.y * kRowBlocks;
-  const int64_t src = r < rows ? source_row(row_index, r, x_rows, err) : -1;
-  const T* row = x + (src >= 0 ? src * ldx : 0);
-  float v[kRowBlocks][8];
+  const int kb0 = blockIdx.y * kBlocks;
+  const int64_t step = (int64_t)gridDim.x * (kQThreads / 16);
+  const int64_t trips = ceil_div(rows, step);  // the same in every lane: the shuffles need all of them
+  int64_t r = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);
+  RowPart<T> cur, next;
+  load_part(cur, x, ldx, r < rows ? source_row(row_index, r, x_rows, err) : -1, kb0, lane16, cols, vec != 0);
+  for (int64_t trip = 0; trip < trips; ++trip, r += step) {
+    // the next row's loads fly while this one is converted
+    if (trip + 1 < trips)
+      load_part(next, x, ldx, r + step < rows ? source_row(row_index, r + step, x_rows, err) : -1, kb0, lane16, cols,
+                vec != 0);
+    // a block's two divisions are one lane's: lane b of the group has block b's
+    float mine = 0.f;
 #pragma unroll
-  for (int b = 0; b < kRowBlocks; ++b) {
-    if (src >= 0 && kb0 + b < blocks) {
-      load8(row, (int64_t)(kb0 + b) * 128 + lane16 * 8, cols, vec != 0, v[b]);
-    } else {
+    for (int b = 0; b < kBlocks; ++b) {
+      MaxPair<T> mp;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[b][i] = 0.f;
+      for (int h = 0; h < 8 / per; ++h)
+#pragma unroll
+        for (int e = 0; e < per; e += 2) mp.add((const T*)&cur.raw[b][h] + e);
+      const float2 m2 = mp.get();
+      float m = max_mag(m2.x, m2.y);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, o));
+      if (lane16 == b) mine = m;
     }
-  }
+    const float amax = at_least_floor(mine);
+    const float inv_mine = __fdiv_rn(kTop, amax);
+    const float s = __fdiv_rn(amax, kTop);
+    if (r < rows && lane16 < kBlocks && kb0 + lane16 < blocks) scale[(kb0 + lane16) * ld_scale + r] = s;
 #pragma unroll
-  for (int b = 0; b < kRowBlocks; ++b) {
-    float m = max_mag(v[b]);
+    for (int b = 0; b < kBlocks; ++b) {
+      const float inv = __shfl_sync(kFull, inv_mine, b, 16);
+      float v[8];
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, o));
-    const float amax = at_least_floor(m);
-    const float inv = __fdiv_rn(kTop, amax);
-    if (r < rows && kb0 + b < blocks) {
-      *(uint2*)(q + (r * blocks + kb0 + b) * 128 + lane16 * 8) =
-          make_uint2(codes4(v[b], inv), codes4(v[b] + 4, inv));
-      if (lane16 == 0) scale[(kb0 + b) * ld_scale + r] = __fdiv_rn(amax, kTop);
+      for (int h = 0; h < 8 / per; ++h) {
+        float f[per];
+        Chunk<T, 16>::unpack(cur.raw[b][h], f);
+#pragma unroll
+        for (int i = 0; i < per; ++i) v[h * per + i] = f[i];
+      }
+      if (r < rows && kb0 + b < blocks)
+        *(uint2*)(q + (r * blocks + kb0 + b) * 128 + lane16 * 8) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
     }
+    cur = next;
   }
 }
 
@@ -147,26 +221,6 @@ template <typename T>
 constexpr int tile_ld() {
   return 128 + 16 / (int)sizeof(T);
 }
-
-// Largest magnitudes, NaN winning, two values at a time: bf16 pairs stay packed.
-template <typename T>
-struct MaxPair;
-template <>
-struct MaxPair<float> {
-  float x = 0.f, y = 0.f;
-  __device__ __forceinline__ void add(const float* p) {
-    const float2 v = *(const float2*)p;
-    x = max_mag(x, v.x);
-    y = max_mag(y, v.y);
-  }
-  __device__ __forceinline__ float2 get() const { return make_float2(x, y); }
-};
-template <>
-struct MaxPair<__nv_bfloat16> {
-  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
-  __device__ __forceinline__ void add(const __nv_bfloat16* p) { m = __hmax2_nan(m, __habs2(*(const __nv_bfloat162*)p)); }
-  __device__ __forceinline__ float2 get() const { return __bfloat1622float2(m); }
-};
 
 // B bytes into shared memory without waiting, of which the first `take` come from src and the rest
 // are zeros.
@@ -417,14 +471,17 @@ extern "C" int ctr_fp8_quantize_rows(const void* x, ctr_dtype dtype, int64_t x_r
   if (!dtype_ok(dtype) || x_rows < 0 || rows < 0 || cols < 1 || ldx < cols || ld_scale < rows)
     return CTR_ERR_INVALID_ARG;
   if (!row_index && rows > x_rows) return CTR_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || cols > 65535 * 128) return CTR_ERR_UNSUPPORTED;
+  if (rows > INT32_MAX || cols > 65535 * 256) return CTR_ERR_UNSUPPORTED;
   if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
   if (rows == 0) return CTR_OK;
   const int eb = dtype_bytes(dtype);
   if (!x || !q || !scale || ((uintptr_t)x % eb) || !aligned16(q)) return CTR_ERR_INVALID_ARG;
   const int vec = aligned16(x) && (ldx * eb) % 16 == 0;
   const int kb = (int)ceil_div(cols, 128);
-  const dim3 grid((unsigned)ceil_div(rows, kQThreads / 16), (unsigned)ceil_div(kb, kRowBlocks));
+  const int64_t parts = ceil_div(kb, dtype == CTR_F32 ? row_blocks<float>() : row_blocks<__nv_bfloat16>());
+  // rows are walked by as many CTAs as are resident, so that a lane group has a next row to load
+  const int64_t resident = imax64(1, ceil_div((int64_t)num_sms() * 5, parts));
+  const dim3 grid((unsigned)imin64(ceil_div(rows, kQThreads / 16), resident), (unsigned)parts);
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == CTR_F32)
     quantize_rows_kernel<<<grid, kQThreads, 0, s>>>((const float*)x, x_rows, rows, cols, ldx, vec, row_index, q,
