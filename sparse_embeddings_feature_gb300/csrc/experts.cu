@@ -4,10 +4,12 @@
 // sample to a few experts); the formulas and the row order are stated in
 // include/ctr.h.
 //
-// Routing.  A token's scores are spread over a group of lanes, EPL consecutive
-// scores to a lane; the k choices are k rounds of "best score not yet taken"
-// (in-lane scan, then an xor-shuffle tournament whose ties go to the lower
-// index).  The stable order by expert is a counting sort without atomics on
+// Routing.  A token's scores are spread over a group of lanes (at least k), EPL
+// consecutive scores to a lane; the k choices are k rounds of "best score not yet
+// taken" (in-lane maximum, then xor-shuffles; ties go to the lower index), after
+// which lane j has choice j, its exponential and its stores.  bf16 scores carry
+// their index in the low half of an ordered 32-bit key, so that a round is integer
+// maxima alone.  Bound by instruction issue.  The stable order by expert is a counting sort without atomics on
 // counts: a block's tile of up to 256 tokens is a bit matrix [expert][token]
 // in shared memory, so a choice's rank within the tile is a population count
 // of the bits before it, and the tile's count of an expert the count of all.
@@ -29,7 +31,7 @@
 namespace ctr {
 namespace {
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512;
 constexpr int kTileTokens = 256;      // tokens of a tile, at most
 // One block does it all up to this many scores (tokens x experts) and kTileTokens tokens.
 constexpr int64_t kOneBlockScores = 16384;
@@ -67,10 +69,11 @@ __device__ __forceinline__ void load_scores(const T* row, int base, int experts,
 }
 
 // Exclusive sum of totals[0 .. experts) into start (shared); returns the sum.  All threads.
+static_assert(kRouteThreads >= CTR_MAX_EXPERTS, "an expert to a thread");
 __device__ __forceinline__ int expert_starts(const int* totals, int experts, int* start, int* warp_sum) {
-  const int e0 = 2 * threadIdx.x;
-  const int a = e0 < experts ? totals[e0] : 0, b = e0 + 1 < experts ? totals[e0 + 1] : 0;
-  int x = a + b;
+  const int e = threadIdx.x;
+  const int mine = e < experts ? totals[e] : 0;
+  int x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(kFull, x, o);
@@ -84,12 +87,74 @@ __device__ __forceinline__ int expert_starts(const int* totals, int experts, int
     if (w < (int)(threadIdx.x >> 5)) before += warp_sum[w];
     all += warp_sum[w];
   }
-  const int first = before + x - a - b;
-  if (e0 < experts) start[e0] = first;
-  if (e0 + 1 < experts) start[e0 + 1] = first + a;
+  if (e < experts) start[e] = before + x - mine;
   __syncthreads();
   return all;
 }
+
+// The k best of a group's scores, one round a choice: choice j's score and expert (-1: none left).
+template <typename T, int EPL, int KMAX>
+struct Picker {
+  // fp32: the value, then the lowest index that has it
+  static __device__ __forceinline__ void pick(float (&v)[EPL], int base, int lanes, int k, float (&val)[KMAX],
+                                              int (&idx)[KMAX]) {
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      val[j] = -INFINITY;
+      idx[j] = -1;
+      if (j < k) {
+        float best = v[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) best = fmaxf(best, v[i]);
+        for (int o = 1; o < lanes; o <<= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
+        int at = 0x7fffffff;
+#pragma unroll
+        for (int i = EPL - 1; i >= 0; --i) at = v[i] == best ? base + i : at;
+        for (int o = 1; o < lanes; o <<= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
+        if (best > -INFINITY) {
+          val[j] = best;
+          idx[j] = at;
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) v[i] = base + i == at ? -INFINITY : v[i];
+      }
+    }
+  }
+};
+
+template <int EPL, int KMAX>
+struct Picker<__nv_bfloat16, EPL, KMAX> {
+  // bf16 values fill the high half of an fp32 word: ordered as an unsigned number, with the complement
+  // of the index below, so one maximum finds value and lowest index.  Masked scores are key 0.
+  static __device__ __forceinline__ void pick(float (&v)[EPL], int base, int lanes, int k, float (&val)[KMAX],
+                                              int (&idx)[KMAX]) {
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const uint32_t b = __float_as_uint(v[i] + 0.f);  // -0 becomes +0
+      const uint32_t ordered = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+      key[i] = v[i] > -INFINITY ? (ordered & 0xffff0000u) | (uint32_t)(0xffff - (base + i)) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) {
+      val[j] = -INFINITY;
+      idx[j] = -1;
+      if (j < k) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+        for (int o = 1; o < lanes; o <<= 1) best = max(best, __shfl_xor_sync(kFull, best, o));
+        if (best != 0) {
+          const uint32_t hi = best & 0xffff0000u;
+          val[j] = __uint_as_float((hi & 0x80000000u) ? hi & 0x7fffffffu : ~hi & 0xffff0000u);
+          idx[j] = 0xffff - (int)(best & 0xffffu);
+        }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = key[i] == best ? 0u : key[i];
+      }
+    }
+  }
+};
 
 // Ranks of the tile's choices from its bit matrix: slot and token of each, given the first row of
 // every expert's choices in this tile.  `before` gets each word's count of earlier tokens.
@@ -148,53 +213,39 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
       for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
       if (sub == 0) set_error(a.err, CTR_ERR_BAD_VALUE);
     }
-    uint32_t taken = 0;
-    float z[KMAX], m = 0.f, chosen = 0.f;
-    int idx[KMAX];
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      if (j < a.k) {
-        float best = -INFINITY;
-        int at = 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (!((taken >> i) & 1) && v[i] > best) {
-            best = v[i];
-            at = base + i;
-          }
-        for (int o = 1; o < a.lanes; o <<= 1) {
-          const float ob = __shfl_xor_sync(kFull, best, o);
-          const int oi = __shfl_xor_sync(kFull, at, o);
-          if (ob > best || (ob == best && oi < at)) {
-            best = ob;
-            at = oi;
-          }
-        }
-        const bool live = best > -INFINITY;
-        if (j == 0) m = live ? best : 0.f;
-        if (live && at >= base && at < base + EPL) taken |= 1u << (at - base);
-        idx[j] = live ? at : -1;
-        z[j] = live ? expf(best - m) : 0.f;
-        chosen += z[j];
-      }
-    }
-    float total = chosen;
+    float total = 0.f;
     if (!a.renormalize) {
-      total = 0.f;
+      float m = v[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      if (!(m > -INFINITY)) m = 0.f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) total += expf(v[i] - m);  // exp(-inf) = 0: masked scores add nothing
       for (int o = 1; o < a.lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
     }
-    if (mine && sub == 0) {
+    float val[KMAX];
+    int idx[KMAX];
+    Picker<T, EPL, KMAX>::pick(v, base, a.lanes, a.k, val, idx);
+    // lane j of the group has choice j
+    float mine_v = -INFINITY;
+    int mine_e = -1;
 #pragma unroll
-      for (int j = 0; j < KMAX; ++j) {
-        if (j < a.k) {
-          const int64_t at = (t0 + tl) * a.k + j;
-          a.expert[at] = idx[j];
-          a.weight[at] = idx[j] >= 0 ? z[j] / total : 0.f;
-          if (idx[j] >= 0) atomicOr(&bits[idx[j] * words + (tl >> 5)], 1u << (tl & 31));
-        }
+    for (int j = 0; j < KMAX; ++j)
+      if (j == sub) {
+        mine_v = val[j];
+        mine_e = idx[j];
       }
+    const float z = mine_e >= 0 ? expf(mine_v - val[0]) : 0.f;
+    if (a.renormalize) {
+      total = z;
+      for (int o = 1; o < a.lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
+    }
+    if (mine && sub < a.k) {
+      const int64_t at = (t0 + tl) * a.k + sub;
+      a.expert[at] = mine_e;
+      a.weight[at] = mine_e >= 0 ? z / total : 0.f;
+      if (mine_e >= 0) atomicOr(&bits[mine_e * words + (tl >> 5)], 1u << (tl & 31));
     }
   }
   __syncthreads();
@@ -233,8 +284,10 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a) {
   const int per = (a.tiles + 31) / 32;
   const int b0 = min(a.tiles, warp * per), b1 = min(a.tiles, b0 + per);
   int sum = 0;
-  if (e < a.experts)
+  if (e < a.experts) {
+#pragma unroll 8
     for (int b = b0; b < b1; ++b) sum += a.counts[(int64_t)b * a.experts + e];
+  }
   seg[warp][lane] = sum;
   __syncthreads();
   int run = 0, all = 0;
@@ -243,11 +296,15 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a) {
     all += seg[w][lane];
   }
   if (e >= a.experts) return;
-  for (int b = b0; b < b1; ++b) {
-    int* c = &a.counts[(int64_t)b * a.experts + e];
-    const int x = *c;
-    *c = run;
-    run += x;
+  for (int b = b0; b < b1; b += 8) {
+    int x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = b + i < b1 ? a.counts[(int64_t)(b + i) * a.experts + e] : 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (b + i < b1) a.counts[(int64_t)(b + i) * a.experts + e] = run;
+      run += x[i];
+    }
   }
   if (warp == 0) a.counts[(int64_t)a.tiles * a.experts + e] = all;
 }
@@ -285,86 +342,110 @@ __global__ void route_empty_kernel(int32_t* offsets, int experts) {
   for (int e = threadIdx.x; e <= experts; e += blockDim.x) offsets[e] = 0;
 }
 
+// Writes a lane's EPL values of a row (base + EPL may pass the last expert).
 template <typename T, int EPL>
+__device__ __forceinline__ void store_scores(T* out, int base, int experts, bool vec, const float (&v)[EPL]) {
+  constexpr int per = 16 / (int)sizeof(T);
+  if (vec && base + EPL <= experts) {
+#pragma unroll
+    for (int i = 0; i < EPL; i += per) {
+      float f[per];
+#pragma unroll
+      for (int q = 0; q < per; ++q) f[q] = v[i + q];
+      *(uint4*)(out + i) = Chunk<T, 16>::pack(f);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+      if (base + i < experts) out[i] = from_f32<T>(v[i]);
+  }
+}
+
+// RENORM: the softmax is over the choices, so lane j of the group reads choice j's score alone and
+// the other scores' gradient is zero.  Else the whole row takes part.
+template <typename T, int EPL, bool RENORM>
 __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArgs a, const float* dweight, T* dscores,
                                                                   int64_t ldd, int vec_out) {
   const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
   const int base = sub * EPL;
   const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / a.lanes);
-  const int64_t g0 = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) / a.lanes;
+  int64_t t = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) / a.lanes;
   const int64_t trips = ceil_div(a.tokens, groups);  // the same in every lane
-  for (int64_t trip = 0; trip < trips; ++trip) {
-    const int64_t t = g0 + trip * groups;
+  for (int64_t trip = 0; trip < trips; ++trip, t += groups) {
     const bool mine = t < a.tokens;
-    float v[EPL], g[EPL];
-    if (mine) {
-      load_scores<T, EPL>((const T*)a.scores + t * a.ld, base, a.experts, a.vec != 0, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
-    }
-    uint32_t sel = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) g[i] = 0.f;
-    if (mine) {
-      for (int j = 0; j < a.k; ++j) {
-        const int at = a.expert[t * a.k + j] - base;
-        if (at >= 0 && at < EPL) {
-          const float d = dweight[t * a.k + j];
-#pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (i == at) g[i] = d;
-          sel |= 1u << at;
-        }
-      }
-    }
-    // a token with no choice (all masked, or flagged by the routing) has no gradient
+    const T* row = (const T*)a.scores + t * a.ld;
+    // lane j has choice j
+    const int e = mine && sub < a.k ? a.expert[t * a.k + sub] : -1;
+    const bool live = e >= 0 && e < a.experts;
+    const float g = live ? dweight[t * a.k + sub] : 0.f;
     const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
-    const bool routed = (__ballot_sync(kFull, sel != 0) & group) != 0;
-    float m = -INFINITY;
+    // a token with no choice (all masked, or flagged by the routing) has no gradient
+    const bool routed = (__ballot_sync(kFull, live) & group) != 0;
+    float out[EPL];
+    if constexpr (RENORM) {
+      const float l = live ? to_f32<T>(row[e]) : -INFINITY;
+      float m = l;
+      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      const float z = live ? expf(l - m) : 0.f;
+      float total = z, dot = z * g;
+      for (int o = 1; o < a.lanes; o <<= 1) {
+        total += __shfl_xor_sync(kFull, total, o);
+        dot += __shfl_xor_sync(kFull, dot, o);
+      }
+      const float inv = routed ? 1.f / total : 0.f;
+      const float d = z * inv * (g - dot * inv);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) m = fmaxf(m, v[i]);
-    for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if (!routed) m = 0.f;
-    float total = 0.f, dot = 0.f;
+      for (int i = 0; i < EPL; ++i) out[i] = 0.f;
+      for (int j = 0; j < a.k; ++j) {
+        const int at = __shfl_sync(kFull, e, j, a.lanes) - base;
+        const float dj = __shfl_sync(kFull, d, j, a.lanes);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const bool in = a.renormalize ? ((sel >> i) & 1) : true;
-      v[i] = in && routed ? expf(v[i] - m) : 0.f;
-      total += v[i];
-      dot += v[i] * g[i];
-    }
-    for (int o = 1; o < a.lanes; o <<= 1) {
-      total += __shfl_xor_sync(kFull, total, o);
-      dot += __shfl_xor_sync(kFull, dot, o);
-    }
-    if (!mine) continue;
-    const float inv = routed ? 1.f / total : 0.f;
-    dot *= inv;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) v[i] = v[i] * inv * (g[i] - dot);
-    T* out = dscores + t * ldd + base;
-    constexpr int per = 16 / (int)sizeof(T);
-    if (vec_out && base + EPL <= a.experts) {
-#pragma unroll
-      for (int i = 0; i < EPL; i += per) {
-        float f[per];
-#pragma unroll
-        for (int q = 0; q < per; ++q) f[q] = v[i + q];
-        *(uint4*)(out + i) = Chunk<T, 16>::pack(f);
+        for (int i = 0; i < EPL; ++i) out[i] = at == i ? dj : out[i];
       }
     } else {
+      float v[EPL], gi[EPL];
+      if (mine) {
+        load_scores<T, EPL>(row, base, a.experts, a.vec != 0, v);
+      } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (base + i < a.experts) out[i] = from_f32<T>(v[i]);
+        for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) gi[i] = 0.f;
+      for (int j = 0; j < a.k; ++j) {
+        const int at = __shfl_sync(kFull, live ? e : -1, j, a.lanes) - base;
+        const float gj = __shfl_sync(kFull, g, j, a.lanes);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) gi[i] = at == i ? gj : gi[i];
+      }
+      float m = v[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      float total = 0.f, dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        v[i] = routed ? expf(v[i] - m) : 0.f;
+        total += v[i];
+        dot += v[i] * gi[i];
+      }
+      for (int o = 1; o < a.lanes; o <<= 1) {
+        total += __shfl_xor_sync(kFull, total, o);
+        dot += __shfl_xor_sync(kFull, dot, o);
+      }
+      const float inv = routed ? 1.f / total : 0.f;
+      dot *= inv;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) out[i] = v[i] * inv * (gi[i] - dot);
     }
+    if (mine) store_scores<T, EPL>(dscores + t * ldd + base, base, a.experts, vec_out != 0, out);
   }
 }
 
-// Lanes per token: 8 scores a lane (16 above 256 experts), a power of two.
-int route_lanes(int experts) {
+// Lanes per token: 8 scores a lane (16 above 256 experts) and a lane for each choice, a power of two.
+int route_lanes(int experts, int k) {
   int lanes = 1;
-  while (lanes < 32 && lanes * 8 < experts) lanes *= 2;
+  while (lanes < 32 && (lanes * 8 < experts || lanes < k)) lanes *= 2;
   return lanes;
 }
 
@@ -395,6 +476,15 @@ void launch_choose(const RouteArgs& a, size_t smem, cudaStream_t s) {
     route_choose_kernel<T, EPL, 4><<<a.tiles, kRouteThreads, smem, s>>>(a);
   else
     route_choose_kernel<T, EPL, CTR_MAX_CHOICES><<<a.tiles, kRouteThreads, smem, s>>>(a);
+  count_launch();
+}
+
+template <typename T>
+void launch_bwd(const RouteArgs& a, const float* dweight, T* dscores, int64_t ldd, int vec_out, int grid,
+                cudaStream_t s) {
+  auto k = a.experts <= 256 ? (a.renormalize ? route_bwd_kernel<T, 8, true> : route_bwd_kernel<T, 8, false>)
+                            : (a.renormalize ? route_bwd_kernel<T, 16, true> : route_bwd_kernel<T, 16, false>);
+  k<<<grid, kRouteThreads, 0, s>>>(a, dweight, dscores, ldd, vec_out);
   count_launch();
 }
 
@@ -623,7 +713,7 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   a.ld = ld_scores;
   a.experts = experts;
   a.k = k;
-  a.lanes = route_lanes(experts);
+  a.lanes = route_lanes(experts, k);
   a.tile = route_tile(tokens, experts);
   a.tiles = (int32_t)ceil_div(tokens, a.tile);
   a.renormalize = renormalize != 0;
@@ -670,7 +760,7 @@ extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ct
   a.ld = ld_scores;
   a.experts = experts;
   a.k = k;
-  a.lanes = route_lanes(experts);
+  a.lanes = route_lanes(experts, k);
   a.renormalize = renormalize != 0;
   const int eb = dtype_bytes(dtype);
   a.vec = ((uintptr_t)scores % 16) == 0 && (ld_scores * eb) % 16 == 0;
@@ -678,21 +768,9 @@ extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ct
   a.expert = const_cast<int32_t*>(expert);
   a.err = (int*)ws;
   cudaStream_t s = (cudaStream_t)stream;
-  const int grid = (int)imin64(ceil_div(tokens * a.lanes, kRouteThreads), (int64_t)num_sms() * 16);
-  if (dtype == CTR_F32) {
-    if (experts <= 256)
-      route_bwd_kernel<float, 8><<<grid, kRouteThreads, 0, s>>>(a, dweight, (float*)dscores, ld_dscores, vec_out);
-    else
-      route_bwd_kernel<float, 16><<<grid, kRouteThreads, 0, s>>>(a, dweight, (float*)dscores, ld_dscores, vec_out);
-  } else {
-    if (experts <= 256)
-      route_bwd_kernel<__nv_bfloat16, 8>
-          <<<grid, kRouteThreads, 0, s>>>(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out);
-    else
-      route_bwd_kernel<__nv_bfloat16, 16>
-          <<<grid, kRouteThreads, 0, s>>>(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out);
-  }
-  count_launch();
+  const int grid = (int)imin64(ceil_div(tokens * a.lanes, kRouteThreads), (int64_t)num_sms() * 8);
+  if (dtype == CTR_F32) launch_bwd(a, dweight, (float*)dscores, ld_dscores, vec_out, grid, s);
+  else launch_bwd(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out, grid, s);
   return launch_status();
 }
 
