@@ -8,10 +8,11 @@
 // fp64; joins are fp64 in a fixed order, so the result does not change from run
 // to run.  A part whose sum of squares comes near either end of fp32's range is
 // read again and squared in fp64 by its warp (fp64 in the common path, even
-// predicated off, tripled the pass: 724 us against 230 for 5e8 elements).  The
-// last block to finish adds the blocks' sums up.  Two passes over the data, bound
-// by HBM: the second walks the chunks in reverse, so what the first read last is
-// still in L2.
+// predicated off, tripled the pass: 724 us against 252 for 5e8 elements).  Every
+// block of the second pass adds the first one's sums up for itself, in the same
+// order: no counter, and no launch between the two.  Two passes over the data,
+// bound by HBM: the second walks the chunks in reverse, so what the first read
+// last is still in L2.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -26,7 +27,8 @@ constexpr int kClipThreads = 256;
 constexpr int kChunk = 8192;        // elements of a chunk
 constexpr int kListMax = 256;       // tensors of one launch
 constexpr int kClipBlocksPerSm = 6;
-constexpr int kMaxBlocks = 2048;    // bound of the grid, for the workspace
+constexpr int kMaxBlocks = 2048;    // bound of a launch's grid
+constexpr int kMaxSums = 16384;     // bound of all launches' blocks, for the workspace
 constexpr int kFlush = 8;           // chunks between moves of the fp32 sums into fp64
 // A thread's sum over its part of a chunk is used within these bounds: above, a sum of them could
 // overflow; below, squares that fall under fp32's smallest numbers would weigh in (at or above it
@@ -41,13 +43,6 @@ struct ClipList {
   int64_t first[kListMax + 1];  // chunks before each tensor
   uint8_t dtype[kListMax];
   int32_t count;
-};
-
-// Workspace after the header.  `sum` runs over the launches of one call.
-struct ClipState {
-  double sum;
-  float factor;
-  uint32_t done;
 };
 
 __device__ __forceinline__ int tensor_of(const ClipList& l, int64_t chunk) {
@@ -113,11 +108,20 @@ __device__ __noinline__ double chunk_squares_wide(const T* g, int n) {
   return s;
 }
 
-__global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constant__ ClipList l, ClipState* st,
-                                                            double* part, float* norm, float max_norm, int first,
-                                                            int last) {
+// Sum over the block's threads, valid in thread 0.
+__device__ __forceinline__ double block_sum(double v, double* warp_sum) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_down_sync(kFull, v, o);
+  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kClipThreads / 32; ++w) s += warp_sum[w];
+  return s;
+}
+
+__global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constant__ ClipList l, double* part) {
   __shared__ double warp_sum[kClipThreads / 32];
-  __shared__ bool am_last;
   float acc = 0.f;
   double wide = 0.0;
   int since = 0;
@@ -142,37 +146,28 @@ __global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constan
     }
   }
   wide += (double)acc;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) wide += __shfl_down_sync(kFull, wide, o);
-  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = wide;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int w = 0; w < kClipThreads / 32; ++w) s += warp_sum[w];
-    part[blockIdx.x] = s;
-    __threadfence();
-    am_last = atomicAdd(&st->done, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!am_last) return;
-  __threadfence();
+  wide = block_sum(wide, warp_sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = wide;
+}
+
+// The factor of the n sums in part; the first block of a launch that is told to writes the norm.
+__device__ __forceinline__ float clip_factor(const double* part, int n, float max_norm, float* norm) {
+  __shared__ double warp_sum[kClipThreads / 32];
+  __shared__ float factor;
   double s = 0.0;
-  for (int b = threadIdx.x; b < (int)gridDim.x; b += kClipThreads) s += __ldcg(part + b);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(kFull, s, o);
-  if ((threadIdx.x & 31) == 0) warp_sum[threadIdx.x >> 5] = s;
-  __syncthreads();
+  for (int b = threadIdx.x; b < n; b += kClipThreads) s += part[b];
+  s = block_sum(s, warp_sum);
   if (threadIdx.x == 0) {
-    double all = first ? 0.0 : st->sum;
-    for (int w = 0; w < kClipThreads / 32; ++w) all += warp_sum[w];
-    st->sum = all;
-    st->done = 0;
-    if (last) {
-      const float v = (float)sqrt(all);
-      *norm = v;
-      st->factor = v > max_norm && v < INFINITY ? max_norm / v : 1.f;  // NaN and inf leave the gradients as they are
-    }
+    const float v = (float)sqrt(s);
+    if (norm && blockIdx.x == 0) *norm = v;
+    factor = v > max_norm && v < INFINITY ? max_norm / v : 1.f;  // NaN and inf leave the gradients as they are
   }
+  __syncthreads();
+  return factor;
+}
+
+__global__ void __launch_bounds__(kClipThreads) norm_only_kernel(const double* part, int n, float* norm) {
+  clip_factor(part, n, 0.f, norm);
 }
 
 template <typename T>
@@ -208,8 +203,9 @@ __device__ __forceinline__ void chunk_scale(const T* g, T* out, int n, float f) 
   for (int i = i0 + threadIdx.x; i < n; i += kClipThreads) out[i] = from_f32<T>(to_f32<T>(g[i]) * f);
 }
 
-__global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_constant__ ClipList l, const ClipState* st) {
-  const float f = st->factor;
+__global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_constant__ ClipList l, const double* part, int n_sums,
+                                                             float max_norm, float* norm) {
+  const float f = clip_factor(part, n_sums, max_norm, norm);
   for (int64_t c = l.first[l.count] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int t = tensor_of(l, c);
     if (f == 1.f && l.out[t] == l.g[t]) continue;  // in place and nothing to change
@@ -238,8 +234,8 @@ int64_t fill_list(ClipList* l, const void* const* grads, void* const* outs, cons
   return chunks;
 }
 
-int clip_grid(int64_t chunks) {
-  return (int)imax64(1, imin64(imin64(chunks, (int64_t)num_sms() * kClipBlocksPerSm), kMaxBlocks));
+int clip_grid(int64_t chunks, int64_t most) {
+  return (int)imax64(1, imin64(imin64(chunks, (int64_t)num_sms() * kClipBlocksPerSm), most));
 }
 
 }  // namespace
@@ -249,8 +245,7 @@ using namespace ctr;
 
 extern "C" size_t ctr_clip_grads_workspace_size(void) {
   WsSizer z;
-  z.take<ClipState>(1);
-  z.take<double>(kMaxBlocks);
+  z.take<double>(kMaxSums);
   return z.used;
 }
 
@@ -267,26 +262,35 @@ extern "C" int ctr_clip_grads(const void* const* grads, void* const* outs, const
     if (outs && (!outs[i] || ((uintptr_t)outs[i] % eb) != 0)) return CTR_ERR_INVALID_ARG;
   }
   if (!ws_valid(ws, ws_bytes, ctr_clip_grads_workspace_size())) return CTR_ERR_WORKSPACE;
+  // launches of up to kListMax tensors, with the workspace's sums shared out between them
+  const int batches = std::max(1, (n_tensors + kListMax - 1) / kListMax);
+  if (batches > kMaxSums) return CTR_ERR_UNSUPPORTED;
+  const int64_t most = std::min(kMaxBlocks, kMaxSums / batches);
   WsCarver c(ws, ws_bytes);
-  ClipState* st = c.take<ClipState>(1);
-  double* part = c.take<double>(kMaxBlocks);
+  double* part = c.take<double>(kMaxSums);
   cudaStream_t s = (cudaStream_t)stream;
   ClipList l;
-  const int batches = std::max(1, (n_tensors + kListMax - 1) / kListMax);
+  int sums = 0;
   for (int b = 0; b < batches; ++b) {
     const int i0 = b * kListMax, i1 = std::min(n_tensors, i0 + kListMax);
-    const int64_t chunks = fill_list(&l, grads, outs, dtypes, counts, i0, i1);
-    norm_kernel<<<clip_grid(chunks), kClipThreads, 0, s>>>(l, st, part, norm, max_norm, b == 0, b == batches - 1);
+    const int grid = clip_grid(fill_list(&l, grads, outs, dtypes, counts, i0, i1), most);
+    norm_kernel<<<grid, kClipThreads, 0, s>>>(l, part + sums);
     count_launch();
+    sums += grid;
   }
-  if (outs) {
-    for (int b = batches - 1; b >= 0; --b) {
-      const int i0 = b * kListMax, i1 = std::min(n_tensors, i0 + kListMax);
-      const int64_t chunks = fill_list(&l, grads, outs, dtypes, counts, i0, i1);
-      if (chunks == 0) continue;
-      scale_kernel<<<clip_grid(chunks), kClipThreads, 0, s>>>(l, st);
-      count_launch();
-    }
+  bool told = false;
+  for (int b = batches - 1; outs && b >= 0; --b) {
+    const int i0 = b * kListMax, i1 = std::min(n_tensors, i0 + kListMax);
+    if (batches > 1) fill_list(&l, grads, outs, dtypes, counts, i0, i1);
+    const int64_t chunks = l.first[l.count];
+    if (chunks == 0) continue;
+    scale_kernel<<<clip_grid(chunks, most), kClipThreads, 0, s>>>(l, part, sums, max_norm, told ? nullptr : norm);
+    count_launch();
+    told = true;
+  }
+  if (!told) {
+    norm_only_kernel<<<1, kClipThreads, 0, s>>>(part, sums, norm);
+    count_launch();
   }
   return launch_status();
 }

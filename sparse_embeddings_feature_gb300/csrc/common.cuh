@@ -108,6 +108,19 @@ __device__ __forceinline__ unsigned lanemask_lt() {
 
 __device__ __forceinline__ int lane_id() { return threadIdx.x & 31; }
 
+// Barrier of all threads of a thread-block cluster.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Address of the same shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
 // L2 cache policies for data with known reuse: keep (evict_last) rows that are
 // read many times within a kernel, let streamed data go first (evict_first).
 __device__ __forceinline__ uint64_t l2_evict_last() {

@@ -120,13 +120,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
     tma_load_2d(dst, map, c0, c1, bar);
 }
 
-// Address of the same variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-
 // Bounded wait of a whole warp.  The hint lets the hardware park the warp for up to 20 us a try:
 // warps that poll take issue slots from the ones that scale.
 __device__ __forceinline__ bool park(uint32_t bar, uint32_t parity) {
@@ -162,11 +155,6 @@ __device__ __forceinline__ bool elected() {
 // thread's accumulator reads, which are complete; at cluster scope an arrival took 1500 cycles.
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // acc += f * v for 32 values, two at a time.  volatile: stays after the wait for the load of v.
