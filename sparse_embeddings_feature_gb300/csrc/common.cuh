@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ctr.h"
 
 namespace ctr {
@@ -64,6 +66,18 @@ void count_launch();
 
 // Number of SMs of the current device (cached per device).
 int num_sms();
+
+// Runs `setup` once for each device (`done`: a bit each) and again after a failure; its result.
+template <typename F>
+inline bool once_per_device(std::atomic<uint64_t>& done, F&& setup) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return setup();
+  const uint64_t bit = 1ull << dev;
+  if (done.load(std::memory_order_relaxed) & bit) return true;
+  if (!setup()) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
 
 // Map the last CUDA error to a ctr_status.
 inline int launch_status() {

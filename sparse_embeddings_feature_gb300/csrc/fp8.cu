@@ -446,7 +446,11 @@ template <typename T, bool ROW_BLOCK, bool COL_BLOCK>
 int launch_tiles(const TileArgs& a, int64_t tiles, cudaStream_t s) {
   auto k = quantize_tile_kernel<T, ROW_BLOCK, COL_BLOCK>;
   const int smem = 128 * tile_ld<T>() * (int)sizeof(T);
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return CTR_ERR_CUDA;
+  static std::atomic<uint64_t> ready{0};
+  if (!once_per_device(ready, [&] {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+      }))
+    return CTR_ERR_CUDA;
   k<<<dim3((unsigned)tiles, (unsigned)a.col_blocks), kQThreads, smem, s>>>(a);
   count_launch();
   return launch_status();

@@ -650,9 +650,12 @@ int launch_mm(MmArgs& p, const uint8_t* a, int64_t a_rows, const uint8_t* b, int
   if (WGRAD) p.mt = (int32_t)ceil_div(p.m, kCtas * kBM);
   auto k = fp8_matmul_kernel<PAIR, WGRAD>;
   // the split of registers between the warps waits for ever if the kernel was launched with fewer
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, k) != cudaSuccess || fa.numRegs != kLaunchRegs) return CTR_ERR_CUDA;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem) != cudaSuccess)
+  static std::atomic<uint64_t> ready{0};
+  if (!once_per_device(ready, [&] {
+        cudaFuncAttributes fa;
+        return cudaFuncGetAttributes(&fa, k) == cudaSuccess && fa.numRegs == kLaunchRegs &&
+               cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem) == cudaSuccess;
+      }))
     return CTR_ERR_CUDA;
   const int64_t tiles = (WGRAD ? (int64_t)p.groups * p.mt : tiles_m) * p.nt;
   if (tiles > INT32_MAX - 65536) return CTR_ERR_UNSUPPORTED;

@@ -133,8 +133,11 @@ def _ptr(t: Optional[torch.Tensor]):
 def _stream(stream=None):
     # the current stream's handle, without building a torch.cuda.Stream object on every call
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     return stream.cuda_stream
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _host_i32(a) -> C.Array:
@@ -403,42 +406,45 @@ def ctr_embedding_bag_bwd_update_phases(grad_pooled: torch.Tensor, g_stride_b: i
 # ---------------------------------------------------------------------------
 # These calls take their sizes from the tensors' shapes, so the shapes, types and
 # layouts are checked here: the library sees only pointers.  Matrices may have a
-# row stride; maps, weights, codes and scales are dense.
+# row stride; maps, weights, codes and scales are dense.  The checks are written
+# for their cost: a call of a small batch is a few microseconds of kernels.
 _F = (torch.float32, torch.bfloat16)
 _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
+_F32_ONLY = (torch.float32,)
 
 
-def _mat(t: torch.Tensor, what: str, dtypes=_F) -> torch.Tensor:
-    """A 2-d CUDA matrix whose rows are contiguous and do not overlap; returns it."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.dim() == 2:
-        if t.is_contiguous():
-            return t
-        (rows, cols), (ld, step) = t.shape, t.stride()
-        if (cols <= 1 or step == 1) and (rows <= 1 or ld >= cols):
-            return t
+def _mat(t: torch.Tensor, what: str, dtypes=_F):
+    """(rows, columns, row stride) of a CUDA matrix whose rows are contiguous and do not overlap."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes:
+        shape = t.shape
+        if len(shape) == 2:
+            rows, cols = shape
+            if t.is_contiguous():
+                return rows, cols, cols or 1
+            ld, step = t.stride()
+            if (cols <= 1 or step == 1) and (rows <= 1 or ld >= cols):
+                return rows, cols, ld if rows > 1 else max(1, cols)
     raise ValueError(f"{what} must be a CUDA matrix of {' or '.join(str(d) for d in dtypes)} with contiguous rows "
                      f"that do not overlap")
 
 
-def _ld(t: torch.Tensor) -> int:
-    rows, cols = t.shape
-    return t.stride(0) if rows > 1 else max(1, cols)
-
-
-def _dense(t: torch.Tensor, what: str, dtype, shape) -> torch.Tensor:
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
-        return t
+def _dense(t: torch.Tensor, what: str, dtype, shape) -> None:
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
+        return
     raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
-
-
-def _same(t: torch.Tensor, other: torch.Tensor, what: str) -> None:
-    if t.dtype != other.dtype:
-        raise ValueError(f"{what} must be {other.dtype}, not {t.dtype}")
 
 
 def _want(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
+
+
+def _like(t: torch.Tensor, what: str, rows: int, cols: int, dtype) -> int:
+    """Row stride of a matrix of the given shape and type."""
+    r, c, ld = _mat(t, what, (dtype,))
+    if r != rows or c != cols:
+        raise ValueError(f"{what} must be {(rows, cols)}, not {(r, c)}")
+    return ld
 
 
 def ctr_expert_workspace_size() -> int:
@@ -453,82 +459,85 @@ def ctr_expert_route(scores: torch.Tensor, k: int, renormalize: bool, expert: to
                      slot: torch.Tensor, token: torch.Tensor, offsets: torch.Tensor, ws: torch.Tensor,
                      stream=None) -> None:
     """The k best experts of every token (row of scores), their softmax weights, and the order by expert."""
-    T, E = _mat(scores, "scores").shape
-    i32 = torch.int32
-    _dense(expert, "expert", i32, (T, k))
-    _dense(weight, "weight", torch.float32, (T, k))
-    _dense(slot, "slot", i32, (T, k))
-    _dense(token, "token", i32, (T * k,))
-    _dense(offsets, "offsets", i32, (E + 1,))
-    st = lib().ctr_expert_route(_ptr(scores), DTYPES[scores.dtype], T, E, _ld(scores), int(k), 1 if renormalize else 0,
-                                _ptr(expert), _ptr(weight), _ptr(slot), _ptr(token), _ptr(offsets), _ptr(ws),
-                                ws.numel(), _stream(stream))
-    _ok("ctr_expert_route", st)
+    T, E, ld = _mat(scores, "scores")
+    tk = (T, k)
+    _dense(expert, "expert", _I32, tk)
+    _dense(weight, "weight", _F32, tk)
+    _dense(slot, "slot", _I32, tk)
+    _dense(token, "token", _I32, (T * k,))
+    _dense(offsets, "offsets", _I32, (E + 1,))
+    st = lib().ctr_expert_route(scores.data_ptr(), DTYPES[scores.dtype], T, E, ld, k, 1 if renormalize else 0,
+                                expert.data_ptr(), weight.data_ptr(), slot.data_ptr(), token.data_ptr(),
+                                offsets.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok("ctr_expert_route", st)
 
 
 def ctr_expert_route_bwd(dweight: torch.Tensor, scores: torch.Tensor, renormalize: bool, expert: torch.Tensor,
                          dscores: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
-    T, E = _mat(scores, "scores").shape
+    T, E, ld = _mat(scores, "scores")
     _want(expert.dim() == 2, "expert must be a matrix")
     k = expert.shape[1]
-    _dense(expert, "expert", torch.int32, (T, k))
-    _dense(dweight, "dweight", torch.float32, (T, k))
-    _same(_mat(dscores, "dscores"), scores, "dscores")
-    _want(dscores.shape == scores.shape, "dscores must have the shape of scores")
-    st = lib().ctr_expert_route_bwd(_ptr(dweight), _ptr(scores), DTYPES[scores.dtype], T, E, _ld(scores), k,
-                                    1 if renormalize else 0, _ptr(expert), _ptr(dscores), _ld(dscores), _ptr(ws),
-                                    ws.numel(), _stream(stream))
-    _ok("ctr_expert_route_bwd", st)
+    _dense(expert, "expert", _I32, (T, k))
+    _dense(dweight, "dweight", _F32, (T, k))
+    ldd = _like(dscores, "dscores", T, E, scores.dtype)
+    st = lib().ctr_expert_route_bwd(dweight.data_ptr(), scores.data_ptr(), DTYPES[scores.dtype], T, E, ld, k,
+                                    1 if renormalize else 0, expert.data_ptr(), dscores.data_ptr(), ldd,
+                                    ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok("ctr_expert_route_bwd", st)
 
 
 def _slots(slot: torch.Tensor, T: int) -> int:
+    """k of a slot map [T, k]."""
     _want(isinstance(slot, torch.Tensor) and slot.dim() == 2, "slot must be a matrix")
-    _dense(slot, "slot", torch.int32, (T, slot.shape[1]))
-    return slot.shape[1]
+    k = slot.shape[1]
+    _dense(slot, "slot", _I32, (T, k))
+    return k
 
 
 def ctr_expert_dispatch(x: torch.Tensor, slot: torch.Tensor, token: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
                         stream=None) -> None:
     """Token rows of x into the order by expert: out [T*k, d]."""
-    T, d = _mat(x, "x").shape
+    T, d, ld = _mat(x, "x")
     k = _slots(slot, T)
-    _dense(token, "token", torch.int32, (T * k,))
-    _same(_mat(out, "out"), x, "out")
-    _want(tuple(out.shape) == (T * k, d), f"out must be {(T * k, d)}")
-    st = lib().ctr_expert_dispatch(_ptr(x), DTYPES[x.dtype], T, d, _ld(x), k, _ptr(slot), _ptr(token), _ptr(out),
-                                   _ld(out), _ptr(ws), ws.numel(), _stream(stream))
-    _ok("ctr_expert_dispatch", st)
+    _dense(token, "token", _I32, (T * k,))
+    ldo = _like(out, "out", T * k, d, x.dtype)
+    st = lib().ctr_expert_dispatch(x.data_ptr(), DTYPES[x.dtype], T, d, ld, k, slot.data_ptr(), token.data_ptr(),
+                                   out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok("ctr_expert_dispatch", st)
 
 
 def ctr_expert_combine(rows: torch.Tensor, slot: torch.Tensor, weight: Optional[torch.Tensor], y: torch.Tensor,
                        ws: torch.Tensor, stream=None) -> None:
     """Rows [T*k, d] added back to tokens under the weights (None: all 1, the gradient of the dispatch)."""
-    T, d = _mat(y, "y").shape
+    T, d, ldy = _mat(y, "y")
     k = _slots(slot, T)
-    _same(_mat(rows, "rows"), y, "rows")
-    _want(tuple(rows.shape) == (T * k, d), f"rows must be {(T * k, d)}")
+    ldr = _like(rows, "rows", T * k, d, y.dtype)
     if weight is not None:
-        _dense(weight, "weight", torch.float32, (T, k))
-    st = lib().ctr_expert_combine(_ptr(rows), DTYPES[y.dtype], T, d, _ld(rows), k, _ptr(slot), _ptr(weight), _ptr(y),
-                                  _ld(y), _ptr(ws), ws.numel(), _stream(stream))
-    _ok("ctr_expert_combine", st)
+        _dense(weight, "weight", _F32, (T, k))
+    st = lib().ctr_expert_combine(rows.data_ptr(), DTYPES[y.dtype], T, d, ldr, k, slot.data_ptr(), _ptr(weight),
+                                  y.data_ptr(), ldy, ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok("ctr_expert_combine", st)
 
 
 def ctr_expert_combine_bwd(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor,
                            token: torch.Tensor, drows: torch.Tensor, dweight: torch.Tensor, ws: torch.Tensor,
                            stream=None) -> None:
-    T, d = _mat(dy, "dy").shape
+    T, d, ldy = _mat(dy, "dy")
     k = _slots(slot, T)
-    for t, what in ((rows, "rows"), (drows, "drows")):
-        _same(_mat(t, what), dy, what)
-        _want(tuple(t.shape) == (T * k, d), f"{what} must be {(T * k, d)}")
-    _dense(weight, "weight", torch.float32, (T, k))
-    _dense(dweight, "dweight", torch.float32, (T, k))
-    _dense(token, "token", torch.int32, (T * k,))
-    st = lib().ctr_expert_combine_bwd(_ptr(dy), DTYPES[dy.dtype], T, d, _ld(dy), k, _ptr(rows), _ld(rows), _ptr(slot),
-                                      _ptr(weight), _ptr(token), _ptr(drows), _ld(drows), _ptr(dweight), _ptr(ws),
-                                      ws.numel(), _stream(stream))
-    _ok("ctr_expert_combine_bwd", st)
+    ldr = _like(rows, "rows", T * k, d, dy.dtype)
+    ldd = _like(drows, "drows", T * k, d, dy.dtype)
+    _dense(weight, "weight", _F32, (T, k))
+    _dense(dweight, "dweight", _F32, (T, k))
+    _dense(token, "token", _I32, (T * k,))
+    st = lib().ctr_expert_combine_bwd(dy.data_ptr(), DTYPES[dy.dtype], T, d, ldy, k, rows.data_ptr(), ldr,
+                                      slot.data_ptr(), weight.data_ptr(), token.data_ptr(), drows.data_ptr(), ldd,
+                                      dweight.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok("ctr_expert_combine_bwd", st)
 
 
 # -- 8-bit products -----------------------------------------------------------
@@ -554,54 +563,50 @@ def ctr_fp8_matmul_workspace_size(rows: int, groups: int, n: int, k: int) -> int
     return int(lib().ctr_fp8_matmul_workspace_size(rows, groups, n, k))
 
 
-def _scales(scale: torch.Tensor, what: str, blocks: int, rows: int) -> int:
-    """Checks row scales [blocks, rows] (a row stride is allowed); returns the stride."""
-    _mat(scale, what, (torch.float32,))
-    _want(tuple(scale.shape) == (blocks, rows), f"{what} must be {(blocks, rows)}, not {tuple(scale.shape)}")
-    return _ld(scale)
-
-
-def _index(row_index: Optional[torch.Tensor], q: torch.Tensor, x: torch.Tensor) -> int:
+def _codes_of(q: torch.Tensor, row_index: Optional[torch.Tensor], n: int, cols: int) -> int:
+    """Rows of the row codes q of a matrix [n, cols], through a map or without."""
     _want(isinstance(q, torch.Tensor) and q.dim() == 2, "q must be a matrix")
     rows = q.shape[0]
+    _dense(q, "q", _U8, (rows, (cols + 127) // 128 * 128))
     if row_index is not None:
-        _dense(row_index, "row_index", torch.int32, (rows,))
-    else:
-        _want(rows <= x.shape[0], "without row_index, q may not have more rows than x")
+        _dense(row_index, "row_index", _I32, (rows,))
+    elif rows > n:
+        raise ValueError("without row_index, q may not have more rows than x")
     return rows
 
 
 def ctr_fp8_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, ws: torch.Tensor,
                           row_index: Optional[torch.Tensor] = None, stream=None) -> None:
     """Row codes q [rows, padded cols] and scales [blocks, rows] of x, or of its rows row_index."""
-    n, cols = _mat(x, "x").shape
-    rows = _index(row_index, q, x)
-    _dense(q, "q", torch.uint8, (rows, fp8_padded(cols)))
-    lds = _scales(scale, "scale", fp8_blocks(cols), rows)
-    st = lib().ctr_fp8_quantize_rows(_ptr(x), DTYPES[x.dtype], n, rows, cols, _ld(x), _ptr(row_index), _ptr(q),
-                                     _ptr(scale), lds, _ptr(ws), ws.numel(), _stream(stream))
-    _ok("ctr_fp8_quantize_rows", st)
+    n, cols, ld = _mat(x, "x")
+    rows = _codes_of(q, row_index, n, cols)
+    lds = _like(scale, "scale", (cols + 127) // 128, rows, _F32)
+    st = lib().ctr_fp8_quantize_rows(x.data_ptr(), DTYPES[x.dtype], n, rows, cols, ld, _ptr(row_index), q.data_ptr(),
+                                     scale.data_ptr(), lds, ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok("ctr_fp8_quantize_rows", st)
 
 
 def ctr_fp8_quantize_rows_cols(x: torch.Tensor, offsets: torch.Tensor, q: torch.Tensor, scale: torch.Tensor,
                                qc: torch.Tensor, scale_c: torch.Tensor, cols_by: int, ws: torch.Tensor,
                                row_index: Optional[torch.Tensor] = None, stream=None) -> None:
     """Row codes as above, and the column codes qc [cols, padded rows] of the grouped rows, in one read of x."""
-    n, cols = _mat(x, "x").shape
-    rows = _index(row_index, q, x)
+    n, cols, ld = _mat(x, "x")
+    rows = _codes_of(q, row_index, n, cols)
     groups = offsets.numel() - 1
-    _dense(offsets, "offsets", torch.int32, (groups + 1,))
     _want(groups >= 1, "offsets must have at least two entries")
+    _dense(offsets, "offsets", _I32, (groups + 1,))
     padded = fp8_padded_rows(rows, groups)
-    _dense(q, "q", torch.uint8, (rows, fp8_padded(cols)))
-    lds = _scales(scale, "scale", fp8_blocks(cols), rows)
-    _dense(qc, "qc", torch.uint8, (cols, padded))
-    _dense(scale_c, "scale_c", torch.float32, (padded // 128, cols) if cols_by == FP8_COLS_BY_COLUMN
-           else (fp8_blocks(cols), padded // 128))
-    st = lib().ctr_fp8_quantize_rows_cols(_ptr(x), DTYPES[x.dtype], n, rows, cols, _ld(x), _ptr(row_index),
-                                          _ptr(offsets), groups, int(cols_by), _ptr(q), _ptr(scale), lds, _ptr(qc),
-                                          _ptr(scale_c), _ptr(ws), ws.numel(), _stream(stream))
-    _ok("ctr_fp8_quantize_rows_cols", st)
+    lds = _like(scale, "scale", (cols + 127) // 128, rows, _F32)
+    _dense(qc, "qc", _U8, (cols, padded))
+    _dense(scale_c, "scale_c", _F32, (padded // 128, cols) if cols_by == FP8_COLS_BY_COLUMN
+           else ((cols + 127) // 128, padded // 128))
+    st = lib().ctr_fp8_quantize_rows_cols(x.data_ptr(), DTYPES[x.dtype], n, rows, cols, ld, _ptr(row_index),
+                                          offsets.data_ptr(), groups, cols_by, q.data_ptr(), scale.data_ptr(), lds,
+                                          qc.data_ptr(), scale_c.data_ptr(), ws.data_ptr(), ws.numel(),
+                                          _stream(stream))
+    if st:
+        _ok("ctr_fp8_quantize_rows_cols", st)
 
 
 def ctr_fp8_quantize_blocks(w: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, ws: torch.Tensor,
@@ -625,20 +630,22 @@ def ctr_fp8_quantize_blocks(w: torch.Tensor, q: torch.Tensor, scale: torch.Tenso
 def ctr_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
                    offsets: Optional[torch.Tensor], out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """out[r] = W_g a_r for the rows of each group, from row codes a [rows, P(k)] and block codes b [groups, n, P(k)]."""
+    rows, n, ldo = _mat(out, "out")
     _want(isinstance(b, torch.Tensor) and b.dim() == 3, "b must be [groups, n, padded k]")
-    G, n, kp = b.shape
-    rows = _mat(out, "out").shape[0]
+    G, bn, kp = b.shape
+    _want(bn == n, "out must have a column for each row of b")
     _want(kp % 128 == 0 and kp > 0, "codes must have whole blocks of 128")
-    _want(out.shape[1] == n, f"out must have {n} columns")
-    _dense(a, "a", torch.uint8, (rows, kp))
-    _dense(b, "b", torch.uint8, (G, n, kp))
-    lds = _scales(a_scale, "a_scale", kp // 128, rows)
-    _dense(b_scale, "b_scale", torch.float32, (G, fp8_blocks(n), kp // 128))
+    _dense(a, "a", _U8, (rows, kp))
+    _dense(b, "b", _U8, (G, n, kp))
+    lds = _like(a_scale, "a_scale", kp // 128, rows, _F32)
+    _dense(b_scale, "b_scale", _F32, (G, (n + 127) // 128, kp // 128))
     if offsets is not None:
-        _dense(offsets, "offsets", torch.int32, (G + 1,))
-    st = lib().ctr_fp8_matmul(_ptr(a), _ptr(a_scale), lds, _ptr(b), _ptr(b_scale), _ptr(offsets), rows, G, n, kp,
-                              _ptr(out), DTYPES[out.dtype], _ld(out), _ptr(ws), ws.numel(), _stream(stream))
-    _ok("ctr_fp8_matmul", st)
+        _dense(offsets, "offsets", _I32, (G + 1,))
+    st = lib().ctr_fp8_matmul(a.data_ptr(), a_scale.data_ptr(), lds, b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),
+                              rows, G, n, kp, out.data_ptr(), DTYPES[out.dtype], ldo, ws.data_ptr(), ws.numel(),
+                              _stream(stream))
+    if st:
+        _ok("ctr_fp8_matmul", st)
 
 
 def ctr_fp8_matmul_wgrad(d: torch.Tensor, d_scale: torch.Tensor, x: torch.Tensor, x_scale: torch.Tensor,
@@ -684,6 +691,8 @@ class GradList:
         self.out_ptrs = None if outs is None else (C.c_void_p * max(1, n))(*[t.data_ptr() for t in outs])
         self.dtypes = (C.c_int32 * max(1, n))(*[DTYPES[t.dtype] for t in grads])
         self.counts = (C.c_int64 * max(1, n))(*[t.numel() for t in grads])
+        self.addresses = tuple(None if a is None else C.addressof(a)
+                               for a in (self.ptrs, self.out_ptrs, self.dtypes, self.counts))
 
 
 def grad_list(grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None) -> GradList:
@@ -706,6 +715,7 @@ def ctr_clip_grads_workspace_size() -> int:
 def ctr_clip_grads(grads: GradList, max_norm: float, norm: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """The global norm of a grad_list into norm (fp32 [1]), and its outs = grads * min(1, max_norm / norm)."""
     _dense(norm, "norm", torch.float32, (1,))
-    st = lib().ctr_clip_grads(grads.ptrs, grads.out_ptrs, grads.dtypes, grads.counts, grads.n, float(max_norm),
-                              _ptr(norm), _ptr(ws), ws.numel(), _stream(stream))
-    _ok("ctr_clip_grads", st)
+    st = lib().ctr_clip_grads(*grads.addresses, grads.n, max_norm,
+                              norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+    if st:
+        _ok("ctr_clip_grads", st)
