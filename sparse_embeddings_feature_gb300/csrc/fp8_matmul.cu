@@ -69,6 +69,7 @@ struct MmArgs {
   int64_t rows;
   int32_t groups, m, n, kb;  // m: rows of a group's result (weight gradient); kb: blocks (product)
   int32_t nt, mt;            // column tiles; row tiles of a group (weight gradient)
+  int32_t splits;            // few rows: CTAs that share a tile's blocks
   int32_t out_f32, wide_rows;  // wide_rows: output rows start 16-byte aligned, and TMA may store them
 };
 
@@ -611,6 +612,208 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
   }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows a group: the weights are the left operand (128 of their rows to a
+// CTA), up to 32 of a group's rows the right one, so that a tile reads each
+// weight once and multiplies no more than 32 columns.  The blocks are shared out
+// over a cluster of up to eight CTAs, enough to keep every SM reading, and their
+// sums joined through distributed shared memory in the order of the blocks.  Two
+// CTAs an SM.  Bound by the weights' bytes, and below some megabytes by latency.
+// ---------------------------------------------------------------------------
+constexpr int kFewCols = 32;
+constexpr int kFewThreads = 192;  // warp 0: loads, 1: MMAs, 2..5: scaling
+constexpr int kFewStages = 5;
+constexpr uint32_t kFewStageBytes = kOperandBytes + kFewCols * 128;
+constexpr int kFewSmem = (int)(1024 + kFewStages * kFewStageBytes);
+constexpr int kFewChunk = 8;      // blocks whose scales are read together
+
+__global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(const MmArgs p,
+                                                                 const __grid_constant__ CUtensorMap wmap,
+                                                                 const __grid_constant__ CUtensorMap xmap) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bars[2 * kFewStages + 4];
+  __shared__ uint32_t tmem_base_slot;
+  __shared__ int32_t start[CTR_MAX_EXPERTS + 1], offs[CTR_MAX_EXPERTS + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  // [row of x][row of the weights]: this CTA's share of the sums, over the stages once they are used up
+  float(*sums)[kBM] = (float(*)[kBM])(smem_raw + (base - raw));
+  const uint32_t full0 = smem_u32(&bars[0]), empty0 = smem_u32(&bars[kFewStages]);
+  const uint32_t tfull0 = smem_u32(&bars[2 * kFewStages]), tempty0 = smem_u32(&bars[2 * kFewStages + 2]);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kFewStages; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 4);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
+                 "r"(2 * kFewCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (warp == 2) group_starts(p, start, offs, kFewCols);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_base_slot;
+
+  // this cluster's tile: 128 rows of the weights of a group, and up to 32 of its rows
+  const int split = (int)(blockIdx.x % p.splits), tile = (int)(blockIdx.x / p.splits);
+  const int u = tile / p.nt, ni = tile - u * p.nt;
+  const bool work = u < start[p.groups];
+  int lo = 0, hi = p.groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (start[mid] <= u) lo = mid;
+    else hi = mid - 1;
+  }
+  const int g = lo;
+  const int row0 = offs[g] + (u - start[g]) * kFewCols;
+  const int rows = work ? min(kFewCols, offs[g + 1] - row0) : 0;
+  const int j0 = (int)((int64_t)p.kb * split / p.splits), j1 = (int)((int64_t)p.kb * (split + 1) / p.splits);
+  const int nkb = work ? j1 - j0 : 0;
+
+  if (warp == 0) {
+    for (int j = 0; j < nkb; ++j) {
+      const int s = j % kFewStages;
+      if (j >= kFewStages && !park(empty0 + 8 * s, (uint32_t)((j / kFewStages - 1) & 1))) {
+        if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
+        break;
+      }
+      if (elected()) {
+        mbar_expect_tx(full0 + 8 * s, kFewStageBytes);
+        const uint32_t dst = base + (uint32_t)s * kFewStageBytes;
+        tma_load_2d(dst, &wmap, (j0 + j) * 128, g * p.n + ni * kBM, full0 + 8 * s);
+        tma_load_2d(dst + kOperandBytes, &xmap, (j0 + j) * 128, row0, full0 + 8 * s);
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t idesc = idesc_e4m3(kBM, kFewCols);
+    const uint64_t desc0 = smem_desc_sw128(base);
+    int done = 0;
+    for (int j = 0; j < nkb; ++j, ++done) {
+      const int s = j % kFewStages, b = j & 1;
+      if (!park(full0 + 8 * s, (uint32_t)((j / kFewStages) & 1)) ||
+          (j >= 2 && !park(tempty0 + 8 * b, (uint32_t)((j / 2 - 1) & 1)))) {
+        if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
+        break;
+      }
+      fence_after();
+      const uint64_t d = desc0 + (uint64_t)((uint32_t)s * (kFewStageBytes >> 4));
+      if (elected()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_e4m3<false>(tmem + b * kFewCols, d + 2 * k, d + (kOperandBytes >> 4) + 2 * k, idesc, k != 0);
+        mma_commit(empty0 + 8 * s);
+        mma_commit(tfull0 + 8 * b);
+      }
+      __syncwarp();
+    }
+    // drain: the MMAs are done with shared memory and TMEM, and every load that was waited for has landed
+    for (int j = max(0, done - 2); j < done; ++j)
+      if (!park(tfull0 + 8 * (j & 1), (uint32_t)((j / 2) & 1)) && lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
+    for (int j = done; j < min(nkb, done + kFewStages); ++j)  // after a failure: loads nobody used
+      park(full0 + 8 * (j % kFewStages), (uint32_t)((j / kFewStages) & 1));
+  } else {
+    const int q = warp & 3, n = q * 32 + lane;  // row of the weights
+    const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
+    const float* sa = p.sa + (int64_t)j0 * p.ld_sa + row0 + lane;  // lane t has row t of x
+    const float* sb = p.sb + (int64_t)(g * p.nt + ni) * p.ld_sb + j0;
+    uint64_t acc[kFewCols / 2];
+#pragma unroll
+    for (int i = 0; i < kFewCols / 2; ++i) acc[i] = 0;
+    bool ok = true;
+    for (int c = 0; ok && c < nkb; c += kFewChunk) {
+      float f[kFewChunk];
+#pragma unroll
+      for (int i = 0; i < kFewChunk; ++i)
+        f[i] = c + i < nkb && lane < rows ? __ldg(sa + (int64_t)(c + i) * p.ld_sa) * __ldg(sb + c + i) : 0.f;
+#pragma unroll
+      for (int i = 0; i < kFewChunk; ++i) {
+        const int j = c + i, b = j & 1;
+        if (j >= nkb) break;
+        if (!park(tfull0 + 8 * b, (uint32_t)((j / 2) & 1))) {
+          if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
+          ok = false;
+          break;
+        }
+        fence_after();
+        uint32_t v[kFewCols];
+        tmem_ld32(lane_base + b * kFewCols, v);
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty0 + 8 * b);
+#pragma unroll
+        for (int t = 0; t < kFewCols / 2; ++t) {
+          const float f0 = __shfl_sync(kFull, f[i], 2 * t), f1 = __shfl_sync(kFull, f[i], 2 * t + 1);
+          asm volatile(
+              "{\n\t.reg .b64 t, w;\n\t"
+              "mov.b64 t, {%1, %2};\n\t"
+              "mov.b64 w, {%3, %4};\n\t"
+              "fma.rn.f32x2 %0, t, w, %0;\n\t}"
+              : "+l"(acc[t])
+              : "r"(v[2 * t]), "r"(v[2 * t + 1]), "r"(__float_as_uint(f0)), "r"(__float_as_uint(f1)));
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kFewCols / 2; ++t) {
+      uint32_t a0, a1;
+      asm("mov.b64 {%0, %1}, %2;" : "=r"(a0), "=r"(a1) : "l"(acc[t]));
+      sums[2 * t][n] = __uint_as_float(a0);
+      sums[2 * t + 1][n] = __uint_as_float(a1);
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  if (p.splits > 1) cluster_sync();  // every CTA's sums are there
+  if (warp >= 2) {
+    const int n = (warp - 2) * 32 + lane, col = ni * kBM + n;
+    if (col < p.n) {
+      // the cluster's CTAs take the tile's rows in turn
+#pragma unroll 4
+      for (int t = split; t < rows; t += p.splits) {
+        float v = 0.f;
+        if (p.splits == 1) {
+          v = sums[t][n];
+        } else {
+          for (int r = 0; r < p.splits; ++r) {
+            float w;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(w) : "r"(in_cta(smem_u32(&sums[t][n]), r)) : "memory");
+            v += w;
+          }
+        }
+        const int64_t at = (int64_t)(row0 + t) * p.ldo + col;
+        if (p.out_f32) ((float*)p.out)[at] = v;
+        else ((__nv_bfloat16*)p.out)[at] = __float2bfloat16_rn(v);
+      }
+    }
+    if (p.offsets) {  // rows past the last group: zeros
+      const int64_t stride = (int64_t)gridDim.x * 4;
+      for (int64_t r = offs[p.groups] + (int64_t)blockIdx.x * 4 + (warp - 2); r < p.rows; r += stride)
+        for (int c = lane; c < p.n; c += 32) {
+          if (p.out_f32) ((float*)p.out)[r * p.ldo + c] = 0.f;
+          else ((uint16_t*)p.out)[r * p.ldo + c] = 0;
+        }
+    }
+  }
+  __syncthreads();
+  if (p.splits > 1) cluster_sync();  // no CTA leaves while another reads its sums
+  if (warp == 1) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kFewCols) : "memory");
+  }
+}
+
 // Codes [rows, bytes per row] in tiles of 128 bytes x `box` rows.
 bool code_map(CUtensorMap* map, const void* codes, int64_t rows, int64_t row_bytes, int box) {
   EncodeTiledFn enc = encode_fn();
@@ -675,6 +878,45 @@ int launch_mm(MmArgs& p, const uint8_t* a, int64_t a_rows, const uint8_t* b, int
   return e == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
 }
 
+int launch_few(MmArgs& p, const uint8_t* a, int64_t a_rows, const uint8_t* b, int64_t b_rows, int64_t row_bytes,
+               cudaStream_t s) {
+  CUtensorMap wmap, xmap;
+  if (!code_map(&wmap, b, b_rows, row_bytes, kBM) || !code_map(&xmap, a, a_rows, row_bytes, kFewCols))
+    return CTR_ERR_CUDA;
+  p.nt = (int32_t)ceil_div(p.n, kBM);
+  const int64_t units = imin64((a_rows + (kFewCols - 1) * (int64_t)p.groups) / kFewCols, a_rows);  // row tiles, at most
+  const int64_t tiles = imax64(1, p.offsets ? units : ceil_div(a_rows, kFewCols)) * p.nt;
+  // CTAs to a tile: until two fill every SM, at least two blocks each
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= 2 * num_sms() && p.splits * 4 <= p.kb) p.splits *= 2;
+  if (tiles * p.splits > INT32_MAX) return CTR_ERR_UNSUPPORTED;
+  static std::atomic<uint64_t> ready{0};
+  if (!once_per_device(ready, [&] {
+        return cudaFuncSetAttribute(fp8_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem) == cudaSuccess;
+      }))
+    return CTR_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * p.splits));
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = kFewSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)p.splits;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_few_kernel, p, wmap, xmap);
+  count_launch();
+  return e == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
+}
+
+// Up to 16 rows a group on average go to the kernel that streams the weights (device time of one
+// call with cold caches, its launch included; few rows against 128 x 128 tiles): 1 row of 4096 x 4096
+// 15.0 us against 21.2, 16 groups of 8 rows of 2048 x 1024 17.1 against 19.1, of 32 rows 19.1 against
+// 19.1, of 64 rows 25.2 against 19.1; 32 rows of 1024 x 512 13.0 against 10.9.
+bool few_rows(int64_t rows, int32_t groups) { return rows <= 16 * (int64_t)groups; }
+
 // A pair of CTAs on 256 x 256 tiles where there are tiles for most of the pairs.
 bool use_pair(int64_t tiles_m256, int64_t n) { return n > 128 && tiles_m256 * ceil_div(n, 256) >= num_sms() / 3; }
 
@@ -728,6 +970,7 @@ extern "C" int ctr_fp8_matmul(const uint8_t* a, const float* a_scale, int64_t ld
   p.wide_rows = ((uintptr_t)out % 16) == 0 && (ldo * eb) % 16 == 0 && ldo * eb < (1ll << 40);
   cudaStream_t s = (cudaStream_t)stream;
   const int64_t row_bytes = (int64_t)p.kb * 128;
+  if (few_rows(rows, groups)) return launch_few(p, a, rows, b, groups * n, row_bytes, s);
   const int64_t m256 = ceil_div(rows + 255 * (int64_t)(groups - 1), 256);  // row tiles, at most
   const int64_t m128 = ceil_div(rows + 127 * (int64_t)(groups - 1), 128);
   if (rows >= 128 * (int64_t)groups && use_pair(ceil_div(rows, 256), n))
