@@ -233,16 +233,24 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int take)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(take) : "memory");
 }
 
+// Threads of a tile's CTA: fp32 tiles are twice as large, so only three CTAs fit an SM, and get twice
+// the threads to keep as many warps (65536 x 479 fp32: 37 us with 256).
+template <typename T>
+constexpr int tile_threads() {
+  return sizeof(T) == 4 ? 512 : 256;
+}
+
 // One 128 x 128 tile.  ROW_BLOCK: the row codes have one scale for the tile (else one a row);
 // COL_BLOCK: the column codes have (else one a column).
 template <typename T, bool ROW_BLOCK, bool COL_BLOCK>
-__global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_tile_kernel(const TileArgs a) {
-  constexpr int kLd = tile_ld<T>();
+__global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) quantize_tile_kernel(const TileArgs a) {
+  constexpr int kLd = tile_ld<T>(), kThreads = tile_threads<T>();
+  constexpr int kPartRows = 64 * 128 / kThreads, kParts = 128 / kPartRows;  // rows of two columns that a thread takes
   extern __shared__ __align__(16) uint8_t smem[];
   T* tile = (T*)smem;
-  __shared__ float col_max[4][128];  // then [0]: the columns' multipliers
+  __shared__ float col_max[kParts][128];  // then [0]: the columns' multipliers
   __shared__ float row_max[128];     // then the rows' multipliers
-  __shared__ float warp_max[kQThreads / 32];
+  __shared__ float warp_max[kThreads / 32];
   __shared__ int where[4];  // group, first row, rows, tile number (of all groups)
   const int col0 = blockIdx.y * 128;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -309,12 +317,12 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
     const int take = max(0, min(16, (ncols - c) * (int)sizeof(T)));
     const T* from = (const T*)a.x + xbase * a.ldx + (take ? col0 + c : 0);
 #pragma unroll 4
-    for (int i = (int)threadIdx.x / parts; i < 128; i += kQThreads / parts) {
+    for (int i = (int)threadIdx.x / parts; i < 128; i += kThreads / parts) {
       const int64_t src = i < n ? source_row(a.row_index, row0 + i, a.x_rows, a.err) : -1;
       copy_async<16>(tile + i * kLd + c, src >= 0 ? from + src * a.ldx : (const T*)a.x, src >= 0 ? take : 0);
     }
   } else {
-    for (int i = warp; i < 128; i += kQThreads / 32) {
+    for (int i = warp; i < 128; i += kThreads / 32) {
       const int64_t src = i < n ? xbase + source_row(a.row_index, row0 + i, a.x_rows, a.err) : -1;
       const T* row = (const T*)a.x + (src >= 0 ? src * a.ldx + col0 : 0);
 #pragma unroll
@@ -332,11 +340,11 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
   // Maxima.  Rows: 16 lanes a row, 8 values each; columns: two and 32 of their rows to a thread.
   const int64_t qcol = col0 + lane16 * 8;
   const int c = (threadIdx.x & 63) * 2, part = threadIdx.x >> 6;
-  const T* mine = tile + part * 32 * kLd + c;
+  const T* mine = tile + part * kPartRows * kLd + c;
   float tile_max = 0.f;
 #pragma unroll 4
-  for (int p = 0; p < 8; ++p) {
-    const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
+  for (int p = 0; p < 128 * 16 / kThreads; ++p) {
+    const int i = p * (kThreads / 16) + (threadIdx.x >> 4);
     MaxPair<T> mp;
 #pragma unroll
     for (int e = 0; e < 8; e += 2) mp.add(tile + i * kLd + lane16 * 8 + e);
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
   if constexpr (!COL_BLOCK) {
     MaxPair<T> mp;
 #pragma unroll 8
-    for (int i = 0; i < 32; ++i) mp.add(mine + i * kLd);
+    for (int i = 0; i < kPartRows; ++i) mp.add(mine + i * kLd);
     *(float2*)&col_max[part][c] = mp.get();
   }
   float block_amax = 0.f, block_inv = 0.f;
@@ -366,7 +374,7 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
   if constexpr (ROW_BLOCK || COL_BLOCK) {
     tile_max = 0.f;
 #pragma unroll
-    for (int w = 0; w < kQThreads / 32; ++w) tile_max = max_mag(tile_max, warp_max[w]);
+    for (int w = 0; w < kThreads / 32; ++w) tile_max = max_mag(tile_max, warp_max[w]);
     block_amax = at_least_floor(tile_max);
     block_inv = __fdiv_rn(kTop, block_amax);
   }
@@ -383,10 +391,11 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
       const float m = at_least_floor(row_max[i]);
       row_max[i] = __fdiv_rn(kTop, m);
       if (i < n) a.scale[(int64_t)blockIdx.y * a.ld_scale + row0 + i] = __fdiv_rn(m, kTop);
+    } else if (threadIdx.x >= 256) {
     } else if constexpr (!COL_BLOCK) {
       float m = 0.f;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) m = max_mag(m, col_max[p][i]);
+      for (int p = 0; p < kParts; ++p) m = max_mag(m, col_max[p][i]);
       m = at_least_floor(m);
       col_max[0][i] = __fdiv_rn(kTop, m);
       if (i < ncols) a.scale_t[(int64_t)tnum * a.ld_scale_t + col0 + i] = __fdiv_rn(m, kTop);
@@ -398,8 +407,8 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
   // Row codes.
   uint8_t* q = a.q + ((ROW_BLOCK ? xbase : 0) + row0) * a.ldq + qcol;
 #pragma unroll 4
-  for (int p = 0; p < 8; ++p) {
-    const int i = p * (kQThreads / 16) + (threadIdx.x >> 4);
+  for (int p = 0; p < 128 * 16 / kThreads; ++p) {
+    const int i = p * (kThreads / 16) + (threadIdx.x >> 4);
     float v[8];
     load8(tile + i * kLd, lane16 * 8, 128, true, v);
     const float inv = ROW_BLOCK ? block_inv : row_max[i];
@@ -409,9 +418,9 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
   const float inv0 = COL_BLOCK ? block_inv : col_max[0][c], inv1 = COL_BLOCK ? block_inv : col_max[0][c + 1];
   // The codes go through shared memory (over the tile, which is in registers by then), so that eight
   // lanes write a column's 128 bytes together.
-  uint32_t w[2][8];
+  uint32_t w[2][kPartRows / 4];
 #pragma unroll
-  for (int b = 0; b < 8; ++b) {
+  for (int b = 0; b < kPartRows / 4; ++b) {
     float f0[4], f1[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -427,15 +436,16 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 2 ? 5 : 3) quantize_ti
   __syncthreads();
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint4* dst = (uint4*)(codes + (c + h) * kCodeLd + part * 32);
-    dst[0] = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
-    dst[1] = make_uint4(w[h][4], w[h][5], w[h][6], w[h][7]);
+    uint4* dst = (uint4*)(codes + (c + h) * kCodeLd + part * kPartRows);
+#pragma unroll
+    for (int b = 0; b < kPartRows / 16; ++b)
+      dst[b] = make_uint4(w[h][4 * b], w[h][4 * b + 1], w[h][4 * b + 2], w[h][4 * b + 3]);
   }
   __syncthreads();
   const int64_t qrow = (ROW_BLOCK ? (int64_t)g * a.cols : 0) + col0;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const int cc = p * 32 + (threadIdx.x >> 3), piece = threadIdx.x & 7;
+  for (int p = 0; p < 128 * 8 / kThreads; ++p) {
+    const int cc = p * (kThreads / 8) + (threadIdx.x >> 3), piece = threadIdx.x & 7;
     if (col0 + cc < a.cols)
       *(uint4*)(a.qt + (qrow + cc) * a.ldt + (int64_t)tnum * 128 + piece * 16) =
           *(const uint4*)(codes + cc * kCodeLd + piece * 16);
@@ -451,7 +461,7 @@ int launch_tiles(const TileArgs& a, int64_t tiles, cudaStream_t s) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
       }))
     return CTR_ERR_CUDA;
-  k<<<dim3((unsigned)tiles, (unsigned)a.col_blocks), kQThreads, smem, s>>>(a);
+  k<<<dim3((unsigned)tiles, (unsigned)a.col_blocks), tile_threads<T>(), smem, s>>>(a);
   count_launch();
   return launch_status();
 }

@@ -50,6 +50,7 @@ constexpr uint32_t kOperandBytes = kBM * 128;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 4;
 constexpr int kSuper = 8;                       // row tiles that take the column tiles together
+constexpr int kSorted = 128;                    // groups whose sums are sorted by length
 constexpr int kChunk = 8;                       // blocks whose scales come together
 // A scaling warp's pieces of the result on their way out: 32 rows of 128 bytes each, two of them, in
 // the 128-byte swizzle (16-byte part i of row r at i ^ (r mod 8)).
@@ -193,7 +194,8 @@ struct Tile {
   int64_t out_row;    // first output row of this CTA
 };
 
-// Tile t, as seen from CTA `rank` of a pair (0 alone).
+// Tile t, as seen from CTA `rank` of a pair (0 alone).  Weight gradient: offs holds the groups, the
+// one with most blocks first.
 template <bool PAIR, bool WGRAD>
 __device__ __forceinline__ Tile locate(const MmArgs& p, const int32_t* start, const int32_t* offs, int t, int rank) {
   constexpr int kTileM = PAIR ? 2 * kBM : kBM, kBN = PAIR ? 256 : 128;
@@ -203,6 +205,7 @@ __device__ __forceinline__ Tile locate(const MmArgs& p, const int32_t* start, co
     const int per = p.mt * p.nt;
     g = t / per;
     const int l = t - g * per;
+    g = offs[g];
     ni = l / p.mt;
     mi = l - ni * p.mt;
     x.nkb = start[g + 1] - start[g];
@@ -347,6 +350,20 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
   if (warp == 4) group_starts(p, start, offs, WGRAD ? 128 : kCtas * kBM);
   fence_before();
   __syncthreads();
+  if constexpr (WGRAD) {
+    // Long sums first, so that the last tiles to start are short ones (experts are chosen unevenly).  A
+    // group's place is the number of groups before it; beyond kSorted groups they keep their order.
+    for (int g = threadIdx.x; g < p.groups; g += kMmThreads) {
+      const int mine = start[g + 1] - start[g];
+      int place = p.groups <= kSorted ? 0 : g;
+      for (int o = 0; o < p.groups && p.groups <= kSorted; ++o) {
+        const int other = start[o + 1] - start[o];
+        place += other > mine || (other == mine && o < g);
+      }
+      offs[place] = g;
+    }
+    __syncthreads();
+  }
   if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are ready too
   fence_after();
   const uint32_t tmem = tmem_base_slot;
@@ -1003,6 +1020,8 @@ extern "C" int ctr_fp8_matmul_wgrad(const uint8_t* d, const float* d_scale, cons
   const int eb = dtype_bytes(out_dtype);
   p.wide_rows = ((uintptr_t)out % 16) == 0 && (k * eb) % 16 == 0 && groups * n < INT32_MAX;
   cudaStream_t s = (cudaStream_t)stream;
-  if (n > 128 && use_pair(groups * ceil_div(n, 256), k)) return launch_mm<true, true>(p, d, n, x, k, padded, 0, s);
+  // sums of uneven length want more tiles than the products' even ones: 64 tiles of 256 x 256 for 16
+  // uneven groups left the longest alone, 32 us against 22 with 256 tiles of 128 x 128
+  if (n > 128 && k > 128 && groups * ceil_div(n, 256) * ceil_div(k, 256) >= num_sms()) return launch_mm<true, true>(p, d, n, x, k, padded, 0, s);
   return launch_mm<false, true>(p, d, n, x, k, padded, 0, s);
 }
