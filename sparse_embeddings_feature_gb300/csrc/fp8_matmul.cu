@@ -305,6 +305,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
   __shared__ uint64_t bars[2 * kStages + 8];
   __shared__ uint32_t tmem_base_slot;
   __shared__ int32_t start[CTR_MAX_EXPERTS + 1], offs[CTR_MAX_EXPERTS + 1];
+  __shared__ Tile info[2];  // a tile's place, with its first chunk of scales
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t raw = smem_u32(smem_raw);
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
       mbar_init(tempty0 + 8 * b, kCtas * kScaleWarps);
-      mbar_init(cfull0 + 8 * b, 32);
+      mbar_init(cfull0 + 8 * b, 33);
       mbar_init(cempty0 + 8 * b, kScaleWarps);
     }
     fence_mbar_init();
@@ -464,7 +465,8 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
         const int h = lane / kChunk, u = lane % kChunk;  // 16 lanes: a block scale each
         const bool has_b = h < kCtas && x.col + 128 * h < p.n;
         const float* sb = p.sb + (int64_t)(x.sb0 + h) * p.ld_sb + x.k0 + u;
-        for (int j0 = 0; j0 < x.nkb; j0 += kChunk) {
+        // a tile without blocks has one empty chunk: its place has to reach the scaling warps
+        for (int j0 = 0; j0 == 0 || j0 < x.nkb; j0 += kChunk) {
           if (!park(cempty0 + 8 * b, ph ^ 1)) {
             if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
             ok = false;
@@ -479,6 +481,10 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
           if (h < 2)
             copy_scale(smem_u32(col_scales + (b * 2 + h) * kChunk + u), sb + j0, has_b && j0 + u < x.nkb, p.sb);
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(cfull0 + 8 * b) : "memory");
+          if (lane == 0) {
+            info[b] = x;
+            mbar_arrive(cfull0 + 8 * b);
+          }
           ph ^= b;
           b ^= 1;
         }
@@ -496,16 +502,21 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
     uint8_t* staging = after_stages + (size_t)(warp - 4) * kStagingBytes;
     const uint32_t tempty_at = PAIR ? in_cta(tempty0, 0) : tempty0;
     uint32_t b = 0, ph = 0, cb = 0, cph = 0;  // accumulator, chunk of scales
-    uint32_t turn = 0;                         // piece of the staging
     bool ok = true;
     for (int t = first; ok && t < ntiles; t += step) {
-      const Tile x = locate<PAIR, WGRAD>(p, start, offs, t, (int)rank);
+      // the tile's place comes with its first scales: finding it here would hold the sums up
+      if (!park(cfull0 + 8 * cb, cph)) {
+        if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
+        ok = false;
+        break;
+      }
+      const int nkb = info[cb].nkb;
       uint64_t acc[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
-      for (int j = 0; j < x.nkb; ++j) {
+      for (int j = 0; j < nkb; ++j) {
         const int u = j % kChunk;
-        if ((u == 0 && !park(cfull0 + 8 * cb, cph)) || !park(tfull0 + 8 * b, ph)) {
+        if ((u == 0 && j > 0 && !park(cfull0 + 8 * cb, cph)) || !park(tfull0 + 8 * b, ph)) {
           if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
           ok = false;
           break;
@@ -531,7 +542,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
           scale_add32(acc + c / 2, v0, f2);
           scale_add32(acc + c / 2 + 16, v1, f2);
         }
-        if (u == kChunk - 1 || j + 1 == x.nkb) {
+        if (u == kChunk - 1 && j + 1 < nkb) {
           __syncwarp();
           if (lane == 0) mbar_arrive(cempty0 + 8 * cb);
           cph ^= cb;
@@ -541,67 +552,87 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
         b ^= 1;
       }
       if (!ok) break;
-      // ---- the rows leave through shared memory, 32 rows of 128 bytes at a time (64 columns of bf16, 32
-      // of fp32), two pieces in turn.  Where the output's rows are 16-byte aligned a piece of 32 rows
-      // leaves as one TMA store, which drains while the next tile is summed (stores from the threads, or a
-      // bulk copy a row, held the warps up for 3800 cycles a tile); else, and at a group's last rows and the
-      // result's last columns, the warp stores elements, consecutive columns together.
+      // the place is read again: the registers are full while the blocks are summed
+      const Tile x = info[cb];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cempty0 + 8 * cb);
+      cph ^= cb;
+      cb ^= 1;
+      // ---- the rows leave through shared memory, 32 rows of 128 bytes to a piece (64 columns of bf16, 32
+      // of fp32).  Where the output's rows are 16-byte aligned a piece of 32 rows leaves as one TMA store,
+      // which drains while the next tile is summed (stores from the threads, or a bulk copy a row, held the
+      // warps up for 3800 cycles a tile); else, and at a group's last rows and the result's last columns,
+      // the warp stores elements, consecutive columns together.  bf16: both pieces under one fence; fp32:
+      // four pieces in turn through the two places.
       const int nrows = min(32, x.rows - q * 32);
-      const int eb = p.out_f32 ? 4 : 2, width = 128 / eb;
-      const int64_t ld = p.ldo * eb;
-#pragma unroll
-      for (int c = 0; c < kCols; c += 32) {
-        if (!p.out_f32 && c % 64 != 0) continue;
-        const int col = x.col + part * kCols + c;
-        if (col >= p.n || nrows <= 0) break;
-        uint8_t* piece = staging + turn * kPieceBytes;
-        turn ^= 1;
-        asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the last piece in this place has left
-        __syncwarp();
-        uint8_t* row = piece + lane * 128;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint32_t w[4];
-          if (p.out_f32) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              asm("mov.b64 {%0, %1}, %2;" : "=r"(w[2 * k]), "=r"(w[2 * k + 1]) : "l"(acc[c / 2 + 2 * i + k]));
-          } else if (c % 64 == 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t lo, hi;
-              asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(acc[c / 2 + 4 * i + k]));
-              w[k] = bf16_pair(__uint_as_float(lo), __uint_as_float(hi));
-            }
-          }
-          *(uint4*)(row + ((i ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (p.wide_rows && nrows == 32 && col + width <= p.n) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
+      const int col0 = x.col + part * kCols;
+      if (nrows <= 0 || col0 >= p.n) continue;
+      const bool whole = p.wide_rows && nrows == 32;
+      auto leave = [&](const uint8_t* piece, int col) {
+        const int width = p.out_f32 ? 32 : 64;
+        if (whole && col + width <= p.n) {
           if (lane == 0)
             asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                              (uint64_t)&omap),
                          "r"(col), "r"((int32_t)(x.out_row + q * 32)), "r"(smem_u32(piece))
                          : "memory");
+        } else if (p.out_f32) {
+          float* out = (float*)p.out + (x.out_row + q * 32) * p.ldo + col + lane;
+          if (col + lane < p.n)
+            for (int r = 0; r < nrows; ++r)
+              out[r * p.ldo] = *(const float*)(piece + r * 128 + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
         } else {
-          __syncwarp();
-          char* out = p.out + ((x.out_row + q * 32) * p.ldo + col) * eb;
-          for (int r = 0; r < nrows; ++r) {
-            const uint8_t* src = piece + r * 128;
-            if (p.out_f32) {
-              if (col + lane < p.n)
-                ((float*)(out + r * ld))[lane] = *(const float*)(src + (((lane >> 2) ^ (r & 7)) * 16) + (lane & 3) * 4);
-            } else {
+          uint16_t* out = (uint16_t*)p.out + (x.out_row + q * 32) * p.ldo + col + lane;
 #pragma unroll
-              for (int h = 0; h < 64; h += 32)
-                if (col + h + lane < p.n)
-                  ((uint16_t*)(out + r * ld))[h + lane] =
-                      *(const uint16_t*)(src + ((((h + lane) >> 3) ^ (r & 7)) * 16) + ((h + lane) & 7) * 2);
-            }
-          }
+          for (int e = 0; e < 64; e += 32)
+            if (col + e + lane < p.n)
+              for (int r = 0; r < nrows; ++r)
+                out[r * p.ldo + e] =
+                    *(const uint16_t*)(piece + r * 128 + ((((e + lane) >> 3) ^ (r & 7)) * 16) + (lane & 7) * 2);
         }
-        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      };
+      uint8_t* row = staging + lane * 128;
+      if (p.out_f32) {
+#pragma unroll
+        for (int h = 0; h < kCols / 32; ++h) {
+          if (col0 + 32 * h >= p.n) break;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the place is free
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              asm("mov.b64 {%0, %1}, %2;" : "=r"(w[2 * k]), "=r"(w[2 * k + 1]) : "l"(acc[16 * h + 2 * i + k]));
+            *(uint4*)(row + (h & 1) * kPieceBytes + ((i ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          leave(staging + (h & 1) * kPieceBytes, col0 + 32 * h);
+          if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+      } else {
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last tile's pieces have left
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < kCols / 64; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t lo, hi;
+              asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(acc[32 * h + 4 * i + k]));
+              w[k] = bf16_pair(__uint_as_float(lo), __uint_as_float(hi));
+            }
+            *(uint4*)(row + h * kPieceBytes + ((i ^ (lane & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        if (whole) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < kCols / 64; ++h)
+          if (col0 + 64 * h < p.n) leave(staging + h * kPieceBytes, col0 + 64 * h);
+        if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       }
     }
     asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
