@@ -122,6 +122,7 @@ __device__ __forceinline__ double block_sum(double v, double* warp_sum) {
 
 __global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constant__ ClipList l, double* part) {
   __shared__ double warp_sum[kClipThreads / 32];
+  grid_wait();
   float acc = 0.f;
   double wide = 0.0;
   int since = 0;
@@ -167,6 +168,7 @@ __device__ __forceinline__ float clip_factor(const double* part, int n, float ma
 }
 
 __global__ void __launch_bounds__(kClipThreads) norm_only_kernel(const double* part, int n, float* norm) {
+  grid_wait();
   clip_factor(part, n, 0.f, norm);
 }
 
@@ -205,6 +207,7 @@ __device__ __forceinline__ void chunk_scale(const T* g, T* out, int n, float f) 
 
 __global__ void __launch_bounds__(kClipThreads) scale_kernel(const __grid_constant__ ClipList l, const double* part, int n_sums,
                                                              float max_norm, float* norm) {
+  grid_wait();
   const float f = clip_factor(part, n_sums, max_norm, norm);
   for (int64_t c = l.first[l.count] - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const int t = tensor_of(l, c);
@@ -274,8 +277,7 @@ extern "C" int ctr_clip_grads(const void* const* grads, void* const* outs, const
   for (int b = 0; b < batches; ++b) {
     const int i0 = b * kListMax, i1 = std::min(n_tensors, i0 + kListMax);
     const int grid = clip_grid(fill_list(&l, grads, outs, dtypes, counts, i0, i1), most);
-    norm_kernel<<<grid, kClipThreads, 0, s>>>(l, part + sums);
-    count_launch();
+    launch_after(norm_kernel, dim3(grid), kClipThreads, 0, s, 1, l, part + sums);
     sums += grid;
   }
   bool told = false;
@@ -284,13 +286,12 @@ extern "C" int ctr_clip_grads(const void* const* grads, void* const* outs, const
     if (batches > 1) fill_list(&l, grads, outs, dtypes, counts, i0, i1);
     const int64_t chunks = l.first[l.count];
     if (chunks == 0) continue;
-    scale_kernel<<<clip_grid(chunks, most), kClipThreads, 0, s>>>(l, part, sums, max_norm, told ? nullptr : norm);
-    count_launch();
+    launch_after(scale_kernel, dim3(clip_grid(chunks, most)), kClipThreads, 0, s, 1, l, part, sums, max_norm,
+                 told ? (float*)nullptr : norm);
     told = true;
   }
   if (!told) {
-    norm_only_kernel<<<1, kClipThreads, 0, s>>>(part, sums, norm);
-    count_launch();
+    launch_after(norm_only_kernel, dim3(1), kClipThreads, 0, s, 1, part, sums, norm);
   }
   return launch_status();
 }

@@ -79,6 +79,36 @@ inline bool once_per_device(std::atomic<uint64_t>& done, F&& setup) {
   return true;
 }
 
+// Launches `k` so that its blocks may be set up while the kernel before it in the stream drains
+// (programmatic dependent launch).  Such a kernel calls grid_wait() before it touches memory.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, unsigned cluster,
+                                const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+  count_launch();
+  return e;
+}
+
+// Waits until the kernel before this one in the stream is complete and its writes are visible; lets
+// the next one's blocks be set up from here on (they wait in turn).
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // Map the last CUDA error to a ctr_status.
 inline int launch_status() {
   cudaError_t e = cudaGetLastError();

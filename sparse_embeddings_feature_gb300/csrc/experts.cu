@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
   const int n = (int)imin64(a.tile, a.tokens - t0);
   for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
   __syncthreads();
+  grid_wait();
   const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
   const int per_pass = kRouteThreads / a.lanes;
   for (int p0 = 0; p0 < n; p0 += per_pass) {  // the same trips in every lane: the shuffles need all of them
@@ -310,6 +311,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 // lane, the tiles cut into one segment a warp.
 __global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a) {
   __shared__ int seg[32][33];
+  grid_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e = blockIdx.x * 32 + lane;
   const int per = (a.tiles + 31) / 32;
@@ -350,6 +352,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_rank_kernel(const RouteAr
   const int n = (int)imin64(a.tile, a.tokens - t0);
   for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
   __syncthreads();
+  grid_wait();
   for (int i = threadIdx.x; i < n * a.k; i += kRouteThreads) {
     const int e = a.expert[t0 * a.k + i], t = i / a.k;
     if (e >= 0) atomicOr(&bits[e * words + (t >> 5)], 1u << (t & 31));
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_rank_kernel(const RouteAr
 }
 
 __global__ void route_empty_kernel(int32_t* offsets, int experts) {
+  grid_wait();
   for (int e = threadIdx.x; e <= experts; e += blockDim.x) offsets[e] = 0;
 }
 
@@ -402,6 +406,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
   const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / a.lanes);
   int64_t t = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) / a.lanes;
   const int64_t trips = ceil_div(a.tokens, groups);  // the same in every lane
+  grid_wait();
   for (int64_t trip = 0; trip < trips; ++trip, t += groups) {
     const bool mine = t < a.tokens;
     const T* row = (const T*)a.scores + t * a.ld;
@@ -510,19 +515,7 @@ void launch_choose(const RouteArgs& a, size_t smem, bool cluster, cudaStream_t s
   auto k = a.k <= 4 ? (cluster ? route_choose_kernel<T, EPL, 4, true> : route_choose_kernel<T, EPL, 4, false>)
                     : (cluster ? route_choose_kernel<T, EPL, CTR_MAX_CHOICES, true>
                                : route_choose_kernel<T, EPL, CTR_MAX_CHOICES, false>);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)a.tiles);
-  cfg.blockDim = dim3(kRouteThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)a.tiles;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, k, a);
-  count_launch();
+  launch_after(k, dim3((unsigned)a.tiles), kRouteThreads, smem, s, cluster ? (unsigned)a.tiles : 1u, a);
 }
 
 template <typename T>
@@ -530,8 +523,7 @@ void launch_bwd(const RouteArgs& a, const float* dweight, T* dscores, int64_t ld
                 cudaStream_t s) {
   auto k = a.experts <= 256 ? (a.renormalize ? route_bwd_kernel<T, 8, true> : route_bwd_kernel<T, 8, false>)
                             : (a.renormalize ? route_bwd_kernel<T, 16, true> : route_bwd_kernel<T, 16, false>);
-  k<<<grid, kRouteThreads, 0, s>>>(a, dweight, dscores, ldd, vec_out);
-  count_launch();
+  launch_after(k, dim3(grid), kRouteThreads, 0, s, 1, a, dweight, dscores, ldd, vec_out);
 }
 
 // ---------------------------------------------------------------------------
@@ -584,6 +576,7 @@ __device__ __forceinline__ void zero_unused(const RowArgs& a, const Raw& zero) {
 template <int VB>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a) {
   using Raw = typename RawOf<VB>::type;
+  grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
   for (int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes; t < a.tokens; t += groups) {
@@ -610,6 +603,7 @@ template <typename T, int VB>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
   using Ch = Chunk<T, VB>;
   using Raw = typename Ch::Raw;
+  grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
   for (int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes; t < a.tokens; t += groups) {
@@ -650,6 +644,7 @@ template <typename T, int VB>
 __global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(const RowArgs a) {
   using Ch = Chunk<T, VB>;
   using Raw = typename Ch::Raw;
+  grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
   const int64_t trips = ceil_div(a.tokens, groups);  // the same in every lane: the shuffles need all of them
@@ -710,19 +705,13 @@ int plan_rows(RowArgs* a, int64_t row_bytes, int vb) {
   return (int)imax64(1, imin64(blocks, (int64_t)num_sms() * 16));
 }
 
-#define CTR_LAUNCH_TYPED(kernel, dtype, vb, grid, stream, args)                              \
-  do {                                                                                       \
-    if ((dtype) == CTR_F32) {                                                                \
-      if ((vb) == 16) kernel<float, 16><<<grid, kRowThreads, 0, stream>>>(args);             \
-      else if ((vb) == 8) kernel<float, 8><<<grid, kRowThreads, 0, stream>>>(args);          \
-      else kernel<float, 4><<<grid, kRowThreads, 0, stream>>>(args);                         \
-    } else {                                                                                 \
-      if ((vb) == 16) kernel<__nv_bfloat16, 16><<<grid, kRowThreads, 0, stream>>>(args);     \
-      else if ((vb) == 8) kernel<__nv_bfloat16, 8><<<grid, kRowThreads, 0, stream>>>(args);  \
-      else if ((vb) == 4) kernel<__nv_bfloat16, 4><<<grid, kRowThreads, 0, stream>>>(args);  \
-      else kernel<__nv_bfloat16, 2><<<grid, kRowThreads, 0, stream>>>(args);                 \
-    }                                                                                        \
-    count_launch();                                                                          \
+#define CTR_LAUNCH_TYPED(kernel, dtype, vb, grid, stream, args)                                       \
+  do {                                                                                                \
+    auto k = kernel<float, 4>;                                                                        \
+    if ((dtype) == CTR_F32) k = (vb) == 16 ? kernel<float, 16> : (vb) == 8 ? kernel<float, 8> : k;    \
+    else k = (vb) == 16 ? kernel<__nv_bfloat16, 16> : (vb) == 8 ? kernel<__nv_bfloat16, 8>            \
+             : (vb) == 4 ? kernel<__nv_bfloat16, 4> : kernel<__nv_bfloat16, 2>;                       \
+    launch_after(k, dim3(grid), kRowThreads, 0, stream, 1, args);                                     \
   } while (0)
 
 }  // namespace
@@ -749,8 +738,7 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   if (!ws_valid(ws, ws_bytes, ctr_expert_route_workspace_size(tokens, experts, k))) return CTR_ERR_WORKSPACE;
   cudaStream_t s = (cudaStream_t)stream;
   if (tokens == 0) {
-    route_empty_kernel<<<1, 128, 0, s>>>(offsets, experts);
-    count_launch();
+    launch_after(route_empty_kernel, dim3(1), 128, 0, s, 1, offsets, experts);
     return launch_status();
   }
   RouteArgs a = {};
@@ -783,10 +771,8 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
     else launch_choose<__nv_bfloat16, 16>(a, smem, cluster, s);
   }
   if (a.tiles > 1 && !cluster) {
-    route_scan_kernel<<<(unsigned)ceil_div(experts, 32), 1024, 0, s>>>(a);
-    count_launch();
-    route_rank_kernel<<<a.tiles, kRouteThreads, smem, s>>>(a);
-    count_launch();
+    launch_after(route_scan_kernel, dim3((unsigned)ceil_div(experts, 32)), 1024, 0, s, 1, a);
+    launch_after(route_rank_kernel, dim3((unsigned)a.tiles), kRouteThreads, smem, s, 1, a);
   }
   return launch_status();
 }
@@ -846,11 +832,10 @@ extern "C" int ctr_expert_dispatch(const void* x, ctr_dtype dtype, int64_t token
                                (uint64_t)row}, eb);
   const int grid = plan_rows(&a, row, vb);
   cudaStream_t s = (cudaStream_t)stream;
-  if (vb == 16) dispatch_kernel<16><<<grid, kRowThreads, 0, s>>>(a);
-  else if (vb == 8) dispatch_kernel<8><<<grid, kRowThreads, 0, s>>>(a);
-  else if (vb == 4) dispatch_kernel<4><<<grid, kRowThreads, 0, s>>>(a);
-  else dispatch_kernel<2><<<grid, kRowThreads, 0, s>>>(a);
-  count_launch();
+  if (vb == 16) launch_after(dispatch_kernel<16>, dim3(grid), kRowThreads, 0, s, 1, a);
+  else if (vb == 8) launch_after(dispatch_kernel<8>, dim3(grid), kRowThreads, 0, s, 1, a);
+  else if (vb == 4) launch_after(dispatch_kernel<4>, dim3(grid), kRowThreads, 0, s, 1, a);
+  else launch_after(dispatch_kernel<2>, dim3(grid), kRowThreads, 0, s, 1, a);
   return launch_status();
 }
 

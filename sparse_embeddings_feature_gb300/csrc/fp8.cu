@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(kQThreads) quantize_rows_kernel(const T* x, in
   const int64_t trips = ceil_div(rows, step);  // the same in every lane: the shuffles need all of them
   int64_t r = (int64_t)blockIdx.x * (kQThreads / 16) + (threadIdx.x >> 4);
   RowPart<T> cur, next;
+  grid_wait();
   load_part(cur, x, ldx, r < rows ? source_row(row_index, r, x_rows, err) : -1, kb0, lane16, cols, vec != 0);
   for (int64_t trip = 0; trip < trips; ++trip, r += step) {
     // the next row's loads fly while this one is converted
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
   __shared__ int where[4];  // group, first row, rows, tile number (of all groups)
   const int col0 = blockIdx.y * 128;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_wait();
   if (a.offsets) {
     // the groups' tiles come one after another: find this block's (one warp, 32 groups at a time)
     if (warp == 0) {
@@ -461,8 +463,7 @@ int launch_tiles(const TileArgs& a, int64_t tiles, cudaStream_t s) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
       }))
     return CTR_ERR_CUDA;
-  k<<<dim3((unsigned)tiles, (unsigned)a.col_blocks), tile_threads<T>(), smem, s>>>(a);
-  count_launch();
+  launch_after(k, dim3((unsigned)tiles, (unsigned)a.col_blocks), tile_threads<T>(), smem, s, 1, a);
   return launch_status();
 }
 
@@ -498,12 +499,11 @@ extern "C" int ctr_fp8_quantize_rows(const void* x, ctr_dtype dtype, int64_t x_r
   const dim3 grid((unsigned)imin64(ceil_div(rows, kQThreads / 16), resident), (unsigned)parts);
   cudaStream_t s = (cudaStream_t)stream;
   if (dtype == CTR_F32)
-    quantize_rows_kernel<<<grid, kQThreads, 0, s>>>((const float*)x, x_rows, rows, cols, ldx, vec, row_index, q,
-                                                    scale, ld_scale, kb, (int*)ws);
+    launch_after(quantize_rows_kernel<float>, grid, kQThreads, 0, s, 1, (const float*)x, x_rows, rows, cols, ldx, vec,
+                 row_index, q, scale, ld_scale, kb, (int*)ws);
   else
-    quantize_rows_kernel<<<grid, kQThreads, 0, s>>>((const __nv_bfloat16*)x, x_rows, rows, cols, ldx, vec, row_index,
-                                                    q, scale, ld_scale, kb, (int*)ws);
-  count_launch();
+    launch_after(quantize_rows_kernel<__nv_bfloat16>, grid, kQThreads, 0, s, 1, (const __nv_bfloat16*)x, x_rows, rows,
+                 cols, ldx, vec, row_index, q, scale, ld_scale, kb, (int*)ws);
   return launch_status();
 }
 
