@@ -101,9 +101,11 @@ struct MaxPair<float> {
 };
 template <>
 struct MaxPair<__nv_bfloat16> {
-  __nv_bfloat162 m = __float2bfloat162_rn(0.f);
-  __device__ __forceinline__ void add(const __nv_bfloat16* p) { m = __hmax2_nan(m, __habs2(*(const __nv_bfloat162*)p)); }
-  __device__ __forceinline__ float2 get() const { return __bfloat1622float2(m); }
+  uint32_t m = 0;  // magnitudes as unsigned 16-bit numbers: their order is the values', NaN above all
+  __device__ __forceinline__ void add(const __nv_bfloat16* p) { m = __vmaxu2(m, *(const uint32_t*)p & 0x7fff7fffu); }
+  __device__ __forceinline__ float2 get() const {
+    return make_float2(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
 };
 
 // Blocks of one row that a lane group takes at once: 64 bytes of loads a lane.
@@ -214,7 +216,10 @@ struct TileArgs {
 
 // Values of two neighbouring columns of a tile row.
 __device__ __forceinline__ float2 two(const float* p) { return *(const float2*)p; }
-__device__ __forceinline__ float2 two(const __nv_bfloat16* p) { return __bfloat1622float2(*(const __nv_bfloat162*)p); }
+__device__ __forceinline__ float2 two(const __nv_bfloat16* p) {
+  const uint32_t w = *(const uint32_t*)p;
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 
 // A tile row is 128 elements and 16 bytes more: 16-byte accesses stay aligned and a row's do not
 // meet the next one's banks.
