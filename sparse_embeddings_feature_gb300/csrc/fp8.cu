@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
   const int c = (threadIdx.x & 63) * 2, part = threadIdx.x >> 6;
   const T* mine = tile + part * kPartRows * kLd + c;
   float tile_max = 0.f;
-#pragma unroll 4
+#pragma unroll
   for (int p = 0; p < 128 * 16 / kThreads; ++p) {
     const int i = p * (kThreads / 16) + (threadIdx.x >> 4);
     MaxPair<T> mp;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
   }
   if constexpr (!COL_BLOCK) {
     MaxPair<T> mp;
-#pragma unroll 8
+#pragma unroll
     for (int i = 0; i < kPartRows; ++i) mp.add(mine + i * kLd);
     *(float2*)&col_max[part][c] = mp.get();
   }
@@ -412,14 +412,15 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
     __syncthreads();
   }
   // Row codes.
-  uint8_t* q = a.q + ((ROW_BLOCK ? xbase : 0) + row0) * a.ldq + qcol;
-#pragma unroll 4
+  uint8_t* q = a.q + ((ROW_BLOCK ? xbase : 0) + row0 + (threadIdx.x >> 4)) * a.ldq + qcol;
+#pragma unroll
   for (int p = 0; p < 128 * 16 / kThreads; ++p) {
     const int i = p * (kThreads / 16) + (threadIdx.x >> 4);
     float v[8];
     load8(tile + i * kLd, lane16 * 8, 128, true, v);
     const float inv = ROW_BLOCK ? block_inv : row_max[i];
-    if (i < n) *(uint2*)(q + i * a.ldq) = make_uint2(codes4(v, inv), codes4(v + 4, inv));
+    if (i < n) *(uint2*)q = make_uint2(codes4(v, inv), codes4(v + 4, inv));
+    q += (kThreads / 16) * a.ldq;
   }
   if (!a.qt) return;
   const float inv0 = COL_BLOCK ? block_inv : col_max[0][c], inv1 = COL_BLOCK ? block_inv : col_max[0][c + 1];
