@@ -539,7 +539,10 @@ int ctr_fp8_quantize_blocks(const void* w, ctr_dtype dtype, int32_t groups, int6
  * out [rows, n], row stride ldo.  Device errors: CTR_ERR_BAD_OFFSETS (zeros are
  * written), CTR_ERR_TIMEOUT.  The input gradient of out = W x is the same call
  * with dout's row codes and the transposed block codes.
- * Workspace (both products): ctr_fp8_matmul_workspace_size(rows, groups, n, k). */
+ * Workspace (both products): ctr_fp8_matmul_workspace_size(rows, groups, n, k),
+ * asked on the device of the call: the error word and, for a weight gradient
+ * whose tiles are few and sums long, the partial sums (up to 20 MB).  Of it
+ * ctr_fp8_matmul takes the error word alone. */
 size_t ctr_fp8_matmul_workspace_size(int64_t rows, int32_t groups, int64_t n, int64_t k);
 int ctr_fp8_matmul(const uint8_t* a, const float* a_scale, int64_t ld_scale, const uint8_t* b, const float* b_scale,
                    const int32_t* offsets, int64_t rows, int32_t groups, int64_t n, int64_t k, void* out,
@@ -548,7 +551,7 @@ int ctr_fp8_matmul(const uint8_t* a, const float* a_scale, int64_t ld_scale, con
 /* Weight gradient: out[g, i, j] = sum over the rows r of group g of d[r, i]
  * x[r, j], from column codes of d (by column, [n, P_rows]) and of x (by block,
  * [k, P_rows]) made with the same offsets.  out [groups, n, k], dense; zeros
- * for a group without rows. */
+ * for a group without rows, and everywhere after CTR_ERR_BAD_OFFSETS. */
 int ctr_fp8_matmul_wgrad(const uint8_t* d, const float* d_scale, const uint8_t* x, const float* x_scale,
                          const int32_t* offsets, int64_t rows, int32_t groups, int64_t n, int64_t k, void* out,
                          ctr_dtype out_dtype, void* ws, size_t ws_bytes, ctr_stream_t stream);

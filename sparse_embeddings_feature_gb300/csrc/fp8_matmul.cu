@@ -71,6 +71,7 @@ struct MmArgs {
   int32_t groups, m, n, kb;  // m: rows of a group's result (weight gradient); kb: blocks (product)
   int32_t nt, mt;            // column tiles; row tiles of a group (weight gradient)
   int32_t splits;            // few rows: CTAs that share a tile's blocks
+  int32_t seg;               // weight gradient: blocks of a partial sum; 0: sums are whole
   int32_t out_f32, wide_rows;  // wide_rows: output rows start 16-byte aligned, and TMA may store them
 };
 
@@ -195,7 +196,7 @@ struct Tile {
 };
 
 // Tile t, as seen from CTA `rank` of a pair (0 alone).  Weight gradient: offs holds the groups, the
-// one with most blocks first.
+// one with most blocks first; of partial sums, the number of them before each group.
 template <bool PAIR, bool WGRAD>
 __device__ __forceinline__ Tile locate(const MmArgs& p, const int32_t* start, const int32_t* offs, int t, int rank) {
   constexpr int kTileM = PAIR ? 2 * kBM : kBM, kBN = PAIR ? 256 : 128;
@@ -203,13 +204,21 @@ __device__ __forceinline__ Tile locate(const MmArgs& p, const int32_t* start, co
   int g, mi, ni;
   if constexpr (WGRAD) {
     const int per = p.mt * p.nt;
-    g = t / per;
-    const int l = t - g * per;
-    g = offs[g];
+    const int q = t / per;
+    const int l = t - q * per;
     ni = l / p.mt;
     mi = l - ni * p.mt;
-    x.nkb = start[g + 1] - start[g];
-    x.k0 = start[g];
+    if (p.seg) {
+      g = 0;
+      while (offs[g + 1] <= q) ++g;
+      x.k0 = start[g] + (q - offs[g]) * p.seg;
+      x.nkb = min(p.seg, start[g + 1] - x.k0);
+      g = q;  // the partial result's place
+    } else {
+      g = offs[q];
+      x.k0 = start[g];
+      x.nkb = start[g + 1] - start[g];
+    }
     x.a_row = mi * kTileM + rank * kBM;
     x.rows = min(kBM, p.m - x.a_row);
     x.b_row = ni * kBN;
@@ -293,6 +302,13 @@ __device__ __forceinline__ void group_starts(const MmArgs& p, int32_t* start, in
   }
 }
 
+// Partial sums of the groups before g.
+__device__ __forceinline__ int sums_before(const int32_t* start, int g, int seg) {
+  int n = 0;
+  for (int o = 0; o < g; ++o) n += (start[o + 1] - start[o] + seg - 1) / seg;
+  return n;
+}
+
 template <bool PAIR, bool WGRAD>
 __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs p,
                                                                    const __grid_constant__ CUtensorMap amap,
@@ -353,9 +369,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
   fence_before();
   __syncthreads();
   if constexpr (WGRAD) {
-    // Long sums first, so that the last tiles to start are short ones (experts are chosen unevenly).  A
-    // group's place is the number of groups before it; beyond kSorted groups they keep their order.
-    for (int g = threadIdx.x; g < p.groups; g += kMmThreads) {
+    // Partial sums in the order of the groups.  Whole ones: the long first, so that the last tiles to
+    // start are short (experts are chosen unevenly).  A group's place is the number of groups before it;
+    // beyond kSorted groups they keep their order.
+    if (p.seg) {
+      for (int g = threadIdx.x; g <= p.groups; g += kMmThreads) offs[g] = sums_before(start, g, p.seg);
+    } else for (int g = threadIdx.x; g < p.groups; g += kMmThreads) {
       const int mine = start[g + 1] - start[g];
       int place = p.groups <= kSorted ? 0 : g;
       for (int o = 0; o < p.groups && p.groups <= kSorted; ++o) {
@@ -369,7 +388,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
   if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are ready too
   fence_after();
   const uint32_t tmem = tmem_base_slot;
-  const int ntiles = (WGRAD ? p.groups * p.mt : start[p.groups]) * p.nt;
+  const int ntiles = (!WGRAD ? start[p.groups] : (p.seg ? offs[p.groups] : p.groups) * p.mt) * p.nt;
   const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
   if (warp < 4) {
@@ -667,6 +686,47 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
 }
 
 // ---------------------------------------------------------------------------
+// Weight gradient in partial sums: the groups' planes of n x k, four columns of one row to a thread,
+// added in their order.
+// ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) join_sums_kernel(const MmArgs p, const float* __restrict__ part,
+                                                                 int64_t ld, bool vec) {
+  __shared__ int32_t start[CTR_MAX_EXPERTS + 1], offs[CTR_MAX_EXPERTS + 1];
+  grid_wait();
+  if (threadIdx.x < 32) group_starts(p, start, offs, 128);
+  __syncthreads();
+  const int g = blockIdx.y;
+  const int count = (start[g + 1] - start[g] + p.seg - 1) / p.seg;
+  const int quads = (int)(ld / 4), e = blockIdx.x * kJoinThreads + threadIdx.x;
+  const int row = e / quads, c = (e - row * quads) * 4;
+  if (row >= p.m) return;
+  const int64_t plane = p.m * ld;
+  const float* from = part + sums_before(start, g, p.seg) * plane + row * ld + c;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int s = 0; s < count; ++s) {
+    const float4 v = *(const float4*)(from + s * plane);
+    sum.x += v.x;
+    sum.y += v.y;
+    sum.z += v.z;
+    sum.w += v.w;
+  }
+  T* out = (T*)p.out + ((int64_t)g * p.m + row) * p.n + c;
+  if (vec) {
+    if constexpr (sizeof(T) == 4) *(float4*)out = sum;
+    else *(uint2*)out = make_uint2(bf16_pair(sum.x, sum.y), bf16_pair(sum.z, sum.w));
+  } else {
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < p.n) out[i] = from_f32<T>(v[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
 // Few rows a group: the weights are the left operand (128 of their rows to a
 // CTA), up to 32 of a group's rows the right one, so that a tile reads each
 // weight once and multiplies no more than 32 columns.  The blocks are shared out
@@ -902,7 +962,8 @@ int launch_mm(MmArgs& p, const uint8_t* a, int64_t a_rows, const uint8_t* b, int
   CUtensorMap amap, bmap;
   if (!code_map(&amap, a, a_rows, row_bytes, kBM) || !code_map(&bmap, b, b_rows, row_bytes, kBM)) return CTR_ERR_CUDA;
   CUtensorMap omap = amap;  // not used unless the output's rows are aligned
-  if (p.wide_rows && !out_map(&omap, p, WGRAD ? (int64_t)p.groups * p.m : p.rows)) return CTR_ERR_CUDA;
+  const int64_t planes = p.seg ? tiles_m : p.groups;  // weight gradient: results of m rows
+  if (p.wide_rows && !out_map(&omap, p, WGRAD ? planes * p.m : p.rows)) return CTR_ERR_CUDA;
   constexpr int kCtas = PAIR ? 2 : 1;
   p.nt = (int32_t)ceil_div(p.n, PAIR ? 256 : 128);
   if (WGRAD) p.mt = (int32_t)ceil_div(p.m, kCtas * kBM);
@@ -915,7 +976,7 @@ int launch_mm(MmArgs& p, const uint8_t* a, int64_t a_rows, const uint8_t* b, int
                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem) == cudaSuccess;
       }))
     return CTR_ERR_CUDA;
-  const int64_t tiles = (WGRAD ? (int64_t)p.groups * p.mt : tiles_m) * p.nt;
+  const int64_t tiles = (WGRAD ? planes * p.mt : tiles_m) * p.nt;
   if (tiles > INT32_MAX - 65536) return CTR_ERR_UNSUPPORTED;
   const cudaError_t e = launch_after(k, dim3((unsigned)(kCtas * imax64(1, imin64(tiles, num_sms() / kCtas)))), kMmThreads,
                                      kMmSmem, s, kCtas, p, amap, bmap, omap);
@@ -950,8 +1011,59 @@ int launch_few(MmArgs& p, const uint8_t* a, int64_t a_rows, const uint8_t* b, in
 // 19.1, of 64 rows 25.2 against 19.1; 32 rows of 1024 x 512 13.0 against 10.9.
 bool few_rows(int64_t rows, int32_t groups) { return rows <= 16 * (int64_t)groups; }
 
-// A pair of CTAs on 256 x 256 tiles where there are tiles for most of the pairs.
-bool use_pair(int64_t tiles_m256, int64_t n) { return n > 128 && tiles_m256 * ceil_div(n, 256) >= num_sms() / 3; }
+// A pair of CTAs on 256 x 256 tiles where the groups fill a tile's rows and there are tiles for most of the
+// pairs (as above, pairs against 128 x 128 tiles): 16 groups of 2048 x 1024 with 128 rows each 23.2 us
+// against 19.1, 256 rows 23.2 against 25.2, 512 rows 31.4 against 35.5; one group of 8192 x 1024 with 256
+// rows (32 pairs) 14.9 against 13.0, 512 rows (64) 15.1 against 17.1.
+bool use_pair(int64_t rows, int64_t groups, int64_t n) {
+  return n > 128 && rows >= 256 * groups && ceil_div(rows, 256) * ceil_div(n, 256) >= num_sms() / 3;
+}
+
+// How a weight gradient is taken apart (figures: device time of a call with cold caches).  A pair of CTAs
+// has to have sums of some length, or more than a round of tiles, to be worth its setting up, and of
+// several groups, which are as a rule uneven, enough tiles for every pair (pairs against 128 x 128 tiles):
+// 16 groups of 2 to 3 blocks, 512 x 512, 15.0 us against 13.0, of 16 blocks 23.2 against 25.2 but uneven
+// 37.5 against 35.5; 4 groups of 32, 2048 x 1024, 43.7 against 58.0, uneven 49.9 against 58.0; one of 64
+// blocks, 2048 x 2048, 39.6 against 53.9.
+// Where the tiles of whole sums would leave half of the SMs idle, each group's sum is cut into partial
+// sums of `seg` blocks, as many as run at once, and a second kernel adds them up in their order: 65536
+// rows of 1024 x 1024 175 -> 76 us, 16384 rows of 512 x 479 52 -> 25, 8 uneven groups of 65536 rows of
+// 512 x 512 103 -> 46 (even ones 42 -> 48).  The parts and their kernel cost about as much as 8 blocks, so
+// shorter sums stay whole: 12 blocks of 1024 x 1024 17.0 us whole against 21.1, 16 19.1 against 21.1, 32
+// 25.2 against 23.2; 26 blocks of 512 x 479 25.2 against 21.1.
+struct WgradPlan {
+  bool pair;
+  int32_t seg = 0;     // blocks of a partial sum; 0: sums are whole
+  int64_t planes = 0;  // partial results of all groups, at most
+  int64_t ld = 0;      // their rows' stride, in elements (16-byte aligned rows)
+  size_t bytes() const { return (size_t)planes * ld * 4; }  // a row of each
+};
+
+// Blocks of a partial sum, at least: 4096 rows of 512 x 479 take 19.1 us with 4, 21.2 with 8 and 24.2 with
+// 16; 16384 rows 27.3, 25.3 and 25.2.
+constexpr int kMinSeg = 8;
+
+WgradPlan plan_wgrad(int64_t rows, int64_t groups, int64_t n, int64_t k) {
+  WgradPlan w;
+  const int64_t blocks = ctr_fp8_padded_rows(rows, (int32_t)groups) / 128;
+  const int64_t pairs = groups * ceil_div(n, 256) * ceil_div(k, 256);  // tiles of whole sums
+  const bool wide = n > 128 && k > 128;
+  w.pair = wide && (blocks >= 8 * groups || pairs >= num_sms());
+  const int64_t side = w.pair ? 256 : 128, workers = num_sms() / (w.pair ? 2 : 1);
+  const int64_t room = workers / (ceil_div(n, side) * ceil_div(k, side));  // planes that run at once
+  const auto whole = [&] {
+    w.pair = w.pair && (groups == 1 || pairs >= num_sms() / 2);
+    return w;
+  };
+  if (room < 2 * groups) return whole();
+  // a group's last partial sum may be short: as many are left over as there are groups
+  const int64_t seg = imax64(kMinSeg, ceil_div(blocks, groups == 1 ? room : room - groups));
+  if (blocks < groups * (seg + kMinSeg)) return whole();
+  w.seg = (int32_t)seg;
+  w.planes = groups == 1 ? ceil_div(blocks, seg) : room;
+  w.ld = ceil_div(k, 4) * 4;
+  return w;
+}
 
 int check_mm(const void* a, const float* sa, const void* b, const float* sb, const int32_t* offsets, int64_t rows,
              int32_t groups, int64_t n, int64_t k, const void* out, int out_dtype, void* ws, size_t ws_bytes) {
@@ -974,7 +1086,7 @@ using namespace ctr;
 
 extern "C" size_t ctr_fp8_matmul_workspace_size(int64_t rows, int32_t groups, int64_t n, int64_t k) {
   if (rows < 0 || groups < 1 || n < 1 || k < 1) return 0;
-  return kWsHeader;
+  return kWsHeader + plan_wgrad(rows, groups, n, k).bytes() * n;
 }
 
 extern "C" int ctr_fp8_matmul(const uint8_t* a, const float* a_scale, int64_t ld_scale, const uint8_t* b,
@@ -1006,7 +1118,7 @@ extern "C" int ctr_fp8_matmul(const uint8_t* a, const float* a_scale, int64_t ld
   if (few_rows(rows, groups)) return launch_few(p, a, rows, b, groups * n, row_bytes, s);
   const int64_t m256 = ceil_div(rows + 255 * (int64_t)(groups - 1), 256);  // row tiles, at most
   const int64_t m128 = ceil_div(rows + 127 * (int64_t)(groups - 1), 128);
-  if (rows >= 128 * (int64_t)groups && use_pair(ceil_div(rows, 256), n))
+  if (use_pair(rows, groups, n))
     return launch_mm<true, false>(p, a, rows, b, groups * n, row_bytes, m256, s);
   return launch_mm<false, false>(p, a, rows, b, groups * n, row_bytes, m128, s);
 }
@@ -1036,8 +1148,24 @@ extern "C" int ctr_fp8_matmul_wgrad(const uint8_t* d, const float* d_scale, cons
   const int eb = dtype_bytes(out_dtype);
   p.wide_rows = ((uintptr_t)out % 16) == 0 && (k * eb) % 16 == 0 && groups * n < INT32_MAX;
   cudaStream_t s = (cudaStream_t)stream;
-  // sums of uneven length want more tiles than the products' even ones: 64 tiles of 256 x 256 for 16
-  // uneven groups left the longest alone, 32 us against 22 with 256 tiles of 128 x 128
-  if (n > 128 && k > 128 && groups * ceil_div(n, 256) * ceil_div(k, 256) >= num_sms()) return launch_mm<true, true>(p, d, n, x, k, padded, 0, s);
-  return launch_mm<false, true>(p, d, n, x, k, padded, 0, s);
+  const WgradPlan w = plan_wgrad(rows, groups, n, k);
+  if (!w.seg)
+    return w.pair ? launch_mm<true, true>(p, d, n, x, k, padded, 0, s) : launch_mm<false, true>(p, d, n, x, k, padded, 0, s);
+  if (ws_bytes < kWsHeader + w.bytes() * n) return CTR_ERR_WORKSPACE;
+  float* part = (float*)((char*)ws + kWsHeader);
+  MmArgs q = p;
+  q.seg = p.seg = w.seg;
+  q.out = (char*)part;
+  q.out_f32 = q.wide_rows = 1;
+  q.ldo = w.ld;
+  const int e = w.pair ? launch_mm<true, true>(q, d, n, x, k, padded, w.planes, s)
+                       : launch_mm<false, true>(q, d, n, x, k, padded, w.planes, s);
+  if (e != CTR_OK) return e;
+  const dim3 grid((unsigned)ceil_div(n * (w.ld / 4), kJoinThreads), (unsigned)groups);
+  const bool vec = k % 4 == 0 && ((uintptr_t)out % (4 * eb)) == 0;
+  const cudaError_t j =
+      out_dtype == CTR_F32
+          ? launch_after(join_sums_kernel<float>, grid, kJoinThreads, 0, s, 1, p, (const float*)part, w.ld, vec)
+          : launch_after(join_sums_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, s, 1, p, (const float*)part, w.ld, vec);
+  return j == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
 }

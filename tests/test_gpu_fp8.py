@@ -325,6 +325,64 @@ def test_gradients_are_the_formulas(counts, n, k, dtype, out):
         assert R.within(dw[g], ref, R.product_bound(mag, _tiles([c])[0]) * 1.01, out)
 
 
+# sums long enough to be taken in parts: a few columns; one part of a block; uneven, empty and tiny groups;
+# rows past the last group; result rows that are not 16-byte aligned
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("counts,spare,n,k", [([5000], 0, 64, 70), ([16384], 0, 200, 479), ([2049], 300, 300, 260),
+                                              ([9000, 0, 3, 7000], 0, 300, 257), ([1, 6000], 100, 130, 128),
+                                              ([3000, 0, 2500, 40, 4000, 0, 900, 700], 0, 129, 300)])
+def test_weight_gradient_of_long_sums(counts, spare, n, k, out):
+    rng = np.random.default_rng(6)
+    off, rows, G = _offsets(counts), sum(counts) + spare, len(counts)
+    x, dy = _draw(rng, (rows, k), "bf16"), _draw(rng, (rows, n), "bf16")
+    Rp = ctr.fp8_padded_rows(rows, G)
+    kb, nb = ctr.fp8_blocks(k), ctr.fp8_blocks(n)
+    ws = ctr.workspace(ctr.ctr_fp8_matmul_workspace_size(rows, G, n, k))
+    o = torch.from_numpy(off).cuda()
+    xc, xcs, dc, dcs = _u8(k, Rp), _f32(kb, Rp // 128), _u8(n, Rp), _f32(Rp // 128, n)
+    ctr.ctr_fp8_quantize_rows_cols(x.cuda(), o, _u8(rows, kb * 128), _f32(kb, rows), xc, xcs, ctr.FP8_COLS_BY_BLOCK, ws)
+    ctr.ctr_fp8_quantize_rows_cols(dy.cuda(), o, _u8(rows, nb * 128), _f32(nb, rows), dc, dcs, ctr.FP8_COLS_BY_COLUMN,
+                                   ws)
+    got = []
+    for _ in range(2):
+        dw = torch.full((G, n, k), 7.0, dtype=DT[out], device="cuda")
+        ctr.ctr_fp8_matmul_wgrad(dc, dcs, xc, xcs, o, dw, ws, rows=rows)
+        got.append(dw)
+    assert ctr.ctr_check_status(ws) == 0
+    assert torch.equal(got[0], got[1])
+    dw, xv, dv = _np(got[0]), x.double().numpy(), dy.double().numpy()
+    for g, c in enumerate(counts):
+        if c == 0:
+            assert np.all(dw[g] == 0)
+            continue
+        r = slice(off[g], off[g + 1])
+        q, s = R.quantize(dv[r], 128, 1)
+        d_val = q * R.spread(s, 128, 1, c, n)
+        q, s = R.quantize(xv[r], 128, 128)
+        x_val = q * R.spread(s, 128, 128, c, k)
+        ref, mag = d_val.T @ x_val, np.abs(d_val).T @ np.abs(x_val)
+        assert R.within(dw[g], ref, R.product_bound(mag, _tiles([c])[0]) * 1.01, out)
+
+
+def test_weight_gradient_of_long_sums_bad_offsets_and_small_workspace():
+    rows, n, k = 6000, 64, 64
+    Rp = ctr.fp8_padded_rows(rows, 2)
+    need = ctr.ctr_fp8_matmul_workspace_size(rows, 2, n, k)
+    assert need > 256                             # the sums' parts are in it
+    ws = ctr.workspace(need)
+    xc, dc = torch.zeros((k, Rp), dtype=torch.uint8, device="cuda"), torch.zeros((n, Rp), dtype=torch.uint8, device="cuda")
+    xcs, dcs = torch.ones((1, Rp // 128), device="cuda"), torch.ones((Rp // 128, n), device="cuda")
+    for bad in ([0, 7, 3], [1, 4, 10], [0, 4, rows + 1], [0, -1, 10]):
+        dw = torch.full((2, n, k), 7.0, device="cuda")
+        ctr.ctr_fp8_matmul_wgrad(dc, dcs, xc, xcs, torch.tensor(bad, dtype=torch.int32, device="cuda"), dw, ws, rows=rows)
+        assert ctr.ctr_check_status(ws) == ctr.ERR_BAD_OFFSETS
+        assert torch.all(dw == 0)
+    o = torch.tensor([0, 10, rows], dtype=torch.int32, device="cuda")
+    with pytest.raises(ctr.CtrError) as e:
+        ctr.ctr_fp8_matmul_wgrad(dc, dcs, xc, xcs, o, dw, ctr.workspace(need - 256), rows=rows)
+    assert e.value.status == ctr.ERR_WORKSPACE
+
+
 def test_gradients_are_the_differences():
     # L = <dy, W x>.  Small integers with a 448 in every scale's block: all scales are 1, the codes hold
     # every value, the sums looked at stay below 2^24, so a difference of L by any step is the gradient
