@@ -530,7 +530,19 @@ void launch_bwd(const RouteArgs& a, const float* dweight, T* dscores, int64_t ld
 // rows
 // ---------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
-constexpr int kUnroll = 4;  // chunks of a row a lane holds at once
+// Chunks of a row that a lane holds at once: what it has in flight is what hides the reads' latency.  Rows
+// that can only be read in small parts want more of them (65536 x 478 bf16, two rows a token, 4-byte parts:
+// dispatch 41 us with 4, 37 with 8, the gradients 80 and 71; 479, 2 bytes: 53 with 4, 45 with 16, and
+// 100 and 89).
+template <int VB>
+constexpr int row_unroll() {
+  return VB >= 8 ? 4 : VB == 4 ? 8 : 16;
+}
+// Sums, where a lane reads two rows at once: 55 us with 4 against 66 with 8, and 76 with 4 against 72 with 16.
+template <int VB>
+constexpr int sum_unroll() {
+  return VB >= 4 ? 4 : 16;
+}
 
 struct RowArgs {
   const char* x;     // token rows (dispatch: read; backward: dy)
@@ -576,6 +588,7 @@ __device__ __forceinline__ void zero_unused(const RowArgs& a, const Raw& zero) {
 template <int VB>
 __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a) {
   using Raw = typename RawOf<VB>::type;
+  constexpr int kUnroll = row_unroll<VB>();
   grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
@@ -603,6 +616,7 @@ template <typename T, int VB>
 __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
   using Ch = Chunk<T, VB>;
   using Raw = typename Ch::Raw;
+  constexpr int kUnroll = sum_unroll<VB>();
   grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
@@ -644,6 +658,7 @@ template <typename T, int VB>
 __global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(const RowArgs a) {
   using Ch = Chunk<T, VB>;
   using Raw = typename Ch::Raw;
+  constexpr int kUnroll = row_unroll<VB>();
   grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
@@ -696,11 +711,17 @@ int check_rows(ctr_dtype dtype, int64_t tokens, int32_t d, int32_t k, void* ws, 
   return CTR_OK;
 }
 
-// Chunk count, lanes per row and grid of a row kernel.
+// Chunk count, lanes per row and grid of a row kernel.  A row gets as few lanes as hold it at once,
+// unless too few threads had one (65536 rows of 256 bf16, two rows a token, 8 lanes against 32: dispatch
+// 20 us against 25, combine 25 against 49, its gradients 37 against 72; 20000 rows of 480, 16 lanes
+// against 32, combine 18 against 25; 5000 rows of 256, 16 lanes: 8.2 against 10.2).
 int plan_rows(RowArgs* a, int64_t row_bytes, int vb) {
   a->chunks = (int32_t)(row_bytes / vb);
+  const int unroll = vb >= 8 ? row_unroll<8>() : vb == 4 ? row_unroll<4>() : row_unroll<2>();
   a->lanes = 1;
-  while (a->lanes < 32 && a->lanes < a->chunks) a->lanes *= 2;
+  while (a->lanes < 32 && a->lanes < a->chunks &&
+         (a->lanes * unroll < a->chunks || a->tokens * a->lanes < (int64_t)num_sms() * 512))
+    a->lanes *= 2;
   const int64_t blocks = ceil_div(a->tokens * a->lanes, kRowThreads);
   return (int)imax64(1, imin64(blocks, (int64_t)num_sms() * 16));
 }

@@ -204,7 +204,7 @@ struct TileArgs {
   int64_t x_rows, rows, cols, ldx;
   const int32_t* row_index;
   const int32_t* offsets;  // NULL: `groups` groups of `rows` rows each
-  int32_t groups, vec, col_blocks;
+  int32_t groups, unit, col_blocks;  // unit: bytes that every row can be read in
   uint8_t* q;
   float* scale;
   int64_t ldq, ld_scale;  // scale: [col block][row], or with blocks [group][row block][col block]
@@ -228,6 +228,13 @@ constexpr int tile_ld() {
   return 128 + 16 / (int)sizeof(T);
 }
 
+// Threads of a tile's CTA: fp32 tiles are twice as large, so only three CTAs fit an SM, and get twice
+// the threads to keep as many warps (65536 x 479 fp32: 37 us with 256).
+template <typename T>
+constexpr int tile_threads() {
+  return sizeof(T) == 4 ? 512 : 256;
+}
+
 // B bytes into shared memory without waiting, of which the first `take` come from src and the rest
 // are zeros.
 template <int B>
@@ -236,14 +243,56 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int take)
   if constexpr (B == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(take) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(take) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(d), "l"(src), "r"(take), "n"(B) : "memory");
 }
 
-// Threads of a tile's CTA: fp32 tiles are twice as large, so only three CTAs fit an SM, and get twice
-// the threads to keep as many warps (65536 x 479 fp32: 37 us with 256).
-template <typename T>
-constexpr int tile_threads() {
-  return sizeof(T) == 4 ? 512 : 256;
+// A 128 x 128 tile from the rows source(i) of x (-1: zeros), by asynchronous copies of B bytes: nothing
+// waits in registers, so that all of a CTA's reads are in flight.
+template <typename T, int B, typename Source>
+__device__ __forceinline__ void stage_tile(T* tile, const T* x, int64_t ldx, int col0, int ncols, Source source) {
+  constexpr int per = B / (int)sizeof(T), parts = 128 / per;
+  constexpr int kLanes = parts < 32 ? parts : 32, kTurns = parts / kLanes, kStep = tile_threads<T>() / kLanes;
+  const int c0 = ((int)threadIdx.x % kLanes) * per;
+#pragma unroll(kTurns == 1 ? 4 : 1)
+  for (int i = (int)threadIdx.x / kLanes; i < 128; i += kStep) {
+    const int64_t src = source(i);
+    const T* row = x + (src >= 0 ? src * ldx + col0 : 0);
+    const int have = src >= 0 ? ncols : 0;
+#pragma unroll
+    for (int h = 0; h < kTurns; ++h) {
+      const int c = c0 + h * kLanes * per;
+      int take = c < have ? B : 0;
+      if constexpr (per > 1) take = min(take, max(0, (have - c) * (int)sizeof(T)));
+      copy_async<B>(tile + i * tile_ld<T>() + c, take ? row + c : x, take);
+    }
+  }
+}
+
+// The same where rows start at odd elements, which no asynchronous copy can take: eight rows' elements
+// in registers at once (a row at a time, the reads' latency was the kernel's: 23 x 1407 x 973, both
+// orders, 51 us against 41).
+template <typename T, typename Source>
+__device__ __forceinline__ void stage_elements(T* tile, const T* x, int64_t ldx, int col0, int ncols, Source source) {
+  constexpr int kWarps = tile_threads<T>() / 32, kRows = 8;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int i0 = threadIdx.x >> 5; i0 < 128; i0 += kWarps * kRows) {
+    int64_t src[kRows];
+    T v[kRows][4];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) src[u] = source(i0 + u * kWarps);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int c = h * 32 + lane;
+        v[u][h] = src[u] >= 0 && c < ncols ? __ldg(x + src[u] * ldx + col0 + c) : from_f32<T>(0.f);
+      }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+#pragma unroll
+      for (int h = 0; h < 4; ++h) tile[(i0 + u * kWarps) * tile_ld<T>() + h * 32 + lane] = v[u][h];
+  }
 }
 
 // One 128 x 128 tile.  ROW_BLOCK: the row codes have one scale for the tile (else one a row);
@@ -314,33 +363,18 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
   if (n <= 0) return;
   const int64_t xbase = a.offsets ? 0 : (int64_t)g * a.rows;  // rows of earlier groups
 
-  // The tile into shared memory by asynchronous copies: nothing waits in registers, so that five CTAs
-  // an SM keep their reads in flight.  Rows past n and columns past the end are zeros.
+  // The tile into shared memory; rows past n and columns past the end are zeros.
   const int lane16 = threadIdx.x & 15;
   const int ncols = (int)imin64(128, a.cols - col0);
-  if (a.vec) {
-    constexpr int per = 16 / (int)sizeof(T), parts = 128 / per;  // 16-byte parts of a row
-    const int c = ((int)threadIdx.x % parts) * per;
-    const int take = max(0, min(16, (ncols - c) * (int)sizeof(T)));
-    const T* from = (const T*)a.x + xbase * a.ldx + (take ? col0 + c : 0);
-#pragma unroll 4
-    for (int i = (int)threadIdx.x / parts; i < 128; i += kThreads / parts) {
-      const int64_t src = i < n ? source_row(a.row_index, row0 + i, a.x_rows, a.err) : -1;
-      copy_async<16>(tile + i * kLd + c, src >= 0 ? from + src * a.ldx : (const T*)a.x, src >= 0 ? take : 0);
-    }
-  } else {
-    for (int i = warp; i < 128; i += kThreads / 32) {
-      const int64_t src = i < n ? xbase + source_row(a.row_index, row0 + i, a.x_rows, a.err) : -1;
-      const T* row = (const T*)a.x + (src >= 0 ? src * a.ldx + col0 : 0);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int c = h * 32 + lane;
-        const bool take = src >= 0 && c < ncols;
-        if constexpr (sizeof(T) == 4) copy_async<4>(tile + i * kLd + c, take ? row + c : (const T*)a.x, take ? 4 : 0);
-        else tile[i * kLd + c] = take ? row[c] : from_f32<T>(0.f);
-      }
-    }
-  }
+  auto source = [&](int i) -> int64_t {
+    if (i >= n) return -1;
+    const int64_t r = source_row(a.row_index, row0 + i, a.x_rows, a.err);
+    return r >= 0 ? xbase + r : -1;
+  };
+  if (a.unit == 16) stage_tile<T, 16>(tile, (const T*)a.x, a.ldx, col0, ncols, source);
+  else if (a.unit == 8) stage_tile<T, 8>(tile, (const T*)a.x, a.ldx, col0, ncols, source);
+  else if (a.unit == 4) stage_tile<T, 4>(tile, (const T*)a.x, a.ldx, col0, ncols, source);
+  else if constexpr (sizeof(T) == 2) stage_elements(tile, (const T*)a.x, a.ldx, col0, ncols, source);
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 
@@ -539,7 +573,7 @@ extern "C" int ctr_fp8_quantize_rows_cols(const void* x, ctr_dtype dtype, int64_
   a.row_index = row_index;
   a.offsets = offsets;
   a.groups = groups;
-  a.vec = aligned16(x) && (ldx * eb) % 16 == 0;
+  a.unit = vector_bytes({(uint64_t)(uintptr_t)x, (uint64_t)(ldx * eb)}, eb);
   a.col_blocks = (int32_t)ceil_div(cols, 128);
   a.q = q;
   a.scale = scale;
@@ -575,7 +609,7 @@ extern "C" int ctr_fp8_quantize_blocks(const void* w, ctr_dtype dtype, int32_t g
   a.cols = k;
   a.ldx = k;
   a.groups = groups;
-  a.vec = aligned16(w) && (k * eb) % 16 == 0;
+  a.unit = vector_bytes({(uint64_t)(uintptr_t)w, (uint64_t)(k * eb)}, eb);
   a.col_blocks = (int32_t)ceil_div(k, 128);
   a.q = q;
   a.scale = scale;
