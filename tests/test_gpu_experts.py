@@ -214,6 +214,13 @@ def test_rows_into_expert_order_and_back(T, d, k, dtype, pad):
     assert np.all(_np(buf)[:, d:] == 7.0), "a write left its row"
 
 
+# enough tokens that a row gets few lanes, down to one
+@pytest.mark.parametrize("T,d,k,dtype,pad", [(90001, 1, 1, "bf16", 0), (90001, 7, 2, "f32", 1), (90001, 24, 2, "bf16", 0),
+                                             (70003, 64, 2, "f32", 0), (30011, 130, 2, "bf16", 1)])
+def test_rows_of_many_tokens(T, d, k, dtype, pad):
+    test_rows_into_expert_order_and_back(T, d, k, dtype, pad)
+
+
 def test_rows_gradients_are_the_differences():
     # L = <dy, combine(rows, weight)> is linear in rows and in weight: a difference of any step is the
     # derivative, up to the rounding of the forward pass (k u |.|) over the step
