@@ -5,18 +5,20 @@
 // include/ctr.h.
 //
 // Routing.  A token's scores are spread over a group of lanes (at least k), EPL
-// consecutive scores to a lane; the k choices are k rounds of "best score not yet
-// taken" (in-lane maximum, then xor-shuffles; ties go to the lower index), after
-// which lane j has choice j, its exponential and its stores.  bf16 scores carry
-// their index in the low half of an ordered 32-bit key, so that a round is integer
-// maxima alone.  Bound by instruction issue.  The stable order by expert is a counting sort without atomics on
+// consecutive scores to a lane.  fp32: the k choices are k rounds of "best score
+// not yet taken" (in-lane maximum, then xor-shuffles; ties go to the lower index).
+// bf16 scores carry their index in the low half of an ordered 32-bit key, so that
+// integer maxima and minima are all it takes; three or four choices come from
+// sorting networks (131072 x 64, k 4, with the order: 36 us before, 26 with both).
+// Then lane j has choice j, its exponential and its stores.  Bound by instruction
+// issue.  The stable order by expert is a counting sort without atomics on
 // counts: a block's tile of up to 256 tokens is a bit matrix [expert][token]
 // in shared memory, so a choice's rank within the tile is a population count
 // of the bits before it, and the tile's count of an expert the count of all.
 // Three launches: choices + tile counts; exclusive sums of the counts over the
 // tiles (one warp column per expert); ranks and the two maps.  Up to kTileTokens
 // x 8 tokens run as one launch, a block or a cluster of up to eight blocks that
-// read each other's counts (2048 x 26: 23 -> 14 us, of which most is the call).
+// read each other's counts (2048 x 26, k 4: 8 us, most of it the call).
 //
 // Rows.  A token's group of lanes reads its row once and writes its k rows (or
 // reads k rows and writes one): every byte crosses HBM once, and rows of 1 KB
@@ -93,67 +95,187 @@ __device__ __forceinline__ int expert_starts(const int* totals, int experts, int
   return all;
 }
 
-// The k best of a group's scores, one round a choice: choice j's score and expert (-1: none left).
+// What a lane learns of its group's token: choice `sub`'s score and expert (-1: none), the best score,
+// and, where the weights are over the whole row, the sum of exp(score - best).
+struct Choice {
+  float value = -INFINITY, best = 0.f, total = 0.f;
+  int expert = -1;
+};
+
+// fp32: a round a choice, the value first, then the lowest index that has it.
 template <typename T, int EPL, int KMAX>
-struct Picker {
-  // fp32: the value, then the lowest index that has it
-  static __device__ __forceinline__ void pick(float (&v)[EPL], int base, int lanes, int k, float (&val)[KMAX],
-                                              int (&idx)[KMAX]) {
+struct Chooser {
+  static __device__ __forceinline__ Choice run(const RouteArgs& a, const T* row, bool mine, int sub) {
+    const int base = sub * EPL;
+    float v[EPL];
+    if (mine) {
+      load_scores<T, EPL>(row, base, a.experts, a.vec != 0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+    }
+    bool odd = false;  // NaN or +inf: the token is routed nowhere
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) odd |= !(v[i] < INFINITY);
+    const int lane = threadIdx.x & 31;
+    const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
+    const bool bad = (__ballot_sync(kFull, odd) & group) != 0;
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+      if (sub == 0) set_error(a.err, CTR_ERR_BAD_VALUE);
+    }
+    Choice c;
+    if (!a.renormalize) {
+      float m = v[0];
+#pragma unroll
+      for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      if (!(m > -INFINITY)) m = 0.f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) c.total += expf(v[i] - m);  // exp(-inf) = 0: masked scores add nothing
+      for (int o = 1; o < a.lanes; o <<= 1) c.total += __shfl_xor_sync(kFull, c.total, o);
+    }
 #pragma unroll
     for (int j = 0; j < KMAX; ++j) {
-      val[j] = -INFINITY;
-      idx[j] = -1;
-      if (j < k) {
+      if (j < a.k) {
         float best = v[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) best = fmaxf(best, v[i]);
-        for (int o = 1; o < lanes; o <<= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
+        for (int o = 1; o < a.lanes; o <<= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, o));
         int at = 0x7fffffff;
 #pragma unroll
         for (int i = EPL - 1; i >= 0; --i) at = v[i] == best ? base + i : at;
-        for (int o = 1; o < lanes; o <<= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
+        for (int o = 1; o < a.lanes; o <<= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
         if (best > -INFINITY) {
-          val[j] = best;
-          idx[j] = at;
+          if (j == 0) c.best = best;
+          if (j == sub) {
+            c.value = best;
+            c.expert = at;
+          }
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) v[i] = base + i == at ? -INFINITY : v[i];
       }
     }
+    return c;
   }
 };
 
+// bf16: a score is a 32-bit key, its 16 bits made to order as an unsigned number (negative ones
+// complemented, else the sign set) above the complement of the index, so that integer maxima find value
+// and lowest index together.  -inf is 0x007f, below every number; +inf and, as adding zero makes them all
+// positive, NaNs are 0xff80 and above and come out as the best.
 template <int EPL, int KMAX>
-struct Picker<__nv_bfloat16, EPL, KMAX> {
-  // bf16 values fill the high half of an fp32 word: ordered as an unsigned number, with the complement
-  // of the index below, so one maximum finds value and lowest index.  Masked scores are key 0.
-  static __device__ __forceinline__ void pick(float (&v)[EPL], int base, int lanes, int k, float (&val)[KMAX],
-                                              int (&idx)[KMAX]) {
-    uint32_t key[EPL];
+struct Chooser<__nv_bfloat16, EPL, KMAX> {
+  static constexpr uint32_t kLeast = 0x00800000u, kBad = 0xff800000u;  // keys of numbers lie between
+
+  static __device__ __forceinline__ float value(uint32_t key) {
+    return __uint_as_float((key & 0xffff0000u) ^ (key & 0x80000000u ? 0x80000000u : 0xffff0000u));
+  }
+  static __device__ __forceinline__ void order(uint32_t& x, uint32_t& y) {
+    const uint32_t hi = max(x, y);
+    y = min(x, y);
+    x = hi;
+  }
+  // a and b in falling order: a becomes the four largest of both, in falling order
+  static __device__ __forceinline__ void merge4(uint32_t* a, const uint32_t* b) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const uint32_t b = __float_as_uint(v[i] + 0.f);  // -0 becomes +0
-      const uint32_t ordered = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
-      key[i] = v[i] > -INFINITY ? (ordered & 0xffff0000u) | (uint32_t)(0xffff - (base + i)) : 0u;
-    }
+    for (int i = 0; i < 4; ++i) a[i] = max(a[i], b[3 - i]);
+    order(a[0], a[2]);
+    order(a[1], a[3]);
+    order(a[0], a[1]);
+    order(a[2], a[3]);
+  }
+  // The group's k largest keys.  Three and four by sorting networks: fours within the lane, then the best
+  // four of two lists until one is left.  Else a round a choice.
+  static __device__ __forceinline__ void largest(uint32_t (&key)[EPL], int lanes, int k, uint32_t (&top)[KMAX]) {
+    if (KMAX == 4 && k > 2) {
 #pragma unroll
-    for (int j = 0; j < KMAX; ++j) {
-      val[j] = -INFINITY;
-      idx[j] = -1;
-      if (j < k) {
-        uint32_t best = key[0];
+      for (int i = 0; i < EPL; i += 4) {
+        order(key[i], key[i + 1]);
+        order(key[i + 2], key[i + 3]);
+        order(key[i], key[i + 2]);
+        order(key[i + 1], key[i + 3]);
+        order(key[i + 1], key[i + 2]);
+      }
 #pragma unroll
-        for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
-        for (int o = 1; o < lanes; o <<= 1) best = max(best, __shfl_xor_sync(kFull, best, o));
-        if (best != 0) {
-          const uint32_t hi = best & 0xffff0000u;
-          val[j] = __uint_as_float((hi & 0x80000000u) ? hi & 0x7fffffffu : ~hi & 0xffff0000u);
-          idx[j] = 0xffff - (int)(best & 0xffffu);
+      for (int w = 4; w < EPL; w *= 2)
+#pragma unroll
+        for (int i = 0; i < EPL; i += 2 * w) merge4(key + i, key + i + w);
+      for (int o = 1; o < lanes; o <<= 1) {
+        uint32_t other[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) other[i] = __shfl_xor_sync(kFull, key[i], o);
+        merge4(key, other);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top[j] = key[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < KMAX; ++j) {
+        top[j] = 0;
+        if (j < k) {
+          uint32_t best = key[0];
+#pragma unroll
+          for (int i = 1; i < EPL; ++i) best = max(best, key[i]);
+          for (int o = 1; o < lanes; o <<= 1) best = max(best, __shfl_xor_sync(kFull, best, o));
+          top[j] = best;
+          if (j + 1 < k) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) key[i] = key[i] == best ? 0u : key[i];
+          }
         }
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = key[i] == best ? 0u : key[i];
       }
     }
+  }
+
+  static __device__ __forceinline__ Choice run(const RouteArgs& a, const __nv_bfloat16* row, bool mine, int sub) {
+    const int base = sub * EPL;
+    uint32_t w[EPL / 2];  // pairs of scores
+    if (mine && a.vec && base + EPL <= a.experts) {
+#pragma unroll
+      for (int i = 0; i < EPL / 8; ++i) *(uint4*)(w + 4 * i) = *(const uint4*)(row + base + 8 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL / 2; ++i) {
+        const int e = base + 2 * i;
+        const uint32_t lo = mine && e < a.experts ? __bfloat16_as_ushort(row[e]) : 0xff80u;
+        const uint32_t hi = mine && e + 1 < a.experts ? __bfloat16_as_ushort(row[e + 1]) : 0xff80u;
+        w[i] = lo | (hi << 16);
+      }
+    }
+    uint32_t key[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL / 2; ++i) {
+      uint32_t x, sign;
+      asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(w[i]), "r"(0u));  // -0 becomes +0
+      asm("prmt.b32 %0, %1, 0, 0xbb99;" : "=r"(sign) : "r"(x));         // all ones for a negative half
+      x ^= sign | 0x80008000u;
+      const uint32_t index = 0xfffeffffu - 0x00010001u * (uint32_t)(base + 2 * i);  // complements, two
+      key[2 * i] = __byte_perm(x, index, 0x1054);
+      key[2 * i + 1] = __byte_perm(x, index, 0x3276);
+    }
+    uint32_t top[KMAX];
+    largest(key, a.lanes, a.k, top);
+    const bool bad = top[0] >= kBad;
+    if (bad && sub == 0) set_error(a.err, CTR_ERR_BAD_VALUE);
+    uint32_t own = 0;
+#pragma unroll
+    for (int j = 0; j < KMAX; ++j) own = j == sub ? top[j] : own;
+    Choice c;
+    if (!bad && top[0] >= kLeast) c.best = value(top[0]);
+    if (!bad && own >= kLeast && sub < a.k) {
+      c.value = value(own);
+      c.expert = 0xffff - (int)(own & 0xffffu);
+    }
+    if (!a.renormalize) {
+#pragma unroll
+      for (int i = 0; i < EPL / 2; ++i)  // exp(-inf) = 0: masked scores add nothing
+        c.total += expf(__uint_as_float(w[i] << 16) - c.best) + expf(__uint_as_float(w[i] & 0xffff0000u) - c.best);
+      for (int o = 1; o < a.lanes; o <<= 1) c.total += __shfl_xor_sync(kFull, c.total, o);
+    }
+    return c;
   }
 };
 
@@ -197,57 +319,19 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
   for (int p0 = 0; p0 < n; p0 += per_pass) {  // the same trips in every lane: the shuffles need all of them
     const int tl = p0 + (int)threadIdx.x / a.lanes;
     const bool mine = tl < n;
-    const int base = sub * EPL;
-    float v[EPL];
-    if (mine) {
-      load_scores<T, EPL>((const T*)a.scores + (t0 + tl) * a.ld, base, a.experts, a.vec != 0, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
-    }
-    bool odd = false;  // NaN or +inf: the token is routed nowhere
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) odd |= !(v[i] < INFINITY);
-    const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
-    const bool bad = (__ballot_sync(kFull, odd) & group) != 0;
-    if (bad) {
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
-      if (sub == 0) set_error(a.err, CTR_ERR_BAD_VALUE);
-    }
-    float total = 0.f;
-    if (!a.renormalize) {
-      float m = v[0];
-#pragma unroll
-      for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
-      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      if (!(m > -INFINITY)) m = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) total += expf(v[i] - m);  // exp(-inf) = 0: masked scores add nothing
-      for (int o = 1; o < a.lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
-    }
-    float val[KMAX];
-    int idx[KMAX];
-    Picker<T, EPL, KMAX>::pick(v, base, a.lanes, a.k, val, idx);
     // lane j of the group has choice j
-    float mine_v = -INFINITY;
-    int mine_e = -1;
-#pragma unroll
-    for (int j = 0; j < KMAX; ++j)
-      if (j == sub) {
-        mine_v = val[j];
-        mine_e = idx[j];
-      }
-    const float z = mine_e >= 0 ? expf(mine_v - val[0]) : 0.f;
+    const Choice c = Chooser<T, EPL, KMAX>::run(a, (const T*)a.scores + (t0 + tl) * a.ld, mine, sub);
+    const float z = c.expert >= 0 ? expf(c.value - c.best) : 0.f;
+    float total = c.total;
     if (a.renormalize) {
       total = z;
       for (int o = 1; o < a.lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
     }
     if (mine && sub < a.k) {
       const int64_t at = (t0 + tl) * a.k + sub;
-      a.expert[at] = mine_e;
-      a.weight[at] = mine_e >= 0 ? z / total : 0.f;
-      if (mine_e >= 0) atomicOr(&bits[mine_e * words + (tl >> 5)], 1u << (tl & 31));
+      a.expert[at] = c.expert;
+      a.weight[at] = c.expert >= 0 ? z / total : 0.f;
+      if (c.expert >= 0) atomicOr(&bits[c.expert * words + (tl >> 5)], 1u << (tl & 31));
     }
   }
   __syncthreads();
@@ -396,9 +480,52 @@ __device__ __forceinline__ void store_scores(T* out, int base, int experts, bool
   }
 }
 
-// RENORM: the softmax is over the choices, so lane j of the group reads choice j's score alone and
-// the other scores' gradient is zero.  Else the whole row takes part.
-template <typename T, int EPL, bool RENORM>
+// Softmax over the choices: lane j of a token's lanes (as few as hold its choices) reads choice j's score
+// alone.  The other scores' gradient is zero: the lanes write the row's zeros first, then each its choice
+// over them (selecting the values' places in registers took twice the instructions: 131072 x 64 bf16, k 4,
+// 18.4 us against 14.3; 256, k 8, 61 against 29).
+template <typename T>
+__global__ void __launch_bounds__(kRouteThreads) route_bwd_choices_kernel(const RouteArgs a, const float* dweight,
+                                                                          T* dscores, int64_t ldd, int vec_out) {
+  constexpr int per = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
+  const int64_t groups = (int64_t)gridDim.x * (kRouteThreads / a.lanes);
+  int64_t t = ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x) / a.lanes;
+  const int64_t trips = ceil_div(a.tokens, groups);  // the same in every lane
+  grid_wait();
+  for (int64_t trip = 0; trip < trips; ++trip, t += groups) {
+    const bool mine = t < a.tokens;
+    T* out = dscores + t * ldd;
+    const int e = mine && sub < a.k ? a.expert[t * a.k + sub] : -1;
+    const bool live = e >= 0 && e < a.experts;
+    const float l = live ? to_f32<T>(((const T*)a.scores)[t * a.ld + e]) : -INFINITY;
+    const float g = live ? dweight[t * a.k + sub] : 0.f;
+    if (mine) {
+      int done = 0;
+      if (vec_out) {
+        done = a.experts & ~(per - 1);
+        for (int i = sub * per; i < done; i += a.lanes * per) *(uint4*)(out + i) = make_uint4(0, 0, 0, 0);
+      }
+      for (int i = done + sub; i < a.experts; i += a.lanes) out[i] = from_f32<T>(0.f);
+    }
+    float m = l;
+    for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const float z = live ? expf(l - m) : 0.f;
+    float total = z, dot = z * g;
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      total += __shfl_xor_sync(kFull, total, o);
+      dot += __shfl_xor_sync(kFull, dot, o);
+    }
+    __syncwarp();  // the row's zeros come before its choices
+    if (live) {    // then total >= its own exponential > 0
+      const float inv = 1.f / total;
+      out[e] = from_f32<T>(z * inv * (g - dot * inv));
+    }
+  }
+}
+
+// Softmax over the whole row: d score_i = p_i (g_i - sum p g), g of the scores not chosen 0.
+template <typename T, int EPL>
 __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArgs a, const float* dweight, T* dscores,
                                                                   int64_t ldd, int vec_out) {
   const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
@@ -418,72 +545,55 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
     // a token with no choice (all masked, or flagged by the routing) has no gradient
     const bool routed = (__ballot_sync(kFull, live) & group) != 0;
     float out[EPL];
-    if constexpr (RENORM) {
-      const float l = live ? to_f32<T>(row[e]) : -INFINITY;
-      float m = l;
-      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      const float z = live ? expf(l - m) : 0.f;
-      float total = z, dot = z * g;
-      for (int o = 1; o < a.lanes; o <<= 1) {
-        total += __shfl_xor_sync(kFull, total, o);
-        dot += __shfl_xor_sync(kFull, dot, o);
-      }
-      const float inv = routed ? 1.f / total : 0.f;
-      const float d = z * inv * (g - dot * inv);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) out[i] = 0.f;
-      for (int j = 0; j < a.k; ++j) {
-        const int at = __shfl_sync(kFull, e, j, a.lanes) - base;
-        const float dj = __shfl_sync(kFull, d, j, a.lanes);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) out[i] = at == i ? dj : out[i];
-      }
+    float v[EPL], gi[EPL];
+    if (mine) {
+      load_scores<T, EPL>(row, base, a.experts, a.vec != 0, v);
     } else {
-      float v[EPL], gi[EPL];
-      if (mine) {
-        load_scores<T, EPL>(row, base, a.experts, a.vec != 0, v);
-      } else {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) gi[i] = 0.f;
-      for (int j = 0; j < a.k; ++j) {
-        const int at = __shfl_sync(kFull, live ? e : -1, j, a.lanes) - base;
-        const float gj = __shfl_sync(kFull, g, j, a.lanes);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) gi[i] = at == i ? gj : gi[i];
-      }
-      float m = v[0];
-#pragma unroll
-      for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
-      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      float total = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        v[i] = routed ? expf(v[i] - m) : 0.f;
-        total += v[i];
-        dot += v[i] * gi[i];
-      }
-      for (int o = 1; o < a.lanes; o <<= 1) {
-        total += __shfl_xor_sync(kFull, total, o);
-        dot += __shfl_xor_sync(kFull, dot, o);
-      }
-      const float inv = routed ? 1.f / total : 0.f;
-      dot *= inv;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) out[i] = v[i] * inv * (gi[i] - dot);
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
     }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) gi[i] = 0.f;
+    for (int j = 0; j < a.k; ++j) {
+      const int at = __shfl_sync(kFull, live ? e : -1, j, a.lanes) - base;
+      const float gj = __shfl_sync(kFull, g, j, a.lanes);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) gi[i] = at == i ? gj : gi[i];
+    }
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+    for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    float total = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      v[i] = routed ? expf(v[i] - m) : 0.f;
+      total += v[i];
+      dot += v[i] * gi[i];
+    }
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      total += __shfl_xor_sync(kFull, total, o);
+      dot += __shfl_xor_sync(kFull, dot, o);
+    }
+    const float inv = routed ? 1.f / total : 0.f;
+    dot *= inv;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) out[i] = v[i] * inv * (gi[i] - dot);
     if (mine) store_scores<T, EPL>(dscores + t * ldd + base, base, a.experts, vec_out != 0, out);
   }
 }
 
-// Lanes per token: 8 scores a lane (16 above 256 experts) and a lane for each choice, a power of two.
-int route_lanes(int experts, int k) {
+// Lanes per token: `per` scores a lane and a lane for each choice, a power of two.
+int route_lanes(int experts, int k, int per) {
   int lanes = 1;
-  while (lanes < 32 && (lanes * 8 < experts || lanes < k)) lanes *= 2;
+  while (lanes < 32 && (lanes * per < experts || lanes < k)) lanes *= 2;
   return lanes;
 }
+
+// Scores of a lane: work within a lane is cheaper than between lanes, down to four lanes a token (131072
+// x 64, k 4, 16 scores against 8: bf16 25.6 us against 29.7, fp32 33.8 against 37.9; x 128, k 2, fp32 40
+// against 48).
+int lane_scores(int experts) { return experts > 32 ? 16 : 8; }
 
 constexpr int kClusterTiles = 8;  // blocks of a portable cluster
 
@@ -518,11 +628,20 @@ void launch_choose(const RouteArgs& a, size_t smem, bool cluster, cudaStream_t s
   launch_after(k, dim3((unsigned)a.tiles), kRouteThreads, smem, s, cluster ? (unsigned)a.tiles : 1u, a);
 }
 
+// Lanes of a token whose softmax is over its choices: one for each, and enough that the row's zeros leave
+// in pieces of 64 bytes a lane (131072 rows of 64 bf16, k 1: 2 lanes 12.3 us, one 16.4, 8 16.4; 128 fp32, k
+// 2: 8 lanes 22.5, 2 24.6), of 32 where rows are not 16-byte aligned (63 fp32, k 2: 8 lanes 18.4, 4 22.5, 2
+// 53).  More than 8 gained nothing (512 bf16, k 4: 8 lanes 36.9, 16 38.9).
+int choice_lanes(int row_bytes, int k, int vec_out) {
+  return route_lanes((int)imin64(row_bytes, vec_out ? 512 : 256), k, vec_out ? 64 : 32);
+}
+
 template <typename T>
-void launch_bwd(const RouteArgs& a, const float* dweight, T* dscores, int64_t ldd, int vec_out, int grid,
-                cudaStream_t s) {
-  auto k = a.experts <= 256 ? (a.renormalize ? route_bwd_kernel<T, 8, true> : route_bwd_kernel<T, 8, false>)
-                            : (a.renormalize ? route_bwd_kernel<T, 16, true> : route_bwd_kernel<T, 16, false>);
+void launch_bwd(RouteArgs& a, const float* dweight, T* dscores, int64_t ldd, int vec_out, cudaStream_t s) {
+  const int per = lane_scores(a.experts);
+  a.lanes = a.renormalize ? choice_lanes(a.experts * (int)sizeof(T), a.k, vec_out) : route_lanes(a.experts, a.k, per);
+  auto k = a.renormalize ? route_bwd_choices_kernel<T> : per == 16 ? route_bwd_kernel<T, 16> : route_bwd_kernel<T, 8>;
+  const int grid = (int)imin64(ceil_div(a.tokens * a.lanes, kRouteThreads), (int64_t)num_sms() * 8);
   launch_after(k, dim3(grid), kRouteThreads, 0, s, 1, a, dweight, dscores, ldd, vec_out);
 }
 
@@ -768,7 +887,8 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   a.ld = ld_scores;
   a.experts = experts;
   a.k = k;
-  a.lanes = route_lanes(experts, k);
+  const int per = lane_scores(experts);
+  a.lanes = route_lanes(experts, k, per);
   a.tile = route_tile(tokens, experts);
   a.tiles = (int32_t)ceil_div(tokens, a.tile);
   a.renormalize = renormalize != 0;
@@ -785,10 +905,10 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   const size_t smem = route_smem(experts, a.tile);
   const bool cluster = a.tiles > 1 && a.tiles <= kClusterTiles;
   if (dtype == CTR_F32) {
-    if (experts <= 256) launch_choose<float, 8>(a, smem, cluster, s);
+    if (per == 8) launch_choose<float, 8>(a, smem, cluster, s);
     else launch_choose<float, 16>(a, smem, cluster, s);
   } else {
-    if (experts <= 256) launch_choose<__nv_bfloat16, 8>(a, smem, cluster, s);
+    if (per == 8) launch_choose<__nv_bfloat16, 8>(a, smem, cluster, s);
     else launch_choose<__nv_bfloat16, 16>(a, smem, cluster, s);
   }
   if (a.tiles > 1 && !cluster) {
@@ -814,7 +934,6 @@ extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ct
   a.ld = ld_scores;
   a.experts = experts;
   a.k = k;
-  a.lanes = route_lanes(experts, k);
   a.renormalize = renormalize != 0;
   const int eb = dtype_bytes(dtype);
   a.vec = ((uintptr_t)scores % 16) == 0 && (ld_scores * eb) % 16 == 0;
@@ -822,9 +941,8 @@ extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ct
   a.expert = const_cast<int32_t*>(expert);
   a.err = (int*)ws;
   cudaStream_t s = (cudaStream_t)stream;
-  const int grid = (int)imin64(ceil_div(tokens * a.lanes, kRouteThreads), (int64_t)num_sms() * 8);
-  if (dtype == CTR_F32) launch_bwd(a, dweight, (float*)dscores, ld_dscores, vec_out, grid, s);
-  else launch_bwd(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out, grid, s);
+  if (dtype == CTR_F32) launch_bwd(a, dweight, (float*)dscores, ld_dscores, vec_out, s);
+  else launch_bwd(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out, s);
   return launch_status();
 }
 

@@ -109,6 +109,46 @@ def test_route_nan_and_infinity_are_flagged_and_routed_nowhere():
     check_route(s, 3, True, "f32")
 
 
+@pytest.mark.parametrize("E", [7, 32, 40, 300])
+def test_route_every_bf16_number(E):
+    # every finite bf16 number, subnormals and both zeros among them, in shuffled rows; a score's distance
+    # from the best is rounded once, up to 104 before its exponential leaves fp32
+    bits = np.arange(65536, dtype=np.uint32)
+    finite = bits[(bits & 0x7f80) != 0x7f80]
+    rng = np.random.default_rng(2)
+    pick = np.concatenate([rng.permutation(finite), finite[:-len(finite) % E]]).reshape(-1, E)
+    s = (pick << 16).astype(np.uint32).view(np.float32).astype(np.float64)
+    s[::3] = rng.integers(-2, 3, size=s[::3].shape) * 2.0 ** -133  # ties of the smallest numbers
+    for k in (1, 2, 3, 4, 5):
+        for renorm in (True, False):
+            st, got = gpu_route(s, k, renorm, "bf16")
+            assert st == 0
+            expert, weight, slot, token, offsets, _ = R.route(s, k, renorm)
+            for n, ref in (("expert", expert), ("slot", slot), ("token", token), ("offsets", offsets)):
+                np.testing.assert_array_equal(got[n], ref)
+            assert np.all(np.abs(got["weight"] - weight) <= (E + 8 + 104) * R.U * weight + 1e-38)
+
+
+@pytest.mark.parametrize("E", [8, 48])
+def test_route_every_bf16_nan_and_infinity_is_flagged_and_routed_nowhere(E):
+    bits = np.arange(65536, dtype=np.uint32)
+    odd = bits[((bits & 0x7f80) == 0x7f80) & (bits != 0xff80)]   # -inf is a mask
+    raw = torch.zeros((2 * len(odd), E), dtype=torch.int16)
+    at = np.arange(len(odd))
+    raw[2 * at, at % E] = torch.from_numpy(odd.astype(np.uint16).view(np.int16))
+    x = raw.view(torch.bfloat16).cuda()
+    for k in (1, 3):
+        i32 = dict(dtype=torch.int32, device="cuda")
+        T = x.shape[0]
+        out = [torch.full((T, k), -9, **i32), torch.full((T, k), -9.0, device="cuda"), torch.full((T, k), -9, **i32),
+               torch.full((T * k,), -9, **i32), torch.full((E + 1,), -9, **i32)]
+        ws = ctr.workspace(ctr.ctr_expert_route_workspace_size(T, E, k))
+        ctr.ctr_expert_route(x, k, True, *out, ws)
+        assert ctr.ctr_check_status(ws) == ctr.ERR_BAD_VALUE
+        assert torch.all(out[0][::2] == -1) and torch.all(out[2][::2] == -1) and torch.all(out[1][::2] == 0)
+        assert torch.all(out[0][1::2] == torch.arange(k, device="cuda"))
+
+
 def test_route_all_tokens_to_one_expert_and_repeats_bit_for_bit():
     s = _scores(30000, 40, "f32", 0, 5)
     s[:, 11] = 50.0
