@@ -268,12 +268,12 @@ __device__ __forceinline__ void stage_tile(T* tile, const T* x, int64_t ldx, int
   }
 }
 
-// The same where rows start at odd elements, which no asynchronous copy can take: eight rows' elements
+// The same where rows start at odd elements, which no asynchronous copy can take: four rows' elements
 // in registers at once (a row at a time, the reads' latency was the kernel's: 23 x 1407 x 973, both
 // orders, 51 us against 41).
 template <typename T, typename Source>
 __device__ __forceinline__ void stage_elements(T* tile, const T* x, int64_t ldx, int col0, int ncols, Source source) {
-  constexpr int kWarps = tile_threads<T>() / 32, kRows = 8;
+  constexpr int kWarps = tile_threads<T>() / 32, kRows = 4;
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
   for (int i0 = threadIdx.x >> 5; i0 < 128; i0 += kWarps * kRows) {
@@ -378,12 +378,15 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
 
-  // Maxima.  Rows: 16 lanes a row, 8 values each; columns: two and 32 of their rows to a thread.
+  // Maxima.  Rows: 16 lanes a row, 8 values each; columns: two and 32 of their rows to a thread.  The
+  // loops are unrolled in part: in full, a small call with cold caches spent its time on instruction
+  // fetches (the training step of 6 rows of 376 x 560 bf16 42.6 us against 38.6), and large ones gained
+  // nothing.
   const int64_t qcol = col0 + lane16 * 8;
   const int c = (threadIdx.x & 63) * 2, part = threadIdx.x >> 6;
   const T* mine = tile + part * kPartRows * kLd + c;
   float tile_max = 0.f;
-#pragma unroll
+#pragma unroll 2
   for (int p = 0; p < 128 * 16 / kThreads; ++p) {
     const int i = p * (kThreads / 16) + (threadIdx.x >> 4);
     MaxPair<T> mp;
@@ -400,7 +403,7 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
   }
   if constexpr (!COL_BLOCK) {
     MaxPair<T> mp;
-#pragma unroll
+#pragma unroll 8
     for (int i = 0; i < kPartRows; ++i) mp.add(mine + i * kLd);
     *(float2*)&col_max[part][c] = mp.get();
   }
@@ -447,7 +450,7 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
   }
   // Row codes.
   uint8_t* q = a.q + ((ROW_BLOCK ? xbase : 0) + row0 + (threadIdx.x >> 4)) * a.ldq + qcol;
-#pragma unroll
+#pragma unroll 2
   for (int p = 0; p < 128 * 16 / kThreads; ++p) {
     const int i = p * (kThreads / 16) + (threadIdx.x >> 4);
     float v[8];
