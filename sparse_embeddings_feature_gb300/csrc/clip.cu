@@ -8,7 +8,7 @@
 // fp64; joins are fp64 in a fixed order, so the result does not change from run
 // to run.  A part whose sum of squares comes near either end of fp32's range is
 // read again and squared in fp64 by its warp (fp64 in the common path, even
-// predicated off, tripled the pass: 724 us against 252 for 5e8 elements).  Every
+// predicated off, tripled the pass: 724 us against 248 for 5e8 elements).  Every
 // block of the second pass adds the first one's sums up for itself, in the same
 // order: no counter, and no launch between the two.  Two passes over the data,
 // bound by HBM: the second walks the chunks in reverse, so what the first read

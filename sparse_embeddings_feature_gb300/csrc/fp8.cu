@@ -16,7 +16,9 @@
 // as 128 consecutive bytes: a second pass over x would cost as much as the
 // first.  For the column order a thread holds 32 rows of two neighbouring columns
 // in registers (one shared-memory read of both columns' values per row) for the
-// maximum and for the codes, which leave in 16-byte stores.
+// maximum and for the codes, which leave in 16-byte stores.  Bound by instruction
+// issue (0.73 of the slots; 65536 x 1024 bf16, both orders, 59 us: 268 MB at 4.5
+// TB/s; rows alone 45 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -229,7 +231,7 @@ constexpr int tile_ld() {
 }
 
 // Threads of a tile's CTA: fp32 tiles are twice as large, so only three CTAs fit an SM, and get twice
-// the threads to keep as many warps (65536 x 479 fp32: 37 us with 256).
+// the threads to keep as many warps (65536 x 479 fp32, both orders: 59 us, with 256 threads 64).
 template <typename T>
 constexpr int tile_threads() {
   return sizeof(T) == 4 ? 512 : 256;

@@ -537,17 +537,13 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
       for (int j = 0; j < nkb; ++j) {
         const int u = j % kChunk;
         if (u == 0 && j > 0) ok = park(cfull0 + 8 * cb, cph);
-        // read before the wait (in the pair's weight gradient that one register more spills: 161 us
-        // against 145 for 32 experts of 2048 x 1024)
-        float f = 0.f;
-        if constexpr (!WGRAD) f = row_scale[(cb * kChunk + u) * kBM] * col_scale[cb * (2 * kChunk) + u];
+        const float f = row_scale[(cb * kChunk + u) * kBM] * col_scale[cb * (2 * kChunk) + u];
         ok = ok && park(tfull0 + 8 * b, ph);
         if (!ok) {
           if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
           break;
         }
         fence_after();
-        if constexpr (WGRAD) f = row_scale[(cb * kChunk + u) * kBM] * col_scale[cb * (2 * kChunk) + u];
         uint64_t f2;
         asm("mov.b64 %0, {%1, %1};" : "=l"(f2) : "r"(__float_as_uint(f)));
 #pragma unroll
