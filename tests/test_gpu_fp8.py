@@ -330,7 +330,9 @@ def test_gradients_are_the_formulas(counts, n, k, dtype, out):
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("counts,spare,n,k", [([5000], 0, 64, 70), ([16384], 0, 200, 479), ([2049], 300, 300, 260),
                                               ([9000, 0, 3, 7000], 0, 300, 257), ([1, 6000], 100, 130, 128),
-                                              ([3000, 0, 2500, 40, 4000, 0, 900, 700], 0, 129, 300)])
+                                              ([3000, 0, 2500, 40, 4000, 0, 900, 700], 0, 129, 300),
+                                              ([5000, 0, 40, 300, 2500] + [200] * 8, 50, 300, 260),
+                                              ([0] * 39 + [4000], 0, 260, 130)])
 def test_weight_gradient_of_long_sums(counts, spare, n, k, out):
     rng = np.random.default_rng(6)
     off, rows, G = _offsets(counts), sum(counts) + spare, len(counts)
