@@ -2,6 +2,8 @@
 
 Each .cu file under csrc/ is compiled by nvcc in parallel, then linked with the
 static CUDA runtime into sparse_embeddings_feature_gb300/_build/libctr.so.
+csrc/calls.cpp, which reads the arguments of small calls from tensors, is compiled
+against the installed PyTorch into _build/ctr_calls.so.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libctr.so")
+CALLS = os.path.join(OUT_DIR, "ctr_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -35,8 +38,23 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _calls_command(src: str, out: str):
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    dirs = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+            *[a for d in dirs for a in ("-isystem", d)], src, "-o", out, "-L" + os.path.join(home, "lib"), "-L" + OUT_DIR,
+            "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-lctr", "-Wl,-rpath,$ORIGIN"]
+
+
 def _fingerprint(extra=()) -> str:
-    h = hashlib.sha256()
+    import torch
+    h = hashlib.sha256(torch.__version__.encode())
     for p in sorted(glob.glob(os.path.join(CSRC, "*")) + [os.path.join(INCLUDE, "ctr.h"), __file__]):
         with open(p, "rb") as f:
             h.update(p.encode())
@@ -50,7 +68,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     stamp = os.path.join(OUT_DIR, "fingerprint")
     extra_flags = list(extra_flags or []) + os.environ.get("CTR_NVCC_EXTRA", "").split()
     fp = _fingerprint(extra_flags)
-    if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == fp:
+    if not force and os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(stamp) and open(stamp).read() == fp:
         return LIB
     cc = nvcc()
     flags = ARCH + NVCC_FLAGS + extra_flags
@@ -74,6 +92,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    r = subprocess.run(_calls_command(os.path.join(CSRC, "calls.cpp"), tmp), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"calls.cpp failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
     with open(stamp, "w") as f:
         f.write(fp)
     return LIB

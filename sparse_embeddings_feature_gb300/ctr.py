@@ -9,6 +9,8 @@ cannot be built or loaded the first call raises.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.machinery
+import importlib.util
 import os
 import threading
 from typing import Optional, Sequence
@@ -29,6 +31,7 @@ MAX_EXPERTS, MAX_CHOICES = 512, 16
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 _p = C.c_void_p
 _i32, _i64, _u64, _f32, _sz = C.c_int32, C.c_int64, C.c_uint64, C.c_float, C.c_size_t
 
@@ -96,7 +99,7 @@ class CtrError(RuntimeError):
 
 def lib() -> C.CDLL:
     """Load libctr.so, building it first if the sources changed.  Raises if that fails."""
-    global _lib
+    global _lib, _calls
     if _lib is not None:
         return _lib
     with _lock:
@@ -109,8 +112,24 @@ def lib() -> C.CDLL:
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args
-            _lib = L
+            loader = importlib.machinery.ExtensionFileLoader("ctr_calls", _build.CALLS)
+            calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("ctr_calls", loader))
+            loader.exec_module(calls)
+            _calls, _lib = calls, L
     return _lib
+
+
+def _usual():
+    """The calls in their usual layouts (csrc/calls.cpp): each returns its status, or None if it did not take it."""
+    if _calls is None:
+        lib()
+    return _calls
+
+
+def _took(name: str, st: Optional[int]) -> bool:
+    if st:
+        raise CtrError(name, st)
+    return st is not None
 
 
 def library_path() -> str:
@@ -459,6 +478,9 @@ def ctr_expert_route(scores: torch.Tensor, k: int, renormalize: bool, expert: to
                      slot: torch.Tensor, token: torch.Tensor, offsets: torch.Tensor, ws: torch.Tensor,
                      stream=None) -> None:
     """The k best experts of every token (row of scores), their softmax weights, and the order by expert."""
+    if stream is None and _took("ctr_expert_route", _usual().expert_route(scores, k, renormalize, expert, weight, slot,
+                                                                          token, offsets, ws)):
+        return
     T, E, ld = _mat(scores, "scores")
     tk = (T, k)
     _dense(expert, "expert", _I32, tk)
@@ -475,6 +497,9 @@ def ctr_expert_route(scores: torch.Tensor, k: int, renormalize: bool, expert: to
 
 def ctr_expert_route_bwd(dweight: torch.Tensor, scores: torch.Tensor, renormalize: bool, expert: torch.Tensor,
                          dscores: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
+    if stream is None and _took("ctr_expert_route_bwd", _usual().expert_route_bwd(dweight, scores, renormalize,
+                expert, dscores, ws)):
+        return
     T, E, ld = _mat(scores, "scores")
     _want(expert.dim() == 2, "expert must be a matrix")
     k = expert.shape[1]
@@ -499,6 +524,8 @@ def _slots(slot: torch.Tensor, T: int) -> int:
 def ctr_expert_dispatch(x: torch.Tensor, slot: torch.Tensor, token: torch.Tensor, out: torch.Tensor, ws: torch.Tensor,
                         stream=None) -> None:
     """Token rows of x into the order by expert: out [T*k, d]."""
+    if stream is None and _took("ctr_expert_dispatch", _usual().expert_dispatch(x, slot, token, out, ws)):
+        return
     T, d, ld = _mat(x, "x")
     k = _slots(slot, T)
     _dense(token, "token", _I32, (T * k,))
@@ -512,6 +539,8 @@ def ctr_expert_dispatch(x: torch.Tensor, slot: torch.Tensor, token: torch.Tensor
 def ctr_expert_combine(rows: torch.Tensor, slot: torch.Tensor, weight: Optional[torch.Tensor], y: torch.Tensor,
                        ws: torch.Tensor, stream=None) -> None:
     """Rows [T*k, d] added back to tokens under the weights (None: all 1, the gradient of the dispatch)."""
+    if stream is None and _took("ctr_expert_combine", _usual().expert_combine(rows, slot, weight, y, ws)):
+        return
     T, d, ldy = _mat(y, "y")
     k = _slots(slot, T)
     ldr = _like(rows, "rows", T * k, d, y.dtype)
@@ -526,6 +555,9 @@ def ctr_expert_combine(rows: torch.Tensor, slot: torch.Tensor, weight: Optional[
 def ctr_expert_combine_bwd(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Tensor, weight: torch.Tensor,
                            token: torch.Tensor, drows: torch.Tensor, dweight: torch.Tensor, ws: torch.Tensor,
                            stream=None) -> None:
+    if stream is None and _took("ctr_expert_combine_bwd", _usual().expert_combine_bwd(dy, rows, slot, weight, token,
+                drows, dweight, ws)):
+        return
     T, d, ldy = _mat(dy, "dy")
     k = _slots(slot, T)
     ldr = _like(rows, "rows", T * k, d, dy.dtype)
@@ -578,6 +610,8 @@ def _codes_of(q: torch.Tensor, row_index: Optional[torch.Tensor], n: int, cols: 
 def ctr_fp8_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor, ws: torch.Tensor,
                           row_index: Optional[torch.Tensor] = None, stream=None) -> None:
     """Row codes q [rows, padded cols] and scales [blocks, rows] of x, or of its rows row_index."""
+    if stream is None and _took("ctr_fp8_quantize_rows", _usual().fp8_quantize_rows(x, q, scale, ws, row_index)):
+        return
     n, cols, ld = _mat(x, "x")
     rows = _codes_of(q, row_index, n, cols)
     lds = _like(scale, "scale", (cols + 127) // 128, rows, _F32)
@@ -591,6 +625,9 @@ def ctr_fp8_quantize_rows_cols(x: torch.Tensor, offsets: torch.Tensor, q: torch.
                                qc: torch.Tensor, scale_c: torch.Tensor, cols_by: int, ws: torch.Tensor,
                                row_index: Optional[torch.Tensor] = None, stream=None) -> None:
     """Row codes as above, and the column codes qc [cols, padded rows] of the grouped rows, in one read of x."""
+    if stream is None and _took("ctr_fp8_quantize_rows_cols", _usual().fp8_quantize_rows_cols(x, offsets, q, scale,
+                qc, scale_c, cols_by, ws, row_index)):
+        return
     n, cols, ld = _mat(x, "x")
     rows = _codes_of(q, row_index, n, cols)
     groups = offsets.numel() - 1
@@ -613,6 +650,8 @@ def ctr_fp8_quantize_blocks(w: torch.Tensor, q: torch.Tensor, scale: torch.Tenso
                             qt: Optional[torch.Tensor] = None, scale_t: Optional[torch.Tensor] = None,
                             stream=None) -> None:
     """Block codes of w [groups, n, k], and of its transpose where qt and scale_t are given."""
+    if stream is None and _took("ctr_fp8_quantize_blocks", _usual().fp8_quantize_blocks(w, q, scale, ws, qt, scale_t)):
+        return
     _want(isinstance(w, torch.Tensor) and w.dim() == 3 and w.dtype in DTYPES, "w must be [groups, n, k] fp32 or bf16")
     G, n, k = w.shape
     _dense(w, "w", w.dtype, (G, n, k))
@@ -630,6 +669,8 @@ def ctr_fp8_quantize_blocks(w: torch.Tensor, q: torch.Tensor, scale: torch.Tenso
 def ctr_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
                    offsets: Optional[torch.Tensor], out: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """out[r] = W_g a_r for the rows of each group, from row codes a [rows, P(k)] and block codes b [groups, n, P(k)]."""
+    if stream is None and _took("ctr_fp8_matmul", _usual().fp8_matmul(a, a_scale, b, b_scale, offsets, out, ws)):
+        return
     rows, n, ldo = _mat(out, "out")
     _want(isinstance(b, torch.Tensor) and b.dim() == 3, "b must be [groups, n, padded k]")
     G, bn, kp = b.shape
@@ -655,6 +696,9 @@ def ctr_fp8_matmul_wgrad(d: torch.Tensor, d_scale: torch.Tensor, x: torch.Tensor
 
     `rows` is the row count the codes were made for (it fixes their padding); by
     default the largest that has the codes' padded length."""
+    if stream is None and _took("ctr_fp8_matmul_wgrad", _usual().fp8_matmul_wgrad(d, d_scale, x, x_scale, offsets,
+                out, ws, rows)):
+        return
     _want(isinstance(out, torch.Tensor) and out.dim() == 3 and out.dtype in DTYPES, "out must be [groups, n, k]")
     G, n, k = out.shape
     _dense(out, "out", out.dtype, (G, n, k))
@@ -714,6 +758,8 @@ def ctr_clip_grads_workspace_size() -> int:
 
 def ctr_clip_grads(grads: GradList, max_norm: float, norm: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """The global norm of a grad_list into norm (fp32 [1]), and its outs = grads * min(1, max_norm / norm)."""
+    if stream is None and _took("ctr_clip_grads", _usual().clip_grads(*grads.addresses, grads.n, max_norm, norm, ws)):
+        return
     _dense(norm, "norm", torch.float32, (1,))
     st = lib().ctr_clip_grads(*grads.addresses, grads.n, max_norm,
                               norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
