@@ -17,8 +17,8 @@
 // of the bits before it, and the tile's count of an expert the count of all.
 // Three launches: choices + tile counts; exclusive sums of the counts over the
 // tiles (one warp column per expert); ranks and the two maps.  Up to kTileTokens
-// x 8 tokens run as one launch, a block or a cluster of up to eight blocks that
-// read each other's counts (2048 x 26, k 4: 8 us, most of it the call).
+// x 16 tokens run as one launch, a block or a cluster of up to sixteen blocks that
+// read each other's counts (2048 x 26, k 4: 6.1 us).
 //
 // Rows.  A token's group of lanes reads its row once and writes its k rows (or
 // reads k rows and writes one): every byte crosses HBM once, and rows of 1 KB
@@ -595,7 +595,9 @@ int route_lanes(int experts, int k, int per) {
 // against 48).
 int lane_scores(int experts) { return experts > 32 ? 16 : 8; }
 
-constexpr int kClusterTiles = 8;  // blocks of a portable cluster
+// Blocks of the largest cluster that a kernel may ask for (eight without asking: 2048 x 26 7.7 us against
+// 6.1, 4096 x 26 in three launches 12.6 against 8.6; both k 4).
+constexpr int kClusterTiles = 16;
 
 // Tokens of a tile: small batches are cut finer so that they spread over SMs, those that fit one
 // launch over the blocks of one cluster.
@@ -620,12 +622,22 @@ int check_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t exp
   return CTR_OK;
 }
 
+template <typename T, int EPL, int KMAX>
+bool launch_choose(const RouteArgs& a, size_t smem, bool cluster, cudaStream_t s) {
+  auto k = cluster ? route_choose_kernel<T, EPL, KMAX, true> : route_choose_kernel<T, EPL, KMAX, false>;
+  static std::atomic<uint64_t> ready{0};
+  if (cluster && !once_per_device(ready, [&] {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      }))
+    return false;
+  return launch_after(k, dim3((unsigned)a.tiles), kRouteThreads, smem, s, cluster ? (unsigned)a.tiles : 1u, a) ==
+         cudaSuccess;
+}
+
 template <typename T, int EPL>
-void launch_choose(const RouteArgs& a, size_t smem, bool cluster, cudaStream_t s) {
-  auto k = a.k <= 4 ? (cluster ? route_choose_kernel<T, EPL, 4, true> : route_choose_kernel<T, EPL, 4, false>)
-                    : (cluster ? route_choose_kernel<T, EPL, CTR_MAX_CHOICES, true>
-                               : route_choose_kernel<T, EPL, CTR_MAX_CHOICES, false>);
-  launch_after(k, dim3((unsigned)a.tiles), kRouteThreads, smem, s, cluster ? (unsigned)a.tiles : 1u, a);
+bool launch_choose(const RouteArgs& a, size_t smem, bool cluster, cudaStream_t s) {
+  return a.k <= 4 ? launch_choose<T, EPL, 4>(a, smem, cluster, s)
+                  : launch_choose<T, EPL, CTR_MAX_CHOICES>(a, smem, cluster, s);
 }
 
 // Lanes of a token whose softmax is over its choices: one for each, and enough that the row's zeros leave
@@ -904,13 +916,11 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   a.err = (int*)ws;
   const size_t smem = route_smem(experts, a.tile);
   const bool cluster = a.tiles > 1 && a.tiles <= kClusterTiles;
-  if (dtype == CTR_F32) {
-    if (per == 8) launch_choose<float, 8>(a, smem, cluster, s);
-    else launch_choose<float, 16>(a, smem, cluster, s);
-  } else {
-    if (per == 8) launch_choose<__nv_bfloat16, 8>(a, smem, cluster, s);
-    else launch_choose<__nv_bfloat16, 16>(a, smem, cluster, s);
-  }
+  const bool ok = dtype == CTR_F32 ? (per == 8 ? launch_choose<float, 8>(a, smem, cluster, s)
+                                               : launch_choose<float, 16>(a, smem, cluster, s))
+                                   : (per == 8 ? launch_choose<__nv_bfloat16, 8>(a, smem, cluster, s)
+                                               : launch_choose<__nv_bfloat16, 16>(a, smem, cluster, s));
+  if (!ok) return CTR_ERR_CUDA;
   if (a.tiles > 1 && !cluster) {
     launch_after(route_scan_kernel, dim3((unsigned)ceil_div(experts, 32)), 1024, 0, s, 1, a);
     launch_after(route_rank_kernel, dim3((unsigned)a.tiles), kRouteThreads, smem, s, 1, a);

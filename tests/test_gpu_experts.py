@@ -109,6 +109,14 @@ def test_route_nan_and_infinity_are_flagged_and_routed_nowhere():
     check_route(s, 3, True, "f32")
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E,k,pad", [(1025, 26, 4, 0), (2049, 26, 4, 0), (3777, 512, 16, 3), (4096, 200, 4, 0), (4097, 40, 1, 0)])
+def test_route_around_the_largest_cluster(T, E, k, pad, dtype):
+    s = _scores(T, E, dtype, 0.05, T)
+    for renorm in (False, True):
+        check_route(s, k, renorm, dtype, pad)
+
+
 @pytest.mark.parametrize("E", [7, 32, 40, 300])
 def test_route_every_bf16_number(E):
     # every finite bf16 number, subnormals and both zeros among them, in shuffled rows; a score's distance
