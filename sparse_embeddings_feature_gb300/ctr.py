@@ -5,6 +5,10 @@ arguments: torch tensors become device pointers, the current CUDA stream is
 passed along, and a negative ctr_status becomes a CtrError.  All computation
 happens in libctr's CUDA kernels; there is no CPU fallback.  If the library
 cannot be built or loaded the first call raises.
+
+The expert layer's calls are short enough that reading their arguments here
+costs more than the kernels: in the usual layouts (dense tensors, the current
+stream) csrc/calls.cpp reads them, and what it does not take comes back here.
 """
 from __future__ import annotations
 
