@@ -53,9 +53,22 @@ __device__ __forceinline__ float max_mag(const float (&v)[N]) {
   return m;
 }
 
+// (x, y) * inv, each rounded to fp32, in one instruction.
+__device__ __forceinline__ float2 times(float x, float y, float inv) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\t"
+      "mov.b64 a, {%2, %3};\n\t"
+      "mov.b64 b, {%4, %4};\n\t"
+      "mul.rn.f32x2 c, a, b;\n\t"
+      "mov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x), "f"(y), "f"(inv));
+  return r;
+}
+
 __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(times(v[0], v[1], inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(times(v[2], v[3], inv), __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
 
