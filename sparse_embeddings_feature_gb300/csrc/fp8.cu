@@ -66,10 +66,17 @@ __device__ __forceinline__ float2 times(float x, float y, float inv) {
   return r;
 }
 
+// Four codes, put together as halves of a word.
 __device__ __forceinline__ uint32_t codes4(const float* v, float inv) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(times(v[0], v[1], inv), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(times(v[2], v[3], inv), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  const float2 a = times(v[0], v[1], inv), b = times(v[2], v[3], inv);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
 
 // Columns c0 .. c0 + 7 of a row of `cols` elements as fp32; zeros past the end.
