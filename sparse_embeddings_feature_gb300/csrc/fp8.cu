@@ -17,7 +17,7 @@
 // first.  For the column order a thread holds 32 rows of two neighbouring columns
 // in registers (one shared-memory read of both columns' values per row) for the
 // maximum and for the codes, which leave in 16-byte stores.  Bound by instruction
-// issue (0.73 of the slots; 65536 x 1024 bf16, both orders, 59 us: 268 MB at 4.5
+// issue (0.71 of the slots; 65536 x 1024 bf16, both orders, 57 us: 268 MB at 4.7
 // TB/s; rows alone 45 us).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
