@@ -279,6 +279,15 @@ struct Chooser<__nv_bfloat16, EPL, KMAX> {
   }
 };
 
+// i / k for the choices of a tile, i < kTileTokens * k: with m = ceil(2^16 / k), i m / 2^16 is too large by
+// less than i / 2^16 < 1 / k.
+struct TokenOf {
+  uint32_t m;
+  __device__ __forceinline__ explicit TokenOf(int k) : m((65535u + (uint32_t)k) / (uint32_t)k) {}
+  __device__ __forceinline__ int operator()(int i) const { return (int)(((uint32_t)i * m) >> 16); }
+};
+static_assert(kTileTokens * CTR_MAX_CHOICES * CTR_MAX_CHOICES <= 65536, "a tile's choices leave the bound of TokenOf");
+
 // Ranks of the tile's choices from its bit matrix: slot and token of each, given the first row of
 // every expert's choices in this tile.  `before` gets each word's count of earlier tokens.
 __device__ __forceinline__ void write_slots(const RouteArgs& a, int64_t t0, int n, const uint32_t* bits,
@@ -292,12 +301,13 @@ __device__ __forceinline__ void write_slots(const RouteArgs& a, int64_t t0, int 
     }
   }
   __syncthreads();
+  const TokenOf token_of(a.k);
   for (int i = threadIdx.x; i < n * a.k; i += kRouteThreads) {
     const int64_t at = t0 * a.k + i;
     const int e = a.expert[at];
     int s = -1;
     if (e >= 0) {
-      const int t = i / a.k, w = e * words + (t >> 5);
+      const int t = token_of(i), w = e * words + (t >> 5);
       s = first[e] + before[w] + __popc(bits[w] & ((1u << (t & 31)) - 1));
       a.token[s] = (int32_t)(t0 + t);
     }
@@ -437,8 +447,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_rank_kernel(const RouteAr
   for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
   __syncthreads();
   grid_wait();
+  const TokenOf token_of(a.k);
   for (int i = threadIdx.x; i < n * a.k; i += kRouteThreads) {
-    const int e = a.expert[t0 * a.k + i], t = i / a.k;
+    const int e = a.expert[t0 * a.k + i], t = token_of(i);
     if (e >= 0) atomicOr(&bits[e * words + (t >> 5)], 1u << (t & 31));
   }
   const int all = expert_starts(a.counts + (int64_t)a.tiles * a.experts, a.experts, first, warp_sum);
