@@ -617,7 +617,12 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
 #pragma unroll
         for (int h = 0; h < kCols / 32; ++h) {
           if (col0 + 32 * h >= p.n) break;
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");  // the place is free
+          // The place is free: all of the last tile's pieces have left (an odd number of them ends in the first
+          // place), then of this tile's all but the newest.
+          if (lane == 0) {
+            if (h == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            else asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          }
           __syncwarp();
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
