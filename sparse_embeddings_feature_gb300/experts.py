@@ -30,7 +30,8 @@ class ExpertLayer:
     """y[t] = sum over t's k experts e of weight(t, e) W_e x[t], with W [experts, out_width, width].
 
     x and y are fp32 or bf16 (`dtype`); rows of x may be strided.  With `train`, forward keeps what
-    backward needs: backward(dy) returns (dx, dscores, dw) for the latest forward."""
+    backward needs, a copy of the scores with it: backward(dy) returns (dx, dscores, dw) for the latest
+    forward, whatever became of its arguments."""
 
     def __init__(self, tokens: int, width: int, out_width: int, experts: int, k: int, dtype=torch.float32,
                  renormalize: bool = True, train: bool = False, device="cuda"):
@@ -64,7 +65,7 @@ class ExpertLayer:
             self.dcq, self.dcs = buf(N, P, dt=u8), buf(P // 128, N)
             self.dxs, self.dx = buf(R, K, dt=dtype), buf(T, K, dt=dtype)
             self.dw = buf(E, N, K)
-            self.dscores = None
+            self.kept = {}   # type of the scores -> their copy and their gradient; kept, as a captured graph uses them
         self.norm = buf(1)
         self.ws_route = ctr.workspace(ctr.ctr_expert_route_workspace_size(T, E, k), device)
         self.ws_rows = ctr.workspace(ctr.ctr_expert_workspace_size(), device)
@@ -85,7 +86,11 @@ class ExpertLayer:
         ctr.ctr_expert_route(scores, self.k, self.renormalize, self.expert, self.weight, self.slot, self.token,
                              self.offsets, self.ws_route)
         if self.train:
-            self.scores = scores
+            if scores.dtype not in self.kept:
+                self.kept[scores.dtype] = tuple(torch.empty(scores.shape, dtype=scores.dtype, device=scores.device)
+                                                for _ in range(2))
+            self.scores, self.dscores = self.kept[scores.dtype]
+            self.scores.copy_(scores)
             ctr.ctr_fp8_quantize_rows_cols(x, self.offsets, self.xq, self.xs, self.xcq, self.xcs,
                                            ctr.FP8_COLS_BY_BLOCK, self.ws_mm, row_index=self.token)
         else:
@@ -105,8 +110,6 @@ class ExpertLayer:
         if not self.train or self.scores is None:
             raise RuntimeError("backward needs train=True and a forward")
         dx = self.dx if dx is None else dx
-        if self.dscores is None or self.dscores.shape != self.scores.shape or self.dscores.dtype != self.scores.dtype:
-            self.dscores = torch.empty_like(self.scores, memory_format=torch.contiguous_format)
         ctr.ctr_expert_combine_bwd(dy, self.ys, self.slot, self.weight, self.token, self.dys, self.dweight, self.ws_rows)
         ctr.ctr_fp8_quantize_rows_cols(self.dys, self.offsets, self.dq, self.ds, self.dcq, self.dcs,
                                        ctr.FP8_COLS_BY_COLUMN, self.ws_mm)

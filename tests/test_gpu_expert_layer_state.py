@@ -1,0 +1,47 @@
+"""What ExpertLayer keeps between its calls, and what it refuses."""
+import pytest
+import torch
+
+from sparse_embeddings_feature_gb300 import ctr
+from sparse_embeddings_feature_gb300.experts import ExpertLayer
+
+pytestmark = pytest.mark.gpu
+
+T, K, N, E, TOP = 300, 479, 96, 8, 2
+
+
+def _case(seed=0, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x, s, dy = (torch.randn(shape, generator=g, device="cuda").to(dtype) for shape in ((T, K), (T, E), (T, N)))
+    return x, s, torch.randn((E, N, K), generator=g, device="cuda") / K ** 0.5, dy
+
+
+def _layer(w, **kw):
+    layer = ExpertLayer(T, K, N, E, TOP, **kw)
+    layer.set_weights(w)
+    return layer
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_scores_may_change_after_forward(dtype, renorm):
+    x, s, w, dy = _case()
+    s = s.to(dtype)
+    layer = _layer(w, train=True, renormalize=renorm)
+    layer.forward(x, s)
+    ref = [t.clone() for t in layer.backward(dy)]
+    layer.forward(x, s)
+    s.copy_(torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(9), device="cuda"))
+    for a, b in zip(ref, layer.backward(dy)):
+        assert torch.equal(a, b)
+
+
+def test_strided_scores_of_either_type_in_turn():
+    x, s, w, dy = _case()
+    layer, fresh = _layer(w, train=True), _layer(w, train=True)
+    wide = torch.zeros((T, E + 5), device="cuda")
+    for scores in (s, s.bfloat16(), wide[:, :E].copy_(s), s):
+        layer.forward(x, scores)
+        fresh.forward(x, scores.contiguous())
+        a, b = layer.backward(dy)[1], fresh.backward(dy)[1]
+        assert a.dtype == scores.dtype and torch.equal(a, b)
