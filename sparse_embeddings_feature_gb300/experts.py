@@ -76,9 +76,11 @@ class ExpertLayer:
 
     def set_weights(self, w: torch.Tensor) -> None:
         """Quantise the experts' weights [experts, out_width, width] (fp32 or bf16): once for serving, after
-        every update in training."""
+        every update in training.  The latest forward is then no longer there for backward, whose input
+        gradient would be that of other weights."""
         if tuple(w.shape) != (self.experts, self.out_width, self.width):
             raise ValueError(f"weights must be {(self.experts, self.out_width, self.width)}")
+        self.scores = None
         ctr.ctr_fp8_quantize_blocks(w, self.wq, self.ws, self.ws_mm, *((self.wtq, self.wts) if self.train else ()))
 
     def forward(self, x: torch.Tensor, scores: torch.Tensor) -> torch.Tensor:
@@ -108,7 +110,7 @@ class ExpertLayer:
     def backward(self, dy: torch.Tensor, dx: Optional[torch.Tensor] = None):
         """(dx, dscores, dw) of the latest forward; dx goes to `dx` where one is given."""
         if not self.train or self.scores is None:
-            raise RuntimeError("backward needs train=True and a forward")
+            raise RuntimeError("backward needs train=True and a forward since the weights were set")
         dx = self.dx if dx is None else dx
         ctr.ctr_expert_combine_bwd(dy, self.ys, self.slot, self.weight, self.token, self.dys, self.dweight, self.ws_rows)
         ctr.ctr_fp8_quantize_rows_cols(self.dys, self.offsets, self.dq, self.ds, self.dcq, self.dcs,

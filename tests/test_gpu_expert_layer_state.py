@@ -45,3 +45,14 @@ def test_strided_scores_of_either_type_in_turn():
         fresh.forward(x, scores.contiguous())
         a, b = layer.backward(dy)[1], fresh.backward(dy)[1]
         assert a.dtype == scores.dtype and torch.equal(a, b)
+
+
+def test_new_weights_end_the_forward():
+    x, s, w, dy = _case()
+    layer = _layer(w, train=True)
+    layer.forward(x, s)
+    layer.set_weights(w * 2)
+    with pytest.raises(RuntimeError):
+        layer.backward(dy)
+    layer.forward(x, s)
+    layer.backward(dy)
