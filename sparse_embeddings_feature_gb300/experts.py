@@ -85,20 +85,23 @@ class ExpertLayer:
 
     def forward(self, x: torch.Tensor, scores: torch.Tensor) -> torch.Tensor:
         """y [tokens, out_width] of x [tokens, width] under the router's scores [tokens, experts]."""
+        self.scores = None   # until this forward is complete there is none
         ctr.ctr_expert_route(scores, self.k, self.renormalize, self.expert, self.weight, self.slot, self.token,
                              self.offsets, self.ws_route)
         if self.train:
             if scores.dtype not in self.kept:
                 self.kept[scores.dtype] = tuple(torch.empty(scores.shape, dtype=scores.dtype, device=scores.device)
                                                 for _ in range(2))
-            self.scores, self.dscores = self.kept[scores.dtype]
-            self.scores.copy_(scores)
+            kept, self.dscores = self.kept[scores.dtype]
+            kept.copy_(scores)
             ctr.ctr_fp8_quantize_rows_cols(x, self.offsets, self.xq, self.xs, self.xcq, self.xcs,
                                            ctr.FP8_COLS_BY_BLOCK, self.ws_mm, row_index=self.token)
         else:
             ctr.ctr_fp8_quantize_rows(x, self.xq, self.xs, self.ws_mm, row_index=self.token)
         ctr.ctr_fp8_matmul(self.xq, self.xs, self.wq, self.ws, self.offsets, self.ys, self.ws_mm)
         ctr.ctr_expert_combine(self.ys, self.slot, self.weight, self.y, self.ws_rows)
+        if self.train:
+            self.scores = kept
         return self.y
 
     def sorted_rows(self, x: torch.Tensor, out: torch.Tensor) -> torch.Tensor:

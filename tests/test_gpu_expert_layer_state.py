@@ -56,3 +56,13 @@ def test_new_weights_end_the_forward():
         layer.backward(dy)
     layer.forward(x, s)
     layer.backward(dy)
+
+
+def test_a_refused_forward_leaves_none():
+    x, s, w, dy = _case()
+    layer = _layer(w, train=True)
+    layer.forward(x, s)
+    with pytest.raises(ValueError):
+        layer.forward(x.double(), s.flip(1))
+    with pytest.raises(RuntimeError):
+        layer.backward(dy)
