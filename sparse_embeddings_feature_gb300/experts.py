@@ -85,6 +85,9 @@ class ExpertLayer:
 
     def forward(self, x: torch.Tensor, scores: torch.Tensor) -> torch.Tensor:
         """y [tokens, out_width] of x [tokens, width] under the router's scores [tokens, experts]."""
+        # the calls see the padded width of x and look its rows up through the map: its sizes are checked here
+        if not isinstance(x, torch.Tensor) or x.shape != (self.tokens, self.width):
+            raise ValueError(f"x must be {(self.tokens, self.width)}")
         self.scores = None   # until this forward is complete there is none
         ctr.ctr_expert_route(scores, self.k, self.renormalize, self.expert, self.weight, self.slot, self.token,
                              self.offsets, self.ws_route)

@@ -66,3 +66,18 @@ def test_a_refused_forward_leaves_none():
         layer.forward(x.double(), s.flip(1))
     with pytest.raises(RuntimeError):
         layer.backward(dy)
+
+
+@pytest.mark.parametrize("train", [False, True])
+def test_forward_takes_its_own_sizes_only(train):
+    x, s, w, _ = _case()
+    layer = _layer(w, train=train)
+    more = torch.zeros((T + 1, K), device="cuda")
+    for bad in (x[:, :400], x[:, :K - 1], x[:-1], more, x[0], None):
+        with pytest.raises(ValueError):
+            layer.forward(bad, s)
+    for bad in (s[:-1], s[:, :-1], torch.zeros((T, E + 1), device="cuda")):
+        with pytest.raises(ValueError):
+            layer.forward(x, bad)
+    layer.forward(x, s)
+    assert all(v == 0 for v in layer.check_status().values())
