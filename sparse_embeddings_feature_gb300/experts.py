@@ -130,6 +130,8 @@ class ExpertLayer:
 
     def clip(self, max_norm: float, others: Iterable[torch.Tensor] = ()) -> torch.Tensor:
         """Scale dw and `others` in place to a global norm of at most max_norm; the norm [1], on the device."""
+        if not self.train:
+            raise RuntimeError("clip needs train=True")
         grads = [self.dw, *others]
         ctr.ctr_clip_grads(ctr.grad_list(grads, grads), max_norm, self.norm, self.ws_clip)
         return self.norm

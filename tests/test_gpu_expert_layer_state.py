@@ -81,3 +81,8 @@ def test_forward_takes_its_own_sizes_only(train):
             layer.forward(x, bad)
     layer.forward(x, s)
     assert all(v == 0 for v in layer.check_status().values())
+
+
+def test_clip_needs_gradients():
+    with pytest.raises(RuntimeError):
+        _layer(_case()[2]).clip(1.0)
