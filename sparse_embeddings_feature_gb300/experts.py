@@ -19,7 +19,7 @@ gradient, so the embedding rows learn too.
 """
 from __future__ import annotations
 
-from typing import Iterable, Optional
+from typing import Iterable, Optional, Union
 
 import torch
 
@@ -128,12 +128,19 @@ class ExpertLayer:
         ctr.ctr_expert_route_bwd(self.dweight, self.scores, self.renormalize, self.expert, self.dscores, self.ws_route)
         return dx, self.dscores, self.dw
 
-    def clip(self, max_norm: float, others: Iterable[torch.Tensor] = ()) -> torch.Tensor:
-        """Scale dw and `others` in place to a global norm of at most max_norm; the norm [1], on the device."""
+    def grads(self, others: Iterable[torch.Tensor] = ()) -> ctr.GradList:
+        """dw and `others` as a list for clip.  For tensors that stay where they are it is built once: it
+        takes the host longer than the clipping of a small net's gradients takes the GPU."""
         if not self.train:
-            raise RuntimeError("clip needs train=True")
+            raise RuntimeError("a layer has gradients with train=True")
         grads = [self.dw, *others]
-        ctr.ctr_clip_grads(ctr.grad_list(grads, grads), max_norm, self.norm, self.ws_clip)
+        return ctr.grad_list(grads, grads)
+
+    def clip(self, max_norm: float, others: Union[ctr.GradList, Iterable[torch.Tensor]] = ()) -> torch.Tensor:
+        """Scale dw and `others` (tensors, or a list from `grads`) in place to a global norm of at most
+        max_norm; the norm [1], on the device."""
+        grads = others if isinstance(others, ctr.GradList) else self.grads(others)
+        ctr.ctr_clip_grads(grads, max_norm, self.norm, self.ws_clip)
         return self.norm
 
     def check_status(self) -> dict:

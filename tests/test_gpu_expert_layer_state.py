@@ -86,3 +86,18 @@ def test_forward_takes_its_own_sizes_only(train):
 def test_clip_needs_gradients():
     with pytest.raises(RuntimeError):
         _layer(_case()[2]).clip(1.0)
+
+
+def test_clip_with_a_list_built_once(monkeypatch):
+    x, s, w, dy = _case()
+    layer, other = _layer(w, train=True), torch.randn(1000, device="cuda")
+    layer.forward(x, s)
+    layer.backward(dy)
+    dw = layer.dw.clone()
+    ref = float((dw.double().square().sum() + other.double().square().sum()).sqrt())
+    kept = layer.grads([other])
+    monkeypatch.setattr(ctr, "grad_list", None)     # nothing is put together in the call
+    assert abs(layer.clip(2 * ref, kept).item() - ref) <= 1e-5 * ref
+    assert torch.equal(layer.dw, dw)
+    assert abs(layer.clip(0.5 * ref, kept).item() - ref) <= 1e-5 * ref
+    assert torch.allclose(layer.dw, dw * 0.5, rtol=1e-5, atol=0)
