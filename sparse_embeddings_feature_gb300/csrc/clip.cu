@@ -8,7 +8,9 @@
 // fp64; joins are fp64 in a fixed order, so the result does not change from run
 // to run.  A part whose sum of squares comes near either end of fp32's range is
 // read again and squared in fp64 by its warp (fp64 in the common path, even
-// predicated off, tripled the pass: 724 us against 248 for 5e8 elements).  Every
+// predicated off, tripled the pass: 724 us against 248 for 5e8 elements), unless
+// all of it is zero, as the weight gradient of an expert without rows is (2.5e8
+// fp32 zeros 150 us; in fp64 973).  Every
 // block of the second pass adds the first one's sums up for itself, in the same
 // order: no counter, and no launch between the two.  Two passes over the data,
 // bound by HBM: the second walks the chunks in reverse, so what the first read
@@ -55,12 +57,15 @@ __device__ __forceinline__ int tensor_of(const ClipList& l, int64_t chunk) {
   return lo;
 }
 
-// Sum of squares of this thread's part of a chunk: 16-byte pieces where the chunk is aligned.
+// Sum of squares of this thread's part of a chunk: 16-byte pieces where the chunk is aligned.  nonzero: whether
+// any of its magnitudes has a bit set, which tells zeros from squares that were too small for fp32.
 template <typename T>
-__device__ __forceinline__ float chunk_squares(const T* g, int n) {
+__device__ __forceinline__ float chunk_squares(const T* g, int n, bool& nonzero) {
   constexpr int per = 16 / (int)sizeof(T);
   constexpr int pieces = kChunk / per / kClipThreads;
+  constexpr uint32_t kMagnitude = sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  uint32_t bits = 0;
   int i0 = 0;
   if (((uintptr_t)g & 15) == 0) {
     const int full = n / per;
@@ -75,6 +80,7 @@ __device__ __forceinline__ float chunk_squares(const T* g, int n) {
     for (int p = 0; p < pieces; ++p) {
       float f[per];
       Chunk<T, 16>::unpack(raw[p], f);
+      bits |= (raw[p].x | raw[p].y | raw[p].z | raw[p].w) & kMagnitude;
 #pragma unroll
       for (int i = 0; i < per; ++i) acc[i & 3] = fmaf(f[i], f[i], acc[i & 3]);
     }
@@ -83,7 +89,9 @@ __device__ __forceinline__ float chunk_squares(const T* g, int n) {
   for (int i = i0 + threadIdx.x; i < n; i += kClipThreads) {
     const float f = to_f32<T>(g[i]);
     acc[0] = fmaf(f, f, acc[0]);
+    bits |= __float_as_uint(f) & 0x7fffffffu;
   }
+  nonzero = bits != 0;
   return (acc[0] + acc[1]) + (acc[2] + acc[3]);
 }
 
@@ -133,8 +141,9 @@ __global__ void __launch_bounds__(kClipThreads) norm_kernel(const __grid_constan
     const bool f32 = l.dtype[t] == CTR_F32;
     const float* g32 = (const float*)l.g[t] + e0;
     const __nv_bfloat16* g16 = (const __nv_bfloat16*)l.g[t] + e0;
-    const float sum = f32 ? chunk_squares(g32, n) : chunk_squares(g16, n);
-    const bool odd = !(sum <= kBig) || (sum < kSmall && (int)threadIdx.x < n);
+    bool nonzero;
+    const float sum = f32 ? chunk_squares(g32, n, nonzero) : chunk_squares(g16, n, nonzero);
+    const bool odd = !(sum <= kBig) || (sum < kSmall && nonzero);
     if (__any_sync(kFull, odd)) {
       wide += f32 ? chunk_squares_wide(g32, n) : chunk_squares_wide(g16, n);
     } else {
