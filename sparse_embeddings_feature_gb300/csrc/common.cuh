@@ -80,7 +80,10 @@ inline bool once_per_device(std::atomic<uint64_t>& done, F&& setup) {
 }
 
 // Launches `k` so that its blocks may be set up while the kernel before it in the stream drains
-// (programmatic dependent launch).  Such a kernel calls grid_wait() before it touches memory.
+// (programmatic dependent launch).  Such a kernel calls grid_wait() before it touches memory, and reads what
+// other kernels may have written by plain loads: read-only ones (__ldg, const __restrict__ pointers) are for
+// data that is constant as long as the kernel runs, which includes the time before the wait, and may be moved
+// over it.
 template <typename... P, typename... A>
 inline cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, unsigned cluster,
                                 const A&... args) {

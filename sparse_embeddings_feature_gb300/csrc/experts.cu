@@ -701,7 +701,7 @@ struct RowArgs {
 };
 
 __device__ __forceinline__ int checked_slot(const RowArgs& a, int64_t i) {
-  const int s = __ldg(a.slot + i);
+  const int s = a.slot[i];
   if (s >= a.total) {
     set_error(a.err, CTR_ERR_INDEX_OUT_OF_RANGE);
     return -1;
@@ -714,9 +714,9 @@ template <typename Raw>
 __device__ __forceinline__ void zero_unused(const RowArgs& a, const Raw& zero) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t)gridDim.x * (kRowThreads / 32);
-  for (int64_t r0 = ((int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * 32; r0 < a.total;
+  for (int64_t r0 = (int64_t)(blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5)) * 32; r0 < a.total;
        r0 += warps * 32) {
-    const bool unused = r0 + lane < a.total && __ldg(a.token + r0 + lane) < 0;
+    const bool unused = r0 + lane < a.total && a.token[r0 + lane] < 0;
     unsigned todo = __ballot_sync(kFull, unused);
     while (todo) {
       const int b = __ffs(todo) - 1;
@@ -727,14 +727,18 @@ __device__ __forceinline__ void zero_unused(const RowArgs& a, const Raw& zero) {
   }
 }
 
+// Blocks of an SM (0: the compiler's choice) where the compiler, left alone, takes fewer registers than the
+// loads in flight want, or more than leave room for blocks: dispatch of 65536 x 1024 bf16 68.2 us against 66.2
+// with five, of 65536 x 479 fp32 71.7 against 70.3, its gradients 119.4 against 115.4 with four, its sums 94 us
+// against 83 with six (2048 rows 5.0 against 6.2).
 template <int VB>
-__global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads, VB == 2 ? 0 : VB == 8 ? 6 : 5) dispatch_kernel(const RowArgs a) {
   using Raw = typename RawOf<VB>::type;
   constexpr int kUnroll = row_unroll<VB>();
   grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
-  for (int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes; t < a.tokens; t += groups) {
+  for (int64_t t = (blockIdx.x * kRowThreads + threadIdx.x) / (uint32_t)a.lanes; t < a.tokens; t += groups) {
     const Raw* x = (const Raw*)(a.x + t * a.ldx);
     for (int c0 = sub; c0 < a.chunks; c0 += kUnroll * a.lanes) {
       Raw v[kUnroll];
@@ -755,14 +759,14 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(const RowArgs a) 
 }
 
 template <typename T, int VB>
-__global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 4 && VB == 4 ? 6 : 0) combine_kernel(const RowArgs a) {
   using Ch = Chunk<T, VB>;
   using Raw = typename Ch::Raw;
   constexpr int kUnroll = sum_unroll<VB>();
   grid_wait();
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
-  for (int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes; t < a.tokens; t += groups) {
+  for (int64_t t = (blockIdx.x * kRowThreads + threadIdx.x) / (uint32_t)a.lanes; t < a.tokens; t += groups) {
     Raw* y = (Raw*)(a.out + t * a.ldo);
     for (int c0 = sub; c0 < a.chunks; c0 += kUnroll * a.lanes) {
       float acc[kUnroll][Ch::n];
@@ -770,11 +774,11 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
       for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (int i = 0; i < Ch::n; ++i) acc[u][i] = 0.f;
-#pragma unroll 2
+#pragma unroll 1  // two choices at a time: 67.7 us against 66.7 for 65536 x 1024 bf16, k 2
       for (int j = 0; j < a.k; ++j) {
         const int s = checked_slot(a, t * a.k + j);
         if (s < 0) continue;
-        const float w = a.weight ? __ldg(a.weight + t * a.k + j) : 1.f;
+        const float w = a.weight ? a.weight[t * a.k + j] : 1.f;
         const Raw* r = (const Raw*)(a.rows + s * a.ldr);
         Raw v[kUnroll];
 #pragma unroll
@@ -797,7 +801,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(const RowArgs a) {
 }
 
 template <typename T, int VB>
-__global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(kRowThreads, sizeof(T) == 4 && VB < 16 ? 4 : 0) combine_bwd_kernel(const RowArgs a) {
   using Ch = Chunk<T, VB>;
   using Raw = typename Ch::Raw;
   constexpr int kUnroll = row_unroll<VB>();
@@ -805,7 +809,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(const RowArgs 
   const int sub = threadIdx.x & (a.lanes - 1);
   const int64_t groups = (int64_t)gridDim.x * (kRowThreads / a.lanes);
   const int64_t trips = ceil_div(a.tokens, groups);  // the same in every lane: the shuffles need all of them
-  int64_t t = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) / a.lanes;
+  int64_t t = (blockIdx.x * kRowThreads + threadIdx.x) / (uint32_t)a.lanes;
   for (int64_t trip = 0; trip < trips; ++trip, t += groups) {
     const bool mine = t < a.tokens;
     const Raw* dy = (const Raw*)(a.x + t * a.ldx);
@@ -813,7 +817,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_bwd_kernel(const RowArgs 
       const int s = mine ? checked_slot(a, t * a.k + j) : -1;
       float dot = 0.f;
       if (s >= 0) {
-        const float w = __ldg(a.weight + t * a.k + j);
+        const float w = a.weight[t * a.k + j];
         const Raw* r = (const Raw*)(a.rows + s * a.ldr);
         Raw* out = (Raw*)(a.out + s * a.ldo);
         for (int c0 = sub; c0 < a.chunks; c0 += kUnroll * a.lanes) {

@@ -100,7 +100,7 @@ __device__ __forceinline__ void load8(const T* row, int64_t c0, int64_t cols, bo
 // Row of x for row r of the codes: row_index[r], or r; -1 for a zero row.
 __device__ __forceinline__ int64_t source_row(const int32_t* row_index, int64_t r, int64_t x_rows, int* err) {
   if (!row_index) return r;
-  const int64_t i = __ldg(row_index + r);
+  const int64_t i = row_index[r];
   if (i >= x_rows) {
     set_error(err, CTR_ERR_INDEX_OUT_OF_RANGE);
     return -1;
@@ -154,7 +154,7 @@ __device__ __forceinline__ void load_part(RowPart<T>& p, const T* x, int64_t ldx
 #pragma unroll
     for (int h = 0; h < 8 / per; ++h) {
       if (vec && src >= 0 && c + (h + 1) * per <= cols) {
-        p.raw[b][h] = __ldg((const uint4*)(row + h * per));
+        p.raw[b][h] = *(const uint4*)(row + h * per);
       } else {
         float f[per];
 #pragma unroll
@@ -275,17 +275,23 @@ __device__ __forceinline__ void stage_tile(T* tile, const T* x, int64_t ldx, int
   constexpr int per = B / (int)sizeof(T), parts = 128 / per;
   constexpr int kLanes = parts < 32 ? parts : 32, kTurns = parts / kLanes, kStep = tile_threads<T>() / kLanes;
   const int c0 = ((int)threadIdx.x % kLanes) * per;
-#pragma unroll(kTurns == 1 ? 4 : 1)
-  for (int i = (int)threadIdx.x / kLanes; i < 128; i += kStep) {
-    const int64_t src = source(i);
-    const T* row = x + (src >= 0 ? src * ldx + col0 : 0);
-    const int have = src >= 0 ? ncols : 0;
+  constexpr int kRows = kTurns == 1 ? 4 : 1;  // rows whose places are looked up together
+#pragma unroll 1
+  for (int i0 = (int)threadIdx.x / kLanes; i0 < 128; i0 += kRows * kStep) {
+    int64_t src[kRows];
 #pragma unroll
-    for (int h = 0; h < kTurns; ++h) {
-      const int c = c0 + h * kLanes * per;
-      int take = c < have ? B : 0;
-      if constexpr (per > 1) take = min(take, max(0, (have - c) * (int)sizeof(T)));
-      copy_async<B>(tile + i * tile_ld<T>() + c, take ? row + c : x, take);
+    for (int u = 0; u < kRows; ++u) src[u] = source(i0 + u * kStep);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      const T* row = x + (src[u] >= 0 ? src[u] * ldx + col0 : 0);
+      const int have = src[u] >= 0 ? ncols : 0;
+#pragma unroll
+      for (int h = 0; h < kTurns; ++h) {
+        const int c = c0 + h * kLanes * per;
+        int take = c < have ? B : 0;
+        if constexpr (per > 1) take = min(take, max(0, (have - c) * (int)sizeof(T)));
+        copy_async<B>(tile + (i0 + u * kStep) * tile_ld<T>() + c, take ? row + c : x, take);
+      }
     }
   }
 }
@@ -308,7 +314,7 @@ __device__ __forceinline__ void stage_elements(T* tile, const T* x, int64_t ldx,
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int c = h * 32 + lane;
-        v[u][h] = src[u] >= 0 && c < ncols ? __ldg(x + src[u] * ldx + col0 + c) : from_f32<T>(0.f);
+        v[u][h] = src[u] >= 0 && c < ncols ? x[src[u] * ldx + col0 + c] : from_f32<T>(0.f);
       }
 #pragma unroll
     for (int u = 0; u < kRows; ++u)
@@ -338,13 +344,13 @@ __global__ void __launch_bounds__(tile_threads<T>(), sizeof(T) == 2 ? 5 : 3) qua
       if (lane == 0) where[2] = 0;
       __syncwarp();
       int seen = 0;
-      bool ok = __ldg(a.offsets) == 0;
+      bool ok = a.offsets[0] == 0;
       for (int g0 = 0; g0 < a.groups; g0 += 32) {
         const int g = g0 + lane;
         int lo = 0, hi = 0;
         if (g < a.groups) {
-          lo = __ldg(a.offsets + g);
-          hi = __ldg(a.offsets + g + 1);
+          lo = a.offsets[g];
+          hi = a.offsets[g + 1];
           ok = ok && lo >= 0 && hi >= lo && hi <= a.rows;
         }
         const int mine = ok ? (hi - lo + 127) / 128 : 0;

@@ -268,13 +268,13 @@ __device__ __forceinline__ void group_starts(const MmArgs& p, int32_t* start, in
     return;
   }
   int seen = 0;
-  bool ok = __ldg(p.offsets) == 0;
+  bool ok = p.offsets[0] == 0;
   for (int g0 = 0; g0 < p.groups; g0 += 32) {
     const int g = g0 + lane;
     int lo = 0, hi = 0;
     if (g < p.groups) {
-      lo = __ldg(p.offsets + g);
-      hi = __ldg(p.offsets + g + 1);
+      lo = p.offsets[g];
+      hi = p.offsets[g + 1];
       ok = ok && lo >= 0 && hi >= lo && hi <= p.rows;
     }
     int incl = ok ? (hi - lo + size - 1) / size : 0;
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
 constexpr int kJoinThreads = 256;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) join_sums_kernel(const MmArgs p, const float* __restrict__ part,
+__global__ void __launch_bounds__(kJoinThreads) join_sums_kernel(const MmArgs p, const float* part,
                                                                  int64_t ld, bool vec) {
   __shared__ int32_t start[CTR_MAX_EXPERTS + 1], offs[CTR_MAX_EXPERTS + 1];
   grid_wait();
@@ -841,7 +841,8 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(const MmArgs p,
   } else {
     const int q = warp & 3, n = q * 32 + lane;  // row of the weights
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16);
-    const float* sa = p.sa + (int64_t)j0 * p.ld_sa + row0 + lane;  // lane t has row t of x
+    // lane t has row t of x; the other lanes read the last one's scales, so that the loads need no branch
+    const float* sa = p.sa + (int64_t)j0 * p.ld_sa + row0 + min(lane, rows - 1);
     const float* sb = p.sb + (int64_t)(g * p.nt + ni) * p.ld_sb + j0;
     uint64_t acc[kFewCols / 2];
 #pragma unroll
@@ -850,8 +851,11 @@ __global__ void __launch_bounds__(kFewThreads, 2) fp8_few_kernel(const MmArgs p,
     for (int c = 0; ok && c < nkb; c += kFewChunk) {
       float f[kFewChunk];
 #pragma unroll
-      for (int i = 0; i < kFewChunk; ++i)
-        f[i] = c + i < nkb && lane < rows ? __ldg(sa + (int64_t)(c + i) * p.ld_sa) * __ldg(sb + c + i) : 0.f;
+      for (int i = 0; i < kFewChunk; ++i) {
+        const int j = min(c + i, nkb - 1);
+        const float v = sa[(int64_t)j * p.ld_sa] * sb[j];
+        f[i] = lane < rows ? v : 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < kFewChunk; ++i) {
         const int j = c + i, b = j & 1;
