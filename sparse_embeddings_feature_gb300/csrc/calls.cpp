@@ -1,8 +1,9 @@
 // The expert layer's calls from Python in their usual layouts: the arguments' types and shapes are read
 // from the tensors here, on the current stream, and the C entry point called.  A call whose arguments
-// are anything else (strided rows, a wrong shape, not a tensor) returns None: the binding in Python then
-// takes it, with its own checks and messages.  Reading and checking eight tensors there, and handing 16
-// numbers over, takes 5 us of the host, more than the kernels of a small call.
+// are anything else (strided rows, a wrong shape, tensors of another device than the current one, not a
+// tensor) returns None: the binding in Python then takes it, with its own checks and messages.  Reading
+// and checking eight tensors there, and handing 16 numbers over, takes 5 us of the host, more than the
+// kernels of a small call.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -18,10 +19,12 @@ namespace {
 
 struct Odd {};  // not the usual layout
 
+thread_local int device = 0;  // the current one, where the call's kernels run
+
 const at::Tensor& tensor(PyObject* o) {
   if (!THPVariable_Check(o)) throw Odd();
   const at::Tensor& t = THPVariable_Unpack(o);
-  if (!t.is_cuda() || !t.is_contiguous()) throw Odd();
+  if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous()) throw Odd();
   return t;
 }
 
@@ -97,6 +100,7 @@ PyObject* run(Py_ssize_t n, F&& call) {
   int st;
   if (n != N) Py_RETURN_NONE;
   try {
+    device = c10::cuda::current_device();
     st = call();
   } catch (...) {
     PyErr_Clear();
@@ -245,15 +249,15 @@ CALL(fp8_matmul_wgrad) {
   });
 }
 
-// addresses of grads, outs (or None), dtypes, counts; number of tensors, max_norm, norm, ws
+// addresses of grads, outs (or None), dtypes, counts; number of tensors, their device (or None), max_norm, norm, ws
 CALL(clip_grads) {
-  return run<8>(n, [&] {
+  return run<9>(n, [&] {
     const int64_t grads = number(a[0]), outs = a[1] == Py_None ? 0 : number(a[1]), types = number(a[2]);
     const int64_t counts = number(a[3]), tensors = number(a[4]);
-    if (!PyFloat_Check(a[5]) || tensors > INT32_MAX) throw Odd();
-    const Workspace w = workspace(a[7]);
+    if (!PyFloat_Check(a[6]) || tensors > INT32_MAX || (a[5] != Py_None && number(a[5]) != device)) throw Odd();
+    const Workspace w = workspace(a[8]);
     return ctr_clip_grads((const void* const*)grads, (void* const*)outs, (const int32_t*)types, (const int64_t*)counts,
-                          (int32_t)tensors, (float)PyFloat_AS_DOUBLE(a[5]), floats(a[6], {1}), w.p, w.n, stream());
+                          (int32_t)tensors, (float)PyFloat_AS_DOUBLE(a[6]), floats(a[7], {1}), w.p, w.n, stream());
   });
 }
 

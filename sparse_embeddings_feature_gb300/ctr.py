@@ -436,9 +436,16 @@ _F32, _I32, _U8 = torch.float32, torch.int32, torch.uint8
 _F32_ONLY = (torch.float32,)
 
 
+def _here(device: Optional[int], what: str) -> None:
+    """Refuse data of another device than the current one, where the call's kernels run."""
+    if device is not None and device != torch.cuda.current_device():
+        raise ValueError(f"{what} is on cuda:{device}, and the current device is cuda:{torch.cuda.current_device()}")
+
+
 def _mat(t: torch.Tensor, what: str, dtypes=_F):
     """(rows, columns, row stride) of a CUDA matrix whose rows are contiguous and do not overlap."""
     if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes:
+        _here(t.get_device(), what)
         shape = t.shape
         if len(shape) == 2:
             rows, cols = shape
@@ -453,6 +460,7 @@ def _mat(t: torch.Tensor, what: str, dtypes=_F):
 
 def _dense(t: torch.Tensor, what: str, dtype, shape) -> None:
     if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.is_cuda:
+        _here(t.get_device(), what)
         return
     raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
 
@@ -735,6 +743,7 @@ class GradList:
     def __init__(self, grads, outs):
         n = len(grads)
         self.n, self.grads, self.outs = n, list(grads), None if outs is None else list(outs)
+        self.device = self.grads[0].get_device() if n else None
         self.ptrs = (C.c_void_p * max(1, n))(*[t.data_ptr() for t in grads])
         self.out_ptrs = None if outs is None else (C.c_void_p * max(1, n))(*[t.data_ptr() for t in outs])
         self.dtypes = (C.c_int32 * max(1, n))(*[DTYPES[t.dtype] for t in grads])
@@ -746,9 +755,12 @@ class GradList:
 def grad_list(grads: Sequence[torch.Tensor], outs: Optional[Sequence[torch.Tensor]] = None) -> GradList:
     """A list for ctr_clip_grads: dense fp32 or bf16 CUDA tensors, and where the clipped ones go
     (`grads` itself for in place; None for the norm alone)."""
+    devices = set()
     for t in list(grads) + list(outs or []):
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in DTYPES or not t.is_contiguous():
             raise ValueError("gradients must be contiguous fp32 or bf16 CUDA tensors")
+        devices.add(t.get_device())
+    _want(len(devices) <= 1, "gradients must be on one device")
     if outs is not None:
         _want(len(outs) == len(grads), "outs must be as many as grads")
         for g, o in zip(grads, outs):
@@ -762,8 +774,10 @@ def ctr_clip_grads_workspace_size() -> int:
 
 def ctr_clip_grads(grads: GradList, max_norm: float, norm: torch.Tensor, ws: torch.Tensor, stream=None) -> None:
     """The global norm of a grad_list into norm (fp32 [1]), and its outs = grads * min(1, max_norm / norm)."""
-    if stream is None and _took("ctr_clip_grads", _usual().clip_grads(*grads.addresses, grads.n, max_norm, norm, ws)):
+    if stream is None and _took("ctr_clip_grads", _usual().clip_grads(*grads.addresses, grads.n, grads.device, max_norm,
+                                                                      norm, ws)):
         return
+    _here(grads.device, "the list of gradients")
     _dense(norm, "norm", torch.float32, (1,))
     st = lib().ctr_clip_grads(*grads.addresses, grads.n, max_norm,
                               norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
