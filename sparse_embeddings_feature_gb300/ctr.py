@@ -465,6 +465,14 @@ def _dense(t: torch.Tensor, what: str, dtype, shape) -> None:
     raise ValueError(f"{what} must be a contiguous CUDA tensor of {dtype} and shape {tuple(shape)}")
 
 
+def _room(ws: torch.Tensor):
+    """(address, bytes) of a workspace: dense bytes on the current device."""
+    if isinstance(ws, torch.Tensor) and ws.is_cuda and ws.dtype is _U8 and ws.is_contiguous():
+        _here(ws.get_device(), "ws")
+        return ws.data_ptr(), ws.numel()
+    raise ValueError("ws must be a contiguous CUDA tensor of torch.uint8")
+
+
 def _want(ok: bool, what: str) -> None:
     if not ok:
         raise ValueError(what)
@@ -502,7 +510,7 @@ def ctr_expert_route(scores: torch.Tensor, k: int, renormalize: bool, expert: to
     _dense(offsets, "offsets", _I32, (E + 1,))
     st = lib().ctr_expert_route(scores.data_ptr(), DTYPES[scores.dtype], T, E, ld, k, 1 if renormalize else 0,
                                 expert.data_ptr(), weight.data_ptr(), slot.data_ptr(), token.data_ptr(),
-                                offsets.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+                                offsets.data_ptr(), *_room(ws), _stream(stream))
     if st:
         _ok("ctr_expert_route", st)
 
@@ -520,7 +528,7 @@ def ctr_expert_route_bwd(dweight: torch.Tensor, scores: torch.Tensor, renormaliz
     ldd = _like(dscores, "dscores", T, E, scores.dtype)
     st = lib().ctr_expert_route_bwd(dweight.data_ptr(), scores.data_ptr(), DTYPES[scores.dtype], T, E, ld, k,
                                     1 if renormalize else 0, expert.data_ptr(), dscores.data_ptr(), ldd,
-                                    ws.data_ptr(), ws.numel(), _stream(stream))
+                                    *_room(ws), _stream(stream))
     if st:
         _ok("ctr_expert_route_bwd", st)
 
@@ -543,7 +551,7 @@ def ctr_expert_dispatch(x: torch.Tensor, slot: torch.Tensor, token: torch.Tensor
     _dense(token, "token", _I32, (T * k,))
     ldo = _like(out, "out", T * k, d, x.dtype)
     st = lib().ctr_expert_dispatch(x.data_ptr(), DTYPES[x.dtype], T, d, ld, k, slot.data_ptr(), token.data_ptr(),
-                                   out.data_ptr(), ldo, ws.data_ptr(), ws.numel(), _stream(stream))
+                                   out.data_ptr(), ldo, *_room(ws), _stream(stream))
     if st:
         _ok("ctr_expert_dispatch", st)
 
@@ -559,7 +567,7 @@ def ctr_expert_combine(rows: torch.Tensor, slot: torch.Tensor, weight: Optional[
     if weight is not None:
         _dense(weight, "weight", _F32, (T, k))
     st = lib().ctr_expert_combine(rows.data_ptr(), DTYPES[y.dtype], T, d, ldr, k, slot.data_ptr(), _ptr(weight),
-                                  y.data_ptr(), ldy, ws.data_ptr(), ws.numel(), _stream(stream))
+                                  y.data_ptr(), ldy, *_room(ws), _stream(stream))
     if st:
         _ok("ctr_expert_combine", st)
 
@@ -579,7 +587,7 @@ def ctr_expert_combine_bwd(dy: torch.Tensor, rows: torch.Tensor, slot: torch.Ten
     _dense(token, "token", _I32, (T * k,))
     st = lib().ctr_expert_combine_bwd(dy.data_ptr(), DTYPES[dy.dtype], T, d, ldy, k, rows.data_ptr(), ldr,
                                       slot.data_ptr(), weight.data_ptr(), token.data_ptr(), drows.data_ptr(), ldd,
-                                      dweight.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+                                      dweight.data_ptr(), *_room(ws), _stream(stream))
     if st:
         _ok("ctr_expert_combine_bwd", st)
 
@@ -628,7 +636,7 @@ def ctr_fp8_quantize_rows(x: torch.Tensor, q: torch.Tensor, scale: torch.Tensor,
     rows = _codes_of(q, row_index, n, cols)
     lds = _like(scale, "scale", (cols + 127) // 128, rows, _F32)
     st = lib().ctr_fp8_quantize_rows(x.data_ptr(), DTYPES[x.dtype], n, rows, cols, ld, _ptr(row_index), q.data_ptr(),
-                                     scale.data_ptr(), lds, ws.data_ptr(), ws.numel(), _stream(stream))
+                                     scale.data_ptr(), lds, *_room(ws), _stream(stream))
     if st:
         _ok("ctr_fp8_quantize_rows", st)
 
@@ -652,7 +660,7 @@ def ctr_fp8_quantize_rows_cols(x: torch.Tensor, offsets: torch.Tensor, q: torch.
            else ((cols + 127) // 128, padded // 128))
     st = lib().ctr_fp8_quantize_rows_cols(x.data_ptr(), DTYPES[x.dtype], n, rows, cols, ld, _ptr(row_index),
                                           offsets.data_ptr(), groups, cols_by, q.data_ptr(), scale.data_ptr(), lds,
-                                          qc.data_ptr(), scale_c.data_ptr(), ws.data_ptr(), ws.numel(),
+                                          qc.data_ptr(), scale_c.data_ptr(), *_room(ws),
                                           _stream(stream))
     if st:
         _ok("ctr_fp8_quantize_rows_cols", st)
@@ -674,7 +682,7 @@ def ctr_fp8_quantize_blocks(w: torch.Tensor, q: torch.Tensor, scale: torch.Tenso
         _dense(qt, "qt", torch.uint8, (G, k, fp8_padded(n)))
         _dense(scale_t, "scale_t", torch.float32, (G, fp8_blocks(k), fp8_blocks(n)))
     st = lib().ctr_fp8_quantize_blocks(_ptr(w), DTYPES[w.dtype], G, n, k, _ptr(q), _ptr(scale), _ptr(qt),
-                                       _ptr(scale_t), _ptr(ws), ws.numel(), _stream(stream))
+                                       _ptr(scale_t), *_room(ws), _stream(stream))
     _ok("ctr_fp8_quantize_blocks", st)
 
 
@@ -695,7 +703,7 @@ def ctr_fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_sc
     if offsets is not None:
         _dense(offsets, "offsets", _I32, (G + 1,))
     st = lib().ctr_fp8_matmul(a.data_ptr(), a_scale.data_ptr(), lds, b.data_ptr(), b_scale.data_ptr(), _ptr(offsets),
-                              rows, G, n, kp, out.data_ptr(), DTYPES[out.dtype], ldo, ws.data_ptr(), ws.numel(),
+                              rows, G, n, kp, out.data_ptr(), DTYPES[out.dtype], ldo, *_room(ws),
                               _stream(stream))
     if st:
         _ok("ctr_fp8_matmul", st)
@@ -725,7 +733,7 @@ def ctr_fp8_matmul_wgrad(d: torch.Tensor, d_scale: torch.Tensor, x: torch.Tensor
     _dense(x_scale, "x_scale", torch.float32, (fp8_blocks(k), padded // 128))
     _dense(offsets, "offsets", torch.int32, (G + 1,))
     st = lib().ctr_fp8_matmul_wgrad(_ptr(d), _ptr(d_scale), _ptr(x), _ptr(x_scale), _ptr(offsets), rows, G, n, k,
-                                    _ptr(out), DTYPES[out.dtype], _ptr(ws), ws.numel(), _stream(stream))
+                                    _ptr(out), DTYPES[out.dtype], *_room(ws), _stream(stream))
     _ok("ctr_fp8_matmul_wgrad", st)
 
 
@@ -780,6 +788,6 @@ def ctr_clip_grads(grads: GradList, max_norm: float, norm: torch.Tensor, ws: tor
     _here(grads.device, "the list of gradients")
     _dense(norm, "norm", torch.float32, (1,))
     st = lib().ctr_clip_grads(*grads.addresses, grads.n, max_norm,
-                              norm.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
+                              norm.data_ptr(), *_room(ws), _stream(stream))
     if st:
         _ok("ctr_clip_grads", st)

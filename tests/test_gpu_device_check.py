@@ -1,4 +1,5 @@
-"""The expert layer's calls launch on the current device and refuse tensors of another one."""
+"""The expert layer's calls launch on the current device and refuse tensors of another one, and workspaces that are
+no dense bytes on it."""
 import pytest
 import torch
 
@@ -41,8 +42,10 @@ def _calls(T=8, E=4, k=2, d=16, n=32):
     }
 
 
-@pytest.mark.parametrize("name", ["route", "route_bwd", "dispatch", "combine", "combine_bwd", "rows", "rows_cols", "blocks",
-                                  "matmul", "wgrad", "clip"])
+NAMES = ["route", "route_bwd", "dispatch", "combine", "combine_bwd", "rows", "rows_cols", "blocks", "matmul", "wgrad", "clip"]
+
+
+@pytest.mark.parametrize("name", NAMES)
 def test_tensors_of_another_device_are_refused(name, monkeypatch):
     # with one GPU, another device is current as far as the checks can see
     calls, here = _calls(), torch.cuda.current_stream()
@@ -53,3 +56,18 @@ def test_tensors_of_another_device_are_refused(name, monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="cuda:1"):
         calls[name](here)
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_only_bytes_on_the_device_are_a_workspace(name):
+    calls = _calls()
+    wide = torch.zeros((1 << 20, 2), dtype=U8, device="cuda")
+    bad = (None, torch.zeros(1 << 20, dtype=U8), torch.zeros(1 << 20, dtype=I32, device="cuda"), wide[:, 0],
+           ctr.ctr_expert_workspace_size())
+    for stream in (None, torch.cuda.current_stream()):
+        for ws in bad:
+            with pytest.raises(ValueError, match="ws"):
+                calls[name](stream, ws)
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(ctr.CtrError):
+            calls[name](stream, torch.zeros(128, dtype=U8, device="cuda"))
