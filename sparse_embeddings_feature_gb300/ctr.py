@@ -521,7 +521,7 @@ def ctr_expert_route_bwd(dweight: torch.Tensor, scores: torch.Tensor, renormaliz
                 expert, dscores, ws)):
         return
     T, E, ld = _mat(scores, "scores")
-    _want(expert.dim() == 2, "expert must be a matrix")
+    _want(isinstance(expert, torch.Tensor) and expert.dim() == 2, "expert must be a matrix")
     k = expert.shape[1]
     _dense(expert, "expert", _I32, (T, k))
     _dense(dweight, "dweight", _F32, (T, k))
@@ -650,8 +650,8 @@ def ctr_fp8_quantize_rows_cols(x: torch.Tensor, offsets: torch.Tensor, q: torch.
         return
     n, cols, ld = _mat(x, "x")
     rows = _codes_of(q, row_index, n, cols)
+    _want(isinstance(offsets, torch.Tensor) and offsets.numel() >= 2, "offsets must have at least two entries")
     groups = offsets.numel() - 1
-    _want(groups >= 1, "offsets must have at least two entries")
     _dense(offsets, "offsets", _I32, (groups + 1,))
     padded = fp8_padded_rows(rows, groups)
     lds = _like(scale, "scale", (cols + 127) // 128, rows, _F32)
