@@ -587,7 +587,8 @@ extern "C" int ctr_fp8_quantize_rows_cols(const void* x, ctr_dtype dtype, int64_
     return CTR_ERR_INVALID_ARG;
   if (!offsets || (!row_index && rows > x_rows) || (cols_by_block != 0 && cols_by_block != 1))
     return CTR_ERR_INVALID_ARG;
-  if (rows > INT32_MAX || cols > INT32_MAX || groups > CTR_MAX_EXPERTS) return CTR_ERR_UNSUPPORTED;
+  // the kernel rounds a group's rows up to tiles in 32 bits; the products take no more rows either
+  if (rows > INT32_MAX - 65536 || cols > INT32_MAX || groups > CTR_MAX_EXPERTS) return CTR_ERR_UNSUPPORTED;
   if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
   if (rows == 0) return CTR_OK;
   const int eb = dtype_bytes(dtype);
