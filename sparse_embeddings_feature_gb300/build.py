@@ -3,7 +3,9 @@
 Each .cu file under csrc/ is compiled by nvcc in parallel, then linked with the
 static CUDA runtime into sparse_embeddings_feature_gb300/_build/libctr.so.
 csrc/calls.cpp, which reads the arguments of small calls from tensors, is compiled
-against the installed PyTorch into _build/ctr_calls.so.
+against the installed Python and PyTorch into _build/ctr_calls.so.  libctr needs
+neither: where that fails (no Python headers, say) there is a warning, and the
+binding in ctr.py serves every call.
 """
 from __future__ import annotations
 
@@ -14,6 +16,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -38,9 +42,7 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _calls_command(src: str, out: str):
-    import sysconfig
-
+def _calls_command(out: str):
     import torch
     home = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -48,19 +50,60 @@ def _calls_command(src: str, out: str):
             os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
             "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
-            *[a for d in dirs for a in ("-isystem", d)], src, "-o", out, "-L" + os.path.join(home, "lib"), "-L" + OUT_DIR,
+            *[a for d in dirs for a in ("-isystem", d)], os.path.join(CSRC, "calls.cpp"), "-o", out,
+            "-L" + os.path.join(home, "lib"), "-L" + OUT_DIR,
             "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-lctr", "-Wl,-rpath,$ORIGIN"]
 
 
-def _fingerprint(extra=()) -> str:
-    import torch
-    h = hashlib.sha256(torch.__version__.encode())
-    for p in sorted(glob.glob(os.path.join(CSRC, "*")) + [os.path.join(INCLUDE, "ctr.h"), __file__]):
+def _hash_files(h, paths) -> None:
+    for p in paths:
         with open(p, "rb") as f:
             h.update(p.encode())
             h.update(f.read())
+
+
+def _fingerprint(extra=()) -> str:
+    h = hashlib.sha256()
+    _hash_files(h, _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [os.path.join(INCLUDE, "ctr.h"), __file__])
     h.update(" ".join(ARCH + NVCC_FLAGS + list(extra)).encode())
     return h.hexdigest()
+
+
+def _calls_fingerprint() -> str:
+    """Of the extension's source, its compile command, and the PyTorch it is for."""
+    import torch
+    try:
+        command = _calls_command("")
+    except RuntimeError:      # no CUDA toolkit: nothing can be compiled, but what is there may be used
+        command = []
+    h = hashlib.sha256(repr((torch.__version__, command[:6])).encode())
+    _hash_files(h, [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "ctr.h")])
+    return h.hexdigest()
+
+
+def build_calls(force: bool = False):
+    """The extension's path, compiled if need be, or None where it cannot be (said once, by a warning)."""
+    stamp = os.path.join(OUT_DIR, "calls_fingerprint")
+    fp = _calls_fingerprint()
+    seen = open(stamp).read() if os.path.exists(stamp) else ""
+    if not force and seen == fp and os.path.exists(CALLS):
+        return CALLS
+    if not force and seen == fp + " failed":
+        return None
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    try:
+        r = subprocess.run(_calls_command(tmp), capture_output=True, text=True)
+        failed = f"{r.stdout}\n{r.stderr}" if r.returncode != 0 else ""
+    except (OSError, RuntimeError) as e:
+        failed = str(e)
+    if failed:
+        warnings.warn(f"calls.cpp was not compiled, the expert layer's calls read their arguments in Python:\n{failed}",
+                      RuntimeWarning)
+    else:
+        os.replace(tmp, CALLS)
+    with open(stamp, "w") as f:
+        f.write(fp + (" failed" if failed else ""))
+    return None if failed else CALLS
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -68,7 +111,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     stamp = os.path.join(OUT_DIR, "fingerprint")
     extra_flags = list(extra_flags or []) + os.environ.get("CTR_NVCC_EXTRA", "").split()
     fp = _fingerprint(extra_flags)
-    if not force and os.path.exists(LIB) and os.path.exists(CALLS) and os.path.exists(stamp) and open(stamp).read() == fp:
+    if not force and os.path.exists(LIB) and os.path.exists(stamp) and open(stamp).read() == fp:
+        build_calls()
         return LIB
     cc = nvcc()
     flags = ARCH + NVCC_FLAGS + extra_flags
@@ -92,13 +136,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    tmp = CALLS + ".tmp%d" % os.getpid()
-    r = subprocess.run(_calls_command(os.path.join(CSRC, "calls.cpp"), tmp), capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"calls.cpp failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
     with open(stamp, "w") as f:
         f.write(fp)
+    build_calls(force)
     return LIB
 
 

@@ -17,6 +17,7 @@ import importlib.machinery
 import importlib.util
 import os
 import threading
+import warnings
 from typing import Optional, Sequence
 
 import numpy as np
@@ -103,7 +104,7 @@ class CtrError(RuntimeError):
 
 def lib() -> C.CDLL:
     """Load libctr.so, building it first if the sources changed.  Raises if that fails."""
-    global _lib, _calls
+    global _lib
     if _lib is not None:
         return _lib
     with _lock:
@@ -116,17 +117,35 @@ def lib() -> C.CDLL:
                 fn = getattr(L, name)
                 fn.restype = res
                 fn.argtypes = args
-            loader = importlib.machinery.ExtensionFileLoader("ctr_calls", _build.CALLS)
-            calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("ctr_calls", loader))
-            loader.exec_module(calls)
-            _calls, _lib = calls, L
+            _lib = L
     return _lib
+
+
+class _NoCalls:
+    """In the place of csrc/calls.cpp where it cannot be compiled or loaded: takes no call."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
 
 
 def _usual():
     """The calls in their usual layouts (csrc/calls.cpp): each returns its status, or None if it did not take it."""
+    global _calls
     if _calls is None:
         lib()
+        with _lock:
+            path = _build.build_calls() if _calls is None else None
+            if path is not None:
+                try:
+                    loader = importlib.machinery.ExtensionFileLoader("ctr_calls", path)
+                    calls = importlib.util.module_from_spec(importlib.util.spec_from_loader("ctr_calls", loader))
+                    loader.exec_module(calls)
+                    _calls = calls
+                except ImportError as e:
+                    warnings.warn(f"{path} cannot be loaded, the expert layer's calls read their arguments in Python: {e}",
+                                  RuntimeWarning)
+            if _calls is None:
+                _calls = _NoCalls()
     return _calls
 
 
