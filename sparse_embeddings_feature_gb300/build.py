@@ -70,13 +70,13 @@ def _fingerprint(extra=()) -> str:
 
 
 def _calls_fingerprint() -> str:
-    """Of the extension's source, its compile command, and the PyTorch it is for."""
+    """Of the extension's source, its compile command, and the Python and PyTorch it is for."""
     import torch
     try:
         command = _calls_command("")
     except RuntimeError:      # no CUDA toolkit: nothing can be compiled, but what is there may be used
         command = []
-    h = hashlib.sha256(repr((torch.__version__, command[:6])).encode())
+    h = hashlib.sha256(repr((sys.version, sysconfig.get_config_var("SOABI"), torch.__version__, command[:6])).encode())
     _hash_files(h, [os.path.join(CSRC, "calls.cpp"), os.path.join(INCLUDE, "ctr.h")])
     return h.hexdigest()
 

@@ -1,6 +1,7 @@
 """The extension that reads the expert layer's arguments is built and loaded apart from libctr (CPU only)."""
 import os
 import shutil
+import sysconfig
 
 import pytest
 
@@ -43,3 +44,19 @@ def test_an_extension_that_cannot_be_loaded(place):
         f.write(b"not a library")
     with pytest.warns(RuntimeWarning, match="cannot be loaded"):
         assert ctr._usual().expert_route(1, 2) is None
+
+
+def test_the_extension_is_for_this_python(place, monkeypatch):
+    assert B.build_calls() == B.CALLS
+    made = os.stat(B.CALLS).st_mtime_ns
+    assert B.build_calls() == B.CALLS and os.stat(B.CALLS).st_mtime_ns == made
+    mine = B._calls_fingerprint()
+    var = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-399-other" if n == "SOABI" else var(n))
+    assert B._calls_fingerprint() != mine
+    monkeypatch.undo()
+    monkeypatch.setenv("CXX", "another-compiler")
+    assert B._calls_fingerprint() != mine
+    monkeypatch.undo()
+    monkeypatch.setattr("sys.version", "4.0")
+    assert B._calls_fingerprint() != mine
