@@ -442,7 +442,12 @@ int ctr_embedding_bag_bwd_update_opt(const float* grad_pooled, int64_t g_stride_
  * treated as if A were empty, and flagged CTR_ERR_BAD_VALUE.
  * Outputs: expert int32, weight fp32, slot int32 [tokens, k] (dense), token
  * int32 [tokens*k], offsets int32 [experts + 1].
- * Workspace: ctr_expert_route_workspace_size(tokens, experts, k) bytes. */
+ * Workspace: ctr_expert_route_workspace_size(tokens, experts, k) bytes.
+ * Batches of 257 to 4096 tokens (and smaller ones of many experts) run as one
+ * thread-block cluster where the device can place one of 16 blocks, else as
+ * three launches like larger ones; ctr_set_route_cluster(0) takes the three
+ * always (diagnostics; process-wide, returns the previous setting). */
+int ctr_set_route_cluster(int on);
 size_t ctr_expert_route_workspace_size(int64_t tokens, int32_t experts, int32_t k);
 int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, int64_t ld_scores,
                      int32_t k, int renormalize, int32_t* expert, float* weight, int32_t* slot, int32_t* token,

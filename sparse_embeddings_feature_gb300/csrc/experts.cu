@@ -18,7 +18,7 @@
 // Three launches: choices + tile counts; exclusive sums of the counts over the
 // tiles (one warp column per expert); ranks and the two maps.  Up to kTileTokens
 // x 16 tokens run as one launch, a block or a cluster of up to sixteen blocks that
-// read each other's counts (2048 x 26, k 4: 6.1 us).
+// read each other's counts (2048 x 26, k 4: 6.1 us), where the device can place it.
 //
 // Rows.  A token's group of lanes reads its row once and writes its k rows (or
 // reads k rows and writes one): every byte crosses HBM once, and rows of 1 KB
@@ -633,20 +633,49 @@ int check_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t exp
   return CTR_OK;
 }
 
+std::atomic<int> g_route_cluster{1};  // ctr_set_route_cluster
+
+// Whether the current device can place the kernel's largest cluster, asked once for each device: clusters of more
+// than eight blocks are not portable, and a process may be given part of a GPU.
+template <auto k>
+bool largest_cluster_fits() {
+  static std::atomic<uint64_t> asked{0}, fits{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  const uint64_t bit = 1ull << dev;
+  if (!(asked.load(std::memory_order_acquire) & bit)) {
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = kClusterTiles;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kClusterTiles);
+    cfg.blockDim = dim3(kRouteThreads);
+    cfg.dynamicSmemBytes = route_smem(CTR_MAX_EXPERTS, kTileTokens);
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) == cudaSuccess && clusters > 0)
+      fits.fetch_or(bit, std::memory_order_relaxed);
+    else
+      cudaGetLastError();  // not a failure of this call
+    asked.fetch_or(bit, std::memory_order_release);
+  }
+  return (fits.load(std::memory_order_relaxed) & bit) != 0;
+}
+
+// cluster: whether one is wanted, then whether the launch was one.
 template <typename T, int EPL, int KMAX>
-bool launch_choose(const RouteArgs& a, size_t smem, bool cluster, cudaStream_t s) {
+bool launch_choose(const RouteArgs& a, size_t smem, bool& cluster, cudaStream_t s) {
+  cluster = cluster && largest_cluster_fits<route_choose_kernel<T, EPL, KMAX, true>>();
   auto k = cluster ? route_choose_kernel<T, EPL, KMAX, true> : route_choose_kernel<T, EPL, KMAX, false>;
-  static std::atomic<uint64_t> ready{0};
-  if (cluster && !once_per_device(ready, [&] {
-        return cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-      }))
-    return false;
   return launch_after(k, dim3((unsigned)a.tiles), kRouteThreads, smem, s, cluster ? (unsigned)a.tiles : 1u, a) ==
          cudaSuccess;
 }
 
 template <typename T, int EPL>
-bool launch_choose(const RouteArgs& a, size_t smem, bool cluster, cudaStream_t s) {
+bool launch_choose(const RouteArgs& a, size_t smem, bool& cluster, cudaStream_t s) {
   return a.k <= 4 ? launch_choose<T, EPL, 4>(a, smem, cluster, s)
                   : launch_choose<T, EPL, CTR_MAX_CHOICES>(a, smem, cluster, s);
 }
@@ -895,6 +924,8 @@ extern "C" size_t ctr_expert_route_workspace_size(int64_t tokens, int32_t expert
   return z.used;
 }
 
+extern "C" int ctr_set_route_cluster(int on) { return g_route_cluster.exchange(on ? 1 : 0); }
+
 extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts,
                                 int64_t ld_scores, int32_t k, int renormalize, int32_t* expert, float* weight,
                                 int32_t* slot, int32_t* token, int32_t* offsets, void* ws, size_t ws_bytes,
@@ -930,7 +961,7 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   a.counts = c.take<int32_t>((size_t)(a.tiles + 1) * experts);
   a.err = (int*)ws;
   const size_t smem = route_smem(experts, a.tile);
-  const bool cluster = a.tiles > 1 && a.tiles <= kClusterTiles;
+  bool cluster = a.tiles > 1 && a.tiles <= kClusterTiles && g_route_cluster.load(std::memory_order_relaxed) != 0;
   const bool ok = dtype == CTR_F32 ? (per == 8 ? launch_choose<float, 8>(a, smem, cluster, s)
                                                : launch_choose<float, 16>(a, smem, cluster, s))
                                    : (per == 8 ? launch_choose<__nv_bfloat16, 8>(a, smem, cluster, s)

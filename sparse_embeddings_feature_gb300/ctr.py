@@ -75,6 +75,7 @@ _SIGS = {
     "ctr_dot_interaction_bwd_mode": (C.c_int, [_p, _p, _i32, _i32, _i32, C.c_int, _p, _p, _sz, _p]),
     "ctr_embedding_bag_bwd_update_phases": (C.c_int, [_p, _i64, _i64, _p, _i32, _i32, C.c_int, _p, _p, _p, _p, _i64,
                                                       _f32, _p, C.c_int, _i32, _i64, _p, C.c_int, _p, _sz, _p]),
+    "ctr_set_route_cluster": (C.c_int, [C.c_int]),
     "ctr_expert_route_workspace_size": (_sz, [_i64, _i32, _i32]),
     "ctr_expert_route": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _i32, C.c_int, _p, _p, _p, _p, _p, _p, _sz, _p]),
     "ctr_expert_route_bwd": (C.c_int, [_p, _p, C.c_int, _i64, _i32, _i64, _i32, C.c_int, _p, _p, _i64, _p, _sz, _p]),
@@ -511,6 +512,12 @@ def ctr_expert_workspace_size() -> int:
 
 def ctr_expert_route_workspace_size(tokens: int, experts: int, k: int) -> int:
     return int(lib().ctr_expert_route_workspace_size(tokens, experts, k))
+
+
+def ctr_set_route_cluster(on: bool) -> bool:
+    """Routing of mid-sized batches as one thread-block cluster (the default) or always as three launches;
+    returns the previous setting."""
+    return bool(lib().ctr_set_route_cluster(1 if on else 0))
 
 
 def ctr_expert_route(scores: torch.Tensor, k: int, renormalize: bool, expert: torch.Tensor, weight: torch.Tensor,
