@@ -94,6 +94,16 @@ Workspace workspace(PyObject* o) {
 ctr_stream_t stream() { return (ctr_stream_t)c10::cuda::getCurrentCUDAStream().stream(); }
 int64_t blocks(int64_t n) { return (n + 127) / 128; }
 
+// Calls a C entry point without the interpreter's lock: a launch waits while the stream's queue is full, and other
+// threads' Python is not to.  The arguments, which may refuse, are read before.
+template <typename F, typename... A>
+int free_of_lock(F f, A... args) {
+  PyThreadState* state = PyEval_SaveThread();
+  const int st = f(args...);
+  PyEval_RestoreThread(state);
+  return st;
+}
+
 // Runs a call and gives its status, or None.
 template <int N, typename F>
 PyObject* run(Py_ssize_t n, F&& call) {
@@ -119,9 +129,9 @@ CALL(expert_route) {
     const int renorm = PyObject_IsTrue(a[2]);
     if (k < 1 || k > E || renorm < 0) throw Odd();
     const Workspace w = workspace(a[8]);
-    return ctr_expert_route(s.p, s.type, T, (int32_t)E, s.ld(), (int32_t)k, renorm, ints(a[3], {T, k}),
-                            floats(a[4], {T, k}), ints(a[5], {T, k}), ints(a[6], {T * k}), ints(a[7], {E + 1}), w.p, w.n,
-                            stream());
+    return free_of_lock(ctr_expert_route, s.p, s.type, T, (int32_t)E, s.ld(), (int32_t)k, renorm, ints(a[3], {T, k}),
+                        floats(a[4], {T, k}), ints(a[5], {T, k}), ints(a[6], {T * k}), ints(a[7], {E + 1}), w.p, w.n,
+                        stream());
   });
 }
 
@@ -133,8 +143,8 @@ CALL(expert_route_bwd) {
     const int renorm = PyObject_IsTrue(a[2]);
     if (d.n[0] != T || d.n[1] != E || d.scalar != s.scalar || k > E || renorm < 0) throw Odd();
     const Workspace w = workspace(a[5]);
-    return ctr_expert_route_bwd(floats(a[0], {T, k}), s.p, s.type, T, (int32_t)E, s.ld(), (int32_t)k, renorm,
-                                ints(a[3], {T, k}), d.p, d.ld(), w.p, w.n, stream());
+    return free_of_lock(ctr_expert_route_bwd, floats(a[0], {T, k}), s.p, s.type, T, (int32_t)E, s.ld(), (int32_t)k,
+                        renorm, ints(a[3], {T, k}), d.p, d.ld(), w.p, w.n, stream());
   });
 }
 
@@ -145,8 +155,8 @@ CALL(expert_dispatch) {
     const int64_t T = x.n[0], d = x.n[1], k = size(a[1], 2, 1);
     if (o.n[0] != T * k || o.n[1] != d || o.scalar != x.scalar || d > INT32_MAX || k > INT32_MAX) throw Odd();
     const Workspace w = workspace(a[4]);
-    return ctr_expert_dispatch(x.p, x.type, T, (int32_t)d, x.ld(), (int32_t)k, ints(a[1], {T, k}), ints(a[2], {T * k}),
-                               o.p, o.ld(), w.p, w.n, stream());
+    return free_of_lock(ctr_expert_dispatch, x.p, x.type, T, (int32_t)d, x.ld(), (int32_t)k, ints(a[1], {T, k}),
+                        ints(a[2], {T * k}), o.p, o.ld(), w.p, w.n, stream());
   });
 }
 
@@ -157,8 +167,8 @@ CALL(expert_combine) {
     const int64_t T = y.n[0], d = y.n[1], k = size(a[1], 2, 1);
     if (r.n[0] != T * k || r.n[1] != d || r.scalar != y.scalar || d > INT32_MAX || k > INT32_MAX) throw Odd();
     const Workspace w = workspace(a[4]);
-    return ctr_expert_combine(r.p, r.type, T, (int32_t)d, r.ld(), (int32_t)k, ints(a[1], {T, k}),
-                              floats(a[2], {T, k}, true), y.p, y.ld(), w.p, w.n, stream());
+    return free_of_lock(ctr_expert_combine, r.p, r.type, T, (int32_t)d, r.ld(), (int32_t)k, ints(a[1], {T, k}),
+                        floats(a[2], {T, k}, true), y.p, y.ld(), w.p, w.n, stream());
   });
 }
 
@@ -171,9 +181,9 @@ CALL(expert_combine_bwd) {
       if (v.n[0] != T * k || v.n[1] != d || v.scalar != y.scalar) throw Odd();
     if (d > INT32_MAX || k > INT32_MAX) throw Odd();
     const Workspace w = workspace(a[7]);
-    return ctr_expert_combine_bwd(y.p, y.type, T, (int32_t)d, y.ld(), (int32_t)k, r.p, r.ld(), ints(a[2], {T, k}),
-                                  floats(a[3], {T, k}), ints(a[4], {T * k}), o.p, o.ld(), floats(a[6], {T, k}), w.p, w.n,
-                                  stream());
+    return free_of_lock(ctr_expert_combine_bwd, y.p, y.type, T, (int32_t)d, y.ld(), (int32_t)k, r.p, r.ld(),
+                        ints(a[2], {T, k}), floats(a[3], {T, k}), ints(a[4], {T * k}), o.p, o.ld(),
+                        floats(a[6], {T, k}), w.p, w.n, stream());
   });
 }
 
@@ -184,9 +194,9 @@ CALL(fp8_quantize_rows) {
     const int64_t cols = x.n[1], rows = size(a[1], 2, 0), kb = blocks(cols);
     if (a[4] == Py_None && rows > x.n[0]) throw Odd();
     const Workspace w = workspace(a[3]);
-    return ctr_fp8_quantize_rows(x.p, x.type, x.n[0], rows, cols, x.ld(), ints(a[4], {rows}, true),
-                                 bytes(a[1], {rows, kb * 128}), floats(a[2], {kb, rows}), rows > 0 ? rows : 1, w.p, w.n,
-                                 stream());
+    return free_of_lock(ctr_fp8_quantize_rows, x.p, x.type, x.n[0], rows, cols, x.ld(), ints(a[4], {rows}, true),
+                        bytes(a[1], {rows, kb * 128}), floats(a[2], {kb, rows}), rows > 0 ? rows : 1, w.p, w.n,
+                        stream());
   });
 }
 
@@ -201,10 +211,10 @@ CALL(fp8_quantize_rows_cols) {
     const int64_t padded = ctr_fp8_padded_rows(rows, (int32_t)groups);
     float* sc = by_block ? floats(a[5], {kb, padded / 128}) : floats(a[5], {padded / 128, cols});
     const Workspace w = workspace(a[7]);
-    return ctr_fp8_quantize_rows_cols(x.p, x.type, x.n[0], rows, cols, x.ld(), ints(a[8], {rows}, true),
-                                      ints(a[1], {groups + 1}), (int32_t)groups, (int)by_block,
-                                      bytes(a[2], {rows, kb * 128}), floats(a[3], {kb, rows}), rows > 0 ? rows : 1,
-                                      bytes(a[4], {cols, padded}), sc, w.p, w.n, stream());
+    return free_of_lock(ctr_fp8_quantize_rows_cols, x.p, x.type, x.n[0], rows, cols, x.ld(), ints(a[8], {rows}, true),
+                        ints(a[1], {groups + 1}), (int32_t)groups, (int)by_block, bytes(a[2], {rows, kb * 128}),
+                        floats(a[3], {kb, rows}), rows > 0 ? rows : 1, bytes(a[4], {cols, padded}), sc, w.p, w.n,
+                        stream());
   });
 }
 
@@ -215,9 +225,9 @@ CALL(fp8_quantize_blocks) {
     const int64_t G = v.n[0], r = v.n[1], k = v.n[2], nb = blocks(r), kb = blocks(k);
     if (G > INT32_MAX || (a[4] == Py_None) != (a[5] == Py_None)) throw Odd();
     const Workspace w = workspace(a[3]);
-    return ctr_fp8_quantize_blocks(v.p, v.type, (int32_t)G, r, k, bytes(a[1], {G, r, kb * 128}), floats(a[2], {G, nb, kb}),
-                                   bytes(a[4], {G, k, nb * 128}, true), floats(a[5], {G, kb, nb}, true), w.p, w.n,
-                                   stream());
+    return free_of_lock(ctr_fp8_quantize_blocks, v.p, v.type, (int32_t)G, r, k, bytes(a[1], {G, r, kb * 128}),
+                        floats(a[2], {G, nb, kb}), bytes(a[4], {G, k, nb * 128}, true),
+                        floats(a[5], {G, kb, nb}, true), w.p, w.n, stream());
   });
 }
 
@@ -228,9 +238,9 @@ CALL(fp8_matmul) {
     const int64_t rows = o.n[0], cols = o.n[1], G = size(a[2], 3, 0), kp = size(a[2], 3, 2), kb = kp / 128;
     if (kp < 128 || kp % 128 || G > INT32_MAX) throw Odd();
     const Workspace w = workspace(a[6]);
-    return ctr_fp8_matmul(bytes(a[0], {rows, kp}), floats(a[1], {kb, rows}), rows > 0 ? rows : 1, bytes(a[2], {G, cols, kp}),
-                          floats(a[3], {G, blocks(cols), kb}), ints(a[4], {G + 1}, true), rows, (int32_t)G, cols, kp, o.p,
-                          o.type, o.ld(), w.p, w.n, stream());
+    return free_of_lock(ctr_fp8_matmul, bytes(a[0], {rows, kp}), floats(a[1], {kb, rows}), rows > 0 ? rows : 1,
+                        bytes(a[2], {G, cols, kp}), floats(a[3], {G, blocks(cols), kb}), ints(a[4], {G + 1}, true),
+                        rows, (int32_t)G, cols, kp, o.p, o.type, o.ld(), w.p, w.n, stream());
   });
 }
 
@@ -243,9 +253,9 @@ CALL(fp8_matmul_wgrad) {
     const int64_t rows = a[7] != Py_None ? number(a[7]) : most > tiles ? most : tiles;
     if (G < 1 || G > INT32_MAX || rows < 0 || ctr_fp8_padded_rows(rows, (int32_t)G) != padded) throw Odd();
     const Workspace w = workspace(a[6]);
-    return ctr_fp8_matmul_wgrad(bytes(a[0], {r, padded}), floats(a[1], {padded / 128, r}), bytes(a[2], {k, padded}),
-                                floats(a[3], {blocks(k), padded / 128}), ints(a[4], {G + 1}), rows, (int32_t)G, r, k, o.p,
-                                o.type, w.p, w.n, stream());
+    return free_of_lock(ctr_fp8_matmul_wgrad, bytes(a[0], {r, padded}), floats(a[1], {padded / 128, r}),
+                        bytes(a[2], {k, padded}), floats(a[3], {blocks(k), padded / 128}), ints(a[4], {G + 1}), rows,
+                        (int32_t)G, r, k, o.p, o.type, w.p, w.n, stream());
   });
 }
 
@@ -256,8 +266,9 @@ CALL(clip_grads) {
     const int64_t counts = number(a[3]), tensors = number(a[4]);
     if (!PyFloat_Check(a[6]) || tensors > INT32_MAX || (a[5] != Py_None && number(a[5]) != device)) throw Odd();
     const Workspace w = workspace(a[8]);
-    return ctr_clip_grads((const void* const*)grads, (void* const*)outs, (const int32_t*)types, (const int64_t*)counts,
-                          (int32_t)tensors, (float)PyFloat_AS_DOUBLE(a[6]), floats(a[7], {1}), w.p, w.n, stream());
+    return free_of_lock(ctr_clip_grads, (const void* const*)grads, (void* const*)outs, (const int32_t*)types,
+                        (const int64_t*)counts, (int32_t)tensors, (float)PyFloat_AS_DOUBLE(a[6]), floats(a[7], {1}),
+                        w.p, w.n, stream());
   });
 }
 
