@@ -539,7 +539,10 @@ int ctr_fp8_quantize_blocks(const void* w, ctr_dtype dtype, int32_t groups, int6
  * row codes (a, [rows, P(k)]) and block codes (b, [groups, n, P(k)]) stand for,
  *   out[r, i] = sum over c < k of a[r, c] b[g, i, c],
  * blocks of 128 summed by the tensor cores in fp32, the blocks' sums scaled and
- * added in fp32, one rounding to out_dtype.  offsets as above; NULL means that
+ * added in fp32, one rounding to out_dtype (a row's and a block's scale are
+ * multiplied first: a product of theirs that is no normal fp32 number, as of
+ * blocks whose largest magnitudes multiply to less than 2.4e-33, loses bits, and
+ * one that overflows gives infinities or NaN).  offsets as above; NULL means that
  * all rows are group 0 (groups = 1).  Rows past offsets[groups] get zeros.
  * out [rows, n], row stride ldo.  Device errors: CTR_ERR_BAD_OFFSETS (zeros are
  * written), CTR_ERR_TIMEOUT.  The input gradient of out = W x is the same call

@@ -10,8 +10,8 @@
 // bf16 scores carry their index in the low half of an ordered 32-bit key, so that
 // integer maxima and minima are all it takes; three or four choices come from
 // sorting networks (131072 x 64, k 4, with the order: 36 us before, 26 with both).
-// Then lane j has choice j, its exponential and its stores.  Bound by instruction
-// issue.  The stable order by expert is a counting sort without atomics on
+// Then lane j has choice j, its exponential and its stores.  Bound by latency and
+// issue (0.57 of the cycles issue, 41% of the warps are active).  The stable order by expert is a counting sort without atomics on
 // counts: a block's tile of up to 256 tokens is a bit matrix [expert][token]
 // in shared memory, so a choice's rank within the tile is a population count
 // of the bits before it, and the tile's count of an expert the count of all.

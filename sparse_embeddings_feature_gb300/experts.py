@@ -31,7 +31,8 @@ class ExpertLayer:
 
     x and y are fp32 or bf16 (`dtype`); rows of x may be strided.  With `train`, forward keeps what
     backward needs, a copy of the scores with it: backward(dy) returns (dx, dscores, dw) for the latest
-    forward, whatever became of its arguments.  Its calls run on the current device, which has to be
+    forward, whatever became of its arguments.  Results are the layer's own buffers, which the next call
+    writes.  Its calls run on the current device, which has to be
     `device`."""
 
     def __init__(self, tokens: int, width: int, out_width: int, experts: int, k: int, dtype=torch.float32,
