@@ -581,6 +581,48 @@ int ctr_clip_grads(const void* const* grads, void* const* outs, const int32_t* d
                    int32_t n_tensors, float max_norm, float* norm, void* ws, size_t ws_bytes, ctr_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* c. Layers around the experts                                               */
+/* ------------------------------------------------------------------------ */
+/* Source: "DHEN" notes, section 2.2 (a layer's output is Norm(Ensemble(...) +
+ * ShortCut)) and the mixture-of-experts section; "Meta DLRM", section 02 (the
+ * dense stacks below and above the interaction).  The pages give no shapes and
+ * no norm; the formulas below are this library's.  Matrices, types, alignment
+ * and NULL pointers as in section b. */
+
+/* ---- Root-mean-square norm on a residual stream ------------------------- */
+/* For each row:
+ *   s = x + residual, rounded to the rows' type (s = x where residual is NULL)
+ *   v = s / sqrt(mean(s^2) + eps) * gamma        (fp32; gamma NULL: all 1)
+ *   y = v in the rows' type (optional), and/or its row codes q [rows, P(d)]
+ *       (dense) with scale [B(d), ld_scale]: the left operand of ctr_fp8_matmul,
+ *       as ctr_fp8_quantize_rows would write it for v
+ * s is written where it is wanted (the stream's new value).  x, residual, s and
+ * y are [rows, d] of `dtype`; gamma is fp32 [d].  s and y may be x or residual
+ * themselves (the same rows and stride); nothing else may overlap.  One of y and
+ * q is needed; q and scale go together.  eps > 0.  Squares that leave fp32's
+ * range do not: such a row is summed again with scaled values.  A row with a NaN
+ * or an infinity gets what the formula gives (NaN among it), other rows do not
+ * see it.  d up to CTR_MAX_NORM_WIDTH.
+ * Workspace: of ctr_rms_norm_workspace_size(rows, d) bytes ctr_rms_norm takes the
+ * first 256 alone, ctr_rms_norm_bwd all of them for dgamma. */
+#define CTR_MAX_NORM_WIDTH 16384
+size_t ctr_rms_norm_workspace_size(int64_t rows, int32_t d);
+int ctr_rms_norm(const void* x, ctr_dtype dtype, int64_t rows, int32_t d, int64_t ldx, const void* residual,
+                 int64_t ld_residual, const float* gamma, float eps, void* s, int64_t ld_s, void* y, int64_t ld_y,
+                 uint8_t* q, float* scale, int64_t ld_scale, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* Its gradient.  With u = s / sqrt(mean(s^2) + eps), g = dy gamma and ds the
+ * gradient that arrives on the stream (optional):
+ *   dx = ds + (g - u mean(g u)) / sqrt(mean(s^2) + eps)
+ * the gradient of s, and so of x and of the residual; in the rows' type.
+ *   dgamma = sum over rows of dy u     (fp32 [d]; optional; zeros of no rows)
+ * in a fixed order.  s is what the forward wrote (x without a residual), gamma
+ * and eps as there.  dx may be dy, ds or s themselves. */
+int ctr_rms_norm_bwd(const void* dy, ctr_dtype dtype, int64_t rows, int32_t d, int64_t ld_dy, const void* ds,
+                     int64_t ld_ds, const void* s, int64_t ld_s, const float* gamma, float eps, void* dx,
+                     int64_t ld_dx, float* dgamma, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* Allocation-free dedup (no counterpart in the paper)                       */
 /* ------------------------------------------------------------------------ */
 /* ctr_dedup for callers that may not allocate device memory on this path: a

@@ -272,11 +272,52 @@ CALL(clip_grads) {
   });
 }
 
+// fp32 or bf16 values [rows, cols] of the given type; NULL for None.
+void* like(PyObject* o, at::ScalarType type, int64_t rows, int64_t cols) {
+  if (o == Py_None) return nullptr;
+  const Values v = values(o, 2);
+  if (v.n[0] != rows || v.n[1] != cols || v.scalar != type) throw Odd();
+  return v.p;
+}
+
+float number_f32(PyObject* o) {
+  if (!PyFloat_Check(o)) throw Odd();
+  return (float)PyFloat_AS_DOUBLE(o);
+}
+
+// x, residual, gamma, eps, s, y, q, scale, ws
+CALL(rms_norm) {
+  return run<9>(n, [&] {
+    const Values x = values(a[0], 2);
+    const int64_t rows = x.n[0], d = x.n[1], kb = blocks(d), ld = x.ld();
+    if (d > INT32_MAX || (a[6] == Py_None) != (a[7] == Py_None)) throw Odd();
+    const Workspace w = workspace(a[8]);
+    return free_of_lock(ctr_rms_norm, x.p, x.type, rows, (int32_t)d, ld, like(a[1], x.scalar, rows, d), ld,
+                        floats(a[2], {d}, true), number_f32(a[3]), like(a[4], x.scalar, rows, d), ld,
+                        like(a[5], x.scalar, rows, d), ld, bytes(a[6], {rows, kb * 128}, true),
+                        floats(a[7], {kb, rows}, true), rows > 0 ? rows : 1, w.p, w.n, stream());
+  });
+}
+
+// dy, ds, s, gamma, eps, dx, dgamma, ws
+CALL(rms_norm_bwd) {
+  return run<8>(n, [&] {
+    const Values y = values(a[0], 2);
+    const int64_t rows = y.n[0], d = y.n[1], ld = y.ld();
+    if (d > INT32_MAX || a[2] == Py_None || a[5] == Py_None) throw Odd();
+    const Workspace w = workspace(a[7]);
+    return free_of_lock(ctr_rms_norm_bwd, y.p, y.type, rows, (int32_t)d, ld, like(a[1], y.scalar, rows, d), ld,
+                        like(a[2], y.scalar, rows, d), ld, floats(a[3], {d}, true), number_f32(a[4]),
+                        like(a[5], y.scalar, rows, d), ld, floats(a[6], {d}, true), w.p, w.n, stream());
+  });
+}
+
 #define ENTRY(name) {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(expert_route),          ENTRY(expert_route_bwd),   ENTRY(expert_dispatch),
                          ENTRY(expert_combine),        ENTRY(expert_combine_bwd), ENTRY(fp8_quantize_rows),
                          ENTRY(fp8_quantize_rows_cols), ENTRY(fp8_quantize_blocks), ENTRY(fp8_matmul),
-                         ENTRY(fp8_matmul_wgrad),      ENTRY(clip_grads),         {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(fp8_matmul_wgrad),      ENTRY(clip_grads),
+                         ENTRY(rms_norm),              ENTRY(rms_norm_bwd),       {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ctr_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

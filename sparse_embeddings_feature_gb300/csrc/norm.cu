@@ -1,0 +1,473 @@
+// c1. Root-mean-square norm on a residual stream, its 8-bit codes, and its gradient.
+//
+// Source: "DHEN" notes, section 2.2 (a layer's output is Norm(Ensemble(...) +
+// ShortCut)); the page names no norm, the formulas are stated in include/ctr.h.
+//
+// A row is held in registers by a group of lanes (8 lanes up to 128 columns, a
+// warp up to 1024, up to 16 warps beyond), read once and written once: sum, sum of
+// squares, result and codes need no second pass.  A warp owns a contiguous run of
+// 32 EPT columns, so that a block of 128 columns never crosses warps and its
+// largest magnitude is a few shuffles.  Sums are fp32; bound by HBM.
+//
+// Backward.  With u = s rstd:  dx = ds + rstd (g - u mean(g u)), g = dy gamma, and
+// dgamma = sum over rows of dy u.  A block walks rows with its columns' sums in
+// registers, adds its warps' up through shared memory in their order, and leaves
+// one partial row; a second kernel adds those in their order.  No atomics, so the
+// result is the same in every run.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "codes.cuh"
+#include "common.cuh"
+#include "rows.cuh"
+
+namespace ctr {
+namespace {
+
+constexpr int kNormMaxCols = CTR_MAX_NORM_WIDTH;  // 16 warps of 1024 columns
+static_assert(kNormMaxCols <= 16 * 1024, "a row has 16 warps at most");
+constexpr int kNormParts = 304;      // blocks of the backward, at most: two an SM of 152
+constexpr int kJoinCols = 32, kJoinRows = 16;
+
+struct NormArgs {
+  const void* x;
+  const void* residual;  // forward: NULL without; backward: the gradient that arrives on the stream
+  const void* dy;        // backward
+  const float* gamma;    // NULL: all 1
+  void* s;               // NULL: not wanted
+  void* y;               // forward: NULL for codes alone; backward: dx
+  uint8_t* q;
+  float* scale;
+  float* part;           // backward: partial sums of dgamma
+  int64_t rows, ldx, ldr, lds, ldy, ld_dy, ld_scale;
+  int32_t d, qcols, wpr; // qcols: d rounded up to blocks; wpr: warps to a row
+  int32_t gvec;          // gamma is 16-byte aligned
+  float eps;
+};
+
+// Where a thread's elements are: chunk c of a lane holds columns col(c) .. col(c) + n - 1.
+template <int N, int LANES, int EPT>
+struct Place {
+  static constexpr int span = LANES * EPT;  // columns of a lane group
+  int first, sub;
+  __device__ __forceinline__ Place(int warp_in_row, int lane)
+      : first(warp_in_row * span + (lane & (LANES - 1)) * N), sub(lane & (LANES - 1)) {}
+  __device__ __forceinline__ int col(int c) const { return first + c * (LANES * N); }
+};
+
+template <typename T, int VB, int EPT, typename P>
+__device__ __forceinline__ void load_row(const P& at, const T* row, int d, bool mine, float (&f)[EPT]) {
+  using C = Chunk<T, VB>;
+  typename C::Raw raw[EPT / C::n];
+#pragma unroll
+  for (int c = 0; c < EPT / C::n; ++c) {
+    raw[c] = typename C::Raw{};
+    if (mine && at.col(c) < d) raw[c] = *(const typename C::Raw*)(row + at.col(c));
+  }
+#pragma unroll
+  for (int c = 0; c < EPT / C::n; ++c) {
+    float v[C::n];
+    C::unpack(raw[c], v);
+#pragma unroll
+    for (int i = 0; i < C::n; ++i) f[c * C::n + i] = v[i];
+  }
+}
+
+template <typename T, int VB, int EPT, typename P>
+__device__ __forceinline__ void store_row(const P& at, T* row, int d, const float (&f)[EPT]) {
+  using C = Chunk<T, VB>;
+#pragma unroll
+  for (int c = 0; c < EPT / C::n; ++c) {
+    float v[C::n];
+#pragma unroll
+    for (int i = 0; i < C::n; ++i) v[i] = f[c * C::n + i];
+    if (at.col(c) < d) *(typename C::Raw*)(row + at.col(c)) = C::pack(v);
+  }
+}
+
+// gamma's values at a thread's columns; 1 without a gamma.
+template <int N, int EPT, typename P>
+__device__ __forceinline__ void load_gamma(const P& at, const NormArgs& a, float (&g)[EPT]) {
+#pragma unroll
+  for (int c = 0; c < EPT / N; ++c) {
+    if (a.gamma && at.col(c) < a.d) {
+      if (N >= 4 && a.gvec) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+          const float4 v = *(const float4*)(a.gamma + at.col(c) + i);
+          const float w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4 && i + j < N; ++j) g[c * N + i + j] = w[j];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[c * N + i] = a.gamma[at.col(c) + i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) g[c * N + i] = 1.f;
+    }
+  }
+}
+
+// Sum over a row's lanes, the same in all of them.  wpr > 1: `sums` has a word a warp, and every thread of
+// the block calls.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, int wpr, float* sums) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
+  if (wpr > 1) {
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) sums[warp] = v;
+    __syncthreads();
+    v = 0.f;
+    const int first = warp & ~(wpr - 1);
+    for (int w = 0; w < wpr; ++w) v += sums[first + w];
+    __syncthreads();
+  }
+  return v;
+}
+
+// 1 / sqrt(mean(f^2) + eps) over a row.  Squares that leave fp32's range (or all but do, against a small eps)
+// are taken again of scaled values; a NaN or an infinity in the row gives NaN or 0, and NaN results.
+template <int LANES, int EPT>
+__device__ __forceinline__ float row_rstd(const float (&f)[EPT], const NormArgs& a, float* sums) {
+  float sq = 0.f;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) sq = fmaf(f[i], f[i], sq);
+  sq = row_sum<LANES>(sq, a.wpr, sums);
+  const float mean = sq / (float)a.d + a.eps;
+  float rstd = 1.f / sqrtf(mean);
+  // with several warps to a row every thread of the block takes part, or none
+  const bool odd = !(mean < 1e37f) || mean < 1e-30f;
+  if (a.wpr > 1 ? __syncthreads_or(odd) : __any_sync(kFull, odd)) {
+    const float by = mean < 1e-30f ? 0x1p70f : 0x1p-70f;
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) t = fmaf(f[i] * by, f[i] * by, t);
+    t = row_sum<LANES>(t, a.wpr, sums);
+    if (odd) rstd = (float)((double)by / sqrt((double)t / a.d + (double)a.eps * by * by));
+  }
+  return rstd;
+}
+
+// Codes of a thread's values: the largest magnitude of each block of 128 columns, its scale and the bytes.
+template <int N, int LANES, int EPT, typename P>
+__device__ __forceinline__ void store_codes(const P& at, const NormArgs& a, int64_t r, bool mine, const float (&v)[EPT]) {
+  constexpr int kChunks = EPT / N;
+  constexpr int kWide = LANES * N;                       // columns of a chunk over the lanes
+  constexpr int kPer = kWide >= 128 ? 1 : (LANES == 32 ? 128 / kWide : kChunks);  // chunks of a block
+  constexpr int kLanes = kWide >= 128 ? 128 / N : LANES;  // lanes of a block
+#pragma unroll
+  for (int c0 = 0; c0 < kChunks; c0 += kPer) {
+    float m = 0.f;
+#pragma unroll
+    for (int c = c0; c < c0 + kPer; ++c)
+#pragma unroll
+      for (int i = 0; i < N; ++i) m = max_mag(m, v[c * N + i]);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, o));
+    m = at_least_floor(m);
+    const float inv = __fdiv_rn(kTop, m);
+    if (!mine) continue;
+    if ((at.sub & (kLanes - 1)) == 0 && at.col(c0) < a.qcols)
+      a.scale[(int64_t)(at.col(c0) / 128) * a.ld_scale + r] = __fdiv_rn(m, kTop);
+    uint8_t* row = a.q + r * a.qcols;
+#pragma unroll
+    for (int c = c0; c < c0 + kPer; ++c) {
+      if (at.col(c) >= a.qcols) continue;
+      if constexpr (N >= 4) {
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int i = 0; i < N; i += 4) w[i / 4] = codes4(v + c * N + i, inv);
+        if constexpr (N == 8) *(uint2*)(row + at.col(c)) = make_uint2(w[0], w[1]);
+        else *(uint32_t*)(row + at.col(c)) = w[0];
+      } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float one[4] = {v[c * N + i], 0.f, 0.f, 0.f};
+          row[at.col(c) + i] = (uint8_t)codes4(one, inv);
+        }
+      }
+    }
+  }
+}
+
+// qcols may be past what 8 lanes hold of a narrow row: a group of 8 lanes covers 64 or 128 columns, and the
+// codes' row is 128; the rest is zeros.
+template <int LANES, int EPT, typename P>
+__device__ __forceinline__ void zero_codes(const P& at, const NormArgs& a, int64_t r, bool mine) {
+  if constexpr (LANES * EPT < 128) {
+    if (mine)
+      for (int c = LANES * EPT + at.sub * 4; c < a.qcols; c += LANES * 4) *(uint32_t*)(a.q + r * a.qcols + c) = 0;
+  }
+}
+
+template <typename T, int VB, int LANES, int EPT>
+__global__ void __launch_bounds__(512) rms_norm_kernel(const NormArgs a) {
+  constexpr int N = Chunk<T, VB>::n;
+  __shared__ float sums[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_block = (int)blockDim.x / (LANES * a.wpr);  // rows of a block
+  const Place<N, LANES, EPT> at(warp & (a.wpr - 1), lane);
+  const int64_t r = (int64_t)blockIdx.x * per_block + (int)threadIdx.x / (LANES * a.wpr);
+  const bool mine = r < a.rows;
+  grid_wait();
+  float f[EPT];
+  load_row<T, VB, EPT>(at, (const T*)a.x + r * a.ldx, a.d, mine, f);
+  if (a.residual) {
+    float p[EPT];
+    load_row<T, VB, EPT>(at, (const T*)a.residual + r * a.ldr, a.d, mine, p);
+    // the stream's value is what its type holds
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) f[i] = to_f32<T>(from_f32<T>(f[i] + p[i]));
+  }
+  if (a.s && mine) store_row<T, VB, EPT>(at, (T*)a.s + r * a.lds, a.d, f);
+  const float rstd = row_rstd<LANES, EPT>(f, a, sums);
+  {
+    float g[EPT];
+    load_gamma<N, EPT>(at, a, g);
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) f[i] = f[i] * rstd * g[i];
+  }
+  if (a.y && mine) store_row<T, VB, EPT>(at, (T*)a.y + r * a.ldy, a.d, f);
+  if (a.q) {
+    store_codes<N, LANES, EPT>(at, a, r, mine, f);
+    zero_codes<LANES, EPT>(at, a, r, mine);
+  }
+}
+
+template <typename T, int VB, int LANES, int EPT>
+__global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const NormArgs a) {
+  constexpr int N = Chunk<T, VB>::n;
+  extern __shared__ float total[];  // a column's sum over the block's rows
+  __shared__ float sums[16];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per_block = (int)blockDim.x / (LANES * a.wpr);
+  const Place<N, LANES, EPT> at(warp & (a.wpr - 1), lane);
+  float acc[EPT];
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) acc[i] = 0.f;
+  grid_wait();
+  const int64_t step = (int64_t)gridDim.x * per_block;
+  const int64_t trips = ceil_div(a.rows, step);  // the same in every thread: sums over a row need all of them
+  int64_t r = (int64_t)blockIdx.x * per_block + (int)threadIdx.x / (LANES * a.wpr);
+  for (int64_t trip = 0; trip < trips; ++trip, r += step) {
+    const bool mine = r < a.rows;
+    float u[EPT], g[EPT];
+    load_row<T, VB, EPT>(at, (const T*)a.x + r * a.ldx, a.d, mine, u);
+    load_row<T, VB, EPT>(at, (const T*)a.dy + r * a.ld_dy, a.d, mine, g);
+    const float rstd = row_rstd<LANES, EPT>(u, a, sums);
+    float dot = 0.f;
+    {
+      float gamma[EPT];
+      load_gamma<N, EPT>(at, a, gamma);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) {
+        u[i] *= rstd;
+        if (mine) acc[i] = fmaf(g[i], u[i], acc[i]);
+        g[i] *= gamma[i];
+        dot = fmaf(g[i], u[i], dot);
+      }
+    }
+    dot = row_sum<LANES>(dot, a.wpr, sums) / (float)a.d;
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) g[i] = rstd * (g[i] - u[i] * dot);
+    if (a.residual) {
+      float p[EPT];
+      load_row<T, VB, EPT>(at, (const T*)a.residual + r * a.ldr, a.d, mine, p);
+#pragma unroll
+      for (int i = 0; i < EPT; ++i) g[i] += p[i];
+    }
+    if (mine) store_row<T, VB, EPT>(at, (T*)a.y + r * a.ldy, a.d, g);
+  }
+  if (!a.part) return;
+  // lane groups of a warp in the order of their rows, then the warps
+#pragma unroll
+  for (int o = LANES; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
+  const int groups = (int)(blockDim.x >> 5) / a.wpr;  // warps that hold the same columns
+  for (int w = 0; w < groups; ++w) {
+    if (warp / a.wpr == w && lane < LANES) {
+#pragma unroll
+      for (int c = 0; c < EPT / N; ++c)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int col = at.col(c) + i;
+          if (col < a.d) total[col] = (w ? total[col] : 0.f) + acc[c * N + i];
+        }
+    }
+    __syncthreads();
+  }
+  for (int c = threadIdx.x; c < a.d; c += blockDim.x) a.part[(int64_t)blockIdx.x * a.d + c] = total[c];
+}
+
+// dgamma[c] = the sum of the partial rows, kJoinRows strands of them and then the strands, in their order.
+__global__ void __launch_bounds__(kJoinCols* kJoinRows) join_rows_kernel(const float* part, int parts, int d, float* out) {
+  __shared__ float strand[kJoinRows][kJoinCols + 1];
+  grid_wait();
+  const int x = threadIdx.x % kJoinCols, y = threadIdx.x / kJoinCols;
+  const int c = blockIdx.x * kJoinCols + x;
+  float sum = 0.f;
+  if (c < d) {
+#pragma unroll 4
+    for (int p = y; p < parts; p += kJoinRows) sum += part[(int64_t)p * d + c];
+  }
+  strand[y][x] = sum;
+  __syncthreads();
+  if (y == 0 && c < d) {
+    for (int i = 1; i < kJoinRows; ++i) sum += strand[i][x];
+    out[c] = sum;
+  }
+}
+
+// Lanes and elements of a thread by the row's width, warps to a row beyond 1024 columns.
+template <template <typename, int, int, int> class K, typename T, int VB, typename... A>
+auto pick_width(int d) {
+  return d <= 64 ? K<T, VB, 8, 8>::get() : d <= 128 ? K<T, VB, 8, 16>::get()
+       : d <= 256 ? K<T, VB, 32, 8>::get() : d <= 512 ? K<T, VB, 32, 16>::get() : K<T, VB, 32, 32>::get();
+}
+template <typename T, int VB, int LANES, int EPT>
+struct Forward {
+  static auto get() { return rms_norm_kernel<T, VB, LANES, EPT>; }
+};
+template <typename T, int VB, int LANES, int EPT>
+struct Backward {
+  static auto get() { return rms_norm_bwd_kernel<T, VB, LANES, EPT>; }
+};
+template <template <typename, int, int, int> class K>
+auto pick(ctr_dtype dtype, bool wide, int d) {
+  if (dtype == CTR_F32) return wide ? pick_width<K, float, 16>(d) : pick_width<K, float, 4>(d);
+  return wide ? pick_width<K, __nv_bfloat16, 16>(d) : pick_width<K, __nv_bfloat16, 2>(d);
+}
+
+struct NormPlan {
+  int lanes, wpr = 1, threads = 256, per_block;
+  explicit NormPlan(int d) {
+    lanes = d <= 128 ? 8 : 32;
+    while (wpr * 1024 < d) wpr *= 2;
+    if (wpr > 8) threads = 512;
+    per_block = threads / (lanes * wpr);
+  }
+};
+
+int norm_parts(int64_t rows, int d) { return (int)imin64(kNormParts, ceil_div(rows, NormPlan(d).per_block)); }
+
+bool misaligned(const void* p, int by) { return ((uintptr_t)p % by) != 0; }
+
+int check_norm(ctr_dtype dtype, int64_t rows, int32_t d, float eps) {
+  if (!dtype_ok(dtype) || rows < 0 || d < 1 || !(eps > 0.f) || !(eps < INFINITY)) return CTR_ERR_INVALID_ARG;
+  if (d > kNormMaxCols || rows > INT32_MAX - 65536) return CTR_ERR_UNSUPPORTED;
+  return CTR_OK;
+}
+
+}  // namespace
+}  // namespace ctr
+
+using namespace ctr;
+
+extern "C" size_t ctr_rms_norm_workspace_size(int64_t rows, int32_t d) {
+  if (rows < 0 || d < 1 || d > kNormMaxCols) return 0;
+  WsSizer z;
+  z.take<float>((size_t)norm_parts(rows, d) * d);
+  return z.used;
+}
+
+extern "C" int ctr_rms_norm(const void* x, ctr_dtype dtype, int64_t rows, int32_t d, int64_t ldx, const void* residual,
+                            int64_t ld_residual, const float* gamma, float eps, void* s, int64_t ld_s, void* y,
+                            int64_t ld_y, uint8_t* q, float* scale, int64_t ld_scale, void* ws, size_t ws_bytes,
+                            ctr_stream_t stream) {
+  const int st = check_norm(dtype, rows, d, eps);
+  if (st != CTR_OK) return st;
+  if ((q == nullptr) != (scale == nullptr) || (!y && !q && rows > 0)) return CTR_ERR_INVALID_ARG;
+  if (ldx < d || (residual && ld_residual < d) || (s && ld_s < d) || (y && ld_y < d) || (q && ld_scale < rows))
+    return CTR_ERR_INVALID_ARG;
+  const int eb = dtype_bytes(dtype);
+  if (rows > 0 && !x) return CTR_ERR_INVALID_ARG;
+  for (const void* p : {x, residual, (const void*)s, (const void*)y})
+    if (misaligned(p, eb)) return CTR_ERR_INVALID_ARG;
+  if (misaligned(gamma, 4) || misaligned(scale, 4) || misaligned(q, 16)) return CTR_ERR_INVALID_ARG;
+  if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
+  if (rows == 0) return CTR_OK;
+  const NormPlan plan(d);
+  NormArgs a = {};
+  a.x = x;
+  a.residual = residual;
+  a.gamma = gamma;
+  a.s = s;
+  a.y = y;
+  a.q = q;
+  a.scale = scale;
+  a.rows = rows;
+  a.ldx = ldx;
+  a.ldr = ld_residual;
+  a.lds = ld_s;
+  a.ldy = ld_y;
+  a.ld_scale = ld_scale;
+  a.d = d;
+  a.qcols = (d + 127) / 128 * 128;
+  a.wpr = plan.wpr;
+  a.gvec = !misaligned(gamma, 16);
+  a.eps = eps;
+  uint64_t parts = (uint64_t)x | (uint64_t)(ldx * eb) | (uint64_t)d * eb;
+  if (residual) parts |= (uint64_t)residual | (uint64_t)(ld_residual * eb);
+  if (s) parts |= (uint64_t)s | (uint64_t)(ld_s * eb);
+  if (y) parts |= (uint64_t)y | (uint64_t)(ld_y * eb);
+  const cudaError_t e = launch_after(pick<Forward>(dtype, parts % 16 == 0, d),
+                                     dim3((unsigned)ceil_div(rows, plan.per_block)), plan.threads, 0,
+                                     (cudaStream_t)stream, 1, a);
+  return e == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
+}
+
+extern "C" int ctr_rms_norm_bwd(const void* dy, ctr_dtype dtype, int64_t rows, int32_t d, int64_t ld_dy, const void* ds,
+                                int64_t ld_ds, const void* s, int64_t ld_s, const float* gamma, float eps, void* dx,
+                                int64_t ld_dx, float* dgamma, void* ws, size_t ws_bytes, ctr_stream_t stream) {
+  const int st = check_norm(dtype, rows, d, eps);
+  if (st != CTR_OK) return st;
+  if (ld_dy < d || (ds && ld_ds < d) || ld_s < d || ld_dx < d) return CTR_ERR_INVALID_ARG;
+  if (rows > 0 && (!dy || !s || !dx)) return CTR_ERR_INVALID_ARG;
+  const int eb = dtype_bytes(dtype);
+  for (const void* p : {dy, ds, s, (const void*)dx})
+    if (misaligned(p, eb)) return CTR_ERR_INVALID_ARG;
+  if (misaligned(gamma, 4) || misaligned(dgamma, 4)) return CTR_ERR_INVALID_ARG;
+  if (!ws_valid(ws, ws_bytes, dgamma ? ctr_rms_norm_workspace_size(rows, d) : kWsHeader)) return CTR_ERR_WORKSPACE;
+  const cudaStream_t stm = (cudaStream_t)stream;
+  const NormPlan plan(d);
+  const int parts = norm_parts(rows, d);
+  WsCarver c(ws, ws_bytes);
+  float* part = dgamma ? c.take<float>((size_t)parts * d) : nullptr;
+  if (rows > 0) {
+    NormArgs a = {};
+    a.x = s;
+    a.residual = ds;
+    a.dy = dy;
+    a.gamma = gamma;
+    a.y = dx;
+    a.part = part;
+    a.rows = rows;
+    a.ldx = ld_s;
+    a.ldr = ld_ds;
+    a.ld_dy = ld_dy;
+    a.ldy = ld_dx;
+    a.d = d;
+    a.wpr = plan.wpr;
+    a.gvec = !misaligned(gamma, 16);
+    a.eps = eps;
+    uint64_t all = (uint64_t)dy | (uint64_t)s | (uint64_t)dx | (uint64_t)(ld_dy * eb) | (uint64_t)(ld_s * eb) |
+                   (uint64_t)(ld_dx * eb) | (uint64_t)d * eb;
+    if (ds) all |= (uint64_t)ds | (uint64_t)(ld_ds * eb);
+    const auto k = pick<Backward>(dtype, all % 16 == 0, d);
+    const size_t smem = (size_t)d * 4;
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return CTR_ERR_CUDA;
+    if (launch_after(k, dim3((unsigned)parts), plan.threads, smem, stm, 1, a) != cudaSuccess) return CTR_ERR_CUDA;
+  }
+  if (dgamma &&
+      launch_after(join_rows_kernel, dim3((unsigned)ceil_div(d, kJoinCols)), kJoinCols * kJoinRows, 0, stm, 1,
+                   (const float*)part, parts, (int)d, dgamma) != cudaSuccess)
+    return CTR_ERR_CUDA;
+  return launch_status();
+}

@@ -92,6 +92,11 @@ _SIGS = {
     "ctr_fp8_matmul_workspace_size": (_sz, [_i64, _i32, _i64, _i64]),
     "ctr_fp8_matmul": (C.c_int, [_p, _p, _i64, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _i64, _p, _sz, _p]),
     "ctr_fp8_matmul_wgrad": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _p, _sz, _p]),
+    "ctr_rms_norm_workspace_size": (_sz, [_i64, _i32]),
+    "ctr_rms_norm": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _i64, _p, _p, _i64, _p,
+                               _sz, _p]),
+    "ctr_rms_norm_bwd": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _p, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _p, _sz,
+                                   _p]),
     "ctr_clip_grads_workspace_size": (_sz, []),
     "ctr_clip_grads": (C.c_int, [_p, _p, _p, _p, _i32, _f32, _p, _p, _sz, _p]),
 }
@@ -817,3 +822,61 @@ def ctr_clip_grads(grads: GradList, max_norm: float, norm: torch.Tensor, ws: tor
                               norm.data_ptr(), *_room(ws), _stream(stream))
     if st:
         _ok("ctr_clip_grads", st)
+
+
+# ---------------------------------------------------------------------------
+# layers around the experts
+# ---------------------------------------------------------------------------
+MAX_NORM_WIDTH = 16384
+
+
+def _like_or_none(t: Optional[torch.Tensor], what: str, rows: int, cols: int, dtype):
+    """(address, row stride) of an optional matrix of the given shape and type."""
+    return (None, 0) if t is None else (t.data_ptr() if isinstance(t, torch.Tensor) else None,
+                                        _like(t, what, rows, cols, dtype))
+
+
+def _dense_or_none(t: Optional[torch.Tensor], what: str, dtype, shape):
+    """Address of an optional dense tensor."""
+    if t is None:
+        return None
+    _dense(t, what, dtype, shape)
+    return t.data_ptr()
+
+
+def ctr_rms_norm_workspace_size(rows: int, d: int) -> int:
+    return int(lib().ctr_rms_norm_workspace_size(rows, d))
+
+
+def ctr_rms_norm(x: torch.Tensor, residual: Optional[torch.Tensor], gamma: Optional[torch.Tensor], eps: float,
+                 s: Optional[torch.Tensor], y: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                 scale: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    """s = x + residual, and its norm times gamma as values y or as row codes q with their scales, or both."""
+    if stream is None and _took("ctr_rms_norm", _usual().rms_norm(x, residual, gamma, eps, s, y, q, scale, ws)):
+        return
+    rows, d, ldx = _mat(x, "x")
+    pr, ldr = _like_or_none(residual, "residual", rows, d, x.dtype)
+    pg = _dense_or_none(gamma, "gamma", _F32, (d,))
+    ps, lds = _like_or_none(s, "s", rows, d, x.dtype)
+    py, ldy = _like_or_none(y, "y", rows, d, x.dtype)
+    _want((q is None) == (scale is None), "q and scale go together")
+    pq = _dense_or_none(q, "q", _U8, (rows, fp8_padded(d)))
+    pc, ldc = _like_or_none(scale, "scale", fp8_blocks(d), rows, _F32)
+    _ok("ctr_rms_norm", lib().ctr_rms_norm(x.data_ptr(), DTYPES[x.dtype], rows, d, ldx, pr, ldr, pg, eps, ps, lds, py,
+                                           ldy, pq, pc, ldc, *_room(ws), _stream(stream)))
+
+
+def ctr_rms_norm_bwd(dy: torch.Tensor, ds: Optional[torch.Tensor], s: torch.Tensor, gamma: Optional[torch.Tensor],
+                     eps: float, dx: torch.Tensor, dgamma: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    """dx = ds + the norm's gradient by dy, and gamma's; s is what the forward wrote (x without a residual)."""
+    if stream is None and _took("ctr_rms_norm_bwd", _usual().rms_norm_bwd(dy, ds, s, gamma, eps, dx, dgamma, ws)):
+        return
+    rows, d, ld_dy = _mat(dy, "dy")
+    pd, ldd = _like_or_none(ds, "ds", rows, d, dy.dtype)
+    ld_s = _like(s, "s", rows, d, dy.dtype)
+    pg = _dense_or_none(gamma, "gamma", _F32, (d,))
+    ld_dx = _like(dx, "dx", rows, d, dy.dtype)
+    po = _dense_or_none(dgamma, "dgamma", _F32, (d,))
+    _ok("ctr_rms_norm_bwd", lib().ctr_rms_norm_bwd(dy.data_ptr(), DTYPES[dy.dtype], rows, d, ld_dy, pd, ldd, s.data_ptr(),
+                                                   ld_s, pg, eps, dx.data_ptr(), ld_dx, po, *_room(ws),
+                                                   _stream(stream)))

@@ -1,0 +1,73 @@
+"""Plain 64-bit (numpy) forms of the layers around the experts, and their tolerances.
+
+u = 2^-24.  Bounds, each from the kernels' own sums and derived before any run:
+
+  rstd        a thread adds up to 32 squares, then 5 shuffles and up to 16 warps: 53
+              additions, one rounding in each square's fused step, so the sum is
+              within 54 u; division by d and + eps 2 u; halved by the root, 28 u; root
+              and reciprocal 2 u: relative 30 u
+  norm        two products on top: 32 u relative
+  codes       the scale is the largest of values within 32 u, one division: 33 u; what is
+              rounded to a code is v (32 u) times 448 / max (33 u), one product: 66 u
+  dx          with t = g u (g = dy gamma 1 u, u = s rstd 31 u): mean(t) is within 54 u +
+              33 u of mean|t|, one division: 88 u; u mean(t): 31 u + 1; the difference, the
+              product with rstd (30 u) and the last sum: 3 u
+  dgamma      terms within 31 u; a thread adds `trips` rows, a block 32 lane groups and
+              warps at most, the second kernel 19 + 16 partial rows
+"""
+import numpy as np
+
+import _experts_ref as R
+
+U = R.U
+
+
+def norm(s, gamma, eps):
+    """(v, rstd) of s (fp64)."""
+    rstd = 1 / np.sqrt((s * s).mean(axis=1, keepdims=True) + eps)
+    return s * rstd * gamma, rstd
+
+
+def norm_tol(v):
+    return 32 * U * np.abs(v) + 1e-45
+
+
+def norm_grad(dy, ds, s, gamma, eps):
+    """(dx, its tolerance, dgamma, sum of magnitudes for its tolerance)."""
+    rstd = norm(s, gamma, eps)[1]
+    unit, g = s * rstd, dy * gamma
+    dot, mag = (g * unit).mean(axis=1, keepdims=True), np.abs(g * unit).mean(axis=1, keepdims=True)
+    dx = ds + rstd * (g - unit * dot)
+    tol = U * rstd * (36 * np.abs(g) + np.abs(unit) * (66 * np.abs(dot) + 88 * mag)) + 2 * U * (np.abs(ds) + np.abs(dx))
+    return dx, tol + 1e-44, (dy * unit).sum(axis=0), np.abs(dy * unit).sum(axis=0)
+
+
+def norm_sums(rows, d):
+    """Additions in a sum of dgamma: see above (303 blocks of 256 or 512 threads take rows in turn)."""
+    lanes = 8 if d <= 128 else 32
+    wpr = 1
+    while wpr * 1024 < d:
+        wpr *= 2
+    per = (512 if wpr > 8 else 256) // (lanes * wpr)
+    return -(-rows // (304 * per)) + 32 + 19 + 16 + 31 + 1
+
+
+def row_codes(v):
+    """(block maxima [blocks, rows], v * 448 / max [rows, padded]) of v (fp64)."""
+    rows, d = v.shape
+    blocks = -(-d // 128)
+    p = np.zeros((rows, blocks * 128))
+    p[:, :d] = v
+    p = p.reshape(rows, blocks, 128)
+    m = np.maximum(np.abs(p).max(axis=2), 2.0 ** -100)
+    return m.T, (p * (448 / m[:, :, None])).reshape(rows, blocks * 128)
+
+
+def codes_fit(codes, scale, v):
+    """Whether codes (bytes) and scales are those of values within 32 u of v."""
+    m, t = row_codes(v)
+    if not np.all(np.abs(scale * 448 - m) <= 36 * U * m):
+        return False
+    got = R.e4m3_values(codes)
+    lo, hi = R.e4m3_round(np.clip(t - 66 * U * np.abs(t), -448, 448)), R.e4m3_round(np.clip(t + 66 * U * np.abs(t), -448, 448))
+    return bool(np.all((got >= lo) & (got <= hi)))
