@@ -589,6 +589,52 @@ int ctr_clip_grads(const void* const* grads, void* const* outs, const int32_t* d
  * no norm; the formulas below are this library's.  Matrices, types, alignment
  * and NULL pointers as in section b. */
 
+/* ---- Dense layers ---------------------------------------------------------- */
+typedef enum {
+  CTR_ACT_NONE = 0,
+  CTR_ACT_RELU = 1,    /* max(z, 0) */
+  CTR_ACT_SILU = 2,    /* z / (1 + exp(-z)) */
+  CTR_ACT_GELU = 3,    /* z (1 + erf(z / sqrt 2)) / 2 */
+  CTR_ACT_SIGMOID = 4  /* 1 / (1 + exp(-z)) */
+} ctr_activation;
+
+/* z = x W^T + bias and y = act(z) + residual:
+ *   z[t, i] = sum over c < k of x[t, c] w[i, c]  + bias[i],    y[t, i] = act(z[t, i]) + residual[t, i]
+ * x [rows, k], w [n, k], bias [n] (optional), residual (optional), y and pre
+ * [rows, n], all of `dtype`.  pre (optional) gets z, which the backward call
+ * needs where there is an activation.  Sums are fp32, bias, activation and
+ * residual are applied to them in fp32, y and pre are rounded once.
+ * bf16: products of the tensor cores.  fp32: also there, x and w each as three
+ * bf16 numbers that add up to it, six of their nine products: what is dropped is
+ * below 2^-24 of |x| |w|, so results are as near as those of fp32 sums.  A NaN
+ * or an infinity in x or w makes what it enters NaN, or the infinity that the
+ * formula gives.  y may be residual itself (the same rows and stride); nothing
+ * else may overlap.
+ * Device errors: CTR_ERR_TIMEOUT.
+ * Workspace: ctr_dense_workspace_size(rows, n, k, dtype, train, packed) bytes,
+ * asked on the device of the call: train != 0 for ctr_dense_bwd (with room for
+ * ctr_dense too), packed != 0 where rows of a bf16 matrix do not start at
+ * multiples of 16 bytes.  A call that needs more than it is given is refused
+ * (CTR_ERR_WORKSPACE). */
+size_t ctr_dense_workspace_size(int64_t rows, int64_t n, int64_t k, ctr_dtype dtype, int train, int packed);
+int ctr_dense(const void* x, ctr_dtype dtype, int64_t rows, int64_t k, int64_t ldx, const void* w, int64_t n,
+              int64_t ldw, const void* bias, int act, const void* residual, int64_t ld_residual, void* y, int64_t ld_y,
+              void* pre, int64_t ld_pre, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* Its gradients.  With dz = dy act'(pre) (relu: 1 where pre > 0, else 0; pre as
+ * ctr_dense wrote it, not read without an activation):
+ *   dx[t, c] = sum over i of dz[t, i] w[i, c]      (dtype)
+ *   dw[i, c] = sum over t of dz[t, i] x[t, c]      (grad_dtype)
+ *   dbias[i] = sum over t of dz[t, i]              (grad_dtype)
+ * each optional; the residual's gradient is dy.  grad_dtype is dtype or CTR_F32.
+ * For bf16, dz is rounded to bf16 for the two products (not for dbias); sums are
+ * fp32 in an order that is the same in every run.  No rows: dw and dbias are
+ * zeros.  Outputs may not overlap anything. */
+int ctr_dense_bwd(const void* dy, ctr_dtype dtype, int64_t rows, int64_t n, int64_t ld_dy, const void* x, int64_t k,
+                  int64_t ldx, const void* w, int64_t ldw, const void* pre, int64_t ld_pre, int act, void* dx,
+                  int64_t ld_dx, ctr_dtype grad_dtype, void* dw, int64_t ld_dw, void* dbias, void* ws, size_t ws_bytes,
+                  ctr_stream_t stream);
+
 /* ---- Root-mean-square norm on a residual stream ------------------------- */
 /* For each row:
  *   s = x + residual, rounded to the rows' type (s = x where residual is NULL)

@@ -285,6 +285,38 @@ float number_f32(PyObject* o) {
   return (float)PyFloat_AS_DOUBLE(o);
 }
 
+// x, w, bias, act, residual, y, pre, ws
+CALL(dense) {
+  return run<8>(n, [&] {
+    const Values x = values(a[0], 2), w = values(a[1], 2), y = values(a[5], 2);
+    const int64_t rows = x.n[0], k = x.n[1], cols = w.n[0], act = number(a[3]);
+    if (w.n[1] != k || w.scalar != x.scalar || y.n[0] != rows || y.n[1] != cols || y.scalar != x.scalar || act > INT32_MAX)
+      throw Odd();
+    const Workspace room = workspace(a[7]);
+    return free_of_lock(ctr_dense, x.p, x.type, rows, k, x.ld(), w.p, cols, w.ld(), data<void>(a[2], x.scalar, {cols}, true),
+                        (int)act, like(a[4], x.scalar, rows, cols), y.ld(), y.p, y.ld(), like(a[6], x.scalar, rows, cols),
+                        y.ld(), room.p, room.n, stream());
+  });
+}
+
+// dy, x, w, pre, act, dx, dw, dbias, ws
+CALL(dense_bwd) {
+  return run<9>(n, [&] {
+    const Values y = values(a[0], 2), x = values(a[1], 2);
+    const int64_t rows = y.n[0], cols = y.n[1], k = x.n[1], act = number(a[4]);
+    if (x.n[0] != rows || x.scalar != y.scalar || a[2] == Py_None || act > INT32_MAX || (act != 0 && a[3] == Py_None))
+      throw Odd();
+    PyObject* some = a[6] != Py_None ? a[6] : a[7];
+    const at::ScalarType grad = some != Py_None ? tensor(some).scalar_type() : y.scalar;
+    if (grad != at::kFloat && grad != y.scalar) throw Odd();
+    const Workspace room = workspace(a[8]);
+    return free_of_lock(ctr_dense_bwd, y.p, y.type, rows, cols, y.ld(), x.p, k, x.ld(), like(a[2], y.scalar, cols, k),
+                        x.ld(), like(a[3], y.scalar, rows, cols), y.ld(), (int)act, like(a[5], y.scalar, rows, k), x.ld(),
+                        grad == at::kFloat ? CTR_F32 : CTR_BF16, like(a[6], grad, cols, k), x.ld(),
+                        data<void>(a[7], grad, {cols}, true), room.p, room.n, stream());
+  });
+}
+
 // x, residual, gamma, eps, s, y, q, scale, ws
 CALL(rms_norm) {
   return run<9>(n, [&] {
@@ -317,7 +349,8 @@ PyMethodDef methods[] = {ENTRY(expert_route),          ENTRY(expert_route_bwd), 
                          ENTRY(expert_combine),        ENTRY(expert_combine_bwd), ENTRY(fp8_quantize_rows),
                          ENTRY(fp8_quantize_rows_cols), ENTRY(fp8_quantize_blocks), ENTRY(fp8_matmul),
                          ENTRY(fp8_matmul_wgrad),      ENTRY(clip_grads),
-                         ENTRY(rms_norm),              ENTRY(rms_norm_bwd),       {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(dense),                 ENTRY(dense_bwd),          ENTRY(rms_norm),
+                         ENTRY(rms_norm_bwd),            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ctr_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

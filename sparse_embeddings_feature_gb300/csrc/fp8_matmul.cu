@@ -98,18 +98,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b
         : "memory");
 }
 
-// The issued MMAs' completion arrives at the barrier `bar`, in both CTAs of a pair.
-template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t bar) {
-  if constexpr (PAIR)
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-  else
-    mma_commit(bar);
-}
-
 // Loads into this CTA's shared memory, counted at `bar` (of the pair's even CTA).
 template <bool PAIR>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int32_t c0, int32_t c1, uint32_t bar) {
@@ -121,43 +109,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         : "memory");
   else
     tma_load_2d(dst, map, c0, c1, bar);
-}
-
-// Bounded wait of a whole warp.  The hint lets the hardware park the warp for up to 20 us a try:
-// warps that poll take issue slots from the ones that scale.
-__device__ __forceinline__ bool park(uint32_t bar, uint32_t parity) {
-  uint64_t t0 = 0;
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (__all_sync(kFull, ok)) return true;
-    if (t0 == 0) t0 = globaltimer();
-    if (__any_sync(kFull, globaltimer() - t0 > kWaitLimitNs)) return false;
-  }
-}
-
-// One lane of the warp, the same every time.  The roles' loops are run by whole warps, so that
-// their values stay in uniform registers; only the copies, MMAs and arrivals are one lane's.
-__device__ __forceinline__ bool elected() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
-
-// Arrival at a barrier of either CTA.  Release at CTA scope (the default): what it orders are this
-// thread's accumulator reads, which are complete; at cluster scope an arrival took 1500 cycles.
-__device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // acc += f * v for 32 values, two at a time.  volatile: stays after the wait for the load of v.
@@ -177,11 +128,6 @@ __device__ __forceinline__ void scale_add32(uint64_t* acc, const uint32_t (&v)[3
 __device__ __forceinline__ void copy_scale(uint32_t dst, const float* src, bool take, const float* any) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(take ? src : any), "r"(take ? 4 : 0)
                : "memory");
-}
-
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-  return *(const uint32_t*)&h;
 }
 
 struct Tile {
@@ -352,17 +298,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
     fence_mbar_init();
   }
   if (warp == 1) {
-    if constexpr (PAIR) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
-                   "r"(2 * kBN)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
-                   "r"(2 * kBN)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
+    tmem_alloc<PAIR>(smem_u32(&tmem_base_slot), 2 * kBN);
   }
   grid_wait();
   if (warp == 4) group_starts(p, start, offs, WGRAD ? 128 : kCtas * kBM);
@@ -679,10 +615,7 @@ __global__ void __launch_bounds__(kMmThreads, 1) fp8_matmul_kernel(const MmArgs 
   if constexpr (PAIR) cluster_sync();  // nothing of this CTA is the other's target any more
   if (warp == 1) {
     fence_after();
-    if constexpr (PAIR)
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kBN) : "memory");
-    else
-      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * kBN) : "memory");
+    tmem_free<PAIR>(tmem, 2 * kBN);
   }
 }
 

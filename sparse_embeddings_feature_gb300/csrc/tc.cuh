@@ -1,6 +1,8 @@
 // tcgen05 helpers (sm_100+ PTX, written inline) shared by the tensor-core kernels.
 #pragma once
 
+#include <cuda_bf16.h>
+
 #include "tma.cuh"
 
 namespace ctr {
@@ -45,6 +47,80 @@ static __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t 
 static __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
   tmem_ld32_async(taddr, r);
   tmem_wait_ld();
+}
+
+// The issued MMAs' completion arrives at the barrier `bar`, in both CTAs of a pair.
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    mma_commit(bar);
+}
+
+// Bounded wait of a whole warp.  The hint lets the hardware park the warp for up to 20 us a try:
+// warps that poll take issue slots from the ones that scale.
+static __device__ __forceinline__ bool park(uint32_t bar, uint32_t parity) {
+  uint64_t t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (__all_sync(kFull, ok)) return true;
+    if (t0 == 0) t0 = globaltimer();
+    if (__any_sync(kFull, globaltimer() - t0 > kWaitLimitNs)) return false;
+  }
+}
+
+// One lane of the warp, the same every time.  The roles' loops are run by whole warps, so that
+// their values stay in uniform registers; only the copies, MMAs and arrivals are one lane's.
+static __device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// Arrival at a barrier of either CTA.  Release at CTA scope (the default): what it orders are this
+// thread's accumulator reads, which are complete; at cluster scope an arrival took 1500 cycles.
+static __device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+static __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *(const uint32_t*)&h;
+}
+
+// TMEM of `cols` columns (a power of two from 32): its address goes to the shared word `slot`; by one whole warp of
+// each CTA.
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t cols) {
+  if constexpr (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot), "r"(cols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+}
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t cols) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols) : "memory");
 }
 
 }  // namespace ctr

@@ -92,6 +92,11 @@ _SIGS = {
     "ctr_fp8_matmul_workspace_size": (_sz, [_i64, _i32, _i64, _i64]),
     "ctr_fp8_matmul": (C.c_int, [_p, _p, _i64, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _i64, _p, _sz, _p]),
     "ctr_fp8_matmul_wgrad": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _p, _sz, _p]),
+    "ctr_dense_workspace_size": (_sz, [_i64, _i64, _i64, C.c_int, C.c_int, C.c_int]),
+    "ctr_dense": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, _i64, _p, C.c_int, _p, _i64, _p, _i64, _p, _i64, _p,
+                            _sz, _p]),
+    "ctr_dense_bwd": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, C.c_int, _p, _i64,
+                                C.c_int, _p, _i64, _p, _p, _sz, _p]),
     "ctr_rms_norm_workspace_size": (_sz, [_i64, _i32]),
     "ctr_rms_norm": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _i64, _p, _p, _i64, _p,
                                _sz, _p]),
@@ -842,6 +847,58 @@ def _dense_or_none(t: Optional[torch.Tensor], what: str, dtype, shape):
         return None
     _dense(t, what, dtype, shape)
     return t.data_ptr()
+
+
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_SIGMOID = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU, "sigmoid": ACT_SIGMOID}
+
+
+def ctr_dense_workspace_size(rows: int, n: int, k: int, dtype: torch.dtype, train: bool = False,
+                             packed: Optional[bool] = None) -> int:
+    """Workspace of a dense layer's calls.  packed: rows of some matrix do not start at multiples of 16 bytes (by
+    default, whether those of dense bf16 matrices with n or k columns do not)."""
+    if packed is None:
+        packed = n % 8 != 0 or k % 8 != 0
+    return int(lib().ctr_dense_workspace_size(rows, n, k, DTYPES[dtype], 1 if train else 0, 1 if packed else 0))
+
+
+def ctr_dense(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor], act: int, residual: Optional[torch.Tensor],
+              y: torch.Tensor, pre: Optional[torch.Tensor], ws: torch.Tensor, stream=None) -> None:
+    """y = act(x w^T + bias) + residual; pre gets what the activation is of."""
+    if stream is None and _took("ctr_dense", _usual().dense(x, w, bias, act, residual, y, pre, ws)):
+        return
+    rows, k, ldx = _mat(x, "x")
+    n, wk, ldw = _mat(w, "w", (x.dtype,))
+    _want(wk == k, "w must have as many columns as x")
+    pb = _dense_or_none(bias, "bias", x.dtype, (n,))
+    pr, ldr = _like_or_none(residual, "residual", rows, n, x.dtype)
+    ldy = _like(y, "y", rows, n, x.dtype)
+    pp, ldp = _like_or_none(pre, "pre", rows, n, x.dtype)
+    _ok("ctr_dense", lib().ctr_dense(x.data_ptr(), DTYPES[x.dtype], rows, k, ldx, w.data_ptr(), n, ldw, pb, act, pr, ldr,
+                                     y.data_ptr(), ldy, pp, ldp, *_room(ws), _stream(stream)))
+
+
+def ctr_dense_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, pre: Optional[torch.Tensor], act: int,
+                  dx: Optional[torch.Tensor], dw: Optional[torch.Tensor], dbias: Optional[torch.Tensor],
+                  ws: torch.Tensor, stream=None) -> None:
+    """Gradients of x, w and bias, each where it is given; the residual's is dy."""
+    if stream is None and _took("ctr_dense_bwd", _usual().dense_bwd(dy, x, w, pre, act, dx, dw, dbias, ws)):
+        return
+    rows, n, ld_dy = _mat(dy, "dy")
+    xr, k, ldx = _mat(x, "x", (dy.dtype,))
+    _want(xr == rows, "x must have as many rows as dy")
+    ldw = _like(w, "w", n, k, dy.dtype)
+    _want(act == ACT_NONE or pre is not None, "an activation's gradient needs pre")
+    pp, ldp = _like_or_none(pre, "pre", rows, n, dy.dtype)
+    px, ld_dx = _like_or_none(dx, "dx", rows, k, dy.dtype)
+    some = dw if dw is not None else dbias
+    grad = some.dtype if isinstance(some, torch.Tensor) else dy.dtype
+    _want(grad in (torch.float32, dy.dtype), "dw and dbias must be fp32 or of dy's type")
+    pw, ld_dw = _like_or_none(dw, "dw", n, k, grad)
+    pb = _dense_or_none(dbias, "dbias", grad, (n,))
+    _ok("ctr_dense_bwd", lib().ctr_dense_bwd(dy.data_ptr(), DTYPES[dy.dtype], rows, n, ld_dy, x.data_ptr(), k, ldx,
+                                             w.data_ptr(), ldw, pp, ldp, act, px, ld_dx, DTYPES[grad], pw, ld_dw, pb,
+                                             *_room(ws), _stream(stream)))
 
 
 def ctr_rms_norm_workspace_size(rows: int, d: int) -> int:

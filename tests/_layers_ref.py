@@ -71,3 +71,54 @@ def codes_fit(codes, scale, v):
     got = R.e4m3_values(codes)
     lo, hi = R.e4m3_round(np.clip(t - 66 * U * np.abs(t), -448, 448)), R.e4m3_round(np.clip(t + 66 * U * np.abs(t), -448, 448))
     return bool(np.all((got >= lo) & (got <= hi)))
+
+
+# ---------------------------------------------------------------------------
+# dense layers (torch, fp64)
+# ---------------------------------------------------------------------------
+# A tensor core's addition may drop, not round, its last bit: within 2 u of the running sum of magnitudes.  bf16: k
+# products, 2 k u.  fp32: the first planes' products are read back every 128 of them, 256 u, and added, k / 128 u; the
+# five other products are 2^-7 of the magnitudes together and are read back every 4096: 2 * 5 * 2^-7 min(k, 4096) u; what
+# is dropped, twice 2^-24, and the planes' own rounding, twice 2^-24: 4 u.  Weight gradients: bf16 too is read back every
+# 512 rows; up to 152 parts are added.  The 2-norm of an fp32 result's error: 8 additions that drop 2 u of a running sum,
+# which for terms of random sign is no larger than the whole, 16 u.
+def sum_bound(dtype, k, mag, gradient=False):
+    if dtype == "f32":
+        return (256 + k / 128 + 10 / 128 * min(k, 4096) + 4 + (152 if gradient else 0) + 2) * U * mag
+    return (2 * (min(k, 512) if gradient else k) + (k / 512 + 152 if gradient else 0) + 2) * U * mag
+
+
+def act64(act, z):
+    import torch
+    s = torch.sigmoid(z)
+    phi = 0.5 * (1 + torch.erf(z / 2 ** 0.5))
+    return {"none": (z, torch.ones_like(z)), "relu": (z.clamp(min=0), (z > 0).to(z.dtype)),
+            "sigmoid": (s, s * (1 - s)), "silu": (z * s, s * (1 + z * (1 - s))),
+            "gelu": (z * phi, phi + z * torch.exp(-z * z / 2) / (2 * np.pi) ** 0.5)}[act]
+
+
+def act_tol(z, y, tol_z):
+    """Of act(z) with z within tol_z: slopes are at most 1.13; expf and erff are within 2 ulp, then a sum, a division
+    and a product: 10 u (|z| + 1)."""
+    return 1.13 * tol_z + 10 * U * (z.abs() + 1) + U * y.abs()
+
+
+def fits(got, ref, tol, dtype):
+    """R.within for torch tensors."""
+    import torch
+    if dtype == "f32":
+        return bool(((got.double() - ref).abs() <= tol).all())
+    lo, hi = (ref - tol).to(torch.bfloat16), (ref + tol).to(torch.bfloat16)
+    return bool(((got >= lo) & (got <= hi)).all())
+
+
+def dz64(dtype, act, dy, pre):
+    """(dz as the products have it, how far it may be off): rounded to bf16 where the inputs are bf16."""
+    import torch
+    dz = dy * act64(act, pre)[1]
+    err = 16 * U * (1 + pre.abs()) * dy.abs() if act != "none" else 0 * dy
+    if dtype == "f32":
+        return dz, err, dz, err
+    mid = dz.to(torch.bfloat16).double()
+    lo, hi = (dz - err).to(torch.bfloat16).double(), (dz + err).to(torch.bfloat16).double()
+    return mid, torch.maximum(hi - mid, mid - lo), dz, err

@@ -36,3 +36,40 @@ def test_norm_refusals(lib):
     assert back(dy=ODD) == -1 and back(ds=ODD) == -1 and back(s=ODD) == -1 and back(dx=ODD) == -1 and back(dg=ODD) == -1
     assert back(size=256) == -3 and back(dg=None, size=255) == -3
     assert lib.ctr_rms_norm_workspace_size(-1, 8) == 0 and lib.ctr_rms_norm_workspace_size(4, 16385) == 0
+
+
+def test_dense_refusals(lib):
+    big = 1 << 30
+
+    def call(x=P, dt=1, rows=40, k=16, ldx=16, w=P, n=24, ldw=16, bias=None, act=0, r=None, ldr=24, y=P, ldy=24, pre=None,
+             ldp=24, ws=P, size=big):
+        return lib.ctr_dense(x, dt, rows, k, ldx, w, n, ldw, bias, act, r, ldr, y, ldy, pre, ldp, ws, size, None)
+    assert call(x=None) == -1 and call(w=None) == -1 and call(y=None) == -1 and call(dt=2) == -1 and call(rows=-1) == -1
+    assert call(k=0) == -1 and call(n=0) == -1 and call(act=5) == -1 and call(act=-1) == -1
+    assert call(ldx=15) == -1 and call(ldw=15) == -1 and call(ldy=23) == -1
+    assert call(r=P, ldr=23) == -1 and call(pre=P, ldp=23) == -1
+    odd = C.c_void_p(257)
+    for name in ("x", "w", "bias", "r", "y", "pre"):
+        assert call(**{name: odd}) == -1, name
+        assert call(dt=0, **{name: ODD}) == -1, name
+    assert call(rows=1 << 31) == -2 and call(n=1 << 30, ldy=1 << 30) == -2 and call(k=1 << 30, ldx=1 << 30, ldw=1 << 30) == -2
+    assert call(size=100) == -3 and call(ws=None) == -3 and call(ws=C.c_void_p(100)) == -3
+    assert call(dt=0, size=256) == -3                                   # no room for the planes
+    assert call(k=15, ldx=15, ldw=15, size=256) == -3                   # nor for rows off 16 bytes
+    assert call(rows=0, x=None, y=None) == 0
+
+    def back(dy=P, dt=1, rows=40, n=24, ld=24, x=P, k=16, ldx=16, w=P, ldw=16, pre=P, ldp=24, act=1, dx=P, ldd=16, gt=0, dw=P,
+             ldg=16, db=P, ws=P, size=big):
+        return lib.ctr_dense_bwd(dy, dt, rows, n, ld, x, k, ldx, w, ldw, pre, ldp, act, dx, ldd, gt, dw, ldg, db, ws, size, None)
+    assert back(dy=None) == -1 and back(x=None) == -1 and back(w=None) == -1 and back(pre=None) == -1
+    assert back(dt=0, gt=1) == -1 and back(gt=2) == -1 and back(act=9) == -1
+    assert back(ld=23) == -1 and back(ldx=15) == -1 and back(ldw=15) == -1 and back(ldp=23) == -1 and back(ldd=15) == -1
+    assert back(ldg=15) == -1
+    for name in ("dy", "x", "w", "pre", "dx", "dw", "db"):
+        assert back(**{name: odd}) == -1, name
+    assert back(dw=ODD) == -1 and back(db=ODD) == -1                    # fp32 gradients of a bf16 layer
+    assert back(size=256) == -3 and back(ws=None) == -3
+    size = lib.ctr_dense_workspace_size
+    assert size(-1, 24, 16, 0, 0, 0) == 0 and size(4, 0, 16, 0, 0, 0) == 0 and size(4, 24, 16, 7, 0, 0) == 0
+    assert size(40, 24, 16, 1, 0, 0) == 256 and size(40, 24, 16, 1, 0, 1) > 256 and size(40, 24, 16, 0, 0, 0) > 256
+    assert size(40, 24, 16, 1, 1, 0) < size(40, 24, 16, 0, 1, 0)
