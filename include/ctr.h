@@ -589,6 +589,38 @@ int ctr_clip_grads(const void* const* grads, void* const* outs, const int32_t* d
  * no norm; the formulas below are this library's.  Matrices, types, alignment
  * and NULL pointers as in section b. */
 
+/* ---- Balanced routing ----------------------------------------------------- */
+/* ctr_expert_route with a score function, a bias for balance and groups of
+ * experts.  With l = scores[t, :] and A = the experts with l_e > -inf:
+ *   p_e   = softmax over A of l (CTR_SCORE_SOFTMAX), or 1 / (1 + exp(-l_e))
+ *   key_e = p_e + bias_e, for e in A with bias_e > -inf (bias fp32 [experts],
+ *           optional; the program moves it towards even loads, it has no gradient)
+ * Experts are `groups` groups of experts / groups neighbours.  The group_k groups
+ * with the largest sums of their two largest keys (of the one that they have)
+ * stay; choice j is the j-th largest key in them.  Keys and sums are those of
+ * 64-bit arithmetic (choices without a bias go by the scores themselves, whose
+ * order is the keys'); ties go to the lower index.
+ *   weight_j = factor p_j, divided by the sum of the choices' p if renormalize != 0
+ * Maps, missing choices, NaN or +inf scores, limits and workspace as in
+ * ctr_expert_route; a NaN or +inf in bias is taken for -inf and flagged
+ * CTR_ERR_BAD_VALUE.  experts is a multiple of groups, 1 <= group_k <= groups <=
+ * CTR_MAX_GROUPS, k <= group_k experts / groups; factor is finite. */
+#define CTR_MAX_GROUPS 32
+typedef enum { CTR_SCORE_SOFTMAX = 0, CTR_SCORE_SIGMOID = 1 } ctr_score;
+int ctr_expert_route_balanced(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, int64_t ld_scores,
+                              int32_t k, int score, const float* bias, int32_t groups, int32_t group_k,
+                              int renormalize, float factor, int32_t* expert, float* weight, int32_t* slot,
+                              int32_t* token, int32_t* offsets, void* ws, size_t ws_bytes, ctr_stream_t stream);
+
+/* Its gradient, the choices held fixed: dscores = the gradient of sum over j of
+ * dweight_j weight_j, in the scores' type; 0 for masked scores, for tokens with
+ * nothing routed and, with sigmoids or renormalized weights, for experts that
+ * were not chosen.  ws: as ctr_expert_route_bwd. */
+int ctr_expert_route_balanced_bwd(const float* dweight, const void* scores, ctr_dtype dtype, int64_t tokens,
+                                  int32_t experts, int64_t ld_scores, int32_t k, int score, int renormalize,
+                                  float factor, const int32_t* expert, void* dscores, int64_t ld_dscores, void* ws,
+                                  size_t ws_bytes, ctr_stream_t stream);
+
 /* ---- Dense layers ---------------------------------------------------------- */
 typedef enum {
   CTR_ACT_NONE = 0,

@@ -81,6 +81,19 @@ int64_t number(PyObject* o) {
   return v;
 }
 
+// fp32 or bf16 values [rows, cols] of the given type; NULL for None.
+void* like(PyObject* o, at::ScalarType type, int64_t rows, int64_t cols) {
+  if (o == Py_None) return nullptr;
+  const Values v = values(o, 2);
+  if (v.n[0] != rows || v.n[1] != cols || v.scalar != type) throw Odd();
+  return v.p;
+}
+
+float number_f32(PyObject* o) {
+  if (!PyFloat_Check(o)) throw Odd();
+  return (float)PyFloat_AS_DOUBLE(o);
+}
+
 struct Workspace {
   void* p;
   size_t n;
@@ -272,17 +285,34 @@ CALL(clip_grads) {
   });
 }
 
-// fp32 or bf16 values [rows, cols] of the given type; NULL for None.
-void* like(PyObject* o, at::ScalarType type, int64_t rows, int64_t cols) {
-  if (o == Py_None) return nullptr;
-  const Values v = values(o, 2);
-  if (v.n[0] != rows || v.n[1] != cols || v.scalar != type) throw Odd();
-  return v.p;
+// scores, k, score, bias, groups, group_k, renormalize, factor, expert, weight, slot, token, offsets, ws
+CALL(expert_route_balanced) {
+  return run<14>(n, [&] {
+    const Values s = values(a[0], 2);
+    const int64_t T = s.n[0], E = s.n[1], k = number(a[1]), score = number(a[2]), groups = number(a[4]), kept = number(a[5]);
+    const int renorm = PyObject_IsTrue(a[6]);
+    if (k < 1 || k > E || renorm < 0 || E > INT32_MAX || score < 0 || score > 1 || groups < 1 || groups > E || kept < 1 ||
+        kept > groups)
+      throw Odd();
+    const Workspace w = workspace(a[13]);
+    return free_of_lock(ctr_expert_route_balanced, s.p, s.type, T, (int32_t)E, s.ld(), (int32_t)k, (int)score,
+                        floats(a[3], {E}, true), (int32_t)groups, (int32_t)kept, renorm, number_f32(a[7]), ints(a[8], {T, k}),
+                        floats(a[9], {T, k}), ints(a[10], {T, k}), ints(a[11], {T * k}), ints(a[12], {E + 1}), w.p, w.n,
+                        stream());
+  });
 }
 
-float number_f32(PyObject* o) {
-  if (!PyFloat_Check(o)) throw Odd();
-  return (float)PyFloat_AS_DOUBLE(o);
+// dweight, scores, score, renormalize, factor, expert, dscores, ws
+CALL(expert_route_balanced_bwd) {
+  return run<8>(n, [&] {
+    const Values s = values(a[1], 2), d = values(a[6], 2);
+    const int64_t T = s.n[0], E = s.n[1], score = number(a[2]), k = size(a[5], 2, 1);
+    const int renorm = PyObject_IsTrue(a[3]);
+    if (d.n[0] != T || d.n[1] != E || d.scalar != s.scalar || k > E || renorm < 0 || score < 0 || score > 1) throw Odd();
+    const Workspace w = workspace(a[7]);
+    return free_of_lock(ctr_expert_route_balanced_bwd, floats(a[0], {T, k}), s.p, s.type, T, (int32_t)E, s.ld(), (int32_t)k,
+                        (int)score, renorm, number_f32(a[4]), ints(a[5], {T, k}), d.p, d.ld(), w.p, w.n, stream());
+  });
 }
 
 // x, w, bias, act, residual, y, pre, ws
@@ -350,7 +380,8 @@ PyMethodDef methods[] = {ENTRY(expert_route),          ENTRY(expert_route_bwd), 
                          ENTRY(fp8_quantize_rows_cols), ENTRY(fp8_quantize_blocks), ENTRY(fp8_matmul),
                          ENTRY(fp8_matmul_wgrad),      ENTRY(clip_grads),
                          ENTRY(dense),                 ENTRY(dense_bwd),          ENTRY(rms_norm),
-                         ENTRY(rms_norm_bwd),            {nullptr, nullptr, 0, nullptr}};
+                         ENTRY(rms_norm_bwd),          ENTRY(expert_route_balanced), ENTRY(expert_route_balanced_bwd),
+                               {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "ctr_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -44,6 +44,10 @@ struct RouteArgs {
   int64_t tokens, ld;
   int32_t experts, k, lanes, tile, tiles;  // lanes: per token; tile: tokens of a tile
   int32_t renormalize, vec;                // vec: rows start 16-byte aligned
+  float factor;                            // of the weights
+  // balanced routing
+  const float* bias;                       // NULL without
+  int32_t sigmoid, groups, group_k, seg;   // seg: lanes of a group of experts, 0 where groups end inside lanes
   int32_t* expert;
   float* weight;
   int32_t* slot;
@@ -93,6 +97,12 @@ __device__ __forceinline__ int expert_starts(const int* totals, int experts, int
   if (e < experts) start[e] = before + x - mine;
   __syncthreads();
   return all;
+}
+
+// What a choice's weight is in proportion to, by its score s and the choices' largest score m.  Sigmoids that fp32
+// cannot hold (all of them below e^-20) are in proportion to their exponentials.
+__device__ __forceinline__ float choice_value(const RouteArgs& a, float s, float m) {
+  return a.sigmoid && (m > -20.f || !a.renormalize) ? 1.f / (1.f + expf(-s)) : expf(s - m);
 }
 
 // What a lane learns of its group's token: choice `sub`'s score and expert (-1: none), the best score,
@@ -315,35 +325,11 @@ __device__ __forceinline__ void write_slots(const RouteArgs& a, int64_t t0, int 
   }
 }
 
-template <typename T, int EPL, int KMAX, bool CLUSTER>
-__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
-  extern __shared__ uint32_t bits[];  // [experts][tile / 32], then uint16 before[...] and int first[experts]
+// The order of a tile whose choices are in `bits`: its counts for the scan, or, where all tiles are this block's or
+// this cluster's, its choices' rows.
+template <bool CLUSTER>
+__device__ __forceinline__ void finish_tile(const RouteArgs& a, int64_t t0, int n, uint32_t* bits) {
   const int words = a.tile / 32;
-  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
-  const int n = (int)imin64(a.tile, a.tokens - t0);
-  for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
-  __syncthreads();
-  grid_wait();
-  const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
-  const int per_pass = kRouteThreads / a.lanes;
-  for (int p0 = 0; p0 < n; p0 += per_pass) {  // the same trips in every lane: the shuffles need all of them
-    const int tl = p0 + (int)threadIdx.x / a.lanes;
-    const bool mine = tl < n;
-    // lane j of the group has choice j
-    const Choice c = Chooser<T, EPL, KMAX>::run(a, (const T*)a.scores + (t0 + tl) * a.ld, mine, sub);
-    const float z = c.expert >= 0 ? expf(c.value - c.best) : 0.f;
-    float total = c.total;
-    if (a.renormalize) {
-      total = z;
-      for (int o = 1; o < a.lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
-    }
-    if (mine && sub < a.k) {
-      const int64_t at = (t0 + tl) * a.k + sub;
-      a.expert[at] = c.expert;
-      a.weight[at] = c.expert >= 0 ? z / total : 0.f;
-      if (c.expert >= 0) atomicOr(&bits[c.expert * words + (tl >> 5)], 1u << (tl & 31));
-    }
-  }
   __syncthreads();
   if (!CLUSTER && a.tiles > 1) {
     for (int e = threadIdx.x; e < a.experts; e += kRouteThreads) {
@@ -399,6 +385,274 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
     a.token[r] = -1;
   __syncthreads();
   if constexpr (CLUSTER) cluster_sync();  // no block leaves while another reads its counts
+}
+
+template <typename T, int EPL, int KMAX, bool CLUSTER>
+__global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const RouteArgs a) {
+  extern __shared__ uint32_t bits[];  // [experts][tile / 32], then uint16 before[...] and int first[experts]
+  const int words = a.tile / 32;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
+  const int n = (int)imin64(a.tile, a.tokens - t0);
+  for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
+  __syncthreads();
+  grid_wait();
+  const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
+  const int per_pass = kRouteThreads / a.lanes;
+  for (int p0 = 0; p0 < n; p0 += per_pass) {  // the same trips in every lane: the shuffles need all of them
+    const int tl = p0 + (int)threadIdx.x / a.lanes;
+    const bool mine = tl < n;
+    // lane j of the group has choice j
+    const Choice c = Chooser<T, EPL, KMAX>::run(a, (const T*)a.scores + (t0 + tl) * a.ld, mine, sub);
+    const float z = c.expert >= 0 ? expf(c.value - c.best) : 0.f;
+    float total = c.total;
+    if (a.renormalize) {
+      total = z;
+      for (int o = 1; o < a.lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
+    }
+    if (mine && sub < a.k) {
+      const int64_t at = (t0 + tl) * a.k + sub;
+      a.expert[at] = c.expert;
+      a.weight[at] = c.expert >= 0 ? z / total : 0.f;
+      if (c.expert >= 0) atomicOr(&bits[c.expert * words + (tl >> 5)], 1u << (tl & 31));
+    }
+  }
+  finish_tile<CLUSTER>(a, t0, n, bits);
+}
+
+// ---------------------------------------------------------------------------
+// Balanced routing: keys (score function + bias), groups, weights from the score function
+// ---------------------------------------------------------------------------
+// Keys are compared as real numbers.  They are computed in fp32 with a bound on their errors; where two that have to
+// be told apart are nearer than that (one token in a thousand), the warp does its tokens again in 64 bits, whose
+// arithmetic is too slow to do all of them in.
+template <typename K>
+__device__ __forceinline__ K exp_of(K x);
+template <>
+__device__ __forceinline__ float exp_of<float>(float x) {
+  return expf(x);
+}
+template <>
+__device__ __forceinline__ double exp_of<double>(double x) {
+  return exp(x);
+}
+
+// A softmax's shift and sum over a row, from a lane's scores (-inf: masked).
+template <typename K, int EPL>
+__device__ __forceinline__ K row_softmax(const float (&v)[EPL], int lanes, float& m) {
+  m = v[0];
+#pragma unroll
+  for (int i = 1; i < EPL; ++i) m = fmaxf(m, v[i]);
+  for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  if (!(m > -INFINITY)) m = 0.f;
+  K total = 0;
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) total += exp_of<K>((K)v[i] - (K)m);
+  for (int o = 1; o < lanes; o <<= 1) total += __shfl_xor_sync(kFull, total, o);
+  return total;
+}
+
+// The two largest of a group's keys, in falling order, -inf for none; r: the scores that they are of.
+template <typename K>
+struct Pair {
+  K k0, k1;
+  float r0, r1;
+  __device__ __forceinline__ void take(K k, float r) {
+    if (k > k0) {
+      k1 = k0;
+      r1 = r0;
+      k0 = k;
+      r0 = r;
+    } else if (k > k1) {
+      k1 = k;
+      r1 = r;
+    }
+  }
+  __device__ __forceinline__ void join(int o) {
+    const K a = __shfl_xor_sync(kFull, k0, o), b = __shfl_xor_sync(kFull, k1, o);
+    const float x = __shfl_xor_sync(kFull, r0, o), y = __shfl_xor_sync(kFull, r1, o);
+    take(a, x);
+    take(b, y);
+  }
+};
+
+// The expert of choice `sub` of the lanes' token, -1: none.  v: the lane's scores (-inf: masked, all of them for a
+// token that is routed nowhere); b: its experts' biases.  near: whether a decision was too near to call.
+template <typename K, int EPL>
+__device__ __forceinline__ int choose_balanced(const RouteArgs& a, const float (&v)[EPL], const float (&b)[EPL], int sub,
+                                               bool& near) {
+  constexpr bool kExact = sizeof(K) == 8;
+  const K none = -INFINITY;
+  const int base = sub * EPL, per = a.experts / a.groups;
+  const bool plain = !a.bias;  // then the scores themselves are in the keys' order
+  float m = 0.f;
+  K total = 1, key[EPL];
+  // what a key may be off by, over 2^-24: sigmoid, expf 4, sum, division; softmax, its largest p times: expf 4, the
+  // exponent's rounding (below 0.4 of p = 1), a sum of 16 + 5 additions of such terms, division.  Their bias's sum: 1.
+  float err = 7.f;
+  if (!a.sigmoid) {
+    total = row_softmax<K, EPL>(v, a.lanes, m);
+    err = 40.f / (float)total;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    K p;
+    if (a.sigmoid) p = (K)1 / ((K)1 + exp_of<K>(-(K)v[i]));
+    else p = exp_of<K>((K)v[i] - (K)m) / total;
+    key[i] = v[i] > -INFINITY && b[i] > -INFINITY ? p + (K)b[i] : none;
+  }
+  constexpr float kUnit = 0x1p-24f;
+  near = false;
+  if (a.group_k < a.groups) {
+    // lane g learns group g's two best keys
+    Pair<K> best = {none, none, -INFINITY, -INFINITY};
+    if (a.seg) {
+      Pair<K> own = {none, none, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) own.take(key[i], v[i]);
+      for (int o = 1; o < a.seg; o <<= 1) own.join(o);
+      const int from = sub * a.seg;
+      best.k0 = __shfl_sync(kFull, own.k0, from, a.lanes);
+      best.k1 = __shfl_sync(kFull, own.k1, from, a.lanes);
+      best.r0 = __shfl_sync(kFull, own.r0, from, a.lanes);
+      best.r1 = __shfl_sync(kFull, own.r1, from, a.lanes);
+    } else {
+      for (int g = 0; g < a.groups; ++g) {
+        Pair<K> own = {none, none, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const int e = base + i;
+          if (e >= g * per && e < (g + 1) * per) own.take(key[i], v[i]);
+        }
+        for (int o = 1; o < a.lanes; o <<= 1) own.join(o);
+        if (g == sub) best = own;
+      }
+    }
+    const bool some = sub < a.groups && best.k0 > none;
+    const K worth = some ? (best.k1 > none ? best.k0 + best.k1 : best.k0) : none;
+    const float size = some ? fabsf((float)best.k0) + (best.k1 > none ? fabsf((float)best.k1) : 0.f) : 0.f;
+    int place = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const K other = __shfl_sync(kFull, worth, g, a.lanes);
+      place += other > worth || (other == worth && g < sub);
+      if constexpr (!kExact) {
+        const float r0 = __shfl_sync(kFull, best.r0, g, a.lanes), r1 = __shfl_sync(kFull, best.r1, g, a.lanes);
+        const bool same = plain && r0 == best.r0 && r1 == best.r1;
+        // two keys each: what they may be off by, their bias's sum and theirs
+        const float room = kUnit * (4.f * err + 2.f * (size + __shfl_sync(kFull, size, g, a.lanes)));
+        if (g != sub && some && other > none && !same && fabsf((float)(worth - other)) <= room) near = true;
+      }
+    }
+    const int lane = threadIdx.x & 31;
+    const uint32_t kept = __ballot_sync(kFull, some && place < a.group_k) >> (lane & ~(a.lanes - 1));
+    int g = base / per, left = per - base % per;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      if (g >= a.groups || !((kept >> g) & 1)) key[i] = none;
+      if (--left == 0) {
+        ++g;
+        left = per;
+      }
+    }
+  }
+  if (plain) {  // their order is the keys', without rounding
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = key[i] > none ? (K)v[i] : none;
+  }
+  int expert = -1;
+  K last = none;
+  for (int j = 0; j < a.k + (kExact || plain ? 0 : 1); ++j) {
+    K best = key[0];
+#pragma unroll
+    for (int i = 1; i < EPL; ++i) best = key[i] > best ? key[i] : best;
+    for (int o = 1; o < a.lanes; o <<= 1) {
+      const K other = __shfl_xor_sync(kFull, best, o);
+      best = other > best ? other : best;
+    }
+    if constexpr (!kExact) {
+      if (!plain && j > 0 && best > none &&
+          (float)(last - best) <= kUnit * (2.f * err + fabsf((float)last) + fabsf((float)best)))
+        near = true;
+      last = best;
+      if (j == a.k) break;
+    }
+    int at = 0x7fffffff;
+#pragma unroll
+    for (int i = EPL - 1; i >= 0; --i) at = key[i] == best ? base + i : at;
+    for (int o = 1; o < a.lanes; o <<= 1) at = min(at, __shfl_xor_sync(kFull, at, o));
+    if (best > none && j == sub) expert = at;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) key[i] = base + i == at ? none : key[i];
+  }
+  return expert;
+}
+
+template <typename T, int EPL, bool CLUSTER>
+__global__ void __launch_bounds__(kRouteThreads) route_balanced_kernel(const RouteArgs a) {
+  extern __shared__ uint32_t bits[];  // as in route_choose_kernel
+  const int words = a.tile / 32;
+  const int64_t t0 = (int64_t)blockIdx.x * a.tile;
+  const int n = (int)imin64(a.tile, a.tokens - t0);
+  for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
+  __syncthreads();
+  grid_wait();
+  const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
+  const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
+  float b[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    b[i] = a.bias && sub * EPL + i < a.experts ? a.bias[sub * EPL + i] : 0.f;
+    if (!(b[i] < INFINITY)) {  // NaN, +inf: as -inf, and flagged
+      b[i] = -INFINITY;
+      set_error(a.err, CTR_ERR_BAD_VALUE);
+    }
+  }
+  const int per_pass = kRouteThreads / a.lanes;
+  for (int p0 = 0; p0 < n; p0 += per_pass) {  // the same trips in every lane: the shuffles need all of them
+    const int tl = p0 + (int)threadIdx.x / a.lanes;
+    const bool mine = tl < n;
+    const T* row = (const T*)a.scores + (t0 + tl) * a.ld;
+    float v[EPL];
+    if (mine) {
+      load_scores<T, EPL>(row, sub * EPL, a.experts, a.vec != 0, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+    }
+    bool odd = false;  // NaN or +inf: the token is routed nowhere
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) odd |= !(v[i] < INFINITY);
+    if (__ballot_sync(kFull, odd) & group) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
+      if (sub == 0) set_error(a.err, CTR_ERR_BAD_VALUE);
+    }
+    bool near, again;
+    int expert = choose_balanced<float, EPL>(a, v, b, sub, near);
+    if (__any_sync(kFull, near)) expert = choose_balanced<double, EPL>(a, v, b, sub, again);
+    // weights: lane j has choice j
+    const bool live = expert >= 0;
+    const float s = live ? to_f32<T>(row[expert]) : -INFINITY;
+    float z, sum = 1.f, m = 0.f;
+    if (a.renormalize || a.sigmoid) {
+      m = s;
+      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      z = live ? choice_value(a, s, m) : 0.f;
+      if (a.renormalize) {
+        sum = z;
+        for (int o = 1; o < a.lanes; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+      }
+    } else {
+      sum = row_softmax<float, EPL>(v, a.lanes, m);
+      z = live ? expf(s - m) : 0.f;
+    }
+    if (mine && sub < a.k) {
+      const int64_t at = (t0 + tl) * a.k + sub;
+      a.expert[at] = expert;
+      a.weight[at] = live ? a.factor * (z / sum) : 0.f;
+      if (live) atomicOr(&bits[expert * words + (tl >> 5)], 1u << (tl & 31));
+    }
+  }
+  finish_tile<CLUSTER>(a, t0, n, bits);
 }
 
 // counts[tile][e] -> exclusive sum over the tiles, and the totals: 32 experts to a block, one to a
@@ -491,7 +745,7 @@ __device__ __forceinline__ void store_scores(T* out, int base, int experts, bool
   }
 }
 
-// Softmax over the choices: lane j of a token's lanes (as few as hold its choices) reads choice j's score
+// Softmax over the choices, or sigmoids: lane j of a token's lanes (as few as hold its choices) reads choice j's score
 // alone.  The other scores' gradient is zero: the lanes write the row's zeros first, then each its choice
 // over them (selecting the values' places in registers took twice the instructions: 131072 x 64 bf16, k 4,
 // 18.4 us against 14.3; 256, k 8, 61 against 29).
@@ -510,7 +764,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_choices_kernel(const 
     const int e = mine && sub < a.k ? a.expert[t * a.k + sub] : -1;
     const bool live = e >= 0 && e < a.experts;
     const float l = live ? to_f32<T>(((const T*)a.scores)[t * a.ld + e]) : -INFINITY;
-    const float g = live ? dweight[t * a.k + sub] : 0.f;
+    const float g = live ? a.factor * dweight[t * a.k + sub] : 0.f;
     if (mine) {
       int done = 0;
       if (vec_out) {
@@ -521,7 +775,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_choices_kernel(const 
     }
     float m = l;
     for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    const float z = live ? expf(l - m) : 0.f;
+    const float z = live ? choice_value(a, l, m) : 0.f;
     float total = z, dot = z * g;
     for (int o = 1; o < a.lanes; o <<= 1) {
       total += __shfl_xor_sync(kFull, total, o);
@@ -530,7 +784,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_choices_kernel(const 
     __syncwarp();  // the row's zeros come before its choices
     if (live) {    // then total >= its own exponential > 0
       const float inv = 1.f / total;
-      out[e] = from_f32<T>(z * inv * (g - dot * inv));
+      float d = a.renormalize ? z * inv * (g - dot * inv) : z * g;
+      if (a.sigmoid) d *= 1.f / (1.f + expf(l));  // d ln p / dl = 1 - p
+      out[e] = from_f32<T>(d);
     }
   }
 }
@@ -551,7 +807,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_kernel(const RouteArg
     // lane j has choice j
     const int e = mine && sub < a.k ? a.expert[t * a.k + sub] : -1;
     const bool live = e >= 0 && e < a.experts;
-    const float g = live ? dweight[t * a.k + sub] : 0.f;
+    const float g = live ? a.factor * dweight[t * a.k + sub] : 0.f;
     const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
     // a token with no choice (all masked, or flagged by the routing) has no gradient
     const bool routed = (__ballot_sync(kFull, live) & group) != 0;
@@ -680,6 +936,14 @@ bool launch_choose(const RouteArgs& a, size_t smem, bool& cluster, cudaStream_t 
                   : launch_choose<T, EPL, CTR_MAX_CHOICES>(a, smem, cluster, s);
 }
 
+template <typename T, int EPL>
+bool launch_balanced(const RouteArgs& a, size_t smem, bool& cluster, cudaStream_t s) {
+  cluster = cluster && largest_cluster_fits<route_balanced_kernel<T, EPL, true>>();
+  auto k = cluster ? route_balanced_kernel<T, EPL, true> : route_balanced_kernel<T, EPL, false>;
+  return launch_after(k, dim3((unsigned)a.tiles), kRouteThreads, smem, s, cluster ? (unsigned)a.tiles : 1u, a) ==
+         cudaSuccess;
+}
+
 // Lanes of a token whose softmax is over its choices: one for each, and enough that the row's zeros leave
 // in pieces of 64 bytes a lane (131072 rows of 64 bf16, k 1: 2 lanes 12.3 us, one 16.4, 8 16.4; 128 fp32, k
 // 2: 8 lanes 22.5, 2 24.6), of 32 where rows are not 16-byte aligned (63 fp32, k 2: 8 lanes 18.4, 4 22.5, 2
@@ -691,8 +955,9 @@ int choice_lanes(int row_bytes, int k, int vec_out) {
 template <typename T>
 void launch_bwd(RouteArgs& a, const float* dweight, T* dscores, int64_t ldd, int vec_out, cudaStream_t s) {
   const int per = lane_scores(a.experts);
-  a.lanes = a.renormalize ? choice_lanes(a.experts * (int)sizeof(T), a.k, vec_out) : route_lanes(a.experts, a.k, per);
-  auto k = a.renormalize ? route_bwd_choices_kernel<T> : per == 16 ? route_bwd_kernel<T, 16> : route_bwd_kernel<T, 8>;
+  const bool choices = a.renormalize || a.sigmoid;
+  a.lanes = choices ? choice_lanes(a.experts * (int)sizeof(T), a.k, vec_out) : route_lanes(a.experts, a.k, per);
+  auto k = choices ? route_bwd_choices_kernel<T> : per == 16 ? route_bwd_kernel<T, 16> : route_bwd_kernel<T, 8>;
   const int grid = (int)imin64(ceil_div(a.tokens * a.lanes, kRouteThreads), (int64_t)num_sms() * 8);
   launch_after(k, dim3(grid), kRouteThreads, 0, s, 1, a, dweight, dscores, ldd, vec_out);
 }
@@ -926,10 +1191,20 @@ extern "C" size_t ctr_expert_route_workspace_size(int64_t tokens, int32_t expert
 
 extern "C" int ctr_set_route_cluster(int on) { return g_route_cluster.exchange(on ? 1 : 0); }
 
-extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts,
-                                int64_t ld_scores, int32_t k, int renormalize, int32_t* expert, float* weight,
-                                int32_t* slot, int32_t* token, int32_t* offsets, void* ws, size_t ws_bytes,
-                                ctr_stream_t stream) {
+namespace ctr {
+namespace {
+
+// Score function, bias and groups of a routing; the default is none of them.
+struct Balance {
+  bool on = false, sigmoid = false;
+  const float* bias = nullptr;
+  int32_t groups = 1, group_k = 1;
+  float factor = 1.f;
+};
+
+int route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, int64_t ld_scores, int32_t k, int renormalize,
+          const Balance& b, int32_t* expert, float* weight, int32_t* slot, int32_t* token, int32_t* offsets, void* ws,
+          size_t ws_bytes, ctr_stream_t stream) {
   const int st = check_route(scores, dtype, tokens, experts, ld_scores, k);
   if (st != CTR_OK) return st;
   if (!offsets || (tokens > 0 && (!expert || !weight || !slot || !token))) return CTR_ERR_INVALID_ARG;
@@ -945,13 +1220,23 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   a.ld = ld_scores;
   a.experts = experts;
   a.k = k;
-  const int per = lane_scores(experts);
+  int per = lane_scores(experts);
+  const int members = experts / b.groups;
+  const bool grouped = b.group_k < b.groups;
+  if (grouped && members % per != 0 && members % 8 == 0 && experts <= 256) per = 8;  // groups of whole lanes, if they can be
   a.lanes = route_lanes(experts, k, per);
+  while (grouped && a.lanes < b.groups) a.lanes *= 2;  // a lane for each group
+  if (grouped && members % per == 0 && ((members / per) & (members / per - 1)) == 0) a.seg = members / per;
   a.tile = route_tile(tokens, experts);
   a.tiles = (int32_t)ceil_div(tokens, a.tile);
   a.renormalize = renormalize != 0;
   const int eb = dtype_bytes(dtype);
   a.vec = ((uintptr_t)scores % 16) == 0 && (ld_scores * eb) % 16 == 0;
+  a.factor = b.factor;
+  a.bias = b.bias;
+  a.sigmoid = b.sigmoid;
+  a.groups = b.groups;
+  a.group_k = b.group_k;
   a.expert = expert;
   a.weight = weight;
   a.slot = slot;
@@ -962,10 +1247,17 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   a.err = (int*)ws;
   const size_t smem = route_smem(experts, a.tile);
   bool cluster = a.tiles > 1 && a.tiles <= kClusterTiles && g_route_cluster.load(std::memory_order_relaxed) != 0;
-  const bool ok = dtype == CTR_F32 ? (per == 8 ? launch_choose<float, 8>(a, smem, cluster, s)
-                                               : launch_choose<float, 16>(a, smem, cluster, s))
-                                   : (per == 8 ? launch_choose<__nv_bfloat16, 8>(a, smem, cluster, s)
-                                               : launch_choose<__nv_bfloat16, 16>(a, smem, cluster, s));
+  bool ok;
+  if (b.on)
+    ok = dtype == CTR_F32 ? (per == 8 ? launch_balanced<float, 8>(a, smem, cluster, s)
+                                      : launch_balanced<float, 16>(a, smem, cluster, s))
+                          : (per == 8 ? launch_balanced<__nv_bfloat16, 8>(a, smem, cluster, s)
+                                      : launch_balanced<__nv_bfloat16, 16>(a, smem, cluster, s));
+  else
+    ok = dtype == CTR_F32 ? (per == 8 ? launch_choose<float, 8>(a, smem, cluster, s)
+                                      : launch_choose<float, 16>(a, smem, cluster, s))
+                          : (per == 8 ? launch_choose<__nv_bfloat16, 8>(a, smem, cluster, s)
+                                      : launch_choose<__nv_bfloat16, 16>(a, smem, cluster, s));
   if (!ok) return CTR_ERR_CUDA;
   if (a.tiles > 1 && !cluster) {
     launch_after(route_scan_kernel, dim3((unsigned)ceil_div(experts, 32)), 1024, 0, s, 1, a);
@@ -974,10 +1266,9 @@ extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tok
   return launch_status();
 }
 
-extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ctr_dtype dtype, int64_t tokens,
-                                    int32_t experts, int64_t ld_scores, int32_t k, int renormalize,
-                                    const int32_t* expert, void* dscores, int64_t ld_dscores, void* ws,
-                                    size_t ws_bytes, ctr_stream_t stream) {
+int route_bwd(const float* dweight, const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, int64_t ld_scores,
+              int32_t k, int renormalize, bool sigmoid, float factor, const int32_t* expert, void* dscores,
+              int64_t ld_dscores, void* ws, size_t ws_bytes, ctr_stream_t stream) {
   const int st = check_route(scores, dtype, tokens, experts, ld_scores, k);
   if (st != CTR_OK) return st;
   if (ld_dscores < experts || (tokens > 0 && (!dweight || !expert || !dscores))) return CTR_ERR_INVALID_ARG;
@@ -991,6 +1282,8 @@ extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ct
   a.experts = experts;
   a.k = k;
   a.renormalize = renormalize != 0;
+  a.sigmoid = sigmoid;
+  a.factor = factor;
   const int eb = dtype_bytes(dtype);
   a.vec = ((uintptr_t)scores % 16) == 0 && (ld_scores * eb) % 16 == 0;
   const int vec_out = ((uintptr_t)dscores % 16) == 0 && (ld_dscores * eb) % 16 == 0;
@@ -1000,6 +1293,58 @@ extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ct
   if (dtype == CTR_F32) launch_bwd(a, dweight, (float*)dscores, ld_dscores, vec_out, s);
   else launch_bwd(a, dweight, (__nv_bfloat16*)dscores, ld_dscores, vec_out, s);
   return launch_status();
+}
+
+bool score_ok(int score) { return score == CTR_SCORE_SOFTMAX || score == CTR_SCORE_SIGMOID; }
+
+}  // namespace
+}  // namespace ctr
+
+extern "C" int ctr_expert_route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts,
+                                int64_t ld_scores, int32_t k, int renormalize, int32_t* expert, float* weight,
+                                int32_t* slot, int32_t* token, int32_t* offsets, void* ws, size_t ws_bytes,
+                                ctr_stream_t stream) {
+  return route(scores, dtype, tokens, experts, ld_scores, k, renormalize, Balance(), expert, weight, slot, token, offsets, ws,
+               ws_bytes, stream);
+}
+
+extern "C" int ctr_expert_route_bwd(const float* dweight, const void* scores, ctr_dtype dtype, int64_t tokens,
+                                    int32_t experts, int64_t ld_scores, int32_t k, int renormalize,
+                                    const int32_t* expert, void* dscores, int64_t ld_dscores, void* ws,
+                                    size_t ws_bytes, ctr_stream_t stream) {
+  return route_bwd(dweight, scores, dtype, tokens, experts, ld_scores, k, renormalize, false, 1.f, expert, dscores, ld_dscores,
+                   ws, ws_bytes, stream);
+}
+
+extern "C" int ctr_expert_route_balanced(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts,
+                                         int64_t ld_scores, int32_t k, int score, const float* bias, int32_t groups,
+                                         int32_t group_k, int renormalize, float factor, int32_t* expert, float* weight,
+                                         int32_t* slot, int32_t* token, int32_t* offsets, void* ws, size_t ws_bytes,
+                                         ctr_stream_t stream) {
+  const int st = check_route(scores, dtype, tokens, experts, ld_scores, k);
+  if (st != CTR_OK) return st;
+  if (!score_ok(score) || groups < 1 || group_k < 1 || group_k > groups || experts % groups != 0 ||
+      k > group_k * (experts / groups) || !(factor < INFINITY) || !(factor > -INFINITY) || ((uintptr_t)bias % 4) != 0)
+    return CTR_ERR_INVALID_ARG;
+  if (groups > CTR_MAX_GROUPS) return CTR_ERR_UNSUPPORTED;
+  Balance b;
+  b.on = true;
+  b.sigmoid = score == CTR_SCORE_SIGMOID;
+  b.bias = bias;
+  b.groups = groups;
+  b.group_k = group_k;
+  b.factor = factor;
+  return route(scores, dtype, tokens, experts, ld_scores, k, renormalize, b, expert, weight, slot, token, offsets, ws, ws_bytes,
+               stream);
+}
+
+extern "C" int ctr_expert_route_balanced_bwd(const float* dweight, const void* scores, ctr_dtype dtype, int64_t tokens,
+                                             int32_t experts, int64_t ld_scores, int32_t k, int score, int renormalize,
+                                             float factor, const int32_t* expert, void* dscores, int64_t ld_dscores,
+                                             void* ws, size_t ws_bytes, ctr_stream_t stream) {
+  if (!score_ok(score) || !(factor < INFINITY) || !(factor > -INFINITY)) return CTR_ERR_INVALID_ARG;
+  return route_bwd(dweight, scores, dtype, tokens, experts, ld_scores, k, renormalize, score == CTR_SCORE_SIGMOID, factor,
+                   expert, dscores, ld_dscores, ws, ws_bytes, stream);
 }
 
 extern "C" int ctr_expert_dispatch(const void* x, ctr_dtype dtype, int64_t tokens, int32_t d, int64_t ldx, int32_t k,

@@ -92,6 +92,10 @@ _SIGS = {
     "ctr_fp8_matmul_workspace_size": (_sz, [_i64, _i32, _i64, _i64]),
     "ctr_fp8_matmul": (C.c_int, [_p, _p, _i64, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _i64, _p, _sz, _p]),
     "ctr_fp8_matmul_wgrad": (C.c_int, [_p, _p, _p, _p, _p, _i64, _i32, _i64, _i64, _p, C.c_int, _p, _sz, _p]),
+    "ctr_expert_route_balanced": (C.c_int, [_p, C.c_int, _i64, _i32, _i64, _i32, C.c_int, _p, _i32, _i32, C.c_int, _f32, _p,
+                                            _p, _p, _p, _p, _p, _sz, _p]),
+    "ctr_expert_route_balanced_bwd": (C.c_int, [_p, _p, C.c_int, _i64, _i32, _i64, _i32, C.c_int, C.c_int, _f32, _p, _p,
+                                                _i64, _p, _sz, _p]),
     "ctr_dense_workspace_size": (_sz, [_i64, _i64, _i64, C.c_int, C.c_int, C.c_int]),
     "ctr_dense": (C.c_int, [_p, C.c_int, _i64, _i64, _i64, _p, _i64, _i64, _p, C.c_int, _p, _i64, _p, _i64, _p, _i64, _p,
                             _sz, _p]),
@@ -847,6 +851,50 @@ def _dense_or_none(t: Optional[torch.Tensor], what: str, dtype, shape):
         return None
     _dense(t, what, dtype, shape)
     return t.data_ptr()
+
+
+MAX_GROUPS = 32
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+
+
+def ctr_expert_route_balanced(scores: torch.Tensor, k: int, score: int, bias: Optional[torch.Tensor], groups: int,
+                              group_k: int, renormalize: bool, factor: float, expert: torch.Tensor,
+                              weight: torch.Tensor, slot: torch.Tensor, token: torch.Tensor, offsets: torch.Tensor,
+                              ws: torch.Tensor, stream=None) -> None:
+    """ctr_expert_route by the largest score function + bias within the best groups of experts."""
+    if stream is None and _took("ctr_expert_route_balanced", _usual().expert_route_balanced(
+            scores, k, score, bias, groups, group_k, renormalize, factor, expert, weight, slot, token, offsets, ws)):
+        return
+    T, E, ld = _mat(scores, "scores")
+    pb = _dense_or_none(bias, "bias", _F32, (E,))
+    tk = (T, k)
+    _dense(expert, "expert", _I32, tk)
+    _dense(weight, "weight", _F32, tk)
+    _dense(slot, "slot", _I32, tk)
+    _dense(token, "token", _I32, (T * k,))
+    _dense(offsets, "offsets", _I32, (E + 1,))
+    _ok("ctr_expert_route_balanced", lib().ctr_expert_route_balanced(
+        scores.data_ptr(), DTYPES[scores.dtype], T, E, ld, k, score, pb, groups, group_k, 1 if renormalize else 0, factor,
+        expert.data_ptr(), weight.data_ptr(), slot.data_ptr(), token.data_ptr(), offsets.data_ptr(), *_room(ws),
+        _stream(stream)))
+
+
+def ctr_expert_route_balanced_bwd(dweight: torch.Tensor, scores: torch.Tensor, score: int, renormalize: bool,
+                                  factor: float, expert: torch.Tensor, dscores: torch.Tensor, ws: torch.Tensor,
+                                  stream=None) -> None:
+    if stream is None and _took("ctr_expert_route_balanced_bwd", _usual().expert_route_balanced_bwd(
+            dweight, scores, score, renormalize, factor, expert, dscores, ws)):
+        return
+    T, E, ld = _mat(scores, "scores")
+    _want(isinstance(expert, torch.Tensor) and expert.dim() == 2, "expert must be a matrix")
+    k = expert.shape[1]
+    _dense(expert, "expert", _I32, (T, k))
+    _dense(dweight, "dweight", _F32, (T, k))
+    ldd = _like(dscores, "dscores", T, E, scores.dtype)
+    _ok("ctr_expert_route_balanced_bwd", lib().ctr_expert_route_balanced_bwd(
+        dweight.data_ptr(), scores.data_ptr(), DTYPES[scores.dtype], T, E, ld, k, score, 1 if renormalize else 0, factor,
+        expert.data_ptr(), dscores.data_ptr(), ldd, *_room(ws), _stream(stream)))
 
 
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_SIGMOID = 0, 1, 2, 3, 4

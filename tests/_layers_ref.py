@@ -122,3 +122,80 @@ def dz64(dtype, act, dy, pre):
     mid = dz.to(torch.bfloat16).double()
     lo, hi = (dz - err).to(torch.bfloat16).double(), (dz + err).to(torch.bfloat16).double()
     return mid, torch.maximum(hi - mid, mid - lo), dz, err
+
+
+# ---------------------------------------------------------------------------
+# balanced routing
+# ---------------------------------------------------------------------------
+def balanced(s, k, score, bias, groups, group_k, renorm, factor):
+    """(expert, weight, slot, token, offsets, p) of scores s (fp64)."""
+    s = np.array(s, dtype=np.float64)
+    T, E = s.shape
+    s[(np.isnan(s) | (s == np.inf)).any(axis=1)] = -np.inf
+    b = np.zeros(E) if bias is None else np.where(np.asarray(bias) < np.inf, np.asarray(bias, dtype=np.float64), -np.inf)
+    live = s > -np.inf
+    with np.errstate(over="ignore"):
+        if score == "sigmoid":
+            p = np.where(live, 1 / (1 + np.exp(-s)), 0.0)
+        else:
+            m = np.where(live.any(axis=1), s.max(axis=1, initial=-np.inf), 0.0)[:, None]
+            p = np.where(live, np.exp(s - m), 0.0)
+            p = p / np.maximum(p.sum(axis=1, keepdims=True), 1e-300)
+    key = np.where(live, p + b, -np.inf)
+    if group_k < groups:
+        per = E // groups
+        member = -np.sort(-key.reshape(T, groups, per), axis=2)[:, :, :2]
+        worth = np.where(np.isfinite(member), member, 0.0).sum(axis=2)
+        worth = np.where(np.isfinite(member).any(axis=2), worth, -np.inf)
+        stay = np.argsort(-worth, axis=1, kind="stable")[:, :group_k]
+        kept = np.zeros((T, groups), dtype=bool)
+        np.put_along_axis(kept, stay, True, axis=1)
+        key = np.where(np.repeat(kept, per, axis=1), key, -np.inf)
+    # without a bias the scores' order is the keys'
+    order = np.argsort(-(key if bias is not None else np.where(key > -np.inf, s, -np.inf)), axis=1, kind="stable")[:, :k]
+    has = np.take_along_axis(key, order, 1) > -np.inf
+    w = np.where(has, np.take_along_axis(p, order, 1), 0.0)
+    if renorm:
+        if score == "sigmoid":   # in proportion, whatever 64 bits can hold
+            ls = np.where(has, -np.logaddexp(0, -np.take_along_axis(s, order, 1)), -np.inf)
+            w = np.where(has, np.exp(ls - np.where(has.any(axis=1), ls.max(axis=1), 0.0)[:, None]), 0.0)
+        w = w / np.where(w.sum(axis=1) > 0, w.sum(axis=1), 1.0)[:, None]
+    expert = np.where(has, order, -1).astype(np.int32)
+    flat = np.where(has, order, E).ravel()
+    at = np.argsort(flat, kind="stable")
+    count = int(has.sum())
+    slot, token = np.full(T * k, -1, dtype=np.int32), np.full(T * k, -1, dtype=np.int32)
+    slot[at[:count]] = np.arange(count)
+    token[:count] = at[:count] // k
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(flat, minlength=E + 1)[:E])]).astype(np.int32)
+    return expert, factor * w, slot.reshape(T, k), token, offsets, p
+
+
+def balanced_grad(dw, s, score, renorm, factor, expert, p):
+    """(dscores, magnitudes that its tolerance goes by) for choices `expert` and score functions p."""
+    T, E = s.shape
+    has = expert >= 0
+    at = np.where(has, expert, 0)
+    pj = np.where(has, np.take_along_axis(p, at, 1), 0.0)
+    if renorm:
+        sj = np.take_along_axis(s, at, 1)
+        ls = np.where(has, -np.logaddexp(0, -sj) if score == "sigmoid" else sj, -np.inf)
+        wj = np.where(has, np.exp(ls - np.where(has.any(axis=1), ls.max(axis=1), 0.0)[:, None]), 0.0)
+        wj = wj / np.where(wj.sum(axis=1) > 0, wj.sum(axis=1), 1.0)[:, None]
+    else:
+        wj = pj
+    g = np.where(has, factor * dw, 0.0)
+    dot, mag = (wj * g).sum(axis=1, keepdims=True), np.abs(wj * g).sum(axis=1, keepdims=True)
+    out, size = np.zeros((T, E)), np.zeros((T, E))
+    if score == "softmax" and not renorm:
+        full = np.zeros((T, E))
+        t, j = np.nonzero(has)
+        full[t, expert[t, j]] = g[t, j]
+        routed = has.any(axis=1, keepdims=True)
+        return np.where(routed, p * (full - dot), 0.0), np.abs(p * full) + p * mag
+    slope = 1 - pj if score == "sigmoid" else np.ones_like(pj)
+    d = wj * (g - dot) * slope if renorm else wj * g * slope
+    m = (np.abs(wj * g) + (wj * mag if renorm else 0)) * (slope if score == "softmax" else 1)
+    t, j = np.nonzero(has)
+    out[t, expert[t, j]], size[t, expert[t, j]] = d[t, j], m[t, j]
+    return out, size

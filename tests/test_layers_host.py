@@ -73,3 +73,24 @@ def test_dense_refusals(lib):
     assert size(-1, 24, 16, 0, 0, 0) == 0 and size(4, 0, 16, 0, 0, 0) == 0 and size(4, 24, 16, 7, 0, 0) == 0
     assert size(40, 24, 16, 1, 0, 0) == 256 and size(40, 24, 16, 1, 0, 1) > 256 and size(40, 24, 16, 0, 0, 0) > 256
     assert size(40, 24, 16, 1, 1, 0) < size(40, 24, 16, 0, 1, 0)
+
+
+def test_balanced_routing_refusals(lib):
+    def call(scores=P, dt=0, tokens=10, experts=8, ld=8, k=2, score=1, bias=P, groups=4, kept=2, factor=1.0, expert=P,
+             offsets=P, size=1 << 30):
+        return lib.ctr_expert_route_balanced(scores, dt, tokens, experts, ld, k, score, bias, groups, kept, 1,
+                                             C.c_float(factor), expert, P, P, P, offsets, P, size, None)
+    assert call(scores=None) == -1 and call(expert=None) == -1 and call(offsets=None) == -1 and call(dt=2) == -1
+    assert call(score=2) == -1 and call(score=-1) == -1 and call(bias=ODD) == -1 and call(ld=7) == -1 and call(k=0) == -1
+    assert call(groups=3) == -1 and call(groups=0) == -1 and call(kept=0) == -1 and call(kept=5) == -1
+    assert call(k=5) == -1                                              # two groups of two hold four
+    assert call(factor=float("nan")) == -1 and call(factor=float("inf")) == -1
+    assert call(experts=66, ld=66, groups=33, kept=2) == -2 and call(experts=513, ld=513, groups=1, kept=1) == -2
+    assert call(size=256) == -3
+
+    def back(dw=P, scores=P, score=1, k=2, factor=1.0, expert=P, out=P, ldd=8, size=256, tokens=10):
+        return lib.ctr_expert_route_balanced_bwd(dw, scores, 0, tokens, 8, 8, k, score, 1, C.c_float(factor), expert, out,
+                                                 ldd, P, size, None)
+    assert back(dw=None) == -1 and back(scores=None) == -1 and back(expert=None) == -1 and back(out=None) == -1
+    assert back(score=2) == -1 and back(k=9) == -1 and back(factor=float("nan")) == -1 and back(ldd=7) == -1
+    assert back(size=255) == -3 and back(tokens=0, dw=None, scores=None, expert=None, out=None) == 0
