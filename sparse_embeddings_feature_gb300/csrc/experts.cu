@@ -48,6 +48,7 @@ struct RouteArgs {
   // balanced routing
   const float* bias;                       // NULL without
   int32_t sigmoid, groups, group_k, seg;   // seg: lanes of a group of experts, 0 where groups end inside lanes
+  int32_t f32, cluster;                    // type of the scores; whether the launch is one cluster
   int32_t* expert;
   float* weight;
   int32_t* slot;
@@ -422,9 +423,15 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 // ---------------------------------------------------------------------------
 // Balanced routing: keys (score function + bias), groups, weights from the score function
 // ---------------------------------------------------------------------------
-// Keys are compared as real numbers.  They are computed in fp32 with a bound on their errors; where two that have to
-// be told apart are nearer than that (one token in a thousand), the warp does its tokens again in 64 bits, whose
-// arithmetic is too slow to do all of them in.
+// Keys are compared to 64 bits' precision.  All of them are computed in fp32 and packed: 23 bits of the keys' range above
+// the complement of the expert's index (without a bias, choices go by the upper 23 bits of the scores, made to order as
+// unsigned numbers), so that integer maxima and minima find keys and lowest indexes together: a lane sorts its keys
+// (Batcher's odd-even merge sort), a round a choice takes the largest of the lanes' first ones.  Where two that have to be
+// told apart are nearer than the bound on what packed keys may be off by (one token in 500; equal scores with equal
+// biases are ties and told apart by their indexes), the warp does its tokens again, with the keys that matter in 64 bits: a
+// group's two best, and as many choices as there are lanes.  Where that is not enough, all keys in 64 bits: a warp's
+// 64-bit instruction takes 64 cycles, so that a token with 16 exponentials a lane takes 30 us.
+// 65536 x 256, k 8, 4 of 8 groups, all tokens in fp32 with a round a choice for the key and one for its index: 196 us.
 template <typename K>
 __device__ __forceinline__ K exp_of(K x);
 template <>
@@ -434,6 +441,12 @@ __device__ __forceinline__ float exp_of<float>(float x) {
 template <>
 __device__ __forceinline__ double exp_of<double>(double x) {
   return exp(x);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // A softmax's shift and sum over a row, from a lane's scores (-inf: masked).
@@ -451,130 +464,58 @@ __device__ __forceinline__ K row_softmax(const float (&v)[EPL], int lanes, float
   return total;
 }
 
-// The two largest of a group's keys, in falling order, -inf for none; r: the scores that they are of.
-template <typename K>
-struct Pair {
-  K k0, k1;
-  float r0, r1;
-  __device__ __forceinline__ void take(K k, float r) {
-    if (k > k0) {
-      k1 = k0;
-      r1 = r0;
-      k0 = k;
-      r0 = r;
-    } else if (k > k1) {
-      k1 = k;
-      r1 = r;
-    }
-  }
-  __device__ __forceinline__ void join(int o) {
-    const K a = __shfl_xor_sync(kFull, k0, o), b = __shfl_xor_sync(kFull, k1, o);
-    const float x = __shfl_xor_sync(kFull, r0, o), y = __shfl_xor_sync(kFull, r1, o);
-    take(a, x);
-    take(b, y);
-  }
-};
-
-// The expert of choice `sub` of the lanes' token, -1: none.  v: the lane's scores (-inf: masked, all of them for a
-// token that is routed nowhere); b: its experts' biases.  near: whether a decision was too near to call.
-template <typename K, int EPL>
-__device__ __forceinline__ int choose_balanced(const RouteArgs& a, const float (&v)[EPL], const float (&b)[EPL], int sub,
-                                               bool& near) {
-  constexpr bool kExact = sizeof(K) == 8;
-  const K none = -INFINITY;
+// The expert of choice `sub` of the lanes' token, -1: none, with all keys in 64 bits.  v: the lane's scores (-inf: masked,
+// all of them for a token that is routed nowhere); b: its experts' biases.
+template <int EPL>
+__device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&v)[EPL], const float (&b)[EPL], int sub) {
+  const double none = -INFINITY;
   const int base = sub * EPL, per = a.experts / a.groups;
-  const bool plain = !a.bias;  // then the scores themselves are in the keys' order
   float m = 0.f;
-  K total = 1, key[EPL];
-  // what a key may be off by, over 2^-24: sigmoid, expf 4, sum, division; softmax, its largest p times: expf 4, the
-  // exponent's rounding (below 0.4 of p = 1), a sum of 16 + 5 additions of such terms, division.  Their bias's sum: 1.
-  float err = 7.f;
-  if (!a.sigmoid) {
-    total = row_softmax<K, EPL>(v, a.lanes, m);
-    err = 40.f / (float)total;
-  }
+  double total = 1, key[EPL];
+  if (!a.sigmoid) total = row_softmax<double, EPL>(v, a.lanes, m);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    K p;
-    if (a.sigmoid) p = (K)1 / ((K)1 + exp_of<K>(-(K)v[i]));
-    else p = exp_of<K>((K)v[i] - (K)m) / total;
-    key[i] = v[i] > -INFINITY && b[i] > -INFINITY ? p + (K)b[i] : none;
+    const double p = a.sigmoid ? 1 / (1 + exp(-(double)v[i])) : exp((double)v[i] - m) / total;
+    key[i] = v[i] > -INFINITY && b[i] > -INFINITY ? p + b[i] : none;
   }
-  constexpr float kUnit = 0x1p-24f;
-  near = false;
+  auto take = [](double& x0, double& x1, double x) {
+    x1 = fmax(x1, fmin(x0, x));
+    x0 = fmax(x0, x);
+  };
   if (a.group_k < a.groups) {
-    // lane g learns group g's two best keys
-    Pair<K> best = {none, none, -INFINITY, -INFINITY};
-    if (a.seg) {
-      Pair<K> own = {none, none, -INFINITY, -INFINITY};
+    double worth = none;  // lane g: of group g
+    for (int g = 0; g < a.groups; ++g) {
+      double x0 = none, x1 = none;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) own.take(key[i], v[i]);
-      for (int o = 1; o < a.seg; o <<= 1) own.join(o);
-      const int from = sub * a.seg;
-      best.k0 = __shfl_sync(kFull, own.k0, from, a.lanes);
-      best.k1 = __shfl_sync(kFull, own.k1, from, a.lanes);
-      best.r0 = __shfl_sync(kFull, own.r0, from, a.lanes);
-      best.r1 = __shfl_sync(kFull, own.r1, from, a.lanes);
-    } else {
-      for (int g = 0; g < a.groups; ++g) {
-        Pair<K> own = {none, none, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const int e = base + i;
-          if (e >= g * per && e < (g + 1) * per) own.take(key[i], v[i]);
-        }
-        for (int o = 1; o < a.lanes; o <<= 1) own.join(o);
-        if (g == sub) best = own;
+      for (int i = 0; i < EPL; ++i) take(x0, x1, base + i >= g * per && base + i < (g + 1) * per ? key[i] : none);
+      for (int o = 1; o < a.lanes; o <<= 1) {
+        const double y0 = __shfl_xor_sync(kFull, x0, o), y1 = __shfl_xor_sync(kFull, x1, o);
+        take(x0, x1, y0);
+        take(x0, x1, y1);
       }
+      if (g == sub) worth = x1 > none ? x0 + x1 : x0;
     }
-    const bool some = sub < a.groups && best.k0 > none;
-    const K worth = some ? (best.k1 > none ? best.k0 + best.k1 : best.k0) : none;
-    const float size = some ? fabsf((float)best.k0) + (best.k1 > none ? fabsf((float)best.k1) : 0.f) : 0.f;
     int place = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const K other = __shfl_sync(kFull, worth, g, a.lanes);
+      const double other = __shfl_sync(kFull, worth, g, a.lanes);
       place += other > worth || (other == worth && g < sub);
-      if constexpr (!kExact) {
-        const float r0 = __shfl_sync(kFull, best.r0, g, a.lanes), r1 = __shfl_sync(kFull, best.r1, g, a.lanes);
-        const bool same = plain && r0 == best.r0 && r1 == best.r1;
-        // two keys each: what they may be off by, their bias's sum and theirs
-        const float room = kUnit * (4.f * err + 2.f * (size + __shfl_sync(kFull, size, g, a.lanes)));
-        if (g != sub && some && other > none && !same && fabsf((float)(worth - other)) <= room) near = true;
-      }
     }
     const int lane = threadIdx.x & 31;
-    const uint32_t kept = __ballot_sync(kFull, some && place < a.group_k) >> (lane & ~(a.lanes - 1));
-    int g = base / per, left = per - base % per;
+    const uint32_t kept = __ballot_sync(kFull, worth > none && place < a.group_k) >> (lane & ~(a.lanes - 1));
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      if (g >= a.groups || !((kept >> g) & 1)) key[i] = none;
-      if (--left == 0) {
-        ++g;
-        left = per;
-      }
-    }
+    for (int i = 0; i < EPL; ++i)
+      if (base + i < a.experts && !((kept >> ((base + i) / per)) & 1)) key[i] = none;
   }
-  if (plain) {  // their order is the keys', without rounding
+  if (!a.bias) {  // the scores are in the keys' order, without rounding
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = key[i] > none ? (K)v[i] : none;
+    for (int i = 0; i < EPL; ++i) key[i] = key[i] > none ? (double)v[i] : none;
   }
   int expert = -1;
-  K last = none;
-  for (int j = 0; j < a.k + (kExact || plain ? 0 : 1); ++j) {
-    K best = key[0];
+  for (int j = 0; j < a.k; ++j) {
+    double best = key[0];
 #pragma unroll
-    for (int i = 1; i < EPL; ++i) best = key[i] > best ? key[i] : best;
-    for (int o = 1; o < a.lanes; o <<= 1) {
-      const K other = __shfl_xor_sync(kFull, best, o);
-      best = other > best ? other : best;
-    }
-    if constexpr (!kExact) {
-      if (!plain && j > 0 && best > none &&
-          (float)(last - best) <= kUnit * (2.f * err + fabsf((float)last) + fabsf((float)best)))
-        near = true;
-      last = best;
-      if (j == a.k) break;
-    }
+    for (int i = 1; i < EPL; ++i) best = fmax(best, key[i]);
+    for (int o = 1; o < a.lanes; o <<= 1) best = fmax(best, __shfl_xor_sync(kFull, best, o));
     int at = 0x7fffffff;
 #pragma unroll
     for (int i = EPL - 1; i >= 0; --i) at = key[i] == best ? base + i : at;
@@ -586,34 +527,328 @@ __device__ __forceinline__ int choose_balanced(const RouteArgs& a, const float (
   return expert;
 }
 
-template <typename T, int EPL, bool CLUSTER>
-__global__ void __launch_bounds__(kRouteThreads) route_balanced_kernel(const RouteArgs a) {
+// Scores of a row in either type.
+template <int EPL>
+__device__ __forceinline__ void load_scores(const RouteArgs& a, int64_t t, int base, float (&v)[EPL]) {
+  if (a.f32) load_scores<float, EPL>((const float*)a.scores + t * a.ld, base, a.experts, a.vec != 0, v);
+  else load_scores<__nv_bfloat16, EPL>((const __nv_bfloat16*)a.scores + t * a.ld, base, a.experts, a.vec != 0, v);
+}
+__device__ __forceinline__ float score_at(const RouteArgs& a, int64_t t, int e) {
+  return a.f32 ? ((const float*)a.scores)[t * a.ld + e] : to_f32(((const __nv_bfloat16*)a.scores)[t * a.ld + e]);
+}
+
+// A number as an integer in the same order (64-bit comparisons of integers are not slow); -0 as +0.
+__device__ __forceinline__ int64_t in_order(double x) {
+  const int64_t b = __double_as_longlong(x + 0.0);
+  return b ^ ((b >> 63) & INT64_MAX);
+}
+
+// Whether two packed keys are of equal scores with equal biases.
+__device__ __forceinline__ bool same_inputs(const RouteArgs& a, int64_t t, uint32_t x, uint32_t y) {
+  const int e = 511 - (int)(x & 511u), f = 511 - (int)(y & 511u);
+  return score_at(a, t, e) == score_at(a, t, f) && (!a.bias || a.bias[e] == a.bias[f]);
+}
+
+// Falling order, by Batcher's odd-even merge sort (Sorting networks and their applications, 1968).
+template <int N>
+__device__ __forceinline__ void sort_falling(uint32_t (&x)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const uint32_t hi = max(x[i + j], x[i + j + k]);
+            x[i + j + k] = min(x[i + j], x[i + j + k]);
+            x[i + j] = hi;
+          }
+}
+
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) x = max(x, __shfl_xor_sync(kFull, x, o));
+  return x;
+}
+
+// Packed keys: the keys' range from the smallest bias on is cut into 2^23 - 4 parts of 1 / scale, numbered from 1.
+// off: what a key may be off by besides p's own error, in parts (2^-24 of a range is half a part): 4 for the sums and
+// products here and for cutting off, and the bias's own, |bias| / 2 ranges for each of two roundings.
+struct Packing {
+  float scale, off;
+};
+static_assert(CTR_MAX_EXPERTS <= 512, "an index has 9 bits");
+
+// Each expert's part number at p = 0 into `at` (shared; -inf: never chosen), by all threads of the block.
+__device__ __forceinline__ Packing pack_range(const RouteArgs& a, float* at, float* ends) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = threadIdx.x;
+  float b = a.bias && e < a.experts ? a.bias[e] : 0.f;
+  if (!(b < INFINITY)) {  // NaN, +inf: as -inf, and flagged
+    b = -INFINITY;
+    set_error(a.err, CTR_ERR_BAD_VALUE);
+  }
+  const bool some = e < a.experts && b > -INFINITY;
+  float lo = some ? b : INFINITY, hi = some ? b : -INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    lo = fminf(lo, __shfl_xor_sync(kFull, lo, o));
+    hi = fmaxf(hi, __shfl_xor_sync(kFull, hi, o));
+  }
+  if (lane == 0) {
+    ends[2 * warp] = lo;
+    ends[2 * warp + 1] = hi;
+  }
+  __syncthreads();
+  for (int w = 0; w < kRouteThreads / 32; ++w) {
+    lo = fminf(lo, ends[2 * w]);
+    hi = fmaxf(hi, ends[2 * w + 1]);
+  }
+  if (!(lo <= hi)) lo = hi = 0.f;
+  const float range = 1.f + (hi - lo), scale = 8388604.f / range;
+  if (e < CTR_MAX_EXPERTS) at[e] = e < a.experts ? 1.f + (b - lo) * scale : -INFINITY;
+  __syncthreads();
+  return {scale, 4.f + (fmaxf(fabsf(lo), fabsf(hi)) + 1.f) / range};
+}
+
+// The expert of choice `sub` of the lanes' token t, -1: none; near: this could not tell.  KMAX: choices at most.  REFINE:
+// the keys that matter are computed in 64 bits.
+template <int EPL, int KMAX, int LANES, bool REFINE>
+__device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v)[EPL], const float* at, const Packing& pack,
+                                             int64_t t, int sub, float shift, float total, bool& near) {
+  constexpr float kLog2e = 1.44269504f;
+  const int base = sub * EPL, per = a.experts / a.groups;
+  const bool plain = !a.bias, grouped = a.group_k < a.groups;
+  const int lane = threadIdx.x & 31, first = lane & ~(LANES - 1);
+  near = false;
+  uint32_t key[EPL];
+  int margin = 0;
+  uint32_t kept = kFull;
+  double sum = 1;  // of a softmax, in 64 bits
+  if (REFINE && !a.sigmoid && (!plain || grouped)) sum = row_softmax<double, EPL>(v, LANES, shift);
+  auto exact = [&](uint32_t x) {  // a packed key's value in 64 bits
+    const int e = 511 - (int)(x & 511u);
+    const double l = score_at(a, t, e), b = a.bias ? a.bias[e] : 0.f;
+    return (a.sigmoid ? 1 / (1 + exp(-l)) : exp(l - shift) / sum) + b;
+  };
+  if (!plain || grouped) {
+    // p's error in parts (two of 2^-24), sigmoid: exponential 4 of 2^-24 and its argument's rounding, sum, reciprocal 4:
+    // 8; softmax, of its largest p: exponential 4, its argument's rounding 1, a sum of 16 + 5 additions of such terms and
+    // its division, product: 33
+    const float times = 1.f / total;
+    margin = 1 + (int)fminf(2.f * (pack.off + (a.sigmoid ? 4.f : 24.f * times)), 1e8f);
+    auto part = [&](int i, float p) {
+      // -inf, of a bias, becomes 0: no key
+      const uint32_t q = (uint32_t)fmaf(p, pack.scale, at[base + i]);
+      key[i] = v[i] > -INFINITY && q > 0 ? q * 512u + (uint32_t)(511 - base - i) : 0u;
+    };
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) part(i, __fdividef(1.f, 1.f + exp2_fast(-v[i] * kLog2e)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) part(i, exp2_fast((v[i] - shift) * kLog2e) * times);
+    }
+  }
+  if (grouped) {
+    uint32_t k0 = 0, k1 = 0, k2 = 0;  // lane g learns group g's two (REFINE: three) best keys
+    auto take = [](uint32_t& x0, uint32_t& x1, uint32_t& x2, uint32_t x) {
+      const uint32_t y = min(x0, x);
+      x0 = max(x0, x);
+      if (REFINE) x2 = max(x2, min(x1, y));
+      x1 = max(x1, y);
+    };
+    auto join = [&](uint32_t& x0, uint32_t& x1, uint32_t& x2, int o) {
+      const uint32_t y0 = __shfl_xor_sync(kFull, x0, o), y1 = __shfl_xor_sync(kFull, x1, o);
+      const uint32_t y2 = REFINE ? __shfl_xor_sync(kFull, x2, o) : 0;
+      take(x0, x1, x2, y0);
+      take(x0, x1, x2, y1);
+      if (REFINE) take(x0, x1, x2, y2);
+    };
+    if (a.seg) {
+      uint32_t x0 = 0, x1 = 0, x2 = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) take(x0, x1, x2, key[i]);
+      for (int o = 1; o < a.seg; o <<= 1) join(x0, x1, x2, o);
+      k0 = __shfl_sync(kFull, x0, sub * a.seg, LANES);
+      k1 = __shfl_sync(kFull, x1, sub * a.seg, LANES);
+      if (REFINE) k2 = __shfl_sync(kFull, x2, sub * a.seg, LANES);
+    } else {
+      for (int g = 0; g < a.groups; ++g) {
+        uint32_t x0 = 0, x1 = 0, x2 = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) take(x0, x1, x2, base + i >= g * per && base + i < (g + 1) * per ? key[i] : 0u);
+#pragma unroll
+        for (int o = 1; o < LANES; o <<= 1) join(x0, x1, x2, o);
+        if (g == sub) {
+          k0 = x0;
+          k1 = x1;
+          k2 = x2;
+        }
+      }
+    }
+    const bool some = sub < a.groups && k0 != 0;
+    const int worth = some ? (int)((k0 >> 9) + (k1 >> 9)) : -0x40000000;
+    int place = 0, gap = 0x7fffffff;
+    for (int g = 0; g < a.groups; ++g) {
+      const int other = __shfl_sync(kFull, worth, g, LANES);
+      place += other > worth || (other == worth && g < sub);
+      if (g != sub) gap = min(gap, abs(worth - other));
+    }
+    // near: on either side of the border, and not of the same keys.  A sum of one key is not to be compared with one of two
+    // in parts.
+    const uint32_t all = LANES == 32 ? kFull : (1u << (LANES & 31)) - 1;
+    const uint32_t ones = __ballot_sync(kFull, some && k1 == 0) >> first & all;
+    const uint32_t twos = __ballot_sync(kFull, some && k1 != 0) >> first & all;
+    bool close = ones != 0 && twos != 0;
+    if (__any_sync(kFull, some && gap <= 2 * margin)) {
+      for (int g = 0; g < a.groups; ++g) {
+        const int other = __shfl_sync(kFull, worth, g, LANES), there = __shfl_sync(kFull, place, g, LANES);
+        const uint32_t y0 = __shfl_sync(kFull, k0, g, LANES), y1 = __shfl_sync(kFull, k1, g, LANES);
+        if (some && y0 != 0 && (place < a.group_k) != (there < a.group_k) && abs(worth - other) <= 2 * margin &&
+            !(same_inputs(a, t, k0, y0) && (k1 == 0 || y1 == 0 ? k1 == y1 : same_inputs(a, t, k1, y1))))
+          close = true;
+      }
+    }
+    if constexpr (REFINE) {
+      if (__any_sync(kFull, close)) {
+        // the two best are the two best unless the third may be the second
+        if (some && k2 != 0 && (int)((k1 >> 9) - (k2 >> 9)) <= margin && !same_inputs(a, t, k1, k2)) near = true;
+        const int64_t value = some ? in_order(exact(k0) + (k1 ? exact(k1) : 0.0)) : INT64_MIN;
+        place = 0;
+        for (int g = 0; g < a.groups; ++g) {
+          const int64_t other = __shfl_sync(kFull, value, g, LANES);
+          place += other > value || (other == value && g < sub);
+        }
+      }
+    } else {
+      near = close;
+    }
+    kept = __ballot_sync(kFull, some && place < a.group_k) >> first;
+  }
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      uint32_t u = __float_as_uint(v[i] + 0.f);  // -0 becomes +0
+      u ^= (uint32_t)((int32_t)u >> 31) | 0x80000000u;
+      key[i] = v[i] > -INFINITY ? (u & 0xfffffe00u) | (uint32_t)(511 - base - i) : 0u;
+    }
+  }
+  if (grouped) {
+    if (a.seg) {
+      const uint32_t in = (uint32_t)-(int32_t)((kept >> (sub / a.seg)) & 1);  // lanes past the last group have no keys
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] &= in;
+    } else {
+      int g = base / per, left = per - base % per;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (g >= a.groups || !((kept >> g) & 1)) key[i] = 0;
+        if (--left == 0) {
+          ++g;
+          left = per;
+        }
+      }
+    }
+  }
+  sort_falling(key);
+  // scores of one upper part differ in what was cut off, but for bf16 ones, which have nothing there
+  const int apart = !plain ? margin : a.f32 ? 0 : -1;
+  uint32_t mine = 0;  // lane j gets the j-th largest key
+  if constexpr (REFINE) {
+    for (int j = 0; j < LANES; ++j) {
+      const uint32_t best = lanes_max<LANES>(key[0]);
+      mine = j == sub ? best : mine;
+      const bool pop = key[0] == best;
+#pragma unroll
+      for (int i = 0; i < EPL - 1; ++i) key[i] = pop ? key[i + 1] : key[i];
+      if (pop) key[EPL - 1] = 0;
+    }
+    // the choices are among them unless one that is left may be the last of them
+    const uint32_t left = lanes_max<LANES>(key[0]), last = __shfl_sync(kFull, mine, a.k - 1, LANES);
+    near |= left != 0 && (int)((last >> 9) - (left >> 9)) <= apart;
+    int64_t value = INT64_MIN;
+    if (mine != 0) value = in_order(plain ? (double)score_at(a, t, 511 - (int)(mine & 511u)) : exact(mine));
+    int rank = 0;
+    for (int j = 0; j < LANES; ++j) {
+      const int64_t other = __shfl_sync(kFull, value, j, LANES);
+      const uint32_t there = __shfl_sync(kFull, mine, j, LANES);
+      rank += other > value || (other == value && (there & 511u) > (mine & 511u));  // the larger complement first
+    }
+    uint32_t chosen = 0;
+    for (int j = 0; j < LANES; ++j) {
+      const int r = __shfl_sync(kFull, mine != 0 ? rank : -1, j, LANES);
+      const uint32_t there = __shfl_sync(kFull, mine, j, LANES);
+      if (r == sub) chosen = there;
+    }
+    return sub < a.k && chosen != 0 ? 511 - (int)(chosen & 511u) : -1;
+  } else {
+    uint32_t after = 0;  // the best one left
+#pragma unroll
+    for (int j = 0; j <= KMAX; ++j) {
+      if (j > a.k) break;
+      const uint32_t best = lanes_max<LANES>(key[0]);
+      mine = j == sub ? best : mine;
+      after = best;
+      const bool pop = key[0] == best;
+#pragma unroll
+      for (int i = 0; i < EPL - 1 && i < KMAX - j; ++i) key[i] = pop ? key[i + 1] : key[i];
+      if (EPL - 1 < KMAX - j && pop) key[EPL - 1] = 0;
+    }
+    const uint32_t below = __shfl_down_sync(kFull, mine, 1, LANES), next = sub + 1 == a.k ? after : below;
+    if (sub < a.k && next != 0 && (int)((mine >> 9) - (next >> 9)) <= apart) near |= !same_inputs(a, t, mine, next);
+    return sub < a.k && mine != 0 ? 511 - (int)(mine & 511u) : -1;
+  }
+}
+
+// The same again with 64 bits, from the row itself.  Not inlined: few tokens come here.
+template <int EPL, int LANES>
+__device__ __noinline__ int choose_again(const RouteArgs& a, const float* at, float scale, float off, int64_t t, bool mine,
+                                         int sub) {
+  float v[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = sub * EPL + i;
+    v[i] = mine && e < a.experts ? score_at(a, t, e) : -INFINITY;
+  }
+  float shift = 0.f, total = 1.f;
+  if (!a.sigmoid) total = row_softmax<float, EPL>(v, LANES, shift);
+  bool near;
+  int expert = choose_packed<EPL, CTR_MAX_CHOICES, LANES, true>(a, v, at, Packing{scale, off}, t, sub, shift, total, near);
+  if (__any_sync(kFull, near)) {
+    float b[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = sub * EPL + i;
+      b[i] = a.bias && e < a.experts ? a.bias[e] : 0.f;
+      if (!(b[i] < INFINITY)) b[i] = -INFINITY;
+    }
+    expert = choose_exact<EPL>(a, v, b, sub);
+  }
+  return expert;
+}
+
+template <int EPL, int KMAX, int LANES>
+__global__ void __launch_bounds__(kRouteThreads, 2) route_balanced_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ uint32_t bits[];  // as in route_choose_kernel
+  __shared__ float at[CTR_MAX_EXPERTS], ends[kRouteThreads / 16];
   const int words = a.tile / 32;
   const int64_t t0 = (int64_t)blockIdx.x * a.tile;
   const int n = (int)imin64(a.tile, a.tokens - t0);
   for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
-  __syncthreads();
   grid_wait();
-  const int lane = threadIdx.x & 31, sub = lane & (a.lanes - 1);
-  const uint32_t group = (a.lanes == 32 ? kFull : ((1u << a.lanes) - 1)) << (lane & ~(a.lanes - 1));
-  float b[EPL];
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    b[i] = a.bias && sub * EPL + i < a.experts ? a.bias[sub * EPL + i] : 0.f;
-    if (!(b[i] < INFINITY)) {  // NaN, +inf: as -inf, and flagged
-      b[i] = -INFINITY;
-      set_error(a.err, CTR_ERR_BAD_VALUE);
-    }
-  }
-  const int per_pass = kRouteThreads / a.lanes;
+  const Packing pack = pack_range(a, at, ends);
+  const int lane = threadIdx.x & 31, sub = lane & (LANES - 1);
+  const uint32_t group = (LANES == 32 ? kFull : (1u << (LANES & 31)) - 1) << (lane & ~(LANES - 1));
+  constexpr int per_pass = kRouteThreads / LANES;
   for (int p0 = 0; p0 < n; p0 += per_pass) {  // the same trips in every lane: the shuffles need all of them
-    const int tl = p0 + (int)threadIdx.x / a.lanes;
+    const int tl = p0 + (int)threadIdx.x / LANES;
     const bool mine = tl < n;
-    const T* row = (const T*)a.scores + (t0 + tl) * a.ld;
     float v[EPL];
     if (mine) {
-      load_scores<T, EPL>(row, sub * EPL, a.experts, a.vec != 0, v);
+      load_scores<EPL>(a, t0 + tl, sub * EPL, v);
     } else {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
@@ -621,38 +856,42 @@ __global__ void __launch_bounds__(kRouteThreads) route_balanced_kernel(const Rou
     bool odd = false;  // NaN or +inf: the token is routed nowhere
 #pragma unroll
     for (int i = 0; i < EPL; ++i) odd |= !(v[i] < INFINITY);
-    if (__ballot_sync(kFull, odd) & group) {
+    const bool bad = (__ballot_sync(kFull, odd) & group) != 0;
+    if (bad) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
       if (sub == 0) set_error(a.err, CTR_ERR_BAD_VALUE);
     }
-    bool near, again;
-    int expert = choose_balanced<float, EPL>(a, v, b, sub, near);
-    if (__any_sync(kFull, near)) expert = choose_balanced<double, EPL>(a, v, b, sub, again);
+    float shift = 0.f, total = 1.f;
+    if (!a.sigmoid) total = row_softmax<float, EPL>(v, LANES, shift);
+    bool near;
+    int expert = choose_packed<EPL, KMAX, LANES, false>(a, v, at, pack, t0 + tl, sub, shift, total, near);
+    if (__any_sync(kFull, near))
+      expert = choose_again<EPL, LANES>(a, at, pack.scale, pack.off, t0 + tl, mine && !bad, sub);
     // weights: lane j has choice j
     const bool live = expert >= 0;
-    const float s = live ? to_f32<T>(row[expert]) : -INFINITY;
-    float z, sum = 1.f, m = 0.f;
-    if (a.renormalize || a.sigmoid) {
-      m = s;
-      for (int o = 1; o < a.lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      z = live ? choice_value(a, s, m) : 0.f;
-      if (a.renormalize) {
-        sum = z;
-        for (int o = 1; o < a.lanes; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      }
-    } else {
-      sum = row_softmax<float, EPL>(v, a.lanes, m);
-      z = live ? expf(s - m) : 0.f;
+    const float s = live ? score_at(a, t0 + tl, expert) : -INFINITY;
+    float z = 0.f, sum = total;
+    if (a.renormalize) {
+      float m = s;
+#pragma unroll
+      for (int o = 1; o < LANES; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      if (live) z = choice_value(a, s, m);
+      sum = z;
+#pragma unroll
+      for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    } else if (live) {
+      z = choice_value(a, s, shift);
     }
     if (mine && sub < a.k) {
-      const int64_t at = (t0 + tl) * a.k + sub;
-      a.expert[at] = expert;
-      a.weight[at] = live ? a.factor * (z / sum) : 0.f;
+      const int64_t place = (t0 + tl) * a.k + sub;
+      a.expert[place] = expert;
+      a.weight[place] = live ? a.factor * (z / sum) : 0.f;
       if (live) atomicOr(&bits[expert * words + (tl >> 5)], 1u << (tl & 31));
     }
   }
-  finish_tile<CLUSTER>(a, t0, n, bits);
+  if (a.cluster) finish_tile<true>(a, t0, n, bits);
+  else finish_tile<false>(a, t0, n, bits);
 }
 
 // counts[tile][e] -> exclusive sum over the tiles, and the totals: 32 experts to a block, one to a
@@ -936,12 +1175,26 @@ bool launch_choose(const RouteArgs& a, size_t smem, bool& cluster, cudaStream_t 
                   : launch_choose<T, EPL, CTR_MAX_CHOICES>(a, smem, cluster, s);
 }
 
-template <typename T, int EPL>
-bool launch_balanced(const RouteArgs& a, size_t smem, bool& cluster, cudaStream_t s) {
-  cluster = cluster && largest_cluster_fits<route_balanced_kernel<T, EPL, true>>();
-  auto k = cluster ? route_balanced_kernel<T, EPL, true> : route_balanced_kernel<T, EPL, false>;
+template <int EPL, int KMAX, int LANES>
+bool launch_balanced(RouteArgs& a, size_t smem, bool& cluster, cudaStream_t s) {
+  constexpr auto k = route_balanced_kernel<EPL, KMAX, LANES>;
+  cluster = cluster && largest_cluster_fits<k>();
+  a.cluster = cluster;
   return launch_after(k, dim3((unsigned)a.tiles), kRouteThreads, smem, s, cluster ? (unsigned)a.tiles : 1u, a) ==
          cudaSuccess;
+}
+
+template <int EPL, int KMAX>
+bool launch_balanced(RouteArgs& a, size_t smem, bool& cluster, cudaStream_t s) {
+  return a.lanes == 8 ? launch_balanced<EPL, KMAX, 8>(a, smem, cluster, s)
+         : a.lanes == 16 ? launch_balanced<EPL, KMAX, 16>(a, smem, cluster, s)
+                         : launch_balanced<EPL, KMAX, 32>(a, smem, cluster, s);
+}
+
+template <int EPL>
+bool launch_balanced(RouteArgs& a, size_t smem, bool& cluster, cudaStream_t s) {
+  return a.k <= 8 ? launch_balanced<EPL, 8>(a, smem, cluster, s)
+                  : launch_balanced<EPL, CTR_MAX_CHOICES>(a, smem, cluster, s);
 }
 
 // Lanes of a token whose softmax is over its choices: one for each, and enough that the row's zeros leave
@@ -1225,13 +1478,14 @@ int route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, 
   const bool grouped = b.group_k < b.groups;
   if (grouped && members % per != 0 && members % 8 == 0 && experts <= 256) per = 8;  // groups of whole lanes, if they can be
   a.lanes = route_lanes(experts, k, per);
-  while (grouped && a.lanes < b.groups) a.lanes *= 2;  // a lane for each group
+  while (b.on && (a.lanes < 8 || (grouped && a.lanes < b.groups))) a.lanes *= 2;  // 8, 16 or 32; one for each group
   if (grouped && members % per == 0 && ((members / per) & (members / per - 1)) == 0) a.seg = members / per;
   a.tile = route_tile(tokens, experts);
   a.tiles = (int32_t)ceil_div(tokens, a.tile);
   a.renormalize = renormalize != 0;
   const int eb = dtype_bytes(dtype);
   a.vec = ((uintptr_t)scores % 16) == 0 && (ld_scores * eb) % 16 == 0;
+  a.f32 = dtype == CTR_F32;
   a.factor = b.factor;
   a.bias = b.bias;
   a.sigmoid = b.sigmoid;
@@ -1249,10 +1503,7 @@ int route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, 
   bool cluster = a.tiles > 1 && a.tiles <= kClusterTiles && g_route_cluster.load(std::memory_order_relaxed) != 0;
   bool ok;
   if (b.on)
-    ok = dtype == CTR_F32 ? (per == 8 ? launch_balanced<float, 8>(a, smem, cluster, s)
-                                      : launch_balanced<float, 16>(a, smem, cluster, s))
-                          : (per == 8 ? launch_balanced<__nv_bfloat16, 8>(a, smem, cluster, s)
-                                      : launch_balanced<__nv_bfloat16, 16>(a, smem, cluster, s));
+    ok = per == 8 ? launch_balanced<8>(a, smem, cluster, s) : launch_balanced<16>(a, smem, cluster, s);
   else
     ok = dtype == CTR_F32 ? (per == 8 ? launch_choose<float, 8>(a, smem, cluster, s)
                                       : launch_choose<float, 16>(a, smem, cluster, s))
