@@ -8,7 +8,7 @@
 // bf16 rows off 16 bytes as a copy.  Bound by HBM.
 //
 // Backward: dz = dy act'(pre), rounded to bf16 (or split in planes) for both products, and dbias from it before that
-// rounding, in one read of dy and pre: a thread holds four columns' sums over a strip of rows, the strips are added
+// rounding, in one read of dy and pre: a thread holds its columns' sums over a strip of rows, the strips are added
 // in their order by a second kernel.
 //
 // Up to 8 rows are not worth a tensor core's tile: a warp reads one row of W, as it lies in memory, and multiplies
@@ -49,44 +49,53 @@ __device__ __forceinline__ void split3(float x, float (&p)[3]) {
   p[2] = r - p[1];  // rounded to bf16 where it is stored
 }
 
-// Columns c .. c + 3 of a row into the planes `plane` elements apart.
-template <int PLANES>
-__device__ __forceinline__ void store_planes(__nv_bfloat16* to, int64_t plane, const float (&v)[4]) {
+// N columns of a row into the planes `plane` elements apart.
+template <int PLANES, int N>
+__device__ __forceinline__ void store_planes(__nv_bfloat16* to, int64_t plane, const float (&v)[N]) {
   if constexpr (PLANES == 1) {
-    *(uint2*)to = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+    *(typename RawOf<2 * N>::type*)to = Chunk<__nv_bfloat16, 2 * N>::pack(v);
   } else {
-    float p[4][3];
+    float p[3][N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split3(v[i], p[i]);
+    for (int i = 0; i < N; ++i) {
+      float one[3];
+      split3(v[i], one);
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-      *(uint2*)(to + q * plane) = make_uint2(bf16_pair(p[0][q], p[1][q]), bf16_pair(p[2][q], p[3][q]));
+      for (int q = 0; q < 3; ++q) p[q][i] = one[q];
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) *(typename RawOf<2 * N>::type*)(to + q * plane) = Chunk<__nv_bfloat16, 2 * N>::pack(p[q]);
   }
 }
 
-// Four columns of a row as fp32; zeros past the end.
+// Columns that a thread takes at once: 16 bytes of either type.
+template <typename T>
+constexpr int kPart = 16 / (int)sizeof(T);
+
+// The kPart columns from c on as fp32; zeros past the end.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load4(const T* row, int c, int cols, float (&v)[4]) {
-  if constexpr (VEC) {  // rows on 4 elements, so that only whole parts are read
-    if (c + 4 <= cols) {
-      Chunk<T, 4 * (int)sizeof(T)>::unpack(*(const typename RawOf<4 * (int)sizeof(T)>::type*)(row + c), v);
+__device__ __forceinline__ void load_part(const T* row, int c, int cols, float (&v)[kPart<T>]) {
+  if constexpr (VEC) {
+    if (c + kPart<T> <= cols) {
+      Chunk<T, 16>::unpack(*(const uint4*)(row + c), v);
       return;
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = c + i < cols ? to_f32<T>(row[c + i]) : 0.f;
+  for (int i = 0; i < kPart<T>; ++i) v[i] = c + i < cols ? to_f32<T>(row[c + i]) : 0.f;
 }
 
 template <typename T, int PLANES, bool VEC>
 __global__ void __launch_bounds__(kThreads) pack_kernel(const T* x, int64_t rows, int cols, int64_t ldx, __nv_bfloat16* out,
                                                         int64_t ld, int64_t plane) {
   grid_wait();
-  const int64_t quads = ld / 4, total = rows * quads, step = (int64_t)gridDim.x * kThreads;
+  constexpr int N = kPart<T>;
+  const int64_t parts = ld / N, total = rows * parts, step = (int64_t)gridDim.x * kThreads;
   for (int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x; e < total; e += step) {
-    const int64_t r = e / quads;
-    const int c = (int)(e - r * quads) * 4;
-    float v[4];
-    load4<T, VEC>(x + r * ldx, c, cols, v);
+    const int64_t r = e / parts;
+    const int c = (int)(e - r * parts) * N;
+    float v[N];
+    load_part<T, VEC>(x + r * ldx, c, cols, v);
     store_planes<PLANES>(out + r * ld + c, plane, v);
   }
 }
@@ -94,23 +103,6 @@ __global__ void __launch_bounds__(kThreads) pack_kernel(const T* x, int64_t rows
 // ---------------------------------------------------------------------------
 // dz = dy act'(pre), and its column sums
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float derivative(int act, float z) {
-  switch (act) {
-    case CTR_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-    case CTR_ACT_SILU: {
-      const float s = sigmoid_of(z);
-      return s * (1.f + z * (1.f - s));
-    }
-    case CTR_ACT_GELU:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-    case CTR_ACT_SIGMOID: {
-      const float e = expf(-fabsf(z)), s = 1.f / (1.f + e);
-      return e * s * s;
-    }
-    default: return 1.f;
-  }
-}
-
 struct DzArgs {
   const void* dy;
   const void* pre;          // NULL without an activation
@@ -119,42 +111,45 @@ struct DzArgs {
   int64_t rows, ld_dy, ld_pre, ld, plane;
   int32_t n, strip, act;    // strip: rows of a block
 };
-constexpr int kDzCols = 256, kDzLanes = kThreads / (kDzCols / 4);  // columns of a block, rows at a time
+constexpr int kDzCols = 256;  // columns of a block
 
 template <typename T, int PLANES, bool VEC>
 __global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
-  __shared__ float sums[kDzLanes][kDzCols];
-  const int quad = threadIdx.x % (kDzCols / 4), lane = threadIdx.x / (kDzCols / 4);
-  const int c = blockIdx.x * kDzCols + quad * 4;
+  constexpr int N = kPart<T>, kAcross = kDzCols / N, kLanes = kThreads / kAcross;  // threads of a row, rows at a time
+  __shared__ float sums[kLanes][kDzCols];
+  const int part = threadIdx.x % kAcross, lane = threadIdx.x / kAcross;
+  const int c = blockIdx.x * kDzCols + part * N;
   const int64_t r0 = (int64_t)blockIdx.y * a.strip, r1 = imin64(a.rows, r0 + a.strip);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
   grid_wait();
   if (c < a.ld) {
-#pragma unroll 4
-    for (int64_t r = r0 + lane; r < r1; r += kDzLanes) {
-      float v[4], z[4];
-      load4<T, VEC>((const T*)a.dy + r * a.ld_dy, c, a.n, v);
+#pragma unroll 2
+    for (int64_t r = r0 + lane; r < r1; r += kLanes) {
+      float v[N], z[N];
+      load_part<T, VEC>((const T*)a.dy + r * a.ld_dy, c, a.n, v);
       if (a.pre) {
-        load4<T, VEC>((const T*)a.pre + r * a.ld_pre, c, a.n, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= derivative(a.act, z[i]);
+        load_part<T, VEC>((const T*)a.pre + r * a.ld_pre, c, a.n, z);
+        times_derivative<sizeof(T) == 2>(a.act, v, z);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += v[i];
+      for (int i = 0; i < N; ++i) acc[i] += v[i];
       if (a.dz) store_planes<PLANES>(a.dz + r * a.ld + c, a.plane, v);
     }
   }
   if (!a.part) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sums[lane][quad * 4 + i] = acc[i];
+  for (int i = 0; i < N; ++i) sums[lane][part * N + i] = acc[i];
   __syncthreads();
   const int col = blockIdx.x * kDzCols + threadIdx.x;
   if (col >= a.n) return;
   float sum = 0.f;
 #pragma unroll
-  for (int l = 0; l < kDzLanes; ++l) sum += sums[l][threadIdx.x];
+  for (int l = 0; l < kLanes; ++l) sum += sums[l][threadIdx.x];
   a.part[(int64_t)blockIdx.y * a.n + col] = sum;
 }
+static_assert(kThreads == kDzCols, "a column to a thread in the end");
 
 // dbias[c] = the sum of the strips' rows, 16 strands of them and then the strands, in their order.
 constexpr int kJoinCols = 32, kJoinRows = 16;
@@ -257,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const FewArgs a) {
   if (lane >= a.rows || col >= a.n) return;
   if (a.bias) z += to_f32<T>(((const T*)a.bias)[col]);
   if (a.pre) ((T*)a.pre)[lane * a.ldp + col] = from_f32<T>(z);
-  z = activation(a.act, z);
+  z = activation<false>(a.act, z);
   if (a.residual) z += to_f32<T>(((const T*)a.residual)[lane * a.ldr + col]);
   ((T*)a.y)[lane * a.ldy + col] = from_f32<T>(z);
 }
@@ -334,9 +329,9 @@ bool operand(MmOperand* o, const void* p, ctr_dtype dtype, int64_t rows, int64_t
   o->p = room;
   o->ld = up8(cols);
   o->plane = rows * o->ld;
-  const dim3 grid((unsigned)imax64(1, imin64(ceil_div(rows * (o->ld / 4), kThreads), (int64_t)num_sms() * 16)));
+  const dim3 grid((unsigned)imax64(1, imin64(ceil_div(rows * o->ld * dtype_bytes(dtype) / 16, kThreads), (int64_t)num_sms() * 16)));
   const int eb = dtype_bytes(dtype);
-  const bool vec = ((uintptr_t)p % (4 * eb)) == 0 && ld % 4 == 0;
+  const bool vec = ((uintptr_t)p % 16) == 0 && (ld * eb) % 16 == 0;
   if (dtype == CTR_F32) {
     auto k = vec ? pack_kernel<float, 3, true> : pack_kernel<float, 3, false>;
     return fine(launch_after(k, grid, kThreads, 0, s, 1, (const float*)p, rows, (int)cols, ld, room, o->ld, o->plane));
@@ -464,7 +459,7 @@ extern "C" int ctr_dense_bwd(const void* dy, ctr_dtype dtype, int64_t rows, int6
     a.strip = strip_rows(rows, n);
     a.act = act;
     if (make_dz) dz = MmOperand{room.dz, n, rows, a.ld, a.plane};
-    const bool vec = !off(dy, 4 * eb) && ld_dy % 4 == 0 && (!a.pre || (!off(pre, 4 * eb) && ld_pre % 4 == 0));
+    const bool vec = !off(dy, 16) && (ld_dy * eb) % 16 == 0 && (!a.pre || (!off(pre, 16) && (ld_pre * eb) % 16 == 0));
     const int strips = (int)ceil_div(rows, a.strip);
     const dim3 grid((unsigned)ceil_div(a.ld, kDzCols), (unsigned)strips);
     auto kernel = dtype == CTR_F32 ? (vec ? dz_kernel<float, 3, true> : dz_kernel<float, 3, false>)

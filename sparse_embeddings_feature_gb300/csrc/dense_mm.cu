@@ -198,19 +198,6 @@ __device__ __forceinline__ float bias_at(const DmArgs& p, int col) {
   return p.bias_f32 ? ((const float*)p.bias)[col] : __bfloat162float(((const __nv_bfloat16*)p.bias)[col]);
 }
 
-__device__ __forceinline__ void activate8(int act, float (&z)[8]) {
-  if (act == CTR_ACT_SILU || act == CTR_ACT_SIGMOID) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = (act == CTR_ACT_SILU ? z[i] : 1.f) * sigmoid_of(z[i]);
-  } else if (act == CTR_ACT_GELU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = activation(CTR_ACT_GELU, z[i]);
-  } else if (act == CTR_ACT_RELU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = activation(CTR_ACT_RELU, z[i]);
-  }
-}
-
 // A piece to or from a matrix whose rows are not 16-byte aligned: rows row0 .. row0 + nrows - 1, a warp's lanes on
 // consecutive columns.
 template <typename E>
@@ -554,7 +541,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             float z[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[8 * g + i]);
-            activate8(p.act, z);
+            activate<false>(p.act, z);
             if (p.res) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) z[i] += res[8 * g + i];
@@ -576,7 +563,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             if (S::places == 2 && p.pre)
               *(uint4*)(row + kPiece + at) =
                   make_uint4(bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]), bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7]));
-            activate8(p.act, z);
+            activate<true>(p.act, z);
             if (p.res) {
               float r[8];
               Chunk<__nv_bfloat16, 16>::unpack(*(const uint4*)(row + at), r);

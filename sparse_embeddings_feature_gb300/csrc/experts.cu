@@ -1481,6 +1481,8 @@ int route(const void* scores, ctr_dtype dtype, int64_t tokens, int32_t experts, 
   while (b.on && (a.lanes < 8 || (grouped && a.lanes < b.groups))) a.lanes *= 2;  // 8, 16 or 32; one for each group
   if (grouped && members % per == 0 && ((members / per) & (members / per - 1)) == 0) a.seg = members / per;
   a.tile = route_tile(tokens, experts);
+  // two blocks an SM: finer tiles even them out (65536 x 256, tiles of 256, 128 and 64 tokens: 108, 101 and 102 us)
+  if (b.on && tokens > kClusterTiles * kTileTokens) a.tile = std::min(a.tile, 128);
   a.tiles = (int32_t)ceil_div(tokens, a.tile);
   a.renormalize = renormalize != 0;
   const int eb = dtype_bytes(dtype);
