@@ -114,7 +114,7 @@ struct DzArgs {
 constexpr int kDzCols = 256;  // columns of a block
 
 template <typename T, int PLANES, bool VEC>
-__global__ void __launch_bounds__(kThreads) dz_kernel(const DzArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
   constexpr int N = kPart<T>, kAcross = kDzCols / N, kLanes = kThreads / kAcross;  // threads of a row, rows at a time
   __shared__ float sums[kLanes][kDzCols];
   const int part = threadIdx.x % kAcross, lane = threadIdx.x / kAcross;
@@ -277,10 +277,10 @@ size_t packed_elems(ctr_dtype dtype, int64_t rows, int64_t cols) {
   return (size_t)(dtype == CTR_F32 ? 3 : 1) * (size_t)rows * (size_t)up8(cols);
 }
 
-// Rows of a strip of dz_kernel: enough blocks to fill the GPU, at least 32 rows each.
+// Rows of a strip of dz_kernel: as many blocks as run at once (four an SM of 152), at least 32 rows each.
 int strip_rows(int64_t rows, int64_t n) {
   const int64_t blocks = ceil_div(up8(n), kDzCols);
-  return (int)imax64(32, ceil_div(rows, imax64(1, 1216 / blocks)));
+  return (int)imax64(32, ceil_div(rows, imax64(1, 608 / blocks)));
 }
 
 // What a call takes from the workspace; `carver` is a WsSizer or a WsCarver.

@@ -57,9 +57,12 @@ static_assert(kControlRegs * 128 + kOutRegs * 32 * kOutWarps <= kLaunchRegs * kD
 
 template <int PLANES>
 struct Shape {
-  static constexpr int stages = PLANES == 1 ? 5 : 2;
+  static constexpr int stages = PLANES == 1 ? 4 : 2;
   static constexpr uint32_t stage_bytes = 2 * PLANES * kTileBytes;
-  static constexpr int places = PLANES == 1 ? 2 : 1;  // pieces of an epilogue warp
+  // Places for pieces of an epilogue warp.  Three: pieces of y (and their residual) take the first two in turn, those of
+  // pre the third.  One: each piece of pre leaves before that of y takes its place.
+  static constexpr int places = PLANES == 1 ? 3 : 1;
+  static constexpr int turns = PLANES == 1 ? 2 : 1;
   static constexpr int smem = (int)(1024 + stages * stage_bytes + kOutWarps * places * kPiece);
 };
 static_assert(Shape<1>::smem <= 231 * 1024 && Shape<3>::smem <= 231 * 1024, "more shared memory than a CTA has");
@@ -394,30 +397,54 @@ __global__ void __launch_bounds__(kDmThreads, 1)
     const uint32_t rfull = rfull0 + 16 * (warp - 4);
     const uint32_t tempty_at = PAIR ? in_cta(tempty0, 0) : tempty0;
     const int width = p.f32 ? 32 : 64;  // columns of a piece
-    // With pre, one place is y's (and the residual's) and the other pre's; else pieces take the places in turn.
-    const bool two = S::places == 2 && !p.pre;
     uint32_t b = 0, ph = 0, cph = 0;  // accumulators, as the MMAs' issuer has them
     uint32_t rph = 0, flying = 0;     // phases of the residual's barriers, and which are awaited
     bool ok = true;
+    // The warp's part of a tile.
+    struct Part {
+      int64_t row0;
+      int nrows, col0, cols;  // cols: to do (may be <= 0)
+    };
+    auto part_of = [&](const DmTile& x) {
+      Part r;
+      r.row0 = x.a_row + q * 32;
+      r.nrows = (int)imin64(32, p.m - r.row0);
+      r.col0 = x.col + part * kCols;
+      r.cols = r.nrows <= 0 ? 0 : min(kCols, p.n - r.col0);
+      return r;
+    };
+    auto ask = [&](int place, int64_t row0, int col) {  // a piece of residual into a place that is free
+      if (lane == 0) {
+        mbar_expect_tx(rfull + 8 * place, kPiece);
+        load_box<false>(smem_u32(staging + place * kPiece), &rmap, col, (int32_t)row0, 0, rfull + 8 * place);
+      }
+      flying |= 1u << place;
+    };
+    // A piece of residual for a place that is being read out: asked for when the next piece has begun.
+    struct Later {
+      int place, col;
+      int64_t row0;
+    } later = {-1, 0, 0};
+    auto ask_later = [&] {
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
+      ask(later.place, later.row0, later.col);
+      later.place = -1;
+    };
+    // The first pieces of residual.  Later ones, the next tile's too, are asked for as their places become free: asked for
+    // at their tile's start, they took 1 us of every tile.
+    if (p.wide_res && first < p.tiles) {
+      const Part f = part_of(locate<PAIR>(p, first, (int)rank));
+      for (int h = 0; h < S::turns; ++h)
+        if (h * width < f.cols) ask(h, f.row0, f.col0 + h * width);
+    }
     for (int t = first; ok && t < p.tiles; t += step) {
       const DmTile x = locate<PAIR>(p, t, (int)rank);
-      const int64_t row0 = x.a_row + q * 32;
-      const int nrows = (int)imin64(32, p.m - row0);
-      const int col0 = x.col + part * kCols;
-      const int cols = nrows <= 0 ? 0 : min(kCols, p.n - col0);  // columns to do (may be <= 0)
-      auto ask = [&](int place, int col) {  // a piece of residual into a place that is free
-        if (lane == 0) {
-          mbar_expect_tx(rfull + 8 * place, kPiece);
-          load_box<false>(smem_u32(staging + place * kPiece), &rmap, col, (int32_t)row0, 0, rfull + 8 * place);
-        }
-        flying |= 1u << place;
-      };
-      if (p.wide_res && cols > 0) {
-        if (lane == 0) bulk_wait_read<0>();  // the last tile's pieces have left
-        __syncwarp();
-        ask(0, col0);
-        if (two && cols > width) ask(1, col0 + width);
-      }
+      const Part me = part_of(x);
+      const int64_t row0 = me.row0;
+      const int nrows = me.nrows, col0 = me.col0, cols = me.cols;
+      Part ahead = {};
+      if (p.wide_res && t + step < p.tiles) ahead = part_of(locate<PAIR>(p, t + step, (int)rank));
       auto give = [&](uint32_t acc) {  // an accumulator has been read: the next MMAs may have it
         fence_before();
         __syncwarp();
@@ -475,6 +502,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         uint8_t* piece = staging + place * kPiece;
         if (half == 0) {
           if (p.wide_res) {
+            if (later.place == place) ask_later();
             ok = park(rfull + 8 * place, (rph >> place) & 1);
             if (!ok) {
               if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
@@ -483,9 +511,9 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             rph ^= 1u << place;
             flying &= ~(1u << place);
           } else {
-            // the place is free: all pieces have left, or (two places, within a tile) all but the newest
+            // the place is free: all pieces have left, or (places in turn, within a tile) all but the newest
             if (lane == 0) {
-              if (two && c > 0) bulk_wait_read<1>();
+              if (S::turns == 2 && c > 0) bulk_wait_read<1>();
               else bulk_wait_read<0>();
             }
             __syncwarp();
@@ -497,6 +525,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
           }
         }
         get();
+        if (later.place >= 0) ask_later();
         const float bias = bias_at(p, col + lane);
         uint8_t* row = piece + lane * 128;
         auto leave = [&](const CUtensorMap* map, int wide, char* to, int64_t ld, const uint8_t* from, int at) {
@@ -508,25 +537,25 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             piece_out<uint16_t>(from, to, ld, row0, nrows, at, p.n);
           }
         };
+        // All 32 at once: a thread's chains of exponentials and reciprocals hide each other's latency (8 at a time:
+        // 65536 x 1024 x 1024 with silu 110 us).
+        float z[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]);
+        if (p.bias) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) z[i] += __shfl_sync(kFull, bias, i);
+        }
         if (p.f32) {
-          float res[32];
+          float4 res[8];
+          if (p.res) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (p.res) w = *(const uint4*)(row + ((i ^ (lane & 7)) * 16));
-            res[4 * i] = __uint_as_float(w.x);
-            res[4 * i + 1] = __uint_as_float(w.y);
-            res[4 * i + 2] = __uint_as_float(w.z);
-            res[4 * i + 3] = __uint_as_float(w.w);
-          }
-          if (p.bias) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __shfl_sync(kFull, bias, i));
+            for (int i = 0; i < 8; ++i) res[i] = *(const float4*)(row + ((i ^ (lane & 7)) * 16));
           }
           if (p.pre) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *(uint4*)(row + ((i ^ (lane & 7)) * 16)) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+              *(float4*)(row + ((i ^ (lane & 7)) * 16)) = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             leave(&pmap, p.wide_pre, p.pre, p.ldp, piece, col);
@@ -536,43 +565,45 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             }
             __syncwarp();
           }
+          activate<false>(p.act, z);
+          if (p.res) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float z[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[8 * g + i]);
-            activate<false>(p.act, z);
-            if (p.res) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) z[i] += res[8 * g + i];
+            for (int i = 0; i < 8; ++i) {
+              z[4 * i] += res[i].x;
+              z[4 * i + 1] += res[i].y;
+              z[4 * i + 2] += res[i].z;
+              z[4 * i + 3] += res[i].w;
             }
-            *(float4*)(row + (((2 * g) ^ (lane & 7)) * 16)) = make_float4(z[0], z[1], z[2], z[3]);
-            *(float4*)(row + (((2 * g + 1) ^ (lane & 7)) * 16)) = make_float4(z[4], z[5], z[6], z[7]);
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *(float4*)(row + ((i ^ (lane & 7)) * 16)) = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
         } else {
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t at = (uint32_t)(((4 * half + g) ^ (lane & 7)) * 16);
-            float z[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = __uint_as_float(v[8 * g + i]);
-            if (p.bias) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) z[i] += __shfl_sync(kFull, bias, 8 * g + i);
+          auto pack8 = [&](int g) {
+            return make_uint4(bf16_pair(z[8 * g], z[8 * g + 1]), bf16_pair(z[8 * g + 2], z[8 * g + 3]),
+                              bf16_pair(z[8 * g + 4], z[8 * g + 5]), bf16_pair(z[8 * g + 6], z[8 * g + 7]));
+          };
+          const auto at = [&](int g) { return (uint32_t)(((4 * half + g) ^ (lane & 7)) * 16); };
+          if (S::places == 3 && p.pre) {
+            if (half == 0) {  // pre's place is free
+              if (lane == 0) bulk_wait_read<0>();
+              __syncwarp();
             }
-            if (S::places == 2 && p.pre)
-              *(uint4*)(row + kPiece + at) =
-                  make_uint4(bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]), bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7]));
-            activate<true>(p.act, z);
-            if (p.res) {
-              float r[8];
-              Chunk<__nv_bfloat16, 16>::unpack(*(const uint4*)(row + at), r);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) z[i] += r[i];
-            }
-            *(uint4*)(row + at) =
-                make_uint4(bf16_pair(z[0], z[1]), bf16_pair(z[2], z[3]), bf16_pair(z[4], z[5]), bf16_pair(z[6], z[7]));
+            for (int g = 0; g < 4; ++g) *(uint4*)(staging + 2 * kPiece + lane * 128 + at(g)) = pack8(g);
           }
+          activate<true>(p.act, z);
+          if (p.res) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              float r[8];
+              Chunk<__nv_bfloat16, 16>::unpack(*(const uint4*)(row + at(g)), r);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) z[8 * g + i] += r[i];
+            }
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) *(uint4*)(row + at(g)) = pack8(g);
         }
         if (half == 0 && !p.f32 && c + 32 < cols) return;
         // the piece is complete
@@ -580,16 +611,16 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         leave(&omap, p.wide_out, p.out, p.ldo, piece, at);
-        if (S::places == 2 && p.pre) leave(&pmap, p.wide_pre, p.pre, p.ldp, piece + kPiece, at);
+        if (S::places == 3 && p.pre) leave(&pmap, p.wide_pre, p.pre, p.ldp, staging + 2 * kPiece, at);
         if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        // the piece after next (after this one, with one place) of the residual comes here
-        const int next = at + (two ? 2 : 1) * width;
-        if (p.wide_res && next < col0 + cols) {
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          ask(place, next);
+        if (p.wide_res) {
+          // what comes here next: this tile's piece after the next ones, or the next tile's of the same turn
+          const int next = at - col0 + S::turns * width;
+          const bool here = next < cols;
+          const int col = here ? next : place * width;
+          if (here || col < ahead.cols) later = {place, (here ? col0 : ahead.col0) + col, here ? row0 : ahead.row0};
         }
-        if (two) place ^= 1;
+        if (S::turns == 2) place ^= 1;
       };
       if constexpr (kFlush) {
 #pragma unroll
@@ -608,6 +639,14 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         }
       }
       if (!ok) break;
+      // places that this tile had no piece for
+      if (p.wide_res)
+        for (int h = 0; h < S::turns; ++h)
+          if (h * width >= cols && h * width < ahead.cols) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+            ask(h, ahead.row0, ahead.col0 + h * width);
+          }
       if constexpr (!kFlush) {
         give(b);
         ph ^= b;
