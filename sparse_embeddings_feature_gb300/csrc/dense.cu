@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
       load_part<T, VEC>((const T*)a.dy + r * a.ld_dy, c, a.n, v);
       if (a.pre) {
         load_part<T, VEC>((const T*)a.pre + r * a.ld_pre, c, a.n, z);
-        times_derivative<sizeof(T) == 2>(a.act, v, z);
+        times_derivative(a.act, v, z);
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] += v[i];
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const FewArgs a) {
   if (lane >= a.rows || col >= a.n) return;
   if (a.bias) z += to_f32<T>(((const T*)a.bias)[col]);
   if (a.pre) ((T*)a.pre)[lane * a.ldp + col] = from_f32<T>(z);
-  z = activation<false>(a.act, z);
+  z = activation(a.act, z);
   if (a.residual) z += to_f32<T>(((const T*)a.residual)[lane * a.ldr + col]);
   ((T*)a.y)[lane * a.ldy + col] = from_f32<T>(z);
 }
@@ -310,7 +310,7 @@ Room carve(Z& z, ctr_dtype dtype, int64_t rows, int64_t n, int64_t k, const Want
   if (want.x) r.x = take<Z, __nv_bfloat16>(z, packed_elems(dtype, rows, k));
   if (want.w) r.w = take<Z, __nv_bfloat16>(z, packed_elems(dtype, n, k));
   if (want.dz) r.dz = take<Z, __nv_bfloat16>(z, packed_elems(dtype, rows, n));
-  if (want.dw) r.part = take<Z, float>(z, mm_plan(2, planes, n, k, rows).bytes(n) / 4);
+  if (want.dw) r.part = take<Z, float>(z, mm_plan(2, planes, n, k, rows).bytes() / 4);
   if (want.strips) r.strips = take<Z, float>(z, (size_t)ceil_div(imax64(rows, 1), strip_rows(rows, n)) * n);
   return r;
 }

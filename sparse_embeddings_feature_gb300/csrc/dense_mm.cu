@@ -48,6 +48,7 @@ constexpr uint32_t kTileBytes = kRows * kBlock * 2;
 constexpr uint32_t kChunkBytes = 64 * 128;        // MN-major: 64 of i or j times 64 of r
 constexpr uint32_t kPiece = 32 * 128;             // a warp's piece of the result on its way: 32 rows of 128 bytes
 constexpr int kSuper = 8;                         // row tiles that take the column tiles together
+constexpr int kMinShare = 8;                      // blocks of a part of a sum, at least
 constexpr int kMainBlocks = 2, kCrossBlocks = 64; // blocks between two readings (planes): 8 and 1280 instructions
 constexpr int kFlushBlocks = 8;                   // without planes: 32 instructions
 // Registers of a FLUSH kernel: 384 threads are launched with 168 each; the first four warps give some up so that an
@@ -74,7 +75,8 @@ struct DmArgs {
   const char* bias;
   int* err;
   int64_t ldo, ldr, ldp;      // in elements
-  int32_t m, n, kb, seg, mt, nt, tiles, act;
+  int32_t m, n, kb, mt, nt, tiles, act;
+  int32_t share, parts;       // 0, or blocks of a part of a sum, and parts of a tile
   int32_t f32, bias_f32;      // type of out, residual and pre; of the bias
   // Rows are 16-byte aligned: TMA moves them.  It writes whole 16-byte parts, past the end of a row that ends inside
   // one: 1 where rows do, and the last columns go element by element; 2 where they do not, or may be written past.
@@ -158,29 +160,43 @@ __device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* ma
 }
 
 struct DmTile {
-  int32_t nkb, k0, split;     // blocks of r to sum, the first of them
+  int32_t nkb, k0;            // blocks of r to sum, the first of them
   int32_t a_row, b_row, col;  // this CTA's first row of either operand; first column of the result
+  int32_t slot;               // the part's place
 };
 
+// A worker's way through the tiles: every step-th one.  Where sums are cut, the tiles of the first `share` blocks of r
+// come first, then those of the next: workers that run at once share what they read.  (Shares that end and begin inside
+// tiles, so that all workers have the same, read it again and again: 65536 x 1024 x 1024 123 us against 100.)
 template <bool PAIR>
-__device__ __forceinline__ DmTile locate(const DmArgs& p, int t, int rank) {
-  constexpr int kSide = PAIR ? 256 : 128;
-  DmTile x;
-  const int per = p.mt * p.nt;
-  x.split = t / per;
-  const int l = t - x.split * per;
-  const int sg = l / (kSuper * p.nt);
-  const int rem = l - sg * (kSuper * p.nt);
-  const int mm = min(kSuper, p.mt - sg * kSuper);
-  const int ni = rem / mm;
-  const int mi = sg * kSuper + rem - ni * mm;
-  x.k0 = x.split * p.seg;
-  x.nkb = min(p.seg, p.kb - x.k0);
-  x.a_row = mi * kSide + rank * kRows;
-  x.col = ni * kSide;
-  x.b_row = x.col + (PAIR ? rank * kRows : 0);
-  return x;
-}
+struct Walk {
+  static constexpr int kSide = PAIR ? 256 : 128;
+  const DmArgs& p;
+  int rank, step, at, end;
+  __device__ __forceinline__ Walk(const DmArgs& args, int r) : p(args), rank(r) {
+    at = blockIdx.x / (PAIR ? 2 : 1);
+    step = gridDim.x / (PAIR ? 2 : 1);
+    end = p.tiles * (p.share ? p.parts : 1);
+  }
+  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ DmTile tile() const {
+    DmTile x;
+    const int cut = at / p.tiles, l = at - cut * p.tiles;
+    x.k0 = cut * p.share;
+    x.nkb = p.share ? min(p.share, p.kb - x.k0) : p.kb;
+    x.slot = at;
+    const int sg = l / (kSuper * p.nt);
+    const int rem = l - sg * (kSuper * p.nt);
+    const int mm = min(kSuper, p.mt - sg * kSuper);
+    const int ni = rem / mm;
+    const int mi = sg * kSuper + rem - ni * mm;
+    x.a_row = mi * kSide + rank * kRows;
+    x.col = ni * kSide;
+    x.b_row = x.col + (PAIR ? rank * kRows : 0);
+    return x;
+  }
+  __device__ __forceinline__ void go() { at += step; }
+};
 
 // sum += v for 32 values, two at a time.  volatile: stays after the wait for the load of v.
 __device__ __forceinline__ void add32(float* sum, const uint32_t (&v)[32]) {
@@ -276,7 +292,6 @@ __global__ void __launch_bounds__(kDmThreads, 1)
   if constexpr (PAIR) cluster_sync();  // the other CTA's barriers are ready too
   fence_after();
   const uint32_t tmem = tmem_base_slot;
-  const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas;
 
   if (warp < 4) {
     if constexpr (kFlush) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
@@ -286,8 +301,9 @@ __global__ void __launch_bounds__(kDmThreads, 1)
       int s = 0;
       uint32_t ph = 0, issued = 0;  // issued: blocks so far, at most S::stages counted
       bool ok = true;
-      for (int t = first; ok && t < p.tiles; t += step) {
-        const DmTile x = locate<PAIR>(p, t, (int)rank);
+      DmTile x;
+      for (Walk<PAIR> way(p, (int)rank); ok && way.more(); way.go()) {
+        x = way.tile();
         for (int j = 0; j < x.nkb; ++j) {
           if (!park(empty0 + 8 * s, ph ^ 1)) {
             if (lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
@@ -332,8 +348,10 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         // products, the other (phase cph) the rest.
         uint32_t ph = 0, b = 0, bph = 0, cph = 0;
         bool ok = true;
-        for (int t = first; ok && t < p.tiles; t += step) {
-          const int nkb = locate<PAIR>(p, t, 0).nkb;
+        DmTile x;
+        for (Walk<PAIR> way(p, 0); ok && way.more(); way.go()) {
+          x = way.tile();
+          const int nkb = x.nkb;
           for (int j = 0; ok && j < nkb; ++j) {
             const int every = !kFlush ? nkb : PLANES == 3 ? kMainBlocks : kFlushBlocks;
             const bool opens = j % every == 0, closes = (j + 1) % every == 0 || j + 1 == nkb;
@@ -397,6 +415,8 @@ __global__ void __launch_bounds__(kDmThreads, 1)
     const uint32_t rfull = rfull0 + 16 * (warp - 4);
     const uint32_t tempty_at = PAIR ? in_cta(tempty0, 0) : tempty0;
     const int width = p.f32 ? 32 : 64;  // columns of a piece
+    const bool has_bias = MAJOR == 0 && p.bias, has_res = MAJOR == 0 && p.res, has_pre = MAJOR == 0 && p.pre;
+    const bool wide_res = MAJOR == 0 && p.wide_res;
     uint32_t b = 0, ph = 0, cph = 0;  // accumulators, as the MMAs' issuer has them
     uint32_t rph = 0, flying = 0;     // phases of the residual's barriers, and which are awaited
     bool ok = true;
@@ -407,6 +427,13 @@ __global__ void __launch_bounds__(kDmThreads, 1)
     };
     auto part_of = [&](const DmTile& x) {
       Part r;
+      if (p.share) {  // parts are whole tiles, one below the other
+        r.row0 = (int64_t)x.slot * (kCtas * kRows) + rank * kRows + q * 32;
+        r.nrows = 32;
+        r.col0 = part * kCols;
+        r.cols = kCols;
+        return r;
+      }
       r.row0 = x.a_row + q * 32;
       r.nrows = (int)imin64(32, p.m - r.row0);
       r.col0 = x.col + part * kCols;
@@ -433,18 +460,20 @@ __global__ void __launch_bounds__(kDmThreads, 1)
     };
     // The first pieces of residual.  Later ones, the next tile's too, are asked for as their places become free: asked for
     // at their tile's start, they took 1 us of every tile.
-    if (p.wide_res && first < p.tiles) {
-      const Part f = part_of(locate<PAIR>(p, first, (int)rank));
+    Walk<PAIR> way(p, (int)rank);
+    if (wide_res && way.more()) {
+      const Part f = part_of(way.tile());
       for (int h = 0; h < S::turns; ++h)
         if (h * width < f.cols) ask(h, f.row0, f.col0 + h * width);
     }
-    for (int t = first; ok && t < p.tiles; t += step) {
-      const DmTile x = locate<PAIR>(p, t, (int)rank);
+    while (ok && way.more()) {
+      const DmTile x = way.tile();
+      way.go();
       const Part me = part_of(x);
       const int64_t row0 = me.row0;
       const int nrows = me.nrows, col0 = me.col0, cols = me.cols;
       Part ahead = {};
-      if (p.wide_res && t + step < p.tiles) ahead = part_of(locate<PAIR>(p, t + step, (int)rank));
+      if (wide_res && way.more()) ahead = part_of(way.tile());
       auto give = [&](uint32_t acc) {  // an accumulator has been read: the next MMAs may have it
         fence_before();
         __syncwarp();
@@ -501,7 +530,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         const int half = p.f32 ? 0 : (c >> 5) & 1;
         uint8_t* piece = staging + place * kPiece;
         if (half == 0) {
-          if (p.wide_res) {
+          if (wide_res) {
             if (later.place == place) ask_later();
             ok = park(rfull + 8 * place, (rph >> place) & 1);
             if (!ok) {
@@ -517,7 +546,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
               else bulk_wait_read<0>();
             }
             __syncwarp();
-            if (p.res) {
+            if (has_res) {
               if (p.f32) piece_in<float>(piece, p.res, p.ldr, row0, nrows, col, p.n);
               else piece_in<uint16_t>(piece, p.res, p.ldr, row0, nrows, col, p.n);
               __syncwarp();
@@ -526,11 +555,11 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         }
         get();
         if (later.place >= 0) ask_later();
-        const float bias = bias_at(p, col + lane);
+        const float bias = has_bias ? bias_at(p, col + lane) : 0.f;
         uint8_t* row = piece + lane * 128;
         auto leave = [&](const CUtensorMap* map, int wide, char* to, int64_t ld, const uint8_t* from, int at) {
           if (wide == 2 || (wide == 1 && at + width <= p.n)) {
-            if (lane == 0) store_box(map, at, (int32_t)row0, x.split, smem_u32(from));
+            if (lane == 0) store_box(map, at, (int32_t)row0, 0, smem_u32(from));
           } else if (p.f32) {
             piece_out<float>(from, to, ld, row0, nrows, at, p.n);
           } else {
@@ -542,17 +571,17 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         float z[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]);
-        if (p.bias) {
+        if (has_bias) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) z[i] += __shfl_sync(kFull, bias, i);
         }
         if (p.f32) {
           float4 res[8];
-          if (p.res) {
+          if (has_res) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) res[i] = *(const float4*)(row + ((i ^ (lane & 7)) * 16));
           }
-          if (p.pre) {
+          if (has_pre) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *(float4*)(row + ((i ^ (lane & 7)) * 16)) = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
@@ -565,8 +594,8 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             }
             __syncwarp();
           }
-          activate<false>(p.act, z);
-          if (p.res) {
+          if constexpr (MAJOR == 0) activate(p.act, z);
+          if (has_res) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               z[4 * i] += res[i].x;
@@ -584,7 +613,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
                               bf16_pair(z[8 * g + 4], z[8 * g + 5]), bf16_pair(z[8 * g + 6], z[8 * g + 7]));
           };
           const auto at = [&](int g) { return (uint32_t)(((4 * half + g) ^ (lane & 7)) * 16); };
-          if (S::places == 3 && p.pre) {
+          if (S::places == 3 && has_pre) {
             if (half == 0) {  // pre's place is free
               if (lane == 0) bulk_wait_read<0>();
               __syncwarp();
@@ -592,8 +621,8 @@ __global__ void __launch_bounds__(kDmThreads, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) *(uint4*)(staging + 2 * kPiece + lane * 128 + at(g)) = pack8(g);
           }
-          activate<true>(p.act, z);
-          if (p.res) {
+          if constexpr (MAJOR == 0) activate(p.act, z);
+          if (has_res) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
               float r[8];
@@ -611,9 +640,9 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         leave(&omap, p.wide_out, p.out, p.ldo, piece, at);
-        if (S::places == 3 && p.pre) leave(&pmap, p.wide_pre, p.pre, p.ldp, staging + 2 * kPiece, at);
+        if (S::places == 3 && has_pre) leave(&pmap, p.wide_pre, p.pre, p.ldp, staging + 2 * kPiece, at);
         if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        if (p.wide_res) {
+        if (wide_res) {
           // what comes here next: this tile's piece after the next ones, or the next tile's of the same turn
           const int next = at - col0 + S::turns * width;
           const bool here = next < cols;
@@ -640,7 +669,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
       }
       if (!ok) break;
       // places that this tile had no piece for
-      if (p.wide_res)
+      if (wide_res)
         for (int h = 0; h < S::turns; ++h)
           if (h * width >= cols && h * width < ahead.cols) {
             if (lane == 0) bulk_wait_read<0>();
@@ -670,36 +699,41 @@ __global__ void __launch_bounds__(kDmThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Sums in parts: the planes of m x ld, four columns of one row to a thread, added in their order.
+// Sums in parts: a tile's parts added in their order, four columns of one row to a thread.
 // ---------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) join_planes_kernel(const float* part, int planes, int64_t plane, int64_t ld,
-                                                                   int m, int n, T* out, int64_t ldo, int vec) {
+__global__ void __launch_bounds__(kJoinThreads) join_parts_kernel(const DmArgs p, const float* part, int side, T* out,
+                                                                  int64_t ldo, int vec) {
   grid_wait();
-  const int64_t quads = ld / 4, e = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
-  const int64_t row = e / quads, c = (e - row * quads) * 4;
-  if (row >= m) return;
-  const float* from = part + row * ld + c;
+  const int64_t quads = (p.n + 3) / 4, e = (int64_t)blockIdx.x * kJoinThreads + threadIdx.x;
+  const int row = (int)(e / quads), c = (int)(e - row * quads) * 4;
+  if (row >= p.m) return;
+  const int mi = row / side, ni = c / side;
+  // the tile's number, as Walk has it
+  const int sg = mi / kSuper;
+  const int64_t t = (int64_t)sg * kSuper * p.nt + ni * min(kSuper, p.mt - sg * kSuper) + (mi - sg * kSuper);
+  const int64_t place = (int64_t)side * side, next = place * p.mt * p.nt;
+  const float* from = part + t * place + (row - mi * side) * side + (c - ni * side);
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-  for (int s = 0; s < planes; ++s) {
-    const float4 v = *(const float4*)(from + s * plane);
+  for (int i = 0; i < p.parts; ++i, from += next) {
+    const float4 v = *(const float4*)from;
     sum.x += v.x;
     sum.y += v.y;
     sum.z += v.z;
     sum.w += v.w;
   }
   T* to = out + row * ldo + c;
-  if (vec && c + 4 <= n) {
+  if (vec && c + 4 <= p.n) {
     if constexpr (sizeof(T) == 4) *(float4*)to = sum;
     else *(uint2*)to = make_uint2(bf16_pair(sum.x, sum.y), bf16_pair(sum.z, sum.w));
   } else {
     const float v[4] = {sum.x, sum.y, sum.z, sum.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (c + i < n) to[i] = from_f32<T>(v[i]);
+      if (c + i < p.n) to[i] = from_f32<T>(v[i]);
   }
 }
 
@@ -719,12 +753,12 @@ bool operand_map(CUtensorMap* map, const MmOperand& o, int planes, int box) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Result matrices [planes][m][n] in pieces of 32 rows of 128 bytes.
-bool piece_map(CUtensorMap* map, const void* p, bool f32, int64_t m, int64_t n, int64_t ld, int planes) {
+// A result matrix [m][n] in pieces of 32 rows of 128 bytes.
+bool piece_map(CUtensorMap* map, const void* p, bool f32, int64_t m, int64_t n, int64_t ld) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const int eb = f32 ? 4 : 2;
-  cuuint64_t gdim[3] = {(cuuint64_t)n, (cuuint64_t)m, (cuuint64_t)planes};
+  cuuint64_t gdim[3] = {(cuuint64_t)n, (cuuint64_t)m, 1};
   cuuint64_t gstride[2] = {(cuuint64_t)(ld * eb), (cuuint64_t)(ld * m * eb)};
   cuuint32_t bx[3] = {(cuuint32_t)(128 / eb), 32, 1};
   cuuint32_t es[3] = {1, 1, 1};
@@ -739,28 +773,38 @@ int wide(const void* p, int64_t rows, int64_t cols, int64_t ld, int eb) {
   return (cols * eb) % 16 == 0 ? 2 : 1;
 }
 
-template <bool PAIR, int MAJOR, int PLANES>
-int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) {
-  constexpr int kCtas = PAIR ? 2 : 1, kSide = PAIR ? 256 : 128;
+DmArgs dm_args(const MmCall& c, const MmPlan& plan) {
+  const int side = plan.pair ? 256 : 128;
   DmArgs p = {};
   p.m = (int32_t)c.m;
   p.n = (int32_t)c.n;
   p.kb = (int32_t)ceil_div(c.r, kBlock);
-  p.seg = plan.splits > 1 ? plan.seg : p.kb;
-  p.mt = (int32_t)ceil_div(c.m, kSide);
-  p.nt = (int32_t)ceil_div(c.n, kSide);
-  const int64_t tiles = (int64_t)p.mt * p.nt * plan.splits;
-  if (tiles > INT32_MAX - 65536) return CTR_ERR_UNSUPPORTED;
-  p.tiles = (int32_t)tiles;
+  p.mt = (int32_t)ceil_div(c.m, side);
+  p.nt = (int32_t)ceil_div(c.n, side);
+  p.share = (int32_t)plan.share;
+  p.parts = (int32_t)plan.parts;
   p.err = c.err;
   p.act = c.act;
   p.bias = (const char*)c.bias;
-  p.bias_f32 = PLANES == 3;
-  if (plan.splits > 1) {
+  p.bias_f32 = c.planes == 3;
+  return p;
+}
+
+template <bool PAIR, int MAJOR, int PLANES>
+int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) {
+  constexpr int kCtas = PAIR ? 2 : 1, kSide = PAIR ? 256 : 128;
+  DmArgs p = dm_args(c, plan);
+  const int64_t tiles = (int64_t)p.mt * p.nt;
+  if (tiles > INT32_MAX - 65536) return CTR_ERR_UNSUPPORTED;
+  p.tiles = (int32_t)tiles;
+  const int64_t workers = imin64(tiles * (plan.share ? plan.parts : 1), num_sms() / kCtas);
+  int64_t out_rows = c.m, out_cols = c.n;
+  if (plan.share) {
     p.out = (char*)part;
-    p.ldo = plan.ld;
     p.f32 = 1;
     p.wide_out = 2;
+    p.ldo = out_cols = kSide;
+    out_rows = tiles * plan.parts * kSide;
   } else {
     p.out = (char*)c.out;
     p.ldo = c.ldo;
@@ -778,9 +822,9 @@ int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) 
   if (!operand_map(&amap, c.a, PLANES, MAJOR == 2 ? 64 : kRows) || !operand_map(&bmap, c.b, PLANES, MAJOR >= 1 ? 64 : kRows))
     return CTR_ERR_CUDA;
   CUtensorMap omap = amap, rmap = amap, pmap = amap;  // not used unless the rows are aligned
-  if (p.wide_out && !piece_map(&omap, p.out, p.f32 != 0, c.m, c.n, p.ldo, plan.splits)) return CTR_ERR_CUDA;
-  if (p.wide_res && !piece_map(&rmap, p.res, p.f32 != 0, c.m, c.n, p.ldr, 1)) return CTR_ERR_CUDA;
-  if (p.wide_pre && !piece_map(&pmap, p.pre, p.f32 != 0, c.m, c.n, p.ldp, 1)) return CTR_ERR_CUDA;
+  if (p.wide_out && !piece_map(&omap, p.out, p.f32 != 0, out_rows, out_cols, p.ldo)) return CTR_ERR_CUDA;
+  if (p.wide_res && !piece_map(&rmap, p.res, p.f32 != 0, c.m, c.n, p.ldr)) return CTR_ERR_CUDA;
+  if (p.wide_pre && !piece_map(&pmap, p.pre, p.f32 != 0, c.m, c.n, p.ldp)) return CTR_ERR_CUDA;
   auto k = dense_mm_kernel<PAIR, MAJOR, PLANES>;
   static std::atomic<uint64_t> ready{0};
   if (!once_per_device(ready, [&] {
@@ -790,8 +834,8 @@ int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) 
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::smem) == cudaSuccess;
       }))
     return CTR_ERR_CUDA;
-  const cudaError_t e = launch_after(k, dim3((unsigned)(kCtas * imax64(1, imin64(tiles, num_sms() / kCtas)))), kDmThreads,
-                                     Shape<PLANES>::smem, s, kCtas, p, amap, bmap, omap, rmap, pmap);
+  const cudaError_t e = launch_after(k, dim3((unsigned)(kCtas * imax64(1, workers))), kDmThreads, Shape<PLANES>::smem, s, kCtas,
+                                     p, amap, bmap, omap, rmap, pmap);
   return e == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
 }
 
@@ -808,18 +852,25 @@ MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
   MmPlan w;
   const int64_t kb = ceil_div(r, kBlock);
   const int64_t pairs = ceil_div(m, 256) * ceil_div(n, 256);
-  w.pair = m > 128 && n > 128 && (pairs >= 50 || (major == 2 && kb >= 64));
-  const int64_t side = w.pair ? 256 : 128, workers = w.pair ? 76 : 152;
-  const int64_t room = workers / (ceil_div(m, side) * ceil_div(n, side));
-  if (major == 2 && room >= 2 && kb >= 16) {
-    const int64_t seg = imax64(8, ceil_div(kb, room));
-    const int64_t splits = ceil_div(kb, seg);
-    if (splits > 1) {
-      w.seg = (int32_t)seg;
-      w.splits = (int32_t)splits;
-      w.ld = ceil_div(n, 4) * 4;
+  const int64_t sms = num_sms();
+  w.pair = m > 128 && n > 128 && (pairs >= sms / 3 || (major == 2 && kb >= 64));
+  const int64_t side = w.side(), most = sms / (w.pair ? 2 : 1);
+  const int64_t tiles = ceil_div(m, side) * ceil_div(n, side);
+  if (major != 2) return w;
+  // Sums over a batch are cut into the number of parts that takes least, in blocks' times (0.27 us with planes of bf16
+  // alone): the rounds of all workers, six blocks for each tile's setting up and end, and each part's writing and reading.
+  double best = 0;
+  for (int64_t parts = 1; parts <= imax64(1, kb / kMinShare) && (parts - 1) * tiles <= 3 * most; ++parts) {
+    const double rounds = (double)ceil_div(tiles * parts, most);
+    const double time = rounds * (planes * (planes == 3 ? 2 : 1) * (double)ceil_div(kb, parts) + 6) +
+                        (parts > 1 ? (double)(tiles * parts) * (w.pair ? 0.28 : 0.14) + 8 : 0);
+    if (parts == 1 || time < best) {
+      best = time;
+      w.share = parts > 1 ? ceil_div(kb, parts) : 0;
+      w.parts = parts > 1 ? ceil_div(kb, w.share) : 1;
     }
   }
+  w.places = w.share ? tiles * w.parts : 0;
   return w;
 }
 
@@ -828,18 +879,18 @@ int mm_run(const MmCall& c, float* part, cudaStream_t s) {
   const int st = c.major == 0   ? launch_dm<0>(c, plan, part, s)
                  : c.major == 1 ? launch_dm<1>(c, plan, part, s)
                                 : launch_dm<2>(c, plan, part, s);
-  if (st != CTR_OK || plan.splits == 1) return st;
-  const int64_t blocks = ceil_div(c.m * (plan.ld / 4), kJoinThreads);
+  if (st != CTR_OK || !plan.share) return st;
+  const int64_t blocks = ceil_div(c.m * ceil_div(c.n, 4), kJoinThreads);
   if (blocks > INT32_MAX) return CTR_ERR_UNSUPPORTED;
   const int eb = c.out_f32 ? 4 : 2;
   const int vec = ((uintptr_t)c.out % (4 * eb)) == 0 && c.ldo % 4 == 0;
-  const int64_t plane = c.m * plan.ld;
+  const DmArgs p = dm_args(c, plan);
+  const dim3 grid((unsigned)blocks);
   const cudaError_t e =
-      c.out_f32 ? launch_after(join_planes_kernel<float>, dim3((unsigned)blocks), kJoinThreads, 0, s, 1, (const float*)part,
-                               plan.splits, plane, plan.ld, (int)c.m, (int)c.n, (float*)c.out, c.ldo, vec)
-                : launch_after(join_planes_kernel<__nv_bfloat16>, dim3((unsigned)blocks), kJoinThreads, 0, s, 1,
-                               (const float*)part, plan.splits, plane, plan.ld, (int)c.m, (int)c.n, (__nv_bfloat16*)c.out,
-                               c.ldo, vec);
+      c.out_f32 ? launch_after(join_parts_kernel<float>, grid, kJoinThreads, 0, s, 1, p, (const float*)part, plan.side(),
+                               (float*)c.out, c.ldo, vec)
+                : launch_after(join_parts_kernel<__nv_bfloat16>, grid, kJoinThreads, 0, s, 1, p, (const float*)part,
+                               plan.side(), (__nv_bfloat16*)c.out, c.ldo, vec);
   return e == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
 }
 

@@ -31,23 +31,24 @@ struct MmCall {
   int* err = nullptr;
 };
 
-// How a product is taken apart: CTA pairs on 256 x 256 tiles or CTAs on 128 x 128, and sums in `splits` parts of
-// `seg` blocks of 64, which leave as fp32 planes of m x ld and are added up by a second kernel.
+// How a product is taken apart: CTA pairs on 256 x 256 tiles or CTAs on 128 x 128; where share is not 0, sums in `parts`
+// of `share` blocks of 64, which leave as fp32 (whole tiles, in `places` of the workspace) and are added up by a second
+// kernel.
 struct MmPlan {
   bool pair = false;
-  int32_t seg = 0, splits = 1;
-  int64_t ld = 0;
-  size_t bytes(int64_t m) const { return splits > 1 ? (size_t)splits * m * ld * 4 : 0; }
+  int64_t share = 0, parts = 1, places = 0;
+  int side() const { return pair ? 256 : 128; }
+  size_t bytes() const { return (size_t)places * side() * side() * 4; }
 };
 MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r);
 
-// Runs the product; `part` has mm_plan(..).bytes(m) bytes, 256-byte aligned.  A ctr_status.
+// Runs the product; `part` has mm_plan(..).bytes() bytes, 256-byte aligned.  A ctr_status.
 int mm_run(const MmCall& c, float* part, cudaStream_t s);
 
-// Activations (ctr_activation) and their derivatives.  FAST, for results that are rounded to bf16: the hardware's
-// exponential and reciprocal (within 2 and 1 ulp) and, in gelu, erf within 1.5e-7 by Abramowitz and Stegun, Handbook of
-// Mathematical Functions, 7.1.26.  With expf, erff and divisions the epilogue took twice as long as the products (65536 x
-// 1024 x 1024 with silu 229 us, without an activation 84).
+// Activations (ctr_activation) and their derivatives, by the hardware's exponential and reciprocal (within 2 and 1 ulp)
+// and, in gelu, erf within 1.5e-7 by Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: within 10 2^-24
+// (|z| + 1).  With expf, erff and divisions the epilogue took twice as long as the products (65536 x 1024 x 1024 with
+// silu 229 us, without an activation 84).
 __device__ __forceinline__ float exp2_hw(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -59,59 +60,47 @@ __device__ __forceinline__ float rcp_hw(float x) {
   return r;
 }
 
-template <bool FAST>
-__device__ __forceinline__ float sigmoid_of(float z) {
-  if constexpr (FAST) return rcp_hw(1.f + exp2_hw(-1.44269504f * z));
-  else return __fdividef(1.f, 1.f + expf(-z));
-}
+__device__ __forceinline__ float sigmoid_of(float z) { return rcp_hw(1.f + exp2_hw(-1.44269504f * z)); }
 
 // The normal distribution's integral up to z, and exp(-z^2 / 2).
-template <bool FAST>
 __device__ __forceinline__ float normal_below(float z, float& bell) {
-  if constexpr (FAST) {
-    bell = exp2_hw(-0.72134752f * z * z);
-    const float t = rcp_hw(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.f));
-    float y = fmaf(1.061405429f, t, -1.453152027f);
-    y = fmaf(y, t, 1.421413741f);
-    y = fmaf(y, t, -0.284496736f);
-    y = fmaf(y, t, 0.254829592f);
-    const float tail = 0.5f * (y * t) * bell;
-    return z < 0.f ? tail : 1.f - tail;
-  } else {
-    bell = expf(-0.5f * z * z);
-    return 0.5f * (1.f + erff(z * 0.70710678118654752f));
-  }
+  bell = exp2_hw(-0.72134752f * z * z);
+  const float t = rcp_hw(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.f));
+  float y = fmaf(1.061405429f, t, -1.453152027f);
+  y = fmaf(y, t, 1.421413741f);
+  y = fmaf(y, t, -0.284496736f);
+  y = fmaf(y, t, 0.254829592f);
+  const float tail = 0.5f * (y * t) * bell;
+  return z < 0.f ? tail : 1.f - tail;
 }
 
-template <bool FAST>
 __device__ __forceinline__ float activation(int act, float z) {
   switch (act) {
     case CTR_ACT_RELU: return z < 0.f ? 0.f : z;
-    case CTR_ACT_SILU: return z * sigmoid_of<FAST>(z);
+    case CTR_ACT_SILU: return z * sigmoid_of(z);
     case CTR_ACT_GELU: {
       float bell;
-      return z * normal_below<FAST>(z, bell);
+      return z * normal_below(z, bell);
     }
-    case CTR_ACT_SIGMOID: return sigmoid_of<FAST>(z);
+    case CTR_ACT_SIGMOID: return sigmoid_of(z);
     default: return z;
   }
 }
 
-template <bool FAST>
 __device__ __forceinline__ float derivative(int act, float z) {
   switch (act) {
     case CTR_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case CTR_ACT_SILU: {
-      const float s = sigmoid_of<FAST>(z);
+      const float s = sigmoid_of(z);
       return s * fmaf(z, 1.f - s, 1.f);
     }
     case CTR_ACT_GELU: {
       float bell;
-      const float below = normal_below<FAST>(z, bell);
+      const float below = normal_below(z, bell);
       return fmaf(0.39894228040143268f * z, bell, below);
     }
     case CTR_ACT_SIGMOID: {
-      const float s = sigmoid_of<FAST>(fabsf(z));  // the larger of both: 1 - s is the other
+      const float s = sigmoid_of(fabsf(z));  // the larger of both: 1 - s is the other
       return s * (1.f - s);
     }
     default: return 1.f;
@@ -119,34 +108,34 @@ __device__ __forceinline__ float derivative(int act, float z) {
 }
 
 // The same for N values, the choice made once.
-template <bool FAST, int N>
+template <int N>
 __device__ __forceinline__ void activate(int act, float (&z)[N]) {
   if (act == CTR_ACT_SILU || act == CTR_ACT_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = (act == CTR_ACT_SILU ? z[i] : 1.f) * sigmoid_of<FAST>(z[i]);
+    for (int i = 0; i < N; ++i) z[i] = (act == CTR_ACT_SILU ? z[i] : 1.f) * sigmoid_of(z[i]);
   } else if (act == CTR_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = activation<FAST>(CTR_ACT_GELU, z[i]);
+    for (int i = 0; i < N; ++i) z[i] = activation(CTR_ACT_GELU, z[i]);
   } else if (act == CTR_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = activation<FAST>(CTR_ACT_RELU, z[i]);
+    for (int i = 0; i < N; ++i) z[i] = activation(CTR_ACT_RELU, z[i]);
   }
 }
 // v *= the derivative at z.
-template <bool FAST, int N>
+template <int N>
 __device__ __forceinline__ void times_derivative(int act, float (&v)[N], const float (&z)[N]) {
   if (act == CTR_ACT_SILU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= derivative<FAST>(CTR_ACT_SILU, z[i]);
+    for (int i = 0; i < N; ++i) v[i] *= derivative(CTR_ACT_SILU, z[i]);
   } else if (act == CTR_ACT_SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= derivative<FAST>(CTR_ACT_SIGMOID, z[i]);
+    for (int i = 0; i < N; ++i) v[i] *= derivative(CTR_ACT_SIGMOID, z[i]);
   } else if (act == CTR_ACT_GELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= derivative<FAST>(CTR_ACT_GELU, z[i]);
+    for (int i = 0; i < N; ++i) v[i] *= derivative(CTR_ACT_GELU, z[i]);
   } else if (act == CTR_ACT_RELU) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= derivative<FAST>(CTR_ACT_RELU, z[i]);
+    for (int i = 0; i < N; ++i) v[i] *= derivative(CTR_ACT_RELU, z[i]);
   }
 }
 
