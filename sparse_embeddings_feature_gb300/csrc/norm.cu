@@ -57,57 +57,71 @@ struct Place {
   __device__ __forceinline__ int col(int c) const { return first + c * (LANES * N); }
 };
 
-template <typename T, int VB, int EPT, typename P>
-__device__ __forceinline__ void load_row(const P& at, const T* row, int d, bool mine, float (&f)[EPT]) {
+// A thread's elements are kept as pairs: most of the arithmetic is two operations an instruction.
+template <typename T, int VB, int EPT>
+struct Raw {
   using C = Chunk<T, VB>;
-  typename C::Raw raw[EPT / C::n];
+  static constexpr int N = C::n, chunks = EPT / N;
+  typename C::Raw c[chunks];
+  template <typename P>
+  __device__ __forceinline__ void load(const P& at, const T* row, int d, bool mine) {
 #pragma unroll
-  for (int c = 0; c < EPT / C::n; ++c) {
-    raw[c] = typename C::Raw{};
-    if (mine && at.col(c) < d) raw[c] = *(const typename C::Raw*)(row + at.col(c));
+    for (int i = 0; i < chunks; ++i) {
+      c[i] = typename C::Raw{};
+      if (mine && at.col(i) < d) c[i] = *(const typename C::Raw*)(row + at.col(i));
+    }
   }
+  template <typename P>
+  __device__ __forceinline__ void store(const P& at, T* row, int d) const {
 #pragma unroll
-  for (int c = 0; c < EPT / C::n; ++c) {
-    float v[C::n];
-    C::unpack(raw[c], v);
-#pragma unroll
-    for (int i = 0; i < C::n; ++i) f[c * C::n + i] = v[i];
+    for (int i = 0; i < chunks; ++i)
+      if (at.col(i) < d) *(typename C::Raw*)(row + at.col(i)) = c[i];
   }
-}
+  __device__ __forceinline__ void get(float2 (&f)[EPT / 2]) const {
+#pragma unroll
+    for (int i = 0; i < chunks; ++i) {
+      float v[N];
+      C::unpack(c[i], v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) ((j + i * N) & 1 ? f[(i * N + j) / 2].y : f[(i * N + j) / 2].x) = v[j];
+    }
+  }
+  __device__ __forceinline__ void set(const float2 (&f)[EPT / 2]) {
+#pragma unroll
+    for (int i = 0; i < chunks; ++i) {
+      float v[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = (j + i * N) & 1 ? f[(i * N + j) / 2].y : f[(i * N + j) / 2].x;
+      c[i] = C::pack(v);
+    }
+  }
+};
 
-template <typename T, int VB, int EPT, typename P>
-__device__ __forceinline__ void store_row(const P& at, T* row, int d, const float (&f)[EPT]) {
-  using C = Chunk<T, VB>;
-#pragma unroll
-  for (int c = 0; c < EPT / C::n; ++c) {
-    float v[C::n];
-#pragma unroll
-    for (int i = 0; i < C::n; ++i) v[i] = f[c * C::n + i];
-    if (at.col(c) < d) *(typename C::Raw*)(row + at.col(c)) = C::pack(v);
-  }
-}
-
-// gamma's values at a thread's columns; 1 without a gamma.
+// f *= gamma's values at a thread's columns.
 template <int N, int EPT, typename P>
-__device__ __forceinline__ void load_gamma(const P& at, const NormArgs& a, float (&g)[EPT]) {
+__device__ __forceinline__ void times_gamma(const P& at, const NormArgs& a, float2 (&f)[EPT / 2]) {
+  if (!a.gamma) return;
 #pragma unroll
   for (int c = 0; c < EPT / N; ++c) {
-    if (a.gamma && at.col(c) < a.d) {
-      if (N >= 4 && a.gvec) {
+    float g[N];
+    if (N >= 4 && a.gvec) {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-          const float4 v = *(const float4*)(a.gamma + at.col(c) + i);
-          const float w[4] = {v.x, v.y, v.z, v.w};
+      for (int i = 0; i < N; i += 4) {
+        const float4 v = at.col(c) < a.d ? *(const float4*)(a.gamma + at.col(c) + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 4 && i + j < N; ++j) g[c * N + i + j] = w[j];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) g[c * N + i] = a.gamma[at.col(c) + i];
+        for (int j = 0; j < 4 && i + j < N; ++j) g[i + j] = w[j];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) g[c * N + i] = 1.f;
+      for (int i = 0; i < N; ++i) g[i] = at.col(c) < a.d ? a.gamma[at.col(c) + i] : 0.f;
+    }
+    if constexpr (N >= 2) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) f[(c * N + i) / 2] = mul2(f[(c * N + i) / 2], make_float2(g[i], g[i + 1]));
+    } else {
+      if (c & 1) f[c / 2].y *= g[0];
+      else f[c / 2].x *= g[0];
     }
   }
 }
@@ -133,12 +147,12 @@ __device__ __forceinline__ float row_sum(float v, int wpr, float* sums) {
 // 1 / sqrt(mean(f^2) + eps) over a row.  Squares that leave fp32's range (or all but do, against a small eps)
 // are taken again of scaled values; a NaN or an infinity in the row gives NaN or 0, and NaN results.
 template <int LANES, int EPT>
-__device__ __forceinline__ float row_rstd(const float (&f)[EPT], const NormArgs& a, float* sums) {
-  float sq = 0.f;
+__device__ __forceinline__ float row_rstd(const float2 (&f)[EPT / 2], const NormArgs& a, float* sums) {
+  float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) sq = fmaf(f[i], f[i], sq);
-  sq = row_sum<LANES>(sq, a.wpr, sums);
-  const float mean = sq / (float)a.d + a.eps;
+  for (int i = 0; i < EPT / 2; ++i) sq = fma2(f[i], f[i], sq);
+  const float total = row_sum<LANES>(sq.x + sq.y, a.wpr, sums);
+  const float mean = total / (float)a.d + a.eps;
   float rstd = 1.f / sqrtf(mean);
   // with several warps to a row every thread of the block takes part, or none
   const bool odd = !(mean < 1e37f) || mean < 1e-30f;
@@ -146,16 +160,26 @@ __device__ __forceinline__ float row_rstd(const float (&f)[EPT], const NormArgs&
     const float by = mean < 1e-30f ? 0x1p70f : 0x1p-70f;
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) t = fmaf(f[i] * by, f[i] * by, t);
+    for (int i = 0; i < EPT / 2; ++i) {
+      t = fmaf(f[i].x * by, f[i].x * by, t);
+      t = fmaf(f[i].y * by, f[i].y * by, t);
+    }
     t = row_sum<LANES>(t, a.wpr, sums);
     if (odd) rstd = (float)((double)by / sqrt((double)t / a.d + (double)a.eps * by * by));
   }
   return rstd;
 }
 
+// The largest of three magnitudes, NaN winning.
+__device__ __forceinline__ float max_mag3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Codes of a thread's values: the largest magnitude of each block of 128 columns, its scale and the bytes.
 template <int N, int LANES, int EPT, typename P>
-__device__ __forceinline__ void store_codes(const P& at, const NormArgs& a, int64_t r, bool mine, const float (&v)[EPT]) {
+__device__ __forceinline__ void store_codes(const P& at, const NormArgs& a, int64_t r, bool mine, const float2 (&f)[EPT / 2]) {
   constexpr int kChunks = EPT / N;
   constexpr int kWide = LANES * N;                       // columns of a chunk over the lanes
   constexpr int kPer = kWide >= 128 ? 1 : (LANES == 32 ? 128 / kWide : kChunks);  // chunks of a block
@@ -164,9 +188,7 @@ __device__ __forceinline__ void store_codes(const P& at, const NormArgs& a, int6
   for (int c0 = 0; c0 < kChunks; c0 += kPer) {
     float m = 0.f;
 #pragma unroll
-    for (int c = c0; c < c0 + kPer; ++c)
-#pragma unroll
-      for (int i = 0; i < N; ++i) m = max_mag(m, v[c * N + i]);
+    for (int i = c0 * N / 2; i < (c0 + kPer) * N / 2; ++i) m = max_mag3(m, f[i].x, f[i].y);
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) m = max_mag(m, __shfl_xor_sync(kFull, m, o));
     m = at_least_floor(m);
@@ -181,15 +203,17 @@ __device__ __forceinline__ void store_codes(const P& at, const NormArgs& a, int6
       if constexpr (N >= 4) {
         uint32_t w[N / 4];
 #pragma unroll
-        for (int i = 0; i < N; i += 4) w[i / 4] = codes4(v + c * N + i, inv);
+        for (int i = 0; i < N; i += 4) {
+          const float2 lo = f[(c * N + i) / 2], hi = f[(c * N + i) / 2 + 1];
+          const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+          w[i / 4] = codes4(v, inv);
+        }
         if constexpr (N == 8) *(uint2*)(row + at.col(c)) = make_uint2(w[0], w[1]);
         else *(uint32_t*)(row + at.col(c)) = w[0];
       } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float one[4] = {v[c * N + i], 0.f, 0.f, 0.f};
-          row[at.col(c) + i] = (uint8_t)codes4(one, inv);
-        }
+        static_assert(N == 1, "whole parts or single elements");
+        const float one[4] = {c & 1 ? f[c / 2].y : f[c / 2].x, 0.f, 0.f, 0.f};
+        row[at.col(c)] = (uint8_t)codes4(one, inv);
       }
     }
   }
@@ -205,90 +229,118 @@ __device__ __forceinline__ void zero_codes(const P& at, const NormArgs& a, int64
   }
 }
 
-template <typename T, int VB, int LANES, int EPT>
-__global__ void __launch_bounds__(512) rms_norm_kernel(const NormArgs a) {
+// THREADS: 512 where a row has 16 warps, else 256.  Blocks of an SM: bf16 rows want more threads at once than fp32 ones,
+// whose loads are twice as wide.
+template <typename T>
+constexpr int kNormThreads = sizeof(T) == 2 ? 1024 : 768;
+
+template <typename T, int VB, int LANES, int EPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, kNormThreads<T> / THREADS) rms_norm_kernel(const NormArgs a) {
   constexpr int N = Chunk<T, VB>::n;
+  using Row = Raw<T, VB, EPT>;
   __shared__ float sums[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_block = (int)blockDim.x / (LANES * a.wpr);  // rows of a block
+  const int per_block = THREADS / (LANES * a.wpr);  // rows of a block
   const Place<N, LANES, EPT> at(warp & (a.wpr - 1), lane);
   const int64_t r = (int64_t)blockIdx.x * per_block + (int)threadIdx.x / (LANES * a.wpr);
   const bool mine = r < a.rows;
   grid_wait();
-  float f[EPT];
-  load_row<T, VB, EPT>(at, (const T*)a.x + r * a.ldx, a.d, mine, f);
-  if (a.residual) {
-    float p[EPT];
-    load_row<T, VB, EPT>(at, (const T*)a.residual + r * a.ldr, a.d, mine, p);
-    // the stream's value is what its type holds
-#pragma unroll
-    for (int i = 0; i < EPT; ++i) f[i] = to_f32<T>(from_f32<T>(f[i] + p[i]));
-  }
-  if (a.s && mine) store_row<T, VB, EPT>(at, (T*)a.s + r * a.lds, a.d, f);
-  const float rstd = row_rstd<LANES, EPT>(f, a, sums);
+  float2 f[EPT / 2];
   {
-    float g[EPT];
-    load_gamma<N, EPT>(at, a, g);
+    Row x, p;
+    x.load(at, (const T*)a.x + r * a.ldx, a.d, mine);
+    if (a.residual) {
+      p.load(at, (const T*)a.residual + r * a.ldr, a.d, mine);
+      float2 g[EPT / 2];
+      x.get(f);
+      p.get(g);
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) f[i] = f[i] * rstd * g[i];
+      for (int i = 0; i < EPT / 2; ++i) f[i] = add2(f[i], g[i]);
+      x.set(f);  // the stream's value is what its type holds
+    }
+    if (a.s && mine) x.store(at, (T*)a.s + r * a.lds, a.d);
+    x.get(f);
   }
-  if (a.y && mine) store_row<T, VB, EPT>(at, (T*)a.y + r * a.ldy, a.d, f);
+  const float rstd = row_rstd<LANES, EPT>(f, a, sums);
+  const float2 by = make_float2(rstd, rstd);
+#pragma unroll
+  for (int i = 0; i < EPT / 2; ++i) f[i] = mul2(f[i], by);
+  times_gamma<N, EPT>(at, a, f);
+  if (a.y && mine) {
+    Row y;
+    y.set(f);
+    y.store(at, (T*)a.y + r * a.ldy, a.d);
+  }
   if (a.q) {
     store_codes<N, LANES, EPT>(at, a, r, mine, f);
     zero_codes<LANES, EPT>(at, a, r, mine);
   }
 }
 
-template <typename T, int VB, int LANES, int EPT>
-__global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const NormArgs a) {
+template <typename T, int VB, int LANES, int EPT, int THREADS>
+__global__ void __launch_bounds__(THREADS, 512 / THREADS) rms_norm_bwd_kernel(const NormArgs a) {
   constexpr int N = Chunk<T, VB>::n;
+  using Row = Raw<T, VB, EPT>;
   extern __shared__ float total[];  // a column's sum over the block's rows
   __shared__ float sums[16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int per_block = (int)blockDim.x / (LANES * a.wpr);
+  const int per_block = THREADS / (LANES * a.wpr);
   const Place<N, LANES, EPT> at(warp & (a.wpr - 1), lane);
-  float acc[EPT];
+  float2 acc[EPT / 2];
 #pragma unroll
-  for (int i = 0; i < EPT; ++i) acc[i] = 0.f;
+  for (int i = 0; i < EPT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
   grid_wait();
   const int64_t step = (int64_t)gridDim.x * per_block;
   const int64_t trips = ceil_div(a.rows, step);  // the same in every thread: sums over a row need all of them
   int64_t r = (int64_t)blockIdx.x * per_block + (int)threadIdx.x / (LANES * a.wpr);
   for (int64_t trip = 0; trip < trips; ++trip, r += step) {
     const bool mine = r < a.rows;
-    float u[EPT], g[EPT];
-    load_row<T, VB, EPT>(at, (const T*)a.x + r * a.ldx, a.d, mine, u);
-    load_row<T, VB, EPT>(at, (const T*)a.dy + r * a.ld_dy, a.d, mine, g);
-    const float rstd = row_rstd<LANES, EPT>(u, a, sums);
-    float dot = 0.f;
+    float2 u[EPT / 2], g[EPT / 2];
+    Row p;
     {
-      float gamma[EPT];
-      load_gamma<N, EPT>(at, a, gamma);
-#pragma unroll
-      for (int i = 0; i < EPT; ++i) {
-        u[i] *= rstd;
-        if (mine) acc[i] = fmaf(g[i], u[i], acc[i]);
-        g[i] *= gamma[i];
-        dot = fmaf(g[i], u[i], dot);
-      }
+      Row x, y;
+      x.load(at, (const T*)a.x + r * a.ldx, a.d, mine);
+      y.load(at, (const T*)a.dy + r * a.ld_dy, a.d, mine);
+      // bf16 rows are half as many registers: the gradient on the stream comes with the others
+      if (sizeof(T) == 2 && a.residual) p.load(at, (const T*)a.residual + r * a.ldr, a.d, mine);
+      x.get(u);
+      y.get(g);
     }
-    dot = row_sum<LANES>(dot, a.wpr, sums) / (float)a.d;
+    const float rstd = row_rstd<LANES, EPT>(u, a, sums);
+    const float2 by = make_float2(rstd, rstd);
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) g[i] = rstd * (g[i] - u[i] * dot);
+    for (int i = 0; i < EPT / 2; ++i) {
+      u[i] = mul2(u[i], by);
+      acc[i] = fma2(g[i], u[i], acc[i]);  // rows past the last are zeros
+    }
+    times_gamma<N, EPT>(at, a, g);
+    float2 dot2 = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < EPT / 2; ++i) dot2 = fma2(g[i], u[i], dot2);
+    const float dot = -row_sum<LANES>(dot2.x + dot2.y, a.wpr, sums) / (float)a.d;
+    const float2 less = make_float2(dot, dot);
+#pragma unroll
+    for (int i = 0; i < EPT / 2; ++i) g[i] = mul2(fma2(u[i], less, g[i]), by);
     if (a.residual) {
-      float p[EPT];
-      load_row<T, VB, EPT>(at, (const T*)a.residual + r * a.ldr, a.d, mine, p);
+      if (sizeof(T) == 4) p.load(at, (const T*)a.residual + r * a.ldr, a.d, mine);
+      p.get(u);
 #pragma unroll
-      for (int i = 0; i < EPT; ++i) g[i] += p[i];
+      for (int i = 0; i < EPT / 2; ++i) g[i] = add2(g[i], u[i]);
     }
-    if (mine) store_row<T, VB, EPT>(at, (T*)a.y + r * a.ldy, a.d, g);
+    if (mine) {
+      p.set(g);
+      p.store(at, (T*)a.y + r * a.ldy, a.d);
+    }
   }
   if (!a.part) return;
   // lane groups of a warp in the order of their rows, then the warps
 #pragma unroll
   for (int o = LANES; o < 32; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) acc[i] += __shfl_xor_sync(kFull, acc[i], o);
+    for (int i = 0; i < EPT / 2; ++i) {
+      acc[i].x += __shfl_xor_sync(kFull, acc[i].x, o);
+      acc[i].y += __shfl_xor_sync(kFull, acc[i].y, o);
+    }
   const int groups = (int)(blockDim.x >> 5) / a.wpr;  // warps that hold the same columns
   for (int w = 0; w < groups; ++w) {
     if (warp / a.wpr == w && lane < LANES) {
@@ -297,7 +349,8 @@ __global__ void __launch_bounds__(512) rms_norm_bwd_kernel(const NormArgs a) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int col = at.col(c) + i;
-          if (col < a.d) total[col] = (w ? total[col] : 0.f) + acc[c * N + i];
+          const float v = (c * N + i) & 1 ? acc[(c * N + i) / 2].y : acc[(c * N + i) / 2].x;
+          if (col < a.d) total[col] = (w ? total[col] : 0.f) + v;
         }
     }
     __syncthreads();
@@ -325,20 +378,21 @@ __global__ void __launch_bounds__(kJoinCols* kJoinRows) join_rows_kernel(const f
 }
 
 // Lanes and elements of a thread by the row's width, warps to a row beyond 1024 columns.
-template <template <typename, int, int, int> class K, typename T, int VB, typename... A>
+template <template <typename, int, int, int, int> class K, typename T, int VB>
 auto pick_width(int d) {
-  return d <= 64 ? K<T, VB, 8, 8>::get() : d <= 128 ? K<T, VB, 8, 16>::get()
-       : d <= 256 ? K<T, VB, 32, 8>::get() : d <= 512 ? K<T, VB, 32, 16>::get() : K<T, VB, 32, 32>::get();
+  return d <= 64 ? K<T, VB, 8, 8, 256>::get() : d <= 128 ? K<T, VB, 8, 16, 256>::get()
+       : d <= 256 ? K<T, VB, 32, 8, 256>::get() : d <= 512 ? K<T, VB, 32, 16, 256>::get()
+       : d <= 8192 ? K<T, VB, 32, 32, 256>::get() : K<T, VB, 32, 32, 512>::get();
 }
-template <typename T, int VB, int LANES, int EPT>
+template <typename T, int VB, int LANES, int EPT, int THREADS>
 struct Forward {
-  static auto get() { return rms_norm_kernel<T, VB, LANES, EPT>; }
+  static auto get() { return rms_norm_kernel<T, VB, LANES, EPT, THREADS>; }
 };
-template <typename T, int VB, int LANES, int EPT>
+template <typename T, int VB, int LANES, int EPT, int THREADS>
 struct Backward {
-  static auto get() { return rms_norm_bwd_kernel<T, VB, LANES, EPT>; }
+  static auto get() { return rms_norm_bwd_kernel<T, VB, LANES, EPT, THREADS>; }
 };
-template <template <typename, int, int, int> class K>
+template <template <typename, int, int, int, int> class K>
 auto pick(ctr_dtype dtype, bool wide, int d) {
   if (dtype == CTR_F32) return wide ? pick_width<K, float, 16>(d) : pick_width<K, float, 4>(d);
   return wide ? pick_width<K, __nv_bfloat16, 16>(d) : pick_width<K, __nv_bfloat16, 2>(d);
