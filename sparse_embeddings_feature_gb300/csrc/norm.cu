@@ -126,20 +126,18 @@ __device__ __forceinline__ void times_gamma(const P& at, const NormArgs& a, floa
   }
 }
 
-// Sum over a row's lanes, the same in all of them.  wpr > 1: `sums` has a word a warp, and every thread of
-// the block calls.
+// Sum over a row's lanes, the same in all of them.  wpr > 1: the row's warps meet at a barrier of their own; `sums` has a
+// word a warp of the block, and is not used again before another of the row's sums.
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v, int wpr, float* sums) {
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) v += __shfl_xor_sync(kFull, v, o);
   if (wpr > 1) {
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, first = warp & ~(wpr - 1);
     if ((threadIdx.x & 31) == 0) sums[warp] = v;
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + first / wpr), "r"(32 * wpr) : "memory");
     v = 0.f;
-    const int first = warp & ~(wpr - 1);
     for (int w = 0; w < wpr; ++w) v += sums[first + w];
-    __syncthreads();
   }
   return v;
 }
@@ -147,16 +145,15 @@ __device__ __forceinline__ float row_sum(float v, int wpr, float* sums) {
 // 1 / sqrt(mean(f^2) + eps) over a row.  Squares that leave fp32's range (or all but do, against a small eps)
 // are taken again of scaled values; a NaN or an infinity in the row gives NaN or 0, and NaN results.
 template <int LANES, int EPT>
-__device__ __forceinline__ float row_rstd(const float2 (&f)[EPT / 2], const NormArgs& a, float* sums) {
+__device__ __forceinline__ float row_rstd(const float2 (&f)[EPT / 2], const NormArgs& a, float (*sums)[16]) {
   float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < EPT / 2; ++i) sq = fma2(f[i], f[i], sq);
-  const float total = row_sum<LANES>(sq.x + sq.y, a.wpr, sums);
+  const float total = row_sum<LANES>(sq.x + sq.y, a.wpr, sums[0]);
   const float mean = total / (float)a.d + a.eps;
   float rstd = 1.f / sqrtf(mean);
-  // with several warps to a row every thread of the block takes part, or none
-  const bool odd = !(mean < 1e37f) || mean < 1e-30f;
-  if (a.wpr > 1 ? __syncthreads_or(odd) : __any_sync(kFull, odd)) {
+  const bool odd = !(mean < 1e37f) || mean < 1e-30f;  // the same in all of a row's threads
+  if (__any_sync(kFull, odd)) {
     const float by = mean < 1e-30f ? 0x1p70f : 0x1p-70f;
     float t = 0.f;
 #pragma unroll
@@ -164,7 +161,7 @@ __device__ __forceinline__ float row_rstd(const float2 (&f)[EPT / 2], const Norm
       t = fmaf(f[i].x * by, f[i].x * by, t);
       t = fmaf(f[i].y * by, f[i].y * by, t);
     }
-    t = row_sum<LANES>(t, a.wpr, sums);
+    t = row_sum<LANES>(t, a.wpr, sums[1]);
     if (odd) rstd = (float)((double)by / sqrt((double)t / a.d + (double)a.eps * by * by));
   }
   return rstd;
@@ -238,7 +235,7 @@ template <typename T, int VB, int LANES, int EPT, int THREADS>
 __global__ void __launch_bounds__(THREADS, kNormThreads<T> / THREADS) rms_norm_kernel(const NormArgs a) {
   constexpr int N = Chunk<T, VB>::n;
   using Row = Raw<T, VB, EPT>;
-  __shared__ float sums[16];
+  __shared__ float sums[2][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_block = THREADS / (LANES * a.wpr);  // rows of a block
   const Place<N, LANES, EPT> at(warp & (a.wpr - 1), lane);
@@ -282,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) rms_norm_bwd_kernel(co
   constexpr int N = Chunk<T, VB>::n;
   using Row = Raw<T, VB, EPT>;
   extern __shared__ float total[];  // a column's sum over the block's rows
-  __shared__ float sums[16];
+  __shared__ float sums[3][16];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per_block = THREADS / (LANES * a.wpr);
   const Place<N, LANES, EPT> at(warp & (a.wpr - 1), lane);
@@ -293,18 +290,26 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) rms_norm_bwd_kernel(co
   const int64_t step = (int64_t)gridDim.x * per_block;
   const int64_t trips = ceil_div(a.rows, step);  // the same in every thread: sums over a row need all of them
   int64_t r = (int64_t)blockIdx.x * per_block + (int)threadIdx.x / (LANES * a.wpr);
+  // bf16 rows, half as many registers as fp32 ones, are asked for while the row before is worked on.
+  constexpr bool kAhead = sizeof(T) == 2;
+  Row x, y, p;
+  auto fetch = [&](int64_t row) {
+    const bool mine = row < a.rows;  // nothing past the last row
+    x.load(at, (const T*)a.x + row * a.ldx, a.d, mine);
+    y.load(at, (const T*)a.dy + row * a.ld_dy, a.d, mine);
+    if (kAhead && a.residual) p.load(at, (const T*)a.residual + row * a.ldr, a.d, mine);
+  };
+  if (kAhead) fetch(r);
   for (int64_t trip = 0; trip < trips; ++trip, r += step) {
     const bool mine = r < a.rows;
     float2 u[EPT / 2], g[EPT / 2];
-    Row p;
-    {
-      Row x, y;
-      x.load(at, (const T*)a.x + r * a.ldx, a.d, mine);
-      y.load(at, (const T*)a.dy + r * a.ld_dy, a.d, mine);
-      // bf16 rows are half as many registers: the gradient on the stream comes with the others
-      if (sizeof(T) == 2 && a.residual) p.load(at, (const T*)a.residual + r * a.ldr, a.d, mine);
-      x.get(u);
-      y.get(g);
+    Row arrived;  // the gradient on the stream
+    if (!kAhead) fetch(r);
+    x.get(u);
+    y.get(g);
+    if (kAhead) {
+      arrived = p;
+      fetch(r + step);
     }
     const float rstd = row_rstd<LANES, EPT>(u, a, sums);
     const float2 by = make_float2(rstd, rstd);
@@ -317,19 +322,20 @@ __global__ void __launch_bounds__(THREADS, 512 / THREADS) rms_norm_bwd_kernel(co
     float2 dot2 = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < EPT / 2; ++i) dot2 = fma2(g[i], u[i], dot2);
-    const float dot = -row_sum<LANES>(dot2.x + dot2.y, a.wpr, sums) / (float)a.d;
+    const float dot = -row_sum<LANES>(dot2.x + dot2.y, a.wpr, sums[2]) / (float)a.d;
     const float2 less = make_float2(dot, dot);
 #pragma unroll
     for (int i = 0; i < EPT / 2; ++i) g[i] = mul2(fma2(u[i], less, g[i]), by);
     if (a.residual) {
-      if (sizeof(T) == 4) p.load(at, (const T*)a.residual + r * a.ldr, a.d, mine);
-      p.get(u);
+      if (!kAhead) arrived.load(at, (const T*)a.residual + r * a.ldr, a.d, mine);
+      arrived.get(u);
 #pragma unroll
       for (int i = 0; i < EPT / 2; ++i) g[i] = add2(g[i], u[i]);
     }
     if (mine) {
-      p.set(g);
-      p.store(at, (T*)a.y + r * a.ldy, a.d);
+      Row out;
+      out.set(g);
+      out.store(at, (T*)a.y + r * a.ldy, a.d);
     }
   }
   if (!a.part) return;
@@ -377,19 +383,25 @@ __global__ void __launch_bounds__(kJoinCols* kJoinRows) join_rows_kernel(const f
   }
 }
 
-// Lanes and elements of a thread by the row's width, warps to a row beyond 1024 columns.
+// Lanes and elements of a thread by the row's width.  most: elements of a thread of wide rows, which take more warps
+// instead: 32, but for bf16 rows in the backward kernel, which holds three of them, the next three and the columns' sums
+// (65536 x 2048: 198 us; 32 and the next row not asked for, 238; 16 and three blocks an SM, 253).
 template <template <typename, int, int, int, int> class K, typename T, int VB>
 auto pick_width(int d) {
+  constexpr int kMost = K<T, VB, 32, 8, 256>::most;
   return d <= 64 ? K<T, VB, 8, 8, 256>::get() : d <= 128 ? K<T, VB, 8, 16, 256>::get()
        : d <= 256 ? K<T, VB, 32, 8, 256>::get() : d <= 512 ? K<T, VB, 32, 16, 256>::get()
-       : d <= 8192 ? K<T, VB, 32, 32, 256>::get() : K<T, VB, 32, 32, 512>::get();
+       : d <= 8 * 32 * kMost ? K<T, VB, 32, kMost, 256>::get()
+       : d <= 16 * 32 * kMost ? K<T, VB, 32, kMost, 512>::get() : K<T, VB, 32, 32, 512>::get();
 }
 template <typename T, int VB, int LANES, int EPT, int THREADS>
 struct Forward {
+  static constexpr int most = 32;
   static auto get() { return rms_norm_kernel<T, VB, LANES, EPT, THREADS>; }
 };
 template <typename T, int VB, int LANES, int EPT, int THREADS>
 struct Backward {
+  static constexpr int most = sizeof(T) == 2 ? 16 : 32;
   static auto get() { return rms_norm_bwd_kernel<T, VB, LANES, EPT, THREADS>; }
 };
 template <template <typename, int, int, int, int> class K>
@@ -400,15 +412,19 @@ auto pick(ctr_dtype dtype, bool wide, int d) {
 
 struct NormPlan {
   int lanes, wpr = 1, threads = 256, per_block;
-  explicit NormPlan(int d) {
+  NormPlan(int d, bool backward, int dtype) {
+    const int most = !backward ? Forward<float, 16, 32, 8, 256>::most
+                     : dtype == CTR_F32 ? Backward<float, 16, 32, 8, 256>::most : Backward<__nv_bfloat16, 16, 32, 8, 256>::most;
     lanes = d <= 128 ? 8 : 32;
-    while (wpr * 1024 < d) wpr *= 2;
+    while (wpr < 16 && wpr * 32 * most < d) wpr *= 2;
     if (wpr > 8) threads = 512;
     per_block = threads / (lanes * wpr);
   }
 };
 
-int norm_parts(int64_t rows, int d) { return (int)imin64(kNormParts, ceil_div(rows, NormPlan(d).per_block)); }
+int norm_parts(int64_t rows, int d, int dtype) {
+  return (int)imin64(kNormParts, ceil_div(rows, NormPlan(d, true, dtype).per_block));
+}
 
 bool misaligned(const void* p, int by) { return ((uintptr_t)p % by) != 0; }
 
@@ -426,7 +442,7 @@ using namespace ctr;
 extern "C" size_t ctr_rms_norm_workspace_size(int64_t rows, int32_t d) {
   if (rows < 0 || d < 1 || d > kNormMaxCols) return 0;
   WsSizer z;
-  z.take<float>((size_t)norm_parts(rows, d) * d);
+  z.take<float>((size_t)std::max(norm_parts(rows, d, CTR_F32), norm_parts(rows, d, CTR_BF16)) * d);
   return z.used;
 }
 
@@ -446,7 +462,7 @@ extern "C" int ctr_rms_norm(const void* x, ctr_dtype dtype, int64_t rows, int32_
   if (misaligned(gamma, 4) || misaligned(scale, 4) || misaligned(q, 16)) return CTR_ERR_INVALID_ARG;
   if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
   if (rows == 0) return CTR_OK;
-  const NormPlan plan(d);
+  const NormPlan plan(d, false, dtype);
   NormArgs a = {};
   a.x = x;
   a.residual = residual;
@@ -489,8 +505,8 @@ extern "C" int ctr_rms_norm_bwd(const void* dy, ctr_dtype dtype, int64_t rows, i
   if (misaligned(gamma, 4) || misaligned(dgamma, 4)) return CTR_ERR_INVALID_ARG;
   if (!ws_valid(ws, ws_bytes, dgamma ? ctr_rms_norm_workspace_size(rows, d) : kWsHeader)) return CTR_ERR_WORKSPACE;
   const cudaStream_t stm = (cudaStream_t)stream;
-  const NormPlan plan(d);
-  const int parts = norm_parts(rows, d);
+  const NormPlan plan(d, true, dtype);
+  const int parts = norm_parts(rows, d, dtype);
   WsCarver c(ws, ws_bytes);
   float* part = dgamma ? c.take<float>((size_t)parts * d) : nullptr;
   if (rows > 0) {
