@@ -23,8 +23,11 @@
 //
 // Roles: warp 0 loads the operand tiles into a ring of stages; warp 1 of the issuing CTA owns the MMAs, into two
 // accumulators in turn; 8 warps read them back, a thread one row (TMEM lane) and half of the columns, 32 at a time.
-// Rows leave (and residual rows come) as pieces of 32 rows x 128 bytes through shared memory by TMA, which clips at
-// the matrix's ends; matrices whose rows are not 16-byte aligned go element by element, consecutive columns together.
+// A warp's results pass through shared memory as pieces of 32 rows x 128 bytes and leave by TMA (stores from the threads:
+// 65536 x 1024 x 1024 bf16 with silu and residual 119 us against 104); but those of an fp32 pre, whose place y waits for,
+// by the threads, a line at a time: such a store waits behind the operands' loads, and its place is free 2000 cycles
+// later.  Residual pieces come by TMA, a tile ahead.  Matrices whose rows are not 16-byte aligned go element by element,
+// consecutive columns together.
 // Every mbarrier wait is bounded by a wall-clock limit; on expiry the kernel records CTR_ERR_TIMEOUT, waits (bounded)
 // for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -217,19 +220,39 @@ __device__ __forceinline__ float bias_at(const DmArgs& p, int col) {
   return p.bias_f32 ? ((const float*)p.bias)[col] : __bfloat162float(((const __nv_bfloat16*)p.bias)[col]);
 }
 
-// A piece to or from a matrix whose rows are not 16-byte aligned: rows row0 .. row0 + nrows - 1, a warp's lanes on
-// consecutive columns.
+// A piece to its matrix: rows row0 .. row0 + nrows - 1, columns from col on.  wide: rows are 16-byte aligned, and eight
+// lanes store 128 bytes of a row; else a warp's lanes store consecutive columns.
 template <typename E>
-__device__ __forceinline__ void piece_out(const uint8_t* piece, char* to, int64_t ld, int64_t row0, int nrows, int col, int n) {
+__device__ __forceinline__ void piece_out(const uint8_t* piece, char* to, int64_t ld, int64_t row0, int nrows, int col, int n,
+                                          bool wide) {
   constexpr int width = 128 / (int)sizeof(E), per = 16 / (int)sizeof(E);
   const int lane = threadIdx.x & 31;
-  E* out = (E*)to + row0 * ld + col;
+  if (wide) {
+    const int part = lane & 7, c = col + part * per;
+    E* out = (E*)to + (row0 + (lane >> 3)) * ld + c;
 #pragma unroll
-  for (int e = lane; e < width; e += 32)
-    if (col + e < n)
-      for (int r = 0; r < nrows; ++r)
-        out[r * ld + e] = *(const E*)(piece + r * 128 + (((e / per) ^ (r & 7)) * 16) + (e % per) * sizeof(E));
+    for (int r = lane >> 3; r < 32; r += 4, out += 4 * ld) {
+      const uint4 v = *(const uint4*)(piece + r * 128 + ((part ^ (r & 7)) * 16));
+      if (r >= nrows) continue;
+      if (c + per <= n) {
+        *(uint4*)out = v;
+      } else {
+        const E* e = (const E*)&v;
+#pragma unroll
+        for (int i = 0; i < per; ++i)
+          if (c + i < n) out[i] = e[i];
+      }
+    }
+  } else {
+    E* out = (E*)to + row0 * ld + col;
+#pragma unroll
+    for (int e = lane; e < width; e += 32)
+      if (col + e < n)
+        for (int r = 0; r < nrows; ++r)
+          out[r * ld + e] = *(const E*)(piece + r * 128 + (((e / per) ^ (r & 7)) * 16) + (e % per) * sizeof(E));
+  }
 }
+// A piece of a matrix whose rows are not 16-byte aligned.
 template <typename E>
 __device__ __forceinline__ void piece_in(uint8_t* piece, const char* from, int64_t ld, int64_t row0, int nrows, int col, int n) {
   constexpr int width = 128 / (int)sizeof(E), per = 16 / (int)sizeof(E);
@@ -414,7 +437,8 @@ __global__ void __launch_bounds__(kDmThreads, 1)
     uint8_t* staging = smem_raw + (base - raw) + S::stages * S::stage_bytes + (warp - 4) * (S::places * kPiece);
     const uint32_t rfull = rfull0 + 16 * (warp - 4);
     const uint32_t tempty_at = PAIR ? in_cta(tempty0, 0) : tempty0;
-    const int width = p.f32 ? 32 : 64;  // columns of a piece
+    const bool f32 = MAJOR == 2 ? p.f32 != 0 : PLANES == 3;  // type of the results
+    const int width = f32 ? 32 : 64;                         // columns of a piece
     const bool has_bias = MAJOR == 0 && p.bias, has_res = MAJOR == 0 && p.res, has_pre = MAJOR == 0 && p.pre;
     const bool wide_res = MAJOR == 0 && p.wide_res;
     uint32_t b = 0, ph = 0, cph = 0;  // accumulators, as the MMAs' issuer has them
@@ -441,6 +465,10 @@ __global__ void __launch_bounds__(kDmThreads, 1)
       return r;
     };
     auto ask = [&](int place, int64_t row0, int col) {  // a piece of residual into a place that is free
+      if (PLANES == 3) {  // whose last readers were threads
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+      }
       if (lane == 0) {
         mbar_expect_tx(rfull + 8 * place, kPiece);
         load_box<false>(smem_u32(staging + place * kPiece), &rmap, col, (int32_t)row0, 0, rfull + 8 * place);
@@ -489,15 +517,18 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         auto add = [&](uint32_t acc, uint32_t parity) {
           if (!park(tfull0 + 8 * acc, parity)) return false;
           fence_after();
+          // 64 columns at once; with planes, whose epilogue has more to hold, 32 (spills go to L2: all but nothing is left of
+          // L1 beside the operands)
+          constexpr int kStep = PLANES == 3 ? 32 : 64;
 #pragma unroll
-          for (int c = 0; c < kCols; c += 64) {
+          for (int c = 0; c < kCols; c += kStep) {
             uint32_t v0[32], v1[32];
             tmem_ld32_async(lane_base + acc * kBN + c, v0);
-            tmem_ld32_async(lane_base + acc * kBN + c + 32, v1);
+            if (kStep == 64) tmem_ld32_async(lane_base + acc * kBN + c + 32, v1);
             tmem_wait_ld();
-            if (c + 64 == kCols) give(acc);
+            if (c + kStep == kCols) give(acc);
             add32(sum + c, v0);
-            add32(sum + c + 32, v1);
+            if (kStep == 64) add32(sum + c + 32, v1);
           }
           return true;
         };
@@ -527,7 +558,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
       // columns c .. c + 31 of the tile's part, whose sums are v once `get` has run
       auto leave32 = [&](int c, uint32_t (&v)[32], auto get) {
         const int col = col0 + c;
-        const int half = p.f32 ? 0 : (c >> 5) & 1;
+        const int half = f32 ? 0 : (c >> 5) & 1;
         uint8_t* piece = staging + place * kPiece;
         if (half == 0) {
           if (wide_res) {
@@ -547,7 +578,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             }
             __syncwarp();
             if (has_res) {
-              if (p.f32) piece_in<float>(piece, p.res, p.ldr, row0, nrows, col, p.n);
+              if (f32) piece_in<float>(piece, p.res, p.ldr, row0, nrows, col, p.n);
               else piece_in<uint16_t>(piece, p.res, p.ldr, row0, nrows, col, p.n);
               __syncwarp();
             }
@@ -560,10 +591,10 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         auto leave = [&](const CUtensorMap* map, int wide, char* to, int64_t ld, const uint8_t* from, int at) {
           if (wide == 2 || (wide == 1 && at + width <= p.n)) {
             if (lane == 0) store_box(map, at, (int32_t)row0, 0, smem_u32(from));
-          } else if (p.f32) {
-            piece_out<float>(from, to, ld, row0, nrows, at, p.n);
+          } else if (f32) {
+            piece_out<float>(from, to, ld, row0, nrows, at, p.n, false);
           } else {
-            piece_out<uint16_t>(from, to, ld, row0, nrows, at, p.n);
+            piece_out<uint16_t>(from, to, ld, row0, nrows, at, p.n, false);
           }
         };
         // All 32 at once: a thread's chains of exponentials and reciprocals hide each other's latency (8 at a time:
@@ -575,7 +606,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) z[i] += __shfl_sync(kFull, bias, i);
         }
-        if (p.f32) {
+        if (f32) {
           float4 res[8];
           if (has_res) {
 #pragma unroll
@@ -585,13 +616,9 @@ __global__ void __launch_bounds__(kDmThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               *(float4*)(row + ((i ^ (lane & 7)) * 16)) = make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            // by the threads: y takes its place at once
             __syncwarp();
-            leave(&pmap, p.wide_pre, p.pre, p.ldp, piece, col);
-            if (lane == 0) {
-              asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-              bulk_wait_read<0>();
-            }
+            piece_out<float>(piece, p.pre, p.ldp, row0, nrows, col, p.n, p.wide_pre != 0);
             __syncwarp();
           }
           if constexpr (MAJOR == 0) activate(p.act, z);
@@ -634,7 +661,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
 #pragma unroll
           for (int g = 0; g < 4; ++g) *(uint4*)(row + at(g)) = pack8(g);
         }
-        if (half == 0 && !p.f32 && c + 32 < cols) return;
+        if (half == 0 && !f32 && c + 32 < cols) return;
         // the piece is complete
         const int at = col - 32 * half;
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -652,15 +679,30 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         if (S::turns == 2) place ^= 1;
       };
       if constexpr (kFlush) {
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32)
-          if (ok && c < cols) {
+        // With activations one copy of the code, the sums moving up: four are more than the instruction cache holds (fp32
+        // 16384 x 1024 x 1024 with gelu and pre 292 us).
+        if constexpr (MAJOR == 0) {
+#pragma unroll 1
+          for (int c = 0; ok && c < cols; c += 32) {
             uint32_t v[32];
             leave32(c, v, [&] {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[c + i]);
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[i]);
             });
+#pragma unroll
+            for (int i = 0; i < kCols - 32; ++i) sum[i] = sum[i + 32];
           }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 32)
+            if (ok && c < cols) {
+              uint32_t v[32];
+              leave32(c, v, [&] {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sum[c + i]);
+              });
+            }
+        }
       } else {
         for (int c = 0; ok && c < cols; c += 32) {
           uint32_t v[32];
