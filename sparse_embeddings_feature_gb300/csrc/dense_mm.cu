@@ -59,17 +59,21 @@ constexpr int kFlushBlocks = 8;                   // without planes: 32 instruct
 constexpr int kLaunchRegs = 168, kControlRegs = 56, kOutRegs = 224;
 static_assert(kControlRegs * 128 + kOutRegs * 32 * kOutWarps <= kLaunchRegs * kDmThreads, "more registers than launched");
 
-template <int PLANES>
+// BN: columns of a tile: 256 of a pair, 128, or 32 (with 128 rows).
+template <int PLANES, int BN>
 struct Shape {
-  static constexpr int stages = PLANES == 1 ? 4 : 2;
-  static constexpr uint32_t stage_bytes = 2 * PLANES * kTileBytes;
+  static constexpr uint32_t b_bytes = (BN == 256 ? 128 : BN) * kBlock * 2;  // of the right operand that a CTA holds
+  static constexpr int stages = BN == 32 ? (PLANES == 1 ? 16 : 8) : PLANES == 1 ? 4 : 2;  // at most
+  static constexpr uint32_t stage_bytes = PLANES * (kTileBytes + b_bytes);
+  static constexpr int parts = BN == 32 ? 1 : 2;  // epilogue warps that share a row
   // Places for pieces of an epilogue warp.  Three: pieces of y (and their residual) take the first two in turn, those of
   // pre the third.  One: each piece of pre leaves before that of y takes its place.
   static constexpr int places = PLANES == 1 ? 3 : 1;
   static constexpr int turns = PLANES == 1 ? 2 : 1;
-  static constexpr int smem = (int)(1024 + stages * stage_bytes + kOutWarps * places * kPiece);
+  static constexpr uint32_t room = 4 * parts * places * kPiece;  // all epilogue warps'
+  static constexpr int smem = BN == 32 ? 226 * 1024 : (int)(1024 + stages * stage_bytes + room);
 };
-static_assert(Shape<1>::smem <= 231 * 1024 && Shape<3>::smem <= 231 * 1024, "more shared memory than a CTA has");
+static_assert(Shape<1, 256>::smem <= 231 * 1024 && Shape<3, 256>::smem <= 231 * 1024, "more shared memory than a CTA has");
 
 struct DmArgs {
   char* out;
@@ -80,6 +84,8 @@ struct DmArgs {
   int64_t ldo, ldr, ldp;      // in elements
   int32_t m, n, kb, mt, nt, tiles, act;
   int32_t share, parts;       // 0, or blocks of a part of a sum, and parts of a tile
+  // Of a tile of 32 columns: rows of the left operand that are there (else 128), and how many stages fit.
+  int32_t a_rows, stages;
   int32_t f32, bias_f32;      // type of out, residual and pre; of the bias
   // Rows are 16-byte aligned: TMA moves them.  It writes whole 16-byte parts, past the end of a row that ends inside
   // one: 1 where rows do, and the last columns go element by element; 2 where they do not, or may be written past.
@@ -150,14 +156,15 @@ __device__ __forceinline__ void bulk_wait_read() {
 
 // One operand's block of all planes: rows i0 .. i0 + 127, r0 .. r0 + 63.
 template <bool PAIR, bool MN, int PLANES>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int32_t i0, int32_t r0, uint32_t bar) {
+__device__ __forceinline__ void load_operand(uint32_t dst, uint32_t plane, const CUtensorMap* map, int32_t i0, int32_t r0,
+                                             uint32_t bar) {
 #pragma unroll
   for (int pl = 0; pl < PLANES; ++pl) {
     if constexpr (MN) {
-      load_box<PAIR>(dst + pl * kTileBytes, map, i0, r0, pl, bar);
-      load_box<PAIR>(dst + pl * kTileBytes + kChunkBytes, map, i0 + 64, r0, pl, bar);
+      load_box<PAIR>(dst + pl * plane, map, i0, r0, pl, bar);
+      load_box<PAIR>(dst + pl * plane + kChunkBytes, map, i0 + 64, r0, pl, bar);
     } else {
-      load_box<PAIR>(dst + pl * kTileBytes, map, r0, i0, pl, bar);
+      load_box<PAIR>(dst + pl * plane, map, r0, i0, pl, bar);
     }
   }
 }
@@ -171,9 +178,10 @@ struct DmTile {
 // A worker's way through the tiles: every step-th one.  Where sums are cut, the tiles of the first `share` blocks of r
 // come first, then those of the next: workers that run at once share what they read.  (Shares that end and begin inside
 // tiles, so that all workers have the same, read it again and again: 65536 x 1024 x 1024 123 us against 100.)
-template <bool PAIR>
+template <int BN>
 struct Walk {
-  static constexpr int kSide = PAIR ? 256 : 128;
+  static constexpr bool PAIR = BN == 256;
+  static constexpr int kSide = PAIR ? 256 : 128;  // rows of a tile
   const DmArgs& p;
   int rank, step, at, end;
   __device__ __forceinline__ Walk(const DmArgs& args, int r) : p(args), rank(r) {
@@ -194,7 +202,7 @@ struct Walk {
     const int ni = rem / mm;
     const int mi = sg * kSuper + rem - ni * mm;
     x.a_row = mi * kSide + rank * kRows;
-    x.col = ni * kSide;
+    x.col = ni * BN;
     x.b_row = x.col + (PAIR ? rank * kRows : 0);
     return x;
   }
@@ -268,17 +276,24 @@ __device__ __forceinline__ void piece_in(uint8_t* piece, const char* from, int64
 
 constexpr bool flushes(int major, int planes) { return planes == 3 || major == 2; }
 
-template <bool PAIR, int MAJOR, int PLANES>
+template <int BN, int MAJOR, int PLANES>
 __global__ void __launch_bounds__(kDmThreads, 1)
     dense_mm_kernel(const DmArgs p, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                     const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap rmap,
                     const __grid_constant__ CUtensorMap pmap) {
-  using S = Shape<PLANES>;
+  using S = Shape<PLANES, BN>;
+  constexpr bool PAIR = BN == 256;
+  static_assert(BN != 32 || MAJOR == 0, "32 columns of an MN-major operand are half a row of its layout");
   constexpr bool kAmn = MAJOR == 2, kBmn = MAJOR >= 1;
   constexpr bool kFlush = flushes(MAJOR, PLANES);
-  constexpr int kBN = PAIR ? 256 : 128;
-  constexpr int kCols = kBN / 2;  // columns of an epilogue thread
+  constexpr int kBN = BN;
+  constexpr int kCols = kBN / S::parts;  // columns of an epilogue thread
   constexpr int kCtas = PAIR ? 2 : 1;
+  // Of few rows a stage holds those that are there, so that more of them are on their way.  The products read on past
+  // them, into what comes next in shared memory: rows of the accumulator that nobody reads.
+  const uint32_t a_bytes = BN == 32 ? (uint32_t)p.a_rows * (kBlock * 2) : kTileBytes;
+  const uint32_t stage_bytes = BN == 32 ? PLANES * (a_bytes + S::b_bytes) : S::stage_bytes;
+  const int stages = BN == 32 ? p.stages : S::stages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t bars[2 * S::stages + 5 + 2 * kOutWarps];
   __shared__ uint32_t tmem_base_slot;
@@ -296,13 +311,13 @@ __global__ void __launch_bounds__(kDmThreads, 1)
   if constexpr (PAIR) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S::stages; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(full0 + 8 * s, 1);
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, kCtas * kOutWarps);
+      mbar_init(tempty0 + 8 * b, kCtas * 4 * S::parts);
     }
     for (int w = 0; w < 2 * kOutWarps; ++w) mbar_init(rfull0 + 8 * w, 1);
     mbar_init(drained, 1);
@@ -322,10 +337,10 @@ __global__ void __launch_bounds__(kDmThreads, 1)
       // ---------------- TMA producer ----------------
       const uint32_t count_at = PAIR ? in_cta(full0, 0) : full0;
       int s = 0;
-      uint32_t ph = 0, issued = 0;  // issued: blocks so far, at most S::stages counted
+      uint32_t ph = 0, issued = 0;  // issued: blocks so far, at most stages counted
       bool ok = true;
       DmTile x;
-      for (Walk<PAIR> way(p, (int)rank); ok && way.more(); way.go()) {
+      for (Walk<BN> way(p, (int)rank); ok && way.more(); way.go()) {
         x = way.tile();
         for (int j = 0; j < x.nkb; ++j) {
           if (!park(empty0 + 8 * s, ph ^ 1)) {
@@ -333,16 +348,16 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t dst = base + (uint32_t)s * S::stage_bytes;
+          const uint32_t dst = base + (uint32_t)s * stage_bytes;
           const int32_t r0 = (x.k0 + j) * kBlock;
           if (elected()) {
-            if (rank == 0) mbar_expect_tx(full0 + 8 * s, kCtas * S::stage_bytes);
-            load_operand<PAIR, kAmn, PLANES>(dst, &amap, x.a_row, r0, count_at + 8 * s);
-            load_operand<PAIR, kBmn, PLANES>(dst + PLANES * kTileBytes, &bmap, x.b_row, r0, count_at + 8 * s);
+            if (rank == 0) mbar_expect_tx(full0 + 8 * s, kCtas * stage_bytes);
+            load_operand<PAIR, kAmn, PLANES>(dst, a_bytes, &amap, x.a_row, r0, count_at + 8 * s);
+            load_operand<PAIR, kBmn, PLANES>(dst + PLANES * a_bytes, S::b_bytes, &bmap, x.b_row, r0, count_at + 8 * s);
           }
           __syncwarp();
-          if (issued < S::stages) ++issued;
-          if (++s == S::stages) {
+          if (issued < stages) ++issued;
+          if (++s == stages) {
             s = 0;
             ph ^= 1;
           }
@@ -352,8 +367,8 @@ __global__ void __launch_bounds__(kDmThreads, 1)
       // after a failure no MMA may come, and a stage's own barrier says that it is filled (a pair's odd CTA has none
       // and waits the limit out).
       for (uint32_t i = 0; i < issued; ++i) {
-        s = s == 0 ? S::stages - 1 : s - 1;
-        if (s == S::stages - 1) ph ^= 1;
+        s = s == 0 ? stages - 1 : s - 1;
+        if (s == stages - 1) ph ^= 1;
         if (!park((ok || rank != 0 ? empty0 : full0) + 8 * s, ph) && lane == 0) set_error(p.err, CTR_ERR_TIMEOUT);
       }
     } else if (warp == 1) {
@@ -365,14 +380,14 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         // 16 of r further: 32 bytes along K-major rows, 16 rows of 128 bytes in MN-major chunks (in units of 16 bytes)
         constexpr uint32_t kStepA = kAmn ? 128 : 2, kStepB = kBmn ? 128 : 2;
         const uint64_t a0 = kAmn ? desc_mn(base) : smem_desc_sw128(base);
-        const uint64_t b0 = kBmn ? desc_mn(base + PLANES * kTileBytes) : smem_desc_sw128(base + PLANES * kTileBytes);
+        const uint64_t b0 = kBmn ? desc_mn(base + PLANES * a_bytes) : smem_desc_sw128(base + PLANES * a_bytes);
         int s = 0;
         // Without planes the two accumulators take turns, b's phase bph.  With planes, the first (phase bph) has the main
         // products, the other (phase cph) the rest.
         uint32_t ph = 0, b = 0, bph = 0, cph = 0;
         bool ok = true;
         DmTile x;
-        for (Walk<PAIR> way(p, 0); ok && way.more(); way.go()) {
+        for (Walk<BN> way(p, 0); ok && way.more(); way.go()) {
           x = way.tile();
           const int nkb = x.nkb;
           for (int j = 0; ok && j < nkb; ++j) {
@@ -385,7 +400,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             ok = ok && park(full0 + 8 * s, ph);
             if (!ok) break;
             fence_after();
-            const uint64_t at = (uint64_t)((uint32_t)s * (S::stage_bytes >> 4));
+            const uint64_t at = (uint64_t)((uint32_t)s * (stage_bytes >> 4));
             if constexpr (PLANES == 3) {
               // the small products first: they need not wait until the main accumulator has been read
               if (elected()) {
@@ -393,8 +408,8 @@ __global__ void __launch_bounds__(kDmThreads, 1)
                 for (int q = 0; q < 5; ++q)
 #pragma unroll
                   for (int k = 0; k < kBlock / 16; ++k)
-                    mma_dense<PAIR>(tmem + kBN, a0 + at + kPa[q] * (kTileBytes >> 4) + k * kStepA,
-                                    b0 + at + kPb[q] * (kTileBytes >> 4) + k * kStepB, idesc, !copens || (q | k) != 0);
+                    mma_dense<PAIR>(tmem + kBN, a0 + at + kPa[q] * (a_bytes >> 4) + k * kStepA,
+                                    b0 + at + kPb[q] * (S::b_bytes >> 4) + k * kStepB, idesc, !copens || (q | k) != 0);
               }
               __syncwarp();
               if (opens) ok = park(tempty0, bph ^ 1);
@@ -415,7 +430,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
               b ^= PLANES == 3 ? 0 : 1;
             }
             if (ccloses) cph ^= 1;
-            if (++s == S::stages) {
+            if (++s == stages) {
               s = 0;
               ph ^= 1;
             }
@@ -434,7 +449,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
     const int q = warp & 3;            // TMEM lane quarter this warp may read
     const int part = (warp - 4) >> 2;  // which half of the columns
     const uint32_t lane_base = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(part * kCols);
-    uint8_t* staging = smem_raw + (base - raw) + S::stages * S::stage_bytes + (warp - 4) * (S::places * kPiece);
+    uint8_t* staging = smem_raw + (base - raw) + stages * stage_bytes + (warp - 4) * (S::places * kPiece);
     const uint32_t rfull = rfull0 + 16 * (warp - 4);
     const uint32_t tempty_at = PAIR ? in_cta(tempty0, 0) : tempty0;
     const bool f32 = MAJOR == 2 ? p.f32 != 0 : PLANES == 3;  // type of the results
@@ -488,13 +503,13 @@ __global__ void __launch_bounds__(kDmThreads, 1)
     };
     // The first pieces of residual.  Later ones, the next tile's too, are asked for as their places become free: asked for
     // at their tile's start, they took 1 us of every tile.
-    Walk<PAIR> way(p, (int)rank);
-    if (wide_res && way.more()) {
+    Walk<BN> way(p, (int)rank);
+    if (wide_res && part < S::parts && way.more()) {
       const Part f = part_of(way.tile());
       for (int h = 0; h < S::turns; ++h)
         if (h * width < f.cols) ask(h, f.row0, f.col0 + h * width);
     }
-    while (ok && way.more()) {
+    while (ok && part < S::parts && way.more()) {
       const DmTile x = way.tile();
       way.go();
       const Part me = part_of(x);
@@ -519,7 +534,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
           fence_after();
           // 64 columns at once; with planes, whose epilogue has more to hold, 32 (spills go to L2: all but nothing is left of
           // L1 beside the operands)
-          constexpr int kStep = PLANES == 3 ? 32 : 64;
+          constexpr int kStep = PLANES == 3 || kCols < 64 ? 32 : 64;
 #pragma unroll
           for (int c = 0; c < kCols; c += kStep) {
             uint32_t v0[32], v1[32];
@@ -589,7 +604,10 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         const float bias = has_bias ? bias_at(p, col + lane) : 0.f;
         uint8_t* row = piece + lane * 128;
         auto leave = [&](const CUtensorMap* map, int wide, char* to, int64_t ld, const uint8_t* from, int at) {
-          if (wide == 2 || (wide == 1 && at + width <= p.n)) {
+          if (kCols < 64 && !f32) {  // half a piece
+            __syncwarp();
+            piece_out<uint16_t>(from, to, ld, row0, nrows, at, min(p.n, at + kCols), wide != 0);
+          } else if (wide == 2 || (wide == 1 && at + width <= p.n)) {
             if (lane == 0) store_box(map, at, (int32_t)row0, 0, smem_u32(from));
           } else if (f32) {
             piece_out<float>(from, to, ld, row0, nrows, at, p.n, false);
@@ -816,13 +834,13 @@ int wide(const void* p, int64_t rows, int64_t cols, int64_t ld, int eb) {
 }
 
 DmArgs dm_args(const MmCall& c, const MmPlan& plan) {
-  const int side = plan.pair ? 256 : 128;
+  const int side = plan.side();
   DmArgs p = {};
   p.m = (int32_t)c.m;
   p.n = (int32_t)c.n;
   p.kb = (int32_t)ceil_div(c.r, kBlock);
   p.mt = (int32_t)ceil_div(c.m, side);
-  p.nt = (int32_t)ceil_div(c.n, side);
+  p.nt = (int32_t)ceil_div(c.n, plan.columns);
   p.share = (int32_t)plan.share;
   p.parts = (int32_t)plan.parts;
   p.err = c.err;
@@ -832,9 +850,10 @@ DmArgs dm_args(const MmCall& c, const MmPlan& plan) {
   return p;
 }
 
-template <bool PAIR, int MAJOR, int PLANES>
+template <int BN, int MAJOR, int PLANES>
 int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) {
-  constexpr int kCtas = PAIR ? 2 : 1, kSide = PAIR ? 256 : 128;
+  constexpr int kCtas = BN == 256 ? 2 : 1, kSide = BN == 256 ? 256 : 128;
+  using S = Shape<PLANES, BN>;
   DmArgs p = dm_args(c, plan);
   const int64_t tiles = (int64_t)p.mt * p.nt;
   if (tiles > INT32_MAX - 65536) return CTR_ERR_UNSUPPORTED;
@@ -860,32 +879,39 @@ int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) 
     p.wide_res = wide(p.res, c.m, c.n, p.ldr, eb);
     p.wide_pre = wide(p.pre, c.m, c.n, p.ldp, eb);
   }
+  p.a_rows = BN == 32 ? (int)imin64(kRows, ceil_div(c.m, 8) * 8) : kRows;
+  p.stages = (int)imin64(S::stages, (S::smem - 1024 - S::room) / (PLANES * (p.a_rows * kBlock * 2 + (int)S::b_bytes)));
   CUtensorMap amap, bmap;
-  if (!operand_map(&amap, c.a, PLANES, MAJOR == 2 ? 64 : kRows) || !operand_map(&bmap, c.b, PLANES, MAJOR >= 1 ? 64 : kRows))
+  if (!operand_map(&amap, c.a, PLANES, MAJOR == 2 ? 64 : p.a_rows) || !operand_map(&bmap, c.b, PLANES, MAJOR >= 1 ? 64 : std::min(BN, kRows)))
     return CTR_ERR_CUDA;
   CUtensorMap omap = amap, rmap = amap, pmap = amap;  // not used unless the rows are aligned
   if (p.wide_out && !piece_map(&omap, p.out, p.f32 != 0, out_rows, out_cols, p.ldo)) return CTR_ERR_CUDA;
   if (p.wide_res && !piece_map(&rmap, p.res, p.f32 != 0, c.m, c.n, p.ldr)) return CTR_ERR_CUDA;
   if (p.wide_pre && !piece_map(&pmap, p.pre, p.f32 != 0, c.m, c.n, p.ldp)) return CTR_ERR_CUDA;
-  auto k = dense_mm_kernel<PAIR, MAJOR, PLANES>;
+  auto k = dense_mm_kernel<BN, MAJOR, PLANES>;
   static std::atomic<uint64_t> ready{0};
   if (!once_per_device(ready, [&] {
         // the split of registers between the warps waits for ever if the kernel was launched with fewer
         cudaFuncAttributes fa;
         if (cudaFuncGetAttributes(&fa, k) != cudaSuccess || (flushes(MAJOR, PLANES) && fa.numRegs != kLaunchRegs)) return false;
-        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<PLANES>::smem) == cudaSuccess;
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) == cudaSuccess;
       }))
     return CTR_ERR_CUDA;
-  const cudaError_t e = launch_after(k, dim3((unsigned)(kCtas * imax64(1, workers))), kDmThreads, Shape<PLANES>::smem, s, kCtas,
+  const cudaError_t e = launch_after(k, dim3((unsigned)(kCtas * imax64(1, workers))), kDmThreads, S::smem, s, kCtas,
                                      p, amap, bmap, omap, rmap, pmap);
   return e == cudaSuccess ? launch_status() : CTR_ERR_CUDA;
 }
 
+template <int BN, int MAJOR>
+int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) {
+  return c.planes == 1 ? launch_dm<BN, MAJOR, 1>(c, plan, part, s) : launch_dm<BN, MAJOR, 3>(c, plan, part, s);
+}
+
 template <int MAJOR>
 int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) {
-  if (plan.pair)
-    return c.planes == 1 ? launch_dm<true, MAJOR, 1>(c, plan, part, s) : launch_dm<true, MAJOR, 3>(c, plan, part, s);
-  return c.planes == 1 ? launch_dm<false, MAJOR, 1>(c, plan, part, s) : launch_dm<false, MAJOR, 3>(c, plan, part, s);
+  if constexpr (MAJOR == 0)
+    if (plan.columns == 32) return launch_dm<32, MAJOR>(c, plan, part, s);
+  return plan.columns == 256 ? launch_dm<256, MAJOR>(c, plan, part, s) : launch_dm<128, MAJOR>(c, plan, part, s);
 }
 
 }  // namespace
@@ -895,9 +921,12 @@ MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
   const int64_t kb = ceil_div(r, kBlock);
   const int64_t pairs = ceil_div(m, 256) * ceil_div(n, 256);
   const int64_t sms = num_sms();
-  w.pair = m > 128 && n > 128 && (pairs >= sms / 3 || (major == 2 && kb >= 64));
-  const int64_t side = w.side(), most = sms / (w.pair ? 2 : 1);
+  const bool pair = m > 128 && n > 128 && (pairs >= sms / 3 || (major == 2 && kb >= 64));
+  if (pair) w.columns = 256;
+  const int64_t side = w.side(), most = sms / (pair ? 2 : 1);
   const int64_t tiles = ceil_div(m, side) * ceil_div(n, side);
+  // few rows: more and narrower tiles, so that more SMs read the weights
+  if (!pair && major == 0 && 2 * tiles <= sms && n > 32) w.columns = 32;
   if (major != 2) return w;
   // Sums over a batch are cut into the number of parts that takes least, in blocks' times (0.27 us with planes of bf16
   // alone): the rounds of all workers, six blocks for each tile's setting up and end, and each part's writing and reading.
@@ -905,7 +934,7 @@ MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
   for (int64_t parts = 1; parts <= imax64(1, kb / kMinShare) && (parts - 1) * tiles <= 3 * most; ++parts) {
     const double rounds = (double)ceil_div(tiles * parts, most);
     const double time = rounds * (planes * (planes == 3 ? 2 : 1) * (double)ceil_div(kb, parts) + 6) +
-                        (parts > 1 ? (double)(tiles * parts) * (w.pair ? 0.28 : 0.14) + 8 : 0);
+                        (parts > 1 ? (double)(tiles * parts) * (pair ? 0.28 : 0.14) + 8 : 0);
     if (parts == 1 || time < best) {
       best = time;
       w.share = parts > 1 ? ceil_div(kb, parts) : 0;

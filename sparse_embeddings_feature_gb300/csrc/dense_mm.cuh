@@ -31,13 +31,13 @@ struct MmCall {
   int* err = nullptr;
 };
 
-// How a product is taken apart: CTA pairs on 256 x 256 tiles or CTAs on 128 x 128; where share is not 0, sums in `parts`
+// How a product is taken apart: CTA pairs on 256 x 256 tiles, or CTAs on 128 x 128 or 128 x 32; where share is not 0, sums in `parts`
 // of `share` blocks of 64, which leave as fp32 (whole tiles, in `places` of the workspace) and are added up by a second
 // kernel.
 struct MmPlan {
-  bool pair = false;
+  int columns = 128;  // of a tile
   int64_t share = 0, parts = 1, places = 0;
-  int side() const { return pair ? 256 : 128; }
+  int side() const { return columns == 256 ? 256 : 128; }  // its rows
   size_t bytes() const { return (size_t)places * side() * side() * 4; }
 };
 MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r);
