@@ -11,8 +11,9 @@
 // rounding, in one read of dy and pre: a thread holds its columns' sums over a strip of rows, the strips are added
 // in their order by a second kernel.
 //
-// Up to 8 rows are not worth a tensor core's tile: a warp reads one row of W, as it lies in memory, and multiplies
-// it with all of x's, kept as fp32 in shared memory.  Bound by W's bytes, and below some megabytes by latency.
+// A few rows are not worth a tensor core's tile: a warp reads one to four rows of W, as they lie in memory, and multiplies
+// them with all of x's, kept as fp32 in shared memory.  Bound by W's bytes (one row x 4096 -> 4096 bf16 9.7 us, 3.5 TB/s),
+// and below some megabytes by latency.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -182,7 +183,8 @@ __global__ void __launch_bounds__(kThreads) zero_rows_kernel(T* out, int64_t row
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
-constexpr int kFewRows = 8, kFewChunk = 1024;  // rows at most; columns of x in shared memory at a time
+constexpr int kFewRows = 8;      // at most
+constexpr int kFewWords = 4096;  // of x in shared memory at a time
 
 struct FewArgs {
   const void* x;
@@ -195,72 +197,105 @@ struct FewArgs {
   int32_t rows, n, k, act;
 };
 
-template <typename T, int VB, int ROWS>
+// COLS rows of W to a warp: of more rows of x, what is read of it in shared memory serves more products (8 rows x 4096
+// x 4096 bf16, one row of W to a warp, 65 us).
+template <typename T, int VB, int ROWS, int COLS>
 __global__ void __launch_bounds__(kThreads) dense_few_kernel(const FewArgs a) {
   using C = Chunk<T, VB>;
-  constexpr int N = C::n;
-  constexpr int kHeld = N == 1 ? 16 : 4;  // parts of W's row on their way at once
-  __shared__ float x[ROWS][kFewChunk];
+  constexpr int N = C::n, kChunk = kFewWords / ROWS;
+  constexpr int kHeld = N == 1 ? 8 : 8 / COLS;  // parts of a row of W on their way at once
+  constexpr int kStep = kHeld * 32 * N;
+  __shared__ float x[ROWS][kChunk];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = blockIdx.x * (kThreads / 32) + warp;
-  const T* row = (const T*)a.w + (int64_t)min(col, a.n - 1) * a.ldw;
-  float acc[ROWS];
+  const int col0 = (blockIdx.x * (kThreads / 32) + warp) * COLS;
+  // eight columns of a lane are two parts of four, 128 words apart, so that lanes read consecutive words
+  auto place = [](int c) { return N == 8 ? (c & ~255) + ((c >> 2) & 1) * 128 + ((c >> 3) & 31) * 4 + (c & 3) : c; };
+  float2 acc[ROWS][COLS];
 #pragma unroll
-  for (int t = 0; t < ROWS; ++t) acc[t] = 0.f;
+  for (int t = 0; t < ROWS; ++t)
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) acc[t][j] = make_float2(0.f, 0.f);
   grid_wait();
-  for (int k0 = 0; k0 < a.k; k0 += kFewChunk) {
-    const int len = min(kFewChunk, a.k - k0);
-    typename C::Raw held[kHeld];
+  for (int k0 = 0; k0 < a.k; k0 += kChunk) {
+    const int len = min(kChunk, a.k - k0);
+    typename C::Raw held[COLS][kHeld];
     auto fetch = [&](int c0) {
 #pragma unroll
-      for (int h = 0; h < kHeld; ++h) {
-        const int c = c0 + (h * 32 + lane) * N;
-        held[h] = typename C::Raw{};
-        if (c < len) held[h] = *(const typename C::Raw*)(row + k0 + c);
+      for (int j = 0; j < COLS; ++j) {
+        const T* row = (const T*)a.w + (int64_t)min(col0 + j, a.n - 1) * a.ldw + k0;
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+          const int c = c0 + (h * 32 + lane) * N;
+          held[j][h] = typename C::Raw{};
+          if (c < len) held[j][h] = *(const typename C::Raw*)(row + c);
+        }
       }
     };
     fetch(0);  // W is on its way while x is laid out
     if (k0 > 0) __syncthreads();
-    for (int e = threadIdx.x; e < ROWS * kFewChunk; e += kThreads) {
-      const int t = e / kFewChunk, c = e % kFewChunk;
-      x[t][c] = t < a.rows && c < len ? to_f32<T>(((const T*)a.x)[t * a.ldx + k0 + c]) : 0.f;
+    const int cover = (len + 255) & ~255;  // what the lanes may read
+    for (int e = threadIdx.x; e < ROWS * cover; e += kThreads) {
+      const int t = e / cover, c = e - t * cover;
+      x[t][place(c)] = t < a.rows && c < len ? to_f32<T>(((const T*)a.x)[t * a.ldx + k0 + c]) : 0.f;
     }
     __syncthreads();
-    for (int c0 = 0; c0 < len; c0 += kHeld * 32 * N) {
+    for (int c0 = 0; c0 < len; c0 += kStep) {
       if (c0 > 0) fetch(c0);
 #pragma unroll
       for (int h = 0; h < kHeld; ++h) {
         const int c = c0 + (h * 32 + lane) * N;
-        if (c < len) {
-          float v[N];
-          C::unpack(held[h], v);
+        if (c >= len) continue;
+        float w[COLS][N];
 #pragma unroll
-          for (int t = 0; t < ROWS; ++t)
+        for (int j = 0; j < COLS; ++j) C::unpack(held[j][h], w[j]);
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[t] = fmaf(x[t][c + i], v[i], acc[t]);
+        for (int t = 0; t < ROWS; ++t) {
+          if constexpr (N == 1) {
+            const float v = x[t][c];
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) acc[t][j].x = fmaf(v, w[j][0], acc[t][j].x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+              const float4 v = *(const float4*)&x[t][place(c + i)];
+#pragma unroll
+              for (int j = 0; j < COLS; ++j) {
+                acc[t][j] = fma2(make_float2(v.x, v.y), make_float2(w[j][i], w[j][i + 1]), acc[t][j]);
+                acc[t][j] = fma2(make_float2(v.z, v.w), make_float2(w[j][i + 2], w[j][i + 3]), acc[t][j]);
+              }
+            }
+          }
         }
       }
     }
   }
-#pragma unroll
-  for (int t = 0; t < ROWS; ++t)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(kFull, acc[t], o);
+  // lane t + ROWS j gets the sum of row t and column j
   float z = 0.f;
 #pragma unroll
-  for (int t = 0; t < ROWS; ++t) z = t == lane ? acc[t] : z;
-  if (lane >= a.rows || col >= a.n) return;
+  for (int j = 0; j < COLS; ++j)
+#pragma unroll
+    for (int t = 0; t < ROWS; ++t) {
+      float v = acc[t][j].x + acc[t][j].y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+      z = lane == t + ROWS * j ? v : z;
+    }
+  const int t = lane % ROWS, col = col0 + lane / ROWS;
+  if (lane >= ROWS * COLS || t >= a.rows || col >= a.n) return;
   if (a.bias) z += to_f32<T>(((const T*)a.bias)[col]);
-  if (a.pre) ((T*)a.pre)[lane * a.ldp + col] = from_f32<T>(z);
+  if (a.pre) ((T*)a.pre)[t * a.ldp + col] = from_f32<T>(z);
   z = activation(a.act, z);
-  if (a.residual) z += to_f32<T>(((const T*)a.residual)[lane * a.ldr + col]);
-  ((T*)a.y)[lane * a.ldy + col] = from_f32<T>(z);
+  if (a.residual) z += to_f32<T>(((const T*)a.residual)[t * a.ldr + col]);
+  ((T*)a.y)[t * a.ldy + col] = from_f32<T>(z);
 }
+
+// Rows of W to a warp of a call with `rows` rows.
+int few_cols(int64_t rows) { return rows <= 1 ? 1 : rows <= 4 ? 2 : 4; }
 
 template <typename T, int VB>
 auto few_kernel(int64_t rows) {
-  return rows <= 1 ? dense_few_kernel<T, VB, 1> : rows <= 2 ? dense_few_kernel<T, VB, 2>
-       : rows <= 4 ? dense_few_kernel<T, VB, 4> : dense_few_kernel<T, VB, 8>;
+  return rows <= 1 ? dense_few_kernel<T, VB, 1, 1> : rows <= 2 ? dense_few_kernel<T, VB, 2, 2>
+       : rows <= 4 ? dense_few_kernel<T, VB, 4, 2> : dense_few_kernel<T, VB, 8, 4>;
 }
 
 // ---------------------------------------------------------------------------
@@ -340,6 +375,11 @@ bool operand(MmOperand* o, const void* p, ctr_dtype dtype, int64_t rows, int64_t
   return fine(launch_after(k, grid, kThreads, 0, s, 1, (const __nv_bfloat16*)p, rows, (int)cols, ld, room, o->ld, o->plane));
 }
 
+// Whether a forward call goes to the kernel for few rows.  bf16 matrices that the tensor cores can read as they lie: one or
+// two rows (4 rows of 1024 -> 2048 7.8 us against 7.6, of 4096 -> 4096 26 against 19).  Others would have W laid out first:
+// up to eight (fp32 1024 -> 2048 14 us against 19, 4096 -> 4096 51 against 76; bf16 479 -> 512 6.0 against 8.0).
+bool few_rows(int64_t rows, bool as_they_lie) { return rows <= (as_they_lie ? 2 : kFewRows); }
+
 bool off(const void* p, int by) { return ((uintptr_t)p % by) != 0; }
 
 int check_dense(ctr_dtype dtype, int64_t rows, int64_t n, int64_t k, int act) {
@@ -375,13 +415,14 @@ extern "C" int ctr_dense(const void* x, ctr_dtype dtype, int64_t rows, int64_t k
   if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
   if (rows == 0) return CTR_OK;
   cudaStream_t s = (cudaStream_t)stream;
-  if (rows <= kFewRows) {
+  if (few_rows(rows, direct(x, dtype, rows, ldx) && direct(w, dtype, n, ldw))) {
     FewArgs a = {x, w, bias, residual, y, pre, ldx, ldw, ld_residual, ld_y, ld_pre, (int32_t)rows, (int32_t)n, (int32_t)k, act};
     const bool vec = !off(w, 16) && (ldw * eb) % 16 == 0 && (k * eb) % 16 == 0;
     auto kernel = dtype == CTR_F32 ? (vec ? few_kernel<float, 16>(rows) : few_kernel<float, 4>(rows))
                                    : (vec ? few_kernel<__nv_bfloat16, 16>(rows) : few_kernel<__nv_bfloat16, 2>(rows));
-    return fine(launch_after(kernel, dim3((unsigned)ceil_div(n, kThreads / 32)), kThreads, 0, s, 1, a)) ? launch_status()
-                                                                                                    : CTR_ERR_CUDA;
+    return fine(launch_after(kernel, dim3((unsigned)ceil_div(n, kThreads / 32 * few_cols(rows))), kThreads, 0, s, 1, a))
+               ? launch_status()
+               : CTR_ERR_CUDA;
   }
   WsCarver c(ws, ws_bytes);
   const Room room = carve(c, dtype, rows, n, k, Wants{!direct(x, dtype, rows, ldx), !direct(w, dtype, n, ldw), false, false, false});

@@ -13,7 +13,7 @@ DT = {"f32": torch.float32, "bf16": torch.bfloat16}
 ACTS = ["none", "relu", "silu", "gelu", "sigmoid"]
 # rows, n, k, padding of the rows (0: dense)
 FEW = [(1, 1, 1, 0), (1, 512, 479, 0), (2, 7, 1030, 1), (3, 100, 64, 8), (5, 33, 2051, 0), (8, 257, 1024, 0)]
-SIZES = FEW + [(9, 24, 40, 0), (16, 1, 3, 0), (64, 128, 64, 0), (65, 130, 72, 8), (127, 479, 129, 0), (128, 128, 128, 0),
+SIZES = FEW + [(2, 512, 1024, 0), (3, 512, 1024, 0), (4, 130, 4100, 4), (8, 66, 8200, 0), (9, 24, 40, 0), (16, 1, 3, 0), (64, 128, 64, 0), (65, 130, 72, 8), (127, 479, 129, 0), (128, 128, 128, 0),
                (129, 129, 65, 3), (300, 512, 479, 0), (257, 264, 520, 0), (1000, 96, 1000, 4), (2000, 300, 77, 0),
                (4100, 520, 200, 8), (70, 135, 479, 1), (300, 479, 135, 1)]
 LARGE = [(13000, 264, 512, 0), (3000, 2304, 264, 0), (40000, 257, 129, 0), (2500, 1544, 1100, 0)]
