@@ -33,16 +33,30 @@ class ExpertLayer:
     backward needs, a copy of the scores with it: backward(dy) returns (dx, dscores, dw) for the latest
     forward, whatever became of its arguments.  Results are the layer's own buffers, which the next call
     writes.  Its calls run on the current device, which has to be
-    `device`."""
+    `device`.
+
+    score ("softmax" or "sigmoid"), groups, group_k and factor, or a bias given to forward, make the routing a
+    balanced one (ctr_expert_route_balanced): choices by score function + bias in the best groups, weights from
+    the score function.  The bias is the program's: `loads` has what it goes by."""
 
     def __init__(self, tokens: int, width: int, out_width: int, experts: int, k: int, dtype=torch.float32,
-                 renormalize: bool = True, train: bool = False, device="cuda"):
+                 renormalize: bool = True, train: bool = False, device="cuda", score: str = "softmax", groups: int = 1,
+                 group_k: Optional[int] = None, factor: float = 1.0):
         if dtype not in ctr.DTYPES:
             raise ValueError("dtype must be torch.float32 or torch.bfloat16")
         if not 1 <= k <= min(experts, ctr.MAX_CHOICES) or experts > ctr.MAX_EXPERTS:
             raise ValueError(f"need 1 <= k <= min(experts, {ctr.MAX_CHOICES}) and experts <= {ctr.MAX_EXPERTS}")
         if min(tokens, width, out_width) < 1:
             raise ValueError("tokens, width and out_width must be positive")
+        self.groups, self.group_k = groups, groups if group_k is None else group_k
+        if score not in ctr.SCORES:
+            raise ValueError(f"score must be one of {', '.join(ctr.SCORES)}")
+        if not 1 <= groups <= ctr.MAX_GROUPS or experts % groups or not 1 <= self.group_k <= groups \
+                or k > self.group_k * (experts // groups):
+            raise ValueError(f"need groups <= {ctr.MAX_GROUPS} that divide experts, 1 <= group_k <= groups, and k experts in "
+                             f"group_k groups")
+        self.score, self.factor = ctr.SCORES[score], float(factor)
+        self.balanced = score != "softmax" or self.group_k < groups or self.factor != 1.0
         self.tokens, self.width, self.out_width, self.experts, self.k = tokens, width, out_width, experts, k
         self.dtype, self.renormalize, self.train = dtype, bool(renormalize), bool(train)
         T, K, N, E, R = tokens, width, out_width, experts, tokens * k
@@ -85,14 +99,20 @@ class ExpertLayer:
         self.scores = None
         ctr.ctr_fp8_quantize_blocks(w, self.wq, self.ws, self.ws_mm, *((self.wtq, self.wts) if self.train else ()))
 
-    def forward(self, x: torch.Tensor, scores: torch.Tensor) -> torch.Tensor:
-        """y [tokens, out_width] of x [tokens, width] under the router's scores [tokens, experts]."""
+    def forward(self, x: torch.Tensor, scores: torch.Tensor, bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """y [tokens, out_width] of x [tokens, width] under the router's scores [tokens, experts] and, for balance, a
+        bias [experts] (fp32) on the choices alone."""
         # the calls see the padded width of x and look its rows up through the map: its sizes are checked here
         if not isinstance(x, torch.Tensor) or x.shape != (self.tokens, self.width):
             raise ValueError(f"x must be {(self.tokens, self.width)}")
         self.scores = None   # until this forward is complete there is none
-        ctr.ctr_expert_route(scores, self.k, self.renormalize, self.expert, self.weight, self.slot, self.token,
-                             self.offsets, self.ws_route)
+        self.by_balance = self.balanced or bias is not None
+        maps = (self.expert, self.weight, self.slot, self.token, self.offsets, self.ws_route)
+        if self.by_balance:
+            ctr.ctr_expert_route_balanced(scores, self.k, self.score, bias, self.groups, self.group_k, self.renormalize,
+                                          self.factor, *maps)
+        else:
+            ctr.ctr_expert_route(scores, self.k, self.renormalize, *maps)
         if self.train:
             if scores.dtype not in self.kept:
                 self.kept[scores.dtype] = tuple(torch.empty(scores.shape, dtype=scores.dtype, device=scores.device)
@@ -127,8 +147,16 @@ class ExpertLayer:
         ctr.ctr_fp8_matmul_wgrad(self.dcq, self.dcs, self.xcq, self.xcs, self.offsets, self.dw, self.ws_mm,
                                  rows=self.tokens * self.k)
         ctr.ctr_expert_combine(self.dxs, self.slot, None, dx, self.ws_rows)
-        ctr.ctr_expert_route_bwd(self.dweight, self.scores, self.renormalize, self.expert, self.dscores, self.ws_route)
+        if self.by_balance:
+            ctr.ctr_expert_route_balanced_bwd(self.dweight, self.scores, self.score, self.renormalize, self.factor,
+                                              self.expert, self.dscores, self.ws_route)
+        else:
+            ctr.ctr_expert_route_bwd(self.dweight, self.scores, self.renormalize, self.expert, self.dscores, self.ws_route)
         return dx, self.dscores, self.dw
+
+    def loads(self) -> torch.Tensor:
+        """Rows of each expert [experts] (int32) in the latest forward, on the device: what a balance bias goes by."""
+        return self.offsets[1:] - self.offsets[:-1]
 
     def grads(self, others: Iterable[torch.Tensor] = ()) -> ctr.GradList:
         """dw and `others` as a list for clip.  For tensors that stay where they are it is built once: it
