@@ -432,6 +432,41 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 // group's two best, and as many choices as there are lanes.  Where that is not enough, all keys in 64 bits: a warp's
 // 64-bit instruction takes 64 cycles, so that a token with 16 exponentials a lane takes 30 us.
 // 65536 x 256, k 8, 4 of 8 groups, all tokens in fp32 with a round a choice for the key and one for its index: 196 us.
+// e^x in 64 bits for |x| <= 700 (beyond, e^-700 and e^700): 2^(j / 64) from a table, the rest, below ln 2 / 128, by five
+// terms of the series: a third of the 64-bit instructions of exp, which a warp is bound by.
+__device__ const double kPowers[64] = {
+    1.0, 1.0108892860517005, 1.0218971486541166, 1.0330248790212284,
+    1.0442737824274138, 1.0556451783605572, 1.0671404006768237, 1.0787607977571199,
+    1.0905077326652577, 1.102382583307841, 1.1143867425958924, 1.1265216186082418,
+    1.1387886347566916, 1.1511892299529827, 1.1637248587775775, 1.1763969916502812,
+    1.189207115002721, 1.202156731452703, 1.215247359980469, 1.22848053610687,
+    1.241857812073484, 1.255380757024691, 1.2690509571917332, 1.2828700160787783,
+    1.2968395546510096, 1.3109612115247644, 1.3252366431597413, 1.339667524053303,
+    1.3542555469368927, 1.3690024229745905, 1.383909881963832, 1.3989796725383112,
+    1.4142135623730951, 1.42961333839197, 1.4451808069770467, 1.460917794180647,
+    1.4768261459394993, 1.4929077282912648, 1.5091644275934228, 1.5255981507445384,
+    1.5422108254079407, 1.559004400237837, 1.5759808451078865, 1.593142151342267,
+    1.6104903319492543, 1.6280274218573478, 1.645755478153965, 1.6636765803267364,
+    1.681792830507429, 1.7001063537185235, 1.718619298122478, 1.7373338352737062,
+    1.7562521603732995, 1.7753764925265212, 1.7947090750031072, 1.8142521755003989,
+    1.8340080864093424, 1.8539791250833855, 1.8741676341103, 1.8945759815869656,
+    1.9152065613971474, 1.9360617934922943, 1.9571441241754002, 1.978456026387951};
+__device__ __forceinline__ double exp_64(double x) {
+  x = fmin(fmax(x, -700.0), 700.0);
+  const double shifted = x * 92.33248261689366 + 0x1.8p52;  // the nearest whole number of 64ths of ln 2, in the low bits
+  const int n = __double2loint(shifted);
+  const double k = shifted - 0x1.8p52;
+  double r = fma(k, -0.01083042468962958, x);  // the first factor has 31 bits: its product is exact
+  r = fma(k, -6.619564634077006e-12, r);
+  double p = fma(r, 1.0 / 120, 1.0 / 24);
+  p = fma(p, r, 1.0 / 6);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0) * r;
+  const double t = kPowers[n & 63];
+  const double y = fma(t, p, t);
+  return __hiloint2double(__double2hiint(y) + ((n >> 6) << 20), __double2loint(y));
+}
+
 template <typename K>
 __device__ __forceinline__ K exp_of(K x);
 template <>
@@ -440,7 +475,7 @@ __device__ __forceinline__ float exp_of<float>(float x) {
 }
 template <>
 __device__ __forceinline__ double exp_of<double>(double x) {
-  return exp(x);
+  return x > -700.0 ? exp_64(x) : 0.0;  // a masked score's, among others
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -475,7 +510,7 @@ __device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&v)
   if (!a.sigmoid) total = row_softmax<double, EPL>(v, a.lanes, m);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const double p = a.sigmoid ? 1 / (1 + exp(-(double)v[i])) : exp((double)v[i] - m) / total;
+    const double p = a.sigmoid ? 1 / (1 + exp_64(-(double)v[i])) : exp_of<double>((double)v[i] - m) / total;
     key[i] = v[i] > -INFINITY && b[i] > -INFINITY ? p + b[i] : none;
   }
   auto take = [](double& x0, double& x1, double x) {
@@ -631,7 +666,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
   auto exact = [&](uint32_t x) {  // a packed key's value in 64 bits
     const int e = 511 - (int)(x & 511u);
     const double l = score_at(a, t, e), b = a.bias ? a.bias[e] : 0.f;
-    return (a.sigmoid ? 1 / (1 + exp(-l)) : exp(l - shift) / sum) + b;
+    return (a.sigmoid ? 1 / (1 + exp_64(-l)) : exp_of<double>(l - shift) / sum) + b;
   };
   if (!plain || grouped) {
     // p's error in parts (two of 2^-24), sigmoid: exponential 4 of 2^-24 and its argument's rounding, sum, reciprocal 4:
