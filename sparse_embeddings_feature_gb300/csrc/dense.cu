@@ -114,8 +114,13 @@ struct DzArgs {
 };
 constexpr int kDzCols = 256;  // columns of a block
 
+// Blocks of an SM: six of aligned rows, whose loads are few and wide (65536 x 1024 bf16 with silu, sums alone: four blocks
+// and two rows at once 79 us, six and one 65; eight, 66 and 18 us more with dz), four of others.
+template <bool VEC>
+constexpr int kDzBlocks = VEC ? 6 : 4;
+
 template <typename T, int PLANES, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
+__global__ void __launch_bounds__(kThreads, kDzBlocks<VEC>) dz_kernel(const DzArgs a) {
   constexpr int N = kPart<T>, kAcross = kDzCols / N, kLanes = kThreads / kAcross;  // threads of a row, rows at a time
   __shared__ float sums[kLanes][kDzCols];
   const int part = threadIdx.x % kAcross, lane = threadIdx.x / kAcross;
@@ -126,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 4) dz_kernel(const DzArgs a) {
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
   grid_wait();
   if (c < a.ld) {
-#pragma unroll 2
+#pragma unroll(VEC ? 1 : 2)
     for (int64_t r = r0 + lane; r < r1; r += kLanes) {
       float v[N], z[N];
       load_part<T, VEC>((const T*)a.dy + r * a.ld_dy, c, a.n, v);
@@ -312,10 +317,10 @@ size_t packed_elems(ctr_dtype dtype, int64_t rows, int64_t cols) {
   return (size_t)(dtype == CTR_F32 ? 3 : 1) * (size_t)rows * (size_t)up8(cols);
 }
 
-// Rows of a strip of dz_kernel: as many blocks as run at once (four an SM of 152), at least 32 rows each.
-int strip_rows(int64_t rows, int64_t n) {
-  const int64_t blocks = ceil_div(up8(n), kDzCols);
-  return (int)imax64(32, ceil_div(rows, imax64(1, 608 / blocks)));
+// Rows of a strip of dz_kernel: as many blocks as run at once on 152 SMs, at least 32 rows each.
+int strip_rows(int64_t rows, int64_t n, bool vec) {
+  const int64_t blocks = ceil_div(up8(n), kDzCols), most = 152 * (vec ? kDzBlocks<true> : kDzBlocks<false>);
+  return (int)imax64(32, ceil_div(rows, imax64(1, most / blocks)));
 }
 
 // What a call takes from the workspace; `carver` is a WsSizer or a WsCarver.
@@ -346,7 +351,7 @@ Room carve(Z& z, ctr_dtype dtype, int64_t rows, int64_t n, int64_t k, const Want
   if (want.w) r.w = take<Z, __nv_bfloat16>(z, packed_elems(dtype, n, k));
   if (want.dz) r.dz = take<Z, __nv_bfloat16>(z, packed_elems(dtype, rows, n));
   if (want.dw) r.part = take<Z, float>(z, mm_plan(2, planes, n, k, rows).bytes() / 4);
-  if (want.strips) r.strips = take<Z, float>(z, (size_t)ceil_div(imax64(rows, 1), strip_rows(rows, n)) * n);
+  if (want.strips) r.strips = take<Z, float>(z, (size_t)ceil_div(imax64(rows, 1), strip_rows(rows, n, true)) * n);  // the most strips
   return r;
 }
 
@@ -497,10 +502,10 @@ extern "C" int ctr_dense_bwd(const void* dy, ctr_dtype dtype, int64_t rows, int6
     a.ld = up8(n);
     a.plane = rows * a.ld;
     a.n = (int32_t)n;
-    a.strip = strip_rows(rows, n);
     a.act = act;
     if (make_dz) dz = MmOperand{room.dz, n, rows, a.ld, a.plane};
     const bool vec = !off(dy, 16) && (ld_dy * eb) % 16 == 0 && (!a.pre || (!off(pre, 16) && (ld_pre * eb) % 16 == 0));
+    a.strip = strip_rows(rows, n, vec);
     const int strips = (int)ceil_div(rows, a.strip);
     const dim3 grid((unsigned)ceil_div(a.ld, kDzCols), (unsigned)strips);
     auto kernel = dtype == CTR_F32 ? (vec ? dz_kernel<float, 3, true> : dz_kernel<float, 3, false>)

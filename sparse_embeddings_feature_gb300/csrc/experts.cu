@@ -610,10 +610,11 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
 }
 
 // Packed keys: the keys' range from the smallest bias on is cut into 2^23 - 4 parts of 1 / scale, numbered from 1.
-// off: what a key may be off by besides p's own error, in parts (2^-24 of a range is half a part): 4 for the sums and
-// products here and for cutting off, and the bias's own, |bias| / 2 ranges for each of two roundings.
+// What a key may be off by besides p's own error, in parts (2^-24 of a range is half a part): three roundings of the
+// bias's part number and one of the sum, half a part each, and one part for cutting off.
 struct Packing {
-  float scale, off;
+  float scale;
+  static constexpr float off = 3.f;
 };
 static_assert(CTR_MAX_EXPERTS <= 512, "an index has 9 bits");
 
@@ -645,7 +646,7 @@ __device__ __forceinline__ Packing pack_range(const RouteArgs& a, float* at, flo
   const float range = 1.f + (hi - lo), scale = 8388604.f / range;
   if (e < CTR_MAX_EXPERTS) at[e] = e < a.experts ? 1.f + (b - lo) * scale : -INFINITY;
   __syncthreads();
-  return {scale, 4.f + (fmaxf(fabsf(lo), fabsf(hi)) + 1.f) / range};
+  return {scale};
 }
 
 // The expert of choice `sub` of the lanes' token t, -1: none; near: this could not tell.  KMAX: choices at most.  REFINE:
@@ -673,7 +674,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     // 8; softmax, of its largest p: exponential 4, its argument's rounding 1, a sum of 16 + 5 additions of such terms and
     // its division, product: 33
     const float times = 1.f / total;
-    margin = 1 + (int)fminf(2.f * (pack.off + (a.sigmoid ? 4.f : 24.f * times)), 1e8f);
+    margin = 1 + (int)fminf(2.f * (Packing::off + (a.sigmoid ? 4.f : 17.f * times)), 1e8f);
     auto part = [&](int i, float p) {
       // -inf, of a bias, becomes 0: no key
       const uint32_t q = (uint32_t)fmaf(p, pack.scale, at[base + i]);
@@ -840,8 +841,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
 
 // The same again with 64 bits, from the row itself.  Not inlined: few tokens come here.
 template <int EPL, int LANES>
-__device__ __noinline__ int choose_again(const RouteArgs& a, const float* at, float scale, float off, int64_t t, bool mine,
-                                         int sub) {
+__device__ __noinline__ int choose_again(const RouteArgs& a, const float* at, float scale, int64_t t, bool mine, int sub) {
   float v[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -851,7 +851,7 @@ __device__ __noinline__ int choose_again(const RouteArgs& a, const float* at, fl
   float shift = 0.f, total = 1.f;
   if (!a.sigmoid) total = row_softmax<float, EPL>(v, LANES, shift);
   bool near;
-  int expert = choose_packed<EPL, CTR_MAX_CHOICES, LANES, true>(a, v, at, Packing{scale, off}, t, sub, shift, total, near);
+  int expert = choose_packed<EPL, CTR_MAX_CHOICES, LANES, true>(a, v, at, Packing{scale}, t, sub, shift, total, near);
   if (__any_sync(kFull, near)) {
     float b[EPL];
 #pragma unroll
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_balanced_kernel(const 
     bool near;
     int expert = choose_packed<EPL, KMAX, LANES, false>(a, v, at, pack, t0 + tl, sub, shift, total, near);
     if (__any_sync(kFull, near))
-      expert = choose_again<EPL, LANES>(a, at, pack.scale, pack.off, t0 + tl, mine && !bad, sub);
+      expert = choose_again<EPL, LANES>(a, at, pack.scale, t0 + tl, mine && !bad, sub);
     // weights: lane j has choice j
     const bool live = expert >= 0;
     const float s = live ? score_at(a, t0 + tl, expert) : -INFINITY;
