@@ -646,8 +646,8 @@ typedef enum {
  * Workspace: ctr_dense_workspace_size(rows, n, k, dtype, train, packed) bytes,
  * asked on the device of the call: train != 0 for ctr_dense_bwd (with room for
  * ctr_dense too), packed != 0 where rows of a bf16 matrix do not start at
- * multiples of 16 bytes.  A call that needs more than it is given is refused
- * (CTR_ERR_WORKSPACE). */
+ * multiples of 16 bytes.  Enough for any call of at most `rows` rows; a call that
+ * needs more than it is given is refused (CTR_ERR_WORKSPACE). */
 size_t ctr_dense_workspace_size(int64_t rows, int64_t n, int64_t k, ctr_dtype dtype, int train, int packed);
 int ctr_dense(const void* x, ctr_dtype dtype, int64_t rows, int64_t k, int64_t ldx, const void* w, int64_t n,
               int64_t ldw, const void* bias, int act, const void* residual, int64_t ld_residual, void* y, int64_t ld_y,

@@ -308,6 +308,9 @@ auto few_kernel(int64_t rows) {
 // ---------------------------------------------------------------------------
 int64_t up8(int64_t n) { return ceil_div(n, 8) * 8; }
 
+// The distance between rows: of a single row whatever suits the products.
+int64_t row_distance(int64_t rows, int64_t cols, int64_t ld) { return rows == 1 ? up8(cols) : ld; }
+
 // Whether the products can read a matrix as it lies.
 bool direct(const void* p, ctr_dtype dtype, int64_t rows, int64_t ld) {
   return dtype == CTR_BF16 && ((uintptr_t)p % 16) == 0 && ld % 8 == 0 && ld * 2 * imax64(rows, 1) < (1ll << 40);
@@ -317,13 +320,15 @@ size_t packed_elems(ctr_dtype dtype, int64_t rows, int64_t cols) {
   return (size_t)(dtype == CTR_F32 ? 3 : 1) * (size_t)rows * (size_t)up8(cols);
 }
 
-// Rows of a strip of dz_kernel: as many blocks as run at once on 152 SMs, at least 32 rows each.
-int strip_rows(int64_t rows, int64_t n, bool vec) {
-  const int64_t blocks = ceil_div(up8(n), kDzCols), most = 152 * (vec ? kDzBlocks<true> : kDzBlocks<false>);
-  return (int)imax64(32, ceil_div(rows, imax64(1, most / blocks)));
+// Rows of a strip of dz_kernel: as many blocks as run at once on 152 SMs, at least kMinStrip rows each.
+constexpr int kMinStrip = 32;
+int64_t most_strips(int64_t n, bool vec) {
+  return imax64(1, 152 * (vec ? kDzBlocks<true> : kDzBlocks<false>) / ceil_div(up8(n), kDzCols));
 }
+int strip_rows(int64_t rows, int64_t n, bool vec) { return (int)imax64(kMinStrip, ceil_div(rows, most_strips(n, vec))); }
 
-// What a call takes from the workspace; `carver` is a WsSizer or a WsCarver.
+// What a call takes from the workspace: no less than a call of fewer rows, so that one sized for the largest batch has room
+// for every smaller one.
 struct Room {
   __nv_bfloat16 *x = nullptr, *w = nullptr, *dz = nullptr;
   float *part = nullptr, *strips = nullptr;
@@ -346,12 +351,11 @@ struct Wants {
 template <typename Z>
 Room carve(Z& z, ctr_dtype dtype, int64_t rows, int64_t n, int64_t k, const Wants& want) {
   Room r;
-  const int planes = dtype == CTR_F32 ? 3 : 1;
   if (want.x) r.x = take<Z, __nv_bfloat16>(z, packed_elems(dtype, rows, k));
   if (want.w) r.w = take<Z, __nv_bfloat16>(z, packed_elems(dtype, n, k));
   if (want.dz) r.dz = take<Z, __nv_bfloat16>(z, packed_elems(dtype, rows, n));
-  if (want.dw) r.part = take<Z, float>(z, mm_plan(2, planes, n, k, rows).bytes() / 4);
-  if (want.strips) r.strips = take<Z, float>(z, (size_t)ceil_div(imax64(rows, 1), strip_rows(rows, n, true)) * n);  // the most strips
+  if (want.dw) r.part = take<Z, float>(z, mm_room(n, k, rows) / 4);
+  if (want.strips) r.strips = take<Z, float>(z, (size_t)imin64(ceil_div(imax64(rows, 1), kMinStrip), most_strips(n, true)) * n);
   return r;
 }
 
@@ -419,6 +423,8 @@ extern "C" int ctr_dense(const void* x, ctr_dtype dtype, int64_t rows, int64_t k
     if (off(p, eb)) return CTR_ERR_INVALID_ARG;
   if (!ws_valid(ws, ws_bytes, kWsHeader)) return CTR_ERR_WORKSPACE;
   if (rows == 0) return CTR_OK;
+  ldx = row_distance(rows, k, ldx);
+  ldw = row_distance(n, k, ldw);
   cudaStream_t s = (cudaStream_t)stream;
   if (few_rows(rows, direct(x, dtype, rows, ldx) && direct(w, dtype, n, ldw))) {
     FewArgs a = {x, w, bias, residual, y, pre, ldx, ldw, ld_residual, ld_y, ld_pre, (int32_t)rows, (int32_t)n, (int32_t)k, act};
@@ -482,6 +488,10 @@ extern "C" int ctr_dense_bwd(const void* dy, ctr_dtype dtype, int64_t rows, int6
     }
     return ok ? launch_status() : CTR_ERR_CUDA;
   }
+  ld_dy = row_distance(rows, n, ld_dy);
+  ld_pre = row_distance(rows, n, ld_pre);
+  ldx = row_distance(rows, k, ldx);
+  ldw = row_distance(n, k, ldw);
   // without an activation dz is dy, which the products may be able to read as it lies
   const bool make_dz = (dx || dw) && (act != CTR_ACT_NONE || !direct(dy, dtype, rows, ld_dy));
   const Wants want = {dw && !direct(x, dtype, rows, ldx), dx && !direct(w, dtype, n, ldw), make_dz, dw != nullptr,

@@ -52,6 +52,7 @@ constexpr uint32_t kChunkBytes = 64 * 128;        // MN-major: 64 of i or j time
 constexpr uint32_t kPiece = 32 * 128;             // a warp's piece of the result on its way: 32 rows of 128 bytes
 constexpr int kSuper = 8;                         // row tiles that take the column tiles together
 constexpr int kMinShare = 8;                      // blocks of a part of a sum, at least
+constexpr int kPairBlocks = 64;                   // blocks of a sum that pairs cut up whatever the number of tiles
 constexpr int kMainBlocks = 2, kCrossBlocks = 64; // blocks between two readings (planes): 8 and 1280 instructions
 constexpr int kFlushBlocks = 8;                   // without planes: 32 instructions
 // Registers of a FLUSH kernel: 384 threads are launched with 168 each; the first four warps give some up so that an
@@ -914,6 +915,15 @@ int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) 
   return plan.columns == 256 ? launch_dm<256, MAJOR>(c, plan, part, s) : launch_dm<128, MAJOR>(c, plan, part, s);
 }
 
+// CTA pairs, or CTAs, that run at once.
+int64_t mm_workers(bool pair) { return imax64(1, num_sms() / (pair ? 2 : 1)); }
+
+// Parts of a sum of kb blocks, at most: no fewer than kMinShare blocks each, and no more parts of all tiles than four
+// rounds of the workers take.
+int64_t most_parts(int64_t kb, int64_t tiles, int64_t workers) {
+  return imax64(1, imin64(kb / kMinShare, 3 * workers / tiles + 1));
+}
+
 }  // namespace
 
 MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
@@ -921,9 +931,9 @@ MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
   const int64_t kb = ceil_div(r, kBlock);
   const int64_t pairs = ceil_div(m, 256) * ceil_div(n, 256);
   const int64_t sms = num_sms();
-  const bool pair = m > 128 && n > 128 && (pairs >= sms / 3 || (major == 2 && kb >= 64));
+  const bool pair = m > 128 && n > 128 && (pairs >= sms / 3 || (major == 2 && kb >= kPairBlocks));
   if (pair) w.columns = 256;
-  const int64_t side = w.side(), most = sms / (pair ? 2 : 1);
+  const int64_t side = w.side(), most = mm_workers(pair);
   const int64_t tiles = ceil_div(m, side) * ceil_div(n, side);
   // few rows: more and narrower tiles, so that more SMs read the weights
   if (!pair && major == 0 && 2 * tiles <= sms && n > 32) w.columns = 32;
@@ -931,7 +941,7 @@ MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
   // Sums over a batch are cut into the number of parts that takes least, in blocks' times (0.27 us with planes of bf16
   // alone): the rounds of all workers, six blocks for each tile's setting up and end, and each part's writing and reading.
   double best = 0;
-  for (int64_t parts = 1; parts <= imax64(1, kb / kMinShare) && (parts - 1) * tiles <= 3 * most; ++parts) {
+  for (int64_t parts = 1; parts <= most_parts(kb, tiles, most); ++parts) {
     const double rounds = (double)ceil_div(tiles * parts, most);
     const double time = rounds * (planes * (planes == 3 ? 2 : 1) * (double)ceil_div(kb, parts) + 6) +
                         (parts > 1 ? (double)(tiles * parts) * (pair ? 0.28 : 0.14) + 8 : 0);
@@ -941,8 +951,20 @@ MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
       w.parts = parts > 1 ? ceil_div(kb, w.share) : 1;
     }
   }
-  w.places = w.share ? tiles * w.parts : 0;
   return w;
+}
+
+size_t mm_room(int64_t m, int64_t n, int64_t r) {
+  const int64_t kb = ceil_div(r, kBlock);
+  int64_t most = 0;
+  for (const bool pair : {false, true}) {
+    // which of them a call takes depends on r
+    if (pair && (m <= 128 || n <= 128)) continue;
+    const int64_t side = pair ? 256 : 128, tiles = ceil_div(m, side) * ceil_div(n, side);
+    const int64_t parts = most_parts(kb, tiles, mm_workers(pair));
+    if (parts > 1) most = imax64(most, tiles * parts * side * side * 4);
+  }
+  return (size_t)most;
 }
 
 int mm_run(const MmCall& c, float* part, cudaStream_t s) {

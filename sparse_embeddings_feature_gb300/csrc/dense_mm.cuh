@@ -31,18 +31,20 @@ struct MmCall {
   int* err = nullptr;
 };
 
-// How a product is taken apart: CTA pairs on 256 x 256 tiles, or CTAs on 128 x 128 or 128 x 32; where share is not 0, sums in `parts`
-// of `share` blocks of 64, which leave as fp32 (whole tiles, in `places` of the workspace) and are added up by a second
+// How a product is taken apart: CTA pairs on 256 x 256 tiles, or CTAs on 128 x 128 or 128 x 32; where share is not 0, sums
+// in `parts` of `share` blocks of 64, which leave as fp32 (whole tiles, in the workspace) and are added up by a second
 // kernel.
 struct MmPlan {
   int columns = 128;  // of a tile
-  int64_t share = 0, parts = 1, places = 0;
+  int64_t share = 0, parts = 1;
   int side() const { return columns == 256 ? 256 : 128; }  // its rows
-  size_t bytes() const { return (size_t)places * side() * side() * 4; }
 };
 MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r);
 
-// Runs the product; `part` has mm_plan(..).bytes() bytes, 256-byte aligned.  A ctr_status.
+// Bytes of the parts' places of a sum (major 2), enough for any r up to this one.
+size_t mm_room(int64_t m, int64_t n, int64_t r);
+
+// Runs the product; `part` has mm_room(..) bytes, 256-byte aligned.  A ctr_status.
 int mm_run(const MmCall& c, float* part, cudaStream_t s);
 
 // Activations (ctr_activation) and their derivatives, by the hardware's exponential and reciprocal (within 2 and 1 ulp)

@@ -75,6 +75,18 @@ def test_dense_refusals(lib):
     assert size(40, 24, 16, 1, 1, 0) < size(40, 24, 16, 0, 1, 0)
 
 
+def test_dense_workspace_sizes_without_a_device(lib):
+    size = lib.ctr_dense_workspace_size
+    for n, k in ((1, 3), (128, 128), (264, 512), (1024, 1024), (4096, 300)):
+        for dt in (0, 1):
+            last = 0
+            for rows in (0, 1, 9, 63, 511, 512, 1000, 4095, 4096, 29185, 65536, 100000):   # more rows never take less
+                now = size(rows, n, k, dt, 1, 0)
+                assert now >= max(last, 256)
+                last = now
+            assert last >= 100000 * n * (2 if dt else 6)   # dz
+
+
 def test_balanced_routing_refusals(lib):
     def call(scores=P, dt=0, tokens=10, experts=8, ld=8, k=2, score=1, bias=P, groups=4, kept=2, factor=1.0, expert=P,
              offsets=P, size=1 << 30):
