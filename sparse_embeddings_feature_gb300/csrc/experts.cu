@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 // (Batcher's odd-even merge sort), a round a choice takes the largest of the lanes' first ones.  Where two that have to be
 // told apart are nearer than the bound on what packed keys may be off by (one token in 500; equal scores with equal
 // biases are ties and told apart by their indexes), the warp does its tokens again, with the keys that matter in 64 bits: a
-// group's two best, and as many choices as there are lanes.  Where that is not enough, all keys in 64 bits: a warp's
-// 64-bit instruction takes 64 cycles, so that a token with 16 exponentials a lane takes 30 us.
+// group's two best, and as many choices as there are lanes.  Where that is not enough, all keys in 64 bits, of which
+// a warp's instruction takes 64 cycles (all tokens of 65536 x 256 so: 3.1 ms).
 // 65536 x 256, k 8, 4 of 8 groups, all tokens in fp32 with a round a choice for the key and one for its index: 196 us.
 // e^x in 64 bits for |x| <= 700 (beyond, e^-700 and e^700): 2^(j / 64) from a table, the rest, below ln 2 / 128, by five
 // terms of the series: a third of the 64-bit instructions of exp, which a warp is bound by.
@@ -612,14 +612,25 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
 // Packed keys: the keys' range from the smallest bias on is cut into 2^23 - 4 parts of 1 / scale, numbered from 1.
 // What a key may be off by besides p's own error, in parts (2^-24 of a range is half a part): three roundings of the
 // bias's part number and one of the sum, half a part each, and one part for cutting off.
+// Experts whose bias is more than kSpread below the largest one (pushed out by -1e9, say) would make the parts as coarse as
+// that is.  They have their keys in a range of their own below the others', where a part says only that its key is below
+// theirs (65536 x 256, 4 of 8 groups, a tenth of the biases -1e9: 114 us; in parts of that range, which tell nothing apart,
+// 3083; a wider spread has coarser parts: 62, 220 us).  Of a few biases far above the rest it is the rest that is pushed out.
 struct Packing {
   float scale;
   static constexpr float off = 3.f;
 };
+struct PackedBias {            // shared
+  float at[CTR_MAX_EXPERTS];   // each expert's part number at p = 0; -inf: never chosen
+  int border;                  // keys of smaller parts are of experts pushed out
+};
+constexpr float kSpread = 6.f;
+constexpr float kGap = 1.0625f;      // the smallest bias of the upper range less that of the lower: p is at most 1
+constexpr float kLarge = 1073741824.f;  // 2^30: past it a 64-bit key's last bit is more than a part
 static_assert(CTR_MAX_EXPERTS <= 512, "an index has 9 bits");
 
-// Each expert's part number at p = 0 into `at` (shared; -inf: never chosen), by all threads of the block.
-__device__ __forceinline__ Packing pack_range(const RouteArgs& a, float* at, float* ends) {
+// `to` filled by all threads of the block.
+__device__ __forceinline__ Packing pack_range(const RouteArgs& a, PackedBias& to, float* ends) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = threadIdx.x;
   float b = a.bias && e < a.experts ? a.bias[e] : 0.f;
   if (!(b < INFINITY)) {  // NaN, +inf: as -inf, and flagged
@@ -643,8 +654,13 @@ __device__ __forceinline__ Packing pack_range(const RouteArgs& a, float* at, flo
     hi = fmaxf(hi, ends[2 * w + 1]);
   }
   if (!(lo <= hi)) lo = hi = 0.f;
-  const float range = 1.f + (hi - lo), scale = 8388604.f / range;
-  if (e < CTR_MAX_EXPERTS) at[e] = e < a.experts ? 1.f + (b - lo) * scale : -INFINITY;
+  const bool out = hi - lo > kSpread;
+  if (out) lo = hi - kSpread;
+  const float range = 1.f + (hi - lo) + (out ? kGap : 0.f), scale = 8388604.f / range;
+  const float shift = 1.f + (out ? floorf(kGap * scale) : 0.f);  // a whole number
+  if (e < CTR_MAX_EXPERTS) to.at[e] = !some ? -INFINITY : b < lo ? 1.f : shift + (b - lo) * scale;
+  // between the two ranges are 1/16 of a key's, thousands of parts; of biases past kLarge all keys are near
+  if (e == 0) to.border = fabsf(hi) >= kLarge ? 1 << 23 : out ? (int)shift - 2048 : 0;
   __syncthreads();
   return {scale};
 }
@@ -652,7 +668,7 @@ __device__ __forceinline__ Packing pack_range(const RouteArgs& a, float* at, flo
 // The expert of choice `sub` of the lanes' token t, -1: none; near: this could not tell.  KMAX: choices at most.  REFINE:
 // the keys that matter are computed in 64 bits.
 template <int EPL, int KMAX, int LANES, bool REFINE>
-__device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v)[EPL], const float* at, const Packing& pack,
+__device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v)[EPL], const PackedBias& bias, const Packing& pack,
                                              int64_t t, int sub, float shift, float total, bool& near) {
   constexpr float kLog2e = 1.44269504f;
   const int base = sub * EPL, per = a.experts / a.groups;
@@ -677,7 +693,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     margin = 1 + (int)fminf(2.f * (Packing::off + (a.sigmoid ? 4.f : 17.f * times)), 1e8f);
     auto part = [&](int i, float p) {
       // -inf, of a bias, becomes 0: no key
-      const uint32_t q = (uint32_t)fmaf(p, pack.scale, at[base + i]);
+      const uint32_t q = (uint32_t)fmaf(p, pack.scale, bias.at[base + i]);
       key[i] = v[i] > -INFINITY && q > 0 ? q * 512u + (uint32_t)(511 - base - i) : 0u;
     };
     if (a.sigmoid) {
@@ -738,7 +754,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     const uint32_t all = LANES == 32 ? kFull : (1u << (LANES & 31)) - 1;
     const uint32_t ones = __ballot_sync(kFull, some && k1 == 0) >> first & all;
     const uint32_t twos = __ballot_sync(kFull, some && k1 != 0) >> first & all;
-    bool close = ones != 0 && twos != 0;
+    bool close = (ones != 0 && twos != 0) || (some && (int)((k1 ? k1 : k0) >> 9) < bias.border);
     if (__any_sync(kFull, some && gap <= 2 * margin)) {
       for (int g = 0; g < a.groups; ++g) {
         const int other = __shfl_sync(kFull, worth, g, LANES), there = __shfl_sync(kFull, place, g, LANES);
@@ -751,7 +767,9 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     if constexpr (REFINE) {
       if (__any_sync(kFull, close)) {
         // the two best are the two best unless the third may be the second
-        if (some && k2 != 0 && (int)((k1 >> 9) - (k2 >> 9)) <= margin && !same_inputs(a, t, k1, k2)) near = true;
+        if (some && k2 != 0 && ((int)((k1 >> 9) - (k2 >> 9)) <= margin || (int)(k1 >> 9) < bias.border) &&
+            !same_inputs(a, t, k1, k2))
+          near = true;
         const int64_t value = some ? in_order(exact(k0) + (k1 ? exact(k1) : 0.0)) : INT64_MIN;
         place = 0;
         for (int g = 0; g < a.groups; ++g) {
@@ -792,6 +810,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
   sort_falling(key);
   // scores of one upper part differ in what was cut off, but for bf16 ones, which have nothing there
   const int apart = !plain ? margin : a.f32 ? 0 : -1;
+  const int border = plain ? 0 : bias.border;
   uint32_t mine = 0;  // lane j gets the j-th largest key
   if constexpr (REFINE) {
     for (int j = 0; j < LANES; ++j) {
@@ -804,7 +823,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     }
     // the choices are among them unless one that is left may be the last of them
     const uint32_t left = lanes_max<LANES>(key[0]), last = __shfl_sync(kFull, mine, a.k - 1, LANES);
-    near |= left != 0 && (int)((last >> 9) - (left >> 9)) <= apart;
+    near |= left != 0 && ((int)((last >> 9) - (left >> 9)) <= apart || (int)(last >> 9) < border);
     int64_t value = INT64_MIN;
     if (mine != 0) value = in_order(plain ? (double)score_at(a, t, 511 - (int)(mine & 511u)) : exact(mine));
     int rank = 0;
@@ -834,14 +853,16 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       if (EPL - 1 < KMAX - j && pop) key[EPL - 1] = 0;
     }
     const uint32_t below = __shfl_down_sync(kFull, mine, 1, LANES), next = sub + 1 == a.k ? after : below;
-    if (sub < a.k && next != 0 && (int)((mine >> 9) - (next >> 9)) <= apart) near |= !same_inputs(a, t, mine, next);
+    if (sub < a.k && next != 0 && ((int)((mine >> 9) - (next >> 9)) <= apart || (int)(mine >> 9) < border))
+      near |= !same_inputs(a, t, mine, next);
     return sub < a.k && mine != 0 ? 511 - (int)(mine & 511u) : -1;
   }
 }
 
 // The same again with 64 bits, from the row itself.  Not inlined: few tokens come here.
 template <int EPL, int LANES>
-__device__ __noinline__ int choose_again(const RouteArgs& a, const float* at, float scale, int64_t t, bool mine, int sub) {
+__device__ __noinline__ int choose_again(const RouteArgs& a, const PackedBias& bias, float scale, int64_t t, bool mine,
+                                         int sub) {
   float v[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -851,7 +872,7 @@ __device__ __noinline__ int choose_again(const RouteArgs& a, const float* at, fl
   float shift = 0.f, total = 1.f;
   if (!a.sigmoid) total = row_softmax<float, EPL>(v, LANES, shift);
   bool near;
-  int expert = choose_packed<EPL, CTR_MAX_CHOICES, LANES, true>(a, v, at, Packing{scale}, t, sub, shift, total, near);
+  int expert = choose_packed<EPL, CTR_MAX_CHOICES, LANES, true>(a, v, bias, Packing{scale}, t, sub, shift, total, near);
   if (__any_sync(kFull, near)) {
     float b[EPL];
 #pragma unroll
@@ -868,13 +889,14 @@ __device__ __noinline__ int choose_again(const RouteArgs& a, const float* at, fl
 template <int EPL, int KMAX, int LANES>
 __global__ void __launch_bounds__(kRouteThreads, 2) route_balanced_kernel(const __grid_constant__ RouteArgs a) {
   extern __shared__ uint32_t bits[];  // as in route_choose_kernel
-  __shared__ float at[CTR_MAX_EXPERTS], ends[kRouteThreads / 16];
+  __shared__ PackedBias bias;
+  __shared__ float ends[kRouteThreads / 16];
   const int words = a.tile / 32;
   const int64_t t0 = (int64_t)blockIdx.x * a.tile;
   const int n = (int)imin64(a.tile, a.tokens - t0);
   for (int i = threadIdx.x; i < a.experts * words; i += kRouteThreads) bits[i] = 0;
   grid_wait();
-  const Packing pack = pack_range(a, at, ends);
+  const Packing pack = pack_range(a, bias, ends);
   const int lane = threadIdx.x & 31, sub = lane & (LANES - 1);
   const uint32_t group = (LANES == 32 ? kFull : (1u << (LANES & 31)) - 1) << (lane & ~(LANES - 1));
   constexpr int per_pass = kRouteThreads / LANES;
@@ -900,9 +922,9 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_balanced_kernel(const 
     float shift = 0.f, total = 1.f;
     if (!a.sigmoid) total = row_softmax<float, EPL>(v, LANES, shift);
     bool near;
-    int expert = choose_packed<EPL, KMAX, LANES, false>(a, v, at, pack, t0 + tl, sub, shift, total, near);
+    int expert = choose_packed<EPL, KMAX, LANES, false>(a, v, bias, pack, t0 + tl, sub, shift, total, near);
     if (__any_sync(kFull, near))
-      expert = choose_again<EPL, LANES>(a, at, pack.scale, t0 + tl, mine && !bad, sub);
+      expert = choose_again<EPL, LANES>(a, bias, pack.scale, t0 + tl, mine && !bad, sub);
     // weights: lane j has choice j
     const bool live = expert >= 0;
     const float s = live ? score_at(a, t0 + tl, expert) : -INFINITY;

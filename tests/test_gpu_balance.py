@@ -134,6 +134,32 @@ def test_masked_by_bias_and_bad_biases():
     check(s, 4, "sigmoid", _bias(32, 6), 8, 3, True, "f32", status=ctr.ERR_BAD_VALUE)
 
 
+@pytest.mark.parametrize("low", [-50.0, -62.5, -64.0, -1e4, -1e9, float(torch.finfo(torch.float32).min)])
+def test_experts_pushed_out_by_finite_biases(low):
+    rng = np.random.default_rng(3)
+    for E, groups, group_k, k, part in ((32, 1, 1, 4, 0.3), (32, 8, 3, 4, 0.3), (64, 8, 4, 6, 0.9), (16, 4, 4, 16, 0.5),
+                                        (256, 8, 4, 8, 0.1), (256, 16, 3, 16, 0.7)):
+        s = _scores(400, E, "f32", 0.1, E)
+        bias = _bias(E, E + 1)
+        out = rng.random(E) < part
+        for far in (np.full(E, low), low * (1 - 0.1 * rng.random(E)), low + 0.3 * rng.normal(size=E)):
+            b = np.where(out, np.maximum(far, np.finfo(np.float32).min), bias).astype(np.float32)
+            for score, renorm in (("softmax", False), ("sigmoid", True)):
+                check(s, k, score, b, groups, group_k, renorm, "f32")
+
+
+@pytest.mark.parametrize("big", [1e6, 1e9, 3e10, 3.3e38])
+def test_biases_that_swallow_the_scores(big):
+    # keys in 64 bits lose the score's last bits, or all of them: ties then
+    s = _scores(300, 32, "f32", 0.1, 5)
+    bias = _bias(32, 6)
+    for lift in (np.full(32, True), np.arange(32) % 3 == 0, np.arange(32) == 17):
+        b = np.where(lift, np.float32(big) + bias, np.where(np.arange(32) % 2, -np.float32(big), bias)).astype(np.float32)
+        for groups, group_k in ((1, 1), (8, 3)):
+            for score, renorm in (("softmax", True), ("sigmoid", False)):
+                check(s, 4, score, b, groups, group_k, renorm, "f32")
+
+
 def test_sigmoids_that_fp32_cannot_hold():
     # all of a token's scores far below zero: renormalised weights are still in proportion
     s = _scores(64, 20, "f32", 0, 7, 2.0) - 150
