@@ -429,8 +429,9 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 // (Batcher's odd-even merge sort), a round a choice takes the largest of the lanes' first ones.  Where two that have to be
 // told apart are nearer than the bound on what packed keys may be off by (one token in 500; equal scores with equal
 // biases are ties and told apart by their indexes), the warp does its tokens again, with the keys that matter in 64 bits: a
-// group's two best, and as many choices as there are lanes.  Where that is not enough, all keys in 64 bits, of which
-// a warp's instruction takes 64 cycles (all tokens of 65536 x 256 so: 3.1 ms).
+// group's two best, and as many choices as there are lanes.  Where that is not enough (another key that may be larger than
+// those and is not their equal), all keys in 64 bits, of which a warp's instruction takes 64 cycles (all tokens of 65536 x
+// 256 so: 3.1 ms).
 // 65536 x 256, k 8, 4 of 8 groups, all tokens in fp32 with a round a choice for the key and one for its index: 196 us.
 // e^x in 64 bits for |x| <= 700 (beyond, e^-700 and e^700): 2^(j / 64) from a table, the rest, below ln 2 / 128, by five
 // terms of the series: a third of the 64-bit instructions of exp, which a warp is bound by.
@@ -579,7 +580,7 @@ __device__ __forceinline__ int64_t in_order(double x) {
 }
 
 // Whether two packed keys are of equal scores with equal biases.
-__device__ __forceinline__ bool same_inputs(const RouteArgs& a, int64_t t, uint32_t x, uint32_t y) {
+__device__ __noinline__ bool same_inputs(const RouteArgs& a, int64_t t, uint32_t x, uint32_t y) {
   const int e = 511 - (int)(x & 511u), f = 511 - (int)(y & 511u);
   return score_at(a, t, e) == score_at(a, t, f) && (!a.bias || a.bias[e] == a.bias[f]);
 }
@@ -614,8 +615,8 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
 // bias's part number and one of the sum, half a part each, and one part for cutting off.
 // Experts whose bias is more than kSpread below the largest one (pushed out by -1e9, say) would make the parts as coarse as
 // that is.  They have their keys in a range of their own below the others', where a part says only that its key is below
-// theirs (65536 x 256, 4 of 8 groups, a tenth of the biases -1e9: 114 us; in parts of that range, which tell nothing apart,
-// 3083; a wider spread has coarser parts: 62, 220 us).  Of a few biases far above the rest it is the rest that is pushed out.
+// theirs (65536 x 256, 4 of 8 groups, a tenth of the biases -1e9: 105 us; in parts of that range, which tell nothing apart,
+// 3083; a wider spread has coarser parts: 62, 137 us).  Of a few biases far above the rest it is the rest that is pushed out.
 struct Packing {
   float scale;
   static constexpr float off = 3.f;
@@ -676,7 +677,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
   const int lane = threadIdx.x & 31, first = lane & ~(LANES - 1);
   near = false;
   uint32_t key[EPL];
-  int margin = 0;
+  int apart;  // keys whose parts are no further apart have to be told apart
   uint32_t kept = kFull;
   double sum = 1;  // of a softmax, in 64 bits
   if (REFINE && !a.sigmoid && (!plain || grouped)) sum = row_softmax<double, EPL>(v, LANES, shift);
@@ -685,12 +686,21 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     const double l = score_at(a, t, e), b = a.bias ? a.bias[e] : 0.f;
     return (a.sigmoid ? 1 / (1 + exp_64(-l)) : exp_of<double>(l - shift) / sum) + b;
   };
-  if (!plain || grouped) {
+  if (plain) {
+    // scores of one upper part differ in what was cut off, but for bf16 ones, which have nothing there
+    apart = a.f32 ? 0 : -1;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      uint32_t u = __float_as_uint(v[i] + 0.f);  // -0 becomes +0
+      u ^= (uint32_t)((int32_t)u >> 31) | 0x80000000u;
+      key[i] = v[i] > -INFINITY ? (u & 0xfffffe00u) | (uint32_t)(511 - base - i) : 0u;
+    }
+  } else {
     // p's error in parts (two of 2^-24), sigmoid: exponential 4 of 2^-24 and its argument's rounding, sum, reciprocal 4:
     // 8; softmax, of its largest p: exponential 4, its argument's rounding 1, a sum of 16 + 5 additions of such terms and
     // its division, product: 33
     const float times = 1.f / total;
-    margin = 1 + (int)fminf(2.f * (Packing::off + (a.sigmoid ? 4.f : 17.f * times)), 1e8f);
+    apart = 1 + (int)fminf(2.f * (Packing::off + (a.sigmoid ? 4.f : 17.f * times)), 1e8f);
     auto part = [&](int i, float p) {
       // -inf, of a bias, becomes 0: no key
       const uint32_t q = (uint32_t)fmaf(p, pack.scale, bias.at[base + i]);
@@ -704,6 +714,11 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       for (int i = 0; i < EPL; ++i) part(i, exp2_fast((v[i] - shift) * kLog2e) * times);
     }
   }
+  const int border = plain ? 0 : bias.border;
+  auto nearby = [&](uint32_t x, uint32_t y) {  // whether y, the smaller packed key, may be the larger one
+    return y != 0 && ((int)((x >> 9) - (y >> 9)) <= apart || (int)(x >> 9) < border);
+  };
+  auto unclear = [&](uint32_t x, uint32_t y) { return nearby(x, y) && !same_inputs(a, t, x, y); };
   if (grouped) {
     uint32_t k0 = 0, k1 = 0, k2 = 0;  // lane g learns group g's two (REFINE: three) best keys
     auto take = [](uint32_t& x0, uint32_t& x1, uint32_t& x2, uint32_t x) {
@@ -742,34 +757,77 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       }
     }
     const bool some = sub < a.groups && k0 != 0;
-    const int worth = some ? (int)((k0 >> 9) + (k1 >> 9)) : -0x40000000;
-    int place = 0, gap = 0x7fffffff;
-    for (int g = 0; g < a.groups; ++g) {
-      const int other = __shfl_sync(kFull, worth, g, LANES);
-      place += other > worth || (other == worth && g < sub);
-      if (g != sub) gap = min(gap, abs(worth - other));
-    }
-    // near: on either side of the border, and not of the same keys.  A sum of one key is not to be compared with one of two
-    // in parts.
-    const uint32_t all = LANES == 32 ? kFull : (1u << (LANES & 31)) - 1;
-    const uint32_t ones = __ballot_sync(kFull, some && k1 == 0) >> first & all;
-    const uint32_t twos = __ballot_sync(kFull, some && k1 != 0) >> first & all;
-    bool close = (ones != 0 && twos != 0) || (some && (int)((k1 ? k1 : k0) >> 9) < bias.border);
-    if (__any_sync(kFull, some && gap <= 2 * margin)) {
+    int place = 0;
+    bool close = false;
+    // near: on either side of the border; equal pairs are ties where packed keys are exact, so that the pairs are the best
+    if (!plain) {
+      const int worth = some ? (int)((k0 >> 9) + (k1 >> 9)) : -0x40000000;
+      int gap = 0x7fffffff;
       for (int g = 0; g < a.groups; ++g) {
-        const int other = __shfl_sync(kFull, worth, g, LANES), there = __shfl_sync(kFull, place, g, LANES);
-        const uint32_t y0 = __shfl_sync(kFull, k0, g, LANES), y1 = __shfl_sync(kFull, k1, g, LANES);
-        if (some && y0 != 0 && (place < a.group_k) != (there < a.group_k) && abs(worth - other) <= 2 * margin &&
-            !(same_inputs(a, t, k0, y0) && (k1 == 0 || y1 == 0 ? k1 == y1 : same_inputs(a, t, k1, y1))))
-          close = true;
+        const int other = __shfl_sync(kFull, worth, g, LANES);
+        place += other > worth || (other == worth && g < sub);
+        if (g != sub) gap = min(gap, abs(worth - other));
+      }
+      // a sum of one key is not to be compared with one of two in parts, nor one with a key of the lower range
+      const uint32_t all = LANES == 32 ? kFull : (1u << (LANES & 31)) - 1;
+      const uint32_t ones = __ballot_sync(kFull, some && k1 == 0) >> first & all;
+      const uint32_t twos = __ballot_sync(kFull, some && k1 != 0) >> first & all;
+      close = (ones != 0 && twos != 0) || (some && (int)((k1 ? k1 : k0) >> 9) < border);
+      if (__any_sync(kFull, some && gap <= 2 * apart)) {
+        for (int g = 0; g < a.groups; ++g) {
+          const int other = __shfl_sync(kFull, worth, g, LANES), there = __shfl_sync(kFull, place, g, LANES);
+          close |= some && (place < a.group_k) != (there < a.group_k) && abs(worth - other) <= 2 * apart;
+        }
+      }
+    } else {
+      // What a group is worth, from the scores, as a number whose error is relative, so that the small sums of peaked scores
+      // are told apart too: a softmax's p0 + p1; of sigmoids, which crowd at 1 as well as at 0, the ratio to what is missing
+      // from 2.  Relative errors, twice for the other side's: an exponential's 8 of 2^-24 and twice its argument's x, four
+      // of those in a ratio; what was cut off, up to 2^-14 of a score, twice in a ratio.
+      float worth = -INFINITY, rel = 0.f;
+      if (some) {
+        const float l0 = score_at(a, t, 511 - (int)(k0 & 511u)), l1 = k1 ? score_at(a, t, 511 - (int)(k1 & 511u)) : -INFINITY;
+        const float largest = fmaxf(fabsf(l0), k1 ? fabsf(l1) : 0.f);
+        if (a.sigmoid) {
+          const float p = __fdividef(1.f, 1.f + exp2_fast(-l0 * kLog2e)) + __fdividef(1.f, 1.f + exp2_fast(-l1 * kLog2e));
+          const float q = __fdividef(1.f, 1.f + exp2_fast(l0 * kLog2e)) + __fdividef(1.f, 1.f + exp2_fast(l1 * kLog2e));
+          worth = p / q;
+        } else {
+          worth = exp2_fast((l0 - shift) * kLog2e) + exp2_fast((l1 - shift) * kLog2e);
+        }
+        rel = 0x1p-24f * (128.f + 16.f * (a.sigmoid ? largest : fabsf(shift) + largest)) + (a.f32 ? 0x1p-12f * largest : 0.f);
+        // nearer to 2 than 64 bits' sums can be compared with this error, or past fp32
+        if (a.sigmoid && !(worth < 0x1p30f)) rel = 2.f;
+      }
+      auto apart_from = [&](float other) { return fabsf(worth - other) > rel * fmaxf(worth, other); };  // NaN: no
+      bool tight = false;
+      for (int g = 0; g < a.groups; ++g) {
+        const float other = __shfl_sync(kFull, worth, g, LANES);
+        place += other > worth || (other == worth && g < sub);
+        if (g != sub) tight |= !apart_from(other);
+      }
+      if (__any_sync(kFull, some && tight)) {
+        for (int g = 0; g < a.groups; ++g) {
+          const float other = __shfl_sync(kFull, worth, g, LANES);
+          const int there = __shfl_sync(kFull, place, g, LANES);
+          const uint32_t y0 = __shfl_sync(kFull, k0, g, LANES), y1 = __shfl_sync(kFull, k1, g, LANES);
+          close |= some && y0 != 0 && (place < a.group_k) != (there < a.group_k) && !apart_from(other) &&
+                   !(apart < 0 && k0 >> 9 == y0 >> 9 && k1 >> 9 == y1 >> 9);
+        }
       }
     }
     if constexpr (REFINE) {
       if (__any_sync(kFull, close)) {
-        // the two best are the two best unless the third may be the second
-        if (some && k2 != 0 && ((int)((k1 >> 9) - (k2 >> 9)) <= margin || (int)(k1 >> 9) < bias.border) &&
-            !same_inputs(a, t, k1, k2))
-          near = true;
+        // the two best are the two best unless another one may be larger than either
+        if (__any_sync(kFull, some && nearby(k1, k2))) {
+          for (int g = 0; g < a.groups; ++g) {
+            const uint32_t y0 = __shfl_sync(kFull, k0, g, LANES), y1 = __shfl_sync(kFull, k1, g, LANES);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (base + i >= g * per && base + i < (g + 1) * per && key[i] != y0 && key[i] != y1)
+                near |= unclear(y0, key[i]) || unclear(y1, key[i]);
+          }
+        }
         const int64_t value = some ? in_order(exact(k0) + (k1 ? exact(k1) : 0.0)) : INT64_MIN;
         place = 0;
         for (int g = 0; g < a.groups; ++g) {
@@ -781,14 +839,6 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       near = close;
     }
     kept = __ballot_sync(kFull, some && place < a.group_k) >> first;
-  }
-  if (plain) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      uint32_t u = __float_as_uint(v[i] + 0.f);  // -0 becomes +0
-      u ^= (uint32_t)((int32_t)u >> 31) | 0x80000000u;
-      key[i] = v[i] > -INFINITY ? (u & 0xfffffe00u) | (uint32_t)(511 - base - i) : 0u;
-    }
   }
   if (grouped) {
     if (a.seg) {
@@ -808,9 +858,6 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     }
   }
   sort_falling(key);
-  // scores of one upper part differ in what was cut off, but for bf16 ones, which have nothing there
-  const int apart = !plain ? margin : a.f32 ? 0 : -1;
-  const int border = plain ? 0 : bias.border;
   uint32_t mine = 0;  // lane j gets the j-th largest key
   if constexpr (REFINE) {
     for (int j = 0; j < LANES; ++j) {
@@ -821,9 +868,6 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       for (int i = 0; i < EPL - 1; ++i) key[i] = pop ? key[i + 1] : key[i];
       if (pop) key[EPL - 1] = 0;
     }
-    // the choices are among them unless one that is left may be the last of them
-    const uint32_t left = lanes_max<LANES>(key[0]), last = __shfl_sync(kFull, mine, a.k - 1, LANES);
-    near |= left != 0 && ((int)((last >> 9) - (left >> 9)) <= apart || (int)(last >> 9) < border);
     int64_t value = INT64_MIN;
     if (mine != 0) value = in_order(plain ? (double)score_at(a, t, 511 - (int)(mine & 511u)) : exact(mine));
     int rank = 0;
@@ -837,6 +881,12 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       const int r = __shfl_sync(kFull, mine != 0 ? rank : -1, j, LANES);
       const uint32_t there = __shfl_sync(kFull, mine, j, LANES);
       if (r == sub) chosen = there;
+    }
+    // unless one that is left may be larger than the last of them
+    const uint32_t last = __shfl_sync(kFull, chosen, a.k - 1, LANES);
+    if (nearby(last, lanes_max<LANES>(key[0]))) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) near |= unclear(last, key[i]);
     }
     return sub < a.k && chosen != 0 ? 511 - (int)(chosen & 511u) : -1;
   } else {
@@ -853,8 +903,8 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       if (EPL - 1 < KMAX - j && pop) key[EPL - 1] = 0;
     }
     const uint32_t below = __shfl_down_sync(kFull, mine, 1, LANES), next = sub + 1 == a.k ? after : below;
-    if (sub < a.k && next != 0 && ((int)((mine >> 9) - (next >> 9)) <= apart || (int)(mine >> 9) < border))
-      near |= !same_inputs(a, t, mine, next);
+    // equal ones are ties, but for the last choice and the best one left: what is left behind it may be larger than either
+    if (sub < a.k) near |= sub + 1 == a.k ? nearby(mine, next) : unclear(mine, next);
     return sub < a.k && mine != 0 ? 511 - (int)(mine & 511u) : -1;
   }
 }

@@ -134,6 +134,33 @@ def test_masked_by_bias_and_bad_biases():
     check(s, 4, "sigmoid", _bias(32, 6), 8, 3, True, "f32", status=ctr.ERR_BAD_VALUE)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("E,groups,group_k,k", [(32, 1, 1, 1), (32, 8, 3, 4), (64, 4, 2, 6), (256, 8, 4, 8), (256, 16, 3, 16),
+                                                (130, 13, 5, 7)])
+def test_equal_scores_beside_almost_equal_keys(E, groups, group_k, k, dtype):
+    # scores of a few values whose score functions differ by 1e-6 to 1e-14: in fp32 they, and many equal ones, are one key
+    rng = np.random.default_rng(E + k)
+    tops = [np.array(v) for v in ([20.0, 20.5], [14.0, 14.25, 20.0], [12.0, 30.0, 31.0, 32.0], [-0.5, 20.0, 20.5],
+                                  [-20.0, -20.5, -21.0], [-90.0, -60.0, -20.0], [1.0, 1.0 + 2.0 ** -23])]
+    for v in tops:
+        s = torch.from_numpy(v[rng.integers(0, len(v), size=(200, E))]).to(DT[dtype]).double().numpy()
+        s[::2][rng.random((100, E)) < 0.9] = v[0] if dtype == "f32" else float(torch.tensor(v[0]).to(torch.bfloat16))
+        s[5::7][rng.random(s[5::7].shape) < 0.3] = -np.inf
+        for bias in (None, np.zeros(E, dtype=np.float32), np.repeat(_bias(groups, 7), E // groups)):
+            for score, renorm in (("sigmoid", True), ("softmax", True)):
+                check(s, k, score, bias, groups, group_k, renorm, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("spread", [4.0, 8.0, 16.0, 40.0])
+def test_peaked_scores(spread, dtype):
+    for T, E, groups, group_k, k in ((400, 256, 8, 4, 8), (400, 64, 8, 4, 6), (300, 96, 3, 2, 4), (300, 32, 16, 5, 9)):
+        s = _scores(T, E, dtype, 0.1, E, spread)
+        for score in ("sigmoid", "softmax"):
+            for bias in (None, _bias(E, 3)):
+                check(s, k, score, bias, groups, group_k, True, dtype)
+
+
 @pytest.mark.parametrize("low", [-50.0, -62.5, -64.0, -1e4, -1e9, float(torch.finfo(torch.float32).min)])
 def test_experts_pushed_out_by_finite_biases(low):
     rng = np.random.default_rng(3)
