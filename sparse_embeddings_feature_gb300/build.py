@@ -97,7 +97,7 @@ def build_calls(force: bool = False):
     except (OSError, RuntimeError) as e:
         failed = str(e)
     if failed:
-        warnings.warn(f"calls.cpp was not compiled, the expert layer's calls read their arguments in Python:\n{failed}",
+        warnings.warn(f"calls.cpp was not compiled, the layers' calls read their arguments in Python:\n{failed}",
                       RuntimeWarning)
     else:
         os.replace(tmp, CALLS)

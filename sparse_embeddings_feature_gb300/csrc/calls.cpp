@@ -1,5 +1,5 @@
-// The expert layer's calls from Python in their usual layouts: the arguments' types and shapes are read
-// from the tensors here, on the current stream, and the C entry point called.  A call whose arguments
+// The calls of the expert layer and of the layers around it from Python, in their usual layouts: the arguments' types and
+// shapes are read from the tensors here, on the current stream, and the C entry point called.  A call whose arguments
 // are anything else (strided rows, a wrong shape, tensors of another device than the current one, not a
 // tensor) returns None: the binding in Python then takes it, with its own checks and messages.  Reading
 // and checking eight tensors there, and handing 16 numbers over, takes 5 us of the host, more than the

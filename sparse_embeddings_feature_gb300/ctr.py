@@ -6,8 +6,8 @@ passed along, and a negative ctr_status becomes a CtrError.  All computation
 happens in libctr's CUDA kernels; there is no CPU fallback.  If the library
 cannot be built or loaded the first call raises.
 
-The expert layer's calls are short enough that reading their arguments here
-costs more than the kernels: in the usual layouts (dense tensors, the current
+The calls of the expert layer and of the layers around it are short enough that
+reading their arguments here costs more than the kernels: in the usual layouts (dense tensors, the current
 stream) csrc/calls.cpp reads them, and what it does not take comes back here.
 """
 from __future__ import annotations
@@ -157,7 +157,7 @@ def _usual():
                     loader.exec_module(calls)
                     _calls = calls
                 except ImportError as e:
-                    warnings.warn(f"{path} cannot be loaded, the expert layer's calls read their arguments in Python: {e}",
+                    warnings.warn(f"{path} cannot be loaded, the layers' calls read their arguments in Python: {e}",
                                   RuntimeWarning)
             if _calls is None:
                 _calls = _NoCalls()
