@@ -799,7 +799,8 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
         // nearer to 2 than 64 bits' sums can be compared with this error, or past fp32
         if (a.sigmoid && !(worth < 0x1p30f)) rel = 2.f;
       }
-      auto apart_from = [&](float other) { return fabsf(worth - other) > rel * fmaxf(worth, other); };  // NaN: no
+      // NaN: no; the smallest numbers lose bits, or all of them
+      auto apart_from = [&](float other) { return fabsf(worth - other) > fmaf(rel, fmaxf(worth, other), 0x1p-118f); };
       bool tight = false;
       for (int g = 0; g < a.groups; ++g) {
         const float other = __shfl_sync(kFull, worth, g, LANES);

@@ -141,7 +141,8 @@ def test_equal_scores_beside_almost_equal_keys(E, groups, group_k, k, dtype):
     # scores of a few values whose score functions differ by 1e-6 to 1e-14: in fp32 they, and many equal ones, are one key
     rng = np.random.default_rng(E + k)
     tops = [np.array(v) for v in ([20.0, 20.5], [14.0, 14.25, 20.0], [12.0, 30.0, 31.0, 32.0], [-0.5, 20.0, 20.5],
-                                  [-20.0, -20.5, -21.0], [-90.0, -60.0, -20.0], [1.0, 1.0 + 2.0 ** -23])]
+                                  [-20.0, -20.5, -21.0], [-90.0, -60.0, -20.0], [1.0, 1.0 + 2.0 ** -23],
+                                  [-86.5, -87.0, -87.5, -88.0], [-87.5, 0.0, -87.0, -88.5, -103.0], [-96.0, 5.0, -100.0, -104.0])]
     for v in tops:
         s = torch.from_numpy(v[rng.integers(0, len(v), size=(200, E))]).to(DT[dtype]).double().numpy()
         s[::2][rng.random((100, E)) < 0.9] = v[0] if dtype == "f32" else float(torch.tensor(v[0]).to(torch.bfloat16))
