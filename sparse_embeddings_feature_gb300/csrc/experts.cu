@@ -610,25 +610,81 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
   return x;
 }
 
-// Packed keys: the keys' range from the smallest bias on is cut into 2^23 - 4 parts of 1 / scale, numbered from 1.
+// Packed keys: the keys' range from the smallest bias on is cut into kParts parts of 1 / scale, numbered from 1.
 // What a key may be off by besides p's own error, in parts (2^-24 of a range is half a part): three roundings of the
 // bias's part number and one of the sum, half a part each, and one part for cutting off.
-// Experts whose bias is more than kSpread below the largest one (pushed out by -1e9, say) would make the parts as coarse as
-// that is.  They have their keys in a range of their own below the others', where a part says only that its key is below
-// theirs (65536 x 256, 4 of 8 groups, a tenth of the biases -1e9: 105 us; in parts of that range, which tell nothing apart,
-// 3083; a wider spread has coarser parts: 62, 137 us).  Of a few biases far above the rest it is the rest that is pushed out.
+// Biases further apart than kSpread (experts pushed out by -1e9, or lifted, say) would make the parts as coarse as that is.
+// Their gaps of more than kGap are closed to that: p is at most 1, so keys on either side of such a gap keep their order, and
+// by more parts than a comparison asks for; keys with no such gap between them keep their distance (65536 x 256 bf16, k 8, 4 of
+// 8 groups, sigmoids and softmax: biases of 0.05 96 and 126 us, a tenth of them -1e9 108 and 139, one of them +10 105 and
+// 137; in parts of the whole range -1e9 takes 3.1 ms, +10 106 and 234).  Closing takes a block 1.7 us, so biases spread by less
+// are left as they are.
 struct Packing {
   float scale;
+  bool cut;         // whether gaps have been closed
+  bool top_coarse;  // the largest bias is past kLarge
   static constexpr float off = 3.f;
 };
 struct PackedBias {            // shared
   float at[CTR_MAX_EXPERTS];   // each expert's part number at p = 0; -inf: never chosen
-  int border;                  // keys of smaller parts are of experts pushed out
+  float lift[CTR_MAX_EXPERTS]; // where gaps have been closed: a key less the largest bias's, in parts, less the same of part numbers
+  int low, high;               // keys of smaller parts, and of these and larger ones, have biases past kLarge
 };
+constexpr float kParts = 8388592.f;  // a few below 2^23, which p may pass 1 by
 constexpr float kSpread = 6.f;
-constexpr float kGap = 1.0625f;      // the smallest bias of the upper range less that of the lower: p is at most 1
+constexpr float kGap = 1.0625f;
 constexpr float kLarge = 1073741824.f;  // 2^30: past it a 64-bit key's last bit is more than a part
 static_assert(CTR_MAX_EXPERTS <= 512, "an index has 9 bits");
+
+// `to` of biases b whose gaps are closed; some: whether the thread's expert may be chosen.  Distances are added up as whole
+// numbers of 2^-40: what a distance is off by are the gaps' own roundings, 2^-24 of it (in 64-bit numbers the same took 7 us).
+__device__ __noinline__ Packing pack_apart(PackedBias& to, int experts, float b, bool some) {
+  __shared__ int64_t sums[kRouteThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = threadIdx.x;
+  if (e < experts) to.at[e] = some ? b : INFINITY;
+  const int n = __syncthreads_count(some);
+  int rank = 0;  // by bias, then index
+  if (some) {
+#pragma unroll 8
+    for (int j = 0; j < experts; ++j) rank += to.at[j] < b || (to.at[j] == b && j < e);
+    to.lift[rank] = b;
+  }
+  __syncthreads();
+  // thread r: the r-th smallest, its distance from the smallest with the gaps closed
+  const int r = e;
+  const float mine = r < n ? to.lift[r] : 0.f, before = r > 0 && r < n ? to.lift[r - 1] : mine, top = to.lift[n - 1];
+  const bool cut = __syncthreads_or(mine - before > kGap);  // and the next write to `lift` comes after all reads
+  int64_t c = (int64_t)(fminf(mine - before, kGap) * 0x1p40f);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(kFull, c, o);
+    if (lane >= o) c += y;
+  }
+  if (lane == 31) sums[warp] = c;
+  if (e == 0) to.low = to.high = 1 << 23;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < kRouteThreads / 32; ++w) {
+    if (w < warp) c += sums[w];
+    all += sums[w];
+  }
+  const float scale = kParts / (1.f + (float)all * 0x1p-40f);
+  const float at = fmaf((float)c * 0x1p-40f, scale, 1.f), lift = ((mine - top) + (float)(all - c) * 0x1p-40f) * scale;
+  if (r < n) {
+    to.at[r] = at;
+    to.lift[r] = lift;
+    if (mine > -kLarge && (r == 0 || before <= -kLarge)) to.low = (int)at;
+    if (mine >= kLarge && (r == 0 || before < kLarge)) to.high = (int)at;
+  }
+  __syncthreads();
+  const float my_at = some ? to.at[rank] : -INFINITY, my_lift = some ? to.lift[rank] : 0.f;
+  __syncthreads();
+  to.at[e] = my_at;
+  to.lift[e] = my_lift;
+  return {scale, cut, fabsf(top) >= kLarge};
+}
+static_assert(kRouteThreads == CTR_MAX_EXPERTS, "a rank, and an expert, to a thread");
 
 // `to` filled by all threads of the block.
 __device__ __forceinline__ Packing pack_range(const RouteArgs& a, PackedBias& to, float* ends) {
@@ -655,15 +711,18 @@ __device__ __forceinline__ Packing pack_range(const RouteArgs& a, PackedBias& to
     hi = fmaxf(hi, ends[2 * w + 1]);
   }
   if (!(lo <= hi)) lo = hi = 0.f;
-  const bool out = hi - lo > kSpread;
-  if (out) lo = hi - kSpread;
-  const float range = 1.f + (hi - lo) + (out ? kGap : 0.f), scale = 8388604.f / range;
-  const float shift = 1.f + (out ? floorf(kGap * scale) : 0.f);  // a whole number
-  if (e < CTR_MAX_EXPERTS) to.at[e] = !some ? -INFINITY : b < lo ? 1.f : shift + (b - lo) * scale;
-  // between the two ranges are 1/16 of a key's, thousands of parts; of biases past kLarge all keys are near
-  if (e == 0) to.border = fabsf(hi) >= kLarge ? 1 << 23 : out ? (int)shift - 2048 : 0;
+  Packing pack = {kParts / (1.f + (hi - lo)), false, fabsf(hi) >= kLarge};
+  if (hi - lo > kSpread) {  // the same in all threads
+    pack = pack_apart(to, a.experts, b, some);
+  } else {
+    to.at[e] = some ? fmaf(b - lo, pack.scale, 1.f) : -INFINITY;
+    if (e == 0) {
+      to.low = pack.top_coarse ? 1 << 23 : 0;
+      to.high = 1 << 23;
+    }
+  }
   __syncthreads();
-  return {scale};
+  return pack;
 }
 
 // The expert of choice `sub` of the lanes' token t, -1: none; near: this could not tell.  KMAX: choices at most.  REFINE:
@@ -714,9 +773,9 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
       for (int i = 0; i < EPL; ++i) part(i, exp2_fast((v[i] - shift) * kLog2e) * times);
     }
   }
-  const int border = plain ? 0 : bias.border;
+  const int low = plain ? 0 : bias.low, high = plain ? 1 << 23 : bias.high;
   auto nearby = [&](uint32_t x, uint32_t y) {  // whether y, the smaller packed key, may be the larger one
-    return y != 0 && ((int)((x >> 9) - (y >> 9)) <= apart || (int)(x >> 9) < border);
+    return y != 0 && ((int)((x >> 9) - (y >> 9)) <= apart || (int)(x >> 9) < low || (int)(y >> 9) >= high);
   };
   auto unclear = [&](uint32_t x, uint32_t y) { return nearby(x, y) && !same_inputs(a, t, x, y); };
   if (grouped) {
@@ -761,22 +820,36 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     bool close = false;
     // near: on either side of the border; equal pairs are ties where packed keys are exact, so that the pairs are the best
     if (!plain) {
-      const int worth = some ? (int)((k0 >> 9) + (k1 >> 9)) : -0x40000000;
-      int gap = 0x7fffffff;
-      for (int g = 0; g < a.groups; ++g) {
-        const int other = __shfl_sync(kFull, worth, g, LANES);
-        place += other > worth || (other == worth && g < sub);
-        if (g != sub) gap = min(gap, abs(worth - other));
+      // In parts; where gaps have been closed, what they hid is added again, within 8 parts and a few 2^-23 of itself (a sum
+      // past fp32's range is below all others).
+      float worth = some ? (float)((k0 >> 9) + (k1 >> 9)) : -INFINITY;
+      float least = 2.f * (float)apart, rel = 0.f;
+      if (pack.cut) {
+        least += 16.f;
+        rel = 0x1p-21f;
+        if (some)
+          worth = fmaxf(worth + (bias.lift[511 - (k0 & 511u)] + (k1 ? bias.lift[511 - (k1 & 511u)] : 0.f)), -3e38f);
       }
-      // a sum of one key is not to be compared with one of two in parts, nor one with a key of the lower range
+      auto apart_from = [&](float other) {  // a group without keys from any other
+        return fabsf(worth - other) > fmaf(rel, fmaxf(fabsf(worth), fabsf(other)), least) || other == -INFINITY;
+      };
+      float gap = INFINITY;  // to the nearest other group
+      for (int g = 0; g < a.groups; ++g) {
+        const float other = __shfl_sync(kFull, worth, g, LANES);
+        place += other > worth || (other == worth && g < sub);
+        if (g != sub) gap = fminf(gap, fabsf(worth - other));
+      }
+      const bool tight = gap <= fmaf(rel, fabsf(worth) + gap, least);  // or no other one can be near
+      // a sum of one key is not to be compared with one of two in parts
       const uint32_t all = LANES == 32 ? kFull : (1u << (LANES & 31)) - 1;
       const uint32_t ones = __ballot_sync(kFull, some && k1 == 0) >> first & all;
       const uint32_t twos = __ballot_sync(kFull, some && k1 != 0) >> first & all;
-      close = (ones != 0 && twos != 0) || (some && (int)((k1 ? k1 : k0) >> 9) < border);
-      if (__any_sync(kFull, some && gap <= 2 * apart)) {
+      close = (ones != 0 && twos != 0) || (some && pack.top_coarse);
+      if (__any_sync(kFull, some && tight)) {
         for (int g = 0; g < a.groups; ++g) {
-          const int other = __shfl_sync(kFull, worth, g, LANES), there = __shfl_sync(kFull, place, g, LANES);
-          close |= some && (place < a.group_k) != (there < a.group_k) && abs(worth - other) <= 2 * apart;
+          const float other = __shfl_sync(kFull, worth, g, LANES);
+          const int there = __shfl_sync(kFull, place, g, LANES);
+          close |= some && (place < a.group_k) != (there < a.group_k) && !apart_from(other);
         }
       }
     } else {
@@ -912,8 +985,8 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
 
 // The same again with 64 bits, from the row itself.  Not inlined: few tokens come here.
 template <int EPL, int LANES>
-__device__ __noinline__ int choose_again(const RouteArgs& a, const PackedBias& bias, float scale, int64_t t, bool mine,
-                                         int sub) {
+__device__ __noinline__ int choose_again(const RouteArgs& a, const PackedBias& bias, Packing pack, int64_t t,
+                                         bool mine, int sub) {
   float v[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -923,7 +996,7 @@ __device__ __noinline__ int choose_again(const RouteArgs& a, const PackedBias& b
   float shift = 0.f, total = 1.f;
   if (!a.sigmoid) total = row_softmax<float, EPL>(v, LANES, shift);
   bool near;
-  int expert = choose_packed<EPL, CTR_MAX_CHOICES, LANES, true>(a, v, bias, Packing{scale}, t, sub, shift, total, near);
+  int expert = choose_packed<EPL, CTR_MAX_CHOICES, LANES, true>(a, v, bias, pack, t, sub, shift, total, near);
   if (__any_sync(kFull, near)) {
     float b[EPL];
 #pragma unroll
@@ -975,7 +1048,7 @@ __global__ void __launch_bounds__(kRouteThreads, 2) route_balanced_kernel(const 
     bool near;
     int expert = choose_packed<EPL, KMAX, LANES, false>(a, v, bias, pack, t0 + tl, sub, shift, total, near);
     if (__any_sync(kFull, near))
-      expert = choose_again<EPL, LANES>(a, bias, pack.scale, t0 + tl, mine && !bad, sub);
+      expert = choose_again<EPL, LANES>(a, bias, pack, t0 + tl, mine && !bad, sub);
     // weights: lane j has choice j
     const bool live = expert >= 0;
     const float s = live ? score_at(a, t0 + tl, expert) : -INFINITY;
