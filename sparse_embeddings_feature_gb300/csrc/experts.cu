@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_choose_kernel(const Route
 // those and is not their equal), all keys in 64 bits, of which a warp's instruction takes 64 cycles (all tokens of 65536 x
 // 256 so: 3.1 ms).
 // 65536 x 256, k 8, 4 of 8 groups, all tokens in fp32 with a round a choice for the key and one for its index: 196 us.
-// e^x in 64 bits for |x| <= 700 (beyond, e^-700 and e^700): 2^(j / 64) from a table, the rest, below ln 2 / 128, by five
+// e^x in 64 bits for x from -700 to 709.7 (beyond, as at the ends): 2^(j / 64) from a table, the rest, below ln 2 / 128, by five
 // terms of the series: a third of the 64-bit instructions of exp, which a warp is bound by.
 __device__ const double kPowers[64] = {
     1.0, 1.0108892860517005, 1.0218971486541166, 1.0330248790212284,
@@ -453,7 +453,7 @@ __device__ const double kPowers[64] = {
     1.8340080864093424, 1.8539791250833855, 1.8741676341103, 1.8945759815869656,
     1.9152065613971474, 1.9360617934922943, 1.9571441241754002, 1.978456026387951};
 __device__ __forceinline__ double exp_64(double x) {
-  x = fmin(fmax(x, -700.0), 700.0);
+  x = fmin(fmax(x, -700.0), 709.7);
   const double shifted = x * 92.33248261689366 + 0x1.8p52;  // the nearest whole number of 64ths of ln 2, in the low bits
   const int n = __double2loint(shifted);
   const double k = shifted - 0x1.8p52;
@@ -467,6 +467,12 @@ __device__ __forceinline__ double exp_64(double x) {
   const double y = fma(t, p, t);
   return __hiloint2double(__double2hiint(y) + ((n >> 6) << 20), __double2loint(y));
 }
+// The same down to 64 bits' smallest numbers, below which it is 0.
+__device__ __forceinline__ double exp_64_down(double x) {
+  return x < -700.0 ? exp_64(x + 700.0) * 9.85967654375977e-305 : exp_64(x);  // e^-700
+}
+// 1 / (1 + e^-x); where 64 bits hold no difference, e^x, which has a value longer.
+__device__ __forceinline__ double sigmoid_64(double x) { return x < -40.0 ? exp_64_down(x) : 1 / (1 + exp_64(-x)); }
 
 template <typename K>
 __device__ __forceinline__ K exp_of(K x);
@@ -476,7 +482,7 @@ __device__ __forceinline__ float exp_of<float>(float x) {
 }
 template <>
 __device__ __forceinline__ double exp_of<double>(double x) {
-  return x > -700.0 ? exp_64(x) : 0.0;  // a masked score's, among others
+  return x > -700.0 ? exp_64(x) : 0.0;  // nothing beside a sum of 1 and more
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -511,7 +517,7 @@ __device__ __forceinline__ int choose_exact(const RouteArgs& a, const float (&v)
   if (!a.sigmoid) total = row_softmax<double, EPL>(v, a.lanes, m);
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const double p = a.sigmoid ? 1 / (1 + exp_64(-(double)v[i])) : exp_of<double>((double)v[i] - m) / total;
+    const double p = a.sigmoid ? sigmoid_64(v[i]) : exp_64_down((double)v[i] - m) / total;
     key[i] = v[i] > -INFINITY && b[i] > -INFINITY ? p + b[i] : none;
   }
   auto take = [](double& x0, double& x1, double x) {
@@ -743,7 +749,7 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
   auto exact = [&](uint32_t x) {  // a packed key's value in 64 bits
     const int e = 511 - (int)(x & 511u);
     const double l = score_at(a, t, e), b = a.bias ? a.bias[e] : 0.f;
-    return (a.sigmoid ? 1 / (1 + exp_64(-l)) : exp_of<double>(l - shift) / sum) + b;
+    return (a.sigmoid ? sigmoid_64(l) : exp_64_down(l - shift) / sum) + b;
   };
   if (plain) {
     // scores of one upper part differ in what was cut off, but for bf16 ones, which have nothing there
