@@ -102,7 +102,7 @@ __device__ __forceinline__ float derivative(int act, float z) {
       return fmaf(0.39894228040143268f * z, bell, below);
     }
     case CTR_ACT_SIGMOID: {
-      const float s = sigmoid_of(fabsf(z));  // the larger of both: 1 - s is the other
+      const float s = sigmoid_of(-fabsf(z));  // the smaller of both: 1 less the larger has lost what that rounded away
       return s * (1.f - s);
     }
     default: return 1.f;
