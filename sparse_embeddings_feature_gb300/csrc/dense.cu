@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, kDzBlocks<VEC>) dz_kernel(const DzAr
       load_part<T, VEC>((const T*)a.dy + r * a.ld_dy, c, a.n, v);
       if (a.pre) {
         load_part<T, VEC>((const T*)a.pre + r * a.ld_pre, c, a.n, z);
-        times_derivative(a.act, v, z);
+        times_derivative<T>(a.act, v, z);
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) acc[i] += v[i];
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) dense_few_kernel(const FewArgs a) {
   if (lane >= ROWS * COLS || t >= a.rows || col >= a.n) return;
   if (a.bias) z += to_f32<T>(((const T*)a.bias)[col]);
   if (a.pre) ((T*)a.pre)[t * a.ldp + col] = from_f32<T>(z);
-  z = activation(a.act, z);
+  z = activation<T>(a.act, z);
   if (a.residual) z += to_f32<T>(((const T*)a.residual)[t * a.ldr + col]);
   ((T*)a.y)[t * a.ldy + col] = from_f32<T>(z);
 }

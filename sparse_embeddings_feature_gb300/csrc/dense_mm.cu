@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "dense_mm.cuh"
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
             piece_out<float>(piece, p.pre, p.ldp, row0, nrows, col, p.n, p.wide_pre != 0);
             __syncwarp();
           }
-          if constexpr (MAJOR == 0) activate(p.act, z);
+          if constexpr (MAJOR == 0) activate<std::conditional_t<PLANES == 3, float, __nv_bfloat16>>(p.act, z);
           if (has_res) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -667,7 +668,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
 #pragma unroll
             for (int g = 0; g < 4; ++g) *(uint4*)(staging + 2 * kPiece + lane * 128 + at(g)) = pack8(g);
           }
-          if constexpr (MAJOR == 0) activate(p.act, z);
+          if constexpr (MAJOR == 0) activate<std::conditional_t<PLANES == 3, float, __nv_bfloat16>>(p.act, z);
           if (has_res) {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {

@@ -1,5 +1,11 @@
 """Activations and their derivatives, accurate relative to their own size.
 
+u = 2^-24.  fp32: e^-|z| is within 5 u (the exponential 2^-22, its correction one rounding), 1 + it within 4 u, its
+reciprocal 2 u more; sigmoid (a product, one rounding) within 12 u, sigmoid' = e r^2 within 18 u; silu one rounding
+more, silu' the same of its two terms' magnitudes.  gelu: the tail of the normal distribution is bell P, P within 8 u (a
+polynomial of degree 8 within 1 u, its evaluation 5 u, its argument's reciprocal 2 u) and bell within 6 u: 16 u with the
+products; gelu' the same of its two terms' magnitudes.
+
 bf16 layers: what rounding to bf16 covers, 2^-9 of the derivative, is far above the exponential's (|z| + 8) 2^-24; gelu's erf is
 within 1.5e-7 of itself, so its derivative below 1e-4 by that much.  An exponential below 2^-126 is zero: 1e-37 (1 + |z|)."""
 import math
@@ -39,6 +45,35 @@ def _terms(act, z):
     phi = torch.where(z < 0, below, 1 - below)
     bell = z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
     return z * phi, z.abs() * phi, phi + bell, phi + bell.abs()
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("rows", [1, 7, 40])
+def test_fp32_activations(rows, act):
+    # z = x * 1 with one column of x and w; 1 and 7 rows take the kernel for few rows, 40 the tensor cores
+    n = 4096
+    x = torch.ones((rows, 1), device="cuda")
+    z = _points(n)
+    y, pre = torch.empty((rows, n), device="cuda"), torch.empty((rows, n), device="cuda")
+    ws = ctr.workspace(ctr.ctr_dense_workspace_size(rows, n, 1, torch.float32))
+    ctr.ctr_dense(x, z[:, None].contiguous(), None, ctr.ACTIVATIONS[act], None, y, pre, ws)
+    value, mag, _, _ = _terms(act, pre.double())
+    assert bool(((y.double() - value).abs() <= 16 * U * mag + ABS * (1 + pre.double().abs())).all())
+    assert ctr.ctr_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_fp32_derivatives(act):
+    # one row: the bias's gradient is dz itself
+    n = 8192
+    z, dy = _points(n)[None], torch.ones((1, n), device="cuda")
+    x, w = torch.ones((1, 1), device="cuda"), torch.ones((n, 1), device="cuda")
+    db = torch.empty((n,), device="cuda")
+    ws = ctr.workspace(ctr.ctr_dense_workspace_size(1, n, 1, torch.float32, True))
+    ctr.ctr_dense_bwd(dy, x, w, z, ctr.ACTIVATIONS[act], None, None, db, ws)
+    zz = z[0].double()
+    _, _, d, mag = _terms(act, zz)
+    assert bool(((db.double() - d).abs() <= 20 * U * mag + ABS * (1 + zz.abs())).all())
 
 
 @pytest.mark.parametrize("act", ACTS)
