@@ -636,12 +636,14 @@ typedef enum {
  * [rows, n], all of `dtype`.  pre (optional) gets z, which the backward call
  * needs where there is an activation.  Sums are fp32, bias, activation and
  * residual are applied to them in fp32, y and pre are rounded once.
- * bf16: products of the tensor cores.  fp32: also there, x and w each as three
- * bf16 numbers that add up to it, six of their nine products: what is dropped is
- * below 2^-24 of |x| |w|, so results are as near as those of fp32 sums.  A NaN
- * or an infinity in x or w makes what it enters NaN, or the infinity that the
- * formula gives.  y may be residual itself (the same rows and stride); nothing
- * else may overlap.
+ * bf16: products of the tensor cores, whose additions drop what fp32 cannot hold:
+ * sums of up to 65536 terms are up to 1.8e-4 of their terms' magnitudes too near
+ * to zero; longer ones, and all of fp32's, are read back as they go and added up
+ * with rounding.  fp32: also there, x and w each as three bf16 numbers that add up
+ * to it, six of their nine products: what is dropped is below 2^-24 of |x| |w|, so
+ * results are as near as those of fp32 sums.  A NaN or an infinity in x or w makes
+ * what it enters NaN, or the infinity that the formula gives.  y may be residual
+ * itself (the same rows and stride); nothing else may overlap.
  * Device errors: CTR_ERR_TIMEOUT.
  * Workspace: ctr_dense_workspace_size(rows, n, k, dtype, train, packed) bytes,
  * asked on the device of the call: train != 0 for ctr_dense_bwd (with room for

@@ -13,7 +13,7 @@
 // The tensor core's additions to an accumulator drop what fp32 cannot hold instead of rounding it: a sum of n
 // instructions (16 of r each) comes out about 0.75 n 2^-24 too near to zero (measured: 56 of them 2.5e-6, 256 1.2e-5),
 // which a bf16 result does not show and an fp32 one does.  So where results are fp32, or sums as long as a batch
-// (FLUSH), an accumulator is read back every few blocks and added up in registers, with rounding.  With planes, the
+// or past kLongSum (kFlush), an accumulator is read back every few blocks and added up in registers, with rounding.  With planes, the
 // product of the first ones has an accumulator of its own, flushed every kMainBlocks; the five small ones, 2^-8 of it
 // and less, share the other, flushed every kCrossBlocks.
 //
@@ -56,7 +56,10 @@ constexpr int kMinShare = 8;                      // blocks of a part of a sum, 
 constexpr int kPairBlocks = 64;                   // blocks of a sum that pairs cut up whatever the number of tiles
 constexpr int kMainBlocks = 2, kCrossBlocks = 64; // blocks between two readings (planes): 8 and 1280 instructions
 constexpr int kFlushBlocks = 8;                   // without planes: 32 instructions
-// Registers of a FLUSH kernel: 384 threads are launched with 168 each; the first four warps give some up so that an
+// Forward and input gradient without planes sum up to this many terms in the accumulator alone: 1.8e-4 too near to zero at most, a
+// tenth of a bf16 result's rounding (4096 x 4096 x 65536 1455 us, 64 more terms, read back, 1493).
+constexpr int64_t kLongSum = 65536;
+// Registers of a kFlush kernel: 384 threads are launched with 168 each; the first four warps give some up so that an
 // epilogue thread can hold 128 sums beside the 64 values that it adds.  56 x 128 + 224 x 256 = 168 x 384.
 constexpr int kLaunchRegs = 168, kControlRegs = 56, kOutRegs = 224;
 static_assert(kControlRegs * 128 + kOutRegs * 32 * kOutWarps <= kLaunchRegs * kDmThreads, "more registers than launched");
@@ -278,7 +281,7 @@ __device__ __forceinline__ void piece_in(uint8_t* piece, const char* from, int64
 
 constexpr bool flushes(int major, int planes) { return planes == 3 || major == 2; }
 
-template <int BN, int MAJOR, int PLANES>
+template <int BN, int MAJOR, int PLANES, bool LONG>
 __global__ void __launch_bounds__(kDmThreads, 1)
     dense_mm_kernel(const DmArgs p, const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                     const __grid_constant__ CUtensorMap omap, const __grid_constant__ CUtensorMap rmap,
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kDmThreads, 1)
   constexpr bool PAIR = BN == 256;
   static_assert(BN != 32 || MAJOR == 0, "32 columns of an MN-major operand are half a row of its layout");
   constexpr bool kAmn = MAJOR == 2, kBmn = MAJOR >= 1;
-  constexpr bool kFlush = flushes(MAJOR, PLANES);
+  constexpr bool kFlush = flushes(MAJOR, PLANES) || LONG;
   constexpr int kBN = BN;
   constexpr int kCols = kBN / S::parts;  // columns of an epilogue thread
   constexpr int kCtas = PAIR ? 2 : 1;
@@ -534,9 +537,9 @@ __global__ void __launch_bounds__(kDmThreads, 1)
         auto add = [&](uint32_t acc, uint32_t parity) {
           if (!park(tfull0 + 8 * acc, parity)) return false;
           fence_after();
-          // 64 columns at once; with planes, whose epilogue has more to hold, 32 (spills go to L2: all but nothing is left of
+          // 64 columns at once; with planes, or activations, whose epilogue has more to hold, 32 (spills go to L2: all but nothing is left of
           // L1 beside the operands)
-          constexpr int kStep = PLANES == 3 || kCols < 64 ? 32 : 64;
+          constexpr int kStep = PLANES == 3 || LONG || kCols < 64 ? 32 : 64;
 #pragma unroll
           for (int c = 0; c < kCols; c += kStep) {
             uint32_t v0[32], v1[32];
@@ -852,7 +855,7 @@ DmArgs dm_args(const MmCall& c, const MmPlan& plan) {
   return p;
 }
 
-template <int BN, int MAJOR, int PLANES>
+template <int BN, int MAJOR, int PLANES, bool LONG>
 int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) {
   constexpr int kCtas = BN == 256 ? 2 : 1, kSide = BN == 256 ? 256 : 128;
   using S = Shape<PLANES, BN>;
@@ -890,12 +893,12 @@ int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) 
   if (p.wide_out && !piece_map(&omap, p.out, p.f32 != 0, out_rows, out_cols, p.ldo)) return CTR_ERR_CUDA;
   if (p.wide_res && !piece_map(&rmap, p.res, p.f32 != 0, c.m, c.n, p.ldr)) return CTR_ERR_CUDA;
   if (p.wide_pre && !piece_map(&pmap, p.pre, p.f32 != 0, c.m, c.n, p.ldp)) return CTR_ERR_CUDA;
-  auto k = dense_mm_kernel<BN, MAJOR, PLANES>;
+  auto k = dense_mm_kernel<BN, MAJOR, PLANES, LONG>;
   static std::atomic<uint64_t> ready{0};
   if (!once_per_device(ready, [&] {
         // the split of registers between the warps waits for ever if the kernel was launched with fewer
         cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, k) != cudaSuccess || (flushes(MAJOR, PLANES) && fa.numRegs != kLaunchRegs)) return false;
+        if (cudaFuncGetAttributes(&fa, k) != cudaSuccess || ((flushes(MAJOR, PLANES) || LONG) && fa.numRegs != kLaunchRegs)) return false;
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::smem) == cudaSuccess;
       }))
     return CTR_ERR_CUDA;
@@ -906,7 +909,10 @@ int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) 
 
 template <int BN, int MAJOR>
 int launch_dm(const MmCall& c, const MmPlan& plan, float* part, cudaStream_t s) {
-  return c.planes == 1 ? launch_dm<BN, MAJOR, 1>(c, plan, part, s) : launch_dm<BN, MAJOR, 3>(c, plan, part, s);
+  if (c.planes == 3) return launch_dm<BN, MAJOR, 3, false>(c, plan, part, s);
+  if constexpr (MAJOR != 2 && BN != 32)
+    if (c.r > kLongSum) return launch_dm<BN, MAJOR, 1, true>(c, plan, part, s);
+  return launch_dm<BN, MAJOR, 1, false>(c, plan, part, s);
 }
 
 template <int MAJOR>
@@ -937,7 +943,8 @@ MmPlan mm_plan(int major, int planes, int64_t m, int64_t n, int64_t r) {
   const int64_t side = w.side(), most = mm_workers(pair);
   const int64_t tiles = ceil_div(m, side) * ceil_div(n, side);
   // few rows: more and narrower tiles, so that more SMs read the weights
-  if (!pair && major == 0 && 2 * tiles <= sms && n > 32) w.columns = 32;
+  const bool readback = planes == 1 && r > kLongSum;  // which those tiles have not
+  if (!pair && major == 0 && 2 * tiles <= sms && n > 32 && !readback) w.columns = 32;
   if (major != 2) return w;
   // Sums over a batch are cut into the number of parts that takes least, in blocks' times (0.27 us with planes of bf16
   // alone): the rounds of all workers, six blocks for each tile's setting up and end, and each part's writing and reading.
