@@ -143,7 +143,7 @@ __device__ __forceinline__ float row_sum(float v, int wpr, float* sums) {
 }
 
 // 1 / sqrt(mean(f^2) + eps) over a row.  Squares that leave fp32's range (or all but do, against a small eps)
-// are taken again of scaled values; a NaN or an infinity in the row gives NaN or 0, and NaN results.
+// are taken again of scaled values (2^-80: kNormMaxCols squares of fp32's largest number are 2^110); a NaN or an infinity in the row gives NaN or 0, and NaN results.
 template <int LANES, int EPT>
 __device__ __forceinline__ float row_rstd(const float2 (&f)[EPT / 2], const NormArgs& a, float (*sums)[16]) {
   float2 sq = make_float2(0.f, 0.f);
@@ -154,7 +154,7 @@ __device__ __forceinline__ float row_rstd(const float2 (&f)[EPT / 2], const Norm
   float rstd = 1.f / sqrtf(mean);
   const bool odd = !(mean < 1e37f) || mean < 1e-30f;  // the same in all of a row's threads
   if (__any_sync(kFull, odd)) {
-    const float by = mean < 1e-30f ? 0x1p70f : 0x1p-70f;
+    const float by = mean < 1e-30f ? 0x1p70f : 0x1p-80f;
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < EPT / 2; ++i) {
