@@ -79,7 +79,8 @@ class ResidualBlock:
 
 class NormProduct:
     """s = x + residual and y = (norm(s) gamma) W^T for x [rows, width], the product in 8 bits, W [out_width, width]
-    quantised when it is set: one layer of a serving stack.  The norm writes the codes that the product reads."""
+    quantised when it is set, before the first forward: one layer of a serving stack.  The norm writes the codes that the
+    product reads."""
 
     def __init__(self, rows: int, width: int, out_width: int, dtype=torch.bfloat16, eps: float = 1e-6, device="cuda"):
         if dtype not in ctr.DTYPES:
@@ -96,14 +97,19 @@ class NormProduct:
         self.wq, self.ws = buf(1, out_width, kb * 128, dt=torch.uint8), buf(1, nb, kb)
         self.room = ctr.workspace(max(ctr.ctr_rms_norm_workspace_size(rows, width),
                                       ctr.ctr_fp8_matmul_workspace_size(rows, 1, out_width, width)), device)
+        self.has_weights = False
 
     def set_weights(self, w: torch.Tensor) -> None:
         if tuple(w.shape) != (self.out_width, self.width):
             raise ValueError(f"weights must be {(self.out_width, self.width)}")
+        self.has_weights = False   # until the call is made
         ctr.ctr_fp8_quantize_blocks(w[None], self.wq, self.ws, self.room)
+        self.has_weights = True
 
     def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor], gamma: Optional[torch.Tensor]):
         """(s, y), the layer's own buffers."""
+        if not self.has_weights:
+            raise RuntimeError("forward needs weights: set_weights")
         ctr.ctr_rms_norm(x, residual, gamma, self.eps, self.s, None, self.q, self.scale, self.room)
         ctr.ctr_fp8_matmul(self.q, self.scale, self.wq, self.ws, None, self.y, self.room)
         return self.s, self.y
