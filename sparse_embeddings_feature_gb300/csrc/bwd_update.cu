@@ -1313,9 +1313,7 @@ int launch_tiles(const BwdArgs& a, K tk, size_t tile_smem, cudaStream_t s, int64
       if (a.grad_out) b.grad_out = a.grad_out + c0;
       b.TU = kPairTU;
       const size_t smem = (size_t)kTileWarps * b.TU * b.d * 4;
-      if (smem > 48 * 1024 &&
-          cudaFuncSetAttribute(pk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return CTR_ERR_CUDA;
+      if (smem > 48 * 1024 && !allow_smem(pk, smem)) return CTR_ERR_CUDA;
       if (cudaMemsetAsync(a.work, 0, sizeof(unsigned long long), s) != cudaSuccess) return CTR_ERR_CUDA;
       pk<<<grid_of(pk, kTileThreads, smem, ceil_div(n, (int64_t)b.TU * kTileWarps)), kTileThreads, smem, s>>>(b);
       count_launch();
@@ -1347,9 +1345,7 @@ int launch_short(const BwdArgs& a, cudaStream_t s, int64_t n) {
   if (use_async && ((size_t)a.TU * a.d * (a.bf16 ? 2 : 4)) % 16 != 0) return CTR_ERR_UNSUPPORTED;  // layout rule
   const size_t tile_smem =
       use_async ? (size_t)kTileWarps * tile_warp_bytes(a.TU, a.d, a.bf16 ? 2 : 4, ns, a.sr ? 1 : 0) : acc_smem;
-  if (tile_smem > 48 * 1024 &&
-      cudaFuncSetAttribute(tk, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tile_smem) != cudaSuccess)
-    return CTR_ERR_CUDA;
+  if (tile_smem > 48 * 1024 && !allow_smem(tk, tile_smem)) return CTR_ERR_CUDA;
   timing_mark(CTR_KERNEL_BWD_TILES, true, s);
   if (int st = launch_tiles(a, tk, tile_smem, s, n)) return st;
   timing_mark(CTR_KERNEL_BWD_TILES, false, s);
@@ -1401,9 +1397,7 @@ int launch_long(const BwdArgs& a, WsCarver& c, cudaStream_t s, int64_t n) {
 
 int launch_finish(const BwdArgs& a, cudaStream_t s) {
   const size_t csmem = (size_t)(kCombThreads / 32) * a.d * sizeof(float);
-  if (csmem > 48 * 1024 &&
-      cudaFuncSetAttribute(combine_long_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)csmem) != cudaSuccess)
-    return CTR_ERR_CUDA;
+  if (csmem > 48 * 1024 && !allow_smem(combine_long_kernel, csmem)) return CTR_ERR_CUDA;
   // one CTA per long run in flight, as many as fit (each run is a short latency chain)
   int per_sm = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, combine_long_kernel, kCombThreads, csmem) != cudaSuccess)

@@ -79,6 +79,14 @@ inline bool once_per_device(std::atomic<uint64_t>& done, F&& setup) {
   return true;
 }
 
+// Lets kernel `k` be launched with `bytes` of dynamic shared memory on the current device.  The limit is only raised, so that a
+// call from another thread that needs less does not lower it under a launch that needs more.
+bool allow_smem_of(const void* k, size_t bytes);
+template <typename... P>
+inline bool allow_smem(void (*k)(P...), size_t bytes) {
+  return allow_smem_of((const void*)k, bytes);
+}
+
 // Launches `k` so that its blocks may be set up while the kernel before it in the stream drains
 // (programmatic dependent launch).  Such a kernel calls grid_wait() before it touches memory, and reads what
 // other kernels may have written by plain loads: read-only ones (__ldg, const __restrict__ pointers) are for

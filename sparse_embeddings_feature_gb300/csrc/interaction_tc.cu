@@ -412,7 +412,7 @@ int interaction_bf16_tc(const void* X, int32_t batch, int32_t n, int32_t d, int 
                       (size_t)kTcEpiGroups * p.epi_bytes;
   const size_t smem = std::max(need, (size_t)kTcSmemFloor);
   auto kern = interaction_bf16_tc_kernel;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+  if (!allow_smem(kern, smem) ||
       cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
                            (int)cudaSharedmemCarveoutMaxShared) != cudaSuccess)
     return CTR_ERR_CUDA;

@@ -531,10 +531,7 @@ extern "C" int ctr_rms_norm_bwd(const void* dy, ctr_dtype dtype, int64_t rows, i
     if (ds) all |= (uint64_t)ds | (uint64_t)(ld_ds * eb);
     const auto k = pick<Backward>(dtype, all % 16 == 0, d);
     const size_t smem = (size_t)d * 4;
-    // the same for every width: calls of others may set it between this and the launch
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxCols * 4) != cudaSuccess)
-      return CTR_ERR_CUDA;
+    if (smem > 48 * 1024 && !allow_smem(k, smem)) return CTR_ERR_CUDA;
     if (launch_after(k, dim3((unsigned)parts), plan.threads, smem, stm, 1, a) != cudaSuccess) return CTR_ERR_CUDA;
   }
   if (dgamma &&
