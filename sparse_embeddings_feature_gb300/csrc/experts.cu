@@ -100,10 +100,12 @@ __device__ __forceinline__ int expert_starts(const int* totals, int experts, int
   return all;
 }
 
-// What a choice's weight is in proportion to, by its score s and the choices' largest score m.  Sigmoids that fp32
-// cannot hold (all of them below e^-20) are in proportion to their exponentials.
+// What a choice's weight is in proportion to, by its score s and the choices' largest score m.  Sigmoids' proportions are taken
+// less e^m where m is negative: the sigmoids themselves may be below fp32's numbers, the weights are not.
 __device__ __forceinline__ float choice_value(const RouteArgs& a, float s, float m) {
-  return a.sigmoid && (m > -20.f || !a.renormalize) ? 1.f / (1.f + expf(-s)) : expf(s - m);
+  if (!a.sigmoid) return expf(s - m);
+  const float r = 1.f / (1.f + expf(-fabsf(s)));
+  return s > 0.f ? r : expf(s - (a.renormalize ? fminf(m, 0.f) : 0.f)) * r;
 }
 
 // What a lane learns of its group's token: choice `sub`'s score and expert (-1: none), the best score,
