@@ -641,9 +641,14 @@ typedef enum {
  * to zero; longer ones, and all of fp32's, are read back as they go and added up
  * with rounding.  fp32: also there, x and w each as three bf16 numbers that add up
  * to it, six of their nine products: what is dropped is below 2^-24 of |x| |w|, so
- * results are as near as those of fp32 sums.  A NaN or an infinity in x or w makes
- * what it enters NaN, or the infinity that the formula gives.  y may be residual
- * itself (the same rows and stride); nothing else may overlap.
+ * results are as near as those of fp32 sums, but for numbers below 2^-109, which
+ * the three hold to within 2^-134 (half of bf16's smallest step).  A NaN or an
+ * infinity in x or w, or a sum past fp32's range, makes what it enters NaN, or the
+ * infinity that the formula gives.  Activations and their derivatives: within 16
+ * and 20 times 2^-24 of themselves (of their terms, where those cancel) for fp32;
+ * for bf16 below the result's rounding, but gelu's tail, which is within 1.5e-7; 0
+ * where an exponential is below 2^-126.  y may be residual itself (the same rows
+ * and stride); nothing else may overlap.
  * Device errors: CTR_ERR_TIMEOUT.
  * Workspace: ctr_dense_workspace_size(rows, n, k, dtype, train, packed) bytes,
  * asked on the device of the call: train != 0 for ctr_dense_bwd (with room for

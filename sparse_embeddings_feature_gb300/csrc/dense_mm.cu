@@ -57,7 +57,7 @@ constexpr int kPairBlocks = 64;                   // blocks of a sum that pairs 
 constexpr int kMainBlocks = 2, kCrossBlocks = 64; // blocks between two readings (planes): 8 and 1280 instructions
 constexpr int kFlushBlocks = 8;                   // without planes: 32 instructions
 // Forward and input gradient without planes sum up to this many terms in the accumulator alone: 1.8e-4 too near to zero at most, a
-// tenth of a bf16 result's rounding (4096 x 4096 x 65536 1455 us, 64 more terms, read back, 1493).
+// tenth of a bf16 result's rounding (4096 x 4096 x 65536 1440 us, 64 more terms, read back, 1460).
 constexpr int64_t kLongSum = 65536;
 // Registers of a kFlush kernel: 384 threads are launched with 168 each; the first four warps give some up so that an
 // epilogue thread can hold 128 sums beside the 64 values that it adds.  56 x 128 + 224 x 256 = 168 x 384.
