@@ -624,8 +624,8 @@ __device__ __forceinline__ uint32_t lanes_max(uint32_t x) {
 // Biases further apart than kSpread (experts pushed out by -1e9, or lifted, say) would make the parts as coarse as that is.
 // Their gaps of more than kGap are closed to that: p is at most 1, so keys on either side of such a gap keep their order, and
 // by more parts than a comparison asks for; keys with no such gap between them keep their distance (65536 x 256 bf16, k 8, 4 of
-// 8 groups, sigmoids and softmax: biases of 0.05 96 and 126 us, a tenth of them -1e9 108 and 139, one of them +10 105 and
-// 137; in parts of the whole range -1e9 takes 3.1 ms, +10 106 and 234).  Closing takes a block 1.7 us, so biases spread by less
+// 8 groups, sigmoids and softmax: biases of 0.05 96 and 125 us, a tenth of them -1e9 109 and 142, one of them +10 108 and
+// 156; in parts of the whole range -1e9 takes 3.1 ms, +10 106 and 234).  Closing takes a block 1.7 us, so biases spread by less
 // are left as they are.
 struct Packing {
   float scale;
@@ -828,13 +828,14 @@ __device__ __forceinline__ int choose_packed(const RouteArgs& a, const float (&v
     bool close = false;
     // near: on either side of the border; equal pairs are ties where packed keys are exact, so that the pairs are the best
     if (!plain) {
-      // In parts; where gaps have been closed, what they hid is added again, within 8 parts and a few 2^-23 of itself (a sum
-      // past fp32's range is below all others).
+      // In parts; where gaps have been closed, what they hid is added again (a sum past fp32's range is below all others).  A
+      // lift is off by 3 of 2^-24 of itself and a part, two of them and the parts' sum by one more each: two groups' worths by
+      // 10 of 2^-24 of the larger one's lifts, which are within 2^24 parts of it, and 4 parts.
       float worth = some ? (float)((k0 >> 9) + (k1 >> 9)) : -INFINITY;
       float least = 2.f * (float)apart, rel = 0.f;
       if (pack.cut) {
-        least += 16.f;
-        rel = 0x1p-21f;
+        least += 32.f;
+        rel = 0x1p-20f;
         if (some)
           worth = fmaxf(worth + (bias.lift[511 - (k0 & 511u)] + (k1 ? bias.lift[511 - (k1 & 511u)] : 0.f)), -3e38f);
       }
