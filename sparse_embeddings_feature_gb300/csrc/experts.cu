@@ -1210,10 +1210,16 @@ __global__ void __launch_bounds__(kRouteThreads) route_bwd_choices_kernel(const 
       total += __shfl_xor_sync(kFull, total, o);
       dot += __shfl_xor_sync(kFull, dot, o);
     }
+    float w = z;  // sigmoids renormalised: the weight itself, which is 1 of a single choice, whose gradient is 0
+    if (a.sigmoid && a.renormalize) {
+      w = live ? z / total : 0.f;
+      dot = w * g;
+      for (int o = 1; o < a.lanes; o <<= 1) dot += __shfl_xor_sync(kFull, dot, o);
+    }
     __syncwarp();  // the row's zeros come before its choices
     if (live) {    // then total >= its own exponential > 0
       const float inv = 1.f / total;
-      float d = a.renormalize ? z * inv * (g - dot * inv) : z * g;
+      float d = !a.renormalize ? z * g : a.sigmoid ? w * (g - dot) : z * inv * (g - dot * inv);
       if (a.sigmoid) d *= 1.f / (1.f + expf(l));  // d ln p / dl = 1 - p
       out[e] = from_f32<T>(d);
     }

@@ -32,3 +32,23 @@ def test_weights_far_below_the_largest(top, dtype):
                                               torch.from_numpy(expert).cuda(), d, ctr.workspace(256))
             ref, mag = L.balanced_grad(dw.astype(np.float64), s, "sigmoid", renorm, 1.5, expert, p)
             assert R.within(d.double().cpu().numpy(), ref, (2 * E + 113) * L.U * mag + 1e-37, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("k", [1, 4])
+def test_the_gradient_of_a_single_choice_is_zero(k, score, dtype):
+    # renormalised, its weight is 1 whatever its score: no rounding may be left over
+    rng = np.random.default_rng(k)
+    T, E = 300, 40
+    s = 4 * rng.normal(size=(T, E)) - 2
+    if k > 1:
+        live = rng.integers(0, E, size=T)
+        s[np.arange(E)[None] != live[:, None]] = -np.inf
+    s = torch.from_numpy(s).to({"f32": torch.float32, "bf16": torch.bfloat16}[dtype]).double().numpy()
+    expert, _ = check(s, k, score, _bias(E, 2), 1, 1, True, dtype, factor=2.5)
+    dw = torch.from_numpy(rng.normal(size=(T, k)).astype(np.float32)).cuda()
+    d = torch.full((T, E), 7.0, dtype=torch.float32 if dtype == "f32" else torch.bfloat16, device="cuda")
+    ctr.ctr_expert_route_balanced_bwd(dw, _on(s, dtype), ctr.SCORES[score], True, 2.5, torch.from_numpy(expert).cuda(), d,
+                                      ctr.workspace(256))
+    assert bool((d == 0).all())
